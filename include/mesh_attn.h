@@ -292,6 +292,103 @@ int mesh_attn_bwd_reduce(const mesh_attn_plan* plan, mesh_attn_dtype out_dtype, 
                          void* dV, void* workspace, size_t workspace_bytes, int32_t* d_status,
                          void* stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ *
+ * Rotary positions with several axes (time, height and width of a video, rows and columns of an
+ * image, plain text with one), applied to q and k in one launch before the attention calls.
+ * The pages leave positions to the model; long-context models rotate q and k.
+ * The d columns of a head are `groups` equal groups rotated alike (1; 2 for the halves of a
+ * differential head).  Pair i of a group turns by the angle
+ *   phi = positions[pair_axis[i]][b][s] * freq[i]:   (x, y) -> (x cos phi - y sin phi,
+ *                                                             y cos phi + x sin phi),
+ * by -phi with inverse = 1, which is the backward pass (the gradient of q from the gradient of
+ * the rotated q).  Pairs are columns (i, i + n_pairs) of the group, or (2 i, 2 i + 1) with
+ * adjacent = 1; columns from 2 n_pairs on are copied.  Angles are exact for any integer position:
+ * they are products modulo a whole turn in 64-bit fixed point.
+ *   dtype       of q, k and both outputs; 2 <= d <= 1024, d % groups == 0,
+ *               1 <= n_pairs <= 256, 2 n_pairs <= d / groups.
+ *   q [B, Hq, S, d] with q_strides[3] = the batch, head and token strides in elements (the d
+ *   columns are consecutive), and q_out with q_out_strides; k, Hk likewise.  Hq or Hk may be 0 (its
+ *   pointers are then not used).  An output may be its input with the same strides; otherwise
+ *   nothing may overlap.  Aligned to the element size; 16-byte aligned tensors whose strides,
+ *   n_pairs and unrotated columns are multiples of 16 bytes take the fast path.
+ *   freq, pair_axis   HOST arrays of n_pairs: radians a position, finite; axis, 0 .. n_axes - 1
+ *                     (n_axes 1 to 8).  Read before the call returns.
+ *   positions   device integers of pos_bits 32 or 64, any sign; pos_strides[3] = axis, batch and token
+ *               strides in elements (0 repeats, e.g. positions shared by a batch). */
+int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32_t d, int32_t Hq, const void* q,
+                   const int64_t* q_strides, void* q_out, const int64_t* q_out_strides, int32_t Hk,
+                   const void* k, const int64_t* k_strides, void* k_out, const int64_t* k_out_strides,
+                   int32_t groups, int32_t n_pairs, int32_t n_axes, const double* freq,
+                   const int32_t* pair_axis, int32_t adjacent, int32_t inverse, const void* positions,
+                   int32_t pos_bits, const int64_t* pos_strides, void* stream);
+
+/* ---------------------------------------------------------------- differential attention
+ *
+ * The difference of two softmax maps over one V, with a learned weight lam per query head.  The
+ * columns of a head's query and key are two halves, q = [q1 | q2], k = [k1 | k2], of d/2 each:
+ *   P_m = softmax(scale q_m k_m^T) over the visible keys,  O_m = P_m V,
+ *   O = O_1 - lam O_2,   LSE_m the natural-log row log-sum-exps.
+ * The tile structure, plans, layouts and masks are those of the calls above (1/sqrt(d/2) is the
+ * usual scale); LSE is [B, Hq, 2, S].  Backward, with D_m = dO . O_m and dP = dO V^T:
+ *   dS_1 = P_1 (dP - D_1),  dS_2 = -lam P_2 (dP - D_2),  dV = (P_1 - lam P_2)^T dO,
+ *   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,  dlam_h = - sum over its rows of D_2.
+ * lam: lam_n device values of the inputs' type, one per query head (lam_n = Hq) or one for all
+ * (lam_n = 1); dlam has the same form, a shared lam's gradient being the sum over the heads.
+ * Masked keys get weight 0 in both maps; a weight of 0 still multiplies its value, so V must be
+ * finite in the 128-key block of a row's last visible key. */
+
+/* A plan's constant tables for the device: the caller allocates mesh_attn_plan_tables_size bytes
+ * of host memory, has mesh_attn_plan_tables_write fill them, and copies them once into a 16-byte
+ * aligned device buffer that the differential calls then read (`tables`).  They depend on the
+ * plan alone and are never written: any number of calls, streams and captured graphs may share them.
+ * A call whose tables are of another plan records MESH_ATTN_ERR_INVALID_ARG in its status block
+ * and does nothing else. */
+int mesh_attn_plan_tables_size(const mesh_attn_plan* plan, size_t* bytes);
+int mesh_attn_plan_tables_write(const mesh_attn_plan* plan, void* out, size_t out_bytes);
+
+/* Bytes of device workspace the differential calls need: the forward's, or with backward = 1
+ * enough for both directions.  Caller-allocated, 16-byte aligned, its contents do not matter; calls
+ * that overlap on the GPU, captured graphs among them, need workspaces of their own. */
+int mesh_attn_diff_workspace_size(const mesh_attn_plan* plan, mesh_attn_dtype dtype, int32_t B,
+                                  int32_t Hq, int32_t Hkv, int32_t d, int32_t backward, size_t* bytes);
+
+/* Forward: O [B, Hq, S, d] and LSE [B, Hq, 2, S] (fp32); O2 [B, Hq, S, d], the second map's
+ * output, is what the backward call needs beside them and may be NULL.
+ *   dtype  MESH_ATTN_BF16 or MESH_ATTN_F32, of Q, K, V, lam, O and O2; arithmetic as in
+ *          mesh_attn_tile_fwd.  d 64 or 128, 2 B Hq S < 2^31.  Everything 16-byte aligned. */
+int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn_dtype dtype, int32_t B,
+                       int32_t Hq, int32_t Hkv, int32_t d, const void* Q, const void* K, const void* V,
+                       const void* lam, int32_t lam_n, float scale, void* O, void* O2, float* LSE,
+                       void* workspace, size_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* Backward: dQ [B, Hq, S, d], dK, dV [B, Hkv, S, d] and dlam [lam_n], all of dtype, from the
+ * forward's O, O2 and LSE and the gradient dO [B, Hq, S, d]. */
+int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn_dtype dtype, int32_t B,
+                       int32_t Hq, int32_t Hkv, int32_t d, const void* Q, const void* K, const void* V,
+                       const void* lam, int32_t lam_n, const void* O, const void* O2, const float* LSE,
+                       const void* dO, float scale, void* dQ, void* dK, void* dV, void* dlam,
+                       void* workspace, size_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* One new token a sequence over a cache: O [B, Hq, d] and LSE [B, Hq, 2] of q [B, Hq, d] (dense)
+ * against the first lens[b] tokens of sequence b's cache, k_cache and v_cache [B, Hkv, T, d] with
+ * strides[3] = batch, head and token strides in elements (multiples of 16 bytes; the d columns are
+ * consecutive).  The new token's own key and value are in the cache, and counted, already.
+ *   lens  device int32 [B], read on the device; 0 gives O = 0 and LSE = -inf.  A length outside
+ *         [0, T] records MESH_ATTN_ERR_OUT_OF_RANGE and is taken as the nearer bound.
+ * Tokens from lens[b] on are not read.  B <= 4096, T <= 2^30, d 64 or 128.
+ *   workspace  mesh_attn_diff_decode_workspace_size bytes for these sizes or larger ones, 16-byte
+ *              aligned, ZEROED once by the caller before its first call; every call leaves it ready
+ *              for the next, of whatever sizes fit.  Calls that overlap on the GPU need their own.
+ * This call does not skip its work on a non-zero status block. */
+int mesh_attn_diff_decode_workspace_size(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t T,
+                                         size_t* bytes);
+int mesh_attn_diff_decode(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t T,
+                          const void* q, const void* k_cache, const int64_t* k_strides, const void* v_cache,
+                          const int64_t* v_strides, const int32_t* lens, const void* lam, int32_t lam_n,
+                          float scale, void* O, float* LSE, void* workspace, size_t workspace_bytes,
+                          int32_t* d_status, void* stream);
+
 /* Synchronise `stream`, copy word 0 of the device status block to *out (a mesh_attn_status).
  * Returns MESH_ATTN_ERR_CUDA if the copy or the synchronisation failed. */
 int mesh_attn_read_status(const int32_t* d_status, void* stream, int32_t* out);

@@ -1,0 +1,418 @@
+"""Differential attention (forward, backward, single tokens over a cache) against the fp64 oracle.
+
+Elementwise bounds, derived from the arithmetic (u = finfo.eps / 2, 2^-8 for bf16; mag: the oracle's sums over
+absolute terms):
+  O, bf16      u |O| (rounded once) + u mag (P rounded to bf16 for its product) + (2^-12 + n 2^-23) mag (exponentials, the
+               fp32 scores of exact bf16 products, fp32 accumulation of n terms)
+  LSE          1e-3 for bf16 inputs and 1e-4 for fp32: the tolerances of the plain attention calls
+  O, fp32      1e-4 mag-free, as the plain attention calls: inputs are N(0, 1)
+  gradients    bf16: u |ref| + (u + 2^-9 + n 2^-23) mag: P or dS rounded once, D from the rounded O and O2, the forward's
+               LSE; fp32: 1e-4 * (1 + mag)
+  dlam         u |ref| + (2^-9 + n 2^-23) sum |P2 dP| / sqrt-free worst case; n = S d terms a row
+"""
+import math
+
+import pytest
+import torch
+
+from oracle import diff_attention as OD
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def inputs(B, Hq, Hkv, S, d, dtype, seed, T=None, lam_n=None, k_scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    t = DT[dtype]
+    q, k, v = n(B, Hq, S, d).to(t), (n(B, Hkv, T or S, d) * k_scale).to(t), n(B, Hkv, T or S, d).to(t)
+    lam = (0.8 + 0.3 * n(lam_n or Hq)).to(t)
+    return q, k, v, lam, n(B, Hq, S, d).to(t)
+
+
+def within(got, ref, bound, what):
+    got = got.double().cpu()
+    assert got.shape == ref.shape, what
+    fin = torch.isfinite(ref)
+    assert torch.equal(fin, torch.isfinite(got)), f"{what}: non-finite pattern differs"
+    assert torch.equal(got[~fin], ref[~fin]), f"{what}: infinities differ"
+    ratio = ((got - ref).abs() / bound)[fin]
+    worst = ratio.max().item() if ratio.numel() else 0.0
+    print(f"{what}: {worst:.3f} of the bound")
+    assert worst <= 1.0, f"{what}: {worst:.3f} of the bound"
+
+
+def check_out(O, L, ref, dtype, n):
+    Or, Lr, _, mag = ref
+    if dtype == "bf16":
+        within(O, Or, 2.0 ** -8 * Or.abs() + (2.0 ** -8 + 2.0 ** -12 + n * 2.0 ** -23) * mag + 1e-6, "O")
+        within(L, Lr, torch.full_like(Lr, 1e-3), "LSE")
+    else:
+        within(O, Or, torch.full_like(Or, 1e-4), "O")
+        within(L, Lr, torch.full_like(Lr, 1e-4), "LSE")
+
+
+def check_grads(got, ref, dtype, S, g):
+    for name, x in zip(("q", "k", "v", "lam"), got):
+        r, mag = ref[name]
+        n = S * (g if name in ("k", "v") else 1)
+        if dtype == "f32":
+            b = 1e-4 * (1 + mag) if name != "lam" else 1e-5 * (1 + mag)
+        elif name == "lam":  # sums of P2 dP kept in fp32, rounded once at the end
+            b = 2.0 ** -8 * r.abs() + (2.0 ** -9 + n * 2.0 ** -23) * mag + 1e-6
+        else:
+            b = 2.0 ** -8 * r.abs() + (2.0 ** -8 + 2.0 ** -9 + n * 2.0 ** -23) * mag + 1e-6
+        within(x, r, b, "d" + name)
+
+
+# B, Hq, Hkv, S, d, P (0: a ring plan of 3), causal
+SHAPES = [
+    (1, 1, 1, 1, 128, 1, True),
+    (1, 2, 1, 2, 64, 1, False),
+    (1, 2, 2, 63, 128, 1, True),
+    (2, 2, 1, 64, 64, 1, True),
+    (1, 2, 2, 65, 128, 1, False),
+    (1, 4, 2, 129, 64, 1, True),
+    (2, 3, 1, 300, 128, 1, True),
+    (1, 4, 2, 516, 128, 4, True),
+    (1, 2, 1, 516, 64, 4, False),
+    (1, 2, 2, 1170, 128, 9, True),
+    (1, 2, 1, 1170, 64, 9, False),
+    (1, 2, 2, 459, 128, 0, True),
+    (1, 1, 1, 1024, 128, 1, False),
+    (1, 8, 1, 200, 128, 4, True),
+]
+
+
+def plan_of(lib, S, P, causal):
+    return lib.mesh_attn_plan_create_ring(S, 3, causal) if P == 0 else lib.mesh_attn_plan_create(S, P, causal)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(lib, shape, dtype):
+    B, Hq, Hkv, S, d, P, causal = shape
+    q, k, v, lam, _ = inputs(B, Hq, Hkv, S, d, dtype, 20)
+    plan = plan_of(lib, S, P, causal)
+    O, L = lib.mesh_diff_attention(q.cuda(), k.cuda(), v.cuda(), lam.cuda(), P, causal, plan=plan)
+    check_out(O, L, OD.forward(q, k, v, lam, causal), dtype, S)
+    O1, O2, L1 = lib.mesh_diff_attention(q.cuda(), k.cuda(), v.cuda(), lam.cuda(), P, causal, plan=plan, return_saved=True)
+    assert torch.equal(O, O1) and torch.equal(L, L1)
+    z = torch.zeros_like(lam)  # lam = 0 leaves the first map, and O2 is minus the second's share
+    Oz, _ = lib.mesh_diff_attention(q.cuda(), k.cuda(), v.cuda(), z.cuda(), P, causal, plan=plan)
+    check_out(Oz, L, OD.forward(q, k, v, z, causal), dtype, S)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_backward(lib, shape, dtype):
+    B, Hq, Hkv, S, d, P, causal = shape
+    q, k, v, lam, g = inputs(B, Hq, Hkv, S, d, dtype, 21)
+    plan = plan_of(lib, S, P, causal)
+    qd, kd, vd, ld = (t.cuda() for t in (q, k, v, lam))
+    O, O2, L = lib.mesh_diff_attention(qd, kd, vd, ld, P, causal, plan=plan, return_saved=True)
+    grads = lib.mesh_diff_attention_backward(qd, kd, vd, ld, O, O2, L, g.cuda(), P, causal, plan=plan)
+    check_grads(grads, OD.backward(q, k, v, lam, g, causal), dtype, S, Hq // Hkv)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_lam_for_all_heads_and_signs(lib, dtype):
+    q, k, v, _, g = inputs(2, 4, 2, 150, 128, dtype, 22)
+    for value in (0.0, -0.75, 2.5):
+        lam = torch.tensor([value], dtype=DT[dtype])
+        args = [t.cuda() for t in (q, k, v, lam)]
+        O, O2, L = lib.mesh_diff_attention(*args, 1, True, return_saved=True)
+        check_out(O, L, OD.forward(q, k, v, lam, True), dtype, 150)
+        grads = lib.mesh_diff_attention_backward(*args, O, O2, L, g.cuda(), 1, True)
+        assert grads[3].shape == (1,)
+        check_grads(grads, OD.backward(q, k, v, lam, g, True), dtype, 150, 2)
+
+
+def test_large_scores(lib):
+    """Scores of some hundred: the running maximum moves, most weights vanish."""
+    q, k, v, lam, g = inputs(1, 2, 2, 300, 128, "bf16", 23, k_scale=16.0)
+    args = [t.cuda() for t in (q, k, v, lam)]
+    O, O2, L = lib.mesh_diff_attention(*args, 4, True, return_saved=True)
+    Or, Lr, _, mag = OD.forward(q, k, v, lam, True)
+    # a score of up to 2^10 in fp32 is off by 2^-14 + d 2^-24 2^10: its weight by a relative 2^-10, the LSE by 2^-12
+    within(O, Or, 2.0 ** -8 * Or.abs() + (2.0 ** -8 + 2.0 ** -9) * mag + 1e-6, "O")
+    within(L, Lr, torch.full_like(Lr, 1e-3), "LSE")
+
+
+def test_equals_two_plain_attentions(lib):
+    """O1 and O2 as the framework's plain calls give them, on q and k with the other half zeroed."""
+    q, k, v, lam, _ = (t.cuda() for t in inputs(1, 2, 1, 256, 128, "bf16", 24))
+    scale = 1 / math.sqrt(64)
+    halves = []
+    for part in (slice(0, 64), slice(64, 128)):
+        qm = torch.zeros_like(q)
+        qm[..., part] = q[..., part]
+        halves.append(lib.mesh_attention(qm, k, v, 1, True, scale=scale))
+    O, O2, L = lib.mesh_diff_attention(q, k, v, lam, 1, True, return_saved=True)
+    assert torch.allclose(L[:, :, 0], halves[0][1], atol=2e-6, rtol=0) and torch.allclose(L[:, :, 1], halves[1][1], atol=2e-6, rtol=0)
+    o1, o2 = (h[0].double() for h in halves)
+    ref = o1 - lam.double().view(1, 2, 1, 1) * o2
+    # o1 and o2 are rounded, P is in both: 3 roundings of 2^-8 each relative to the magnitudes, which are below 4
+    assert ((O.double() - ref).abs() <= 3 * 2.0 ** -8 * (o1.abs() + o2.abs() + 0.1)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_autograd_and_differences(lib, dtype):
+    q, k, v, lam, g = inputs(1, 2, 1, 96, 64, dtype, 25)
+    leaves = [t.cuda().requires_grad_(True) for t in (q, k, v, lam)]
+    O, L = lib.mesh_diff_attention_autograd(*leaves, 1, True)
+    assert not L.requires_grad
+    O.backward(g.cuda())
+    check_grads([t.grad for t in leaves], OD.backward(q, k, v, lam, g, True), dtype, 96, 2)
+    # the oracle's gradient against differences of the oracle's output, in fp64
+    ref = OD.backward(q, k, v, lam, g, True)
+    gen = torch.Generator().manual_seed(1)
+    for i, name in enumerate(("q", "k", "v", "lam")):
+        args = [t.double() for t in (q, k, v, lam)]
+        e = torch.randn(args[i].shape, generator=gen, dtype=torch.float64)
+        f = []
+        for h in (1e-6, -1e-6):
+            a = list(args)
+            a[i] = a[i] + h * e
+            f.append((OD.forward(*a, True)[0] * g.double()).sum())
+        d = ((f[0] - f[1]) / 2e-6).item()
+        r = (ref[name][0] * e).sum().item()
+        # central differences: h^2 times a third derivative of order the value, and 2^-53 |f| / h
+        assert abs(d - r) <= 1e-5 * (1 + abs(r)), name
+
+
+def test_shared_leaf_gradients_add_up(lib):
+    """A lam expanded from one value, and k used twice: autograd sums what the calls return."""
+    q, k, v, _, g = inputs(1, 2, 2, 70, 64, "f32", 26)
+    one = torch.tensor([0.6], device="cuda", requires_grad=True)
+    kd = k.cuda().requires_grad_(True)
+    O, _ = lib.mesh_diff_attention_autograd(q.cuda(), kd, kd, one.expand(2).contiguous(), 1, False)
+    O.backward(g.cuda())
+    ref = OD.backward(q, k, k, torch.tensor([0.6]), g, False)
+    within(one.grad, ref["lam"][0], 1e-5 * (1 + ref["lam"][1]), "dlam")
+    within(kd.grad, ref["k"][0] + ref["v"][0], 1e-4 * (2 + ref["k"][1] + ref["v"][1]), "dk + dv")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P", [1, 4])
+def test_same_bits_each_time_and_what_surrounds(lib, dtype, P):
+    """Two runs give the same bits; a workspace full of NaN and outputs full of NaN change nothing."""
+    q, k, v, lam, g = (t.cuda() for t in inputs(2, 4, 2, 520, 128, dtype, 27))
+    plan = lib.mesh_attn_plan_create(520, P, True)
+    runs = []
+    for fill in (0, 255):
+        ws = lib.new_diff_workspace(plan, q, k, backward=True).fill_(fill)
+        O, O2, L = lib.mesh_diff_attention(q, k, v, lam, P, True, plan=plan, workspace=ws, return_saved=True)
+        grads = [torch.full_like(t, float("nan")) for t in (q, k, v, lam)]
+        ws.fill_(fill)
+        st = lib.new_status()
+        lib.mesh_attn_diff_bwd(plan, q, k, v, lam, O, O2, L, g, None, *grads, ws, st)
+        assert lib.mesh_attn_read_status(st) == 0
+        runs.append([O, O2, L, *grads])
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+def test_neighbours_nan_stays_out(lib):
+    """NaN and infinities in another head, batch or partition's padding never reach a result: L = 100 is no multiple
+    of a tile, so tiles reach past a partition's end."""
+    for dtype in ("f32",):
+        q, k, v, lam, g = inputs(2, 2, 2, 400, 128, dtype, 28)
+        bad = [t.clone() for t in (q, k, v, g)]
+        for t in bad:
+            t[1] = float("nan")
+            t[0, 1] = float("inf")
+        plan = lib.mesh_attn_plan_create(400, 4, True)
+        outs = []
+        for qq, kk, vv, gg in ((q, k, v, g), bad):
+            args = [t.cuda() for t in (qq, kk, vv, lam)]
+            O, O2, L = lib.mesh_diff_attention(*args, 4, True, plan=plan, return_saved=True)
+            outs.append([O, L, *lib.mesh_diff_attention_backward(*args, O, O2, L, gg.cuda(), 4, True, plan=plan)[:3]])
+        for a, b in zip(*outs):
+            assert torch.equal(a[0, 0], b[0, 0]), dtype
+
+
+def test_tables_of_another_plan_are_refused(lib):
+    q, k, v, lam, _ = (t.cuda() for t in inputs(1, 1, 1, 64, 64, "bf16", 29))
+    for dtype in (torch.bfloat16, torch.float32):
+        q, k, v, lam = (t.to(dtype) for t in (q, k, v, lam))
+        plan, other = lib.mesh_attn_plan_create(64, 1, True), lib.mesh_attn_plan_create(64, 1, False)
+        ws, st = lib.new_diff_workspace(plan, q, k), lib.new_status()
+        O, L = torch.full_like(q, 7.0), torch.full((1, 1, 2, 64), 7.0, device="cuda")
+        plan._tables[torch.cuda.current_device()] = other.tables("cuda")
+        lib.mesh_attn_diff_fwd(plan, q, k, v, lam, None, O, None, L, ws, st)
+        assert lib.mesh_attn_read_status(st) == 1
+        assert (O == 7).all() and (L == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_training_step(lib, dtype):
+    """Forward and backward in one graph, replayed on other inputs; two graphs with workspaces of their own on two streams."""
+    shape = (1, 2, 1, 200, 128)
+    plan = lib.mesh_attn_plan_create(200, 1, True)
+    plan.tables("cuda")
+    st = lib.new_status()
+    graphs = []
+    for i in range(2):
+        bufs = [t.cuda() for t in inputs(*shape, dtype, 30 + i)]
+        ws = lib.new_diff_workspace(plan, bufs[0], bufs[1], backward=True)
+        s, gr = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr, stream=s):
+            O, O2, L = lib.mesh_diff_attention(*bufs[:4], 1, True, plan=plan, workspace=ws, status=st, check_status=False,
+                                               return_saved=True)
+            grads = lib.mesh_diff_attention_backward(*bufs[:4], O, O2, L, bufs[4], 1, True, plan=plan, workspace=ws,
+                                                     status=st, check_status=False)
+        graphs.append((gr, s, bufs, O, L, grads))
+    new = [inputs(*shape, dtype, 40 + i) for i in range(2)]
+    for (gr, s, bufs, *_), n in zip(graphs, new):
+        for b, x in zip(bufs, n):
+            b.copy_(x)
+    torch.cuda.synchronize()
+    for gr, s, *_ in graphs:
+        with torch.cuda.stream(s):
+            gr.replay()
+    torch.cuda.synchronize()
+    assert lib.mesh_attn_read_status(st) == 0
+    for (_, _, _, O, L, grads), (q, k, v, lam, g) in zip(graphs, new):
+        check_out(O, L, OD.forward(q, k, v, lam, True), dtype, 200)
+        check_grads(grads, OD.backward(q, k, v, lam, g, True), dtype, 200, 2)
+
+
+def test_wait_limit_gives_an_error_and_the_next_call_works(lib):
+    q, k, v, lam, g = (t.cuda() for t in inputs(1, 2, 2, 600, 128, "bf16", 33))
+    O, O2, L = lib.mesh_diff_attention(q, k, v, lam, 1, True, return_saved=True)
+    try:
+        lib.mesh_attn_set_wait_limit_ns(0)
+        with pytest.raises(lib.MeshAttnError) as e:
+            lib.mesh_diff_attention(q, k, v, lam, 1, True)
+        assert e.value.code == 5
+        with pytest.raises(lib.MeshAttnError) as e:
+            lib.mesh_diff_attention_backward(q, k, v, lam, O, O2, L, g, 1, True)
+        assert e.value.code == 5
+    finally:
+        lib.mesh_attn_set_wait_limit_ns(2_000_000_000)
+    O1, _ = lib.mesh_diff_attention(q, k, v, lam, 1, True)
+    assert torch.equal(O, O1)
+
+
+# ------------------------------------------------------------------ single tokens over a cache
+
+DECODE = [  # B, Hq, Hkv, d, T, lens
+    (1, 1, 1, 128, 1, [1]),
+    (1, 2, 2, 64, 16, [0]),
+    (2, 4, 1, 128, 130, [130, 1]),
+    (3, 3, 3, 64, 257, [0, 257, 128]),
+    (2, 6, 2, 128, 1000, [129, 999]),
+    (5, 8, 1, 64, 300, [0, 1, 2, 300, 127]),
+    (2, 16, 1, 128, 700, [700, 300]),      # a group of 16: two head chunks
+    (1, 12, 1, 64, 2000, [1999]),          # 8 + 4 heads
+    (300, 1, 1, 64, 40, None),
+    (1, 4, 2, 128, 40000, [39999]),        # every CTA a piece
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: f"B{c[0]}_{c[1]}_{c[2]}_d{c[3]}_T{c[4]}")
+def test_decode(lib, case, dtype):
+    B, Hq, Hkv, d, T, lens = case
+    lens = torch.tensor(lens if lens is not None else [(7 * b) % (T + 1) for b in range(B)], dtype=torch.int32)
+    q, k, v, lam, _ = inputs(B, Hq, Hkv, 1, d, dtype, 50, T=T)
+    for b in range(B):  # what lies behind a sequence's tokens is never read
+        k[b, :, lens[b]:] = float("nan")
+        v[b, :, lens[b]:] = float("inf")
+    ws = lib.new_diff_decode_workspace(B, Hq, Hkv, d, T)
+    args = [t.cuda() for t in (q, k, v, lens, lam)]
+    O, L = lib.mesh_diff_decode(*args, workspace=ws)
+    check_out(O, L, OD.forward(q, k, v, lam, False, lens=lens), dtype, T)
+    # the workspace serves the next call, and the bits do not depend on what was there
+    O2, L2 = lib.mesh_diff_decode(*args, workspace=ws)
+    assert torch.equal(O, O2) and torch.equal(L, L2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_strided_cache_and_shared_lam(lib, dtype):
+    B, Hq, Hkv, d, T = 2, 4, 2, 64, 190
+    q, k, v, _, _ = inputs(B, Hq, Hkv, 1, d, dtype, 51, T=T)
+    lam = torch.tensor([0.7], dtype=DT[dtype])
+    lens = torch.tensor([190, 65], dtype=torch.int32)
+    both = torch.stack([k, v], 3).permute(0, 2, 3, 1, 4).contiguous().cuda()  # [B, T, 2, Hkv, d]
+    kc, vc = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    O, L = lib.mesh_diff_decode(q.cuda(), kc, vc, lens.cuda(), lam.cuda())
+    check_out(O, L, OD.forward(q, k, v, lam, False, lens=lens), dtype, T)
+
+
+def test_decode_workspace_of_larger_sizes(lib):
+    ws = lib.new_diff_decode_workspace(8, 16, 2, 128, 5000)
+    for B, Hq, Hkv, d, T, seed in ((8, 16, 2, 128, 500, 52), (1, 2, 1, 64, 3000, 53), (3, 4, 2, 128, 77, 54), (8, 16, 2, 128, 500, 55)):
+        q, k, v, lam, _ = inputs(B, Hq, Hkv, 1, d, "bf16", seed, T=T)
+        lens = torch.full((B,), T, dtype=torch.int32)
+        O, L = lib.mesh_diff_decode(q.cuda(), k.cuda(), v.cuda(), lens.cuda(), lam.cuda(), workspace=ws)
+        check_out(O, L, OD.forward(q, k, v, lam, False, lens=lens), "bf16", T)
+
+
+def test_decode_lengths_out_of_range_are_reported(lib):
+    q, k, v, lam, _ = inputs(2, 2, 1, 1, 64, "bf16", 56, T=100)
+    args = [t.cuda() for t in (q, k, v)]
+    st = lib.new_status()
+    O, L = lib.mesh_diff_decode(*args, torch.tensor([-3, 1000], dtype=torch.int32).cuda(), lam.cuda(), status=st,
+                                check_status=False)
+    assert lib.mesh_attn_read_status(st) == 6
+    check_out(O, L, OD.forward(q, k, v, lam, False, lens=[0, 100]), "bf16", 100)
+
+
+def test_decode_captured_with_growing_lengths(lib):
+    q, k, v, lam, _ = inputs(2, 4, 2, 1, 128, "bf16", 57, T=3000)
+    lens = torch.tensor([1, 2900], dtype=torch.int32)
+    args = [t.cuda() for t in (q, k, v, lens, lam)]
+    ws, st = lib.new_diff_decode_workspace(2, 4, 2, 128, 3000), lib.new_status()
+    gr = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(gr):
+        O, L = lib.mesh_diff_decode(*args, workspace=ws, status=st, check_status=False)
+    for step in (0, 1, 60):
+        now = lens + step
+        args[3].copy_(now)
+        gr.replay()
+        torch.cuda.synchronize()
+        check_out(O, L, OD.forward(q, k, v, lam, False, lens=now), "bf16", 3000)
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_model_layer_trained_and_served(lib, dtype):
+    """Projection -> rotary positions -> differential attention -> loss, with every gradient; then the same tokens one at
+    a time over a cache, equal to the rows of the whole pass."""
+    B, Hq, Hkv, S, d = 1, 4, 2, 150, 128
+    t = DT[dtype]
+    xq, xk, v, lam, g = inputs(B, Hq, Hkv, S, d, dtype, 60)
+    xq, xk = xq.transpose(1, 2).contiguous(), xk.transpose(1, 2).contiguous()  # [B, S, H, d]
+    rope = lib.MeshRope(d, (12, 10, 10), groups=2)
+    i = torch.arange(S)
+    pos = torch.stack([i // 16, i // 4 % 4, i % 4]).unsqueeze(1) + 70000
+    leaves = [x.cuda().requires_grad_(True) for x in (xq, xk, v, lam)]
+    q, k = lib.mesh_rope_autograd(leaves[0].transpose(1, 2), leaves[1].transpose(1, 2), pos.cuda(), rope)
+    O, L = lib.mesh_diff_attention_autograd(q, k, leaves[2], leaves[3], 1, True)
+    O.backward(g.cuda())
+    qr, kr = q.detach().cpu(), k.detach().cpu()
+    check_out(O.detach(), L, OD.forward(qr, kr, v, lam, True), dtype, S)
+    ref = OD.backward(qr, kr, v, lam, g, True)
+    for x, name, heads in ((leaves[0], "q", Hq), (leaves[1], "k", Hkv)):
+        r, _ = OD.rope(ref[name][0], pos, rope.freq, rope.axis, 2, False, True)
+        _, m = OD.rope(ref[name][1], pos, rope.freq, rope.axis, 2, False, True)
+        n = S * (Hq // Hkv)
+        u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+        # the attention's gradient within its bound (rotated: both of a pair enter), then one rounding more
+        b = (2 * u + 2.0 ** -8 + 2.0 ** -9 + n * 2.0 ** -23) * m * 2 + 1e-5 if dtype == "bf16" else 4e-4 * (1 + m)
+        within(x.grad.transpose(1, 2), r, b, "dx" + name)
+    kc, vc = torch.zeros(B, Hkv, S, d, dtype=t, device="cuda"), torch.zeros(B, Hkv, S, d, dtype=t, device="cuda")
+    ws = lib.new_diff_decode_workspace(B, Hq, Hkv, d, S)
+    full = OD.forward(qr, kr, v, lam, True)
+    for s in (0, 1, 17, 127, 128, 149):
+        q1, _ = lib.mesh_rope(leaves[0].detach()[:, s:s + 1].transpose(1, 2), None, pos.cuda()[:, :, s:s + 1], rope)
+        lib.mesh_attn_rope(rope, leaves[1].detach()[:, :s + 1].transpose(1, 2), None, pos.cuda()[:, :, :s + 1], kc[:, :, :s + 1], None)
+        vc[:, :, :s + 1] = v.cuda()[:, :, :s + 1]
+        o, l = lib.mesh_diff_decode(q1, kc, vc, torch.tensor([s + 1], dtype=torch.int32, device="cuda"), leaves[3].detach(), workspace=ws)
+        check_out(o, l, [x[:, :, s:s + 1] if x.dim() == 4 and x.shape[2] == S else x[..., s:s + 1] for x in full], dtype, S)

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional, Tuple
+from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
@@ -73,6 +73,19 @@ _SIGS = {
     "mesh_attn_status_string": (ctypes.c_char_p, [c_i32]),
     "mesh_attn_last_error": (ctypes.c_char_p, []),
     "mesh_attn_set_wait_limit_ns": (c_i32, [c_i64]),
+    "mesh_attn_rope": (c_i32, [c_i32, c_i32, c_i64, c_i32, c_i32, c_vp, P_i64, c_vp, P_i64, c_i32, c_vp, P_i64, c_vp,
+                               P_i64, c_i32, c_i32, c_i32, ctypes.POINTER(ctypes.c_double), P_i32, c_i32, c_i32, c_vp,
+                               c_i32, P_i64, c_vp]),
+    "mesh_attn_plan_tables_size": (c_i32, [c_vp, P_sz]),
+    "mesh_attn_plan_tables_write": (c_i32, [c_vp, c_vp, c_sz]),
+    "mesh_attn_diff_workspace_size": (c_i32, [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, P_sz]),
+    "mesh_attn_diff_fwd": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_f32,
+                                   c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "mesh_attn_diff_bwd": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                   c_vp, c_vp, c_vp, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "mesh_attn_diff_decode_workspace_size": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i64, P_sz]),
+    "mesh_attn_diff_decode": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, P_i64, c_vp, P_i64, c_vp, c_vp,
+                                      c_i32, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
 }
 
 
@@ -130,10 +143,27 @@ class Plan:
         info = PlanInfo()
         _check(_lib.mesh_attn_plan_get_info(self._h, ctypes.byref(info)), "mesh_attn_plan_get_info")
         self.info = info
+        self._tables: Dict[int, torch.Tensor] = {}
 
     @property
     def handle(self):
         return self._h
+
+    def tables(self, device=None) -> torch.Tensor:
+        """The plan's constant tables on `device`, copied there on the first call (which waits for the copy,
+        so that every stream may read them; make it before capturing a graph) and shared by all later ones."""
+        dev = torch.device(device if device is not None else "cuda")
+        index = dev.index if dev.index is not None else torch.cuda.current_device()
+        got = self._tables.get(index)
+        if got is None:
+            n = c_sz()
+            _check(_lib.mesh_attn_plan_tables_size(self._h, ctypes.byref(n)), "mesh_attn_plan_tables_size")
+            host = torch.empty(n.value, dtype=torch.uint8)
+            _check(_lib.mesh_attn_plan_tables_write(self._h, _ptr(host), n.value), "mesh_attn_plan_tables_write")
+            got = host.to(torch.device("cuda", index))
+            torch.cuda.current_stream(index).synchronize()
+            self._tables[index] = got
+        return got
 
     def __getattr__(self, name):
         if name in ("S", "L", "P", "R", "causal", "kvr", "greedy", "n_slots", "n_steps", "n_kv_entries",
@@ -468,3 +498,379 @@ def mesh_attention_autograd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, P
     """mesh_attention with autograd: returns (O, LSE); O.backward(...) fills q.grad, k.grad and v.grad
     through the tile backward."""
     return MeshAttentionFunction.apply(q, k, v, P, causal, kvr, greedy, scale)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+class MeshRope:
+    """Rotary positions with several axes: which axis turns each pair of columns, and how fast.
+
+    d         columns of a head, `groups` equal groups of them rotated alike (2 for the halves of a
+              differential head)
+    sections  pairs of each axis, e.g. (12, 10, 10) for time, height and width; their sum is at
+              most d / groups / 2, the columns behind are copied
+    style     "half": pairs (i, i + n); "adjacent": (2 i, 2 i + 1)
+    freq      "global": base^(-i / n) over all n pairs, each axis taking its section of that ladder;
+              "axial": base^(-j / n_a) within the section of each axis; or the frequencies
+              themselves, one a pair, in radians a position
+    axis_of_pair  the axis of each pair where the sections are interleaved
+    """
+
+    def __init__(self, d: int, sections: Sequence[int], base: float = 10000.0, groups: int = 1, style: str = "half",
+                 freq="global", axis_of_pair: Optional[Sequence[int]] = None):
+        sections = [int(n) for n in sections]
+        if not sections or any(n < 0 for n in sections) or sum(sections) < 1:
+            raise ValueError("sections must be one or more pair counts")
+        n = sum(sections)
+        if groups < 1 or d % groups or 2 * n > d // groups:
+            raise ValueError(f"need groups >= 1, d % groups == 0 and 2 * sum(sections) <= d / groups; got d = {d}, "
+                             f"groups = {groups}, sections = {sections}")
+        if style not in ("half", "adjacent"):
+            raise ValueError("style must be 'half' or 'adjacent'")
+        axis = [a for a, m in enumerate(sections) for _ in range(m)]
+        if axis_of_pair is not None:
+            axis = [int(a) for a in axis_of_pair]
+            if len(axis) != n or any(a < 0 or a >= len(sections) for a in axis):
+                raise ValueError("axis_of_pair must give an axis of sections for each pair")
+        if isinstance(freq, str):
+            if not base > 0:
+                raise ValueError("base must be > 0")
+            if freq == "global":
+                freq = [float(base) ** (-i / n) for i in range(n)]
+            elif freq == "axial":
+                at = [0] * len(sections)
+                out = []
+                for a in axis:
+                    out.append(float(base) ** (-at[a] / axis.count(a)))
+                    at[a] += 1
+                freq = out
+            else:
+                raise ValueError("freq must be 'global', 'axial' or a sequence of frequencies")
+        freq = [float(f) for f in freq]
+        if len(freq) != n:
+            raise ValueError("freq must give a frequency for each pair")
+        self.d, self.groups, self.style, self.n_axes, self.n_pairs = int(d), int(groups), style, len(sections), n
+        self.freq, self.axis = tuple(freq), tuple(axis)
+        self._freq = (ctypes.c_double * n)(*freq)
+        self._axis = (c_i32 * n)(*axis)
+
+
+def _strides3(t: torch.Tensor):
+    return (c_i64 * 3)(*t.stride()[:3])
+
+
+def _one_device(*ts):
+    dev = ts[0].device
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        if t.device != dev:
+            raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
+    return dev
+
+
+def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+                   q_out: torch.Tensor, k_out: Optional[torch.Tensor], inverse: bool = False, stream=None) -> None:
+    """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) rotated into q_out and k_out; views with any batch,
+    head and token strides.  positions: int32 or int64 [axes, S] or [axes, B, S] ([S] or [B, S]
+    for one axis), any strides."""
+    load_library()
+    if q.dim() != 4 or q.shape[3] != rope.d:
+        raise ValueError(f"q must be [B, H, S, {rope.d}]")
+    B, Hq, S, d = q.shape
+    pairs = [(q, q_out)] + ([(k, k_out)] if k is not None else [])
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    for x, y in pairs:
+        if x.dim() != 4 or (x.shape[0], x.shape[2], x.shape[3]) != (B, S, d):
+            raise ValueError("q and k must agree in batch, tokens and columns")
+        if y.shape != x.shape:
+            raise ValueError("an output must have its input's shape")
+        if x.dtype != q.dtype or y.dtype != q.dtype:
+            raise ValueError("q, k and the outputs must be of one dtype")
+        if x.numel() and (x.stride(3) != 1 or y.stride(3) != 1):
+            raise ValueError("the columns of a head must be consecutive")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be int32 or int64")
+    pos = positions
+    if rope.n_axes == 1 and (pos.dim() == 1 or (pos.dim() == 2 and pos.shape[0] != 1)):
+        pos = pos.unsqueeze(0)
+    if pos.dim() == 2:
+        pos = pos.unsqueeze(1)
+    if pos.dim() != 3 or pos.shape[0] != rope.n_axes or pos.shape[1] not in (1, B) or pos.shape[2] != S:
+        raise ValueError(f"positions must be [{rope.n_axes}, S] or [{rope.n_axes}, B, S] with B = {B}, S = {S}; got "
+                         f"{tuple(positions.shape)}")
+    dev = _one_device(q, *(t for p in pairs for t in p), positions)
+    pst = list(pos.stride())
+    if pos.shape[1] == 1:
+        pst[1] = 0
+    with torch.cuda.device(dev):
+        _check(_lib.mesh_attn_rope(_dtype_code(q.dtype), B, S, d, Hq, _ptr(q), _strides3(q), _ptr(q_out), _strides3(q_out),
+                                   0 if k is None else k.shape[1], _ptr(k), None if k is None else _strides3(k),
+                                   _ptr(k_out), None if k is None else _strides3(k_out), rope.groups, rope.n_pairs,
+                                   rope.n_axes, rope._freq, rope._axis, int(rope.style == "adjacent"), int(inverse),
+                                   _ptr(pos), 8 * pos.element_size(), (c_i64 * 3)(*pst), _stream_handle(stream)),
+               "mesh_attn_rope")
+
+
+def mesh_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
+    """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) with their positions, as dense [B, H, S, d] tensors, which is what
+    the attention calls take; q and k may be views, e.g. a projection's [B, S, H, d] transposed."""
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    mesh_attn_rope(rope, q, k, positions, q_out, k_out)
+    return q_out, k_out
+
+
+def mesh_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope,
+                       dq_out: Optional[torch.Tensor] = None, dk_out: Optional[torch.Tensor] = None):
+    """The gradients of mesh_rope's q and k from those of its outputs, into dq_out and dk_out where given (any strides,
+    e.g. the projection's layout), else into dense tensors."""
+    if dq_out is None:
+        dq_out = torch.empty(dq.shape, dtype=dq.dtype, device=dq.device)
+    if dk is not None and dk_out is None:
+        dk_out = torch.empty(dk.shape, dtype=dk.dtype, device=dk.device)
+    mesh_attn_rope(rope, dq, dk, positions, dq_out, dk_out, inverse=True)
+    return dq_out, dk_out
+
+
+def _memory_order(t: torch.Tensor):
+    """t's axes from the slowest to the fastest in memory, the columns last."""
+    return sorted(range(t.dim() - 1), key=lambda i: (-t.stride(i), i)) + [t.dim() - 1]
+
+
+def _empty_in_order(like: torch.Tensor, order) -> torch.Tensor:
+    out = torch.empty([like.shape[i] for i in order], dtype=like.dtype, device=like.device)
+    return out.permute([order.index(i) for i in range(like.dim())])
+
+
+class MeshRopeFunction(torch.autograd.Function):
+    """torch.autograd binding of mesh_rope: the backward pass is the inverse rotation, written in
+    the memory order that q and k have (a projection's [B, S, H, d] where they are views of one)."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, rope):
+        ctx.save_for_backward(positions)
+        ctx.rope = rope
+        ctx.orders = (_memory_order(q), None if k is None else _memory_order(k))
+        return mesh_rope(q, k, positions, rope)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        (positions,) = ctx.saved_tensors
+        grads = [None if g is None else g if g.stride(-1) == 1 else g.contiguous() for g in (dq, dk)]
+        outs = [None if g is None else _empty_in_order(g, o) for g, o in zip(grads, ctx.orders)]
+        return (*mesh_rope_backward(*grads, positions, ctx.rope, *outs), None, None)
+
+
+def mesh_rope_autograd(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
+    """mesh_rope with autograd."""
+    return MeshRopeFunction.apply(q, k, positions, rope)
+
+
+# ---------------------------------------------------------------- differential attention
+
+def _diff_scale(scale: Optional[float], d: int) -> float:
+    return 1.0 / math.sqrt(d // 2) if scale is None else float(scale)
+
+
+def _diff_check(q, k, v, lam, *more):
+    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("q must be [B, Hq, S, d], k and v [B, Hkv, S, d]")
+    B, Hq, S, d = q.shape
+    if (k.shape[0], k.shape[3]) != (B, d):
+        raise ValueError("q, k and v must agree in batch and columns")
+    if k.shape[1] < 1 or Hq % k.shape[1]:
+        raise ValueError(f"Hq must be a multiple of Hkv: {Hq} and {k.shape[1]}")
+    if lam.dim() != 1 or lam.shape[0] not in (1, Hq):
+        raise ValueError("lam must be [Hq], or [1] for one value for all heads")
+    for t in (q, k, v, lam) + more:
+        if t.dtype != q.dtype:
+            raise ValueError("q, k, v, lam and the gradients must be of one dtype")
+    dev = _one_device(q, k, v, lam, *more)
+    return B, Hq, S, d, dev
+
+
+def mesh_attn_diff_workspace_size(plan: Plan, dtype: torch.dtype, B: int, Hq: int, Hkv: int, d: int,
+                                  backward: bool = False) -> int:
+    n = c_sz()
+    _check(_lib.mesh_attn_diff_workspace_size(plan.handle, _dtype_code(dtype), B, Hq, Hkv, d, int(backward), ctypes.byref(n)),
+           "mesh_attn_diff_workspace_size")
+    return n.value
+
+
+def new_diff_workspace(plan: Plan, q: torch.Tensor, k: torch.Tensor, backward: bool = False) -> torch.Tensor:
+    """Workspace of mesh_attn_diff_fwd for tensors of q's and k's sizes; with backward, of both directions."""
+    B, Hq, _, d = q.shape
+    n = mesh_attn_diff_workspace_size(plan, q.dtype, B, Hq, k.shape[1], d, backward)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+
+
+def mesh_attn_diff_fwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                       scale: Optional[float], O: torch.Tensor, O2: Optional[torch.Tensor], LSE: torch.Tensor,
+                       workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    outs = (O,) if O2 is None else (O, O2)
+    B, Hq, S, d, dev = _diff_check(q, k, v, lam, *outs)
+    if S != plan.S or k.shape[2] != plan.S:
+        raise ValueError(f"the plan is for S = {plan.S}; q has {S} tokens, k and v {k.shape[2]}")
+    if any(t.shape != q.shape for t in outs) or LSE.shape != (B, Hq, 2, S) or LSE.dtype != torch.float32:
+        raise ValueError("O and O2 must have q's shape, LSE must be fp32 [B, Hq, 2, S]")
+    if not all(t.is_contiguous() for t in (q, k, v, lam, LSE) + outs):
+        raise ValueError("q, k, v, lam and the outputs must be contiguous")
+    _one_device(q, LSE, workspace, status)
+    with torch.cuda.device(dev):
+        _check(_lib.mesh_attn_diff_fwd(plan.handle, _ptr(plan.tables(dev)), _dtype_code(q.dtype), B, Hq, k.shape[1], d,
+                                       _ptr(q), _ptr(k), _ptr(v), _ptr(lam), lam.shape[0], _diff_scale(scale, d), _ptr(O),
+                                       _ptr(O2), _ptr(LSE), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _ptr(status), _stream_handle(stream)), "mesh_attn_diff_fwd")
+
+
+def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, O: torch.Tensor,
+                       O2: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, scale: Optional[float], dQ: torch.Tensor,
+                       dK: torch.Tensor, dV: torch.Tensor, dlam: torch.Tensor, workspace: torch.Tensor,
+                       status: torch.Tensor, stream=None) -> None:
+    B, Hq, S, d, dev = _diff_check(q, k, v, lam, O, O2, dO, dQ, dK, dV, dlam)
+    if S != plan.S or k.shape[2] != plan.S:
+        raise ValueError(f"the plan is for S = {plan.S}; q has {S} tokens, k and v {k.shape[2]}")
+    if any(t.shape != q.shape for t in (O, O2, dO, dQ)) or dK.shape != k.shape or dV.shape != v.shape or \
+            dlam.shape != lam.shape or LSE.shape != (B, Hq, 2, S) or LSE.dtype != torch.float32:
+        raise ValueError("O, O2, dO and dQ must have q's shape, dK, dV and dlam that of k, v and lam, LSE fp32 [B, Hq, 2, S]")
+    if not all(t.is_contiguous() for t in (q, k, v, lam, O, O2, LSE, dO, dQ, dK, dV, dlam)):
+        raise ValueError("tensors must be contiguous")
+    _one_device(q, LSE, workspace, status)
+    with torch.cuda.device(dev):
+        _check(_lib.mesh_attn_diff_bwd(plan.handle, _ptr(plan.tables(dev)), _dtype_code(q.dtype), B, Hq, k.shape[1], d,
+                                       _ptr(q), _ptr(k), _ptr(v), _ptr(lam), lam.shape[0], _ptr(O), _ptr(O2), _ptr(LSE),
+                                       _ptr(dO), _diff_scale(scale, d), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dlam),
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+                                       _stream_handle(stream)), "mesh_attn_diff_bwd")
+
+
+def _raise_status(status: torch.Tensor):
+    code = mesh_attn_read_status(status, torch.cuda.current_stream(status.device))
+    if code != 0:
+        raise MeshAttnError(code, "device", f"status block {status.tolist()}")
+
+
+def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, P: int, causal: bool,
+                        kvr: bool = True, greedy: bool = True, scale: Optional[float] = None,
+                        plan: Optional[Plan] = None, workspace: Optional[torch.Tensor] = None,
+                        status: Optional[torch.Tensor] = None, check_status: bool = True, return_saved: bool = False):
+    """Differential attention on the current stream: softmax(q1 k1^T s) v - lam softmax(q2 k2^T s) v with q = [q1 | q2] and
+    k = [k1 | k2] by columns (s = 1 / sqrt(d / 2) unless given).
+
+    q [B, Hq, S, d], k, v [B, Hkv, S, d], lam [Hq] or [1] (one value for all heads), all bf16 or all fp32.  Returns O (q's
+    shape and dtype) and LSE (fp32 [B, Hq, 2, S]); with return_saved O, O2 and LSE, which
+    mesh_diff_attention_backward takes.  A program that calls it every step keeps plan, workspace
+    (new_diff_workspace) and status (new_status) and passes check_status=False, which leaves out the wait.
+    """
+    B, Hq, S, d, dev = _diff_check(q, k, v, lam)
+    plan = plan or mesh_attn_plan_create(S, P, causal, kvr, greedy)
+    ws = new_diff_workspace(plan, q, k) if workspace is None else workspace
+    st = new_status(dev) if status is None else status
+    O = torch.empty_like(q)
+    O2 = torch.empty_like(q) if return_saved else None
+    LSE = torch.empty(B, Hq, 2, S, dtype=torch.float32, device=dev)
+    mesh_attn_diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, ws, st, torch.cuda.current_stream(dev))
+    if check_status:
+        _raise_status(st)
+    return (O, O2, LSE) if return_saved else (O, LSE)
+
+
+def mesh_diff_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, O: torch.Tensor,
+                                 O2: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, P: int, causal: bool,
+                                 kvr: bool = True, greedy: bool = True, scale: Optional[float] = None,
+                                 plan: Optional[Plan] = None, workspace: Optional[torch.Tensor] = None,
+                                 status: Optional[torch.Tensor] = None, check_status: bool = True):
+    """(dQ, dK, dV, dlam) from the forward's O, O2 and LSE and the gradient dO, on the current stream."""
+    B, Hq, S, d, dev = _diff_check(q, k, v, lam, O, O2, dO)
+    plan = plan or mesh_attn_plan_create(S, P, causal, kvr, greedy)
+    ws = new_diff_workspace(plan, q, k, backward=True) if workspace is None else workspace
+    st = new_status(dev) if status is None else status
+    grads = tuple(torch.empty_like(t) for t in (q, k, v, lam))
+    mesh_attn_diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, *grads, ws, st, torch.cuda.current_stream(dev))
+    if check_status:
+        _raise_status(st)
+    return grads
+
+
+class MeshDiffAttentionFunction(torch.autograd.Function):
+    """torch.autograd binding of mesh_diff_attention: gradients reach q, k, v and lam; LSE is a non-differentiable output."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lam, P, causal, kvr, greedy, scale, plan, check_status):
+        plan = plan or mesh_attn_plan_create(q.shape[2], P, causal, kvr, greedy)
+        O, O2, LSE = mesh_diff_attention(q, k, v, lam, P, causal, kvr, greedy, scale, plan=plan, check_status=check_status,
+                                         return_saved=True)
+        ctx.save_for_backward(q, k, v, lam, O, O2, LSE)
+        ctx.plan = plan
+        ctx.args = (P, causal, kvr, greedy, scale)
+        ctx.check_status = check_status
+        ctx.mark_non_differentiable(LSE)
+        return O, LSE
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO, dLSE):
+        grads = mesh_diff_attention_backward(*ctx.saved_tensors, dO.contiguous(), *ctx.args, plan=ctx.plan,
+                                             check_status=ctx.check_status)
+        return (*grads, None, None, None, None, None, None, None)
+
+
+def mesh_diff_attention_autograd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, P: int, causal: bool,
+                                 kvr: bool = True, greedy: bool = True, scale: Optional[float] = None,
+                                 plan: Optional[Plan] = None, check_status: bool = True):
+    """mesh_diff_attention with autograd: returns (O, LSE); O.backward(...) fills the gradients of q, k, v and lam."""
+    return MeshDiffAttentionFunction.apply(q, k, v, lam, P, causal, kvr, greedy, scale, plan, check_status)
+
+
+def new_diff_decode_workspace(B: int, Hq: int, Hkv: int, d: int, T: int, device=None) -> torch.Tensor:
+    """Workspace of mesh_diff_decode for these sizes and smaller ones, zeroed as the first call wants it."""
+    load_library()
+    n = c_sz()
+    _check(_lib.mesh_attn_diff_decode_workspace_size(B, Hq, Hkv, d, T, ctypes.byref(n)), "mesh_attn_diff_decode_workspace_size")
+    return torch.zeros(max(n.value, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def mesh_attn_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
+                          lam: torch.Tensor, scale: Optional[float], O: torch.Tensor, LSE: torch.Tensor,
+                          workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    load_library()
+    B, Hq, S, d, dev = _diff_check(q, k_cache, v_cache, lam, O)
+    T = k_cache.shape[2]
+    if S != 1:
+        raise ValueError("q must hold one token a sequence: [B, Hq, 1, d]")
+    if lens.shape != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous():
+        raise ValueError("lens must be contiguous int32 [B]")
+    if O.shape != q.shape or LSE.shape != (B, Hq, 2, 1) or LSE.dtype != torch.float32:
+        raise ValueError("O must have q's shape, LSE must be fp32 [B, Hq, 2, 1]")
+    if not all(t.is_contiguous() for t in (q, lam, O, LSE)):
+        raise ValueError("q, lam, O and LSE must be contiguous")
+    if T and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+        raise ValueError("the columns of the caches must be consecutive")
+    _one_device(q, lens, LSE, workspace, status)
+    with torch.cuda.device(dev):
+        _check(_lib.mesh_attn_diff_decode(_dtype_code(q.dtype), B, Hq, k_cache.shape[1], d, T, _ptr(q), _ptr(k_cache),
+                                          _strides3(k_cache), _ptr(v_cache), _strides3(v_cache), _ptr(lens), _ptr(lam),
+                                          lam.shape[0], _diff_scale(scale, d), _ptr(O), _ptr(LSE), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _ptr(status),
+                                          _stream_handle(stream)), "mesh_attn_diff_decode")
+
+
+def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor, lam: torch.Tensor,
+                     scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, check_status: bool = True):
+    """Differential attention of one new token a sequence, on the current stream: q [B, Hq, 1, d] against the first lens[b]
+    (int32, on the device) tokens of k_cache, v_cache [B, Hkv, T, d], which may be views with other strides (16-byte
+    multiples).  Returns O [B, Hq, 1, d] and LSE [B, Hq, 2, 1].  A serving loop keeps workspace
+    (new_diff_decode_workspace) and status and passes check_status=False."""
+    B, Hq, S, d, dev = _diff_check(q, k_cache, v_cache, lam)
+    ws = new_diff_decode_workspace(B, Hq, k_cache.shape[1], d, k_cache.shape[2], dev) if workspace is None else workspace
+    st = new_status(dev) if status is None else status
+    O = torch.empty_like(q, memory_format=torch.contiguous_format)
+    LSE = torch.empty(B, Hq, 2, 1, dtype=torch.float32, device=dev)
+    mesh_attn_diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, torch.cuda.current_stream(dev))
+    if check_status:
+        _raise_status(st)
+    return O, LSE

@@ -1,0 +1,307 @@
+// Differential attention, the passes around its products: queries and gradients laid out one map a
+// head, the merge of the two maps' partial outputs, the row terms of the backward pass and the
+// gradient of lam.  All are bound by memory and read and write whole 16-byte pieces.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mesh {
+namespace daux {
+
+constexpr int THREADS = 256;
+constexpr int MAX_SLOTS = 64;  // R <= 64 for P <= 4096
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ float lam_of(const void* lam, int n, int h) {
+  return to_f(static_cast<const T*>(lam)[n == 1 ? 0 : h]);
+}
+
+// One map a head: row (b, 2 h + m) of qx is q with the other map's half zeroed, so that plain
+// attention of 2 Hq heads over the full d columns gives both maps; of gx (backward) it is the gradient
+// of the map's output: dO for the first map, -lam dO for the second.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) expand_kernel(const DiffArgs a, T* qx, T* gx) {
+  const TablesHeader* th = static_cast<const TablesHeader*>(a.tables);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
+    record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);
+  const int q4 = a.d / 4;
+  const int64_t n = (int64_t)a.B * a.Hq * a.S * q4;
+  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS) {
+    const int c = (int)(i % q4) * 4;
+    const int64_t row = i / q4;            // (b Hq + h) S + s
+    const int64_t bh = row / a.S, s = row - bh * a.S;
+    const int64_t dst = (2 * bh * a.S + s) * a.d + c, dst2 = dst + a.S * a.d;
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 q = load4(static_cast<const T*>(a.Q) + row * a.d + c);
+    const bool first = c < a.d / 2;
+    store4(qx + dst, first ? q : z);
+    store4(qx + dst2, first ? z : q);
+    if (gx) {
+      const float nl = -lam_of<T>(a.lam, a.lam_n, (int)(bh % a.Hq));
+      const float4 g = load4(static_cast<const T*>(a.dO) + row * a.d + c);
+      store4(gx + dst, g);
+      store4(gx + dst2, make_float4(g.x * nl, g.y * nl, g.z * nl, g.w * nl));
+    }
+  }
+}
+
+// O = sum_t w1_t O1_t - lam sum_t w2_t O2_t over a row's slots, w = exp(lse_t - lse) of each map, and
+// the second map's output, which the backward pass needs.  A CTA owns ROWS rows of one (batch,
+// head, partition); a thread a 16-byte piece of both maps.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const float* part_o, const float* part_lse,
+                                                        const int32_t* slot_off, int n_rblk) {
+  constexpr int Q4 = D / 4;
+  constexpr int PER = 2;
+  constexpr int ROWS = PER * THREADS / Q4;
+  __shared__ float w_s[2][MAX_SLOTS][ROWS];
+  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
+  const int tid = threadIdx.x;
+  const int rb = (int)(blockIdx.x % (unsigned)n_rblk);
+  const int bhp = (int)(blockIdx.x / (unsigned)n_rblk);
+  const int p = bhp % a.P, bh = bhp / a.P;
+  const int64_t L = a.L;
+  const int64_t r0 = (int64_t)rb * ROWS;
+  const int nrows = (int)min((int64_t)ROWS, L - r0);
+  const int s0 = __ldg(slot_off + p), ns = __ldg(slot_off + p + 1) - s0;
+  if (ns < 0 || ns > MAX_SLOTS) {
+    if (tid == 0) record_error(a.status, MESH_ATTN_ERR_OUT_OF_RANGE, 5, (int32_t)blockIdx.x);
+    return;
+  }
+  const int64_t base[2] = {((2 * (int64_t)bh) * a.n_slots + s0) * L + r0, ((2 * (int64_t)bh + 1) * a.n_slots + s0) * L + r0};
+  for (int i = tid; i < 2 * ns * ROWS; i += THREADS) {
+    const int r = i % ROWS, t = i / ROWS % ns, m = i / ROWS / ns;
+    w_s[m][t][r] = r < nrows ? __ldg(part_lse + base[m] + (int64_t)t * L + r) : -INFINITY;
+  }
+  __syncthreads();
+  if (tid < 2 * ROWS) {
+    const int r = tid % ROWS, m = tid / ROWS;
+    float M = -INFINITY;
+    for (int t = 0; t < ns; ++t) M = fmaxf(M, w_s[m][t][r]);
+    const float Ms = M == -INFINITY ? 0.f : M;
+    float W = 0.f;
+    for (int t = 0; t < ns; ++t) {
+      const float e = expf(w_s[m][t][r] - Ms);
+      w_s[m][t][r] = e;
+      W += e;
+    }
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    for (int t = 0; t < ns; ++t) w_s[m][t][r] *= inv;
+    if (r < nrows) a.LSE[(2 * (int64_t)bh + m) * a.S + (int64_t)p * L + r0 + r] = W > 0.f ? Ms + logf(W) : -INFINITY;
+  }
+  __syncthreads();
+  const float lam = lam_of<T>(a.lam, a.lam_n, bh % a.Hq);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int idx = tid + k * THREADS, r = idx / Q4, c = idx % Q4 * 4;
+    if (r >= nrows) continue;
+    float4 o[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      o[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* src = part_o + (base[m] + r) * D + c;
+#pragma unroll 4
+      for (int t = 0; t < ns; ++t) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(src + (int64_t)t * L * D));
+        const float w = w_s[m][t][r];
+        o[m].x = fmaf(w, v.x, o[m].x);
+        o[m].y = fmaf(w, v.y, o[m].y);
+        o[m].z = fmaf(w, v.z, o[m].z);
+        o[m].w = fmaf(w, v.w, o[m].w);
+      }
+    }
+    const int64_t at = ((int64_t)bh * a.S + (int64_t)p * L + r0 + r) * D + c;
+    store4(static_cast<T*>(a.O) + at, make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
+                                                  fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
+    if (a.O2) store4(static_cast<T*>(a.O2) + at, o[1]);
+  }
+}
+
+// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2 (times -lam for the path whose
+// second map receives -lam dO).  One warp a row.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* dsum, float* dlam_part, int64_t n_part,
+                                                       int rows_per_part, int scaled) {
+  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t part = blockIdx.x % n_part;
+  const int64_t bh = blockIdx.x / n_part;
+  const float lam = lam_of<T>(a.lam, a.lam_n, (int)(bh % a.Hq));
+  __shared__ double sums[THREADS / 32];
+  double acc = 0.0;
+  const int64_t s_end = min(a.S, (part + 1) * rows_per_part);
+  for (int64_t s = part * rows_per_part + warp; s < s_end; s += THREADS / 32) {
+    const int64_t row = (bh * a.S + s) * a.d;
+    float d1 = 0.f, d2 = 0.f;
+    for (int c = lane * 4; c < a.d; c += 128) {
+      const float4 g = load4(static_cast<const T*>(a.dO) + row + c);
+      const float4 o = load4(static_cast<const T*>(a.O) + row + c);
+      const float4 o2 = load4(static_cast<const T*>(a.O2) + row + c);
+      d1 += g.x * o.x + g.y * o.y + g.z * o.z + g.w * o.w;
+      d2 += g.x * o2.x + g.y * o2.y + g.z * o2.z + g.w * o2.w;
+    }
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) {
+      d1 += __shfl_xor_sync(0xffffffffu, d1, x);
+      d2 += __shfl_xor_sync(0xffffffffu, d2, x);
+    }
+    if (lane == 0) {
+      dsum[2 * bh * a.S + s] = fmaf(lam, d2, d1);
+      dsum[(2 * bh + 1) * a.S + s] = scaled ? -lam * d2 : d2;
+      acc -= (double)d2;
+    }
+  }
+  if (dlam_part) {  // dlam = -sum D2, in a fixed order
+    if (lane == 0) sums[warp] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double t = 0.0;
+      for (int w = 0; w < THREADS / 32; ++w) t += sums[w];
+      dlam_part[bh * n_part + part] = (float)t;
+    }
+  }
+}
+
+// dQ from the per-map partial sums: the first half of the columns from head 2 h, the second from 2 h + 1.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) reduce_dq_kernel(const DiffArgs a, const float* part, const int32_t* slot_off) {
+  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
+  const int q4 = a.d / 4;
+  const int64_t n = (int64_t)a.B * a.Hq * a.S * q4;
+  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS) {
+    const int c = (int)(i % q4) * 4;
+    const int64_t row = i / q4, bh = row / a.S, s = row - bh * a.S;
+    const int p = (int)(s / a.L);
+    const int s0 = __ldg(slot_off + p), s1 = __ldg(slot_off + p + 1);
+    const int64_t bm = 2 * bh + (c < a.d / 2 ? 0 : 1);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = max(s0, 0); k < min(s1, a.n_slots); ++k) {
+      const float4 v = load4(part + ((bm * a.n_slots + k) * a.L + (s - p * a.L)) * a.d + c);
+      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
+    store4(static_cast<T*>(a.dQ) + row * a.d + c, t);
+  }
+}
+
+// dlam of one value (a head, or all heads where lam is shared): the sum of its partial sums, taken
+// in a fixed order in fp64, since terms of both signs nearly cancel over a long batch.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) dlam_kernel(const DiffArgs a, const float* part, int64_t n_part) {
+  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
+  const int h0 = a.lam_n == 1 ? 0 : (int)blockIdx.x, nh = a.lam_n == 1 ? a.Hq : 1;
+  double acc = 0.0;
+  const int64_t n = (int64_t)a.B * nh * n_part;
+  for (int64_t i = threadIdx.x; i < n; i += THREADS) {
+    const int64_t k = i % n_part, bh = i / n_part, b = bh / nh, h = h0 + bh % nh;
+    acc += (double)part[(b * a.Hq + h) * n_part + k];
+  }
+  __shared__ double s[THREADS];
+  s[threadIdx.x] = acc;
+  __syncthreads();
+  for (int x = THREADS / 2; x >= 1; x >>= 1) {
+    if (threadIdx.x < x) s[threadIdx.x] += s[threadIdx.x + x];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    if constexpr (sizeof(T) == 2) static_cast<T*>(a.dlam)[blockIdx.x] = __float2bfloat16_rn((float)s[0]);
+    else static_cast<T*>(a.dlam)[blockIdx.x] = (float)s[0];
+  }
+}
+
+static int done(const char* what, std::string* err) {
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) *err = std::string(what) + ": " + cudaGetErrorString(e);
+  return (int)e;
+}
+static unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + THREADS - 1) / THREADS, 152 * 16)); }
+
+}  // namespace daux
+
+int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool grad, void* stream,
+                       std::string* err) {
+  const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dt == MESH_ATTN_BF16)
+    daux::expand_kernel<__nv_bfloat16><<<grid, daux::THREADS, 0, st>>>(a, reinterpret_cast<__nv_bfloat16*>(a.ws + w.qx),
+                                                                       grad ? reinterpret_cast<__nv_bfloat16*>(a.ws + w.gx) : nullptr);
+  else
+    daux::expand_kernel<float><<<grid, daux::THREADS, 0, st>>>(a, reinterpret_cast<float*>(a.ws + w.qx),
+                                                               grad ? reinterpret_cast<float*>(a.ws + w.gx) : nullptr);
+  return daux::done("diff expand launch", err);
+}
+
+template <int D, typename T>
+static int merge_d(const DiffArgs& a, const DiffWorkspace& w, cudaStream_t st, std::string* err) {
+  constexpr int ROWS = 2 * daux::THREADS / (D / 4);
+  const int64_t n_rblk = (a.L + ROWS - 1) / ROWS;
+  const int64_t blocks = n_rblk * a.B * a.Hq * a.P;
+  if (blocks > 0x7fffffffLL || n_rblk > 0x7fffffffLL) {
+    *err = "too many rows for one merge launch";
+    return (int)cudaErrorInvalidConfiguration;
+  }
+  daux::merge_kernel<D, T><<<(unsigned)blocks, daux::THREADS, 0, st>>>(
+      a, reinterpret_cast<const float*>(a.ws + w.part_o), reinterpret_cast<const float*>(a.ws + w.part_lse),
+      reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + a.tl.slot_off), (int)n_rblk);
+  return daux::done("diff merge launch", err);
+}
+
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dt == MESH_ATTN_BF16)
+    return a.d == 128 ? merge_d<128, __nv_bfloat16>(a, w, st, err) : merge_d<64, __nv_bfloat16>(a, w, st, err);
+  return a.d == 128 ? merge_d<128, float>(a, w, st, err) : merge_d<64, float>(a, w, st, err);
+}
+
+int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+  cudaStream_t st = (cudaStream_t)stream;
+  const int64_t n_part = w.n_dlam, bh = (int64_t)a.B * a.Hq;
+  const int rows = (int)((a.S + n_part - 1) / n_part);
+  if (n_part * bh > 0x7fffffffLL) {
+    *err = "too many rows for one launch";
+    return (int)cudaErrorInvalidConfiguration;
+  }
+  float* dsum = reinterpret_cast<float*>(a.ws + w.dsum);
+  float* dl = reinterpret_cast<float*>(a.ws + w.dlam_part);
+  if (dt == MESH_ATTN_BF16)
+    daux::prep_kernel<__nv_bfloat16><<<(unsigned)(n_part * bh), daux::THREADS, 0, st>>>(a, dsum, dl, n_part, rows, 1);
+  else
+    daux::prep_kernel<float><<<(unsigned)(n_part * bh), daux::THREADS, 0, st>>>(a, dsum, dl, n_part, rows, 1);
+  return daux::done("diff prep launch", err);
+}
+
+int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+  const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
+  cudaStream_t st = (cudaStream_t)stream;
+  const float* part = reinterpret_cast<const float*>(a.ws + w.dq_part);
+  const int32_t* off = reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + a.tl.slot_off);
+  if (dt == MESH_ATTN_BF16) daux::reduce_dq_kernel<__nv_bfloat16><<<grid, daux::THREADS, 0, st>>>(a, part, off);
+  else daux::reduce_dq_kernel<float><<<grid, daux::THREADS, 0, st>>>(a, part, off);
+  return daux::done("diff dq reduction launch", err);
+}
+
+int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+  cudaStream_t st = (cudaStream_t)stream;
+  const float* part = reinterpret_cast<const float*>(a.ws + w.dlam_part);
+  if (dt == MESH_ATTN_BF16) daux::dlam_kernel<__nv_bfloat16><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, w.n_dlam);
+  else daux::dlam_kernel<float><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, w.n_dlam);
+  return daux::done("diff dlam launch", err);
+}
+
+}  // namespace mesh

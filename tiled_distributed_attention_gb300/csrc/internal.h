@@ -157,6 +157,68 @@ struct ReduceArgs {
 };
 int launch_bwd_reduce(const ReduceArgs& a, mesh_attn_dtype out_dtype, void* stream, std::string* err);
 
+// ---------------------------------------------------------------- differential attention
+// Most CTAs of a one-per-SM grid: sizes workspaces without asking a device (GB300 has 152 SMs).
+constexpr int MAX_SMS = 256;
+
+// A plan's constant tables as the differential calls read them from device memory, in one block:
+// [header | slot_off | items | kv_list | kv_slot_off | kv_items | kv_q_list].  The header's tag says
+// which plan they are of; the first kernel of a call compares it with the plan it was given.
+struct TablesHeader {
+  uint64_t magic, tag;
+};
+constexpr uint64_t TABLES_MAGIC = 0x6d6573685f746162ull;
+struct TablesLayout {
+  size_t slot_off, items, kv_list, kv_slot_off, kv_items, q_list, total;
+};
+TablesLayout tables_layout(const Plan& plan);
+uint64_t plan_tag(const Plan& plan);
+
+struct DiffArgs {
+  const void* Q;
+  const void* K;
+  const void* V;
+  const void* lam;
+  const void* tables;
+  TablesLayout tl;
+  uint64_t tag;
+  int32_t* status;
+  void* O;
+  void* O2;     // forward: may be NULL
+  float* LSE;   // [B, Hq, 2, S]
+  const void* dO;
+  void* dQ;
+  void* dK;
+  void* dV;
+  void* dlam;
+  char* ws;
+  int64_t S, L;
+  int32_t B, Hq, Hkv, d, P, n_slots, n_kv_slots, causal, lam_n;
+  bool single_slot, single_kv_slot;  // every partition has one (KV) slot: no partial sums to merge
+  float scale, scale_log2;
+  int64_t wait_limit_ns;
+};
+// Workspace of the differential calls, by type and direction (bytes from its start).
+struct DiffWorkspace {
+  size_t counters;            // 512 bytes
+  size_t part_o, part_lse;    // forward partials
+  size_t qx, pieces;          // fp32: q of each map with the other half zeroed; the forward's bf16 pieces
+  size_t gx;                  // fp32 backward: the gradients that reach each map's output
+  size_t dsum;                // [B, 2 Hq, S] row terms of dS
+  size_t dlam_part;           // [B, Hq, n_dlam]
+  size_t dq_part, dk_part, dv_part;
+  int64_t n_dlam;
+  size_t total;
+};
+DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
+                             bool backward);
+int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool grad, void* stream,
+                       std::string* err);
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
+int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
+int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
+int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
+
 // Record `msg` as the calling thread's last error (mesh_attn_last_error) and return `code`.
 int set_last_error(int code, const std::string& msg);
 // Current process-wide bound on device-side waits (mesh_attn_set_wait_limit_ns).

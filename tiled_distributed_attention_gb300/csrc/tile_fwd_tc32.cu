@@ -67,7 +67,7 @@ struct Params {
   float* part_lse;
   int32_t* status;
   int64_t S, L;
-  int64_t q_rows, kv_rows;  // rows of one piece: B*Hq*S and B*Hkv*S
+  int64_t q_rows, kv_parts;  // of one piece: rows of Q, B*Hq*S, and partitions of K and V, B*Hkv*P
   const uint32_t* q_pieces;  // Q's bf16 pieces [3][q_rows][D], as packed pairs
   int32_t B, Hq, Hkv, P, n_items, n_slots, nqt, nb, causal;
   float scale_log2;
@@ -464,19 +464,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tma_load_2d(sb + Ly::Q_OFF + (uint32_t)c * Ly::QBOX, &tmQ, c * 64, (int32_t)(qrow + 2 * prm.q_rows),
                     bar(Ly::B_QFULL));
     }
-    const int64_t kvbase = ((int64_t)b * prm.Hkv + hk) * prm.S;
+    const int64_t kvpart = ((int64_t)b * prm.Hkv + hk) * prm.P;  // the KV head's first partition
     // Two K stages and two V stages.  Products run S(0), S(1), PV(0), S(2), PV(1), S(3), ...; K(j)
     // takes the stage S(j-2) frees and V(j) the one PV(j-2) frees, so the loads follow the
     // products' completion order: K(0), K(1), V(0), V(1), K(2), then K(j), V(j-1) for j >= 3, then
     // the last V.
-    auto load_pieces = [&](const CUtensorMap* tm, uint32_t off, int64_t krow, uint32_t fullbar) {
+    auto load_pieces = [&](const CUtensorMap* tm, uint32_t off, int64_t part, int row, uint32_t fullbar) {
       mbar_expect_tx(fullbar, 3 * Ly::KP);
       for (int a = 0; a < 3; ++a)
         for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sb + off + (uint32_t)a * Ly::KP + (uint32_t)c * Ly::KBOX, tm, c * 64,
-                      (int32_t)(krow + (int64_t)a * prm.kv_rows), fullbar);
+          tma_load_3d(sb + off + (uint32_t)a * Ly::KP + (uint32_t)c * Ly::KBOX, tm, c * 64, row,
+                      (int32_t)(part + (int64_t)a * prm.kv_parts), fullbar);
     };
-    auto row_of = [&](int j, int64_t& krow) -> bool {
+    auto row_of = [&](int j, int64_t& part, int& row) -> bool {
       int kp, kbk;
       block_at(j, kp, kbk);
       if (kp < 0 || kp >= prm.P) {
@@ -484,28 +484,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         *abort_flag = 1;
         return false;
       }
-      krow = kvbase + (int64_t)kp * L + (int64_t)kbk * BN;
+      part = kvpart + kp;
+      row = kbk * BN;
       return true;
     };
     auto load_k = [&](int j) -> bool {
-      int64_t krow;
-      if (!row_of(j, krow)) return false;
+      int64_t part;
+      int row;
+      if (!row_of(j, part, row)) return false;
       const int ks = j & 1;
       if (j >= 2 && !mbar_wait(bar(Ly::B_KEMPTY + ks), (uint32_t)(((j - 2) >> 1) & 1), prm.wait_limit_ns, abort_flag,
                                prm.status, ROLE_LOAD, j))
         return false;
-      load_pieces(&tmK, Ly::K_OFF + (uint32_t)ks * Ly::KSTAGE, krow, bar(Ly::B_KFULL + ks));
+      load_pieces(&tmK, Ly::K_OFF + (uint32_t)ks * Ly::KSTAGE, part, row, bar(Ly::B_KFULL + ks));
       ++issued_k;
       return true;
     };
     auto load_v = [&](int j) -> bool {
-      int64_t krow;
-      if (!row_of(j, krow)) return false;
+      int64_t part;
+      int row;
+      if (!row_of(j, part, row)) return false;
       const int vs = j & 1;
       if (j >= 2 && !mbar_wait(bar(Ly::B_VEMPTY + vs), (uint32_t)(((j - 2) >> 1) & 1), prm.wait_limit_ns, abort_flag,
                                prm.status, ROLE_LOAD, j))
         return false;
-      load_pieces(&tmV, Ly::V_OFF + (uint32_t)vs * Ly::KSTAGE, krow, bar(Ly::B_VFULL + vs));
+      load_pieces(&tmV, Ly::V_OFF + (uint32_t)vs * Ly::KSTAGE, part, row, bar(Ly::B_VFULL + vs));
       ++issued_v;
       return true;
     };
@@ -593,6 +596,24 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
   return true;
 }
 
+// The same rows as [partitions][L rows][d]: a box that reaches past a partition's end gets zeros there
+// and not the next head's or batch's rows, whose infinities a weight of 0 would turn into NaN.
+static bool make_part_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64_t L, uint64_t parts, int d,
+                          int box_rows, std::string* err) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)L * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return false;
+  }
+  return true;
+}
+
 static int split(const float* x, void* out, int64_t n, int32_t* status, cudaStream_t st, std::string* err) {
   const int64_t n4 = n / 4;
   if (n4 <= 0) return (int)cudaSuccess;
@@ -631,8 +652,8 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   if (!enc) return (int)cudaErrorNotSupported;
   CUtensorMap mq, mk, mv;
   if (!make_map(enc, &mq, base + pc.q_off, (uint64_t)(3 * q_rows), D, BM, err) ||
-      !make_map(enc, &mk, base + pc.k_off, (uint64_t)(3 * kv_rows), D, BN, err) ||
-      !make_map(enc, &mv, base + pc.v_off, (uint64_t)(3 * kv_rows), D, BN, err))
+      !make_part_map(enc, &mk, base + pc.k_off, (uint64_t)a.L, (uint64_t)(3 * kv_rows / a.L), D, BN, err) ||
+      !make_part_map(enc, &mv, base + pc.v_off, (uint64_t)a.L, (uint64_t)(3 * kv_rows / a.L), D, BN, err))
     return (int)cudaErrorInvalidValue;
   Params prm;
   prm.items = a.items;
@@ -643,7 +664,7 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   prm.S = a.S;
   prm.L = a.L;
   prm.q_rows = q_rows;
-  prm.kv_rows = kv_rows;
+  prm.kv_parts = (int64_t)a.B * a.Hkv * a.P;
   prm.q_pieces = reinterpret_cast<const uint32_t*>(base + pc.q_off);
   prm.B = a.B;
   prm.Hq = a.Hq;
