@@ -217,7 +217,7 @@ def test_same_bits_each_time_and_what_surrounds(lib, dtype, P):
 def test_neighbours_nan_stays_out(lib):
     """NaN and infinities in another head, batch or partition's padding never reach a result: L = 100 is no multiple
     of a tile, so tiles reach past a partition's end."""
-    for dtype in ("f32",):
+    for dtype in ("bf16", "f32"):
         q, k, v, lam, g = inputs(2, 2, 2, 400, 128, dtype, 28)
         bad = [t.clone() for t in (q, k, v, g)]
         for t in bad:

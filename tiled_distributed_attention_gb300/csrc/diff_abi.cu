@@ -22,6 +22,8 @@ TablesLayout tables_layout(const Plan& p) {
     at = up(at + bytes, 16);
     return o;
   };
+  t.flat_item = take(sizeof(DevItem));
+  t.flat_list = take(2 * 4);
   t.slot_off = take(p.slot_off.size() * 4);
   t.items = take(p.dev_items.size() * sizeof(DevItem));
   t.kv_list = take(p.kv_list.size() * 4);
@@ -52,12 +54,16 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
   const size_t qrows = (size_t)B * Hq * plan.S;
   const size_t prows = (size_t)B * Hq * plan.n_slots() * (size_t)plan.L;
   w.n_dlam = std::max<int64_t>(1, (plan.S + 63) / 64);
-  w.qx = take(2 * qrows * d * es);
   if (!backward) {
-    w.part_o = take(2 * prows * d * 4);
-    w.part_lse = take(2 * prows * 4);
+    // bf16 needs partials only where the plan's slots split the keys (diff_fwd_direct)
+    if (dt == MESH_ATTN_F32 || (plan.n_slots() != plan.P && (plan.S + 127) / 128 * B * Hq < MAX_SMS)) {
+      w.part_o = take(2 * prows * d * 4);
+      w.part_lse = take(2 * prows * 4);
+    }
+    if (dt == MESH_ATTN_F32) w.qx = take(2 * qrows * d * es);
     if (dt == MESH_ATTN_F32) w.pieces = take(f32_pieces_layout(B, 2 * Hq, Hkv, plan.S, d).total);
   } else {
+    w.qx = take(2 * qrows * d * es);
     w.gx = take(2 * qrows * d * es);
     w.dsum = take(2 * qrows * 4);
     w.dlam_part = take((size_t)B * Hq * w.n_dlam * 4);
@@ -105,6 +111,14 @@ int check_common(const DiffArgs& a, mesh_attn_dtype dt, const void* workspace, s
     return set_last_error(MESH_ATTN_ERR_MISALIGNED, "LSE, lam and status must be aligned to their element size");
   if (workspace_bytes < need)
     return set_last_error(MESH_ATTN_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  return MESH_ATTN_OK;
+}
+
+int sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_last_error(MESH_ATTN_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
   return MESH_ATTN_OK;
 }
 
@@ -170,6 +184,10 @@ int mesh_attn_plan_tables_write(const mesh_attn_plan* plan, void* out, size_t ou
     auto put = [&](size_t off, const void* src, size_t bytes) {
       if (bytes) std::memcpy(o + off, src, bytes);
     };
+    const mesh::DevItem flat{0, 0, 0, 1};
+    const int32_t list[2] = {0, 1};  // its KV partition, and as a slot CSR {0, 1}
+    put(t.flat_item, &flat, sizeof(flat));
+    put(t.flat_list, list, sizeof(list));
     put(t.slot_off, p.slot_off.data(), p.slot_off.size() * 4);
     put(t.items, p.dev_items.data(), p.dev_items.size() * sizeof(mesh::DevItem));
     put(t.kv_list, p.kv_list.data(), p.kv_list.size() * 4);
@@ -206,9 +224,11 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     rc = check_common(a, dtype, workspace, workspace_bytes, w.total);
     if (rc) return rc;
     std::string err;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(a.ws + w.counters, 0, 512, st);
-    if (e != cudaSuccess) return launch_status((int)e, std::string("counter reset: ") + cudaGetErrorString(e));
+    if (dtype == MESH_ATTN_BF16) {
+      int sms = 0;
+      if ((rc = sm_count(&sms))) return rc;
+      return launch_status(mesh::launch_diff_fwd_tc(a, w, sms, stream, &err), err);
+    }
     if ((rc = launch_status(mesh::launch_diff_expand(a, w, dtype, false, stream, &err), err))) return rc;
     mesh::TileArgs t{};
     const char* tb = static_cast<const char*>(tables);
@@ -219,7 +239,6 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     t.part_lse = reinterpret_cast<float*>(a.ws + w.part_lse);
     t.items = reinterpret_cast<const mesh::DevItem*>(tb + a.tl.items);
     t.kv_list = reinterpret_cast<const int32_t*>(tb + a.tl.kv_list);
-    t.counter = reinterpret_cast<uint32_t*>(a.ws + w.counters);
     t.status = d_status;
     t.S = a.S;
     t.L = a.L;
@@ -235,9 +254,7 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     t.scale_log2 = a.scale_log2;
     t.wait_limit_ns = a.wait_limit_ns;
     t.pieces = a.ws + w.pieces;
-    const int ce = dtype == MESH_ATTN_BF16 ? mesh::launch_tile_fwd_tc(t, stream, &err)
-                                           : mesh::launch_tile_fwd_tc32(t, stream, &err);
-    if ((rc = launch_status(ce, err))) return rc;
+    if ((rc = launch_status(mesh::launch_tile_fwd_tc32(t, stream, &err), err))) return rc;
     return launch_status(mesh::launch_diff_merge(a, w, dtype, stream, &err), err);
   });
 }

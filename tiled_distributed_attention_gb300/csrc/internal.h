@@ -162,13 +162,14 @@ int launch_bwd_reduce(const ReduceArgs& a, mesh_attn_dtype out_dtype, void* stre
 constexpr int MAX_SMS = 256;
 
 // A plan's constant tables as the differential calls read them from device memory, in one block:
-// [header | slot_off | items | kv_list | kv_slot_off | kv_items | kv_q_list].  The header's tag says
+// [header | flat item and lists | slot_off | items | kv_list | kv_slot_off | kv_items | kv_q_list].  The header's tag says
 // which plan they are of; the first kernel of a call compares it with the plan it was given.
 struct TablesHeader {
   uint64_t magic, tag;
 };
 constexpr uint64_t TABLES_MAGIC = 0x6d6573685f746162ull;
 struct TablesLayout {
+  size_t flat_item, flat_list;  // the whole sequence as one partition and one work item
   size_t slot_off, items, kv_list, kv_slot_off, kv_items, q_list, total;
 };
 TablesLayout tables_layout(const Plan& plan);
@@ -212,6 +213,8 @@ struct DiffWorkspace {
 };
 DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                              bool backward);
+// bf16 forward on the tensor cores, with its merge where the plan's slots split the keys.
+int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
 int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool grad, void* stream,
                        std::string* err);
 int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
