@@ -50,30 +50,39 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
     at = up(at + bytes, 256);
     return o;
   };
-  const size_t es = dt == MESH_ATTN_BF16 ? 2 : 4;
   const size_t qrows = (size_t)B * Hq * plan.S;
   const size_t prows = (size_t)B * Hq * plan.n_slots() * (size_t)plan.L;
-  w.n_dlam = std::max<int64_t>(1, (plan.S + 63) / 64);
+  const bool f32 = dt == MESH_ATTN_F32;
+  // bf16 needs partial sums only where the plan's slots split an axis (rows_direct)
+  const int64_t tiles = (plan.S + 127) / 128 * B;
+  const bool q_part = f32 || (plan.n_slots() != plan.P && tiles * Hq < MAX_SMS);
+  const bool kv_part = f32 || (plan.n_kv_slots() != plan.P && tiles * Hkv < MAX_SMS);
+  if (f32) w.qx = take(2 * qrows * d * 4);
   if (!backward) {
-    // bf16 needs partials only where the plan's slots split the keys (diff_fwd_direct)
-    if (dt == MESH_ATTN_F32 || (plan.n_slots() != plan.P && (plan.S + 127) / 128 * B * Hq < MAX_SMS)) {
+    if (q_part) {
       w.part_o = take(2 * prows * d * 4);
       w.part_lse = take(2 * prows * 4);
     }
-    if (dt == MESH_ATTN_F32) w.qx = take(2 * qrows * d * es);
-    if (dt == MESH_ATTN_F32) w.pieces = take(f32_pieces_layout(B, 2 * Hq, Hkv, plan.S, d).total);
+    if (f32) w.pieces = take(f32_pieces_layout(B, 2 * Hq, Hkv, plan.S, d).total);
   } else {
-    w.qx = take(2 * qrows * d * es);
-    w.gx = take(2 * qrows * d * es);
+    if (f32) w.gx = take(2 * qrows * d * 4);
     w.dsum = take(2 * qrows * 4);
-    w.dlam_part = take((size_t)B * Hq * w.n_dlam * 4);
-    w.dq_part = take(2 * prows * d * 4);
-    const size_t kv = (size_t)B * Hkv * plan.n_kv_slots() * (size_t)plan.L * d * 4;
-    w.dk_part = take(kv);
-    w.dv_part = take(kv);
+    // per (batch, head): fp32 one sum per 64 rows; bf16 eight per 128-row block of every slot
+    const int64_t by_slot = (int64_t)plan.n_slots() * ((plan.L + 127) / 128) * 8, flat = (plan.S + 127) / 128 * 8;
+    w.dlam_part = take((size_t)B * Hq * 4 * (size_t)(f32 ? (plan.S + 63) / 64 : q_part ? std::max(by_slot, flat) : flat));
+    if (q_part) w.dq_part = take((f32 ? 2 : 1) * prows * d * 4);
+    if (kv_part) {
+      const size_t kv = (size_t)B * Hkv * plan.n_kv_slots() * (size_t)plan.L * d * 4;
+      w.dk_part = take(kv);
+      w.dv_part = take(kv);
+    }
   }
   w.total = at;
   return w;
+}
+
+bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms) {
+  return single || (a.S + 127) / 128 * a.B * H >= sms;
 }
 
 }  // namespace mesh
@@ -229,7 +238,7 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
       if ((rc = sm_count(&sms))) return rc;
       return launch_status(mesh::launch_diff_fwd_tc(a, w, sms, stream, &err), err);
     }
-    if ((rc = launch_status(mesh::launch_diff_expand(a, w, dtype, false, stream, &err), err))) return rc;
+    if ((rc = launch_status(mesh::launch_diff_expand(a, w, false, stream, &err), err))) return rc;
     mesh::TileArgs t{};
     const char* tb = static_cast<const char*>(tables);
     t.Q = a.ws + w.qx;
@@ -285,12 +294,40 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     if (!is_aligned(dlam, dtype == MESH_ATTN_BF16 ? 2 : 4))
       return set_last_error(MESH_ATTN_ERR_MISALIGNED, "dlam must be aligned to its element size");
     std::string err;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaMemsetAsync(a.ws + w.counters, 0, 512, st);
-    if (e != cudaSuccess) return launch_status((int)e, std::string("counter reset: ") + cudaGetErrorString(e));
-    if ((rc = launch_status(mesh::launch_diff_expand(a, w, dtype, true, stream, &err), err))) return rc;
-    if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
     const char* tb = static_cast<const char*>(tables);
+    auto reduce = [&](size_t part, size_t off, void* out, int32_t H, int32_t n) -> int {
+      mesh::ReduceArgs r{};
+      r.part = reinterpret_cast<const float*>(a.ws + part);
+      r.off = reinterpret_cast<const int32_t*>(tb + off);
+      r.out = out;
+      r.status = d_status;
+      r.S = a.S;
+      r.L = a.L;
+      r.B = B;
+      r.H = H;
+      r.d = d;
+      r.P = a.P;
+      r.n_slots = n;
+      return launch_status(mesh::launch_bwd_reduce(r, dtype, stream, &err), err);
+    };
+    if (dtype == MESH_ATTN_BF16) {
+      int sms = 0;
+      if ((rc = sm_count(&sms))) return rc;
+      const bool dq_direct = mesh::rows_direct(a, Hq, a.single_slot, sms);
+      const bool kv_direct = mesh::rows_direct(a, Hkv, a.single_kv_slot, sms);
+      if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
+      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, true, kv_direct, stream, &err), err))) return rc;
+      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, false, dq_direct, stream, &err), err))) return rc;
+      if (!kv_direct) {
+        if ((rc = reduce(w.dk_part, a.tl.kv_slot_off, dK, Hkv, a.n_kv_slots))) return rc;
+        if ((rc = reduce(w.dv_part, a.tl.kv_slot_off, dV, Hkv, a.n_kv_slots))) return rc;
+      }
+      if (!dq_direct && (rc = reduce(w.dq_part, a.tl.slot_off, dQ, Hq, a.n_slots))) return rc;
+      const int64_t n = dq_direct ? (a.S + 127) / 128 * 8 : a.n_slots * ((a.L + 127) / 128) * 8;
+      return launch_status(mesh::launch_diff_dlam(a, w, dtype, n, stream, &err), err);
+    }
+    if ((rc = launch_status(mesh::launch_diff_expand(a, w, true, stream, &err), err))) return rc;
+    if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
     mesh::BwdArgs t{};
     t.Q = a.ws + w.qx;
     t.K = K;
@@ -305,7 +342,6 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     t.kv_list = reinterpret_cast<const int32_t*>(tb + a.tl.kv_list);
     t.kv_items = reinterpret_cast<const mesh::DevItem*>(tb + a.tl.kv_items);
     t.q_list = reinterpret_cast<const int32_t*>(tb + a.tl.q_list);
-    t.counters = reinterpret_cast<uint32_t*>(a.ws + w.counters);
     t.status = d_status;
     t.S = a.S;
     t.L = a.L;
@@ -322,30 +358,11 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     t.scale = scale;
     t.scale_log2 = a.scale_log2;
     t.wait_limit_ns = a.wait_limit_ns;
-    const int ce = dtype == MESH_ATTN_BF16 ? mesh::launch_tile_bwd_tc(t, stream, &err)
-                                           : mesh::launch_tile_bwd_simt(t, stream, &err);
-    if ((rc = launch_status(ce, err))) return rc;
-    if ((rc = launch_status(mesh::launch_diff_reduce_dq(a, w, dtype, stream, &err), err))) return rc;
-    struct Job {
-      const float* part;
-      void* out;
-    };
-    for (const Job& j : {Job{t.dk_part, dK}, Job{t.dv_part, dV}}) {
-      mesh::ReduceArgs r{};
-      r.part = j.part;
-      r.off = reinterpret_cast<const int32_t*>(tb + a.tl.kv_slot_off);
-      r.out = j.out;
-      r.status = d_status;
-      r.S = a.S;
-      r.L = a.L;
-      r.B = B;
-      r.H = Hkv;
-      r.d = d;
-      r.P = a.P;
-      r.n_slots = a.n_kv_slots;
-      if ((rc = launch_status(mesh::launch_bwd_reduce(r, dtype, stream, &err), err))) return rc;
-    }
-    return launch_status(mesh::launch_diff_dlam(a, w, dtype, stream, &err), err);
+    if ((rc = launch_status(mesh::launch_tile_bwd_simt(t, stream, &err), err))) return rc;
+    if ((rc = launch_status(mesh::launch_diff_reduce_dq(a, w, stream, &err), err))) return rc;
+    if ((rc = reduce(w.dk_part, a.tl.kv_slot_off, dK, Hkv, a.n_kv_slots))) return rc;
+    if ((rc = reduce(w.dv_part, a.tl.kv_slot_off, dV, Hkv, a.n_kv_slots))) return rc;
+    return launch_status(mesh::launch_diff_dlam(a, w, dtype, (a.S + 63) / 64, stream, &err), err);
   });
 }
 

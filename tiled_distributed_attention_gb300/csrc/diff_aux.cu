@@ -36,8 +36,8 @@ __device__ __forceinline__ float lam_of(const void* lam, int n, int h) {
 // One map a head: row (b, 2 h + m) of qx is q with the other map's half zeroed, so that plain
 // attention of 2 Hq heads over the full d columns gives both maps; of gx (backward) it is the gradient
 // of the map's output: dO for the first map, -lam dO for the second.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) expand_kernel(const DiffArgs a, T* qx, T* gx) {
+__global__ void __launch_bounds__(THREADS) expand_kernel(const DiffArgs a, float* qx, float* gx) {
+  using T = float;
   const TablesHeader* th = static_cast<const TablesHeader*>(a.tables);
   if (blockIdx.x == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
     record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* 
 }
 
 // dQ from the per-map partial sums: the first half of the columns from head 2 h, the second from 2 h + 1.
-template <typename T>
 __global__ void __launch_bounds__(THREADS) reduce_dq_kernel(const DiffArgs a, const float* part, const int32_t* slot_off) {
+  using T = float;
   if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
   const int q4 = a.d / 4;
   const int64_t n = (int64_t)a.B * a.Hq * a.S * q4;
@@ -234,16 +234,10 @@ static unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std:
 
 }  // namespace daux
 
-int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool grad, void* stream,
-                       std::string* err) {
+int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, bool grad, void* stream, std::string* err) {
   const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
-  cudaStream_t st = (cudaStream_t)stream;
-  if (dt == MESH_ATTN_BF16)
-    daux::expand_kernel<__nv_bfloat16><<<grid, daux::THREADS, 0, st>>>(a, reinterpret_cast<__nv_bfloat16*>(a.ws + w.qx),
-                                                                       grad ? reinterpret_cast<__nv_bfloat16*>(a.ws + w.gx) : nullptr);
-  else
-    daux::expand_kernel<float><<<grid, daux::THREADS, 0, st>>>(a, reinterpret_cast<float*>(a.ws + w.qx),
-                                                               grad ? reinterpret_cast<float*>(a.ws + w.gx) : nullptr);
+  daux::expand_kernel<<<grid, daux::THREADS, 0, (cudaStream_t)stream>>>(
+      a, reinterpret_cast<float*>(a.ws + w.qx), grad ? reinterpret_cast<float*>(a.ws + w.gx) : nullptr);
   return daux::done("diff expand launch", err);
 }
 
@@ -271,36 +265,35 @@ int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype
 
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
-  const int64_t n_part = w.n_dlam, bh = (int64_t)a.B * a.Hq;
-  const int rows = (int)((a.S + n_part - 1) / n_part);
-  if (n_part * bh > 0x7fffffffLL) {
+  constexpr int ROWS = 64;
+  const int64_t n_part = (a.S + ROWS - 1) / ROWS, blocks = n_part * a.B * a.Hq;
+  if (blocks > 0x7fffffff) {
     *err = "too many rows for one launch";
     return (int)cudaErrorInvalidConfiguration;
   }
   float* dsum = reinterpret_cast<float*>(a.ws + w.dsum);
-  float* dl = reinterpret_cast<float*>(a.ws + w.dlam_part);
   if (dt == MESH_ATTN_BF16)
-    daux::prep_kernel<__nv_bfloat16><<<(unsigned)(n_part * bh), daux::THREADS, 0, st>>>(a, dsum, dl, n_part, rows, 1);
+    daux::prep_kernel<__nv_bfloat16><<<(unsigned)blocks, daux::THREADS, 0, st>>>(a, dsum, nullptr, n_part, ROWS, 0);
   else
-    daux::prep_kernel<float><<<(unsigned)(n_part * bh), daux::THREADS, 0, st>>>(a, dsum, dl, n_part, rows, 1);
+    daux::prep_kernel<float><<<(unsigned)blocks, daux::THREADS, 0, st>>>(
+        a, dsum, reinterpret_cast<float*>(a.ws + w.dlam_part), n_part, ROWS, 1);
   return daux::done("diff prep launch", err);
 }
 
-int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err) {
   const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
-  cudaStream_t st = (cudaStream_t)stream;
-  const float* part = reinterpret_cast<const float*>(a.ws + w.dq_part);
-  const int32_t* off = reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + a.tl.slot_off);
-  if (dt == MESH_ATTN_BF16) daux::reduce_dq_kernel<__nv_bfloat16><<<grid, daux::THREADS, 0, st>>>(a, part, off);
-  else daux::reduce_dq_kernel<float><<<grid, daux::THREADS, 0, st>>>(a, part, off);
+  daux::reduce_dq_kernel<<<grid, daux::THREADS, 0, (cudaStream_t)stream>>>(
+      a, reinterpret_cast<const float*>(a.ws + w.dq_part),
+      reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + a.tl.slot_off));
   return daux::done("diff dq reduction launch", err);
 }
 
-int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,
+                     std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
   const float* part = reinterpret_cast<const float*>(a.ws + w.dlam_part);
-  if (dt == MESH_ATTN_BF16) daux::dlam_kernel<__nv_bfloat16><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, w.n_dlam);
-  else daux::dlam_kernel<float><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, w.n_dlam);
+  if (dt == MESH_ATTN_BF16) daux::dlam_kernel<__nv_bfloat16><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, n_part);
+  else daux::dlam_kernel<float><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, n_part);
   return daux::done("diff dlam launch", err);
 }
 

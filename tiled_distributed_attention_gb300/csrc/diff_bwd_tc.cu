@@ -1,0 +1,1156 @@
+// Differential attention backward on the 5th-generation tensor cores (sm_103a), bf16 inputs.
+//
+// With P_m = exp(scale q_m.k_m - LSE_m), dP = dO V^T (one product for both maps) and D_m = dO . O_m:
+//   A = P_1 - lam P_2,            dV = A^T dO,
+//   dS_1 = P_1 (dP - D_1),        dS_2 = -lam P_2 (dP - D_2),
+//   dq_m = scale dS_m k_m,        dk_m = scale dS_m^T q_m,        dlam = -sum P_2 dP.
+// Both maps of a block share dP, and their halves of the columns fill one product of the plain backward
+// pass, so a block costs the tensor cores what plain attention of the same d costs; the exponentials
+// are twice as many.  (The last sum is D_2 summed over the rows, taken from fp32 products instead of
+// the rounded O_2: it nearly cancels over a batch, which a rounded operand would show.)
+//
+// Two persistent kernels after the plain backward pass's pattern: one CTA per SM, units from a counter
+// through a two-entry shared-memory ring, every role in warps of its own:
+//   warps 0-7   elementwise: two warps per TMEM lane quadrant, each taking 32 of a block's 64 columns
+//   warp 8      MMA issuer, warp 9 producer (TMA), warps 10-11 idle
+//   warps 12-15 (dq) copy each unit's Q and dO into TMEM, and drain and store dQ
+// The streamed blocks are 64 rows deep, half of the plain pass's: two score maps, dP and the
+// accumulators then fit the 512 TMEM columns at d = 128.
+//
+// dkdv (unit = KV slot, batch, KV head, 128-key block): K and V stay in shared memory, Q and dO blocks
+// of 64 query rows stream.  TMEM: S_1^T | S_2^T | dP^T | A^T (two buffers) | dV | dK_1 | dK_2.
+//   Issue order per block i: [S(i) read] S(i+1)   [A(i) ready] dV(i)   [dS(i) ready] dK(i), dP(i+1).
+//   dS_1 and dS_2 (bf16) replace dP in its own columns.
+// dq (unit = work item, batch, head, 128-row block): Q and dO are copied into TMEM once per unit and
+// feed the products as A operands; K and V blocks of 64 keys stream.  TMEM: S_1 | S_2 | dP (two
+// buffers) | dQ_1 | dQ_2 | Q | dO.
+//   Issue order per block j: [S(j) read] S(j+1), dP(j+1)   [dS(j) ready] dQ(j).
+// At d = 64 a map's half is 32 columns: dK_m and dQ_m are computed 64 wide and half of them is used.
+//
+// Work items: the whole sequence where its blocks alone fill the GPU; the gradients are then written
+// from the accumulators, rounded once.  With fewer blocks the plan's slots split the other axis and
+// fp32 partial sums go to the reductions.  Rows past a partition's end are loaded as zeros.
+// A, dS_1 and dS_2 are rounded to bf16 for their products (2^-9 relative a term); sums are fp32.
+// Every mbarrier wait is bounded; a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT, the CTA stops,
+// drains its copies and products and frees its tensor memory.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace mesh {
+namespace dbtc {
+
+constexpr int BM = 128;  // resident rows = TMEM lanes
+constexpr int BS = 64;   // streamed rows per block = columns of a score block
+constexpr int NUM_THREADS = 512;
+constexpr int N_EW = 8;  // elementwise warps: two per TMEM lane quadrant, 32 columns each
+constexpr int WARP_MMA = 8;
+constexpr int WARP_LOAD = 9;
+constexpr int WARP_EPI = 12;
+constexpr int N_EPI = 4;
+// Register budgets after setmaxnreg, per warpgroup: elementwise (warps 0-7), MMA / producer (8-11),
+// epilogue (12-15).  They add up to the 512 x 128 registers of the launch; the launcher checks
+// the kernels' register count against that before launching.
+constexpr int EW_REGS = 168, MMA_REGS = 104, EPI_REGS = 72;
+static_assert(2 * 128 * EW_REGS + 128 * MMA_REGS + 128 * EPI_REGS <= NUM_THREADS * 128, "register split");
+constexpr int64_t DRAIN_NS = 200000000;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4, ROLE_EPI = 5;
+// TMEM columns
+constexpr uint32_t COL_S = 0;     // S_1 [64], S_2 [64]
+constexpr uint32_t COL_DP = 128;  // dP [64] (dq: two buffers); dS_1, dS_2 (bf16) in its place
+constexpr uint32_t COL_A = 192;   // dkdv: A^T (bf16), two buffers of 32
+constexpr uint32_t COL_ACC = 256; // dkdv: dV [D]; dq: dQ_1 [64], dQ_2 [64]
+constexpr uint32_t COL_DK = 384;  // dkdv: dK_1 [64], dK_2 [64]
+constexpr uint32_t COL_Q = 384;   // dq: Q [D / 2], then dO [D / 2] (bf16)
+// dS_m of column half hf (32 columns) lies in packed columns [32 hf + 16 m, + 16) of its dP region: inside
+// the half's own input columns.  K-step kk (16 elements, 8 packed columns) of dS_m:
+__device__ __forceinline__ uint32_t ds_col(int m, int kk) { return (uint32_t)((kk >> 1) * 32 + m * 16 + (kk & 1) * 8); }
+
+struct Params {
+  const TablesHeader* header;
+  uint64_t tag;
+  const DevItem* items;  // rows: {p, slot, kv_off, n_kv}, or columns: {k, kv slot, q_off, n_q}
+  const int32_t* list;
+  const float* lse;   // [B, Hq, 2, S]
+  const float* dsum;  // [B, Hq, 2, S]
+  const __nv_bfloat16* lam;
+  __nv_bfloat16* out0;  // direct: dQ, or dK
+  __nv_bfloat16* out1;  //         dV
+  float* part0;         // through the reductions (NULL otherwise): dQ, or dK
+  float* part1;         //         dV
+  float* dlam_part;     // [B, Hq, n_slots, nb, N_EW]
+  int32_t* status;
+  uint32_t* counter;
+  int64_t S, L;
+  int32_t B, Hq, Hkv, P, n_items, n_slots, nb, ns, causal, n_units, lam_n;  // nb 128-row blocks, ns 64-row blocks
+  float scale, scale_log2;
+  int64_t wait_limit_ns;
+};
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t TILE = BM * D * 2;  // resident 128-row block
+  static constexpr uint32_t BOX = BM * 64 * 2;  // its 64-column boxes
+  static constexpr uint32_t SBLK = BS * D * 2;  // streamed 64-row block
+  static constexpr uint32_t SBOX = BS * 64 * 2;
+  static constexpr int NSA = 4, NSB = 4;
+  static constexpr uint32_t RES0 = 0, RES1 = TILE;
+  static constexpr uint32_t A0 = 2 * TILE;              // Q (dkdv) or K (dq) stages
+  static constexpr uint32_t B0 = A0 + NSA * SBLK;       // dO (dkdv) or V (dq) stages
+  static constexpr uint32_t VEC_OFF = B0 + NSB * SBLK;  // dkdv: -LSE_1, -LSE_2 (base 2), -D_1, -D_2: [2][4][64] fp32
+  static constexpr uint32_t BAR_OFF = VEC_OFF + 2 * 4 * BS * 4;
+  static constexpr int B_RES = 0, B_AF = 1, B_AE = B_AF + NSA, B_BF = B_AE + NSA, B_BE = B_BF + NSB,
+                       B_S = B_BE + NSB, B_SREAD = B_S + 1, B_DP = B_SREAD + 1, B_A = B_DP + 2, B_DS = B_A + 1,
+                       B_ACC = B_DS + 1, B_ACCE = B_ACC + 1, B_DRAIN = B_ACCE + 1, B_VEC = B_DRAIN + 1,
+                       B_RESE = B_VEC + 2, B_UF = B_RESE + 1, B_UE = B_UF + 2, B_QTF = B_UE + 2, B_QTE = B_QTF + 1,
+                       NBARS = B_QTE + 1;
+  static constexpr uint32_t MISC_OFF = BAR_OFF + NBARS * 8 + (NBARS % 2) * 8;  // tmem base, abort flag
+  static constexpr uint32_t RING_OFF = MISC_OFF + 16;  // unit ring: 2 decoded units, 16 ints each
+  static constexpr uint32_t TOTAL = RING_OFF + 2 * 64;
+};
+
+__device__ __forceinline__ float4 shfl4(float4 x, int src) {
+  x.x = __shfl_sync(0xffffffffu, x.x, src);
+  x.y = __shfl_sync(0xffffffffu, x.y, src);
+  x.z = __shfl_sync(0xffffffffu, x.z, src);
+  x.w = __shfl_sync(0xffffffffu, x.w, src);
+  return x;
+}
+
+// Store one warp's 32 x 32 fp32 chunk -- lane r holds columns [c, c + 32) of row row0 + r, times
+// `mul` -- into a row-major [rows][D] buffer.  Each group of four lanes transposes its 4 x 4
+// matrix of 16-byte pieces (two exchange steps: lanes ^ 2, then lanes ^ 1), after which lane
+// 4a + i holds piece i of rows 4a .. 4a + 3; so each store instruction writes eight 64-byte row
+// segments (whole sectors) instead of 32 scattered 16-byte pieces, without shared memory.  Rows
+// from `rows_valid` on are not written.
+template <int D>
+__device__ __forceinline__ void store_rows(const float (&v)[32], float mul, float* dst, int64_t row0,
+                                           int rows_valid, int c, int lane) {
+  const int i = lane & 3, rbase = lane & ~3;
+  const bool hi = (i & 2) != 0, odd = (i & 1) != 0;
+#pragma unroll
+  for (int blk = 0; blk < 2; ++blk) {
+    float4 e[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int o = 16 * blk + 4 * q;
+      e[q] = make_float4(v[o] * mul, v[o + 1] * mul, v[o + 2] * mul, v[o + 3] * mul);
+    }
+    {  // swap the off-diagonal 2 x 2 blocks with lane ^ 2
+      const float4 r0 = shfl4(hi ? e[0] : e[2], lane ^ 2), r1 = shfl4(hi ? e[1] : e[3], lane ^ 2);
+      if (hi) {
+        e[0] = r0;
+        e[1] = r1;
+      } else {
+        e[2] = r0;
+        e[3] = r1;
+      }
+    }
+    {  // swap within the 2 x 2 blocks with lane ^ 1
+      const float4 r0 = shfl4(odd ? e[0] : e[1], lane ^ 1), r1 = shfl4(odd ? e[2] : e[3], lane ^ 1);
+      if (odd) {
+        e[0] = r0;
+        e[2] = r1;
+      } else {
+        e[1] = r0;
+        e[3] = r1;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (rbase + j < rows_valid)
+        *reinterpret_cast<float4*>(dst + (row0 + rbase + j) * D + c + 16 * blk + 4 * i) = e[j];
+  }
+}
+// 32 columns of this lane's row, times mul, rounded to bf16: 64 bytes in a row of their own.
+__device__ __forceinline__ void store_bf16(const float* v, float mul, __nv_bfloat16* dst) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(dst + 8 * q) =
+        make_uint4(pack_bf16x2(v[8 * q] * mul, v[8 * q + 1] * mul), pack_bf16x2(v[8 * q + 2] * mul, v[8 * q + 3] * mul),
+                   pack_bf16x2(v[8 * q + 4] * mul, v[8 * q + 5] * mul), pack_bf16x2(v[8 * q + 6] * mul, v[8 * q + 7] * mul));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ float lam_of(const Params& prm, int h) {
+  return __bfloat162float(prm.lam[prm.lam_n == 1 ? 0 : h]);
+}
+
+// 64-key blocks of partition k visited by query block qb (128 rows) of partition p: on the causal
+// diagonal partition up to the query block's last row.
+__device__ __forceinline__ int kblocks_of(const Params& prm, int k, int p, int qb) {
+  return (prm.causal && k == p) ? min(prm.ns, 2 * qb + 2) : prm.ns;
+}
+// first 64-row query block of partition p visited by key block kb (128 keys) of partition k
+__device__ __forceinline__ int qblock_begin(const Params& prm, int k, int p, int kb) {
+  return (prm.causal && k == p) ? 2 * kb : 0;
+}
+
+// Key blocks of a dq unit in the order the producer loads them.
+struct KCursor {
+  int ki, kp, kb, n;
+  __device__ __forceinline__ void load(const Params& prm, const DevItem& it, int qb) {
+    kp = __ldg(prm.list + it.kv_off + ki);
+    kb = 0;
+    n = kblocks_of(prm, kp, it.p, qb);
+  }
+  __device__ __forceinline__ void start(const Params& prm, const DevItem& it, int qb) {
+    ki = 0;
+    load(prm, it, qb);
+  }
+  __device__ __forceinline__ void step(const Params& prm, const DevItem& it, int qb) {
+    if (++kb < n) return;
+    ++ki;
+    if (ki < it.n_kv) load(prm, it, qb);
+    else kp = -1;
+  }
+};
+
+// Query blocks of a dkdv unit: heads of the group, then the slot's Q partitions, then the partition's blocks.
+struct QCursor {
+  int h, qi, p, qb;
+  __device__ __forceinline__ void load(const Params& prm, const DevItem& it, int kb) {
+    p = __ldg(prm.list + it.kv_off + qi);
+    qb = qblock_begin(prm, it.p, p, kb);
+  }
+  __device__ __forceinline__ void start(const Params& prm, const DevItem& it, int kb, int h0) {
+    h = h0;
+    qi = 0;
+    load(prm, it, kb);
+  }
+  __device__ __forceinline__ void step(const Params& prm, const DevItem& it, int kb) {
+    if (++qb < prm.ns) return;
+    if (++qi >= it.n_kv) {
+      qi = 0;
+      ++h;
+    }
+    load(prm, it, kb);
+  }
+};
+
+// A unit of either kernel: a 128-row block `blk` of partition it.p of a (KV) head, and the number
+// of streamed blocks.
+struct Unit {
+  int blk, h, b, NB;
+  DevItem it;
+  bool ok;
+};
+template <bool KV>
+__device__ __forceinline__ Unit unit_of(int u, const Params& prm) {
+  Unit x;
+  const int H = KV ? prm.Hkv : prm.Hq;
+  x.blk = u % prm.nb;
+  if (!KV && prm.causal) x.blk = prm.nb - 1 - x.blk;  // the longest first: the grid's last units are short
+  u /= prm.nb;
+  x.h = u % H;
+  u /= H;
+  x.b = u % prm.B;
+  const int idx = u / prm.B;
+  x.NB = 0;
+  x.ok = idx >= 0 && idx < prm.n_items;
+  if (!x.ok) return x;
+  x.it = prm.items[idx];
+  x.ok = x.it.p >= 0 && x.it.p < prm.P && x.it.slot >= 0 && x.it.slot < prm.n_slots && x.it.n_kv >= 1 && x.it.kv_off >= 0;
+  if (!x.ok) return x;
+  for (int i = 0; i < x.it.n_kv; ++i) {
+    const int o = __ldg(prm.list + x.it.kv_off + i);
+    x.NB += KV ? max(0, prm.ns - qblock_begin(prm, x.it.p, o, x.blk)) : kblocks_of(prm, o, x.it.p, x.blk);
+  }
+  if (KV) x.NB *= prm.Hq / prm.Hkv;
+  return x;
+}
+// A unit travels through the shared-memory ring decoded, so that consumers never wait on the global
+// reads of the decode.
+__device__ __forceinline__ void put_unit(volatile int32_t* e, int u, const Unit& x) {
+  e[0] = u;
+  e[1] = x.blk, e[2] = x.h, e[3] = x.b, e[4] = x.NB, e[5] = x.ok ? 1 : 0;
+  e[6] = x.it.p, e[7] = x.it.slot, e[8] = x.it.kv_off, e[9] = x.it.n_kv;
+}
+__device__ __forceinline__ int get_unit(const volatile int32_t* e, Unit& x) {
+  x.blk = e[1], x.h = e[2], x.b = e[3], x.NB = e[4], x.ok = e[5] != 0;
+  x.it.p = e[6], x.it.slot = e[7], x.it.kv_off = e[8], x.it.n_kv = e[9];
+  return e[0];
+}
+
+// What both kernels share: barrier set-up, the unit ring and the exit.
+template <int D, bool KV>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    diff_bwd_kernel(const __grid_constant__ CUtensorMap tmR0, const __grid_constant__ CUtensorMap tmR1,
+                    const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params prm) {
+  // R0, R1: the resident blocks' tensors (dkdv: K, V; dq: Q, dO); A, B: the streamed ones (Q, dO; K, V)
+  using Ly = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sb = smem_u32(smem_raw);
+  if (sb & 1023u) {  // 128-byte swizzle atoms need 1024-aligned operands; the window starts so on this part
+    if (threadIdx.x == 0) record_error(prm.status, MESH_ATTN_ERR_INTERNAL, ROLE_ITEM, (int32_t)blockIdx.x);
+    return;
+  }
+  uint8_t* smem = smem_raw;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sb + Ly::BAR_OFF + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::MISC_OFF);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + Ly::MISC_OFF + 4);
+  volatile int32_t* unit_ring = reinterpret_cast<volatile int32_t*>(smem + Ly::RING_OFF);
+  const int64_t L = prm.L;
+  const int g = prm.Hq / prm.Hkv;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(Ly::B_RES), 1);
+    mbar_init(bar(Ly::B_RESE), KV ? 1 : N_EPI);  // dq: the epilogue warps have copied Q and dO into TMEM
+    for (int s = 0; s < Ly::NSA; ++s) {
+      mbar_init(bar(Ly::B_AF + s), 1);
+      mbar_init(bar(Ly::B_AE + s), 1);
+    }
+    for (int s = 0; s < Ly::NSB; ++s) {
+      mbar_init(bar(Ly::B_BF + s), 1);
+      mbar_init(bar(Ly::B_BE + s), 1);
+    }
+    mbar_init(bar(Ly::B_S), 1);
+    mbar_init(bar(Ly::B_SREAD), N_EW);  // one lane of each elementwise warp
+    mbar_init(bar(Ly::B_DP), 1);
+    mbar_init(bar(Ly::B_DP + 1), 1);
+    mbar_init(bar(Ly::B_A), N_EW);
+    mbar_init(bar(Ly::B_DS), N_EW);
+    mbar_init(bar(Ly::B_ACC), 1);
+    mbar_init(bar(Ly::B_ACCE), KV ? N_EW : N_EPI);
+    mbar_init(bar(Ly::B_DRAIN), 1);
+    mbar_init(bar(Ly::B_VEC), N_EW * 32);  // every elementwise thread has written its LSE or D value
+    mbar_init(bar(Ly::B_VEC + 1), N_EW * 32);
+    mbar_init(bar(Ly::B_QTF), N_EPI);
+    mbar_init(bar(Ly::B_QTE), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(Ly::B_UF + s), 1);
+      mbar_init(bar(Ly::B_UE + s), N_EW + 1 + (KV ? 0 : N_EPI));  // the warps that read a unit
+    }
+    *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == WARP_LOAD && lane == 0) {
+    tma_prefetch_desc(&tmR0);
+    tma_prefetch_desc(&tmR1);
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const bool run = *abort_flag == 0;
+
+  // the next unit from the ring (every lane of the warp waits, one lane frees the slot)
+  int nu = 0;
+  auto take = [&](int& v, Unit& y, int role) -> bool {
+    const int slot = nu & 1;
+    bool r = mbar_wait_warp(bar(Ly::B_UF + slot), (uint32_t)((nu >> 1) & 1), prm.wait_limit_ns, abort_flag, prm.status, role, -1);
+    if (!r) return false;
+    v = get_unit(unit_ring + 16 * slot, y);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(Ly::B_UE + slot));
+    ++nu;
+    return true;
+  };
+  auto bad_unit = [&](int u, int role) {
+    if (lane == 0) {
+      record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, role, u);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+  };
+  auto wait_all = [&](int b, uint32_t parity, int role, int unit) -> bool {  // warp-uniform
+    const bool r = mbar_wait(bar(b), parity, prm.wait_limit_ns, abort_flag, prm.status, role, unit);
+    return __all_sync(0xffffffffu, r);
+  };
+  auto arrive = [&](int b) {  // after this warp's TMEM accesses
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+
+  if (warp < N_EW) {
+    // ================================================================ elementwise
+    regs_inc<EW_REGS>();
+    const int wq = warp & 3, hf = warp >> 2;  // TMEM lane quadrant, column half
+    const int row = wq * 32 + lane;           // TMEM lane: a key row (dkdv) or a query row (dq) of the block
+    const int c_base = hf * 32;               // this warp's columns [c_base, c_base + 32)
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const uint32_t tm_s = tmem + lane_base + COL_S + (uint32_t)c_base;
+    const uint32_t tm_dp = tmem + lane_base + COL_DP + (uint32_t)c_base;
+    const uint64_t sc2 = f2_pack(prm.scale_log2, prm.scale_log2);
+    bool ok = run;
+    int v = -1;
+    Unit x;
+    if (ok) ok = take(v, x, ROLE_EW);
+    int64_t g0 = 0;  // global index of the unit's first block
+    int k_unit = 0;
+    if constexpr (KV) {
+      // ---------------------------------------------------------------- dK and dV
+      // Vector `vec` (LSE_1, LSE_2, D_1, D_2) of query column `vq`, loaded raw one block ahead and only
+      // used (scaled, published) at the top of the next iteration, so that the load never stalls the
+      // block in flight.
+      float* vec_s = reinterpret_cast<float*>(smem + Ly::VEC_OFF);
+      const int tid = threadIdx.x, vec = tid >> 6, vq = tid & 63;
+      float raw = 0.f, nl_next = 0.f;
+      bool raw_in = false;
+      auto fetch = [&](const Unit& y, const QCursor& c) {
+        const int64_t ql = (int64_t)c.qb * BS + vq;
+        raw_in = c.p >= 0 && c.p < prm.P && ql < L;
+        if (raw_in) {
+          const int64_t at = (((int64_t)y.b * prm.Hq + c.h) * 2 + (vec & 1)) * prm.S + (int64_t)c.p * L + ql;
+          raw = __ldg((vec < 2 ? prm.lse : prm.dsum) + at);
+        }
+        nl_next = -lam_of(prm, c.h);
+      };
+      QCursor cur, nxt;  // blocks i and i + 1
+      if (ok && v >= 0 && x.ok) {
+        cur.start(prm, x.it, x.blk, x.h * g);
+        fetch(x, cur);
+      }
+      while (ok && v >= 0) {
+        if (!x.ok || x.NB < 1) {
+          bad_unit(v, ROLE_EW);
+          ok = false;
+          break;
+        }
+        const int k = x.it.p, kb = x.blk, NB = x.NB;
+        nxt = cur;
+        for (int i = 0; i < NB && ok; ++i) {
+          const int64_t gi = g0 + i;
+          const int vb = (int)(gi & 1);
+          if (i > 0) cur = nxt;
+          if (i + 1 < NB) nxt.step(prm, x.it, kb);
+          const float nl = nl_next;  // -lam of this block's head
+          // publish this thread's value and wait (bounded) for all: a buffer is rewritten two blocks
+          // later, after every thread has arrived for the block between.  No such query row (or one
+          // without a visible key): exp2(s - inf) = 0, so it needs no mask.
+          {
+            float val = vec < 2 ? -INFINITY : 0.f;
+            if (raw_in) val = vec >= 2 ? -raw : (raw == -INFINITY ? -INFINITY : -raw * LOG2E);
+            vec_s[(vb * 4 + vec) * BS + vq] = val;
+            mbar_arrive(bar(Ly::B_VEC + vb));
+            if (i + 1 < NB) fetch(x, nxt);
+          }
+          ok = wait_all(Ly::B_VEC + vb, (uint32_t)((gi >> 1) & 1), ROLE_EW, i);
+          if (!ok) break;
+          // causal diagonal: query columns before this key row are masked
+          const int lo = (prm.causal && cur.p == k) ? kb * BM + row - cur.qb * BS - c_base : 0;
+          ok = wait_all(Ly::B_S, (uint32_t)(gi & 1), ROLE_EW, i);
+          if (!ok) break;
+          tc_fence_after();
+          float p1[32], w2[32];
+          tmem_ld32(tm_s, p1);
+          tmem_ld32(tm_s + 64u, w2);
+          tc_wait_ld();
+          arrive(Ly::B_SREAD);  // the next block's S may overwrite it
+          if (__any_sync(0xffffffffu, lo > 0)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c < lo) p1[c] = w2[c] = -INFINITY;
+          }
+          const float4* l1 = reinterpret_cast<const float4*>(vec_s + (vb * 4 + 0) * BS + c_base);
+          const float4* l2 = reinterpret_cast<const float4*>(vec_s + (vb * 4 + 1) * BS + c_base);
+          const float4* d1 = reinterpret_cast<const float4*>(vec_s + (vb * 4 + 2) * BS + c_base);
+          const float4* d2 = reinterpret_cast<const float4*>(vec_s + (vb * 4 + 3) * BS + c_base);
+          const uint64_t nl2 = f2_pack(nl, nl);
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 a = l1[c / 4], b = l2[c / 4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              float x0, x1, y0, y1;
+              f2_unpack(f2_fma(f2_pack(p1[c + e], p1[c + e + 1]), sc2, e ? f2_pack(a.z, a.w) : f2_pack(a.x, a.y)), x0, x1);
+              f2_unpack(f2_fma(f2_pack(w2[c + e], w2[c + e + 1]), sc2, e ? f2_pack(b.z, b.w) : f2_pack(b.x, b.y)), y0, y1);
+              p1[c + e] = fast_exp2(x0);
+              p1[c + e + 1] = fast_exp2(x1);
+              // -lam P_2
+              const uint64_t w = f2_mul(f2_pack(fast_exp2(y0), fast_exp2(y1)), nl2);
+              f2_unpack(w, w2[c + e], w2[c + e + 1]);
+              float a0, a1;
+              f2_unpack(f2_add(f2_pack(p1[c + e], p1[c + e + 1]), w), a0, a1);
+              pk[(c + e) / 2] = pack_bf16x2(a0, a1);
+            }
+          }
+          tmem_st16(tmem + lane_base + COL_A + (uint32_t)(vb * 32 + hf * 16), pk);
+          tc_wait_st();
+          arrive(Ly::B_A);
+          ok = wait_all(Ly::B_DP, (uint32_t)(gi & 1), ROLE_EW, i);
+          if (!ok) break;
+          tc_fence_after();
+          float dp[32];
+          tmem_ld32(tm_dp, dp);
+          tc_wait_ld();
+          uint32_t s1[16], s2[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 a = d1[c / 4], b = d2[c / 4];
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const uint64_t d = f2_pack(dp[c + e], dp[c + e + 1]);
+              float a0, a1;
+              f2_unpack(f2_mul(f2_add(d, e ? f2_pack(a.z, a.w) : f2_pack(a.x, a.y)), f2_pack(p1[c + e], p1[c + e + 1])), a0, a1);
+              s1[(c + e) / 2] = pack_bf16x2(a0, a1);
+              f2_unpack(f2_mul(f2_add(d, e ? f2_pack(b.z, b.w) : f2_pack(b.x, b.y)), f2_pack(w2[c + e], w2[c + e + 1])), a0, a1);
+              s2[(c + e) / 2] = pack_bf16x2(a0, a1);
+            }
+          }
+          tmem_st16(tm_dp, s1);
+          tmem_st16(tm_dp + 16u, s2);
+          tc_wait_st();
+          arrive(Ly::B_DS);
+        }
+        if (!ok) break;
+        // the next unit, and its first block's values, before this unit's epilogue
+        int vn = -1;
+        Unit xn;
+        ok = take(vn, xn, ROLE_EW);
+        if (!ok) break;
+        if (vn >= 0 && xn.ok) {
+          cur.start(prm, xn.it, xn.blk, xn.h * g);
+          fetch(xn, cur);
+        }
+        // ---- epilogue: this half's columns of the dV and dK rows of this key block
+        ok = wait_all(Ly::B_ACC, (uint32_t)(k_unit & 1), ROLE_EW, -1);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          const uint32_t tm_dv = tmem + lane_base + COL_ACC + (uint32_t)(hf * (D / 2));
+          // map hf's dK: columns [hf D / 2, + D / 2), at d = 64 the half of its 64-wide product that is its own
+          const uint32_t tm_dk = tmem + lane_base + COL_DK + (uint32_t)(hf * 64 + (D == 64 ? hf * 32 : 0));
+          const int64_t rl = (int64_t)kb * BM + row;  // row in the partition
+          float acc[D / 2];
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {  // dV, then dK
+            const uint32_t tm = which ? tm_dk : tm_dv;
+            const float mul = which ? prm.scale : 1.f;
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 32) tmem_ld32(tm + (uint32_t)c, acc + c);
+            tc_wait_ld();
+            if (which) arrive(Ly::B_ACCE);  // both accumulators are copied out: the next unit may overwrite them
+            if (prm.part0) {
+              const int64_t row0 = (((int64_t)x.b * prm.Hkv + x.h) * prm.n_slots + x.it.slot) * L + (int64_t)kb * BM + wq * 32;
+              const int rows_valid = (int)max((int64_t)0, min((int64_t)32, L - ((int64_t)kb * BM + wq * 32)));
+#pragma unroll
+              for (int c = 0; c < D / 2; c += 32)
+                store_rows<D>(*reinterpret_cast<const float(*)[32]>(acc + c), mul, which ? prm.part0 : prm.part1, row0,
+                              rows_valid, hf * (D / 2) + c, lane);
+            } else if (rl < L) {
+              __nv_bfloat16* dst = (which ? prm.out0 : prm.out1) +
+                                   (((int64_t)x.b * prm.Hkv + x.h) * prm.S + (int64_t)k * L + rl) * D + hf * (D / 2);
+#pragma unroll
+              for (int c = 0; c < D / 2; c += 32) store_bf16(acc + c, mul, dst + c);
+            }
+          }
+        }
+        ++k_unit;
+        g0 += NB;
+        v = vn;
+        x = xn;
+      }
+    } else {
+      // ---------------------------------------------------------------- dQ
+      // LSEs and Ds of this thread's row, loaded as soon as the unit is known and used a phase later
+      float raw_l[2] = {0.f, 0.f}, raw_d[2] = {0.f, 0.f}, raw_nl = 0.f;
+      bool row_in = false;
+      auto fetch = [&](const Unit& y) {
+        const int64_t ql = (int64_t)y.blk * BM + row;
+        row_in = ql < L;
+        raw_nl = -lam_of(prm, y.h);
+        if (row_in) {
+          const int64_t at = (((int64_t)y.b * prm.Hq + y.h) * 2) * prm.S + (int64_t)y.it.p * L + ql;
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            raw_l[m] = __ldg(prm.lse + at + m * prm.S);
+            raw_d[m] = __ldg(prm.dsum + at + m * prm.S);
+          }
+        }
+      };
+      if (ok && v >= 0 && x.ok) fetch(x);
+      while (ok && v >= 0) {
+        if (!x.ok || x.NB < 1) {
+          bad_unit(v, ROLE_EW);
+          ok = false;
+          break;
+        }
+        const int p = x.it.p, qb = x.blk;
+        float nl[2], nd[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          nl[m] = row_in && raw_l[m] != -INFINITY ? -raw_l[m] * LOG2E : -INFINITY;
+          nd[m] = row_in ? -raw_d[m] : 0.f;
+        }
+        const uint64_t l1 = f2_pack(nl[0], nl[0]), l2 = f2_pack(nl[1], nl[1]);
+        const uint64_t d1 = f2_pack(nd[0], nd[0]), d2 = f2_pack(nd[1], nd[1]);
+        const uint64_t nlam2 = f2_pack(raw_nl, raw_nl);
+        uint64_t t2[2] = {0ull, 0ull};  // sum of P_2 dP
+        KCursor cur;
+        cur.start(prm, x.it, qb);
+        for (int j = 0; j < x.NB && ok; ++j) {
+          if (j > 0) cur.step(prm, x.it, qb);
+          const int64_t gi = g0 + j;
+          const uint32_t dpb = tm_dp + (uint32_t)((gi & 1) * 64);
+          int hi = (int)min((int64_t)BS, L - (int64_t)cur.kb * BS);  // keys past the partition end
+          if (prm.causal && cur.kp == p) hi = min(hi, qb * BM + row + 1 - cur.kb * BS);
+          hi -= c_base;
+          const bool any_mask = __any_sync(0xffffffffu, hi < 32);
+          ok = wait_all(Ly::B_S, (uint32_t)(gi & 1), ROLE_EW, j);
+          if (!ok) break;
+          tc_fence_after();
+          float p1[32], p2[32];
+          tmem_ld32(tm_s, p1);
+          tmem_ld32(tm_s + 64u, p2);
+          tc_wait_ld();
+          arrive(Ly::B_SREAD);  // the next block's S may overwrite it
+          if (any_mask) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c >= hi) p1[c] = p2[c] = -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(p1[c], p1[c + 1]), sc2, l1), x0, x1);
+            p1[c] = fast_exp2(x0);
+            p1[c + 1] = fast_exp2(x1);
+            f2_unpack(f2_fma(f2_pack(p2[c], p2[c + 1]), sc2, l2), x0, x1);
+            p2[c] = fast_exp2(x0);
+            p2[c + 1] = fast_exp2(x1);
+          }
+          ok = wait_all(Ly::B_DP + (int)(gi & 1), (uint32_t)((gi >> 1) & 1), ROLE_EW, j);
+          if (!ok) break;
+          tc_fence_after();
+          float dp[32];
+          tmem_ld32(dpb, dp);
+          tc_wait_ld();
+          uint32_t s1[16], s2[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const uint64_t d = f2_pack(dp[c], dp[c + 1]);
+            const uint64_t q2 = f2_pack(p2[c], p2[c + 1]);
+            float a0, a1;
+            f2_unpack(f2_mul(f2_add(d, d1), f2_pack(p1[c], p1[c + 1])), a0, a1);
+            s1[c / 2] = pack_bf16x2(a0, a1);
+            t2[(c >> 1) & 1] = f2_fma(q2, d, t2[(c >> 1) & 1]);
+            f2_unpack(f2_mul(f2_add(d, d2), f2_mul(q2, nlam2)), a0, a1);
+            s2[c / 2] = pack_bf16x2(a0, a1);
+          }
+          tmem_st16(dpb, s1);
+          tmem_st16(dpb + 16u, s2);
+          tc_wait_st();
+          arrive(Ly::B_DS);
+        }
+        if (!ok) break;
+        {
+          float a0, a1;
+          f2_unpack(f2_add(t2[0], t2[1]), a0, a1);
+          float t = a0 + a1;
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+          if (lane == 0)
+            prm.dlam_part[((((int64_t)x.b * prm.Hq + x.h) * prm.n_slots + x.it.slot) * prm.nb + qb) * N_EW + warp] = -t;
+        }
+        // the next unit and its row's values (the epilogue warps drain this one)
+        int vn = -1;
+        Unit xn;
+        ok = take(vn, xn, ROLE_EW);
+        if (!ok) break;
+        if (vn >= 0 && xn.ok) fetch(xn);
+        g0 += x.NB;
+        v = vn;
+        x = xn;
+      }
+    }
+  } else if (warp < WARP_EPI) {
+    regs_dec<MMA_REGS>();
+    if (warp == WARP_MMA) {
+      // ================================================================ MMA issuer
+      constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BS, false);   // S, dP: N = 64, K-major B
+      constexpr uint32_t idesc_h = idesc_bf16_f32(BM, 64, true);    // dK_m, dQ_m: N = 64, MN-major B
+      constexpr uint32_t idesc_dv = idesc_bf16_f32(BM, D, true);    // dV
+      constexpr uint64_t SBLK16 = Ly::SBLK >> 4, SBOX16 = Ly::SBOX >> 4, BOX16 = Ly::BOX >> 4;
+      const uint64_t r0 = smem_desc_sw128(sb + Ly::RES0, 16u, 1024u), r1 = smem_desc_sw128(sb + Ly::RES1, 16u, 1024u);
+      const uint64_t a_kmaj = smem_desc_sw128(sb + Ly::A0, 16u, 1024u);
+      const uint64_t a_mn = smem_desc_sw128(sb + Ly::A0, Ly::SBOX, 1024u);
+      const uint64_t b_kmaj = smem_desc_sw128(sb + Ly::B0, 16u, 1024u);
+      const uint64_t b_mn = smem_desc_sw128(sb + Ly::B0, Ly::SBOX, 1024u);
+      // K-step kk of a K-major operand: 16 columns, box kk / 4, byte 32 (kk mod 4)
+      auto res_off = [](int kk) { return (uint64_t)((kk >> 2) * BOX16 + (kk & 3) * 2); };
+      auto str_off = [](int kk) { return (uint64_t)((kk >> 2) * SBOX16 + (kk & 3) * 2); };
+      const uint32_t tm_qt = tmem + COL_Q, tm_gt = tm_qt + (uint32_t)(D / 2);
+      auto issue_s = [&](int64_t gi) {  // both maps
+        const uint64_t sd = a_kmaj + (uint64_t)(gi % Ly::NSA) * SBLK16;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const int c = m * (D / 32) + kk;
+            if (KV) tc_mma_ss_warp(tmem + COL_S + 64u * m, r0 + res_off(c), sd + str_off(c), idesc_s, kk > 0);
+            else tc_mma_ts_warp(tmem + COL_S + 64u * m, tm_qt + (uint32_t)(c * 8), sd + str_off(c), idesc_s, kk > 0);
+          }
+        tc_commit_warp(bar(Ly::B_S));
+      };
+      auto issue_dp = [&](int64_t gi) {
+        const int st = (int)(gi % Ly::NSB);
+        const uint64_t sd = b_kmaj + (uint64_t)st * SBLK16;
+        const uint32_t d = tmem + COL_DP + (KV ? 0u : (uint32_t)((gi & 1) * 64));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (KV) tc_mma_ss_warp(d, r1 + res_off(kk), sd + str_off(kk), idesc_s, kk > 0);
+          else tc_mma_ts_warp(d, tm_gt + (uint32_t)(kk * 8), sd + str_off(kk), idesc_s, kk > 0);
+        }
+        tc_commit_warp(bar(Ly::B_DP + (KV ? 0 : (int)(gi & 1))));
+        if (!KV) tc_commit_warp(bar(Ly::B_BE + st));  // V(gi) is read by this product only
+      };
+      auto issue_dv = [&](int64_t gi, bool first) {  // dV += A^T dO(gi)
+        const int st = (int)(gi % Ly::NSB);
+        const uint64_t sd = b_mn + (uint64_t)st * SBLK16;
+#pragma unroll
+        for (int kk = 0; kk < BS / 16; ++kk)
+          tc_mma_ts_warp(tmem + COL_ACC, tmem + COL_A + (uint32_t)((gi & 1) * 32 + kk * 8), sd + (uint64_t)(kk * 128), idesc_dv,
+                         (!first || kk > 0) ? 1u : 0u);
+        tc_commit_warp(bar(Ly::B_BE + st));  // dO(gi): read by dP(gi) and dV(gi)
+      };
+      auto issue_half = [&](int64_t gi, bool first) {  // dK_m += dS_m^T Q_m(gi), or dQ_m += dS_m K_m(gi)
+        const int st = (int)(gi % Ly::NSA);
+        const uint32_t acc = tmem + (KV ? COL_DK : COL_ACC);
+        const uint32_t ds = tmem + COL_DP + (KV ? 0u : (uint32_t)((gi & 1) * 64));
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          // the map's 64-column box; at d = 64 both maps share one box and half of each product is used
+          const uint64_t sd = a_mn + (uint64_t)st * SBLK16 + (D == 128 ? (uint64_t)m * SBOX16 : 0ull);
+#pragma unroll
+          for (int kk = 0; kk < BS / 16; ++kk)
+            tc_mma_ts_warp(acc + 64u * m, ds + ds_col(m, kk), sd + (uint64_t)(kk * 128), idesc_h, (!first || kk > 0) ? 1u : 0u);
+        }
+        tc_commit_warp(bar(Ly::B_AE + st));  // Q(gi) or K(gi): read by S(gi) and here
+      };
+      auto wait_a = [&](int64_t gi) {
+        return mbar_wait_warp(bar(Ly::B_AF + (int)(gi % Ly::NSA)), (uint32_t)((gi / Ly::NSA) & 1), prm.wait_limit_ns,
+                              abort_flag, prm.status, ROLE_MMA, (int32_t)gi);
+      };
+      auto wait_b = [&](int64_t gi) {
+        return mbar_wait_warp(bar(Ly::B_BF + (int)(gi % Ly::NSB)), (uint32_t)((gi / Ly::NSB) & 1), prm.wait_limit_ns,
+                              abort_flag, prm.status, ROLE_MMA, (int32_t)gi);
+      };
+      auto wait1 = [&](int b, uint32_t parity) {
+        return mbar_wait_warp(bar(b), parity, prm.wait_limit_ns, abort_flag, prm.status, ROLE_MMA, -1);
+      };
+      int nres = 0;
+      // S and dP of a unit's first block, as soon as its resident operands are there
+      auto start_unit = [&](const Unit& y, int64_t gi) -> bool {
+        if (!wait1(KV ? Ly::B_RES : Ly::B_QTF, (uint32_t)(nres & 1))) return false;
+        ++nres;
+        if (!wait_a(gi)) return false;
+        tc_fence_after();
+        issue_s(gi);
+        if (!wait_b(gi)) return false;
+        tc_fence_after();
+        issue_dp(gi);
+        if (y.NB == 1) tc_commit_warp(bar(KV ? Ly::B_RESE : Ly::B_QTE));  // the unit's last S and dP are issued
+        return true;
+      };
+      bool ok = run;
+      int v = -1;
+      Unit x;
+      if (ok) ok = take(v, x, ROLE_MMA);
+      if (ok && v >= 0) {
+        if (!x.ok || x.NB < 1) {
+          bad_unit(v, ROLE_MMA);
+          ok = false;
+        } else {
+          ok = start_unit(x, 0);
+        }
+      }
+      int64_t g0 = 0;
+      int k_unit = 0;
+      while (ok && v >= 0) {
+        const int NB = x.NB;
+        for (int i = 0; i < NB && ok; ++i) {
+          const int64_t gi = g0 + i;
+          // S(gi) is in registers: S(gi + 1) may overwrite it.  (The last block's phase of this barrier is
+          // not waited for, but it precedes the DS arrivals that are.)
+          if (i + 1 < NB) {
+            ok = wait1(Ly::B_SREAD, (uint32_t)(gi & 1)) && wait_a(gi + 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(gi + 1);
+            if (!KV) {  // the other dP buffer: dS(gi - 1) in it has been read by dQ(gi - 1), issued before
+              ok = wait_b(gi + 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_dp(gi + 1);
+              if (i + 2 == NB) tc_commit_warp(bar(Ly::B_QTE));
+            }
+          }
+          if (KV) {
+            ok = wait1(Ly::B_A, (uint32_t)(gi & 1));
+            if (ok && i == 0 && k_unit > 0) ok = wait1(Ly::B_ACCE, (uint32_t)((k_unit - 1) & 1));  // accumulators copied out
+            if (!ok) break;
+            tc_fence_after();
+            issue_dv(gi, i == 0);
+          }
+          ok = wait1(Ly::B_DS, (uint32_t)(gi & 1));
+          if (ok && !KV && i == 0 && k_unit > 0) ok = wait1(Ly::B_ACCE, (uint32_t)((k_unit - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          issue_half(gi, i == 0);
+          if (i + 1 == NB) tc_commit_warp(bar(Ly::B_ACC));  // the unit's accumulators are complete
+          if (KV && i + 1 < NB) {
+            ok = wait_b(gi + 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_dp(gi + 1);
+            if (i + 2 == NB) tc_commit_warp(bar(Ly::B_RESE));  // the unit's last S and dP are issued
+          }
+        }
+        if (!ok) break;
+        int vn = -1;
+        ok = take(vn, x, ROLE_MMA);
+        if (!ok) break;
+        g0 += NB;
+        ++k_unit;
+        v = vn;
+        if (v < 0) break;
+        if (!x.ok || x.NB < 1) {
+          bad_unit(v, ROLE_MMA);
+          ok = false;
+          break;
+        }
+        ok = start_unit(x, g0);
+      }
+      // exit-path drain: every MMA issued completes before TMEM is freed
+      tc_commit_warp(bar(Ly::B_DRAIN));
+      mbar_drain(bar(Ly::B_DRAIN), 0u, DRAIN_NS);
+    } else if (warp == WARP_LOAD && lane == 0) {
+      // ================================================================ producer
+      bool ok = run;
+      if (ok && (prm.header->magic != TABLES_MAGIC || prm.header->tag != prm.tag)) {  // another plan's tables
+        record_error(prm.status, MESH_ATTN_ERR_INVALID_ARG, ROLE_LOAD, 0);
+        *abort_flag = 1;
+        ok = false;
+      }
+      int np = 0;  // units published
+      auto publish = [&](Unit& y) -> int {  // a CTA's first unit is its own index, the others come from the counter
+        const int slot = np & 1;
+        ok = mbar_wait(bar(Ly::B_UE + slot), (uint32_t)(((np >> 1) & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
+                       ROLE_LOAD, -1);
+        if (!ok) return -1;
+        int u = (int)blockIdx.x;
+        if (np > 0) u = prm.n_units > (int)gridDim.x ? (int)(gridDim.x + atomicAdd(prm.counter, 1u)) : prm.n_units;
+        if (u >= prm.n_units) u = -1;
+        if (u >= 0) y = unit_of<KV>(u, prm);
+        put_unit(unit_ring + 16 * slot, u, y);
+        mbar_arrive(bar(Ly::B_UF + slot));
+        ++np;
+        return u;
+      };
+      int nres = 0;
+      int64_t ga = 0, gb = 0;  // streamed blocks issued
+      Unit x{}, y{};
+      int u = ok ? publish(x) : -1;
+      while (ok && u >= 0) {
+        if (!x.ok || x.NB < 1) {
+          record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_LOAD, u);
+          *abort_flag = 1;
+          break;
+        }
+        // publish the following unit now and pull its resident rows into L2
+        const int un = publish(y);
+        if (!ok) break;
+        const int H = KV ? prm.Hkv : prm.Hq;
+        if (un >= 0 && y.ok) {
+          const int32_t pn = (y.b * H + y.h) * prm.P + y.it.p;
+          for (int c = 0; c < D / 64; ++c) {
+            tma_prefetch_l2_3d(&tmR0, c * 64, y.blk * BM, pn);
+            tma_prefetch_l2_3d(&tmR1, c * 64, y.blk * BM, pn);
+          }
+        }
+        // resident operands: the previous unit's must have been used (dkdv) or copied into TMEM (dq)
+        ok = mbar_wait(bar(Ly::B_RESE), (uint32_t)((nres & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, u);
+        if (!ok) break;
+        const int32_t part = (x.b * H + x.h) * prm.P + x.it.p;
+        mbar_expect_tx(bar(Ly::B_RES), 2 * Ly::TILE);
+        for (int c = 0; c < D / 64; ++c) {
+          tma_load_3d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmR0, c * 64, x.blk * BM, part, bar(Ly::B_RES));
+          tma_load_3d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmR1, c * 64, x.blk * BM, part, bar(Ly::B_RES));
+        }
+        ++nres;
+        QCursor qc;
+        KCursor kc;
+        if (KV) qc.start(prm, x.it, x.blk, x.h * g);
+        else kc.start(prm, x.it, x.blk);
+        for (int i = 0; i < x.NB && ok; ++i) {
+          if (i > 0) {
+            if (KV) qc.step(prm, x.it, x.blk);
+            else kc.step(prm, x.it, x.blk);
+          }
+          const int o = KV ? qc.p : kc.kp, blk = KV ? qc.qb : kc.kb;
+          if (o < 0 || o >= prm.P) {
+            record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_LOAD, u);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          const int32_t z = KV ? (x.b * prm.Hq + qc.h) * prm.P + o : (x.b * prm.Hkv + x.h / g) * prm.P + o;
+          const int sa = (int)(ga % Ly::NSA), st = (int)(gb % Ly::NSB);
+          if (ga >= Ly::NSA) {
+            ok = mbar_wait(bar(Ly::B_AE + sa), (uint32_t)((ga / Ly::NSA - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                           ROLE_LOAD, i);
+            if (!ok) break;
+          }
+          mbar_expect_tx(bar(Ly::B_AF + sa), Ly::SBLK);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sb + Ly::A0 + (uint32_t)sa * Ly::SBLK + (uint32_t)c * Ly::SBOX, &tmA, c * 64, blk * BS, z, bar(Ly::B_AF + sa));
+          ++ga;
+          if (gb >= Ly::NSB) {
+            ok = mbar_wait(bar(Ly::B_BE + st), (uint32_t)((gb / Ly::NSB - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                           ROLE_LOAD, i);
+            if (!ok) break;
+          }
+          mbar_expect_tx(bar(Ly::B_BF + st), Ly::SBLK);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sb + Ly::B0 + (uint32_t)st * Ly::SBLK + (uint32_t)c * Ly::SBOX, &tmB, c * 64, blk * BS, z, bar(Ly::B_BF + st));
+          ++gb;
+        }
+        u = un;
+        x = y;
+      }
+      // exit-path drain: every load issued lands before the CTA exits
+      if (nres > 0) mbar_drain(bar(Ly::B_RES), (uint32_t)((nres - 1) & 1), DRAIN_NS);
+      for (int64_t j = (ga > Ly::NSA ? ga - Ly::NSA : 0); j < ga; ++j)
+        mbar_drain(bar(Ly::B_AF + (int)(j % Ly::NSA)), (uint32_t)((j / Ly::NSA) & 1), DRAIN_NS);
+      for (int64_t j = (gb > Ly::NSB ? gb - Ly::NSB : 0); j < gb; ++j)
+        mbar_drain(bar(Ly::B_BF + (int)(j % Ly::NSB)), (uint32_t)((j / Ly::NSB) & 1), DRAIN_NS);
+    }
+  } else {
+    regs_dec<EPI_REGS>();
+    if constexpr (!KV) {
+      // ================================================================ epilogue (dq)
+      // Per unit: copy its Q and dO from shared memory into TMEM as soon as the previous unit's last S
+      // and dP are done with the TMEM copy, releasing the shared buffers to the producer; then drain
+      // the previous unit's dQ while the other roles run this one.
+      const int wq = warp & 3;
+      const int r = wq * 32 + lane;  // this thread's row of the block
+      const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+      const uint32_t tm_dq = tmem + lane_base + COL_ACC;
+      const uint32_t tm_qt = tmem + lane_base + COL_Q, tm_gt = tm_qt + (uint32_t)(D / 2);
+      bool ok = run;
+      int v = -1, k_unit = 0, ncopy = 0;
+      Unit x;
+      // row r of a 128 x D block in 64-column boxes with 128-byte swizzle (16-byte chunk j of a row at
+      // chunk j ^ (r mod 8)), packed two columns per TMEM column
+      auto copy_row = [&](uint32_t src_off, uint32_t dst) {
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          const uint8_t* rowp = smem + src_off + (uint32_t)c * Ly::BOX + (uint32_t)r * 128u;
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 q = *reinterpret_cast<const uint4*>(rowp + ((j ^ (r & 7)) << 4));
+            w[4 * j] = q.x, w[4 * j + 1] = q.y, w[4 * j + 2] = q.z, w[4 * j + 3] = q.w;
+          }
+          tmem_st32(dst + (uint32_t)(32 * c), w);
+        }
+      };
+      auto copy_in = [&]() -> bool {
+        if (!mbar_wait_warp(bar(Ly::B_RES), (uint32_t)(ncopy & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EPI, -1))
+          return false;
+        if (ncopy > 0 && !mbar_wait_warp(bar(Ly::B_QTE), (uint32_t)((ncopy - 1) & 1), prm.wait_limit_ns, abort_flag,
+                                         prm.status, ROLE_EPI, -1))
+          return false;
+        tc_fence_after();
+        copy_row(Ly::RES0, tm_qt);
+        copy_row(Ly::RES1, tm_gt);
+        tc_wait_st();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // reads done before the next TMA write
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(Ly::B_QTF));
+          mbar_arrive(bar(Ly::B_RESE));
+        }
+        ++ncopy;
+        return true;
+      };
+      if (ok) ok = take(v, x, ROLE_EPI);
+      if (ok && v >= 0 && x.ok && x.NB >= 1) ok = copy_in();
+      while (ok && v >= 0) {
+        if (!x.ok || x.NB < 1) {
+          bad_unit(v, ROLE_EPI);
+          ok = false;
+          break;
+        }
+        int vn = -1;
+        Unit xn;
+        ok = take(vn, xn, ROLE_EPI);
+        if (!ok) break;
+        if (vn >= 0 && xn.ok && xn.NB >= 1) {
+          ok = copy_in();
+          if (!ok) break;
+        }
+        const int64_t row0 = (((int64_t)x.b * prm.Hq + x.h) * prm.n_slots + x.it.slot) * L + (int64_t)x.blk * BM + wq * 32;
+        const int rows_valid = (int)max((int64_t)0, min((int64_t)32, L - ((int64_t)x.blk * BM + wq * 32)));
+        __nv_bfloat16* dst = prm.out0 + (((int64_t)x.b * prm.Hq + x.h) * prm.S + (int64_t)x.it.p * L + (int64_t)x.blk * BM + r) * D;
+        ok = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(k_unit & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EPI, -1);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float t[32];
+          // at d = 64 the second map's half lies in the second half of its 64-wide product
+          tmem_ld32(tm_dq + (uint32_t)(D == 64 ? c * 3 : c), t);
+          tc_wait_ld();
+          if (c + 32 == D) arrive(Ly::B_ACCE);
+          if (prm.part0) store_rows<D>(t, prm.scale, prm.part0, row0, rows_valid, c, lane);
+          else if (lane < rows_valid) store_bf16(t, prm.scale, dst + c);
+        }
+        ++k_unit;
+        v = vn;
+        x = xn;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn get_encode(std::string* err) {
+  static EncodeTiledFn fn = nullptr;
+  if (fn) return fn;
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !ptr) {
+    *err = "cuTensorMapEncodeTiled is not available from the driver";
+    return nullptr;
+  }
+  fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  return fn;
+}
+
+// [parts][L][d] bf16 rows, boxes of box_rows x 64 columns with 128-byte swizzle; rows of a box past L
+// are zeros.
+static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64_t L, uint64_t parts, int d, int box_rows,
+                     std::string* err) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)L * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return false;
+  }
+  return true;
+}
+
+template <int D, bool KV>
+static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direct, cudaStream_t st, std::string* err) {
+  const char* tb = static_cast<const char*>(a.tables);
+  Params prm{};
+  prm.header = reinterpret_cast<const TablesHeader*>(tb);
+  prm.tag = a.tag;
+  prm.items = reinterpret_cast<const DevItem*>(tb + (direct ? a.tl.flat_item : KV ? a.tl.kv_items : a.tl.items));
+  prm.list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : KV ? a.tl.q_list : a.tl.kv_list));
+  prm.lse = a.LSE;
+  prm.dsum = reinterpret_cast<const float*>(a.ws + w.dsum);
+  prm.lam = static_cast<const __nv_bfloat16*>(a.lam);
+  prm.out0 = static_cast<__nv_bfloat16*>(KV ? a.dK : a.dQ);
+  prm.out1 = static_cast<__nv_bfloat16*>(a.dV);
+  prm.part0 = direct ? nullptr : reinterpret_cast<float*>(a.ws + (KV ? w.dk_part : w.dq_part));
+  prm.part1 = direct ? nullptr : reinterpret_cast<float*>(a.ws + w.dv_part);
+  prm.dlam_part = reinterpret_cast<float*>(a.ws + w.dlam_part);
+  prm.status = a.status;
+  prm.counter = reinterpret_cast<uint32_t*>(a.ws + w.counters) + (KV ? 0 : 64);
+  prm.S = a.S;
+  prm.L = direct ? a.S : a.L;
+  prm.B = a.B;
+  prm.Hq = a.Hq;
+  prm.Hkv = a.Hkv;
+  prm.P = direct ? 1 : a.P;
+  prm.n_slots = direct ? 1 : KV ? a.n_kv_slots : a.n_slots;
+  prm.n_items = prm.n_slots;
+  prm.nb = (int32_t)((prm.L + BM - 1) / BM);
+  prm.ns = (int32_t)((prm.L + BS - 1) / BS);
+  const int64_t units = (int64_t)prm.nb * prm.n_items * a.B * (KV ? a.Hkv : a.Hq);
+  if (units > 0x3fffffff) {
+    *err = "too many work units for one launch";
+    return (int)cudaErrorInvalidConfiguration;
+  }
+  prm.n_units = (int32_t)units;
+  prm.causal = a.causal;
+  prm.lam_n = a.lam_n;
+  prm.scale = a.scale;
+  prm.scale_log2 = a.scale_log2;
+  prm.wait_limit_ns = a.wait_limit_ns;
+  EncodeTiledFn enc = get_encode(err);
+  if (!enc) return (int)cudaErrorNotSupported;
+  CUtensorMap r0, r1, sa, sbm;
+  const uint64_t L = (uint64_t)prm.L, qp = (uint64_t)a.B * a.Hq * prm.P, kp = (uint64_t)a.B * a.Hkv * prm.P;
+  if (!make_map(enc, &r0, KV ? a.K : a.Q, L, KV ? kp : qp, D, BM, err) ||
+      !make_map(enc, &r1, KV ? a.V : a.dO, L, KV ? kp : qp, D, BM, err) ||
+      !make_map(enc, &sa, KV ? a.Q : a.K, L, KV ? qp : kp, D, BS, err) ||
+      !make_map(enc, &sbm, KV ? a.dO : a.V, L, KV ? qp : kp, D, BS, err))
+    return (int)cudaErrorInvalidValue;
+  auto kern = diff_bwd_kernel<D, KV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::TOTAL);
+  // setmaxnreg hands registers between warpgroups within the launch's pool: the split must fit
+  // the registers the kernel is launched with, or a raising warpgroup would wait forever
+  cudaFuncAttributes fa;
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+  if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * EW_REGS + 128 * MMA_REGS + 128 * EPI_REGS) {
+    *err = "differential backward built with " + std::to_string(fa.numRegs) +
+           " registers per thread, fewer than its warpgroups' register split needs";
+    return (int)cudaErrorInvalidConfiguration;
+  }
+  // with a CTA for every unit the counter is not read
+  if (e == cudaSuccess && units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
+  if (e == cudaSuccess) {
+    kern<<<dim3((unsigned)std::min<int64_t>(units, sms)), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(r0, r1, sa, sbm, prm);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) *err = std::string("diff_bwd launch: ") + cudaGetErrorString(e);
+  return (int)e;
+}
+
+}  // namespace dbtc
+
+int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct, void* stream,
+                       std::string* err) {
+  cudaStream_t st = (cudaStream_t)stream;
+  if (a.d == 128)
+    return kv ? dbtc::launch<128, true>(a, w, sms, direct, st, err) : dbtc::launch<128, false>(a, w, sms, direct, st, err);
+  return kv ? dbtc::launch<64, true>(a, w, sms, direct, st, err) : dbtc::launch<64, false>(a, w, sms, direct, st, err);
+}
+
+}  // namespace mesh

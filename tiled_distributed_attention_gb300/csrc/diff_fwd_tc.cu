@@ -722,15 +722,8 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
 
 }  // namespace dtc
 
-// The whole sequence as one work item, unless its query tiles leave SMs idle and the plan splits
-// the keys (more than one slot a partition).
-bool diff_fwd_direct(const DiffArgs& a, int sms) {
-  const int64_t tiles = (a.S + dtc::BM - 1) / dtc::BM * a.B * a.Hq;
-  return a.single_slot || tiles >= sms;
-}
-
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err) {
-  const bool direct = diff_fwd_direct(a, sms);
+  const bool direct = rows_direct(a, a.Hq, a.single_slot, sms);
   cudaStream_t st = (cudaStream_t)stream;
   const int ce = a.d == 128 ? dtc::launch<128>(a, w, sms, direct, st, err) : dtc::launch<64>(a, w, sms, direct, st, err);
   if (ce != (int)cudaSuccess || direct) return ce;

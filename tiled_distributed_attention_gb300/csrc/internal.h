@@ -204,23 +204,31 @@ struct DiffWorkspace {
   size_t counters;            // 512 bytes
   size_t part_o, part_lse;    // forward partials
   size_t qx, pieces;          // fp32: q of each map with the other half zeroed; the forward's bf16 pieces
-  size_t gx;                  // fp32 backward: the gradients that reach each map's output
+  size_t gx;                  // fp32 backward: the gradient that reaches each map's output
   size_t dsum;                // [B, 2 Hq, S] row terms of dS
-  size_t dlam_part;           // [B, Hq, n_dlam]
+  size_t dlam_part;           // [B, Hq, n], n as the path has it
   size_t dq_part, dk_part, dv_part;
-  int64_t n_dlam;
   size_t total;
 };
 DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                              bool backward);
+// Whether a bf16 pass over the rows of H heads takes the whole sequence as one work item: unless its
+// 128-row blocks leave SMs idle and the plan splits the other axis (`single`: it does not).
+bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms);
 // bf16 forward on the tensor cores, with its merge where the plan's slots split the keys.
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
-int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool grad, void* stream,
+// bf16 backward: dK and dV (kv), or dQ and the sums behind dlam; written as they are (direct) or as
+// partial sums per slot.
+int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct, void* stream,
                        std::string* err);
+// fp32: q (and the gradient) one map a head.
+int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, bool grad, void* stream, std::string* err);
 int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
-int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
-int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
+int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err);
+// dlam from n_part partial sums of every (batch, head).
+int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,
+                     std::string* err);
 
 // Record `msg` as the calling thread's last error (mesh_attn_last_error) and return `code`.
 int set_last_error(int code, const std::string& msg);
