@@ -9,6 +9,7 @@ fallback: if the library is missing, load_library() raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Dict, Optional, Sequence, Tuple
@@ -152,7 +153,10 @@ class Plan:
     def tables(self, device=None) -> torch.Tensor:
         """The plan's constant tables on `device`, copied there on the first call (which waits for the copy,
         so that every stream may read them; make it before capturing a graph) and shared by all later ones."""
-        dev = torch.device(device if device is not None else "cuda")
+        got = self._tables.get(device)  # by index, the usual call
+        if got is not None:
+            return got
+        dev = torch.device("cuda" if device is None else device)
         index = dev.index if dev.index is not None else torch.cuda.current_device()
         got = self._tables.get(index)
         if got is None:
@@ -553,20 +557,46 @@ class MeshRope:
         self.freq, self.axis = tuple(freq), tuple(axis)
         self._freq = (ctypes.c_double * n)(*freq)
         self._axis = (c_i32 * n)(*axis)
+        self._adjacent = int(style == "adjacent")
+
+
+@functools.lru_cache(maxsize=1024)
+def _i64x3(a: int, b: int, c: int):
+    return (c_i64 * 3)(a, b, c)
 
 
 def _strides3(t: torch.Tensor):
-    return (c_i64 * 3)(*t.stride()[:3])
+    st = t.stride()
+    return _i64x3(st[0], st[1], st[2])
 
 
-def _one_device(*ts):
-    dev = ts[0].device
+def _one_device(*ts) -> int:
+    """The CUDA device all tensors are on."""
+    index = ts[0].get_device()
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if t.device != dev:
-            raise ValueError(f"tensors are on different devices: {dev} and {t.device}")
-    return dev
+        if t.get_device() != index or index < 0 or not t.is_cuda:
+            raise ValueError("tensors must be on one CUDA device; got " + ", ".join(str(t.device) for t in ts))
+    return index
+
+
+# A step of a small model is shorter than a few Python calls, so the calls below take the current device
+# and stream by index and pass plain integers, which is several times quicker than the objects.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _raw_stream(index: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _on_device(index: int, where: str, fn, *args) -> None:
+    """fn(*args), a C entry point, with the tensors' device current."""
+    if _current_device() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc:
+        _check(rc, where)
 
 
 def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
@@ -578,17 +608,19 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
     if q.dim() != 4 or q.shape[3] != rope.d:
         raise ValueError(f"q must be [B, H, S, {rope.d}]")
     B, Hq, S, d = q.shape
-    pairs = [(q, q_out)] + ([(k, k_out)] if k is not None else [])
+    pairs = ((q, q_out),) if k is None else ((q, q_out), (k, k_out))
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
+    dtype = q.dtype
     for x, y in pairs:
-        if x.dim() != 4 or (x.shape[0], x.shape[2], x.shape[3]) != (B, S, d):
+        shape = x.shape
+        if len(shape) != 4 or shape[0] != B or shape[2] != S or shape[3] != d:
             raise ValueError("q and k must agree in batch, tokens and columns")
-        if y.shape != x.shape:
+        if y.shape != shape:
             raise ValueError("an output must have its input's shape")
-        if x.dtype != q.dtype or y.dtype != q.dtype:
+        if x.dtype != dtype or y.dtype != dtype:
             raise ValueError("q, k and the outputs must be of one dtype")
-        if x.numel() and (x.stride(3) != 1 or y.stride(3) != 1):
+        if (x.stride(3) != 1 or y.stride(3) != 1) and x.numel():
             raise ValueError("the columns of a head must be consecutive")
     if positions.dtype not in (torch.int32, torch.int64):
         raise ValueError("positions must be int32 or int64")
@@ -600,17 +632,14 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
     if pos.dim() != 3 or pos.shape[0] != rope.n_axes or pos.shape[1] not in (1, B) or pos.shape[2] != S:
         raise ValueError(f"positions must be [{rope.n_axes}, S] or [{rope.n_axes}, B, S] with B = {B}, S = {S}; got "
                          f"{tuple(positions.shape)}")
-    dev = _one_device(q, *(t for p in pairs for t in p), positions)
-    pst = list(pos.stride())
-    if pos.shape[1] == 1:
-        pst[1] = 0
-    with torch.cuda.device(dev):
-        _check(_lib.mesh_attn_rope(_dtype_code(q.dtype), B, S, d, Hq, _ptr(q), _strides3(q), _ptr(q_out), _strides3(q_out),
-                                   0 if k is None else k.shape[1], _ptr(k), None if k is None else _strides3(k),
-                                   _ptr(k_out), None if k is None else _strides3(k_out), rope.groups, rope.n_pairs,
-                                   rope.n_axes, rope._freq, rope._axis, int(rope.style == "adjacent"), int(inverse),
-                                   _ptr(pos), 8 * pos.element_size(), (c_i64 * 3)(*pst), _stream_handle(stream)),
-               "mesh_attn_rope")
+    index = _one_device(positions, *(t for p in pairs for t in p))
+    ps = pos.stride()
+    _on_device(index, "mesh_attn_rope", _lib.mesh_attn_rope, _dtype_code(q.dtype), B, S, d, Hq, q.data_ptr(), _strides3(q),
+               q_out.data_ptr(), _strides3(q_out), 0 if k is None else k.shape[1], None if k is None else k.data_ptr(),
+               None if k is None else _strides3(k), None if k is None else k_out.data_ptr(),
+               None if k is None else _strides3(k_out), rope.groups, rope.n_pairs, rope.n_axes, rope._freq, rope._axis,
+               rope._adjacent, int(inverse), pos.data_ptr(), 8 * pos.element_size(),
+               _i64x3(ps[0], ps[1] if pos.shape[1] != 1 else 0, ps[2]), _raw_stream(index, stream))
 
 
 def mesh_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
@@ -676,20 +705,22 @@ def _diff_scale(scale: Optional[float], d: int) -> float:
 
 
 def _diff_check(q, k, v, lam, *more):
-    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape:
+    """(B, Hq, S, d, device) of matching tensors of one dtype on one device."""
+    qs, ks, ls = q.shape, k.shape, lam.shape
+    if len(qs) != 4 or len(ks) != 4 or v.shape != ks:
         raise ValueError("q must be [B, Hq, S, d], k and v [B, Hkv, S, d]")
-    B, Hq, S, d = q.shape
-    if (k.shape[0], k.shape[3]) != (B, d):
+    B, Hq, S, d = qs
+    if ks[0] != B or ks[3] != d:
         raise ValueError("q, k and v must agree in batch and columns")
-    if k.shape[1] < 1 or Hq % k.shape[1]:
-        raise ValueError(f"Hq must be a multiple of Hkv: {Hq} and {k.shape[1]}")
-    if lam.dim() != 1 or lam.shape[0] not in (1, Hq):
+    if ks[1] < 1 or Hq % ks[1]:
+        raise ValueError(f"Hq must be a multiple of Hkv: {Hq} and {ks[1]}")
+    if len(ls) != 1 or (ls[0] != Hq and ls[0] != 1):
         raise ValueError("lam must be [Hq], or [1] for one value for all heads")
-    for t in (q, k, v, lam) + more:
-        if t.dtype != q.dtype:
+    dtype = q.dtype
+    for t in (k, v, lam) + more:
+        if t.dtype != dtype:
             raise ValueError("q, k, v, lam and the gradients must be of one dtype")
-    dev = _one_device(q, k, v, lam, *more)
-    return B, Hq, S, d, dev
+    return B, Hq, S, d, _one_device(q, k, v, lam, *more)
 
 
 def mesh_attn_diff_workspace_size(plan: Plan, dtype: torch.dtype, B: int, Hq: int, Hkv: int, d: int,
@@ -707,44 +738,65 @@ def new_diff_workspace(plan: Plan, q: torch.Tensor, k: torch.Tensor, backward: b
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
+def _contiguous(*ts):
+    for t in ts:
+        if not t.is_contiguous():
+            raise ValueError("q, k, v, lam, the gradients and the outputs must be contiguous")
+
+
+def _diff_plan_check(plan: Plan, q, k):
+    S = plan.info.S
+    if q.shape[2] != S or k.shape[2] != S:
+        raise ValueError(f"the plan is for S = {S}; q has {q.shape[2]} tokens, k and v {k.shape[2]}")
+
+
 def mesh_attn_diff_fwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
                        scale: Optional[float], O: torch.Tensor, O2: Optional[torch.Tensor], LSE: torch.Tensor,
                        workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     outs = (O,) if O2 is None else (O, O2)
-    B, Hq, S, d, dev = _diff_check(q, k, v, lam, *outs)
-    if S != plan.S or k.shape[2] != plan.S:
-        raise ValueError(f"the plan is for S = {plan.S}; q has {S} tokens, k and v {k.shape[2]}")
+    B, Hq, S, d, index = _diff_check(q, k, v, lam, *outs)
     if any(t.shape != q.shape for t in outs) or LSE.shape != (B, Hq, 2, S) or LSE.dtype != torch.float32:
         raise ValueError("O and O2 must have q's shape, LSE must be fp32 [B, Hq, 2, S]")
-    if not all(t.is_contiguous() for t in (q, k, v, lam, LSE) + outs):
-        raise ValueError("q, k, v, lam and the outputs must be contiguous")
     _one_device(q, LSE, workspace, status)
-    with torch.cuda.device(dev):
-        _check(_lib.mesh_attn_diff_fwd(plan.handle, _ptr(plan.tables(dev)), _dtype_code(q.dtype), B, Hq, k.shape[1], d,
-                                       _ptr(q), _ptr(k), _ptr(v), _ptr(lam), lam.shape[0], _diff_scale(scale, d), _ptr(O),
-                                       _ptr(O2), _ptr(LSE), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _ptr(status), _stream_handle(stream)), "mesh_attn_diff_fwd")
+    _contiguous(LSE, *outs)
+    _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream)
+
+
+def _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream=None):
+    _contiguous(q, k, v, lam)
+    _diff_plan_check(plan, q, k)
+    B, Hq, S, d = q.shape
+    _on_device(index, "mesh_attn_diff_fwd", _lib.mesh_attn_diff_fwd, plan.handle, plan.tables(index).data_ptr(),
+               _dtype_code(q.dtype), B, Hq, k.shape[1], d, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
+               lam.shape[0], _diff_scale(scale, d), O.data_ptr(), None if O2 is None else O2.data_ptr(), LSE.data_ptr(),
+               workspace.data_ptr(), workspace.numel() * workspace.element_size(), status.data_ptr(),
+               _raw_stream(index, stream))
 
 
 def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, O: torch.Tensor,
                        O2: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, scale: Optional[float], dQ: torch.Tensor,
                        dK: torch.Tensor, dV: torch.Tensor, dlam: torch.Tensor, workspace: torch.Tensor,
                        status: torch.Tensor, stream=None) -> None:
-    B, Hq, S, d, dev = _diff_check(q, k, v, lam, O, O2, dO, dQ, dK, dV, dlam)
-    if S != plan.S or k.shape[2] != plan.S:
-        raise ValueError(f"the plan is for S = {plan.S}; q has {S} tokens, k and v {k.shape[2]}")
-    if any(t.shape != q.shape for t in (O, O2, dO, dQ)) or dK.shape != k.shape or dV.shape != v.shape or \
-            dlam.shape != lam.shape or LSE.shape != (B, Hq, 2, S) or LSE.dtype != torch.float32:
-        raise ValueError("O, O2, dO and dQ must have q's shape, dK, dV and dlam that of k, v and lam, LSE fp32 [B, Hq, 2, S]")
-    if not all(t.is_contiguous() for t in (q, k, v, lam, O, O2, LSE, dO, dQ, dK, dV, dlam)):
-        raise ValueError("tensors must be contiguous")
-    _one_device(q, LSE, workspace, status)
-    with torch.cuda.device(dev):
-        _check(_lib.mesh_attn_diff_bwd(plan.handle, _ptr(plan.tables(dev)), _dtype_code(q.dtype), B, Hq, k.shape[1], d,
-                                       _ptr(q), _ptr(k), _ptr(v), _ptr(lam), lam.shape[0], _ptr(O), _ptr(O2), _ptr(LSE),
-                                       _ptr(dO), _diff_scale(scale, d), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dlam),
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-                                       _stream_handle(stream)), "mesh_attn_diff_bwd")
+    index = _diff_check(q, k, v, lam, O, O2, dO, dQ, dK, dV, dlam)[4]
+    if dQ.shape != q.shape or dK.shape != k.shape or dV.shape != v.shape or dlam.shape != lam.shape:
+        raise ValueError("dQ, dK, dV and dlam must have the shapes of q, k, v and lam")
+    _one_device(q, workspace, status)
+    _contiguous(dQ, dK, dV, dlam)
+    _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream)
+
+
+def _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream=None):
+    B, Hq, S, d = q.shape
+    if O.shape != q.shape or O2.shape != q.shape or dO.shape != q.shape or LSE.shape != (B, Hq, 2, S) or \
+            LSE.dtype != torch.float32 or LSE.get_device() != index:
+        raise ValueError("O, O2 and dO must have q's shape, LSE must be fp32 [B, Hq, 2, S] on q's device")
+    _contiguous(q, k, v, lam, O, O2, LSE, dO)
+    _diff_plan_check(plan, q, k)
+    _on_device(index, "mesh_attn_diff_bwd", _lib.mesh_attn_diff_bwd, plan.handle, plan.tables(index).data_ptr(),
+               _dtype_code(q.dtype), B, Hq, k.shape[1], d, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
+               lam.shape[0], O.data_ptr(), O2.data_ptr(), LSE.data_ptr(), dO.data_ptr(), _diff_scale(scale, d),
+               dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dlam.data_ptr(), workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), status.data_ptr(), _raw_stream(index, stream))
 
 
 def _raise_status(status: torch.Tensor):
@@ -765,14 +817,15 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     mesh_diff_attention_backward takes.  A program that calls it every step keeps plan, workspace
     (new_diff_workspace) and status (new_status) and passes check_status=False, which leaves out the wait.
     """
-    B, Hq, S, d, dev = _diff_check(q, k, v, lam)
+    B, Hq, S, d, index = _diff_check(q, k, v, lam)
     plan = plan or mesh_attn_plan_create(S, P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k) if workspace is None else workspace
-    st = new_status(dev) if status is None else status
+    st = new_status(q.device) if status is None else status
+    _one_device(q, ws, st)
     O = torch.empty_like(q)
     O2 = torch.empty_like(q) if return_saved else None
-    LSE = torch.empty(B, Hq, 2, S, dtype=torch.float32, device=dev)
-    mesh_attn_diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, ws, st, torch.cuda.current_stream(dev))
+    LSE = torch.empty((B, Hq, 2, S), dtype=torch.float32, device=q.device)
+    _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
     return (O, O2, LSE) if return_saved else (O, LSE)
@@ -784,12 +837,13 @@ def mesh_diff_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                                  plan: Optional[Plan] = None, workspace: Optional[torch.Tensor] = None,
                                  status: Optional[torch.Tensor] = None, check_status: bool = True):
     """(dQ, dK, dV, dlam) from the forward's O, O2 and LSE and the gradient dO, on the current stream."""
-    B, Hq, S, d, dev = _diff_check(q, k, v, lam, O, O2, dO)
+    B, Hq, S, d, index = _diff_check(q, k, v, lam, O, O2, dO)
     plan = plan or mesh_attn_plan_create(S, P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k, backward=True) if workspace is None else workspace
-    st = new_status(dev) if status is None else status
-    grads = tuple(torch.empty_like(t) for t in (q, k, v, lam))
-    mesh_attn_diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, *grads, ws, st, torch.cuda.current_stream(dev))
+    st = new_status(q.device) if status is None else status
+    _one_device(q, ws, st)
+    grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(lam))
+    _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, *grads, ws, st, index)
     if check_status:
         _raise_status(st)
     return grads
@@ -837,25 +891,28 @@ def mesh_attn_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                           lam: torch.Tensor, scale: Optional[float], O: torch.Tensor, LSE: torch.Tensor,
                           workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     load_library()
-    B, Hq, S, d, dev = _diff_check(q, k_cache, v_cache, lam, O)
+    B, Hq, S, d, index = _diff_check(q, k_cache, v_cache, lam, O)
+    if O.shape != q.shape or LSE.shape != (B, Hq, 2, 1) or LSE.dtype != torch.float32:
+        raise ValueError("O must have q's shape, LSE must be fp32 [B, Hq, 2, 1]")
+    _contiguous(O, LSE)
+    _one_device(q, LSE, workspace, status)
+    _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream)
+
+
+def _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream=None):
+    B, Hq, S, d = q.shape
     T = k_cache.shape[2]
     if S != 1:
         raise ValueError("q must hold one token a sequence: [B, Hq, 1, d]")
-    if lens.shape != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous():
-        raise ValueError("lens must be contiguous int32 [B]")
-    if O.shape != q.shape or LSE.shape != (B, Hq, 2, 1) or LSE.dtype != torch.float32:
-        raise ValueError("O must have q's shape, LSE must be fp32 [B, Hq, 2, 1]")
-    if not all(t.is_contiguous() for t in (q, lam, O, LSE)):
-        raise ValueError("q, lam, O and LSE must be contiguous")
-    if T and (k_cache.stride(3) != 1 or v_cache.stride(3) != 1):
+    if lens.shape != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous() or lens.get_device() != index:
+        raise ValueError("lens must be contiguous int32 [B] on q's device")
+    _contiguous(q, lam)
+    if (k_cache.stride(3) != 1 or v_cache.stride(3) != 1) and T:
         raise ValueError("the columns of the caches must be consecutive")
-    _one_device(q, lens, LSE, workspace, status)
-    with torch.cuda.device(dev):
-        _check(_lib.mesh_attn_diff_decode(_dtype_code(q.dtype), B, Hq, k_cache.shape[1], d, T, _ptr(q), _ptr(k_cache),
-                                          _strides3(k_cache), _ptr(v_cache), _strides3(v_cache), _ptr(lens), _ptr(lam),
-                                          lam.shape[0], _diff_scale(scale, d), _ptr(O), _ptr(LSE), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _ptr(status),
-                                          _stream_handle(stream)), "mesh_attn_diff_decode")
+    _on_device(index, "mesh_attn_diff_decode", _lib.mesh_attn_diff_decode, _dtype_code(q.dtype), B, Hq, k_cache.shape[1], d, T,
+               q.data_ptr(), k_cache.data_ptr(), _strides3(k_cache), v_cache.data_ptr(), _strides3(v_cache), lens.data_ptr(),
+               lam.data_ptr(), lam.shape[0], _diff_scale(scale, d), O.data_ptr(), LSE.data_ptr(), workspace.data_ptr(),
+               workspace.numel() * workspace.element_size(), status.data_ptr(), _raw_stream(index, stream))
 
 
 def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor, lam: torch.Tensor,
@@ -865,12 +922,14 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     (int32, on the device) tokens of k_cache, v_cache [B, Hkv, T, d], which may be views with other strides (16-byte
     multiples).  Returns O [B, Hq, 1, d] and LSE [B, Hq, 2, 1].  A serving loop keeps workspace
     (new_diff_decode_workspace) and status and passes check_status=False."""
-    B, Hq, S, d, dev = _diff_check(q, k_cache, v_cache, lam)
-    ws = new_diff_decode_workspace(B, Hq, k_cache.shape[1], d, k_cache.shape[2], dev) if workspace is None else workspace
-    st = new_status(dev) if status is None else status
-    O = torch.empty_like(q, memory_format=torch.contiguous_format)
-    LSE = torch.empty(B, Hq, 2, 1, dtype=torch.float32, device=dev)
-    mesh_attn_diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, torch.cuda.current_stream(dev))
+    load_library()
+    B, Hq, S, d, index = _diff_check(q, k_cache, v_cache, lam)
+    ws = new_diff_decode_workspace(B, Hq, k_cache.shape[1], d, k_cache.shape[2], q.device) if workspace is None else workspace
+    st = new_status(q.device) if status is None else status
+    _one_device(q, ws, st)
+    O = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    LSE = torch.empty((B, Hq, 2, 1), dtype=torch.float32, device=q.device)
+    _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
     return O, LSE

@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmesh_attn.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["planner.cpp", "abi.cu", "tile_fwd_tc.cu", "tile_fwd_tc32.cu", "merge.cu", "noalloc.cu",
-           "tile_bwd_simt.cu", "tile_bwd_tc.cu", "bwd_aux.cu", "rope.cu", "diff_abi.cu", "diff_aux.cu", "diff_fwd_tc.cu", "diff_bwd_tc.cu", "diff_decode.cu"]
+           "tile_bwd_simt.cu", "tile_bwd_tc.cu", "bwd_aux.cu", "rope.cu", "diff_abi.cu", "diff_aux.cu", "diff_fwd_tc.cu", "diff_bwd_tc.cu", "diff_bwd_simt.cu", "diff_decode.cu"]
 
 
 def nvcc() -> str:

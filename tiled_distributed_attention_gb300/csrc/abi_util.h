@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <exception>
 #include <new>
 #include <stdexcept>
@@ -30,6 +31,35 @@ int guarded_call(F&& f) {
 }
 
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// SMs of the current device, asked once per device (a constant of it).
+inline cudaError_t current_sms(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev >= 0 && dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return e;
+}
+
+// Whether `what` still has to be done on the current device: a kernel's shared-memory limit is set once
+// per device and kernel.  `mark` records that it was.
+struct OncePerDevice {
+  std::atomic<uint64_t> bits{0};
+  static int device() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? dev : -1;
+  }
+  bool pending(int dev) const { return dev < 0 || !(bits.load(std::memory_order_acquire) >> dev & 1); }
+  void mark(int dev) {
+    if (dev >= 0) bits.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+  }
+};
 
 // A launcher's result (a cudaError_t value and its message) as a status.
 inline int launch_status(int ce, const std::string& err) {

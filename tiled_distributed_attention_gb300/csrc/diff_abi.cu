@@ -55,23 +55,31 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
   const bool f32 = dt == MESH_ATTN_F32;
   // bf16 needs partial sums only where the plan's slots split an axis (rows_direct)
   const int64_t tiles = (plan.S + 127) / 128 * B;
-  const bool q_part = f32 || (plan.n_slots() != plan.P && tiles * Hq < MAX_SMS);
-  const bool kv_part = f32 || (plan.n_kv_slots() != plan.P && tiles * Hkv < MAX_SMS);
-  if (f32) w.qx = take(2 * qrows * d * 4);
+  const bool q_slots = plan.n_slots() != plan.P && tiles * Hq < MAX_SMS;
+  const bool kv_slots = plan.n_kv_slots() != plan.P && tiles * Hkv < MAX_SMS;
   if (!backward) {
-    if (q_part) {
-      w.part_o = take(2 * prows * d * 4);
-      w.part_lse = take(2 * prows * 4);
+    if (f32 || q_slots) {  // fp32: both maps' outputs always go through the merge
+      const size_t rows = 2 * (q_slots ? std::max(prows, qrows) : qrows);
+      w.part_o = take(rows * d * 4);
+      w.part_lse = take(rows * 4);
     }
     if (f32) w.pieces = take(f32_pieces_layout(B, 2 * Hq, Hkv, plan.S, d).total);
   } else {
-    if (f32) w.gx = take(2 * qrows * d * 4);
     w.dsum = take(2 * qrows * 4);
     // per (batch, head): fp32 one sum per 64 rows; bf16 eight per 128-row block of every slot
     const int64_t by_slot = (int64_t)plan.n_slots() * ((plan.L + 127) / 128) * 8, flat = (plan.S + 127) / 128 * 8;
-    w.dlam_part = take((size_t)B * Hq * 4 * (size_t)(f32 ? (plan.S + 63) / 64 : q_part ? std::max(by_slot, flat) : flat));
-    if (q_part) w.dq_part = take((f32 ? 2 : 1) * prows * d * 4);
-    if (kv_part) {
+    w.dlam_part = take((size_t)B * Hq * 4 * (size_t)(f32 ? (plan.S + 63) / 64 : q_slots ? std::max(by_slot, flat) : flat));
+    if (f32) {  // partial sums of the splits, and of a KV head's query heads
+      const size_t splits = (size_t)diff_simt_splits(plan.S, B, Hq, MAX_SMS);  // grows with the SM count
+      if (splits > 1) w.dq_part = take(splits * qrows * d * 4);
+      if (splits * (Hq / Hkv) > 1) {
+        w.dk_part = take(splits * qrows * d * 4);
+        w.dv_part = take(splits * qrows * d * 4);
+      }
+    } else if (q_slots) {
+      w.dq_part = take(prows * d * 4);
+    }
+    if (!f32 && kv_slots) {
       const size_t kv = (size_t)B * Hkv * plan.n_kv_slots() * (size_t)plan.L * d * 4;
       w.dk_part = take(kv);
       w.dv_part = take(kv);
@@ -104,6 +112,8 @@ int check_sizes(const mesh_attn_plan* plan, mesh_attn_dtype dt, int32_t B, int32
   if (d != 64 && d != 128) return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "d must be 64 or 128");
   if ((int64_t)B * Hq > 0x3fffffff || 2 * (int64_t)B * Hq * plan->p.S >= (int64_t)1 << 31)
     return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "2 * B * Hq * S must be < 2^31");
+  if (dt == MESH_ATTN_F32 && (6 * (int64_t)B * Hq * plan->p.S >= (int64_t)1 << 31 || B > 8191 || Hq > 65535))
+    return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "fp32: 6 * B * Hq * S must be < 2^31, B < 8192 and Hq < 65536");
   return MESH_ATTN_OK;
 }
 
@@ -124,10 +134,9 @@ int check_common(const DiffArgs& a, mesh_attn_dtype dt, const void* workspace, s
 }
 
 int sm_count(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  const cudaError_t e = mesh::current_sms(sms);
   if (e != cudaSuccess) return set_last_error(MESH_ATTN_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
+  *sms = std::min(*sms, mesh::MAX_SMS);
   return MESH_ATTN_OK;
 }
 
@@ -238,33 +247,35 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
       if ((rc = sm_count(&sms))) return rc;
       return launch_status(mesh::launch_diff_fwd_tc(a, w, sms, stream, &err), err);
     }
-    if ((rc = launch_status(mesh::launch_diff_expand(a, w, false, stream, &err), err))) return rc;
+    // fp32: split into bf16 pieces, one map a head with the other half of its query's columns zero, so
+    // that the plain fp32 tile kernel over 2 Hq heads gives both maps; then the merge
+    int sms = 0;
+    if ((rc = sm_count(&sms))) return rc;
+    const bool direct = mesh::rows_direct(a, 2 * Hq, a.single_slot, sms);
+    if ((rc = launch_status(mesh::launch_diff_split(a, w, stream, &err), err))) return rc;
     mesh::TileArgs t{};
     const char* tb = static_cast<const char*>(tables);
-    t.Q = a.ws + w.qx;
-    t.K = K;
-    t.V = V;
     t.part_o = reinterpret_cast<float*>(a.ws + w.part_o);
     t.part_lse = reinterpret_cast<float*>(a.ws + w.part_lse);
-    t.items = reinterpret_cast<const mesh::DevItem*>(tb + a.tl.items);
-    t.kv_list = reinterpret_cast<const int32_t*>(tb + a.tl.kv_list);
+    t.items = reinterpret_cast<const mesh::DevItem*>(tb + (direct ? a.tl.flat_item : a.tl.items));
+    t.kv_list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : a.tl.kv_list));
     t.status = d_status;
     t.S = a.S;
-    t.L = a.L;
+    t.L = direct ? a.S : a.L;
     t.B = B;
     t.Hq = 2 * Hq;
     t.Hkv = Hkv;
     t.d = d;
-    t.P = a.P;
-    t.n_items = a.n_slots;
-    t.n_slots = a.n_slots;
+    t.P = direct ? 1 : a.P;
+    t.n_items = t.n_slots = direct ? 1 : a.n_slots;
     t.causal = a.causal;
     t.scale = scale;
     t.scale_log2 = a.scale_log2;
     t.wait_limit_ns = a.wait_limit_ns;
     t.pieces = a.ws + w.pieces;
+    t.pieces_ready = true;
     if ((rc = launch_status(mesh::launch_tile_fwd_tc32(t, stream, &err), err))) return rc;
-    return launch_status(mesh::launch_diff_merge(a, w, dtype, stream, &err), err);
+    return launch_status(mesh::launch_diff_merge(a, w, dtype, direct, stream, &err), err);
   });
 }
 
@@ -326,42 +337,10 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
       const int64_t n = dq_direct ? (a.S + 127) / 128 * 8 : a.n_slots * ((a.L + 127) / 128) * 8;
       return launch_status(mesh::launch_diff_dlam(a, w, dtype, n, stream, &err), err);
     }
-    if ((rc = launch_status(mesh::launch_diff_expand(a, w, true, stream, &err), err))) return rc;
     if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
-    mesh::BwdArgs t{};
-    t.Q = a.ws + w.qx;
-    t.K = K;
-    t.V = V;
-    t.dO = a.ws + w.gx;
-    t.LSE = LSE;
-    t.D = reinterpret_cast<const float*>(a.ws + w.dsum);
-    t.dq_part = reinterpret_cast<float*>(a.ws + w.dq_part);
-    t.dk_part = reinterpret_cast<float*>(a.ws + w.dk_part);
-    t.dv_part = reinterpret_cast<float*>(a.ws + w.dv_part);
-    t.items = reinterpret_cast<const mesh::DevItem*>(tb + a.tl.items);
-    t.kv_list = reinterpret_cast<const int32_t*>(tb + a.tl.kv_list);
-    t.kv_items = reinterpret_cast<const mesh::DevItem*>(tb + a.tl.kv_items);
-    t.q_list = reinterpret_cast<const int32_t*>(tb + a.tl.q_list);
-    t.status = d_status;
-    t.S = a.S;
-    t.L = a.L;
-    t.B = B;
-    t.Hq = 2 * Hq;
-    t.Hkv = Hkv;
-    t.d = d;
-    t.P = a.P;
-    t.n_items = a.n_slots;
-    t.n_slots = a.n_slots;
-    t.n_kv_items = a.n_kv_slots;
-    t.n_kv_slots = a.n_kv_slots;
-    t.causal = a.causal;
-    t.scale = scale;
-    t.scale_log2 = a.scale_log2;
-    t.wait_limit_ns = a.wait_limit_ns;
-    if ((rc = launch_status(mesh::launch_tile_bwd_simt(t, stream, &err), err))) return rc;
-    if ((rc = launch_status(mesh::launch_diff_reduce_dq(a, w, stream, &err), err))) return rc;
-    if ((rc = reduce(w.dk_part, a.tl.kv_slot_off, dK, Hkv, a.n_kv_slots))) return rc;
-    if ((rc = reduce(w.dv_part, a.tl.kv_slot_off, dV, Hkv, a.n_kv_slots))) return rc;
+    int sms = 0;
+    if ((rc = sm_count(&sms))) return rc;
+    if ((rc = launch_status(mesh::launch_diff_bwd_simt(a, w, sms, stream, &err), err))) return rc;
     return launch_status(mesh::launch_diff_dlam(a, w, dtype, (a.S + 63) / 64, stream, &err), err);
   });
 }

@@ -1,6 +1,5 @@
-// Differential attention, the passes around its products: queries and gradients laid out one map a
-// head, the merge of the two maps' partial outputs, the row terms of the backward pass and the
-// gradient of lam.  All are bound by memory and read and write whole 16-byte pieces.
+// Differential attention, the passes around its products: fp32 inputs split into bf16 pieces, the merge of
+// the two maps' partial outputs, the row terms of the backward pass and the gradient of lam.  All are bound by memory and read and write whole 16-byte pieces.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,31 +32,45 @@ __device__ __forceinline__ float lam_of(const void* lam, int n, int h) {
   return to_f(static_cast<const T*>(lam)[n == 1 ? 0 : h]);
 }
 
-// One map a head: row (b, 2 h + m) of qx is q with the other map's half zeroed, so that plain
-// attention of 2 Hq heads over the full d columns gives both maps; of gx (backward) it is the gradient
-// of the map's output: dO for the first map, -lam dO for the second.
-__global__ void __launch_bounds__(THREADS) expand_kernel(const DiffArgs a, float* qx, float* gx) {
-  using T = float;
+// fp32 inputs as three bf16 pieces each, x = x1 + x2 + x3 exactly (round to nearest, then the rest), in one
+// launch for Q, K and V: blockIdx.y 0 is K, 1 is V, 2 is Q.  Q goes to two heads, (b, 2 h + m) holding map
+// m's half of the columns and zeros in the other, so that attention of 2 Hq heads over the full d
+// columns gives both maps.
+__global__ void __launch_bounds__(THREADS) split_kernel(const DiffArgs a, uint2* qp, uint2* kp, uint2* vp) {
   const TablesHeader* th = static_cast<const TablesHeader*>(a.tables);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
-    record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);
-  const int q4 = a.d / 4;
-  const int64_t n = (int64_t)a.B * a.Hq * a.S * q4;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
+    record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);  // another plan's tables: the tile kernel does nothing
+  const int which = blockIdx.y, q4 = a.d / 4;
+  const float* src = static_cast<const float*>(which == 0 ? a.K : which == 1 ? a.V : a.Q);
+  uint2* dst = which == 0 ? kp : which == 1 ? vp : qp;
+  const int64_t n = (int64_t)a.B * (which == 2 ? a.Hq : a.Hkv) * a.S * q4;
+  const int64_t piece = which == 2 ? 2 * n : n;  // in groups of four
   for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS) {
-    const int c = (int)(i % q4) * 4;
-    const int64_t row = i / q4;            // (b Hq + h) S + s
-    const int64_t bh = row / a.S, s = row - bh * a.S;
-    const int64_t dst = (2 * bh * a.S + s) * a.d + c, dst2 = dst + a.S * a.d;
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 q = load4(static_cast<const T*>(a.Q) + row * a.d + c);
-    const bool first = c < a.d / 2;
-    store4(qx + dst, first ? q : z);
-    store4(qx + dst2, first ? z : q);
-    if (gx) {
-      const float nl = -lam_of<T>(a.lam, a.lam_n, (int)(bh % a.Hq));
-      const float4 g = load4(static_cast<const T*>(a.dO) + row * a.d + c);
-      store4(gx + dst, g);
-      store4(gx + dst2, make_float4(g.x * nl, g.y * nl, g.z * nl, g.w * nl));
+    const float4 x = load4(src + 4 * i);
+    const float e[4] = {x.x, x.y, x.z, x.w};
+    uint2 w[3];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __nv_bfloat162 p1 = __floats2bfloat162_rn(e[2 * h], e[2 * h + 1]);
+      const float r0 = e[2 * h] - __low2float(p1), r1 = e[2 * h + 1] - __high2float(p1);
+      const __nv_bfloat162 p2 = __floats2bfloat162_rn(r0, r1);
+      const __nv_bfloat162 p3 = __floats2bfloat162_rn(r0 - __low2float(p2), r1 - __high2float(p2));
+      (h ? w[0].y : w[0].x) = *reinterpret_cast<const uint32_t*>(&p1);
+      (h ? w[1].y : w[1].x) = *reinterpret_cast<const uint32_t*>(&p2);
+      (h ? w[2].y : w[2].x) = *reinterpret_cast<const uint32_t*>(&p3);
+    }
+    int64_t at = i, other = -1;
+    if (which == 2) {
+      const int64_t row = i / q4, bh = row / a.S, per_head = a.S * q4;
+      const int64_t first = i + bh * per_head;  // head 2 h; head 2 h + 1 lies per_head behind
+      const bool m1 = i - row * q4 < q4 / 2;
+      at = m1 ? first : first + per_head;
+      other = m1 ? first + per_head : first;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      dst[k * piece + at] = w[k];
+      if (other >= 0) dst[k * piece + other] = make_uint2(0u, 0u);
     }
   }
 }
@@ -67,7 +80,7 @@ __global__ void __launch_bounds__(THREADS) expand_kernel(const DiffArgs a, float
 // head, partition); a thread a 16-byte piece of both maps.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const float* part_o, const float* part_lse,
-                                                        const int32_t* slot_off, int n_rblk) {
+                                                        const int32_t* slot_off, int P, int64_t L, int n_slots, int n_rblk) {
   constexpr int Q4 = D / 4;
   constexpr int PER = 2;
   constexpr int ROWS = PER * THREADS / Q4;
@@ -76,16 +89,15 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
   const int tid = threadIdx.x;
   const int rb = (int)(blockIdx.x % (unsigned)n_rblk);
   const int bhp = (int)(blockIdx.x / (unsigned)n_rblk);
-  const int p = bhp % a.P, bh = bhp / a.P;
-  const int64_t L = a.L;
+  const int p = bhp % P, bh = bhp / P;
   const int64_t r0 = (int64_t)rb * ROWS;
   const int nrows = (int)min((int64_t)ROWS, L - r0);
   const int s0 = __ldg(slot_off + p), ns = __ldg(slot_off + p + 1) - s0;
-  if (ns < 0 || ns > MAX_SLOTS) {
+  if (s0 < 0 || ns < 0 || ns > MAX_SLOTS || s0 + ns > n_slots) {
     if (tid == 0) record_error(a.status, MESH_ATTN_ERR_OUT_OF_RANGE, 5, (int32_t)blockIdx.x);
     return;
   }
-  const int64_t base[2] = {((2 * (int64_t)bh) * a.n_slots + s0) * L + r0, ((2 * (int64_t)bh + 1) * a.n_slots + s0) * L + r0};
+  const int64_t base[2] = {((2 * (int64_t)bh) * n_slots + s0) * L + r0, ((2 * (int64_t)bh + 1) * n_slots + s0) * L + r0};
   for (int i = tid; i < 2 * ns * ROWS; i += THREADS) {
     const int r = i % ROWS, t = i / ROWS % ns, m = i / ROWS / ns;
     w_s[m][t][r] = r < nrows ? __ldg(part_lse + base[m] + (int64_t)t * L + r) : -INFINITY;
@@ -134,11 +146,10 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
   }
 }
 
-// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2 (times -lam for the path whose
-// second map receives -lam dO).  One warp a row.
+// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2.  One warp a row.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* dsum, float* dlam_part, int64_t n_part,
-                                                       int rows_per_part, int scaled) {
+                                                       int rows_per_part) {
   if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t part = blockIdx.x % n_part;
@@ -164,7 +175,7 @@ __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* 
     }
     if (lane == 0) {
       dsum[2 * bh * a.S + s] = fmaf(lam, d2, d1);
-      dsum[(2 * bh + 1) * a.S + s] = scaled ? -lam * d2 : d2;
+      dsum[(2 * bh + 1) * a.S + s] = d2;
       acc -= (double)d2;
     }
   }
@@ -176,27 +187,6 @@ __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* 
       for (int w = 0; w < THREADS / 32; ++w) t += sums[w];
       dlam_part[bh * n_part + part] = (float)t;
     }
-  }
-}
-
-// dQ from the per-map partial sums: the first half of the columns from head 2 h, the second from 2 h + 1.
-__global__ void __launch_bounds__(THREADS) reduce_dq_kernel(const DiffArgs a, const float* part, const int32_t* slot_off) {
-  using T = float;
-  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
-  const int q4 = a.d / 4;
-  const int64_t n = (int64_t)a.B * a.Hq * a.S * q4;
-  for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * THREADS) {
-    const int c = (int)(i % q4) * 4;
-    const int64_t row = i / q4, bh = row / a.S, s = row - bh * a.S;
-    const int p = (int)(s / a.L);
-    const int s0 = __ldg(slot_off + p), s1 = __ldg(slot_off + p + 1);
-    const int64_t bm = 2 * bh + (c < a.d / 2 ? 0 : 1);
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = max(s0, 0); k < min(s1, a.n_slots); ++k) {
-      const float4 v = load4(part + ((bm * a.n_slots + k) * a.L + (s - p * a.L)) * a.d + c);
-      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-    }
-    store4(static_cast<T*>(a.dQ) + row * a.d + c, t);
   }
 }
 
@@ -234,33 +224,40 @@ static unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std:
 
 }  // namespace daux
 
-int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, bool grad, void* stream, std::string* err) {
+int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err) {
+  const F32Pieces pc = f32_pieces_layout(a.B, 2 * a.Hq, a.Hkv, a.S, a.d);
+  char* base = a.ws + w.pieces;
   const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
-  daux::expand_kernel<<<grid, daux::THREADS, 0, (cudaStream_t)stream>>>(
-      a, reinterpret_cast<float*>(a.ws + w.qx), grad ? reinterpret_cast<float*>(a.ws + w.gx) : nullptr);
-  return daux::done("diff expand launch", err);
+  daux::split_kernel<<<dim3(grid, 3), daux::THREADS, 0, (cudaStream_t)stream>>>(
+      a, reinterpret_cast<uint2*>(base + pc.q_off), reinterpret_cast<uint2*>(base + pc.k_off),
+      reinterpret_cast<uint2*>(base + pc.v_off));
+  return daux::done("diff split launch", err);
 }
 
 template <int D, typename T>
-static int merge_d(const DiffArgs& a, const DiffWorkspace& w, cudaStream_t st, std::string* err) {
+static int merge_d(const DiffArgs& a, const DiffWorkspace& w, bool flat, cudaStream_t st, std::string* err) {
   constexpr int ROWS = 2 * daux::THREADS / (D / 4);
-  const int64_t n_rblk = (a.L + ROWS - 1) / ROWS;
-  const int64_t blocks = n_rblk * a.B * a.Hq * a.P;
+  const int64_t L = flat ? a.S : a.L;
+  const int P = flat ? 1 : a.P;
+  const int64_t n_rblk = (L + ROWS - 1) / ROWS;
+  const int64_t blocks = n_rblk * a.B * a.Hq * P;
   if (blocks > 0x7fffffffLL || n_rblk > 0x7fffffffLL) {
     *err = "too many rows for one merge launch";
     return (int)cudaErrorInvalidConfiguration;
   }
   daux::merge_kernel<D, T><<<(unsigned)blocks, daux::THREADS, 0, st>>>(
       a, reinterpret_cast<const float*>(a.ws + w.part_o), reinterpret_cast<const float*>(a.ws + w.part_lse),
-      reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + a.tl.slot_off), (int)n_rblk);
+      reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + (flat ? a.tl.flat_list : a.tl.slot_off)), P, L,
+      flat ? 1 : a.n_slots, (int)n_rblk);
   return daux::done("diff merge launch", err);
 }
 
-int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool flat, void* stream,
+                      std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
   if (dt == MESH_ATTN_BF16)
-    return a.d == 128 ? merge_d<128, __nv_bfloat16>(a, w, st, err) : merge_d<64, __nv_bfloat16>(a, w, st, err);
-  return a.d == 128 ? merge_d<128, float>(a, w, st, err) : merge_d<64, float>(a, w, st, err);
+    return a.d == 128 ? merge_d<128, __nv_bfloat16>(a, w, flat, st, err) : merge_d<64, __nv_bfloat16>(a, w, flat, st, err);
+  return a.d == 128 ? merge_d<128, float>(a, w, flat, st, err) : merge_d<64, float>(a, w, flat, st, err);
 }
 
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
@@ -273,19 +270,11 @@ int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype 
   }
   float* dsum = reinterpret_cast<float*>(a.ws + w.dsum);
   if (dt == MESH_ATTN_BF16)
-    daux::prep_kernel<__nv_bfloat16><<<(unsigned)blocks, daux::THREADS, 0, st>>>(a, dsum, nullptr, n_part, ROWS, 0);
+    daux::prep_kernel<__nv_bfloat16><<<(unsigned)blocks, daux::THREADS, 0, st>>>(a, dsum, nullptr, n_part, ROWS);
   else
     daux::prep_kernel<float><<<(unsigned)blocks, daux::THREADS, 0, st>>>(
-        a, dsum, reinterpret_cast<float*>(a.ws + w.dlam_part), n_part, ROWS, 1);
+        a, dsum, reinterpret_cast<float*>(a.ws + w.dlam_part), n_part, ROWS);
   return daux::done("diff prep launch", err);
-}
-
-int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err) {
-  const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
-  daux::reduce_dq_kernel<<<grid, daux::THREADS, 0, (cudaStream_t)stream>>>(
-      a, reinterpret_cast<const float*>(a.ws + w.dq_part),
-      reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + a.tl.slot_off));
-  return daux::done("diff dq reduction launch", err);
 }
 
 int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,

@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <string>
 
+#include "abi_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -1123,15 +1124,21 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
       !make_map(enc, &sbm, KV ? a.dO : a.V, L, KV ? qp : kp, D, BS, err))
     return (int)cudaErrorInvalidValue;
   auto kern = diff_bwd_kernel<D, KV>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::TOTAL);
-  // setmaxnreg hands registers between warpgroups within the launch's pool: the split must fit
-  // the registers the kernel is launched with, or a raising warpgroup would wait forever
-  cudaFuncAttributes fa;
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
-  if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * EW_REGS + 128 * MMA_REGS + 128 * EPI_REGS) {
-    *err = "differential backward built with " + std::to_string(fa.numRegs) +
-           " registers per thread, fewer than its warpgroups' register split needs";
-    return (int)cudaErrorInvalidConfiguration;
+  static OncePerDevice once;
+  const int dev = OncePerDevice::device();
+  cudaError_t e = cudaSuccess;
+  if (once.pending(dev)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::TOTAL);
+    // setmaxnreg hands registers between warpgroups within the launch's pool: the split must fit
+    // the registers the kernel is launched with, or a raising warpgroup would wait forever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * EW_REGS + 128 * MMA_REGS + 128 * EPI_REGS) {
+      *err = "differential backward built with " + std::to_string(fa.numRegs) +
+             " registers per thread, fewer than its warpgroups' register split needs";
+      return (int)cudaErrorInvalidConfiguration;
+    }
+    if (e == cudaSuccess) once.mark(dev);
   }
   // with a CTA for every unit the counter is not read
   if (e == cudaSuccess && units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);

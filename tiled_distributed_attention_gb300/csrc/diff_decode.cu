@@ -613,7 +613,13 @@ template <typename Engine, int D>
 static int launch(const Params& p, int grid, cudaStream_t st, std::string* err) {
   auto kern = decode_kernel<Engine, D>;
   const size_t smem = Big<Engine, D>::BYTES + 4 * (2 * WARPS * ROWS + 2 * ROWS + 16) + 8 * ((size_t)p.B + 1);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static OncePerDevice once;
+  const int dev = OncePerDevice::device();
+  cudaError_t e = cudaSuccess;
+  if (once.pending(dev)) {  // the most that any batch takes
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(smem + 8 * (size_t)(MAX_B - p.B)));
+    if (e == cudaSuccess) once.mark(dev);
+  }
   if (e == cudaSuccess) {
     kern<<<grid, THREADS, smem, st>>>(p);
     e = cudaGetLastError();
@@ -683,9 +689,8 @@ extern "C" int mesh_attn_diff_decode(mesh_attn_dtype dtype, int32_t B, int32_t H
     for (int i = 0; i < 3; ++i)
       if (k_strides[i] * (int64_t)es % 16 != 0 || v_strides[i] * (int64_t)es % 16 != 0)
         return set_last_error(MESH_ATTN_ERR_MISALIGNED, "cache strides must be multiples of 16 bytes");
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t e = mesh::current_sms(&sms);
     if (e != cudaSuccess) return set_last_error(MESH_ATTN_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
     const Sizes s = sizes_of(B, Hq, Hkv, (int32_t)T, std::min(sms, mesh::MAX_SMS));
     if (workspace_bytes < s.total)

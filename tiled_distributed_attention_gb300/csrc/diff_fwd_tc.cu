@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <string>
 
+#include "abi_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -706,7 +707,13 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
       !make_map(enc, &mv, a.V, (uint64_t)prm.L, (uint64_t)a.B * a.Hkv * prm.P, D, err))
     return (int)cudaErrorInvalidValue;
   auto kern = diff_fwd_tc_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+  static OncePerDevice once;
+  const int dev = OncePerDevice::device();
+  cudaError_t e = cudaSuccess;
+  if (once.pending(dev)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+    if (e == cudaSuccess) once.mark(dev);
+  }
   // with a CTA for every unit the counter is not read
   if (e == cudaSuccess && units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
   if (e != cudaSuccess) {
@@ -727,7 +734,7 @@ int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void*
   cudaStream_t st = (cudaStream_t)stream;
   const int ce = a.d == 128 ? dtc::launch<128>(a, w, sms, direct, st, err) : dtc::launch<64>(a, w, sms, direct, st, err);
   if (ce != (int)cudaSuccess || direct) return ce;
-  return launch_diff_merge(a, w, MESH_ATTN_BF16, stream, err);
+  return launch_diff_merge(a, w, MESH_ATTN_BF16, false, stream, err);
 }
 
 }  // namespace mesh

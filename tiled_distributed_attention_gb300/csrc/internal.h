@@ -77,6 +77,7 @@ struct TileArgs {
   float scale_log2;
   int64_t wait_limit_ns;
   void* pieces;  // fp32 inputs: device buffer for the bf16 pieces of Q, K and V (f32_pieces_layout)
+  bool pieces_ready;  // they are there already; Q, K and V are not read
 };
 // Kernel launchers return a cudaError_t value as int; *err gets a message on failure.
 int launch_tile_fwd_tc(const TileArgs& a, void* stream, std::string* err);
@@ -203,8 +204,7 @@ struct DiffArgs {
 struct DiffWorkspace {
   size_t counters;            // 512 bytes
   size_t part_o, part_lse;    // forward partials
-  size_t qx, pieces;          // fp32: q of each map with the other half zeroed; the forward's bf16 pieces
-  size_t gx;                  // fp32 backward: the gradient that reaches each map's output
+  size_t pieces;              // fp32 forward: the bf16 pieces of Q (one map a head), K and V
   size_t dsum;                // [B, 2 Hq, S] row terms of dS
   size_t dlam_part;           // [B, Hq, n], n as the path has it
   size_t dq_part, dk_part, dv_part;
@@ -221,11 +221,15 @@ int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void*
 // partial sums per slot.
 int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct, void* stream,
                        std::string* err);
-// fp32: q (and the gradient) one map a head.
-int launch_diff_expand(const DiffArgs& a, const DiffWorkspace& w, bool grad, void* stream, std::string* err);
-int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
+// fp32 forward: Q (one map a head), K and V as bf16 pieces.
+int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err);
+// fp32 backward: dQ, dK and dV, with their sums over splits and query heads.
+int launch_diff_bwd_simt(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
+int diff_simt_splits(int64_t S, int32_t B, int32_t Hq, int sms);
+// `flat`: the partials are of the whole sequence as one partition with one slot.
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool flat, void* stream,
+                      std::string* err);
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
-int launch_diff_reduce_dq(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err);
 // dlam from n_part partial sums of every (batch, head).
 int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,
                      std::string* err);

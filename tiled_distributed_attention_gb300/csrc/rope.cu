@@ -265,9 +265,8 @@ extern "C" int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32
     prm.dh = dh;
     prm.n = n_pairs;
     prm.inverse = inverse;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t e = mesh::current_sms(&sms);
     if (e != cudaSuccess) return set_last_error(MESH_ATTN_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
     std::string err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

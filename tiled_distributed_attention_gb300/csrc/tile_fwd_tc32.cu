@@ -641,9 +641,10 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
   const F32Pieces pc = f32_pieces_layout(a.B, a.Hq, a.Hkv, a.S, a.d);
   char* base = static_cast<char*>(a.pieces);
-  int ce = split(static_cast<const float*>(a.Q), base + pc.q_off, q_rows * D, a.status, st, err);
-  if (ce == (int)cudaSuccess) ce = split(static_cast<const float*>(a.K), base + pc.k_off, kv_rows * D, a.status, st, err);
-  if (ce == (int)cudaSuccess) ce = split(static_cast<const float*>(a.V), base + pc.v_off, kv_rows * D, a.status, st, err);
+  int ce = (int)cudaSuccess;
+  if (!a.pieces_ready) ce = split(static_cast<const float*>(a.Q), base + pc.q_off, q_rows * D, a.status, st, err);
+  if (ce == (int)cudaSuccess && !a.pieces_ready) ce = split(static_cast<const float*>(a.K), base + pc.k_off, kv_rows * D, a.status, st, err);
+  if (ce == (int)cudaSuccess && !a.pieces_ready) ce = split(static_cast<const float*>(a.V), base + pc.v_off, kv_rows * D, a.status, st, err);
   if (ce != (int)cudaSuccess) {
     if (err->empty()) *err = std::string("split launch: ") + cudaGetErrorString((cudaError_t)ce);
     return ce;
