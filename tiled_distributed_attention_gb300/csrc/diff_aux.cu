@@ -146,45 +146,67 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
   }
 }
 
-// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2.  One warp a row.
+// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2.  A CTA takes PREP_ROWS rows of a head,
+// a group of lanes a row, 16 bytes of each of the three tensors a lane, all passes' loads in flight together.
+constexpr int PREP_ROWS = 64;
 template <typename T>
-__global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* dsum, float* dlam_part, int64_t n_part,
-                                                       int rows_per_part) {
-  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t part = blockIdx.x % n_part;
-  const int64_t bh = blockIdx.x / n_part;
-  const float lam = lam_of<T>(a.lam, a.lam_n, (int)(bh % a.Hq));
-  __shared__ double sums[THREADS / 32];
-  double acc = 0.0;
-  const int64_t s_end = min(a.S, (part + 1) * rows_per_part);
-  for (int64_t s = part * rows_per_part + warp; s < s_end; s += THREADS / 32) {
-    const int64_t row = (bh * a.S + s) * a.d;
-    float d1 = 0.f, d2 = 0.f;
-    for (int c = lane * 4; c < a.d; c += 128) {
-      const float4 g = load4(static_cast<const T*>(a.dO) + row + c);
-      const float4 o = load4(static_cast<const T*>(a.O) + row + c);
-      const float4 o2 = load4(static_cast<const T*>(a.O2) + row + c);
-      d1 += g.x * o.x + g.y * o.y + g.z * o.z + g.w * o.w;
-      d2 += g.x * o2.x + g.y * o2.y + g.z * o2.z + g.w * o2.w;
-    }
+__device__ __forceinline__ void dot16(uint4 x, uint4 y, float& acc) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) {
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      acc = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), acc);
+      acc = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u), acc);
+    } else {
+      acc = fmaf(__uint_as_float(a[i]), __uint_as_float(b[i]), acc);
+    }
+  }
+}
+template <typename T, int D>
+__global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* dsum, float* dlam_part, int64_t n_part) {
+  constexpr int LANES = D * (int)sizeof(T) / 16, AT_ONCE = THREADS / LANES, PASSES = PREP_ROWS / AT_ONCE;
+  if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
+  const int64_t part = blockIdx.x % n_part, bh = blockIdx.x / n_part;
+  const float lam = lam_of<T>(a.lam, a.lam_n, (int)(bh % a.Hq));
+  const int lr = threadIdx.x / LANES, piece = threadIdx.x % LANES;
+  const int64_t s0 = part * PREP_ROWS + lr;
+  uint4 g[PASSES], o[PASSES], o2[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t s = s0 + i * AT_ONCE;
+    g[i] = o[i] = o2[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (s < a.S) {
+      const int64_t at = (bh * a.S + s) * LANES + piece;
+      g[i] = __ldg(static_cast<const uint4*>(a.dO) + at);
+      o[i] = __ldg(static_cast<const uint4*>(a.O) + at);
+      o2[i] = __ldg(static_cast<const uint4*>(a.O2) + at);
+    }
+  }
+  double acc = 0.0;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int64_t s = s0 + i * AT_ONCE;
+    float d1 = 0.f, d2 = 0.f;
+    dot16<T>(g[i], o[i], d1);
+    dot16<T>(g[i], o2[i], d2);
+#pragma unroll
+    for (int x = LANES / 2; x >= 1; x >>= 1) {
       d1 += __shfl_xor_sync(0xffffffffu, d1, x);
       d2 += __shfl_xor_sync(0xffffffffu, d2, x);
     }
-    if (lane == 0) {
+    if (piece == 0 && s < a.S) {
       dsum[2 * bh * a.S + s] = fmaf(lam, d2, d1);
       dsum[(2 * bh + 1) * a.S + s] = d2;
       acc -= (double)d2;
     }
   }
   if (dlam_part) {  // dlam = -sum D2, in a fixed order
-    if (lane == 0) sums[warp] = acc;
+    __shared__ double sums[AT_ONCE];
+    if (piece == 0) sums[lr] = acc;
     __syncthreads();
     if (threadIdx.x == 0) {
       double t = 0.0;
-      for (int w = 0; w < THREADS / 32; ++w) t += sums[w];
+      for (int r = 0; r < AT_ONCE; ++r) t += sums[r];
       dlam_part[bh * n_part + part] = (float)t;
     }
   }
@@ -262,18 +284,16 @@ int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype
 
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
-  constexpr int ROWS = 64;
-  const int64_t n_part = (a.S + ROWS - 1) / ROWS, blocks = n_part * a.B * a.Hq;
+  const int64_t n_part = (a.S + daux::PREP_ROWS - 1) / daux::PREP_ROWS, blocks = n_part * a.B * a.Hq;
   if (blocks > 0x7fffffff) {
     *err = "too many rows for one launch";
     return (int)cudaErrorInvalidConfiguration;
   }
   float* dsum = reinterpret_cast<float*>(a.ws + w.dsum);
-  if (dt == MESH_ATTN_BF16)
-    daux::prep_kernel<__nv_bfloat16><<<(unsigned)blocks, daux::THREADS, 0, st>>>(a, dsum, nullptr, n_part, ROWS);
-  else
-    daux::prep_kernel<float><<<(unsigned)blocks, daux::THREADS, 0, st>>>(
-        a, dsum, reinterpret_cast<float*>(a.ws + w.dlam_part), n_part, ROWS);
+  float* dl = dt == MESH_ATTN_F32 ? reinterpret_cast<float*>(a.ws + w.dlam_part) : nullptr;
+  auto go = [&](auto kern) { kern<<<(unsigned)blocks, daux::THREADS, 0, st>>>(a, dsum, dl, n_part); };
+  if (dt == MESH_ATTN_BF16) go(a.d == 128 ? daux::prep_kernel<__nv_bfloat16, 128> : daux::prep_kernel<__nv_bfloat16, 64>);
+  else go(a.d == 128 ? daux::prep_kernel<float, 128> : daux::prep_kernel<float, 64>);
   return daux::done("diff prep launch", err);
 }
 

@@ -222,15 +222,23 @@ struct EngineBf16 {
             acc[i][3] *= f[1];
           }
         }
-        // P rounded to bf16 for its product (at most 2^-9 relative a term, the sums stay fp32)
-        const uint32_t a0 = pack_bf16x2(sc[0][0], sc[0][1]), a1 = pack_bf16x2(sc[0][2], sc[0][3]);
-        const uint32_t a2 = pack_bf16x2(sc[1][0], sc[1][1]), a3 = pack_bf16x2(sc[1][2], sc[1][3]);
+        // P as two bf16 pieces (the second takes what the first rounds off, 2^-17 relative together): the
+        // tensor cores have time to spare here, and the output keeps fp32's digits until its own rounding
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x0 = sc[i >> 1][2 * (i & 1)], x1 = sc[i >> 1][2 * (i & 1) + 1];
+          ph[i] = pack_bf16x2(x0, x1);
+          pl[i] = pack_bf16x2(x0 - __uint_as_float(ph[i] << 16), x1 - __uint_as_float(ph[i] & 0xffff0000u));
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t r[4];
           ldsm4t(va + (uint32_t)(vrow * D * 2) + (uint32_t)(((2 * i + vch) ^ (vrow & 7)) << 4), r);
-          mma16816(acc[2 * i], a0, a1, a2, a3, r[0], r[1]);
-          mma16816(acc[2 * i + 1], a0, a1, a2, a3, r[2], r[3]);
+          mma16816(acc[2 * i], ph[0], ph[1], ph[2], ph[3], r[0], r[1]);
+          mma16816(acc[2 * i + 1], ph[0], ph[1], ph[2], ph[3], r[2], r[3]);
+          mma16816(acc[2 * i], pl[0], pl[1], pl[2], pl[3], r[0], r[1]);
+          mma16816(acc[2 * i + 1], pl[0], pl[1], pl[2], pl[3], r[2], r[3]);
         }
       }
       __syncwarp();  // every lane is done with the stage before the next load overwrites it

@@ -59,9 +59,43 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void from_f(float& y, float x) { y = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
+// V elements as fp32 and back (one rounding to the type); bf16 pairs go by 32-bit words.
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Vec<T, V>& x, float (&f)[V]) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f(x.v[i]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void narrow(const float (&f)[V], Vec<T, V>& x) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(x.v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) from_f(x.v[i], f[i]);
+  }
+}
+
 // V: elements of one access (16 bytes' worth, or 1 where sizes or addresses do not allow it).
-// ADJ: adjacent pairs.  A rotation item is V pairs (two accesses: the pairs' members, or for
-// adjacent pairs 2 V consecutive elements); a copy item is V elements behind the rotated ones.
+// ADJ: adjacent pairs.  A rotation item is V pairs by two accesses, one for each member, or for
+// adjacent pairs one access of V / 2 pairs (two of one element at V = 1), so that neighbouring threads
+// always touch neighbouring bytes; a copy item is V elements behind the rotated ones.
+template <int V, bool ADJ>
+struct Item {
+  static constexpr int PAIRS = ADJ ? (V > 1 ? V / 2 : 1) : V;
+  static constexpr bool TWO = !ADJ || V == 1;  // accesses
+};
+
 template <typename T, int V, bool ADJ>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ Params prm) {
   const int64_t lin = (int64_t)blockIdx.x * THREADS + threadIdx.x;
@@ -69,7 +103,9 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
   const int64_t tok = lin / prm.items;
   if (tok >= prm.tokens) return;
   const int64_t b = tok / prm.S, s = tok - b * prm.S;
-  const int rot = prm.n / V;                       // rotation items of a group
+  constexpr int NP = Item<V, ADJ>::PAIRS;
+  constexpr bool TWO = Item<V, ADJ>::TWO;
+  const int rot = prm.n / NP;                      // rotation items of a group
   const int per = rot + (prm.dh - 2 * prm.n) / V;  // items of a group
   const int grp = item / per, r = item - grp * per;
   const bool copy = r >= rot;
@@ -79,19 +115,19 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
     c0 += 2 * prm.n + (r - rot) * V;
     c1 = c0;
   } else if (ADJ) {
-    c0 += 2 * r * V;
-    c1 = c0 + V;
+    c0 += 2 * r * NP;
+    c1 = c0 + 1;
   } else {
     c0 += r * V;
     c1 = c0 + prm.n;
   }
-  float cs[V], sn[V];
+  float cs[NP], sn[NP];
   if (!copy) {
     int have = -1;
     uint64_t p = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int pr = r * V + i;
+    for (int i = 0; i < NP; ++i) {
+      const int pr = r * NP + i;
       const int ax = prm.axis[pr];
       if (ax != have) {
         have = ax;
@@ -105,61 +141,59 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
     }
   }
   using Vc = Vec<T, V>;
-  const int H = prm.H[0] + prm.H[1];
-  const int h_end = min(H, (int)(blockIdx.y + 1) * prm.heads_per_block);
-  auto src = [&](int h) {
-    const int w = h < prm.H[0] ? 0 : 1;
-    const int hh = w ? h - prm.H[0] : h;
-    return static_cast<const T*>(prm.x[w]) + b * prm.xs[w][0] + hh * prm.xs[w][1] + s * prm.xs[w][2];
-  };
-  auto dst = [&](int h) {
-    const int w = h < prm.H[0] ? 0 : 1;
-    const int hh = w ? h - prm.H[0] : h;
-    return static_cast<T*>(prm.y[w]) + b * prm.ys[w][0] + hh * prm.ys[w][1] + s * prm.ys[w][2];
-  };
   constexpr int U = 4;  // heads whose loads are in flight together
-  for (int h0 = (int)blockIdx.y * prm.heads_per_block; h0 < h_end; h0 += U) {
-    Vc a[U], c[U];
+  // this block's heads of q, then those of k; pointers step from head to head
+  const int h_begin = (int)blockIdx.y * prm.heads_per_block, h_stop = h_begin + prm.heads_per_block;
+#pragma unroll 1
+  for (int w = 0; w < 2; ++w) {
+    const int before = w ? prm.H[0] : 0;
+    int h = max(h_begin - before, 0);
+    const int h_end = min(h_stop - before, prm.H[w]);
+    if (h >= h_end) continue;
+    const T* src = static_cast<const T*>(prm.x[w]) + b * prm.xs[w][0] + h * prm.xs[w][1] + s * prm.xs[w][2];
+    T* dst = static_cast<T*>(prm.y[w]) + b * prm.ys[w][0] + h * prm.ys[w][1] + s * prm.ys[w][2];
+    const int64_t xh = prm.xs[w][1], yh = prm.ys[w][1];
+    for (; h < h_end; h += U) {
+      Vc a[U], c[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (h0 + u < h_end) {
-        const T* q = src(h0 + u);
-        a[u] = *reinterpret_cast<const Vc*>(q + c0);
-        if (!copy) c[u] = *reinterpret_cast<const Vc*>(q + c1);
+      for (int u = 0; u < U; ++u) {
+        if (h + u < h_end) {
+          a[u] = *reinterpret_cast<const Vc*>(src + c0);
+          if (TWO && !copy) c[u] = *reinterpret_cast<const Vc*>(src + c1);
+        }
+        src += xh;
       }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (h0 + u < h_end) {
-        T* o = dst(h0 + u);
-        if (copy) {
-          *reinterpret_cast<Vc*>(o + c0) = a[u];
-          continue;
-        }
-        Vc ya, yc;
+      for (int u = 0; u < U; ++u) {
+        if (h + u < h_end) {
+          if (!copy) {
+            float xa[V], xc[V];
+            widen(a[u], xa);
+            if (TWO) widen(c[u], xc);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          // one rounding, of the fp32 result to the type
-          if (ADJ) {  // pair i sits at elements 2 i, 2 i + 1 of the 2 V
-            const int e0 = 2 * i, e1 = 2 * i + 1;
-            const float x0 = to_f(e0 < V ? a[u].v[e0 % V] : c[u].v[e0 % V]);
-            const float x1 = to_f(e1 < V ? a[u].v[e1 % V] : c[u].v[e1 % V]);
-            from_f(e0 < V ? ya.v[e0 % V] : yc.v[e0 % V], fmaf(x0, cs[i], -x1 * sn[i]));
-            from_f(e1 < V ? ya.v[e1 % V] : yc.v[e1 % V], fmaf(x1, cs[i], x0 * sn[i]));
-          } else {
-            const float x0 = to_f(a[u].v[i]), x1 = to_f(c[u].v[i]);
-            from_f(ya.v[i], fmaf(x0, cs[i], -x1 * sn[i]));
-            from_f(yc.v[i], fmaf(x1, cs[i], x0 * sn[i]));
+            for (int i = 0; i < NP; ++i) {
+              const int i0 = TWO ? i : (2 * i) % V, i1 = TWO ? i : (2 * i + 1) % V;
+              const float x0 = xa[i0], x1 = TWO ? xc[i1] : xa[i1];
+              xa[i0] = fmaf(x0, cs[i], -x1 * sn[i]);
+              (TWO ? xc[i1] : xa[i1]) = fmaf(x1, cs[i], x0 * sn[i]);
+            }
+            narrow(xa, a[u]);
+            if (TWO) {
+              narrow(xc, c[u]);
+              *reinterpret_cast<Vc*>(dst + c1) = c[u];
+            }
           }
+          *reinterpret_cast<Vc*>(dst + c0) = a[u];
         }
-        *reinterpret_cast<Vc*>(o + c0) = ya;
-        *reinterpret_cast<Vc*>(o + c1) = yc;
+        dst += yh;
       }
+    }
   }
 }
 
 template <typename T, int V>
 static int launch(Params& prm, bool adjacent, int sms, cudaStream_t st, std::string* err) {
-  prm.items = prm.groups * (prm.n / V + (prm.dh - 2 * prm.n) / V);
+  prm.items = prm.groups * (prm.n / (adjacent ? Item<V, true>::PAIRS : V) + (prm.dh - 2 * prm.n) / V);
   const int64_t blocks = (prm.tokens * prm.items + THREADS - 1) / THREADS;
   if (blocks > 0x7fffffffLL) {
     *err = "too many tokens for one launch";
@@ -232,7 +266,7 @@ extern "C" int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32
     const size_t es = dtype == MESH_ATTN_BF16 ? 2 : 4;
     const int vec = (int)(16 / es);
     // 16-byte accesses where every address they touch allows them
-    bool wide = n_pairs % vec == 0 && (dh - 2 * n_pairs) % vec == 0;
+    bool wide = (adjacent ? 2 * n_pairs : n_pairs) % vec == 0 && (dh - 2 * n_pairs) % vec == 0;
     for (int w = 0; w < 2; ++w) {
       const Arg& a = args[w];
       prm.H[w] = a.H;
