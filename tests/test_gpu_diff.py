@@ -140,6 +140,28 @@ def test_large_scores(lib):
     within(L, Lr, torch.full_like(Lr, 1e-3), "LSE")
 
 
+@pytest.mark.parametrize("P", [1, 4])
+def test_references_that_have_to_rise(lib, P):
+    """Scores that outgrow a row's first block by far more than 2^60, in one map, in the other, in one half of a block's
+    keys or in both, several times in one sequence: the running reference rises block by block."""
+    S, d = 1024, 128
+    q, k, v, lam, g = inputs(1, 2, 1, S, d, "bf16", 35)
+    q[..., 0] = 8.0   # a column of each map whose product with k lifts a key's score for every row
+    q[..., 64] = 8.0
+    k[..., 0] = k[..., 64] = 0.0
+    scale = 1 / 8.0
+    for key, a, b in ((200, 60.0, 0.0), (201, 0.0, 80.0), (330, 120.0, 0.0), (400, 130.0, 140.0), (450, 190.0, 145.0),
+                      (700, 250.0, 220.0), (701, 252.0, 222.0), (1000, 310.0, 0.0)):
+        k[:, :, key, 0], k[:, :, key, 64] = a, b
+    args = [t.cuda() for t in (q, k, v, lam)]
+    for causal in (False, True):
+        O, O2, L = lib.mesh_diff_attention(*args, P, causal, scale=scale, return_saved=True)
+        Or, Lr, _, mag = OD.forward(q, k, v, lam, causal, scale=scale)
+        # scores up to 300 in fp32: 2^-15 and d 2^-24 of 300 off, a relative 2^-12 of a weight
+        within(O, Or, 2.0 ** -8 * Or.abs() + (2.0 ** -8 + 2.0 ** -11) * mag + 1e-6, "O")
+        within(L, Lr, torch.full_like(Lr, 1e-3), "LSE")
+
+
 def test_equals_two_plain_attentions(lib):
     """O1 and O2 as the framework's plain calls give them, on q and k with the other half zeroed."""
     q, k, v, lam, _ = (t.cuda() for t in inputs(1, 2, 1, 256, 128, "bf16", 24))
@@ -153,8 +175,12 @@ def test_equals_two_plain_attentions(lib):
     assert torch.allclose(L[:, :, 0], halves[0][1], atol=2e-6, rtol=0) and torch.allclose(L[:, :, 1], halves[1][1], atol=2e-6, rtol=0)
     o1, o2 = (h[0].double() for h in halves)
     ref = o1 - lam.double().view(1, 2, 1, 1) * o2
-    # o1 and o2 are rounded, P is in both: 3 roundings of 2^-8 each relative to the magnitudes, which are below 4
-    assert ((O.double() - ref).abs() <= 3 * 2.0 ** -8 * (o1.abs() + o2.abs() + 0.1)).all()
+    # On either side P is rounded for its product, u relative to sum P |v| of each map (mag carries both, the second times
+    # lam), and exponentials and accumulation add 2^-12; o1, o2 and O are rounded once each.
+    mag = OD.forward(*(t.cpu() for t in (q, k, v, lam)), True)[3].cuda()
+    lo2 = (lam.double().view(1, 2, 1, 1) * o2).abs()
+    bound = 2 * (2.0 ** -8 + 2.0 ** -12) * mag + 2.0 ** -8 * (o1.abs() + lo2 + O.double().abs()) + 1e-6
+    assert ((O.double() - ref).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -55,8 +55,8 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
   const bool f32 = dt == MESH_ATTN_F32;
   // bf16 needs partial sums only where the plan's slots split an axis (rows_direct)
   const int64_t tiles = (plan.S + 127) / 128 * B;
-  const bool q_slots = plan.n_slots() != plan.P && tiles * Hq < MAX_SMS;
-  const bool kv_slots = plan.n_kv_slots() != plan.P && tiles * Hkv < MAX_SMS;
+  const bool q_slots = plan.n_slots() != plan.P && plan.L >= 128 && 4 * tiles * Hq < MAX_SMS;
+  const bool kv_slots = plan.n_kv_slots() != plan.P && plan.L >= 128 && 4 * tiles * Hkv < MAX_SMS;
   if (!backward) {
     if (f32 || q_slots) {  // fp32: both maps' outputs always go through the merge
       const size_t rows = 2 * (q_slots ? std::max(prows, qrows) : qrows);
@@ -90,7 +90,7 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
 }
 
 bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms) {
-  return single || (a.S + 127) / 128 * a.B * H >= sms;
+  return single || a.L < 128 || 4 * ((a.S + 127) / 128) * a.B * H >= sms;
 }
 
 }  // namespace mesh

@@ -19,7 +19,7 @@
 //
 // dkdv (unit = KV slot, batch, KV head, 128-key block): K and V stay in shared memory, Q and dO blocks
 // of 64 query rows stream.  TMEM: S_1^T | S_2^T | dP^T | A^T (two buffers) | dV | dK_1 | dK_2.
-//   Issue order per block i: [S(i) read] S(i+1)   [A(i) ready] dV(i)   [dS(i) ready] dK(i), dP(i+1).
+//   Issue order per block i: [S(i) read] S(i+1)   [dS(i) and A(i) ready] dK(i), dP(i+1), dV(i).
 //   dS_1 and dS_2 (bf16) replace dP in its own columns.
 // dq (unit = work item, batch, head, 128-row block): Q and dO are copied into TMEM once per unit and
 // feed the products as A operands; K and V blocks of 64 keys stream.  TMEM: S_1 | S_2 | dP (two
@@ -91,6 +91,7 @@ struct Params {
   uint32_t* counter;
   int64_t S, L;
   int32_t B, Hq, Hkv, P, n_items, n_slots, nb, ns, causal, n_units, lam_n;  // nb 128-row blocks, ns 64-row blocks
+  int32_t batch;  // lanes whose units are numbered together (unit_of)
   float scale, scale_log2;
   int64_t wait_limit_ns;
 };
@@ -105,12 +106,12 @@ struct Layout {
   static constexpr uint32_t RES0 = 0, RES1 = TILE;
   static constexpr uint32_t A0 = 2 * TILE;              // Q (dkdv) or K (dq) stages
   static constexpr uint32_t B0 = A0 + NSA * SBLK;       // dO (dkdv) or V (dq) stages
-  static constexpr uint32_t VEC_OFF = B0 + NSB * SBLK;  // dkdv: -LSE_1, -LSE_2 (base 2), -D_1, -D_2: [2][4][64] fp32
-  static constexpr uint32_t BAR_OFF = VEC_OFF + 2 * 4 * BS * 4;
+  static constexpr uint32_t VEC_OFF = B0 + NSB * SBLK;  // dkdv: -LSE_1, -LSE_2 (base 2), -D_1, lam D_2: [3][4][64] fp32
+  static constexpr uint32_t BAR_OFF = VEC_OFF + 3 * 4 * BS * 4;
   static constexpr int B_RES = 0, B_AF = 1, B_AE = B_AF + NSA, B_BF = B_AE + NSA, B_BE = B_BF + NSB,
-                       B_S = B_BE + NSB, B_SREAD = B_S + 1, B_DP = B_SREAD + 1, B_A = B_DP + 2, B_DS = B_A + 1,
+                       B_S = B_BE + NSB, B_SREAD = B_S + 1, B_DP = B_SREAD + 1, B_DS = B_DP + 2,
                        B_ACC = B_DS + 1, B_ACCE = B_ACC + 1, B_DRAIN = B_ACCE + 1, B_VEC = B_DRAIN + 1,
-                       B_RESE = B_VEC + 2, B_UF = B_RESE + 1, B_UE = B_UF + 2, B_QTF = B_UE + 2, B_QTE = B_QTF + 1,
+                       B_RESE = B_VEC + 3, B_UF = B_RESE + 1, B_UE = B_UF + 2, B_QTF = B_UE + 2, B_QTE = B_QTF + 1,
                        NBARS = B_QTE + 1;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBARS * 8 + (NBARS % 2) * 8;  // tmem base, abort flag
   static constexpr uint32_t RING_OFF = MISC_OFF + 16;  // unit ring: 2 decoded units, 16 ints each
@@ -177,14 +178,6 @@ __device__ __forceinline__ void store_bf16(const float* v, float mul, __nv_bfloa
     *reinterpret_cast<uint4*>(dst + 8 * q) =
         make_uint4(pack_bf16x2(v[8 * q] * mul, v[8 * q + 1] * mul), pack_bf16x2(v[8 * q + 2] * mul, v[8 * q + 3] * mul),
                    pack_bf16x2(v[8 * q + 4] * mul, v[8 * q + 5] * mul), pack_bf16x2(v[8 * q + 6] * mul, v[8 * q + 7] * mul));
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 
 __device__ __forceinline__ float lam_of(const Params& prm, int h) {
@@ -254,9 +247,13 @@ template <bool KV>
 __device__ __forceinline__ Unit unit_of(int u, const Params& prm) {
   Unit x;
   const int H = KV ? prm.Hkv : prm.Hq;
-  x.blk = u % prm.nb;
-  if (!KV && prm.causal) x.blk = prm.nb - 1 - x.blk;  // the longest first: the grid's last units are short
-  u /= prm.nb;
+  // numbered batch of (head, sequence, item) lanes by batch, within it block by block from the longest
+  const int per = prm.batch * prm.nb, first = u / per * prm.batch;
+  const int lanes = min(prm.batch, prm.n_units / prm.nb - first);  // the last batch may be smaller
+  u %= per;
+  x.blk = u / lanes;
+  if (!KV && prm.causal) x.blk = prm.nb - 1 - x.blk;
+  u = first + u % lanes;
   x.h = u % H;
   u /= H;
   x.b = u % prm.B;
@@ -324,13 +321,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(bar(Ly::B_SREAD), N_EW);  // one lane of each elementwise warp
     mbar_init(bar(Ly::B_DP), 1);
     mbar_init(bar(Ly::B_DP + 1), 1);
-    mbar_init(bar(Ly::B_A), N_EW);
     mbar_init(bar(Ly::B_DS), N_EW);
     mbar_init(bar(Ly::B_ACC), 1);
     mbar_init(bar(Ly::B_ACCE), KV ? N_EW : N_EPI);
     mbar_init(bar(Ly::B_DRAIN), 1);
     mbar_init(bar(Ly::B_VEC), N_EW * 32);  // every elementwise thread has written its LSE or D value
     mbar_init(bar(Ly::B_VEC + 1), N_EW * 32);
+    mbar_init(bar(Ly::B_VEC + 2), N_EW * 32);
     mbar_init(bar(Ly::B_QTF), N_EPI);
     mbar_init(bar(Ly::B_QTE), 1);
     for (int s = 0; s < 2; ++s) {
@@ -404,13 +401,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int k_unit = 0;
     if constexpr (KV) {
       // ---------------------------------------------------------------- dK and dV
-      // Vector `vec` (LSE_1, LSE_2, D_1, D_2) of query column `vq`, loaded raw one block ahead and only
-      // used (scaled, published) at the top of the next iteration, so that the load never stalls the
-      // block in flight.
+      // Vector `vec` (LSE_1, LSE_2, D_1, D_2) of query column `vq`: loaded raw two blocks ahead, scaled and
+      // published one block ahead, so that neither the load nor the other threads' writes are waited
+      // for.  Three buffers: a warp that publishes block i + 1 has seen dP(i - 1), which was issued
+      // after every warp's dS(i - 2), so nobody reads the buffer of block i - 2 any more.
       float* vec_s = reinterpret_cast<float*>(smem + Ly::VEC_OFF);
       const int tid = threadIdx.x, vec = tid >> 6, vq = tid & 63;
-      float raw = 0.f, nl_next = 0.f;
+      float raw = 0.f;
       bool raw_in = false;
+      float raw_lam = 0.f;  // lam of the head whose value `raw` is
+      int lam_h = -1;
       auto fetch = [&](const Unit& y, const QCursor& c) {
         const int64_t ql = (int64_t)c.qb * BS + vq;
         raw_in = c.p >= 0 && c.p < prm.P && ql < L;
@@ -418,12 +418,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int64_t at = (((int64_t)y.b * prm.Hq + c.h) * 2 + (vec & 1)) * prm.S + (int64_t)c.p * L + ql;
           raw = __ldg((vec < 2 ? prm.lse : prm.dsum) + at);
         }
-        nl_next = -lam_of(prm, c.h);
+        if (c.h != lam_h) {
+          lam_h = c.h;
+          raw_lam = lam_of(prm, c.h);
+        }
       };
-      QCursor cur, nxt;  // blocks i and i + 1
-      if (ok && v >= 0 && x.ok) {
+      // block n of the launch; no such query row (or one without a visible key): exp2(s - inf) = 0, so it
+      // needs no mask
+      auto publish = [&](int64_t n) {
+        const int vb = (int)(n % 3);
+        float val = vec < 2 ? -INFINITY : 0.f;
+        if (raw_in) val = vec == 2 ? -raw : vec == 3 ? raw_lam * raw : raw == -INFINITY ? -INFINITY : -raw * LOG2E;
+        vec_s[(vb * 4 + vec) * BS + vq] = val;
+        mbar_arrive(bar(Ly::B_VEC + vb));
+      };
+      // cursors: block i, and the next one to fetch (i + 2, or the next unit's first)
+      QCursor cur, nxt;
+      float lam_cur = 0.f, lam_pub = 0.f;  // lam of block i and of the block published last
+      if (ok && v >= 0 && x.ok && x.NB >= 1) {
         cur.start(prm, x.it, x.blk, x.h * g);
         fetch(x, cur);
+        lam_pub = raw_lam;
+        publish(0);
+        nxt = cur;
+        if (x.NB > 1) {
+          nxt.step(prm, x.it, x.blk);
+          fetch(x, nxt);
+        }
       }
       while (ok && v >= 0) {
         if (!x.ok || x.NB < 1) {
@@ -432,39 +453,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           break;
         }
         const int k = x.it.p, kb = x.blk, NB = x.NB;
-        nxt = cur;
+        QCursor c1 = nxt;  // block i + 1
         for (int i = 0; i < NB && ok; ++i) {
           const int64_t gi = g0 + i;
-          const int vb = (int)(gi & 1);
-          if (i > 0) cur = nxt;
-          if (i + 1 < NB) nxt.step(prm, x.it, kb);
-          const float nl = nl_next;  // -lam of this block's head
-          // publish this thread's value and wait (bounded) for all: a buffer is rewritten two blocks
-          // later, after every thread has arrived for the block between.  No such query row (or one
-          // without a visible key): exp2(s - inf) = 0, so it needs no mask.
-          {
-            float val = vec < 2 ? -INFINITY : 0.f;
-            if (raw_in) val = vec >= 2 ? -raw : (raw == -INFINITY ? -INFINITY : -raw * LOG2E);
-            vec_s[(vb * 4 + vec) * BS + vq] = val;
-            mbar_arrive(bar(Ly::B_VEC + vb));
-            if (i + 1 < NB) fetch(x, nxt);
+          const int vb = (int)(gi % 3);
+          if (i > 0) {
+            cur = c1;
+            c1 = nxt;
           }
-          ok = wait_all(Ly::B_VEC + vb, (uint32_t)((gi >> 1) & 1), ROLE_EW, i);
+          lam_cur = lam_pub;
+          if (i + 1 < NB) {
+            lam_pub = raw_lam;
+            publish(gi + 1);
+            if (i + 2 < NB) {
+              nxt.step(prm, x.it, kb);
+              fetch(x, nxt);
+            }
+          }
+          const float nl = -lam_cur;
+          ok = wait_all(Ly::B_VEC + vb, (uint32_t)((gi / 3) & 1), ROLE_EW, i);
           if (!ok) break;
           // causal diagonal: query columns before this key row are masked
           const int lo = (prm.causal && cur.p == k) ? kb * BM + row - cur.qb * BS - c_base : 0;
           ok = wait_all(Ly::B_S, (uint32_t)(gi & 1), ROLE_EW, i);
           if (!ok) break;
           tc_fence_after();
-          float p1[32], w2[32];
+          float p1[32], p2[32];
           tmem_ld32(tm_s, p1);
-          tmem_ld32(tm_s + 64u, w2);
+          tmem_ld32(tm_s + 64u, p2);
           tc_wait_ld();
           arrive(Ly::B_SREAD);  // the next block's S may overwrite it
           if (__any_sync(0xffffffffu, lo > 0)) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c < lo) p1[c] = w2[c] = -INFINITY;
+              if (c < lo) p1[c] = p2[c] = -INFINITY;
           }
           const float4* l1 = reinterpret_cast<const float4*>(vec_s + (vb * 4 + 0) * BS + c_base);
           const float4* l2 = reinterpret_cast<const float4*>(vec_s + (vb * 4 + 1) * BS + c_base);
@@ -479,20 +501,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int e = 0; e < 4; e += 2) {
               float x0, x1, y0, y1;
               f2_unpack(f2_fma(f2_pack(p1[c + e], p1[c + e + 1]), sc2, e ? f2_pack(a.z, a.w) : f2_pack(a.x, a.y)), x0, x1);
-              f2_unpack(f2_fma(f2_pack(w2[c + e], w2[c + e + 1]), sc2, e ? f2_pack(b.z, b.w) : f2_pack(b.x, b.y)), y0, y1);
+              f2_unpack(f2_fma(f2_pack(p2[c + e], p2[c + e + 1]), sc2, e ? f2_pack(b.z, b.w) : f2_pack(b.x, b.y)), y0, y1);
               p1[c + e] = fast_exp2(x0);
               p1[c + e + 1] = fast_exp2(x1);
-              // -lam P_2
-              const uint64_t w = f2_mul(f2_pack(fast_exp2(y0), fast_exp2(y1)), nl2);
-              f2_unpack(w, w2[c + e], w2[c + e + 1]);
-              float a0, a1;
-              f2_unpack(f2_add(f2_pack(p1[c + e], p1[c + e + 1]), w), a0, a1);
+              p2[c + e] = fast_exp2(y0);
+              p2[c + e + 1] = fast_exp2(y1);
+              float a0, a1;  // A = P_1 - lam P_2
+              f2_unpack(f2_fma(f2_pack(p2[c + e], p2[c + e + 1]), nl2, f2_pack(p1[c + e], p1[c + e + 1])), a0, a1);
               pk[(c + e) / 2] = pack_bf16x2(a0, a1);
             }
           }
-          tmem_st16(tmem + lane_base + COL_A + (uint32_t)(vb * 32 + hf * 16), pk);
-          tc_wait_st();
-          arrive(Ly::B_A);
+          tmem_st16(tmem + lane_base + COL_A + (uint32_t)((gi & 1) * 32 + hf * 16), pk);  // complete by this block's DS
           ok = wait_all(Ly::B_DP, (uint32_t)(gi & 1), ROLE_EW, i);
           if (!ok) break;
           tc_fence_after();
@@ -509,7 +528,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               float a0, a1;
               f2_unpack(f2_mul(f2_add(d, e ? f2_pack(a.z, a.w) : f2_pack(a.x, a.y)), f2_pack(p1[c + e], p1[c + e + 1])), a0, a1);
               s1[(c + e) / 2] = pack_bf16x2(a0, a1);
-              f2_unpack(f2_mul(f2_add(d, e ? f2_pack(b.z, b.w) : f2_pack(b.x, b.y)), f2_pack(w2[c + e], w2[c + e + 1])), a0, a1);
+              // -lam (dP - D_2) P_2
+              f2_unpack(f2_mul(f2_fma(d, nl2, e ? f2_pack(b.z, b.w) : f2_pack(b.x, b.y)), f2_pack(p2[c + e], p2[c + e + 1])), a0, a1);
               s2[(c + e) / 2] = pack_bf16x2(a0, a1);
             }
           }
@@ -524,7 +544,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         Unit xn;
         ok = take(vn, xn, ROLE_EW);
         if (!ok) break;
-        if (vn >= 0 && xn.ok) {
+        if (vn >= 0 && xn.ok && xn.NB >= 1) {
           cur.start(prm, xn.it, xn.blk, xn.h * g);
           fetch(xn, cur);
         }
@@ -565,6 +585,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         g0 += NB;
         v = vn;
         x = xn;
+        if (v >= 0 && x.ok && x.NB >= 1) {
+          lam_pub = raw_lam;
+          publish(g0);
+          nxt = cur;
+          if (x.NB > 1) {
+            nxt.step(prm, x.it, x.blk);
+            fetch(x, nxt);
+          }
+        }
       }
     } else {
       // ---------------------------------------------------------------- dQ
@@ -599,19 +628,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           nd[m] = row_in ? -raw_d[m] : 0.f;
         }
         const uint64_t l1 = f2_pack(nl[0], nl[0]), l2 = f2_pack(nl[1], nl[1]);
-        const uint64_t d1 = f2_pack(nd[0], nd[0]), d2 = f2_pack(nd[1], nd[1]);
-        const uint64_t nlam2 = f2_pack(raw_nl, raw_nl);
+        const float lam_d2 = raw_nl * nd[1];
+        const uint64_t d1 = f2_pack(nd[0], nd[0]), ld2 = f2_pack(lam_d2, lam_d2), nlam2 = f2_pack(raw_nl, raw_nl);
         uint64_t t2[2] = {0ull, 0ull};  // sum of P_2 dP
         KCursor cur;
         cur.start(prm, x.it, qb);
+        const int n_keys = (int)L, diag_keys = qb * BM + row + 1;  // visible keys of a partition, of the diagonal one
         for (int j = 0; j < x.NB && ok; ++j) {
           if (j > 0) cur.step(prm, x.it, qb);
           const int64_t gi = g0 + j;
           const uint32_t dpb = tm_dp + (uint32_t)((gi & 1) * 64);
-          int hi = (int)min((int64_t)BS, L - (int64_t)cur.kb * BS);  // keys past the partition end
-          if (prm.causal && cur.kp == p) hi = min(hi, qb * BM + row + 1 - cur.kb * BS);
-          hi -= c_base;
-          const bool any_mask = __any_sync(0xffffffffu, hi < 32);
+          // keys past the partition's end, or behind the row, are masked
+          const bool diag = prm.causal && cur.kp == p;
+          const int hi = (diag ? min(n_keys, diag_keys) : n_keys) - cur.kb * BS - c_base;
+          const bool any_mask = (cur.kb + 1) * BS > (diag ? min(n_keys, qb * BM) : n_keys);
           ok = wait_all(Ly::B_S, (uint32_t)(gi & 1), ROLE_EW, j);
           if (!ok) break;
           tc_fence_after();
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             f2_unpack(f2_mul(f2_add(d, d1), f2_pack(p1[c], p1[c + 1])), a0, a1);
             s1[c / 2] = pack_bf16x2(a0, a1);
             t2[(c >> 1) & 1] = f2_fma(q2, d, t2[(c >> 1) & 1]);
-            f2_unpack(f2_mul(f2_add(d, d2), f2_mul(q2, nlam2)), a0, a1);
+            f2_unpack(f2_mul(f2_fma(d, nlam2, ld2), q2), a0, a1);  // -lam (dP - D_2) P_2
             s2[c / 2] = pack_bf16x2(a0, a1);
           }
           tmem_st16(dpb, s1);
@@ -801,26 +831,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (i + 2 == NB) tc_commit_warp(bar(Ly::B_QTE));
             }
           }
-          if (KV) {
-            ok = wait1(Ly::B_A, (uint32_t)(gi & 1));
-            if (ok && i == 0 && k_unit > 0) ok = wait1(Ly::B_ACCE, (uint32_t)((k_unit - 1) & 1));  // accumulators copied out
-            if (!ok) break;
-            tc_fence_after();
-            issue_dv(gi, i == 0);
-          }
-          ok = wait1(Ly::B_DS, (uint32_t)(gi & 1));
-          if (ok && !KV && i == 0 && k_unit > 0) ok = wait1(Ly::B_ACCE, (uint32_t)((k_unit - 1) & 1));
+          ok = wait1(Ly::B_DS, (uint32_t)(gi & 1));  // (dkdv: and A)
+          if (ok && i == 0 && k_unit > 0) ok = wait1(Ly::B_ACCE, (uint32_t)((k_unit - 1) & 1));  // accumulators copied out
           if (!ok) break;
           tc_fence_after();
           issue_half(gi, i == 0);
-          if (i + 1 == NB) tc_commit_warp(bar(Ly::B_ACC));  // the unit's accumulators are complete
-          if (KV && i + 1 < NB) {
-            ok = wait_b(gi + 1);
-            if (!ok) break;
-            tc_fence_after();
-            issue_dp(gi + 1);
-            if (i + 2 == NB) tc_commit_warp(bar(Ly::B_RESE));  // the unit's last S and dP are issued
+          if (KV) {
+            if (i + 1 < NB) {  // in place of dS(gi), which dK(gi) has read; the elementwise warps wait for it next
+              ok = wait_b(gi + 1);
+              if (!ok) break;
+              tc_fence_after();
+              issue_dp(gi + 1);
+              if (i + 2 == NB) tc_commit_warp(bar(Ly::B_RESE));  // the unit's last S and dP are issued
+            }
+            // A's buffer is written again at gi + 2, after S(gi + 2), which follows this product
+            issue_dv(gi, i == 0);
           }
+          if (i + 1 == NB) tc_commit_warp(bar(Ly::B_ACC));  // the unit's accumulators are complete
         }
         if (!ok) break;
         int vn = -1;
@@ -1110,6 +1137,8 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
   }
   prm.n_units = (int32_t)units;
   prm.causal = a.causal;
+  // causal units differ in length: enough lanes together for about three times the grid, so that the last ones are short
+  prm.batch = a.causal ? (int32_t)std::min<int64_t>(units / prm.nb, (3LL * sms + prm.nb - 1) / prm.nb) : 1;
   prm.lam_n = a.lam_n;
   prm.scale = a.scale;
   prm.scale_log2 = a.scale_log2;

@@ -11,8 +11,8 @@
 // for one half of the columns and writes O = O_1 / l_1 - lam O_2 / l_2 (and O_2 for the backward
 // pass) rounded once; no partial output leaves the SM.
 //
-// A work unit is (batch, KV head, work item, query head of the group, 128-row query tile), causal tiles
-// heaviest first.  The work item is the whole sequence where its tiles alone fill the GPU; with
+// A work unit is (batch, KV head, work item, query head of the group, 128-row query tile); causal units
+// go heaviest first within batches of heads that fill the grid a few times (Params::batch).  The work item is the whole sequence where its tiles alone fill the GPU; with
 // fewer the plan's items split the keys, and normalised partial outputs and LSEs of both maps go
 // to the merge (launch_diff_fwd_tc).
 //
@@ -91,12 +91,15 @@ struct Params {
   uint32_t* counter;
   int64_t S, L;
   int32_t B, Hq, Hkv, P, n_items, n_slots, nqt, n_units, causal, lam_n;
+  int32_t batch;  // (head, work item) lanes whose tiles are numbered together
   float scale_log2;
   int64_t wait_limit_ns;
 };
 
-// What every role derives from a unit index: (batch, KV head, work item, query head of the group,
-// query tile), the last fastest, so the units running at once share one KV head's keys in L2.
+// What every role derives from a unit index.  A lane is (batch, KV head, work item, query head of the
+// group), the last fastest; units are numbered batch of lanes by batch, within it tile by tile (causal: from
+// the longest), within a tile lane by lane.  With batch = 1 the units running at once share one
+// KV head's keys in L2; a few lanes together keep the last units short where their lengths differ.
 struct Unit {
   int b, h, hk, qt;
   DevItem it;
@@ -107,9 +110,12 @@ struct Unit {
 __device__ __forceinline__ Unit decode(int u, const Params& prm) {
   Unit x;
   const int g = prm.Hq / prm.Hkv;
-  x.qt = u % prm.nqt;
-  if (prm.causal) x.qt = prm.nqt - 1 - x.qt;  // the longest first: the grid's last units are short
-  u /= prm.nqt;
+  const int per = prm.batch * prm.nqt, first = u / per * prm.batch;
+  const int lanes = min(prm.batch, prm.n_units / prm.nqt - first);  // the last batch may be smaller
+  u %= per;
+  x.qt = u / lanes;
+  if (prm.causal) x.qt = prm.nqt - 1 - x.qt;
+  u = first + u % lanes;
   const int gi = u % g;
   u /= g;
   const int item = u % prm.n_items;
@@ -696,6 +702,8 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
   prm.nqt = (int32_t)nqt;
   prm.n_units = (int32_t)units;
   prm.causal = a.causal;
+  // enough lanes for about three times the grid
+  prm.batch = a.causal ? (int32_t)std::min<int64_t>(units / nqt, (3LL * sms + nqt - 1) / nqt) : 1;
   prm.lam_n = a.lam_n;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
