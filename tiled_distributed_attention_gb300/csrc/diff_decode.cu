@@ -5,10 +5,11 @@
 // Bound by memory: every cached byte is read once (a KV head's cache serves its whole group of
 // query heads and both maps), at 12 flops a byte and query head or fewer.
 //
-// Work split.  The batch's cached tokens, in tiles of 128 over (sequence, KV head, head chunk), are
-// one long list that the CTAs share out evenly: CTA i takes tiles [i W / G, (i + 1) W / G).  So
-// the split does not depend on how ragged the batch is, and one long sequence fills the GPU as
-// well as many short ones.  The lengths are read on the device: a captured graph replays with
+// Work split.  The batch's cached tokens, in tiles of 128 over the segments (sequence, KV head, head chunk),
+// are one long list that the CTAs share out evenly: CTA i takes the units [i W / G, (i + 1) W / G), a
+// unit being a tile, or one of the SEG_COST units that stand before each segment for what a segment
+// costs besides its tiles.  So the split does not depend on how ragged the batch is, one long sequence
+// fills the GPU as well as many short ones, and short ones do not pile up in one CTA.  The lengths are read on the device: a captured graph replays with
 // other lengths.  A (sequence, head) whose tiles fall into one CTA is finished there; of the others every
 // CTA leaves unnormalised sums with their running maxima in a slot of its own (two a CTA: the piece
 // that began before it and the piece that goes on behind it), and the last CTA to arrive
@@ -40,6 +41,9 @@ constexpr int TILE = WARPS * WT;  // tokens of a tile
 constexpr int HEADS = 8;          // query heads of a chunk; rows: map * HEADS + head
 constexpr int ROWS = 2 * HEADS;
 constexpr int STAGES = 3;
+// Filling the ring and adding up the warps' sums at a segment's end take about as long as three tiles
+// (4 us; a tile is 64 KB at d = 128, 1.45 us at the memory's rate).
+constexpr int SEG_COST = 3;
 constexpr int MAX_B = 4096;  // their tile counts are kept in shared memory beside the ring
 constexpr float LN2 = 0.69314718055994531f;
 
@@ -275,99 +279,144 @@ struct EngineBf16 {
   }
 };
 
-// fp32 (and the plain reading of the algorithm): CUDA cores.  A lane owns D / 32 columns, so
-// lanes 0-15 hold the first map's columns of K and lanes 16-31 the second's: one reduction
-// over 16 lanes gives both maps' scores at once.
-template <typename T_, int D, int G>
-struct EngineSimt {
-  using T = T_;
+// fp32: CUDA cores.  A lane owns D / 32 columns, so lanes 0-15 hold the first map's columns of K and
+// lanes 16-31 the second's: one reduction over 16 lanes gives both maps' scores at once.  A warp
+// takes four tokens at a time from its own ring; the reduction transposes as it goes (two
+// values, then one, travel), so that afterwards a lane holds one token's score and takes one
+// exponential, and eight shuffles hand the weights of both maps to all lanes.
+template <int D, int G>
+struct EngineF32 {
+  using T = float;
   static constexpr int E = D / 32;
-  static constexpr int U = 4;  // tokens whose loads are in flight together
-  static constexpr uint32_t SMEM = 0;
+  static constexpr int U = 4;  // tokens of a stage
+  static constexpr int NS = 6;
+  static constexpr uint32_t ROWB = U * D * 4;  // K or V of a stage
+  static constexpr uint32_t STAGE = 2 * ROWB;
+  static constexpr uint32_t SMEM = WARPS * NS * STAGE;
   float acc[2][G][E];
-  float m[G], l[G];  // of this half's map
+  float m[G], l[G];  // of this half's map; l of this lane's tokens
+  uint32_t base;
+  const uint8_t* ring;
 
-  struct alignas(sizeof(T) * E) Row {
-    T v[E];
-  };
+  __device__ __forceinline__ void init(uint32_t smem, int warp) {
+    base = smem + (uint32_t)(warp * NS) * STAGE;
+    extern __shared__ __align__(128) uint8_t smem_bytes[];
+    ring = smem_bytes + (size_t)(warp * NS) * STAGE;
+  }
 
-  __device__ __forceinline__ void init(uint32_t, int) {}
+  __device__ __forceinline__ void load(const Params& p, const T* kb, const T* vb, int stage, int tok0, int len, int lane) {
+    const uint32_t dst = base + (uint32_t)stage * STAGE;
+    constexpr int CH = D / 4;  // 16-byte chunks of a row
+#pragma unroll
+    for (int i = 0; i < U * CH / 32; ++i) {
+      const int idx = i * 32 + lane, row = idx / CH, ch = idx % CH;
+      const bool in = tok0 + row < len;
+      const int64_t t = in ? tok0 + row : 0;  // a safe address where nothing is read
+      cp_async16(dst + (uint32_t)idx * 16u, kb + t * p.ks[2] + ch * 4, in);
+      cp_async16(dst + ROWB + (uint32_t)idx * 16u, vb + t * p.vs[2] + ch * 4, in);
+    }
+  }
 
   __device__ __forceinline__ void piece(const Params& p, int b, int hk, int h0, int nh, int t0, int t1, int len, int warp,
                                         int lane) {
     const T* qp = static_cast<const T*>(p.q) + ((int64_t)b * p.Hq + h0) * D + lane * E;
-    const T* kb = static_cast<const T*>(p.k) + b * p.ks[0] + hk * p.ks[1] + lane * E;
-    const T* vb = static_cast<const T*>(p.v) + b * p.vs[0] + hk * p.vs[1] + lane * E;
+    const T* kb = static_cast<const T*>(p.k) + b * p.ks[0] + hk * p.ks[1];
+    const T* vb = static_cast<const T*>(p.v) + b * p.vs[0] + hk * p.vs[1];
+    const int n = (t1 - t0) * (WT / U);  // groups of four tokens
+    auto tok_of = [&](int g) { return (t0 + g / (WT / U)) * TILE + warp * WT + g % (WT / U) * U; };
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      if (s < n) load(p, kb, vb, s, tok_of(s), len, lane);
+      cp_commit();
+    }
     float q[G][E];
 #pragma unroll
     for (int i = 0; i < G; ++i) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        q[i][e] = i < nh ? to_f(qp[i * D + e]) * p.scale_log2 : 0.f;
+        q[i][e] = i < nh ? qp[i * D + e] * p.scale_log2 : 0.f;
         acc[0][i][e] = acc[1][i][e] = 0.f;
       }
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
-    for (int t = t0; t < t1; ++t) {
-#pragma unroll 1
-      for (int j = 0; j < WT; j += U) {
-        const int tok = t * TILE + warp * WT + j;
-        if (tok >= len) break;
-        Row kr[U], vr[U];
+    const bool b3 = lane & 8, b2 = lane & 4;
+    const int mine = (b3 ? 2 : 0) + (b2 ? 1 : 0);  // this lane's token of a group
+    int stage = 0;
+    for (int g = 0; g < n; ++g) {
+      {
+        int s = stage + NS - 1;
+        if (s >= NS) s -= NS;
+        if (g + NS - 1 < n) load(p, kb, vb, s, tok_of(g + NS - 1), len, lane);
+        cp_commit();
+      }
+      cp_wait<NS - 1>();
+      __syncwarp();
+      const int tok = tok_of(g);
+      if (tok < len) {
+        const float* kr = reinterpret_cast<const float*>(ring + (size_t)stage * STAGE) + lane * E;
+        const float* vr = kr + U * D;
+        float kx[U][E], vx[U][E];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool in = tok + u < len;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 0; e < E; ++e) kr[u].v[e] = vr[u].v[e] = T(0.f);
-          if (in) {
-            kr[u] = *reinterpret_cast<const Row*>(kb + (int64_t)(tok + u) * p.ks[2]);
-            vr[u] = *reinterpret_cast<const Row*>(vb + (int64_t)(tok + u) * p.vs[2]);
+          for (int e = 0; e < E; ++e) {
+            kx[u][e] = kr[u * D + e];
+            vx[u][e] = vr[u * D + e];
           }
-        }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          float s[U], mx = m[i];
+          float s[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             s[u] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[u] = fmaf(q[i][e], to_f(kr[u].v[e]), s[u]);
+            for (int e = 0; e < E; ++e) s[u] = fmaf(q[i][e], kx[u][e], s[u]);
           }
-#pragma unroll
-          for (int x = 8; x >= 1; x >>= 1)
-#pragma unroll
-            for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], x);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (tok + u >= len) s[u] = -INFINITY;
-            mx = fmaxf(mx, s[u]);
-          }
+          float k0 = b3 ? s[2] : s[0], k1 = b3 ? s[3] : s[1];
+          k0 += __shfl_xor_sync(0xffffffffu, b3 ? s[0] : s[2], 8);
+          k1 += __shfl_xor_sync(0xffffffffu, b3 ? s[1] : s[3], 8);
+          float x = b2 ? k1 : k0;
+          x += __shfl_xor_sync(0xffffffffu, b2 ? k0 : k1, 4);
+          x += __shfl_xor_sync(0xffffffffu, x, 2);
+          x += __shfl_xor_sync(0xffffffffu, x, 1);
+          if (tok + mine >= len) x = -INFINITY;
+          float mx = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          mx = fmaxf(m[i], fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8)));
           const float ref = mx == -INFINITY ? 0.f : mx;
           const float f = exp2f(m[i] - ref);
           m[i] = mx;
-          l[i] *= f;
-          const float fo = __shfl_xor_sync(0xffffffffu, f, 16);
-          const float f1 = lane < 16 ? f : fo, f2 = lane < 16 ? fo : f;
+          x = exp2f(x - ref);
+          l[i] = l[i] * f + x;
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+            const float fo = __shfl_xor_sync(0xffffffffu, f, 16);
+            const float f1 = lane < 16 ? f : fo, f2 = lane < 16 ? fo : f;
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            acc[0][i][e] *= f1;
-            acc[1][i][e] *= f2;
+            for (int e = 0; e < E; ++e) {
+              acc[0][i][e] *= f1;
+              acc[1][i][e] *= f2;
+            }
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const float x = exp2f(s[u] - ref);
-            l[i] += x;
-            const float xo = __shfl_xor_sync(0xffffffffu, x, 16);
-            const float p1 = lane < 16 ? x : xo, p2 = lane < 16 ? xo : x;
+            const int src = (u >> 1) * 8 + (u & 1) * 4;
+            const float p1 = __shfl_sync(0xffffffffu, x, src), p2 = __shfl_sync(0xffffffffu, x, 16 + src);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-              acc[0][i][e] = fmaf(p1, to_f(vr[u].v[e]), acc[0][i][e]);
-              acc[1][i][e] = fmaf(p2, to_f(vr[u].v[e]), acc[1][i][e]);
+              acc[0][i][e] = fmaf(p1, vx[u][e], acc[0][i][e]);
+              acc[1][i][e] = fmaf(p2, vx[u][e], acc[1][i][e]);
             }
           }
         }
       }
+      __syncwarp();  // every lane is done with the stage before the next load overwrites it
+      if (++stage == NS) stage = 0;
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
     }
   }
 
@@ -402,6 +451,8 @@ template <typename Engine, int D>
 struct Big {
   static constexpr uint32_t SUMS = (uint32_t)(WARPS * ROWS * D * 4);
   static constexpr uint32_t BYTES = Engine::SMEM > SUMS ? Engine::SMEM : SUMS;
+  // the last CTA's weights, and its columns' sums by group of pieces
+  static_assert(MAX_SMS * ROWS * 4 + 2 * THREADS * 16 <= SUMS, "room for the merge");
 };
 
 template <typename Engine, int D>
@@ -419,7 +470,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + BIG + 4 * (2 * WARPS * ROWS + 2 * ROWS + 16));  // [B + 1] tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // tiles before each sequence
+  // units before each sequence
   {
     int64_t carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
@@ -429,6 +480,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
         const int raw = __ldg(p.lens + b);
         if ((raw < 0 || raw > p.T) && blockIdx.x == 0) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, 6, b);
         n = (length_of(p, b) + TILE - 1) / TILE;
+        if (n > 0) n += SEG_COST;
       }
       int x = n;
 #pragma unroll
@@ -452,10 +504,10 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
   }
   const int per = p.Hkv * p.hc;  // (KV head, head chunk) of a sequence
   const int64_t W = prefix[p.B] * per;
-  // no more CTAs than tiles: every CTA between a segment's first and last then has a piece of it
+  // no more CTAs than units: every CTA between a segment's first and last then has a piece of it
   const int64_t G = max((int64_t)1, min((int64_t)gridDim.x, W));
   auto begin_of = [&](int64_t i) { return W * i / G; };
-  // the CTA whose range holds tile x
+  // the CTA whose range holds unit x
   auto owner_of = [&](int64_t x) {
     int64_t i = x * G / W;
     while (begin_of(i + 1) <= x) ++i;
@@ -467,10 +519,9 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
   // O = sums1 / l1 - lam sums2 / l2 of a head's four columns, and its two LSEs
   auto finish = [&](int b, int h, int c4, float4 x1, float4 x2, float m1, float l1, float m2, float l2) {
     const float lam = to_f(static_cast<const T*>(p.lam)[p.lam_n == 1 ? 0 : h]);
-    const float i1 = l1 > 0.f ? 1.f / l1 : 0.f, i2 = l2 > 0.f ? lam / l2 : 0.f;
-    // l is NaN where a score is: the row is then NaN as its definition is
-    const float y[4] = {l1 == l1 ? x1.x * i1 - x2.x * i2 : l1, l1 == l1 ? x1.y * i1 - x2.y * i2 : l1,
-                        l1 == l1 ? x1.z * i1 - x2.z * i2 : l1, l1 == l1 ? x1.w * i1 - x2.w * i2 : l1};
+    // no cached token: O = 0 (a NaN sum stays NaN)
+    const float i1 = l1 == 0.f ? 0.f : 1.f / l1, i2 = l2 == 0.f ? 0.f : lam / l2;
+    const float y[4] = {x1.x * i1 - x2.x * i2, x1.y * i1 - x2.y * i2, x1.z * i1 - x2.z * i2, x1.w * i1 - x2.w * i2};
     const int64_t at = ((int64_t)b * p.Hq + h) * D + c4;
     if constexpr (sizeof(T) == 2) {
       uint2 w;
@@ -497,7 +548,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
   eng.init(smem_u32(smem), warp);
   int64_t x = lo;
   while (x < hi) {
-    // the sequence of tile x: the last b with prefix[b] * per <= x (empty ones share its prefix)
+    // the sequence of unit x: the last b with prefix[b] * per <= x (empty ones share its prefix)
     int b;
     {
       int a = 0, z = p.B;
@@ -508,12 +559,17 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
       }
       b = a;
     }
-    const int64_t n = prefix[b + 1] - prefix[b];  // > 0
+    const int64_t n = prefix[b + 1] - prefix[b];  // > SEG_COST
     const int64_t seg = (x - prefix[b] * per) / n;
-    const int64_t s0 = prefix[b] * per + seg * n, s1 = s0 + n;  // the segment's tiles
+    const int64_t s1 = prefix[b] * per + (seg + 1) * n, s0 = s1 - n + SEG_COST;  // the segment's tiles are [s0, s1)
+    const int64_t end = min(hi, s1);
+    if (end <= s0) {  // nothing of it but the units before its tiles
+      x = end;
+      continue;
+    }
+    x = max(x, s0);
     const int hk = (int)(seg / p.hc), c = (int)(seg % p.hc);
     const int h0 = hk * p.g + c * HEADS, nh = min(HEADS, p.g - c * HEADS);
-    const int64_t end = min(hi, s1);
     eng.piece(p, b, hk, h0, nh, (int)(x - s0), (int)(end - s0), length_of(p, b), warp, lane);
 
     // the warps' sums as one
@@ -567,32 +623,64 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
         scan[WARPS] = last;
       }
       __syncthreads();
-      if (scan[WARPS] && h < nh) {
+      if (scan[WARPS]) {
+        // the last CTA adds the segment's pieces up, in order.  Row r's weights 2^(m - M) first, sixteen
+        // threads a row; then every thread takes one or two 16-byte columns of the rows over all pieces, or
+        // over every G-th of them where there are fewer columns than threads.  (The pieces copied to
+        // shared memory with cp.async instead: 3 us slower at 38 pieces.)
         __threadfence();
-        auto slot_of = [&](int64_t i) { return p.part + (i * 2 + (i == i0 ? 1 : 0)) * part_floats(D); };
-        float M1 = -INFINITY, M2 = -INFINITY;
-#pragma unroll 8
-        for (int64_t i = i0; i <= i1; ++i) {
-          const float* s = slot_of(i) + ROWS * D;
-          M1 = fmaxf(M1, __ldcg(s + h));
-          M2 = fmaxf(M2, __ldcg(s + HEADS + h));
+        const int n_p = (int)(i1 - i0 + 1);
+        float* wts = sums;                    // [n_p][ROWS]
+        float* part = sums + MAX_SMS * ROWS;  // [G][2 nh][D]
+        auto slot_of = [&](int k) { return p.part + ((i0 + k) * 2 + (k == 0 ? 1 : 0)) * part_floats(D); };
+        {
+          const int r = tid >> 4, k0 = tid & 15;
+          float M = -INFINITY;
+#pragma unroll 4
+          for (int k = k0; k < n_p; k += 16) M = fmaxf(M, __ldcg(slot_of(k) + ROWS * D + r));
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+          float L = 0.f;
+#pragma unroll 4
+          for (int k = k0; k < n_p; k += 16) {
+            const float* st = slot_of(k) + ROWS * D + r;
+            const float m = __ldcg(st), l = __ldcg(st + ROWS);
+            const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+            wts[k * ROWS + r] = f;
+            L += m == -INFINITY ? l : l * f;  // l is 0 there, or NaN
+          }
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+          if (k0 == 0) {
+            Ms[r] = M;
+            Ls[r] = L;
+          }
         }
-        float L1 = 0.f, L2 = 0.f;
-        a1 = a2 = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int64_t i = i0; i <= i1; ++i) {
-          const float* s = slot_of(i);
-          const float4 y1 = __ldcg(reinterpret_cast<const float4*>(s + h * D + c4));
-          const float4 y2 = __ldcg(reinterpret_cast<const float4*>(s + (HEADS + h) * D + c4));
-          const float m1 = __ldcg(s + ROWS * D + h), m2 = __ldcg(s + ROWS * D + HEADS + h);
-          const float f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M1), f2 = m2 == -INFINITY ? 0.f : exp2f(m2 - M2);
-          const float l1 = __ldcg(s + ROWS * D + ROWS + h), l2 = __ldcg(s + ROWS * D + ROWS + HEADS + h);
-          L1 += m1 == -INFINITY ? l1 : l1 * f1;
-          L2 += m2 == -INFINITY ? l2 : l2 * f2;
-          a1.x += y1.x * f1, a1.y += y1.y * f1, a1.z += y1.z * f1, a1.w += y1.w * f1;
-          a2.x += y2.x * f2, a2.y += y2.y * f2, a2.z += y2.z * f2, a2.w += y2.w * f2;
+        __syncthreads();
+        const int cols = 2 * nh * (D / 4), G = cols >= THREADS ? 1 : THREADS / cols;
+        for (int o = tid; o < cols * G; o += THREADS) {
+          const int grp = o / cols, c = o - grp * cols, r = c / (D / 4), at = c % (D / 4) * 4;
+          const int row = r < nh ? r : HEADS + r - nh;
+          float4 t = make_float4(0, 0, 0, 0);
+#pragma unroll 16
+          for (int k = grp; k < n_p; k += G) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k) + row * D + at));
+            const float f = wts[k * ROWS + row];
+            t.x = fmaf(y.x, f, t.x), t.y = fmaf(y.y, f, t.y), t.z = fmaf(y.z, f, t.z), t.w = fmaf(y.w, f, t.w);
+          }
+          *reinterpret_cast<float4*>(part + (grp * 2 * nh + r) * D + at) = t;
         }
-        finish(b, h0 + h, c4, a1, a2, M1, L1, M2, L2);
+        __syncthreads();
+        if (h < nh) {
+          a1 = a2 = make_float4(0, 0, 0, 0);
+          for (int g = 0; g < G; ++g) {
+            const float4 y1 = *reinterpret_cast<const float4*>(part + (g * 2 * nh + h) * D + c4);
+            const float4 y2 = *reinterpret_cast<const float4*>(part + (g * 2 * nh + nh + h) * D + c4);
+            a1.x += y1.x, a1.y += y1.y, a1.z += y1.z, a1.w += y1.w;
+            a2.x += y2.x, a2.y += y2.y, a2.z += y2.z, a2.w += y2.w;
+          }
+          finish(b, h0 + h, c4, a1, a2, Ms[h], Ls[h], Ms[HEADS + h], Ls[HEADS + h]);
+        }
       }
     }
     __syncthreads();  // the sums' memory is the ring's again
@@ -639,10 +727,10 @@ static int launch(const Params& p, int grid, cudaStream_t st, std::string* err) 
 template <int D>
 static int launch_f32(const Params& p, int grid, cudaStream_t st, std::string* err) {
   const int n = std::min(p.g, HEADS);
-  if (n <= 1) return launch<EngineSimt<float, D, 1>, D>(p, grid, st, err);
-  if (n <= 2) return launch<EngineSimt<float, D, 2>, D>(p, grid, st, err);
-  if (n <= 4) return launch<EngineSimt<float, D, 4>, D>(p, grid, st, err);
-  return launch<EngineSimt<float, D, 8>, D>(p, grid, st, err);
+  if (n <= 1) return launch<EngineF32<D, 1>, D>(p, grid, st, err);
+  if (n <= 2) return launch<EngineF32<D, 2>, D>(p, grid, st, err);
+  if (n <= 4) return launch<EngineF32<D, 4>, D>(p, grid, st, err);
+  return launch<EngineF32<D, 8>, D>(p, grid, st, err);
 }
 
 }  // namespace ddec
