@@ -574,9 +574,23 @@ def _one_device(*ts) -> int:
     """The CUDA device all tensors are on."""
     index = ts[0].get_device()
     for t in ts:
-        if t.get_device() != index or index < 0 or not t.is_cuda:
-            raise ValueError("tensors must be on one CUDA device; got " + ", ".join(str(t.device) for t in ts))
+        if t.get_device() != index:
+            index = -1
+    if index < 0 or not ts[0].is_cuda:
+        raise ValueError("tensors must be on one CUDA device; got " + ", ".join(str(t.device) for t in ts))
     return index
+
+
+# Sizes, strides and types that have passed a call's checks: a program repeats them step after step, and the
+# checks cost more than a short kernel.  Holds no tensor and nothing of their contents.
+_passed: Dict[tuple, object] = {}
+
+
+def _remember(key: tuple, value):
+    if len(_passed) >= 4096:
+        _passed.clear()
+    _passed[key] = value
+    return value
 
 
 # A step of a small model is shorter than a few Python calls, so the calls below take the current device
@@ -599,11 +613,8 @@ def _on_device(index: int, where: str, fn, *args) -> None:
         _check(rc, where)
 
 
-def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
-                   q_out: torch.Tensor, k_out: Optional[torch.Tensor], inverse: bool = False, stream=None) -> None:
-    """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) rotated into q_out and k_out; views with any batch,
-    head and token strides.  positions: int32 or int64 [axes, S] or [axes, B, S] ([S] or [B, S]
-    for one axis), any strides."""
+def _rope_args(rope: MeshRope, q, k, positions, q_out, k_out):
+    """Checks of mesh_attn_rope, and its arguments that follow from sizes, strides and types."""
     load_library()
     if q.dim() != 4 or q.shape[3] != rope.d:
         raise ValueError(f"q must be [B, H, S, {rope.d}]")
@@ -632,21 +643,41 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
     if pos.dim() != 3 or pos.shape[0] != rope.n_axes or pos.shape[1] not in (1, B) or pos.shape[2] != S:
         raise ValueError(f"positions must be [{rope.n_axes}, S] or [{rope.n_axes}, B, S] with B = {B}, S = {S}; got "
                          f"{tuple(positions.shape)}")
-    index = _one_device(positions, *(t for p in pairs for t in p))
     ps = pos.stride()
-    _on_device(index, "mesh_attn_rope", _lib.mesh_attn_rope, _dtype_code(q.dtype), B, S, d, Hq, q.data_ptr(), _strides3(q),
-               q_out.data_ptr(), _strides3(q_out), 0 if k is None else k.shape[1], None if k is None else k.data_ptr(),
-               None if k is None else _strides3(k), None if k is None else k_out.data_ptr(),
-               None if k is None else _strides3(k_out), rope.groups, rope.n_pairs, rope.n_axes, rope._freq, rope._axis,
-               rope._adjacent, int(inverse), pos.data_ptr(), 8 * pos.element_size(),
-               _i64x3(ps[0], ps[1] if pos.shape[1] != 1 else 0, ps[2]), _raw_stream(index, stream))
+    return (_dtype_code(dtype), B, S, d, Hq, _strides3(q), _strides3(q_out), 0 if k is None else k.shape[1],
+            None if k is None else _strides3(k), None if k is None else _strides3(k_out), 8 * pos.element_size(),
+            _i64x3(ps[0], ps[1] if pos.shape[1] != 1 else 0, ps[2]))
+
+
+def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+                   q_out: torch.Tensor, k_out: Optional[torch.Tensor], inverse: bool = False, stream=None) -> None:
+    """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) rotated into q_out and k_out; views with any batch,
+    head and token strides.  positions: int32 or int64 [axes, S] or [axes, B, S] ([S] or [B, S]
+    for one axis), any strides."""
+    key = (rope, q.shape, q.stride(), q.dtype, q_out.shape, q_out.stride(), q_out.dtype, positions.shape, positions.stride(),
+           positions.dtype)
+    if k is not None and k_out is not None:
+        key += (k.shape, k.stride(), k.dtype, k_out.shape, k_out.stride(), k_out.dtype)
+        index = _one_device(q, q_out, positions, k, k_out)
+        kp, ko = k.data_ptr(), k_out.data_ptr()
+    else:
+        key += (k is None, k_out is None)
+        index = _one_device(q, q_out, positions)
+        kp = ko = None
+    a = _passed.get(key)
+    if a is None:
+        a = _remember(key, _rope_args(rope, q, k, positions, q_out, k_out))
+    dt, B, S, d, Hq, qs, qos, Hk, ks, kos, bits, ps = a
+    _on_device(index, "mesh_attn_rope", _lib.mesh_attn_rope, dt, B, S, d, Hq, q.data_ptr(), qs, q_out.data_ptr(), qos, Hk, kp, ks,
+               ko, kos, rope.groups, rope.n_pairs, rope.n_axes, rope._freq, rope._axis, rope._adjacent, 1 if inverse else 0,
+               positions.data_ptr(), bits, ps, _raw_stream(index, stream))
 
 
 def mesh_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
     """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) with their positions, as dense [B, H, S, d] tensors, which is what
     the attention calls take; q and k may be views, e.g. a projection's [B, S, H, d] transposed."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    q_out = q.new_empty(q.shape)
+    k_out = None if k is None else k.new_empty(k.shape)
     mesh_attn_rope(rope, q, k, positions, q_out, k_out)
     return q_out, k_out
 
@@ -707,6 +738,13 @@ def _diff_scale(scale: Optional[float], d: int) -> float:
 def _diff_check(q, k, v, lam, *more):
     """(B, Hq, S, d, device) of matching tensors of one dtype on one device."""
     qs, ks, ls = q.shape, k.shape, lam.shape
+    dtype = q.dtype
+    key = (qs, ks, v.shape, ls, dtype, k.dtype, v.dtype, lam.dtype)
+    if key in _passed:
+        for t in more:
+            if t.dtype != dtype:
+                raise ValueError("q, k, v, lam and the gradients must be of one dtype")
+        return (*qs, _one_device(q, k, v, lam, *more))
     if len(qs) != 4 or len(ks) != 4 or v.shape != ks:
         raise ValueError("q must be [B, Hq, S, d], k and v [B, Hkv, S, d]")
     B, Hq, S, d = qs
@@ -716,11 +754,12 @@ def _diff_check(q, k, v, lam, *more):
         raise ValueError(f"Hq must be a multiple of Hkv: {Hq} and {ks[1]}")
     if len(ls) != 1 or (ls[0] != Hq and ls[0] != 1):
         raise ValueError("lam must be [Hq], or [1] for one value for all heads")
-    dtype = q.dtype
     for t in (k, v, lam) + more:
         if t.dtype != dtype:
             raise ValueError("q, k, v, lam and the gradients must be of one dtype")
-    return B, Hq, S, d, _one_device(q, k, v, lam, *more)
+    index = _one_device(q, k, v, lam, *more)
+    _remember(key, True)
+    return B, Hq, S, d, index
 
 
 def mesh_attn_diff_workspace_size(plan: Plan, dtype: torch.dtype, B: int, Hq: int, Hkv: int, d: int,
@@ -824,7 +863,7 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     _one_device(q, ws, st)
     O = torch.empty_like(q)
     O2 = torch.empty_like(q) if return_saved else None
-    LSE = torch.empty((B, Hq, 2, S), dtype=torch.float32, device=q.device)
+    LSE = q.new_empty((B, Hq, 2, S), dtype=torch.float32)
     _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
@@ -927,8 +966,8 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     ws = new_diff_decode_workspace(B, Hq, k_cache.shape[1], d, k_cache.shape[2], q.device) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
     _one_device(q, ws, st)
-    O = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    LSE = torch.empty((B, Hq, 2, 1), dtype=torch.float32, device=q.device)
+    O = q.new_empty(q.shape)
+    LSE = q.new_empty((B, Hq, 2, 1), dtype=torch.float32)
     _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
