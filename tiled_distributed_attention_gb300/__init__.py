@@ -676,8 +676,8 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
 def mesh_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
     """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) with their positions, as dense [B, H, S, d] tensors, which is what
     the attention calls take; q and k may be views, e.g. a projection's [B, S, H, d] transposed."""
-    q_out = q.new_empty(q.shape)
-    k_out = None if k is None else k.new_empty(k.shape)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
     mesh_attn_rope(rope, q, k, positions, q_out, k_out)
     return q_out, k_out
 
@@ -863,7 +863,7 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     _one_device(q, ws, st)
     O = torch.empty_like(q)
     O2 = torch.empty_like(q) if return_saved else None
-    LSE = q.new_empty((B, Hq, 2, S), dtype=torch.float32)
+    LSE = torch.empty((B, Hq, 2, S), dtype=torch.float32, device=q.device)
     _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
@@ -966,8 +966,8 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     ws = new_diff_decode_workspace(B, Hq, k_cache.shape[1], d, k_cache.shape[2], q.device) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
     _one_device(q, ws, st)
-    O = q.new_empty(q.shape)
-    LSE = q.new_empty((B, Hq, 2, 1), dtype=torch.float32)
+    O = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    LSE = torch.empty((B, Hq, 2, 1), dtype=torch.float32, device=q.device)
     _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
