@@ -240,6 +240,25 @@ def test_same_bits_each_time_and_what_surrounds(lib, dtype, P):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_units_many_times(lib, d):
+    """More units than SMs in both passes of the backward call, again and again: CTAs that follow one another on an SM, and
+    units of one CTA, leave every wait satisfied (the status block stays clear) and every call gives the same bits."""
+    q, k, v, lam, g = (t.cuda() for t in inputs(1, 16, 4, 4096, d, "bf16", 36))
+    plan = lib.mesh_attn_plan_create(4096, 1, True)
+    ws, st = lib.new_diff_workspace(plan, q, k, backward=True), lib.new_status()
+    keep = dict(plan=plan, workspace=ws, status=st, check_status=False)
+    O, O2, L = lib.mesh_diff_attention(q, k, v, lam, 1, True, return_saved=True, **keep)
+    first = lib.mesh_diff_attention_backward(q, k, v, lam, O, O2, L, g, 1, True, **keep)
+    for _ in range(50):
+        again = lib.mesh_diff_attention_backward(q, k, v, lam, O, O2, L, g, 1, True, **keep)
+        o, _ = lib.mesh_diff_attention(q, k, v, lam, 1, True, **keep)
+    assert lib.mesh_attn_read_status(st) == 0, st.tolist()
+    assert torch.equal(O, o)
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+
+
 def test_neighbours_nan_stays_out(lib):
     """NaN and infinities in another head, batch or partition's padding never reach a result: L = 100 is no multiple
     of a tile, so tiles reach past a partition's end."""

@@ -327,8 +327,7 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
       const bool dq_direct = mesh::rows_direct(a, Hq, a.single_slot, sms);
       const bool kv_direct = mesh::rows_direct(a, Hkv, a.single_kv_slot, sms);
       if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
-      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, true, kv_direct, stream, &err), err))) return rc;
-      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, false, dq_direct, stream, &err), err))) return rc;
+      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, kv_direct, dq_direct, stream, &err), err))) return rc;
       if (!kv_direct) {
         if ((rc = reduce(w.dk_part, a.tl.kv_slot_off, dK, Hkv, a.n_kv_slots))) return rc;
         if ((rc = reduce(w.dv_part, a.tl.kv_slot_off, dV, Hkv, a.n_kv_slots))) return rc;

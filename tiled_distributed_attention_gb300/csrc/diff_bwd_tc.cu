@@ -9,8 +9,11 @@
 // are twice as many.  (The last sum is D_2 summed over the rows, taken from fp32 products instead of
 // the rounded O_2: it nearly cancels over a batch, which a rounded operand would show.)
 //
-// Two persistent kernels after the plain backward pass's pattern: one CTA per SM, units from a counter
-// through a two-entry shared-memory ring, every role in warps of its own:
+// Two passes after the plain backward pass's pattern, in one launch: the first CTAs of the grid run dkdv, the
+// others dq, each pass persistent over its own units (its own index first, then a counter), published
+// through a two-entry shared-memory ring.  One CTA fills an SM; where both passes together have fewer
+// units than there are SMs they run side by side, and otherwise dq's CTAs start as dkdv's end.
+// Every role has warps of its own:
 //   warps 0-7   elementwise: two warps per TMEM lane quadrant, each taking 32 of a block's 64 columns
 //   warp 8      MMA issuer, warp 9 producer (TMA), warps 10-11 idle
 //   warps 12-15 (dq) copy each unit's Q and dO into TMEM, and drain and store dQ
@@ -110,7 +113,7 @@ struct Layout {
   static constexpr uint32_t BAR_OFF = VEC_OFF + 3 * 4 * BS * 4;
   static constexpr int B_RES = 0, B_AF = 1, B_AE = B_AF + NSA, B_BF = B_AE + NSA, B_BE = B_BF + NSB,
                        B_S = B_BE + NSB, B_SREAD = B_S + 1, B_DP = B_SREAD + 1, B_DS = B_DP + 2,
-                       B_ACC = B_DS + 1, B_ACCE = B_ACC + 1, B_DRAIN = B_ACCE + 1, B_VEC = B_DRAIN + 1,
+                       B_ACC = B_DS + 2, B_ACCE = B_ACC + 1, B_DRAIN = B_ACCE + 1, B_VEC = B_DRAIN + 1,
                        B_RESE = B_VEC + 3, B_UF = B_RESE + 1, B_UE = B_UF + 2, B_QTF = B_UE + 2, B_QTE = B_QTF + 1,
                        NBARS = B_QTE + 1;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBARS * 8 + (NBARS % 2) * 8;  // tmem base, abort flag
@@ -286,9 +289,8 @@ __device__ __forceinline__ int get_unit(const volatile int32_t* e, Unit& x) {
 
 // What both kernels share: barrier set-up, the unit ring and the exit.
 template <int D, bool KV>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
-    diff_bwd_kernel(const __grid_constant__ CUtensorMap tmR0, const __grid_constant__ CUtensorMap tmR1,
-                    const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params prm) {
+__device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensorMap& tmR1, const CUtensorMap& tmA,
+                                         const CUtensorMap& tmB, const Params& prm, int cta, int n_ctas) {
   // R0, R1: the resident blocks' tensors (dkdv: K, V; dq: Q, dO); A, B: the streamed ones (Q, dO; K, V)
   using Ly = Layout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -321,7 +323,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(bar(Ly::B_SREAD), N_EW);  // one lane of each elementwise warp
     mbar_init(bar(Ly::B_DP), 1);
     mbar_init(bar(Ly::B_DP + 1), 1);
+    // two, like dP's: in dq the elementwise warps may finish dS(g + 1) before the issuer has looked at dS(g),
+    // and a barrier two phases ahead looks like one that is not there yet
     mbar_init(bar(Ly::B_DS), N_EW);
+    mbar_init(bar(Ly::B_DS + 1), N_EW);
     mbar_init(bar(Ly::B_ACC), 1);
     mbar_init(bar(Ly::B_ACCE), KV ? N_EW : N_EPI);
     mbar_init(bar(Ly::B_DRAIN), 1);
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_st16(tm_dp, s1);
           tmem_st16(tm_dp + 16u, s2);
           tc_wait_st();
-          arrive(Ly::B_DS);
+          arrive(Ly::B_DS + (int)(gi & 1));
         }
         if (!ok) break;
         // the next unit, and its first block's values, before this unit's epilogue
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_st16(dpb, s1);
           tmem_st16(dpb + 16u, s2);
           tc_wait_st();
-          arrive(Ly::B_DS);
+          arrive(Ly::B_DS + (int)(gi & 1));
         }
         if (!ok) break;
         {
@@ -831,7 +836,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (i + 2 == NB) tc_commit_warp(bar(Ly::B_QTE));
             }
           }
-          ok = wait1(Ly::B_DS, (uint32_t)(gi & 1));  // (dkdv: and A)
+          ok = wait1(Ly::B_DS + (int)(gi & 1), (uint32_t)((gi >> 1) & 1));  // (dkdv: and A)
           if (ok && i == 0 && k_unit > 0) ok = wait1(Ly::B_ACCE, (uint32_t)((k_unit - 1) & 1));  // accumulators copied out
           if (!ok) break;
           tc_fence_after();
@@ -881,8 +886,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = mbar_wait(bar(Ly::B_UE + slot), (uint32_t)(((np >> 1) & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
                        ROLE_LOAD, -1);
         if (!ok) return -1;
-        int u = (int)blockIdx.x;
-        if (np > 0) u = prm.n_units > (int)gridDim.x ? (int)(gridDim.x + atomicAdd(prm.counter, 1u)) : prm.n_units;
+        int u = cta;
+        if (np > 0) u = prm.n_units > n_ctas ? (int)(n_ctas + atomicAdd(prm.counter, 1u)) : prm.n_units;
         if (u >= prm.n_units) u = -1;
         if (u >= 0) y = unit_of<KV>(u, prm);
         put_unit(unit_ring + 16 * slot, u, y);
@@ -1065,6 +1070,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
+// Tensor maps of a 128-row and of a 64-row box for each of Q, K, V and dO.
+struct Maps {
+  CUtensorMap q, k, v, g;
+};
+template <int D>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    diff_bwd_kernel(const __grid_constant__ Maps rows128, const __grid_constant__ Maps rows64,
+                    const __grid_constant__ Params kv, const __grid_constant__ Params dq, const int kv_ctas) {
+  if ((int)blockIdx.x < kv_ctas)
+    run_pass<D, true>(rows128.k, rows128.v, rows64.q, rows64.g, kv, (int)blockIdx.x, kv_ctas);
+  else
+    run_pass<D, false>(rows128.q, rows128.g, rows64.k, rows64.v, dq, (int)blockIdx.x - kv_ctas, (int)gridDim.x - kv_ctas);
+}
+
 // ------------------------------------------------------------------ host side
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1102,39 +1121,33 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
   return true;
 }
 
-template <int D, bool KV>
-static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direct, cudaStream_t st, std::string* err) {
+static int64_t fill(Params& prm, const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct) {
   const char* tb = static_cast<const char*>(a.tables);
-  Params prm{};
   prm.header = reinterpret_cast<const TablesHeader*>(tb);
   prm.tag = a.tag;
-  prm.items = reinterpret_cast<const DevItem*>(tb + (direct ? a.tl.flat_item : KV ? a.tl.kv_items : a.tl.items));
-  prm.list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : KV ? a.tl.q_list : a.tl.kv_list));
+  prm.items = reinterpret_cast<const DevItem*>(tb + (direct ? a.tl.flat_item : kv ? a.tl.kv_items : a.tl.items));
+  prm.list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : kv ? a.tl.q_list : a.tl.kv_list));
   prm.lse = a.LSE;
   prm.dsum = reinterpret_cast<const float*>(a.ws + w.dsum);
   prm.lam = static_cast<const __nv_bfloat16*>(a.lam);
-  prm.out0 = static_cast<__nv_bfloat16*>(KV ? a.dK : a.dQ);
+  prm.out0 = static_cast<__nv_bfloat16*>(kv ? a.dK : a.dQ);
   prm.out1 = static_cast<__nv_bfloat16*>(a.dV);
-  prm.part0 = direct ? nullptr : reinterpret_cast<float*>(a.ws + (KV ? w.dk_part : w.dq_part));
+  prm.part0 = direct ? nullptr : reinterpret_cast<float*>(a.ws + (kv ? w.dk_part : w.dq_part));
   prm.part1 = direct ? nullptr : reinterpret_cast<float*>(a.ws + w.dv_part);
   prm.dlam_part = reinterpret_cast<float*>(a.ws + w.dlam_part);
   prm.status = a.status;
-  prm.counter = reinterpret_cast<uint32_t*>(a.ws + w.counters) + (KV ? 0 : 64);
+  prm.counter = reinterpret_cast<uint32_t*>(a.ws + w.counters) + (kv ? 0 : 64);
   prm.S = a.S;
   prm.L = direct ? a.S : a.L;
   prm.B = a.B;
   prm.Hq = a.Hq;
   prm.Hkv = a.Hkv;
   prm.P = direct ? 1 : a.P;
-  prm.n_slots = direct ? 1 : KV ? a.n_kv_slots : a.n_slots;
+  prm.n_slots = direct ? 1 : kv ? a.n_kv_slots : a.n_slots;
   prm.n_items = prm.n_slots;
   prm.nb = (int32_t)((prm.L + BM - 1) / BM);
   prm.ns = (int32_t)((prm.L + BS - 1) / BS);
-  const int64_t units = (int64_t)prm.nb * prm.n_items * a.B * (KV ? a.Hkv : a.Hq);
-  if (units > 0x3fffffff) {
-    *err = "too many work units for one launch";
-    return (int)cudaErrorInvalidConfiguration;
-  }
+  const int64_t units = (int64_t)prm.nb * prm.n_items * a.B * (kv ? a.Hkv : a.Hq);
   prm.n_units = (int32_t)units;
   prm.causal = a.causal;
   // causal units differ in length: enough lanes together for about three times the grid, so that the last ones are short
@@ -1143,16 +1156,34 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
   prm.scale = a.scale;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
+  return units;
+}
+
+static bool make_maps(EncodeTiledFn enc, Maps* m, const DiffArgs& a, bool flat, int box_rows, bool q_side, bool kv_side,
+                      std::string* err) {
+  const uint64_t L = (uint64_t)(flat ? a.S : a.L), P = (uint64_t)(flat ? 1 : a.P);
+  const uint64_t qp = (uint64_t)a.B * a.Hq * P, kp = (uint64_t)a.B * a.Hkv * P;
+  return (!q_side || (make_map(enc, &m->q, a.Q, L, qp, a.d, box_rows, err) && make_map(enc, &m->g, a.dO, L, qp, a.d, box_rows, err))) &&
+         (!kv_side || (make_map(enc, &m->k, a.K, L, kp, a.d, box_rows, err) && make_map(enc, &m->v, a.V, L, kp, a.d, box_rows, err)));
+}
+
+template <int D>
+static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, cudaStream_t st,
+                  std::string* err) {
+  Params kv{}, dq{};
+  const int64_t kv_units = fill(kv, a, w, sms, true, kv_direct), dq_units = fill(dq, a, w, sms, false, dq_direct);
+  if (kv_units > 0x3fffffff || dq_units > 0x3fffffff) {
+    *err = "too many work units for one launch";
+    return (int)cudaErrorInvalidConfiguration;
+  }
   EncodeTiledFn enc = get_encode(err);
   if (!enc) return (int)cudaErrorNotSupported;
-  CUtensorMap r0, r1, sa, sbm;
-  const uint64_t L = (uint64_t)prm.L, qp = (uint64_t)a.B * a.Hq * prm.P, kp = (uint64_t)a.B * a.Hkv * prm.P;
-  if (!make_map(enc, &r0, KV ? a.K : a.Q, L, KV ? kp : qp, D, BM, err) ||
-      !make_map(enc, &r1, KV ? a.V : a.dO, L, KV ? kp : qp, D, BM, err) ||
-      !make_map(enc, &sa, KV ? a.Q : a.K, L, KV ? qp : kp, D, BS, err) ||
-      !make_map(enc, &sbm, KV ? a.dO : a.V, L, KV ? qp : kp, D, BS, err))
+  Maps rows128{}, rows64{};
+  // each pass in its own partitions: dkdv holds K, V and streams Q, dO; dq the other way round
+  if (!make_maps(enc, &rows128, a, kv_direct, BM, false, true, err) || !make_maps(enc, &rows64, a, kv_direct, BS, true, false, err) ||
+      !make_maps(enc, &rows128, a, dq_direct, BM, true, false, err) || !make_maps(enc, &rows64, a, dq_direct, BS, false, true, err))
     return (int)cudaErrorInvalidValue;
-  auto kern = diff_bwd_kernel<D, KV>;
+  auto kern = diff_bwd_kernel<D>;
   static OncePerDevice once;
   const int dev = OncePerDevice::device();
   cudaError_t e = cudaSuccess;
@@ -1169,10 +1200,11 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
     }
     if (e == cudaSuccess) once.mark(dev);
   }
-  // with a CTA for every unit the counter is not read
-  if (e == cudaSuccess && units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
+  // with a CTA for every unit a pass does not read its counter
+  if (e == cudaSuccess && (kv_units > sms || dq_units > sms)) e = cudaMemsetAsync(kv.counter, 0, 512, st);
   if (e == cudaSuccess) {
-    kern<<<dim3((unsigned)std::min<int64_t>(units, sms)), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(r0, r1, sa, sbm, prm);
+    const int kv_ctas = (int)std::min<int64_t>(kv_units, sms), dq_ctas = (int)std::min<int64_t>(dq_units, sms);
+    kern<<<dim3((unsigned)(kv_ctas + dq_ctas)), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(rows128, rows64, kv, dq, kv_ctas);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) *err = std::string("diff_bwd launch: ") + cudaGetErrorString(e);
@@ -1181,12 +1213,11 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
 
 }  // namespace dbtc
 
-int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct, void* stream,
+int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, void* stream,
                        std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
-  if (a.d == 128)
-    return kv ? dbtc::launch<128, true>(a, w, sms, direct, st, err) : dbtc::launch<128, false>(a, w, sms, direct, st, err);
-  return kv ? dbtc::launch<64, true>(a, w, sms, direct, st, err) : dbtc::launch<64, false>(a, w, sms, direct, st, err);
+  return a.d == 128 ? dbtc::launch<128>(a, w, sms, kv_direct, dq_direct, st, err)
+                    : dbtc::launch<64>(a, w, sms, kv_direct, dq_direct, st, err);
 }
 
 }  // namespace mesh

@@ -220,9 +220,9 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
 bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms);
 // bf16 forward on the tensor cores, with its merge where the plan's slots split the keys.
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
-// bf16 backward: dK and dV (kv), or dQ and the sums behind dlam; written as they are (direct) or as
+// bf16 backward: dK and dV, dQ and the sums behind dlam; either written as they are (direct) or as
 // partial sums per slot.
-int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct, void* stream,
+int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, void* stream,
                        std::string* err);
 // fp32 forward: Q (one map a head), K and V as bf16 pieces.
 int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err);
