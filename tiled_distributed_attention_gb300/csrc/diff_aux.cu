@@ -98,6 +98,16 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
     return;
   }
   const int64_t base[2] = {((2 * (int64_t)bh) * n_slots + s0) * L + r0, ((2 * (int64_t)bh + 1) * n_slots + s0) * L + r0};
+  // the first slot's pieces do not depend on the weights: their loads go out first
+  float4 head[PER][2];
+#pragma unroll
+  for (int k = 0; k < PER; ++k)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int idx = tid + k * THREADS, r = idx / Q4;
+      head[k][m] = r < nrows && ns > 0 ? __ldcs(reinterpret_cast<const float4*>(part_o + (base[m] + r) * D + idx % Q4 * 4))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   for (int i = tid; i < 2 * ns * ROWS; i += THREADS) {
     const int r = i % ROWS, t = i / ROWS % ns, m = i / ROWS / ns;
     w_s[m][t][r] = r < nrows ? __ldg(part_lse + base[m] + (int64_t)t * L + r) : -INFINITY;
@@ -127,10 +137,11 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
     float4 o[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      o[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float w0 = ns > 0 ? w_s[m][0][r] : 0.f;
+      o[m] = make_float4(head[k][m].x * w0, head[k][m].y * w0, head[k][m].z * w0, head[k][m].w * w0);
       const float* src = part_o + (base[m] + r) * D + c;
 #pragma unroll 4
-      for (int t = 0; t < ns; ++t) {
+      for (int t = 1; t < ns; ++t) {
         const float4 v = __ldcs(reinterpret_cast<const float4*>(src + (int64_t)t * L * D));
         const float w = w_s[m][t][r];
         o[m].x = fmaf(w, v.x, o[m].x);

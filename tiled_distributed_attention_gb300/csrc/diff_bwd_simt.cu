@@ -4,8 +4,8 @@
 // dP = dO V^T and D_m = dO . O_m,
 //   A = P_1 - lam P_2,  dS_1 = P_1 (dP - D_1),  dS_2 = -lam P_2 (dP - D_2),
 //   dV = A^T dO,  dk_m = scale dS_m^T q_m,  dq_m = scale dS_m k_m.
-// Two kernels of one shape.  A CTA of 128 threads keeps 32 resident rows of one query head (keys for
-// dK and dV, queries for dQ) and streams 64-row blocks of the other side through two cp.async
+// Two passes of one shape in one launch, the first CTAs along x for dK and dV, the others for dQ.  A CTA of
+// 128 threads keeps 32 resident rows of one query head (keys for dK and dV, queries for dQ) and streams 64-row blocks of the other side through two cp.async
 // buffers.  Per block: the 32 x 64 scores of both maps and dP, 4 x 4 a thread from 16-byte shared
 // loads (12 shared-memory wavefronts to 64 FMA instructions, so the FMA pipe is the bound); the
 // exponentials; then the products with the streamed rows, 4 rows x 4 columns a thread.
@@ -28,7 +28,8 @@ namespace dsimt {
 constexpr int RB = 32;  // resident rows
 constexpr int CB = 64;  // streamed rows
 constexpr int THREADS = 128;
-constexpr int TP = RB + 4;  // row pitch of the transposed tiles
+constexpr int TP = RB + 2;  // row pitch of the transposed tiles: their writes fall into all banks, and two CTAs
+                            // fit an SM at d = 64
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct Params {
@@ -82,9 +83,10 @@ template <int P>
 __device__ __forceinline__ void product(float (&acc)[4][4], const float* T, const float* C, int ty, int col) {
 #pragma unroll 4
   for (int c = 0; c < CB; ++c) {
-    const float4 t = *reinterpret_cast<const float4*>(T + c * TP + 4 * ty);
+    const float2 t0 = *reinterpret_cast<const float2*>(T + c * TP + 4 * ty);
+    const float2 t1 = *reinterpret_cast<const float2*>(T + c * TP + 4 * ty + 2);
     const float4 x = *reinterpret_cast<const float4*>(C + c * P + col);
-    const float tt[4] = {t.x, t.y, t.z, t.w};
+    const float tt[4] = {t0.x, t0.y, t1.x, t1.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       acc[i][0] = fmaf(tt[i], x.x, acc[i][0]);
@@ -96,7 +98,7 @@ __device__ __forceinline__ void product(float (&acc)[4][4], const float* T, cons
 }
 
 template <int D, bool KV>
-__global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p) {
+__device__ __forceinline__ void run_pass(const Params& p, int bx, int n_blocks) {
   using Sm = Smem<D>;
   constexpr int P = Sm::P, NJ = D / 64;
   extern __shared__ float4 smem4[];
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p) {
   const int h = blockIdx.y, b = blockIdx.z / p.splits, split = blockIdx.z % p.splits;
   const int group = p.Hq / p.Hkv, hk = h / group;
   const int64_t S = p.S;
-  const int rb = (int)(!KV && p.causal ? gridDim.x - 1 - blockIdx.x : blockIdx.x);  // the longest first
+  const int rb = !KV && p.causal ? n_blocks - 1 - bx : bx;  // the longest first
   const int64_t r0 = (int64_t)rb * RB;
   const int64_t qrow = ((int64_t)b * p.Hq + h) * S, krow = ((int64_t)b * p.Hkv + hk) * S;
   const int64_t vrow = ((int64_t)b * p.Hq + h) * 2 * S;  // of lse and dsum
@@ -229,6 +231,13 @@ __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params p) {
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(THREADS) bwd_kernel(const Params kv, const Params dq) {
+  const int n = (int)gridDim.x / 2;  // blocks of a pass
+  if ((int)blockIdx.x < n) run_pass<D, true>(kv, (int)blockIdx.x, n);
+  else run_pass<D, false>(dq, (int)blockIdx.x - n, n);
+}
+
 // out[head][i] = sum over the parts, in order; blockIdx.y picks one of up to three tensors
 struct SumArgs {
   const float4* part[3];
@@ -255,19 +264,19 @@ __global__ void __launch_bounds__(256) sum_parts(const SumArgs a) {
   }
 }
 
-template <int D, bool KV>
-static cudaError_t launch(const Params& p, cudaStream_t st) {
+template <int D>
+static cudaError_t launch(const Params& kv, const Params& dq, cudaStream_t st) {
   static OncePerDevice once;
   const int dev = OncePerDevice::device();
   const size_t smem = sizeof(float) * Smem<D>::FLOATS;
-  auto kern = bwd_kernel<D, KV>;
+  auto kern = bwd_kernel<D>;
   if (once.pending(dev)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     once.mark(dev);
   }
-  const dim3 grid((unsigned)((p.S + RB - 1) / RB), (unsigned)p.Hq, (unsigned)(p.B * p.splits));
-  kern<<<grid, THREADS, smem, st>>>(p);
+  const dim3 grid((unsigned)(2 * ((kv.S + RB - 1) / RB)), (unsigned)kv.Hq, (unsigned)(kv.B * kv.splits));
+  kern<<<grid, THREADS, smem, st>>>(kv, dq);
   return cudaGetLastError();
 }
 
@@ -307,14 +316,13 @@ int launch_diff_bwd_simt(const DiffArgs& a, const DiffWorkspace& w, int sms, voi
   p.scale = a.scale;
   p.scale_log2 = a.scale_log2;
   const bool q_parts = splits > 1, kv_parts = splits * group > 1;
+  Params q = p;
   p.n_part = splits * group;
   p.out0 = kv_parts ? reinterpret_cast<float*>(a.ws + w.dk_part) : static_cast<float*>(a.dK);
   p.out1 = kv_parts ? reinterpret_cast<float*>(a.ws + w.dv_part) : static_cast<float*>(a.dV);
-  cudaError_t e = a.d == 128 ? launch<128, true>(p, st) : launch<64, true>(p, st);
-  p.n_part = splits;
-  p.out0 = q_parts ? reinterpret_cast<float*>(a.ws + w.dq_part) : static_cast<float*>(a.dQ);
-  p.out1 = nullptr;
-  if (e == cudaSuccess) e = a.d == 128 ? launch<128, false>(p, st) : launch<64, false>(p, st);
+  q.n_part = splits;
+  q.out0 = q_parts ? reinterpret_cast<float*>(a.ws + w.dq_part) : static_cast<float*>(a.dQ);
+  cudaError_t e = a.d == 128 ? launch<128>(p, q, st) : launch<64>(p, q, st);
   if (e == cudaSuccess && (q_parts || kv_parts)) {
     SumArgs s{};
     int n = 0;
