@@ -335,8 +335,8 @@ int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32_t d, int32
  *   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,  dlam_h = - sum over its rows of D_2.
  * lam: lam_n device values of the inputs' type, one per query head (lam_n = Hq) or one for all
  * (lam_n = 1); dlam has the same form, a shared lam's gradient being the sum over the heads.
- * Masked keys get weight 0 in both maps; a weight of 0 still multiplies its value, so V must be
- * finite in the 128-key block of a row's last visible key. */
+ * Masked keys get weight 0 in both maps; a weight of 0 still multiplies its value, so V (and for the
+ * backward call every tensor) must be finite in the 128-row block of a row's last visible key. */
 
 /* A plan's constant tables for the device: the caller allocates mesh_attn_plan_tables_size bytes
  * of host memory, has mesh_attn_plan_tables_write fill them, and copies them once into a 16-byte
@@ -364,7 +364,8 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
                        void* workspace, size_t workspace_bytes, int32_t* d_status, void* stream);
 
 /* Backward: dQ [B, Hq, S, d], dK, dV [B, Hkv, S, d] and dlam [lam_n], all of dtype, from the
- * forward's O, O2 and LSE and the gradient dO [B, Hq, S, d]. */
+ * forward's O, O2 and LSE and the gradient dO [B, Hq, S, d].  With B, Hq or S of 0 the calls write
+ * nothing: what is left of the gradients (dlam; dK and dV where Hq = 0) is the caller's to zero. */
 int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn_dtype dtype, int32_t B,
                        int32_t Hq, int32_t Hkv, int32_t d, const void* Q, const void* K, const void* V,
                        const void* lam, int32_t lam_n, const void* O, const void* O2, const float* LSE,

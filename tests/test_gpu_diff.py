@@ -342,6 +342,86 @@ def test_wait_limit_gives_an_error_and_the_next_call_works(lib):
     assert torch.equal(O, O1)
 
 
+def test_backward_refuses_tables_of_another_plan(lib):
+    for dtype in ("bf16", "f32"):
+        q, k, v, lam, g = (t.cuda() for t in inputs(1, 1, 1, 64, 64, dtype, 37))
+        plan, other = lib.mesh_attn_plan_create(64, 1, True), lib.mesh_attn_plan_create(64, 1, False)
+        O, O2, L = lib.mesh_diff_attention(q, k, v, lam, 1, True, plan=plan, return_saved=True)
+        grads = [torch.full_like(t, 7.0) for t in (q, k, v, lam)]
+        plan._tables[torch.cuda.current_device()] = other.tables("cuda")
+        ws, st = lib.new_diff_workspace(plan, q, k, backward=True), lib.new_status()
+        lib.mesh_attn_diff_bwd(plan, q, k, v, lam, O, O2, L, g, None, *grads, ws, st)
+        assert lib.mesh_attn_read_status(st) == 1, dtype
+        for t in grads:
+            assert (t == 7).all(), dtype
+
+
+@pytest.mark.parametrize("B, Hq, Hkv, S", [(0, 2, 1, 8), (1, 0, 1, 8), (2, 2, 2, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_rows_give_zero_gradients(lib, B, Hq, Hkv, S, dtype):
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    q = torch.ones(B, Hq, S, 64, dtype=t, device="cuda")
+    k = torch.ones(B, Hkv, S, 64, dtype=t, device="cuda")
+    lam = torch.ones(max(Hq, 1), dtype=t, device="cuda")
+    O, O2, L = lib.mesh_diff_attention(q, k, k, lam, 1, True, return_saved=True)
+    junk = [torch.full((64,), float("nan"), dtype=t, device="cuda") for _ in range(64)]
+    del junk  # what the gradients' memory may hold
+    for a in lib.mesh_diff_attention_backward(q, k, k, lam, O, O2, L, torch.ones_like(q), 1, True):
+        assert (a == 0).all()
+
+
+def test_dropped_plan_keeps_its_tables_until_another_stream_has_read_them(lib):
+    q, k, v, lam, _ = (t.cuda() for t in inputs(1, 2, 1, 200, 64, "bf16", 38))
+    plan = lib.mesh_attn_plan_create(200, 4, True)
+    O, _ = lib.mesh_diff_attention(q, k, v, lam, 4, True, plan=plan)
+    at, n = plan.tables("cuda").data_ptr(), plan.tables("cuda").numel()
+    ws, st = lib.new_diff_workspace(plan, q, k), lib.new_status()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        late, _ = lib.mesh_diff_attention(q, k, v, lam, 4, True, plan=plan, workspace=ws, status=st, check_status=False)
+    del plan
+    others = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    assert not s.query() and all(t.data_ptr() != at for t in others)
+    torch.cuda.synchronize()
+    assert lib.mesh_attn_read_status(st) == 0 and torch.equal(O, late)
+
+
+def test_captured_autograd_step(lib):
+    """torch.autograd.grad of both wrappers inside a graph: the plan and its tables exist before, and nothing waits."""
+    rope = lib.MeshRope(64, (16,), groups=2)
+    pos = torch.arange(130, device="cuda")
+    plan = lib.mesh_attn_plan_create(130, 1, True)
+    plan.tables("cuda")
+
+    def step(q, k, v, lam, g):
+        a, b = lib.mesh_rope_autograd(q, k, pos, rope)
+        O, _ = lib.mesh_diff_attention_autograd(a, b, v, lam, 1, True, plan=plan, check_status=False)
+        return (O.detach(), *torch.autograd.grad(O, (q, k, v, lam), g))
+
+    def fresh(seed):
+        return [t.cuda().requires_grad_(i < 4) for i, t in enumerate(inputs(1, 2, 1, 130, 64, "bf16", seed))]
+
+    bufs, new = fresh(39), fresh(40)
+    want = step(*new)
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(*bufs)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(*bufs)
+    with torch.no_grad():
+        for b, x in zip(bufs, new):
+            b.copy_(x)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ single tokens over a cache
 
 DECODE = [  # B, Hq, Hkv, d, T, lens
@@ -395,6 +475,15 @@ def test_decode_workspace_of_larger_sizes(lib):
         lens = torch.full((B,), T, dtype=torch.int32)
         O, L = lib.mesh_diff_decode(q.cuda(), k.cuda(), v.cuda(), lens.cuda(), lam.cuda(), workspace=ws)
         check_out(O, L, OD.forward(q, k, v, lam, False, lens=lens), "bf16", T)
+
+
+def test_decode_of_an_empty_cache(lib):
+    for dtype in (torch.bfloat16, torch.float32):
+        q = torch.ones(2, 4, 1, 64, dtype=dtype, device="cuda")
+        cache = torch.empty(2, 2, 0, 64, dtype=dtype, device="cuda")
+        O, L = lib.mesh_diff_decode(q, cache, cache, torch.zeros(2, dtype=torch.int32, device="cuda"),
+                                    torch.ones(4, dtype=dtype, device="cuda"))
+        assert (O == 0).all() and (L == -math.inf).all()
 
 
 def test_decode_lengths_out_of_range_are_reported(lib):

@@ -145,6 +145,7 @@ class Plan:
         _check(_lib.mesh_attn_plan_get_info(self._h, ctypes.byref(info)), "mesh_attn_plan_get_info")
         self.info = info
         self._tables: Dict[int, torch.Tensor] = {}
+        self._tables_stream: Dict[int, int] = {}  # the stream that owns their memory
 
     @property
     def handle(self):
@@ -166,6 +167,7 @@ class Plan:
             _check(_lib.mesh_attn_plan_tables_write(self._h, _ptr(host), n.value), "mesh_attn_plan_tables_write")
             got = host.to(torch.device("cuda", index))
             torch.cuda.current_stream(index).synchronize()
+            self._tables_stream[index] = torch.cuda.current_stream(index).cuda_stream
             self._tables[index] = got
         return got
 
@@ -789,6 +791,15 @@ def _diff_plan_check(plan: Plan, q, k):
         raise ValueError(f"the plan is for S = {S}; q has {q.shape[2]} tokens, k and v {k.shape[2]}")
 
 
+def _tables_for(plan: Plan, index: int, stream) -> int:
+    """Pointer of the plan's tables for a call on `stream`.  Where that is not the stream that owns their memory, the
+    memory stays theirs until the call has run, though the plan may be dropped before."""
+    tables = plan.tables(index)
+    if _raw_stream(index, stream) != plan._tables_stream.get(index):
+        tables.record_stream(torch.cuda.current_stream(index) if stream is None else stream)
+    return tables.data_ptr()
+
+
 def mesh_attn_diff_fwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
                        scale: Optional[float], O: torch.Tensor, O2: Optional[torch.Tensor], LSE: torch.Tensor,
                        workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
@@ -805,7 +816,7 @@ def _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, s
     _contiguous(q, k, v, lam)
     _diff_plan_check(plan, q, k)
     B, Hq, S, d = q.shape
-    _on_device(index, "mesh_attn_diff_fwd", _lib.mesh_attn_diff_fwd, plan.handle, plan.tables(index).data_ptr(),
+    _on_device(index, "mesh_attn_diff_fwd", _lib.mesh_attn_diff_fwd, plan.handle, _tables_for(plan, index, stream),
                _dtype_code(q.dtype), B, Hq, k.shape[1], d, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
                lam.shape[0], _diff_scale(scale, d), O.data_ptr(), None if O2 is None else O2.data_ptr(), LSE.data_ptr(),
                workspace.data_ptr(), workspace.numel() * workspace.element_size(), status.data_ptr(),
@@ -831,7 +842,12 @@ def _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, works
         raise ValueError("O, O2 and dO must have q's shape, LSE must be fp32 [B, Hq, 2, S] on q's device")
     _contiguous(q, k, v, lam, O, O2, LSE, dO)
     _diff_plan_check(plan, q, k)
-    _on_device(index, "mesh_attn_diff_bwd", _lib.mesh_attn_diff_bwd, plan.handle, plan.tables(index).data_ptr(),
+    if not q.numel():  # no rows: sums over nothing
+        with torch.cuda.stream(stream):
+            for t in (dK, dV, dlam):
+                t.zero_()
+        return
+    _on_device(index, "mesh_attn_diff_bwd", _lib.mesh_attn_diff_bwd, plan.handle, _tables_for(plan, index, stream),
                _dtype_code(q.dtype), B, Hq, k.shape[1], d, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
                lam.shape[0], O.data_ptr(), O2.data_ptr(), LSE.data_ptr(), dO.data_ptr(), _diff_scale(scale, d),
                dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dlam.data_ptr(), workspace.data_ptr(),

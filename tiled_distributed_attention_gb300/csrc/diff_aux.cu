@@ -176,6 +176,9 @@ __device__ __forceinline__ void dot16(uint4 x, uint4 y, float& acc) {
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* dsum, float* dlam_part, int64_t n_part) {
   constexpr int LANES = D * (int)sizeof(T) / 16, AT_ONCE = THREADS / LANES, PASSES = PREP_ROWS / AT_ONCE;
+  const TablesHeader* th = static_cast<const TablesHeader*>(a.tables);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
+    record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);  // another plan's tables: the launches behind do nothing
   if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
   const int64_t part = blockIdx.x % n_part, bh = blockIdx.x / n_part;
   const float lam = lam_of<T>(a.lam, a.lam_n, (int)(bh % a.Hq));

@@ -78,8 +78,6 @@ constexpr uint32_t COL_Q = 384;   // dq: Q [D / 2], then dO [D / 2] (bf16)
 __device__ __forceinline__ uint32_t ds_col(int m, int kk) { return (uint32_t)((kk >> 1) * 32 + m * 16 + (kk & 1) * 8); }
 
 struct Params {
-  const TablesHeader* header;
-  uint64_t tag;
   const DevItem* items;  // rows: {p, slot, kv_off, n_kv}, or columns: {k, kv slot, q_off, n_q}
   const int32_t* list;
   const float* lse;   // [B, Hq, 2, S]
@@ -875,11 +873,6 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
     } else if (warp == WARP_LOAD && lane == 0) {
       // ================================================================ producer
       bool ok = run;
-      if (ok && (prm.header->magic != TABLES_MAGIC || prm.header->tag != prm.tag)) {  // another plan's tables
-        record_error(prm.status, MESH_ATTN_ERR_INVALID_ARG, ROLE_LOAD, 0);
-        *abort_flag = 1;
-        ok = false;
-      }
       int np = 0;  // units published
       auto publish = [&](Unit& y) -> int {  // a CTA's first unit is its own index, the others come from the counter
         const int slot = np & 1;
@@ -1123,8 +1116,6 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
 
 static int64_t fill(Params& prm, const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct) {
   const char* tb = static_cast<const char*>(a.tables);
-  prm.header = reinterpret_cast<const TablesHeader*>(tb);
-  prm.tag = a.tag;
   prm.items = reinterpret_cast<const DevItem*>(tb + (direct ? a.tl.flat_item : kv ? a.tl.kv_items : a.tl.items));
   prm.list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : kv ? a.tl.q_list : a.tl.kv_list));
   prm.lse = a.LSE;
