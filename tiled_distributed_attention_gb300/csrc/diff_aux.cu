@@ -1,5 +1,6 @@
 // Differential attention, the passes around its products: fp32 inputs split into bf16 pieces, the merge of
-// the two maps' partial outputs, the row terms of the backward pass and the gradient of lam.  All are bound by memory and read and write whole 16-byte pieces.
+// the two maps' partial outputs, the row terms of the backward pass and the gradient of lam.  All are
+// bound by memory and read and write whole 16-byte pieces.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

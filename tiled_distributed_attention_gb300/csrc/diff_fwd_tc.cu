@@ -12,13 +12,20 @@
 // pass) rounded once; no partial output leaves the SM.
 //
 // A work unit is (batch, KV head, work item, query head of the group, 128-row query tile); causal units
-// go heaviest first within batches of heads that fill the grid a few times (Params::batch).  The work item is the whole sequence where its tiles alone fill the GPU; with
-// fewer the plan's items split the keys, and normalised partial outputs and LSEs of both maps go
-// to the merge (launch_diff_fwd_tc).
+// go heaviest first within batches of heads that fill the grid a few times (Params::batch).  The work
+// item is the whole sequence where its tiles alone fill the GPU; with fewer the plan's items split the
+// keys, and normalised partial outputs and LSEs of both maps go to the merge (launch_diff_fwd_tc).
 //
 // Per 128 x 128 block and head: 2 x 4 score products and 2 x 8 PV products of 64 cycles each at
 // d = 128 (1,536 cycles), 32,768 exponentials.  P is rounded to bf16 for its product (2^-9 relative
 // a term), everything else is fp32.
+//
+// Measured (d = 128, 16 heads, 16,384 tokens): causal 1.10 ms, 1,500 TFLOP/s; without a mask, on 4 KV heads,
+// 2.15 ms, 1,530 TFLOP/s (0.81 of the bf16 burst rate).  Bound by the softmax warps: a block takes them
+// 2,350-2,450 cycles for its 1,536 cycles of products; an exponential costs 3.84 cycles a warp and
+// sub-partition, and the products' issue takes dispatch slots from the sub-partition of the MMA warp.
+// Slower (no mask): two warps a row 2.70 ms, 64-key steps with two score buffers a map 2.70 ms, P handed
+// over in halves 2.53 ms.
 //
 // Persistent grid, one CTA per SM; warps 0-7 softmax, warp 8 MMA issuer, warp 9 producer, warps 10-11
 // idle.  TMEM (512 columns): S_1 | S_2 | O_1 | O_2; P_m overwrites S_m.  K, V and Q tiles come by
