@@ -669,18 +669,32 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
     a = _passed.get(key)
     if a is None:
         a = _remember(key, _rope_args(rope, q, k, positions, q_out, k_out))
+    _rope(rope, a, index, q.data_ptr(), kp, positions, q_out.data_ptr(), ko, 1 if inverse else 0, stream)
+
+
+def _rope(rope, a, index, qp, kp, positions, qo, ko, inverse, stream=None):
     dt, B, S, d, Hq, qs, qos, Hk, ks, kos, bits, ps = a
-    _on_device(index, "mesh_attn_rope", _lib.mesh_attn_rope, dt, B, S, d, Hq, q.data_ptr(), qs, q_out.data_ptr(), qos, Hk, kp, ks,
-               ko, kos, rope.groups, rope.n_pairs, rope.n_axes, rope._freq, rope._axis, rope._adjacent, 1 if inverse else 0,
-               positions.data_ptr(), bits, ps, _raw_stream(index, stream))
+    _on_device(index, "mesh_attn_rope", _lib.mesh_attn_rope, dt, B, S, d, Hq, qp, qs, qo, qos, Hk, kp, ks, ko, kos, rope.groups,
+               rope.n_pairs, rope.n_axes, rope._freq, rope._axis, rope._adjacent, inverse, positions.data_ptr(), bits, ps,
+               _raw_stream(index, stream))
 
 
 def mesh_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
     """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) with their positions, as dense [B, H, S, d] tensors, which is what
     the attention calls take; q and k may be views, e.g. a projection's [B, S, H, d] transposed."""
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    mesh_attn_rope(rope, q, k, positions, q_out, k_out)
+    shape, dtype, device = q.shape, q.dtype, q.device
+    q_out = torch.empty(shape, dtype=dtype, device=device)
+    if k is None:
+        mesh_attn_rope(rope, q, None, positions, q_out, None)
+        return q_out, None
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+    # the outputs follow from the inputs, so what is checked, and remembered, is less than mesh_attn_rope's
+    key = (rope, shape, q.stride(), dtype, k.shape, k.stride(), k.dtype, positions.shape, positions.stride(), positions.dtype)
+    index = _one_device(q, k, positions)
+    a = _passed.get(key)
+    if a is None:
+        a = _remember(key, _rope_args(rope, q, k, positions, q_out, k_out))
+    _rope(rope, a, index, q.data_ptr(), k.data_ptr(), positions, q_out.data_ptr(), k_out.data_ptr(), 0)
     return q_out, k_out
 
 
@@ -737,16 +751,14 @@ def _diff_scale(scale: Optional[float], d: int) -> float:
     return 1.0 / math.sqrt(d // 2) if scale is None else float(scale)
 
 
-def _diff_check(q, k, v, lam, *more):
-    """(B, Hq, S, d, device) of matching tensors of one dtype on one device."""
+def _diff_sizes(q, k, v, lam):
+    """(dtype code, B, Hq, S, d, Hkv, values in lam, LSE's shape) of q, k, v and lam that fit together; k's and v's strides and
+    q's length are the caller's to check."""
+    key = (q.shape, k.shape, v.shape, lam.shape, q.dtype, k.dtype, v.dtype, lam.dtype, q.stride(), lam.stride())
+    a = _passed.get(key)
+    if a is not None:
+        return a
     qs, ks, ls = q.shape, k.shape, lam.shape
-    dtype = q.dtype
-    key = (qs, ks, v.shape, ls, dtype, k.dtype, v.dtype, lam.dtype)
-    if key in _passed:
-        for t in more:
-            if t.dtype != dtype:
-                raise ValueError("q, k, v, lam and the gradients must be of one dtype")
-        return (*qs, _one_device(q, k, v, lam, *more))
     if len(qs) != 4 or len(ks) != 4 or v.shape != ks:
         raise ValueError("q must be [B, Hq, S, d], k and v [B, Hkv, S, d]")
     B, Hq, S, d = qs
@@ -756,12 +768,26 @@ def _diff_check(q, k, v, lam, *more):
         raise ValueError(f"Hq must be a multiple of Hkv: {Hq} and {ks[1]}")
     if len(ls) != 1 or (ls[0] != Hq and ls[0] != 1):
         raise ValueError("lam must be [Hq], or [1] for one value for all heads")
-    for t in (k, v, lam) + more:
-        if t.dtype != dtype:
-            raise ValueError("q, k, v, lam and the gradients must be of one dtype")
-    index = _one_device(q, k, v, lam, *more)
-    _remember(key, True)
-    return B, Hq, S, d, index
+    if not q.dtype == k.dtype == v.dtype == lam.dtype:
+        raise ValueError("q, k, v and lam must be of one dtype")
+    _contiguous(q, lam)
+    return _remember(key, (_dtype_code(q.dtype), B, Hq, S, d, ks[1], ls[0], (B, Hq, 2, S)))
+
+
+def _contiguous(*ts):
+    for t in ts:
+        if not t.is_contiguous():
+            raise ValueError("q, k, v, lam, the gradients and the outputs must be contiguous")
+
+
+def _like(q, *ts):
+    """ts are as q: contiguous, of its shape and dtype."""
+    shape, dtype = q.shape, q.dtype
+    for t in ts:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError("O, O2 and dO must have q's shape and dtype, dQ, dK, dV and dlam those of q, k, v and lam")
+        if not t.is_contiguous():
+            raise ValueError("q, k, v, lam, the gradients and the outputs must be contiguous")
 
 
 def mesh_attn_diff_workspace_size(plan: Plan, dtype: torch.dtype, B: int, Hq: int, Hkv: int, d: int,
@@ -777,12 +803,6 @@ def new_diff_workspace(plan: Plan, q: torch.Tensor, k: torch.Tensor, backward: b
     B, Hq, _, d = q.shape
     n = mesh_attn_diff_workspace_size(plan, q.dtype, B, Hq, k.shape[1], d, backward)
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-
-
-def _contiguous(*ts):
-    for t in ts:
-        if not t.is_contiguous():
-            raise ValueError("q, k, v, lam, the gradients and the outputs must be contiguous")
 
 
 def _diff_plan_check(plan: Plan, q, k):
@@ -803,55 +823,54 @@ def _tables_for(plan: Plan, index: int, stream) -> int:
 def mesh_attn_diff_fwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
                        scale: Optional[float], O: torch.Tensor, O2: Optional[torch.Tensor], LSE: torch.Tensor,
                        workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    a = _diff_sizes(q, k, v, lam)
     outs = (O,) if O2 is None else (O, O2)
-    B, Hq, S, d, index = _diff_check(q, k, v, lam, *outs)
-    if any(t.shape != q.shape for t in outs) or LSE.shape != (B, Hq, 2, S) or LSE.dtype != torch.float32:
-        raise ValueError("O and O2 must have q's shape, LSE must be fp32 [B, Hq, 2, S]")
-    _one_device(q, LSE, workspace, status)
-    _contiguous(LSE, *outs)
-    _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream)
+    _like(q, *outs)
+    if LSE.shape != a[7] or LSE.dtype != torch.float32:
+        raise ValueError("LSE must be fp32 [B, Hq, 2, S]")
+    _contiguous(LSE)
+    index = _one_device(q, k, v, lam, LSE, workspace, status, *outs)
+    _diff_fwd(a, plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream)
 
 
-def _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream=None):
-    _contiguous(q, k, v, lam)
+def _diff_fwd(a, plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream=None):
+    dt, B, Hq, S, d, Hkv, n, _ = a
+    _contiguous(k, v)
     _diff_plan_check(plan, q, k)
-    B, Hq, S, d = q.shape
-    _on_device(index, "mesh_attn_diff_fwd", _lib.mesh_attn_diff_fwd, plan.handle, _tables_for(plan, index, stream),
-               _dtype_code(q.dtype), B, Hq, k.shape[1], d, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
-               lam.shape[0], _diff_scale(scale, d), O.data_ptr(), None if O2 is None else O2.data_ptr(), LSE.data_ptr(),
-               workspace.data_ptr(), workspace.numel() * workspace.element_size(), status.data_ptr(),
-               _raw_stream(index, stream))
+    _on_device(index, "mesh_attn_diff_fwd", _lib.mesh_attn_diff_fwd, plan._h, _tables_for(plan, index, stream), dt, B, Hq, Hkv, d,
+               q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), n, _diff_scale(scale, d), O.data_ptr(),
+               None if O2 is None else O2.data_ptr(), LSE.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+               status.data_ptr(), _raw_stream(index, stream))
 
 
 def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, O: torch.Tensor,
                        O2: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, scale: Optional[float], dQ: torch.Tensor,
                        dK: torch.Tensor, dV: torch.Tensor, dlam: torch.Tensor, workspace: torch.Tensor,
                        status: torch.Tensor, stream=None) -> None:
-    index = _diff_check(q, k, v, lam, O, O2, dO, dQ, dK, dV, dlam)[4]
-    if dQ.shape != q.shape or dK.shape != k.shape or dV.shape != v.shape or dlam.shape != lam.shape:
-        raise ValueError("dQ, dK, dV and dlam must have the shapes of q, k, v and lam")
-    _one_device(q, workspace, status)
-    _contiguous(dQ, dK, dV, dlam)
-    _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream)
+    a = _diff_sizes(q, k, v, lam)
+    _like(q, dQ)
+    _like(k, dK, dV)
+    _like(lam, dlam)
+    index = _one_device(q, k, v, lam, O, O2, LSE, dO, dQ, dK, dV, dlam, workspace, status)
+    _diff_bwd(a, plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream)
 
 
-def _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream=None):
-    B, Hq, S, d = q.shape
-    if O.shape != q.shape or O2.shape != q.shape or dO.shape != q.shape or LSE.shape != (B, Hq, 2, S) or \
-            LSE.dtype != torch.float32 or LSE.get_device() != index:
-        raise ValueError("O, O2 and dO must have q's shape, LSE must be fp32 [B, Hq, 2, S] on q's device")
-    _contiguous(q, k, v, lam, O, O2, LSE, dO)
+def _diff_bwd(a, plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream=None):
+    dt, B, Hq, S, d, Hkv, n, lse_shape = a
+    _like(q, O, O2, dO)
+    if LSE.shape != lse_shape or LSE.dtype != torch.float32:
+        raise ValueError("LSE must be fp32 [B, Hq, 2, S]")
+    _contiguous(k, v, LSE)
     _diff_plan_check(plan, q, k)
-    if not q.numel():  # no rows: sums over nothing
+    if not B * Hq * S:  # no rows: sums over nothing
         with torch.cuda.stream(stream):
             for t in (dK, dV, dlam):
                 t.zero_()
         return
-    _on_device(index, "mesh_attn_diff_bwd", _lib.mesh_attn_diff_bwd, plan.handle, _tables_for(plan, index, stream),
-               _dtype_code(q.dtype), B, Hq, k.shape[1], d, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
-               lam.shape[0], O.data_ptr(), O2.data_ptr(), LSE.data_ptr(), dO.data_ptr(), _diff_scale(scale, d),
-               dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dlam.data_ptr(), workspace.data_ptr(),
-               workspace.numel() * workspace.element_size(), status.data_ptr(), _raw_stream(index, stream))
+    _on_device(index, "mesh_attn_diff_bwd", _lib.mesh_attn_diff_bwd, plan._h, _tables_for(plan, index, stream), dt, B, Hq, Hkv, d,
+               q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), n, O.data_ptr(), O2.data_ptr(), LSE.data_ptr(),
+               dO.data_ptr(), _diff_scale(scale, d), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dlam.data_ptr(),
+               workspace.data_ptr(), workspace.nbytes, status.data_ptr(), _raw_stream(index, stream))
 
 
 def _raise_status(status: torch.Tensor):
@@ -872,15 +891,18 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     mesh_diff_attention_backward takes.  A program that calls it every step keeps plan, workspace
     (new_diff_workspace) and status (new_status) and passes check_status=False, which leaves out the wait.
     """
-    B, Hq, S, d, index = _diff_check(q, k, v, lam)
-    plan = plan or mesh_attn_plan_create(S, P, causal, kvr, greedy)
+    a = _diff_sizes(q, k, v, lam)
+    index = _one_device(q, k, v, lam)
+    device = q.device
+    plan = plan or mesh_attn_plan_create(a[3], P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k) if workspace is None else workspace
-    st = new_status(q.device) if status is None else status
-    _one_device(q, ws, st)
+    st = new_status(device) if status is None else status
+    if ws.get_device() != index or st.get_device() != index:
+        _one_device(q, ws, st)
     O = torch.empty_like(q)
     O2 = torch.empty_like(q) if return_saved else None
-    LSE = torch.empty((B, Hq, 2, S), dtype=torch.float32, device=q.device)
-    _diff_fwd(plan, q, k, v, lam, scale, O, O2, LSE, ws, st, index)
+    LSE = torch.empty(a[7], dtype=torch.float32, device=device)
+    _diff_fwd(a, plan, q, k, v, lam, scale, O, O2, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
     return (O, O2, LSE) if return_saved else (O, LSE)
@@ -892,13 +914,15 @@ def mesh_diff_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                                  plan: Optional[Plan] = None, workspace: Optional[torch.Tensor] = None,
                                  status: Optional[torch.Tensor] = None, check_status: bool = True):
     """(dQ, dK, dV, dlam) from the forward's O, O2 and LSE and the gradient dO, on the current stream."""
-    B, Hq, S, d, index = _diff_check(q, k, v, lam, O, O2, dO)
-    plan = plan or mesh_attn_plan_create(S, P, causal, kvr, greedy)
+    a = _diff_sizes(q, k, v, lam)
+    index = _one_device(q, k, v, lam, O, O2, LSE, dO)
+    plan = plan or mesh_attn_plan_create(a[3], P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k, backward=True) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
-    _one_device(q, ws, st)
+    if ws.get_device() != index or st.get_device() != index:
+        _one_device(q, ws, st)
     grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(lam))
-    _diff_bwd(plan, q, k, v, lam, O, O2, LSE, dO, scale, *grads, ws, st, index)
+    _diff_bwd(a, plan, q, k, v, lam, O, O2, LSE, dO, scale, *grads, ws, st, index)
     if check_status:
         _raise_status(st)
     return grads
@@ -946,28 +970,39 @@ def mesh_attn_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                           lam: torch.Tensor, scale: Optional[float], O: torch.Tensor, LSE: torch.Tensor,
                           workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
     load_library()
-    B, Hq, S, d, index = _diff_check(q, k_cache, v_cache, lam, O)
-    if O.shape != q.shape or LSE.shape != (B, Hq, 2, 1) or LSE.dtype != torch.float32:
-        raise ValueError("O must have q's shape, LSE must be fp32 [B, Hq, 2, 1]")
-    _contiguous(O, LSE)
-    _one_device(q, LSE, workspace, status)
-    _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream)
+    a = _diff_decode_sizes(q, k_cache, v_cache, lens, lam)
+    _like(q, O)
+    if LSE.shape != a[9] or LSE.dtype != torch.float32:
+        raise ValueError("LSE must be fp32 [B, Hq, 2, 1]")
+    _contiguous(LSE)
+    index = _one_device(q, k_cache, v_cache, lens, lam, O, LSE, workspace, status)
+    _diff_decode(a, q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream)
 
 
-def _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream=None):
-    B, Hq, S, d = q.shape
+def _diff_decode_sizes(q, k_cache, v_cache, lens, lam):
+    """(dtype code, B, Hq, Hkv, d, T, k's strides, v's strides, values in lam, LSE's shape) of tensors that fit together."""
+    key = (q.shape, k_cache.shape, v_cache.shape, lam.shape, lens.shape, q.dtype, k_cache.dtype, v_cache.dtype, lam.dtype,
+           lens.dtype, q.stride(), k_cache.stride(), v_cache.stride(), lam.stride(), lens.stride())
+    a = _passed.get(key)
+    if a is not None:
+        return a
+    dt, B, Hq, S, d, Hkv, n, _ = _diff_sizes(q, k_cache, v_cache, lam)
     T = k_cache.shape[2]
     if S != 1:
         raise ValueError("q must hold one token a sequence: [B, Hq, 1, d]")
-    if lens.shape != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous() or lens.get_device() != index:
-        raise ValueError("lens must be contiguous int32 [B] on q's device")
-    _contiguous(q, lam)
+    if lens.shape != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous():
+        raise ValueError("lens must be contiguous int32 [B]")
     if (k_cache.stride(3) != 1 or v_cache.stride(3) != 1) and T:
         raise ValueError("the columns of the caches must be consecutive")
-    _on_device(index, "mesh_attn_diff_decode", _lib.mesh_attn_diff_decode, _dtype_code(q.dtype), B, Hq, k_cache.shape[1], d, T,
-               q.data_ptr(), k_cache.data_ptr(), _strides3(k_cache), v_cache.data_ptr(), _strides3(v_cache), lens.data_ptr(),
-               lam.data_ptr(), lam.shape[0], _diff_scale(scale, d), O.data_ptr(), LSE.data_ptr(), workspace.data_ptr(),
-               workspace.numel() * workspace.element_size(), status.data_ptr(), _raw_stream(index, stream))
+    return _remember(key, (dt, B, Hq, Hkv, d, T, _strides3(k_cache), _strides3(v_cache), n, (B, Hq, 2, 1)))
+
+
+def _diff_decode(a, q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream=None):
+    dt, B, Hq, Hkv, d, T, ks, vs, n, _ = a
+    _on_device(index, "mesh_attn_diff_decode", _lib.mesh_attn_diff_decode, dt, B, Hq, Hkv, d, T, q.data_ptr(),
+               k_cache.data_ptr(), ks, v_cache.data_ptr(), vs, lens.data_ptr(), lam.data_ptr(), n, _diff_scale(scale, d),
+               O.data_ptr(), LSE.data_ptr(), workspace.data_ptr(), workspace.nbytes, status.data_ptr(),
+               _raw_stream(index, stream))
 
 
 def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor, lam: torch.Tensor,
@@ -978,13 +1013,14 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     multiples).  Returns O [B, Hq, 1, d] and LSE [B, Hq, 2, 1].  A serving loop keeps workspace
     (new_diff_decode_workspace) and status and passes check_status=False."""
     load_library()
-    B, Hq, S, d, index = _diff_check(q, k_cache, v_cache, lam)
-    ws = new_diff_decode_workspace(B, Hq, k_cache.shape[1], d, k_cache.shape[2], q.device) if workspace is None else workspace
-    st = new_status(q.device) if status is None else status
-    _one_device(q, ws, st)
-    O = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    LSE = torch.empty((B, Hq, 2, 1), dtype=torch.float32, device=q.device)
-    _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, index)
+    a = _diff_decode_sizes(q, k_cache, v_cache, lens, lam)
+    device = q.device
+    ws = new_diff_decode_workspace(a[1], a[2], a[3], a[4], a[5], device) if workspace is None else workspace
+    st = new_status(device) if status is None else status
+    index = _one_device(q, k_cache, v_cache, lens, lam, ws, st)
+    O = torch.empty_like(q)
+    LSE = torch.empty(a[9], dtype=torch.float32, device=device)
+    _diff_decode(a, q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, index)
     if check_status:
         _raise_status(st)
     return O, LSE
