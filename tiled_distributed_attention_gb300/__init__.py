@@ -9,9 +9,9 @@ fallback: if the library is missing, load_library() raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
+import struct
 from typing import Dict, Optional, Sequence, Tuple
 
 import torch
@@ -30,6 +30,7 @@ STATUS_NAMES = {
 }
 
 _lib: Optional[ctypes.CDLL] = None
+_ext = None  # _binding.so: the calls of rotary positions and differential attention
 
 c_i32, c_i64, c_sz, c_f32, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_void_p
 P_i32 = ctypes.POINTER(c_i32)
@@ -98,7 +99,7 @@ class MeshAttnError(RuntimeError):
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libmesh_attn.so (built by __graft_entry__.build()) and declare its signatures."""
-    global _lib
+    global _lib, _ext
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -108,6 +109,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    from . import _binding
+    _binding.bind(*(ctypes.cast(getattr(lib, name), c_vp).value for name in (
+        "mesh_attn_rope", "mesh_attn_diff_fwd", "mesh_attn_diff_bwd", "mesh_attn_diff_decode")))
+    _ext = _binding
     _lib = lib
     return lib
 
@@ -146,6 +151,7 @@ class Plan:
         self.info = info
         self._tables: Dict[int, torch.Tensor] = {}
         self._tables_stream: Dict[int, int] = {}  # the stream that owns their memory
+        self._native = (handle.value, info.S, self._tables, self._tables_stream)  # what _binding takes
 
     @property
     def handle(self):
@@ -557,98 +563,12 @@ class MeshRope:
             raise ValueError("freq must give a frequency for each pair")
         self.d, self.groups, self.style, self.n_axes, self.n_pairs = int(d), int(groups), style, len(sections), n
         self.freq, self.axis = tuple(freq), tuple(axis)
-        self._freq = (ctypes.c_double * n)(*freq)
-        self._axis = (c_i32 * n)(*axis)
-        self._adjacent = int(style == "adjacent")
+        # what _binding takes: a header, the frequencies, the axes
+        self._native = struct.pack(f"=6i{n}d{n}i", d, groups, n, len(sections), int(style == "adjacent"), 0, *freq, *axis)
 
 
-@functools.lru_cache(maxsize=1024)
-def _i64x3(a: int, b: int, c: int):
-    return (c_i64 * 3)(a, b, c)
-
-
-def _strides3(t: torch.Tensor):
-    st = t.stride()
-    return _i64x3(st[0], st[1], st[2])
-
-
-def _one_device(*ts) -> int:
-    """The CUDA device all tensors are on."""
-    index = ts[0].get_device()
-    for t in ts:
-        if t.get_device() != index:
-            index = -1
-    if index < 0 or not ts[0].is_cuda:
-        raise ValueError("tensors must be on one CUDA device; got " + ", ".join(str(t.device) for t in ts))
-    return index
-
-
-# Sizes, strides and types that have passed a call's checks: a program repeats them step after step, and the
-# checks cost more than a short kernel.  Holds no tensor and nothing of their contents.
-_passed: Dict[tuple, object] = {}
-
-
-def _remember(key: tuple, value):
-    if len(_passed) >= 4096:
-        _passed.clear()
-    _passed[key] = value
-    return value
-
-
-# A step of a small model is shorter than a few Python calls, so the calls below take the current device
-# and stream by index and pass plain integers, which is several times quicker than the objects.
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-
-
-def _raw_stream(index: int, stream) -> int:
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
-
-def _on_device(index: int, where: str, fn, *args) -> None:
-    """fn(*args), a C entry point, with the tensors' device current."""
-    if _current_device() == index:
-        rc = fn(*args)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args)
-    if rc:
-        _check(rc, where)
-
-
-def _rope_args(rope: MeshRope, q, k, positions, q_out, k_out):
-    """Checks of mesh_attn_rope, and its arguments that follow from sizes, strides and types."""
-    load_library()
-    if q.dim() != 4 or q.shape[3] != rope.d:
-        raise ValueError(f"q must be [B, H, S, {rope.d}]")
-    B, Hq, S, d = q.shape
-    pairs = ((q, q_out),) if k is None else ((q, q_out), (k, k_out))
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out go together")
-    dtype = q.dtype
-    for x, y in pairs:
-        shape = x.shape
-        if len(shape) != 4 or shape[0] != B or shape[2] != S or shape[3] != d:
-            raise ValueError("q and k must agree in batch, tokens and columns")
-        if y.shape != shape:
-            raise ValueError("an output must have its input's shape")
-        if x.dtype != dtype or y.dtype != dtype:
-            raise ValueError("q, k and the outputs must be of one dtype")
-        if (x.stride(3) != 1 or y.stride(3) != 1) and x.numel():
-            raise ValueError("the columns of a head must be consecutive")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise ValueError("positions must be int32 or int64")
-    pos = positions
-    if rope.n_axes == 1 and (pos.dim() == 1 or (pos.dim() == 2 and pos.shape[0] != 1)):
-        pos = pos.unsqueeze(0)
-    if pos.dim() == 2:
-        pos = pos.unsqueeze(1)
-    if pos.dim() != 3 or pos.shape[0] != rope.n_axes or pos.shape[1] not in (1, B) or pos.shape[2] != S:
-        raise ValueError(f"positions must be [{rope.n_axes}, S] or [{rope.n_axes}, B, S] with B = {B}, S = {S}; got "
-                         f"{tuple(positions.shape)}")
-    ps = pos.stride()
-    return (_dtype_code(dtype), B, S, d, Hq, _strides3(q), _strides3(q_out), 0 if k is None else k.shape[1],
-            None if k is None else _strides3(k), None if k is None else _strides3(k_out), 8 * pos.element_size(),
-            _i64x3(ps[0], ps[1] if pos.shape[1] != 1 else 0, ps[2]))
+def _handle_of(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
@@ -656,58 +576,31 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
     """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) rotated into q_out and k_out; views with any batch,
     head and token strides.  positions: int32 or int64 [axes, S] or [axes, B, S] ([S] or [B, S]
     for one axis), any strides."""
-    key = (rope, q.shape, q.stride(), q.dtype, q_out.shape, q_out.stride(), q_out.dtype, positions.shape, positions.stride(),
-           positions.dtype)
-    if k is not None and k_out is not None:
-        key += (k.shape, k.stride(), k.dtype, k_out.shape, k_out.stride(), k_out.dtype)
-        index = _one_device(q, q_out, positions, k, k_out)
-        kp, ko = k.data_ptr(), k_out.data_ptr()
-    else:
-        key += (k is None, k_out is None)
-        index = _one_device(q, q_out, positions)
-        kp = ko = None
-    a = _passed.get(key)
-    if a is None:
-        a = _remember(key, _rope_args(rope, q, k, positions, q_out, k_out))
-    _rope(rope, a, index, q.data_ptr(), kp, positions, q_out.data_ptr(), ko, 1 if inverse else 0, stream)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    _rope(rope, q, k, positions, q_out, k_out, inverse, stream)
 
 
-def _rope(rope, a, index, qp, kp, positions, qo, ko, inverse, stream=None):
-    dt, B, S, d, Hq, qs, qos, Hk, ks, kos, bits, ps = a
-    _on_device(index, "mesh_attn_rope", _lib.mesh_attn_rope, dt, B, S, d, Hq, qp, qs, qo, qos, Hk, kp, ks, ko, kos, rope.groups,
-               rope.n_pairs, rope.n_axes, rope._freq, rope._axis, rope._adjacent, inverse, positions.data_ptr(), bits, ps,
-               _raw_stream(index, stream))
+def _rope(rope, q, k, positions, q_out, k_out, inverse, stream=None):
+    if _ext is None:
+        load_library()
+    out = _ext.rope(rope._native, q, k, positions, q_out, k_out, 1 if inverse else 0, _handle_of(stream))
+    if out.__class__ is int:
+        _check(out, "mesh_attn_rope")
+    return out
 
 
 def mesh_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope):
     """q [B, Hq, S, d] and k [B, Hk, S, d] (or None) with their positions, as dense [B, H, S, d] tensors, which is what
     the attention calls take; q and k may be views, e.g. a projection's [B, S, H, d] transposed."""
-    shape, dtype, device = q.shape, q.dtype, q.device
-    q_out = torch.empty(shape, dtype=dtype, device=device)
-    if k is None:
-        mesh_attn_rope(rope, q, None, positions, q_out, None)
-        return q_out, None
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
-    # the outputs follow from the inputs, so what is checked, and remembered, is less than mesh_attn_rope's
-    key = (rope, shape, q.stride(), dtype, k.shape, k.stride(), k.dtype, positions.shape, positions.stride(), positions.dtype)
-    index = _one_device(q, k, positions)
-    a = _passed.get(key)
-    if a is None:
-        a = _remember(key, _rope_args(rope, q, k, positions, q_out, k_out))
-    _rope(rope, a, index, q.data_ptr(), k.data_ptr(), positions, q_out.data_ptr(), k_out.data_ptr(), 0)
-    return q_out, k_out
+    return _rope(rope, q, k, positions, None, None, False)
 
 
 def mesh_rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor, rope: MeshRope,
                        dq_out: Optional[torch.Tensor] = None, dk_out: Optional[torch.Tensor] = None):
     """The gradients of mesh_rope's q and k from those of its outputs, into dq_out and dk_out where given (any strides,
     e.g. the projection's layout), else into dense tensors."""
-    if dq_out is None:
-        dq_out = torch.empty(dq.shape, dtype=dq.dtype, device=dq.device)
-    if dk is not None and dk_out is None:
-        dk_out = torch.empty(dk.shape, dtype=dk.dtype, device=dk.device)
-    mesh_attn_rope(rope, dq, dk, positions, dq_out, dk_out, inverse=True)
-    return dq_out, dk_out
+    return _rope(rope, dq, dk, positions, dq_out, dk_out, True)
 
 
 def _memory_order(t: torch.Tensor):
@@ -747,49 +640,6 @@ def mesh_rope_autograd(q: torch.Tensor, k: Optional[torch.Tensor], positions: to
 
 # ---------------------------------------------------------------- differential attention
 
-def _diff_scale(scale: Optional[float], d: int) -> float:
-    return 1.0 / math.sqrt(d // 2) if scale is None else float(scale)
-
-
-def _diff_sizes(q, k, v, lam):
-    """(dtype code, B, Hq, S, d, Hkv, values in lam, LSE's shape) of q, k, v and lam that fit together; k's and v's strides and
-    q's length are the caller's to check."""
-    key = (q.shape, k.shape, v.shape, lam.shape, q.dtype, k.dtype, v.dtype, lam.dtype, q.stride(), lam.stride())
-    a = _passed.get(key)
-    if a is not None:
-        return a
-    qs, ks, ls = q.shape, k.shape, lam.shape
-    if len(qs) != 4 or len(ks) != 4 or v.shape != ks:
-        raise ValueError("q must be [B, Hq, S, d], k and v [B, Hkv, S, d]")
-    B, Hq, S, d = qs
-    if ks[0] != B or ks[3] != d:
-        raise ValueError("q, k and v must agree in batch and columns")
-    if ks[1] < 1 or Hq % ks[1]:
-        raise ValueError(f"Hq must be a multiple of Hkv: {Hq} and {ks[1]}")
-    if len(ls) != 1 or (ls[0] != Hq and ls[0] != 1):
-        raise ValueError("lam must be [Hq], or [1] for one value for all heads")
-    if not q.dtype == k.dtype == v.dtype == lam.dtype:
-        raise ValueError("q, k, v and lam must be of one dtype")
-    _contiguous(q, lam)
-    return _remember(key, (_dtype_code(q.dtype), B, Hq, S, d, ks[1], ls[0], (B, Hq, 2, S)))
-
-
-def _contiguous(*ts):
-    for t in ts:
-        if not t.is_contiguous():
-            raise ValueError("q, k, v, lam, the gradients and the outputs must be contiguous")
-
-
-def _like(q, *ts):
-    """ts are as q: contiguous, of its shape and dtype."""
-    shape, dtype = q.shape, q.dtype
-    for t in ts:
-        if t.shape != shape or t.dtype != dtype:
-            raise ValueError("O, O2 and dO must have q's shape and dtype, dQ, dK, dV and dlam those of q, k, v and lam")
-        if not t.is_contiguous():
-            raise ValueError("q, k, v, lam, the gradients and the outputs must be contiguous")
-
-
 def mesh_attn_diff_workspace_size(plan: Plan, dtype: torch.dtype, B: int, Hq: int, Hkv: int, d: int,
                                   backward: bool = False) -> int:
     n = c_sz()
@@ -805,72 +655,30 @@ def new_diff_workspace(plan: Plan, q: torch.Tensor, k: torch.Tensor, backward: b
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
-def _diff_plan_check(plan: Plan, q, k):
-    S = plan.info.S
-    if q.shape[2] != S or k.shape[2] != S:
-        raise ValueError(f"the plan is for S = {S}; q has {q.shape[2]} tokens, k and v {k.shape[2]}")
-
-
-def _tables_for(plan: Plan, index: int, stream) -> int:
-    """Pointer of the plan's tables for a call on `stream`.  Where that is not the stream that owns their memory, the
-    memory stays theirs until the call has run, though the plan may be dropped before."""
-    tables = plan.tables(index)
-    if _raw_stream(index, stream) != plan._tables_stream.get(index):
-        tables.record_stream(torch.cuda.current_stream(index) if stream is None else stream)
-    return tables.data_ptr()
+def _on_plan(entry, where: str, plan: Plan, device, *args):
+    """One of _binding's calls that read a plan's tables, which are made for the device where they are not there yet."""
+    out = entry(plan._native, *args)
+    if out is None:
+        plan.tables(device)
+        out = entry(plan._native, *args)
+    if out.__class__ is int:
+        _check(out, where)
+    return out
 
 
 def mesh_attn_diff_fwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
                        scale: Optional[float], O: torch.Tensor, O2: Optional[torch.Tensor], LSE: torch.Tensor,
                        workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
-    a = _diff_sizes(q, k, v, lam)
-    outs = (O,) if O2 is None else (O, O2)
-    _like(q, *outs)
-    if LSE.shape != a[7] or LSE.dtype != torch.float32:
-        raise ValueError("LSE must be fp32 [B, Hq, 2, S]")
-    _contiguous(LSE)
-    index = _one_device(q, k, v, lam, LSE, workspace, status, *outs)
-    _diff_fwd(a, plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream)
-
-
-def _diff_fwd(a, plan, q, k, v, lam, scale, O, O2, LSE, workspace, status, index, stream=None):
-    dt, B, Hq, S, d, Hkv, n, _ = a
-    _contiguous(k, v)
-    _diff_plan_check(plan, q, k)
-    _on_device(index, "mesh_attn_diff_fwd", _lib.mesh_attn_diff_fwd, plan._h, _tables_for(plan, index, stream), dt, B, Hq, Hkv, d,
-               q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), n, _diff_scale(scale, d), O.data_ptr(),
-               None if O2 is None else O2.data_ptr(), LSE.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-               status.data_ptr(), _raw_stream(index, stream))
+    _on_plan(_ext.diff_fwd, "mesh_attn_diff_fwd", plan, q.device, q, k, v, lam, scale, O, O2, LSE, 0, workspace, status,
+             _handle_of(stream))
 
 
 def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, O: torch.Tensor,
                        O2: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, scale: Optional[float], dQ: torch.Tensor,
                        dK: torch.Tensor, dV: torch.Tensor, dlam: torch.Tensor, workspace: torch.Tensor,
                        status: torch.Tensor, stream=None) -> None:
-    a = _diff_sizes(q, k, v, lam)
-    _like(q, dQ)
-    _like(k, dK, dV)
-    _like(lam, dlam)
-    index = _one_device(q, k, v, lam, O, O2, LSE, dO, dQ, dK, dV, dlam, workspace, status)
-    _diff_bwd(a, plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream)
-
-
-def _diff_bwd(a, plan, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace, status, index, stream=None):
-    dt, B, Hq, S, d, Hkv, n, lse_shape = a
-    _like(q, O, O2, dO)
-    if LSE.shape != lse_shape or LSE.dtype != torch.float32:
-        raise ValueError("LSE must be fp32 [B, Hq, 2, S]")
-    _contiguous(k, v, LSE)
-    _diff_plan_check(plan, q, k)
-    if not B * Hq * S:  # no rows: sums over nothing
-        with torch.cuda.stream(stream):
-            for t in (dK, dV, dlam):
-                t.zero_()
-        return
-    _on_device(index, "mesh_attn_diff_bwd", _lib.mesh_attn_diff_bwd, plan._h, _tables_for(plan, index, stream), dt, B, Hq, Hkv, d,
-               q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), n, O.data_ptr(), O2.data_ptr(), LSE.data_ptr(),
-               dO.data_ptr(), _diff_scale(scale, d), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dlam.data_ptr(),
-               workspace.data_ptr(), workspace.nbytes, status.data_ptr(), _raw_stream(index, stream))
+    _on_plan(_ext.diff_bwd, "mesh_attn_diff_bwd", plan, q.device, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace,
+             status, _handle_of(stream))
 
 
 def _raise_status(status: torch.Tensor):
@@ -891,18 +699,14 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     mesh_diff_attention_backward takes.  A program that calls it every step keeps plan, workspace
     (new_diff_workspace) and status (new_status) and passes check_status=False, which leaves out the wait.
     """
-    a = _diff_sizes(q, k, v, lam)
-    index = _one_device(q, k, v, lam)
-    device = q.device
-    plan = plan or mesh_attn_plan_create(a[3], P, causal, kvr, greedy)
+    if plan is None or workspace is None or status is None:
+        load_library()
+        _ext.diff_check(q, k, v, lam)
+        plan = plan or mesh_attn_plan_create(q.shape[2], P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k) if workspace is None else workspace
-    st = new_status(device) if status is None else status
-    if ws.get_device() != index or st.get_device() != index:
-        _one_device(q, ws, st)
-    O = torch.empty_like(q)
-    O2 = torch.empty_like(q) if return_saved else None
-    LSE = torch.empty(a[7], dtype=torch.float32, device=device)
-    _diff_fwd(a, plan, q, k, v, lam, scale, O, O2, LSE, ws, st, index)
+    st = new_status(q.device) if status is None else status
+    O, O2, LSE = _on_plan(_ext.diff_fwd, "mesh_attn_diff_fwd", plan, q.device, q, k, v, lam, scale, None, None, None,
+                          1 if return_saved else 0, ws, st, None)
     if check_status:
         _raise_status(st)
     return (O, O2, LSE) if return_saved else (O, LSE)
@@ -914,15 +718,14 @@ def mesh_diff_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                                  plan: Optional[Plan] = None, workspace: Optional[torch.Tensor] = None,
                                  status: Optional[torch.Tensor] = None, check_status: bool = True):
     """(dQ, dK, dV, dlam) from the forward's O, O2 and LSE and the gradient dO, on the current stream."""
-    a = _diff_sizes(q, k, v, lam)
-    index = _one_device(q, k, v, lam, O, O2, LSE, dO)
-    plan = plan or mesh_attn_plan_create(a[3], P, causal, kvr, greedy)
+    if plan is None or workspace is None or status is None:
+        load_library()
+        _ext.diff_check(q, k, v, lam)
+        plan = plan or mesh_attn_plan_create(q.shape[2], P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k, backward=True) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
-    if ws.get_device() != index or st.get_device() != index:
-        _one_device(q, ws, st)
-    grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(lam))
-    _diff_bwd(a, plan, q, k, v, lam, O, O2, LSE, dO, scale, *grads, ws, st, index)
+    grads = _on_plan(_ext.diff_bwd, "mesh_attn_diff_bwd", plan, q.device, q, k, v, lam, O, O2, LSE, dO, scale, None, None, None,
+                     None, ws, st, None)
     if check_status:
         _raise_status(st)
     return grads
@@ -969,40 +772,16 @@ def new_diff_decode_workspace(B: int, Hq: int, Hkv: int, d: int, T: int, device=
 def mesh_attn_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
                           lam: torch.Tensor, scale: Optional[float], O: torch.Tensor, LSE: torch.Tensor,
                           workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
-    load_library()
-    a = _diff_decode_sizes(q, k_cache, v_cache, lens, lam)
-    _like(q, O)
-    if LSE.shape != a[9] or LSE.dtype != torch.float32:
-        raise ValueError("LSE must be fp32 [B, Hq, 2, 1]")
-    _contiguous(LSE)
-    index = _one_device(q, k_cache, v_cache, lens, lam, O, LSE, workspace, status)
-    _diff_decode(a, q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream)
+    _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, stream)
 
 
-def _diff_decode_sizes(q, k_cache, v_cache, lens, lam):
-    """(dtype code, B, Hq, Hkv, d, T, k's strides, v's strides, values in lam, LSE's shape) of tensors that fit together."""
-    key = (q.shape, k_cache.shape, v_cache.shape, lam.shape, lens.shape, q.dtype, k_cache.dtype, v_cache.dtype, lam.dtype,
-           lens.dtype, q.stride(), k_cache.stride(), v_cache.stride(), lam.stride(), lens.stride())
-    a = _passed.get(key)
-    if a is not None:
-        return a
-    dt, B, Hq, S, d, Hkv, n, _ = _diff_sizes(q, k_cache, v_cache, lam)
-    T = k_cache.shape[2]
-    if S != 1:
-        raise ValueError("q must hold one token a sequence: [B, Hq, 1, d]")
-    if lens.shape != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous():
-        raise ValueError("lens must be contiguous int32 [B]")
-    if (k_cache.stride(3) != 1 or v_cache.stride(3) != 1) and T:
-        raise ValueError("the columns of the caches must be consecutive")
-    return _remember(key, (dt, B, Hq, Hkv, d, T, _strides3(k_cache), _strides3(v_cache), n, (B, Hq, 2, 1)))
-
-
-def _diff_decode(a, q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, index, stream=None):
-    dt, B, Hq, Hkv, d, T, ks, vs, n, _ = a
-    _on_device(index, "mesh_attn_diff_decode", _lib.mesh_attn_diff_decode, dt, B, Hq, Hkv, d, T, q.data_ptr(),
-               k_cache.data_ptr(), ks, v_cache.data_ptr(), vs, lens.data_ptr(), lam.data_ptr(), n, _diff_scale(scale, d),
-               O.data_ptr(), LSE.data_ptr(), workspace.data_ptr(), workspace.nbytes, status.data_ptr(),
-               _raw_stream(index, stream))
+def _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, stream=None):
+    if _ext is None:
+        load_library()
+    out = _ext.diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, _handle_of(stream))
+    if out.__class__ is int:
+        _check(out, "mesh_attn_diff_decode")
+    return out
 
 
 def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor, lam: torch.Tensor,
@@ -1012,15 +791,14 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     (int32, on the device) tokens of k_cache, v_cache [B, Hkv, T, d], which may be views with other strides (16-byte
     multiples).  Returns O [B, Hq, 1, d] and LSE [B, Hq, 2, 1].  A serving loop keeps workspace
     (new_diff_decode_workspace) and status and passes check_status=False."""
-    load_library()
-    a = _diff_decode_sizes(q, k_cache, v_cache, lens, lam)
-    device = q.device
-    ws = new_diff_decode_workspace(a[1], a[2], a[3], a[4], a[5], device) if workspace is None else workspace
-    st = new_status(device) if status is None else status
-    index = _one_device(q, k_cache, v_cache, lens, lam, ws, st)
-    O = torch.empty_like(q)
-    LSE = torch.empty(a[9], dtype=torch.float32, device=device)
-    _diff_decode(a, q, k_cache, v_cache, lens, lam, scale, O, LSE, ws, st, index)
+    if workspace is None or status is None:
+        load_library()
+        _ext.diff_check(q, k_cache, v_cache, lam)
+    ws = workspace
+    if ws is None:
+        ws = new_diff_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[3], k_cache.shape[2], q.device)
+    st = new_status(q.device) if status is None else status
+    O, LSE = _diff_decode(q, k_cache, v_cache, lens, lam, scale, None, None, ws, st)
     if check_status:
         _raise_status(st)
     return O, LSE
