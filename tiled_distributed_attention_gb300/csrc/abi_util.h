@@ -9,6 +9,7 @@
 #include <new>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "internal.h"
 
@@ -60,6 +61,23 @@ struct OncePerDevice {
     if (dev >= 0) bits.fetch_or((uint64_t)1 << dev, std::memory_order_release);
   }
 };
+
+// Launch of a kernel that begins with wait_for_kernel_before: its launch and set-up overlap the end of the
+// kernel before it, 1 to 2 us where kernels are short.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, std::forward<A>(args)...);
+}
 
 // A launcher's result (a cudaError_t value and its message) as a status.
 inline int launch_status(int ce, const std::string& err) {

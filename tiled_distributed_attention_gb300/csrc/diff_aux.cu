@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <string>
 
+#include "abi_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -38,6 +39,7 @@ __device__ __forceinline__ float lam_of(const void* lam, int n, int h) {
 // m's half of the columns and zeros in the other, so that attention of 2 Hq heads over the full d
 // columns gives both maps.
 __global__ void __launch_bounds__(THREADS) split_kernel(const DiffArgs a, uint2* qp, uint2* kp, uint2* vp) {
+  wait_for_kernel_before();
   const TablesHeader* th = static_cast<const TablesHeader*>(a.tables);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
     record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);  // another plan's tables: the tile kernel does nothing
@@ -86,6 +88,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
   constexpr int PER = 2;
   constexpr int ROWS = PER * THREADS / Q4;
   __shared__ float w_s[2][MAX_SLOTS][ROWS];
+  wait_for_kernel_before();
   if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
   const int tid = threadIdx.x;
   const int rb = (int)(blockIdx.x % (unsigned)n_rblk);
@@ -177,6 +180,7 @@ __device__ __forceinline__ void dot16(uint4 x, uint4 y, float& acc) {
 template <typename T, int D>
 __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* dsum, float* dlam_part, int64_t n_part) {
   constexpr int LANES = D * (int)sizeof(T) / 16, AT_ONCE = THREADS / LANES, PASSES = PREP_ROWS / AT_ONCE;
+  wait_for_kernel_before();
   const TablesHeader* th = static_cast<const TablesHeader*>(a.tables);
   if (blockIdx.x == 0 && threadIdx.x == 0 && (th->magic != TABLES_MAGIC || th->tag != a.tag))
     record_error(a.status, MESH_ATTN_ERR_INVALID_ARG, 7, 0);  // another plan's tables: the launches behind do nothing
@@ -231,6 +235,7 @@ __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* 
 // in a fixed order in fp64, since terms of both signs nearly cancel over a long batch.
 template <typename T>
 __global__ void __launch_bounds__(THREADS) dlam_kernel(const DiffArgs a, const float* part, int64_t n_part) {
+  wait_for_kernel_before();
   if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
   const int h0 = a.lam_n == 1 ? 0 : (int)blockIdx.x, nh = a.lam_n == 1 ? a.Hq : 1;
   double acc = 0.0;
@@ -252,8 +257,7 @@ __global__ void __launch_bounds__(THREADS) dlam_kernel(const DiffArgs a, const f
   }
 }
 
-static int done(const char* what, std::string* err) {
-  const cudaError_t e = cudaGetLastError();
+static int done(cudaError_t e, const char* what, std::string* err) {
   if (e != cudaSuccess) *err = std::string(what) + ": " + cudaGetErrorString(e);
   return (int)e;
 }
@@ -265,10 +269,10 @@ int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, s
   const F32Pieces pc = f32_pieces_layout(a.B, 2 * a.Hq, a.Hkv, a.S, a.d);
   char* base = a.ws + w.pieces;
   const unsigned grid = daux::grid_for((int64_t)a.B * a.Hq * a.S * (a.d / 4));
-  daux::split_kernel<<<dim3(grid, 3), daux::THREADS, 0, (cudaStream_t)stream>>>(
-      a, reinterpret_cast<uint2*>(base + pc.q_off), reinterpret_cast<uint2*>(base + pc.k_off),
-      reinterpret_cast<uint2*>(base + pc.v_off));
-  return daux::done("diff split launch", err);
+  return daux::done(launch_behind(daux::split_kernel, dim3(grid, 3), daux::THREADS, 0, (cudaStream_t)stream, a,
+                                  reinterpret_cast<uint2*>(base + pc.q_off), reinterpret_cast<uint2*>(base + pc.k_off),
+                                  reinterpret_cast<uint2*>(base + pc.v_off)),
+                    "diff split launch", err);
 }
 
 template <int D, typename T>
@@ -282,11 +286,12 @@ static int merge_d(const DiffArgs& a, const DiffWorkspace& w, bool flat, cudaStr
     *err = "too many rows for one merge launch";
     return (int)cudaErrorInvalidConfiguration;
   }
-  daux::merge_kernel<D, T><<<(unsigned)blocks, daux::THREADS, 0, st>>>(
-      a, reinterpret_cast<const float*>(a.ws + w.part_o), reinterpret_cast<const float*>(a.ws + w.part_lse),
+  const cudaError_t e = launch_behind(
+      daux::merge_kernel<D, T>, dim3((unsigned)blocks), daux::THREADS, 0, st, a, reinterpret_cast<const float*>(a.ws + w.part_o),
+      reinterpret_cast<const float*>(a.ws + w.part_lse),
       reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + (flat ? a.tl.flat_list : a.tl.slot_off)), P, L,
-      flat ? 1 : a.n_slots, (int)n_rblk);
-  return daux::done("diff merge launch", err);
+      (int)(flat ? 1 : a.n_slots), (int)n_rblk);
+  return daux::done(e, "diff merge launch", err);
 }
 
 int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool flat, void* stream,
@@ -306,19 +311,22 @@ int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype 
   }
   float* dsum = reinterpret_cast<float*>(a.ws + w.dsum);
   float* dl = dt == MESH_ATTN_F32 ? reinterpret_cast<float*>(a.ws + w.dlam_part) : nullptr;
-  auto go = [&](auto kern) { kern<<<(unsigned)blocks, daux::THREADS, 0, st>>>(a, dsum, dl, n_part); };
-  if (dt == MESH_ATTN_BF16) go(a.d == 128 ? daux::prep_kernel<__nv_bfloat16, 128> : daux::prep_kernel<__nv_bfloat16, 64>);
-  else go(a.d == 128 ? daux::prep_kernel<float, 128> : daux::prep_kernel<float, 64>);
-  return daux::done("diff prep launch", err);
+  auto go = [&](auto kern) { return launch_behind(kern, dim3((unsigned)blocks), daux::THREADS, 0, st, a, dsum, dl, n_part); };
+  const cudaError_t e =
+      dt == MESH_ATTN_BF16 ? go(a.d == 128 ? daux::prep_kernel<__nv_bfloat16, 128> : daux::prep_kernel<__nv_bfloat16, 64>)
+                           : go(a.d == 128 ? daux::prep_kernel<float, 128> : daux::prep_kernel<float, 64>);
+  return daux::done(e, "diff prep launch", err);
 }
 
 int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,
                      std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
   const float* part = reinterpret_cast<const float*>(a.ws + w.dlam_part);
-  if (dt == MESH_ATTN_BF16) daux::dlam_kernel<__nv_bfloat16><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, n_part);
-  else daux::dlam_kernel<float><<<a.lam_n, daux::THREADS, 0, st>>>(a, part, n_part);
-  return daux::done("diff dlam launch", err);
+  const dim3 grid((unsigned)a.lam_n);
+  const cudaError_t e = dt == MESH_ATTN_BF16
+                            ? launch_behind(daux::dlam_kernel<__nv_bfloat16>, grid, daux::THREADS, 0, st, a, part, n_part)
+                            : launch_behind(daux::dlam_kernel<float>, grid, daux::THREADS, 0, st, a, part, n_part);
+  return daux::done(e, "diff dlam launch", err);
 }
 
 }  // namespace mesh

@@ -236,6 +236,7 @@ __device__ __forceinline__ void run_pass(const Params& p, int bx, int n_blocks) 
 
 template <int D>
 __global__ void __launch_bounds__(THREADS) bwd_kernel(const Params kv, const Params dq) {
+  wait_for_kernel_before();
   const int n = (int)gridDim.x / 2;  // blocks of a pass
   if ((int)blockIdx.x < n) run_pass<D, true>(kv, (int)blockIdx.x, n);
   else run_pass<D, false>(dq, (int)blockIdx.x - n, n);
@@ -251,6 +252,7 @@ struct SumArgs {
   const int32_t* status;
 };
 __global__ void __launch_bounds__(256) sum_parts(const SumArgs a) {
+  wait_for_kernel_before();
   if (*reinterpret_cast<const volatile int32_t*>(a.status) != 0) return;
   const int w = blockIdx.y;
   const int64_t total = a.heads[w] * a.row4;
@@ -279,8 +281,7 @@ static cudaError_t launch(const Params& kv, const Params& dq, cudaStream_t st) {
     once.mark(dev);
   }
   const dim3 grid((unsigned)(2 * ((kv.S + RB - 1) / RB)), (unsigned)kv.Hq, (unsigned)(kv.B * kv.splits));
-  kern<<<grid, THREADS, smem, st>>>(kv, dq);
-  return cudaGetLastError();
+  return launch_behind(kern, grid, THREADS, smem, st, kv, dq);
 }
 
 }  // namespace dsimt
@@ -343,8 +344,7 @@ int launch_diff_bwd_simt(const DiffArgs& a, const DiffWorkspace& w, int sms, voi
     s.row4 = a.S * a.d / 4;
     s.status = a.status;
     const int64_t most = (int64_t)a.B * a.Hq * s.row4;
-    sum_parts<<<dim3((unsigned)std::min<int64_t>((most + 255) / 256, 152 * 8), (unsigned)n), 256, 0, st>>>(s);
-    e = cudaGetLastError();
+    e = launch_behind(sum_parts, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 152 * 8), (unsigned)n), 256, 0, st, s);
   }
   if (e != cudaSuccess) *err = std::string("diff_bwd_simt launch: ") + cudaGetErrorString(e);
   return (int)e;

@@ -342,10 +342,12 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       mbar_init(bar(Ly::B_UF + s), 1);
       mbar_init(bar(Ly::B_UE + s), N_EW + 1 + (KV ? 0 : N_EPI));  // the warps that read a unit
     }
+    wait_for_kernel_before();
     *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  wait_for_kernel_before();  // and before tensor memory is taken, which that kernel may still want
   if (warp == WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -1200,8 +1202,7 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_di
   if (e == cudaSuccess && (kv_units > sms || dq_units > sms)) e = cudaMemsetAsync(kv.counter, 0, 512, st);
   if (e == cudaSuccess) {
     const int kv_ctas = (int)std::min<int64_t>(kv_units, sms), dq_ctas = (int)std::min<int64_t>(dq_units, sms);
-    kern<<<dim3((unsigned)(kv_ctas + dq_ctas)), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(rows128, rows64, kv, dq, kv_ctas);
-    e = cudaGetLastError();
+    e = launch_behind(kern, dim3((unsigned)(kv_ctas + dq_ctas)), NUM_THREADS, Layout<D>::TOTAL, st, rows128, rows64, kv, dq, kv_ctas);
   }
   if (e != cudaSuccess) *err = std::string("diff_bwd launch: ") + cudaGetErrorString(e);
   return (int)e;

@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
   int32_t* scan = reinterpret_cast<int32_t*>(Ls + ROWS);  // [WARPS + 2]
   int64_t* prefix = reinterpret_cast<int64_t*>(smem + BIG + 4 * (2 * WARPS * ROWS + 2 * ROWS + 16));  // [B + 1] tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  wait_for_kernel_before();
 
   // units before each sequence
   {
@@ -721,8 +722,7 @@ static int launch(const Params& p, int grid, cudaStream_t st, std::string* err) 
     if (e == cudaSuccess) once.mark(dev);
   }
   if (e == cudaSuccess) {
-    kern<<<grid, THREADS, smem, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_behind(kern, dim3((unsigned)grid), THREADS, smem, st, p);
   }
   if (e != cudaSuccess) *err = std::string("diff_decode launch: ") + cudaGetErrorString(e);
   return (int)e;

@@ -178,10 +178,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(bar(Ly::B_UEMPTY + t), 1 + 8);  // one lane of the MMA warp and of each softmax warp
     }
     mbar_init(bar(Ly::B_DRAIN), 1);
+    wait_for_kernel_before();
     *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  wait_for_kernel_before();  // and before tensor memory is taken, which that kernel may still want
   if (warp == WARP_MMA) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -736,8 +738,7 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
     return (int)e;
   }
   const unsigned grid = (unsigned)std::min<int64_t>(units, sms);  // persistent: one CTA per SM
-  kern<<<dim3(grid), dim3(NUM_THREADS), Layout<D>::ALLOC, st>>>(mq, mk, mv, prm);
-  e = cudaGetLastError();
+  e = launch_behind(kern, dim3(grid), NUM_THREADS, Layout<D>::ALLOC, st, mq, mk, mv, prm);
   if (e != cudaSuccess) *err = std::string("diff_fwd_tc launch: ") + cudaGetErrorString(e);
   return (int)e;
 }

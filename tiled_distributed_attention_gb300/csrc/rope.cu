@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ P
   const int item = (int)(lin % prm.items);
   const int64_t tok = lin / prm.items;
   if (tok >= prm.tokens) return;
+  wait_for_kernel_before();
   const int64_t b = tok / prm.S, s = tok - b * prm.S;
   constexpr int NP = Item<V, ADJ>::PAIRS;
   constexpr bool TWO = Item<V, ADJ>::TWO;
@@ -208,11 +209,9 @@ static int launch(Params& prm, bool adjacent, int sms, cudaStream_t st, std::str
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(H, (4LL * sms + blocks - 1) / blocks));
   prm.heads_per_block = (int)((H + want - 1) / want);
   const unsigned gy = (unsigned)((H + prm.heads_per_block - 1) / prm.heads_per_block);
-  if (adjacent)
-    rope_kernel<T, V, true><<<dim3((unsigned)blocks, gy), THREADS, 0, st>>>(prm);
-  else
-    rope_kernel<T, V, false><<<dim3((unsigned)blocks, gy), THREADS, 0, st>>>(prm);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid((unsigned)blocks, gy);
+  const cudaError_t e = adjacent ? launch_behind(rope_kernel<T, V, true>, grid, THREADS, 0, st, prm)
+                                 : launch_behind(rope_kernel<T, V, false>, grid, THREADS, 0, st, prm);
   if (e != cudaSuccess) *err = std::string("rope launch: ") + cudaGetErrorString(e);
   return (int)e;
 }

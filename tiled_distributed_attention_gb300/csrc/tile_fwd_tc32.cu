@@ -37,6 +37,7 @@
 
 #include <string>
 
+#include "abi_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + Ly::MISC_OFF + 4);
   const int64_t L = prm.L;
 
+  wait_for_kernel_before();
   // Units are numbered KV-head-major: (batch, KV head, work item in launch order, query head of
   // the group, query tile), so the CTAs resident together share one KV head's partitions in L2.
   int64_t uu = blockIdx.x;
@@ -684,8 +686,12 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
     return (int)e;
   }
-  kern<<<dim3((unsigned)units), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(mq, mk, mv, prm);
-  e = cudaGetLastError();
+  if (a.pieces_ready) {
+    e = launch_behind(kern, dim3((unsigned)units), NUM_THREADS, Layout<D>::TOTAL, st, mq, mk, mv, prm);
+  } else {
+    kern<<<dim3((unsigned)units), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(mq, mk, mv, prm);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) *err = std::string("tile_fwd_tc32 launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
