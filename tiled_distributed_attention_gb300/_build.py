@@ -24,7 +24,7 @@ BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["planner.cpp", "abi.cu", "tile_fwd_tc.cu", "tile_fwd_tc32.cu", "merge.cu", "noalloc.cu",
            "tile_bwd_simt.cu", "tile_bwd_tc.cu", "bwd_aux.cu", "rope.cu", "diff_abi.cu", "diff_aux.cu", "diff_fwd_tc.cu",
-           "diff_bwd_tc.cu", "diff_bwd_simt.cu", "diff_decode.cu"]
+           "diff_bwd_tc.cu", "diff_bwd_tc32.cu", "diff_decode.cu"]
 
 
 def nvcc() -> str:

@@ -70,7 +70,8 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
     const int64_t by_slot = (int64_t)plan.n_slots() * ((plan.L + 127) / 128) * 8, flat = (plan.S + 127) / 128 * 8;
     w.dlam_part = take((size_t)B * Hq * 4 * (size_t)(f32 ? (plan.S + 63) / 64 : q_slots ? std::max(by_slot, flat) : flat));
     if (f32) {  // partial sums of the splits, and of a KV head's query heads
-      const size_t splits = (size_t)diff_simt_splits(plan.S, B, Hq, MAX_SMS);  // grows with the SM count
+      w.pieces = take(bwd32_pieces_layout(B, Hq, Hkv, plan.S, d).total);
+      const size_t splits = (size_t)diff_bwd32_splits(plan.S, B, Hq, MAX_SMS);  // grows with the SM count
       if (splits > 1) w.dq_part = take(splits * qrows * d * 4);
       if (splits * (Hq / Hkv) > 1) {
         w.dk_part = take(splits * qrows * d * 4);
@@ -339,7 +340,7 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
     int sms = 0;
     if ((rc = sm_count(&sms))) return rc;
-    if ((rc = launch_status(mesh::launch_diff_bwd_simt(a, w, sms, stream, &err), err))) return rc;
+    if ((rc = launch_status(mesh::launch_diff_bwd_tc32(a, w, sms, stream, &err), err))) return rc;
     return launch_status(mesh::launch_diff_dlam(a, w, dtype, (a.S + 63) / 64, stream, &err), err);
   });
 }

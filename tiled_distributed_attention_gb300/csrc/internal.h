@@ -204,7 +204,7 @@ struct DiffArgs {
 struct DiffWorkspace {
   size_t counters;            // 512 bytes
   size_t part_o, part_lse;    // forward partials
-  size_t pieces;              // fp32 forward: the bf16 pieces of Q (one map a head), K and V
+  size_t pieces;              // fp32: bf16 pieces; forward: of Q (one map a head), K and V; backward: BwdPieces
   size_t dsum;                // [B, 2 Hq, S] row terms of dS
   size_t dlam_part;           // [B, Hq, n], n as the path has it
   size_t dq_part, dk_part, dv_part;
@@ -227,8 +227,12 @@ int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool 
 // fp32 forward: Q (one map a head), K and V as bf16 pieces.
 int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err);
 // fp32 backward: dQ, dK and dV, with their sums over splits and query heads.
-int launch_diff_bwd_simt(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
-int diff_simt_splits(int64_t S, int32_t B, int32_t Hq, int sms);
+int launch_diff_bwd_tc32(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
+int diff_bwd32_splits(int64_t S, int32_t B, int32_t Hq, int sms);
+struct BwdPieces {
+  size_t q, k, v, g, total;  // the bf16 pieces of Q, K, V and dO ([3][rows][d] each), in bytes
+};
+BwdPieces bwd32_pieces_layout(int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d);
 // `flat`: the partials are of the whole sequence as one partition with one slot.
 int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool flat, void* stream,
                       std::string* err);
