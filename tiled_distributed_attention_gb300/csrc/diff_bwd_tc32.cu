@@ -14,12 +14,13 @@
 // TMEM columns beside dK's: eight products where seven would do.  R1's pieces lie in TMEM (the operand
 // of dP, split by the elementwise warps straight from fp32), R0's in shared memory with one stage of C0 and
 // C1 (two at d = 64); they come by TMA from pieces that pieces_kernel writes.
-//   TMEM: R1's pieces [0, 192) (dV: A's [0, 96)) | S_1, S_2, dP [192, 384), later the pieces of dS_1 and
+//   TMEM: R1's pieces [0, 192) (dV: A's, two buffers) | S_1, S_2, dP [192, 384), later the pieces of dS_1 and
 //   dS_2 in their place | accumulators [384, 512).
 //   warps 0-7   elementwise: two warps per TMEM lane quadrant, each taking 32 of a block's 64 columns
 //   warp 8      MMA issuer, warp 9 producer (TMA)
-// A block's steps follow one another (S and dP, the elementwise part, dS C0); only loads run ahead.  At d = 64
-// a map's half is 32 columns: its product with C0 is computed 64 wide and half of it is used.
+// In dQ and dK a block's steps follow one another (dP and S, the elementwise part, dS C0), TMEM being full; in dV
+// the next block's scores run while A is made.  At d = 64 a map's half is 32 columns: its product with C0
+// is computed 64 wide and half of it is used.
 //
 // Few rows leave SMs idle, so the streamed axis is split between CTAs (`splits`); the splits, and for dK and
 // dV the query heads of a KV head, leave partial sums that sum_parts adds in order.  Rows past the end are
@@ -67,7 +68,7 @@ struct Layout {
   static constexpr uint32_t VEC = C1 + NST * 3 * CP;  // [2][64][4]: LSE_1, LSE_2, D_1, D_2 of a block's query rows
   static constexpr uint32_t BAR = VEC + 2 * BS * 16;
   static constexpr int B_RF = 0, B_R1 = 1, B_C0F = 2, B_C0E = B_C0F + 2, B_C1F = B_C0E + 2, B_C1E = B_C1F + 2, B_S = B_C1E + 2,
-                       B_DS = B_S + 1, B_ACC = B_DS + 1, B_DRAIN = B_ACC + 1, NBARS = B_DRAIN + 1;
+                       B_SR = B_S + 1, B_DS = B_SR + 1, B_ACC = B_DS + 2, B_DRAIN = B_ACC + 1, NBARS = B_DRAIN + 1;
   static constexpr uint32_t MISC = BAR + NBARS * 8;  // tmem base, abort flag
   static constexpr uint32_t ALLOC = MISC + 16 + 1024;
 };
@@ -203,6 +204,11 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         tmem_ld32(lanes + COL_S + 64u + (uint32_t)(32 * hf), s2);
         if (PASS != DV) tmem_ld32(lanes + COL_DP + (uint32_t)(32 * hf), dp);
         tc_wait_ld();
+        if (PASS == DV) {  // the next block's scores may come
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Ly::B_SR));
+        }
       }
       // everyone has read before anyone writes in the scores' place; the vote keeps the warps together
       int all;
@@ -243,7 +249,8 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       };
       if (__any_sync(0xffffffffu, lo > 0 || hi < 32)) weights(std::true_type{});
       else weights(std::false_type{});
-      const uint32_t at = lanes + (PASS == DV ? COL_A : COL_S) + (uint32_t)(16 * hf);
+      // (A's buffer of two blocks ago has been read: that product precedes the scores just waited for)
+      const uint32_t at = lanes + (PASS == DV ? COL_A + 96u * (uint32_t)(j & 1) : COL_S) + (uint32_t)(16 * hf);
 #pragma unroll
       for (int c = 0; c < 16; ++c) split3(s1[2 * c], s1[2 * c + 1], p1[c], p2[c], p3[c]);
       tmem_st16(at, p1);
@@ -259,7 +266,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Ly::B_DS));
+      if (lane == 0) mbar_arrive(bar(Ly::B_DS + (j & 1)));
     }
     if (ok) ok = mbar_wait_warp(bar(Ly::B_ACC), 0u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, -1);
     if (ok || (NB == 0 && *abort_flag == 0)) {
@@ -271,6 +278,10 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       const float f = PASS == DV ? 1.f : prm.scale;
       // d = 64: the second map's accumulator is 64 columns behind, its half of the columns in the second 32
       const uint32_t acc = lanes + COL_ACC + (uint32_t)(hf * (D == 64 && PASS != DV ? 96 : D / 2));
+      // 32 rows x 32 columns at a time through shared memory (C0's, whose last reader is done), 16-byte pieces
+      // swizzled by row, so that a store writes whole 128-byte row pieces
+      float* stage = reinterpret_cast<float*>(smem + Ly::C0 + (uint32_t)warp * 4096u);
+      const int rows = (int)max((int64_t)0, min((int64_t)32, S - (row - lane)));  // of this warp, inside the sequence
 #pragma unroll
       for (int c = 0; c < D / 2; c += 32) {
         float o[32];
@@ -281,10 +292,18 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (row < S)
+        __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            reinterpret_cast<float4*>(dst + c)[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<float4*>(stage + lane * 32 + ((e ^ (lane & 7)) * 4)) =
+              make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3), e = lane & 7;
+          const float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + ((e ^ (r & 7)) * 4));
+          if (r < rows) *reinterpret_cast<float4*>(dst + (int64_t)(r - lane) * D + c + e * 4) = x;
+        }
       }
     }
   } else if (warp == WARP_MMA) {
@@ -305,53 +324,66 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
     bool ok = run;
     if (ok) ok = wait(Ly::B_RF, 0u, -1);
     if (ok && PASS != DV) ok = wait(Ly::B_R1, 0u, -1);
-    for (int j = 0; j < NB && ok; ++j) {
+    auto issue_s = [&](int j) -> bool {  // S_1 and S_2 of block j
       const int st = j % NST;
-      const uint32_t ph = (uint32_t)((j / NST) & 1);
-      const uint64_t stage = (uint64_t)st * ((3 * Ly::CP) >> 4);
-      if (!(ok = wait(Ly::B_C0F + st, ph, j))) break;
+      if (!wait(Ly::B_C0F + st, (uint32_t)((j / NST) & 1), j)) return false;
       tc_fence_after();
+      const uint64_t c = c0d + (uint64_t)st * ((3 * Ly::CP) >> 4);
 #pragma unroll
       for (int pr = 0; pr < N_PAIR; ++pr)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const int m = kk / (D / 32);  // a map's half of the columns
-          tc_mma_ss_warp(tmem + COL_S + 64u * m, rd + r_off(pair_a(pr), kk), c0d + stage + c_off(pair_b(pr), kk), idesc_s,
+          tc_mma_ss_warp(tmem + COL_S + 64u * m, rd + r_off(pair_a(pr), kk), c + c_off(pair_b(pr), kk), idesc_s,
                          (pr > 0 || kk % (D / 32) > 0) ? 1u : 0u);
         }
-      if (PASS == DV) {
-        tc_commit_warp(bar(Ly::B_C0E + st));
-      } else {
-        if (!(ok = wait(Ly::B_C1F + st, ph, j))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int pr = 0; pr < N_PAIR; ++pr)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ts_warp(tmem + COL_DP, tmem + COL_R1 + (uint32_t)(pair_a(pr) * (D / 2) + kk * 8), c1d + stage + c_off(pair_b(pr), kk),
-                           idesc_s, (pr > 0 || kk > 0) ? 1u : 0u);
-        tc_commit_warp(bar(Ly::B_C1E + st));
-      }
+      if (PASS == DV) tc_commit_warp(bar(Ly::B_C0E + st));
       tc_commit_warp(bar(Ly::B_S));
-      if (PASS == DV && !(ok = wait(Ly::B_C1F + st, ph, j))) break;
-      if (!(ok = wait(Ly::B_DS, (uint32_t)(j & 1), j))) break;
+      return true;
+    };
+    auto issue_dp = [&](int j) -> bool {
+      const int st = j % NST;
+      if (!wait(Ly::B_C1F + st, (uint32_t)((j / NST) & 1), j)) return false;
       tc_fence_after();
-      const auto sum = [&](uint32_t acc, uint32_t a, uint64_t c) {  // acc += pieces at a times a block's rows, MN-major
+      const uint64_t c = c1d + (uint64_t)st * ((3 * Ly::CP) >> 4);
 #pragma unroll
-        for (int pr = 0; pr < N_PAIR; ++pr)
+      for (int pr = 0; pr < N_PAIR; ++pr)
 #pragma unroll
-          for (int kk = 0; kk < BS / 16; ++kk)
-            tc_mma_ts_warp(acc, a + (uint32_t)(pair_a(pr) * 32 + kk * 8), c + (c_off(pair_b(pr), 0) + (uint64_t)(kk * 128)), idesc_a,
-                           (j > 0 || pr > 0 || kk > 0) ? 1u : 0u);
-      };
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma_ts_warp(tmem + COL_DP, tmem + COL_R1 + (uint32_t)(pair_a(pr) * (D / 2) + kk * 8), c + c_off(pair_b(pr), kk), idesc_s,
+                         (pr > 0 || kk > 0) ? 1u : 0u);
+      tc_commit_warp(bar(Ly::B_C1E + st));
+      return true;
+    };
+    auto sum = [&](int j, uint32_t acc, uint32_t a, uint64_t c) {  // acc += pieces at a times a block's rows, MN-major
+#pragma unroll
+      for (int pr = 0; pr < N_PAIR; ++pr)
+#pragma unroll
+        for (int kk = 0; kk < BS / 16; ++kk)
+          tc_mma_ts_warp(acc, a + (uint32_t)(pair_a(pr) * 32 + kk * 8), c + (c_off(pair_b(pr), 0) + (uint64_t)(kk * 128)), idesc_a,
+                         (j > 0 || pr > 0 || kk > 0) ? 1u : 0u);
+    };
+    // dP before the scores: C1's stage is free before C0's, whose next load then overlaps this product
+    if (ok) ok = (PASS == DV || issue_dp(0)) && issue_s(0);
+    for (int j = 0; j < NB && ok; ++j) {
+      const int st = j % NST;
+      const uint64_t stage = (uint64_t)st * ((3 * Ly::CP) >> 4);
+      if (PASS == DV) {  // the next scores run while A(j) is made
+        if (j + 1 < NB && !(ok = wait(Ly::B_SR, (uint32_t)(j & 1), j) && issue_s(j + 1))) break;
+        if (!(ok = wait(Ly::B_C1F + st, (uint32_t)((j / NST) & 1), j))) break;
+      }
+      if (!(ok = wait(Ly::B_DS + (j & 1), (uint32_t)((j >> 1) & 1), j))) break;
+      tc_fence_after();
       if (PASS == DV) {
-        sum(tmem + COL_ACC, tmem + COL_A, c1m + stage);
+        sum(j, tmem + COL_ACC, tmem + COL_A + 96u * (uint32_t)(j & 1), c1m + stage);
         tc_commit_warp(bar(Ly::B_C1E + st));
       } else {
 #pragma unroll
         for (int m = 0; m < 2; ++m)  // the map's box of 64 columns; at d = 64 both maps share one
-          sum(tmem + COL_ACC + 64u * m, tmem + COL_S + 96u * m, c0m + stage + (D == 128 ? (uint64_t)m * (Ly::CBOX >> 4) : 0ull));
+          sum(j, tmem + COL_ACC + 64u * m, tmem + COL_S + 96u * m, c0m + stage + (D == 128 ? (uint64_t)m * (Ly::CBOX >> 4) : 0ull));
         tc_commit_warp(bar(Ly::B_C0E + st));
+        // into the place of dS(j)'s pieces, which those products have read
+        if (j + 1 < NB) ok = issue_dp(j + 1) && issue_s(j + 1);
       }
       if (j + 1 == NB) tc_commit_warp(bar(Ly::B_ACC));
     }
@@ -378,7 +410,8 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       const int st = j % NST;
       const uint32_t ph = (uint32_t)((j / NST) & 1);
       const int32_t s0 = (c_begin + j) * BS;
-      for (int w = 0; w < 2 && ok; ++w) {
+      for (int i = 0; i < 2 && ok; ++i) {
+        const int w = PASS == DV ? i : 1 - i;  // in the order in which the stages become free
         const int full = (w ? Ly::B_C1F : Ly::B_C0F) + st, empty = (w ? Ly::B_C1E : Ly::B_C0E) + st;
         ok = mbar_wait(bar(empty), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, j);
         if (!ok) break;
@@ -421,7 +454,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) diff_bwd32_kernel(const __grid
       mbar_init(bar(Ly::B_C1E + s), 1);
     }
     mbar_init(bar(Ly::B_S), 1);
-    mbar_init(bar(Ly::B_DS), N_EW);
+    mbar_init(bar(Ly::B_SR), N_EW);
+    mbar_init(bar(Ly::B_DS), N_EW);  // two: dV's A(j + 1) may be there before the issuer has looked at A(j)
+    mbar_init(bar(Ly::B_DS + 1), N_EW);
     mbar_init(bar(Ly::B_ACC), 1);
     mbar_init(bar(Ly::B_DRAIN), 1);
     wait_for_kernel_before();
