@@ -129,6 +129,22 @@ def test_one_lam_for_all_heads_and_signs(lib, dtype):
         check_grads(grads, OD.backward(q, k, v, lam, g, True), dtype, 150, 2)
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 1, 2304, 128, True), (1, 3, 1, 900, 64, False), (2, 8, 2, 1250, 64, False)], ids=str)
+def test_few_tiles_and_a_last_wave_of_few(lib, shape):
+    """Tiles cut into parts: all of 18 or 24, short ones among them that have fewer blocks than parts, and 8 of 160."""
+    B, Hq, Hkv, S, d, causal = shape
+    q, k, v, lam, _ = inputs(B, Hq, Hkv, S, d, "bf16", 41)
+    dev = [t.cuda() for t in (q, k, v, lam)]
+    plan = lib.mesh_attn_plan_create(S, 1, causal)
+    outs = []
+    for fill in (0, 255):
+        ws = lib.new_diff_workspace(plan, dev[0], dev[1]).fill_(fill)
+        outs.append(lib.mesh_diff_attention(*dev, 1, causal, plan=plan, workspace=ws, return_saved=True))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    check_out(outs[0][0], outs[0][2], OD.forward(q, k, v, lam, causal), "bf16", S)
+
+
 def test_large_scores(lib):
     """Scores of some hundred: the running maximum moves, most weights vanish."""
     q, k, v, lam, g = inputs(1, 2, 2, 300, 128, "bf16", 23, k_scale=16.0)

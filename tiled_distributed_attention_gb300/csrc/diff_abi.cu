@@ -58,8 +58,9 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
   const bool q_slots = plan.n_slots() != plan.P && plan.L >= 128 && 4 * tiles * Hq < MAX_SMS;
   const bool kv_slots = plan.n_kv_slots() != plan.P && plan.L >= 128 && 4 * tiles * Hkv < MAX_SMS;
   if (!backward) {
-    if (f32 || q_slots) {  // fp32: both maps' outputs always go through the merge
-      const size_t rows = 2 * (q_slots ? std::max(prows, qrows) : qrows);
+    // fp32: both maps' outputs always go through the merge; bf16: those of tiles cut into parts
+    if (const size_t rows = 2 * (f32 ? (q_slots ? std::max(prows, qrows) : qrows)
+                                     : (size_t)diff_fwd_max_parts(plan.S, B, Hq, plan.causal) * 128)) {
       w.part_o = take(rows * d * 4);
       w.part_lse = take(rows * 4);
     }
@@ -276,7 +277,7 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     t.pieces = a.ws + w.pieces;
     t.pieces_ready = true;
     if ((rc = launch_status(mesh::launch_tile_fwd_tc32(t, stream, &err), err))) return rc;
-    return launch_status(mesh::launch_diff_merge(a, w, dtype, direct, stream, &err), err);
+    return launch_status(mesh::launch_diff_merge(a, w, direct, stream, &err), err);
   });
 }
 

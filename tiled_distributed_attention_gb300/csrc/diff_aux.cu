@@ -18,15 +18,7 @@ constexpr int THREADS = 256;
 constexpr int MAX_SLOTS = 64;  // R <= 64 for P <= 4096
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
@@ -81,7 +73,7 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const DiffArgs a, uint2*
 // O = sum_t w1_t O1_t - lam sum_t w2_t O2_t over a row's slots, w = exp(lse_t - lse) of each map, and
 // the second map's output, which the backward pass needs.  A CTA owns ROWS rows of one (batch,
 // head, partition); a thread a 16-byte piece of both maps.
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const float* part_o, const float* part_lse,
                                                         const int32_t* slot_off, int P, int64_t L, int n_slots, int n_rblk) {
   constexpr int Q4 = D / 4;
@@ -133,7 +125,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
     if (r < nrows) a.LSE[(2 * (int64_t)bh + m) * a.S + (int64_t)p * L + r0 + r] = W > 0.f ? Ms + logf(W) : -INFINITY;
   }
   __syncthreads();
-  const float lam = lam_of<T>(a.lam, a.lam_n, bh % a.Hq);
+  const float lam = lam_of<float>(a.lam, a.lam_n, bh % a.Hq);
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
     const int idx = tid + k * THREADS, r = idx / Q4, c = idx % Q4 * 4;
@@ -155,9 +147,9 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
       }
     }
     const int64_t at = ((int64_t)bh * a.S + (int64_t)p * L + r0 + r) * D + c;
-    store4(static_cast<T*>(a.O) + at, make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
-                                                  fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
-    if (a.O2) store4(static_cast<T*>(a.O2) + at, o[1]);
+    store4(static_cast<float*>(a.O) + at, make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
+                                                      fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
+    if (a.O2) store4(static_cast<float*>(a.O2) + at, o[1]);
   }
 }
 
@@ -275,7 +267,7 @@ int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, s
                     "diff split launch", err);
 }
 
-template <int D, typename T>
+template <int D>
 static int merge_d(const DiffArgs& a, const DiffWorkspace& w, bool flat, cudaStream_t st, std::string* err) {
   constexpr int ROWS = 2 * daux::THREADS / (D / 4);
   const int64_t L = flat ? a.S : a.L;
@@ -287,19 +279,16 @@ static int merge_d(const DiffArgs& a, const DiffWorkspace& w, bool flat, cudaStr
     return (int)cudaErrorInvalidConfiguration;
   }
   const cudaError_t e = launch_behind(
-      daux::merge_kernel<D, T>, dim3((unsigned)blocks), daux::THREADS, 0, st, a, reinterpret_cast<const float*>(a.ws + w.part_o),
+      daux::merge_kernel<D>, dim3((unsigned)blocks), daux::THREADS, 0, st, a, reinterpret_cast<const float*>(a.ws + w.part_o),
       reinterpret_cast<const float*>(a.ws + w.part_lse),
       reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + (flat ? a.tl.flat_list : a.tl.slot_off)), P, L,
       (int)(flat ? 1 : a.n_slots), (int)n_rblk);
   return daux::done(e, "diff merge launch", err);
 }
 
-int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool flat, void* stream,
-                      std::string* err) {
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, bool flat, void* stream, std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
-  if (dt == MESH_ATTN_BF16)
-    return a.d == 128 ? merge_d<128, __nv_bfloat16>(a, w, flat, st, err) : merge_d<64, __nv_bfloat16>(a, w, flat, st, err);
-  return a.d == 128 ? merge_d<128, float>(a, w, flat, st, err) : merge_d<64, float>(a, w, flat, st, err);
+  return a.d == 128 ? merge_d<128>(a, w, flat, st, err) : merge_d<64>(a, w, flat, st, err);
 }
 
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {

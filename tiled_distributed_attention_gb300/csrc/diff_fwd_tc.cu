@@ -11,10 +11,11 @@
 // for one half of the columns and writes O = O_1 / l_1 - lam O_2 / l_2 (and O_2 for the backward
 // pass) rounded once; no partial output leaves the SM.
 //
-// A work unit is (batch, KV head, work item, query head of the group, 128-row query tile); causal units
-// go heaviest first within batches of heads that fill the grid a few times (Params::batch).  The work
-// item is the whole sequence where its tiles alone fill the GPU; with fewer the plan's items split the
-// keys, and normalised partial outputs and LSEs of both maps go to the merge (launch_diff_fwd_tc).
+// A work unit is (batch, KV head, query head of the group, 128-row query tile); causal units go heaviest
+// first within batches of heads that fill the grid a few times (Params::batch).  Where tiles would
+// leave most SMs idle, all of them (few tiles) or those of the last, mostly empty wave (equal tiles without a
+// mask) are cut into parts of their keys: a part leaves its normalised outputs and LSEs, which
+// merge_parts_kernel adds up (choose_parts).
 //
 // Per 128 x 128 block and head: 2 x 4 score products and 2 x 8 PV products of 64 cycles each at
 // d = 128 (1,536 cycles), 32,768 exponentials.  P is rounded to bf16 for its product (2^-9 relative
@@ -58,6 +59,7 @@ constexpr float LOG2_RESCALE = 8.0f;
 // Row sum of one block accepted without a max pass: every term is then at most 2^16, and a sum
 // this large implies a row maximum more than 2^LOG2_RESCALE above the reference (2^16 / BN > 2^8).
 constexpr float SUM_ACCEPT = 65536.0f;
+constexpr int MAX_PARTS = 16;          // of a tile (choose_parts)
 constexpr int64_t DRAIN_NS = 200000000;  // exit-path waits for copies in flight
 
 // roles recorded with an error
@@ -84,63 +86,61 @@ struct Layout {
 };
 
 struct Params {
-  const DevItem* items;
-  const int32_t* kv_list;
   const TablesHeader* header;
   uint64_t tag;
   const __nv_bfloat16* lam;
-  __nv_bfloat16* o;   // direct: O, O2 (or NULL) and LSE
+  __nv_bfloat16* o;  // O, O2 (or NULL) and LSE
   __nv_bfloat16* o2;
   float* lse;
-  float* part_o;      // through the merge: partials of 2 Hq heads, NULL otherwise
+  float* part_o;  // of the tiles in parts: [part][map][128][D], and their LSEs [part][map][128]
   float* part_lse;
   int32_t* status;
   uint32_t* counter;
-  int64_t S, L;
-  int32_t B, Hq, Hkv, P, n_items, n_slots, nqt, n_units, causal, lam_n;
-  int32_t batch;  // (head, work item) lanes whose tiles are numbered together
+  int64_t S;
+  int32_t B, Hq, Hkv, nqt, n_tiles, n_whole, parts, n_units, causal, lam_n;
+  int32_t batch;  // heads whose tiles are numbered together
   float scale_log2;
   int64_t wait_limit_ns;
 };
 
-// What every role derives from a unit index.  A lane is (batch, KV head, work item, query head of the
-// group), the last fastest; units are numbered batch of lanes by batch, within it tile by tile (causal: from
-// the longest), within a tile lane by lane.  With batch = 1 the units running at once share one
-// KV head's keys in L2; a few lanes together keep the last units short where their lengths differ.
+// What every role derives from a unit index: the first n_whole units are whole tiles, of the other tiles
+// each has `parts`.  A lane is (batch, query head); tiles are numbered batch of lanes by batch, within it
+// row by row (causal: from the longest), within a row lane by lane.  With batch = 1 the units running
+// at once share one KV head's keys in L2; a few lanes together keep the last units short where
+// their lengths differ.
 struct Unit {
   int b, h, hk, qt;
-  DevItem it;
-  bool ok;  // item indices in range
-  int nb;   // 128-key blocks per KV partition
+  int part;      // index of its partial outputs, or -1: a whole tile
+  int blk0, NB;  // its 128-key blocks; a part may be left without
 };
 
-__device__ __forceinline__ Unit decode(int u, const Params& prm) {
+// Parts of a tile that sees nbk blocks, and what tile x is.
+__device__ __forceinline__ int parts_of(int nbk, const Params& prm) { return min(prm.parts, nbk); }
+__device__ __forceinline__ Unit decode_tile(int t, const Params& prm) {
   Unit x;
-  const int g = prm.Hq / prm.Hkv;
-  const int per = prm.batch * prm.nqt, first = u / per * prm.batch;
-  const int lanes = min(prm.batch, prm.n_units / prm.nqt - first);  // the last batch may be smaller
-  u %= per;
-  x.qt = u / lanes;
+  const int per = prm.batch * prm.nqt, first = t / per * prm.batch;
+  const int lanes = min(prm.batch, prm.n_tiles / prm.nqt - first);  // the last batch may be smaller
+  t %= per;
+  x.qt = t / lanes;
   if (prm.causal) x.qt = prm.nqt - 1 - x.qt;
-  u = first + u % lanes;
-  const int gi = u % g;
-  u /= g;
-  const int item = u % prm.n_items;
-  u /= prm.n_items;
-  x.hk = u % prm.Hkv;
-  x.b = u / prm.Hkv;
-  x.h = x.hk * g + gi;
-  x.it = prm.items[item];
-  x.ok = x.b < prm.B && x.it.p >= 0 && x.it.p < prm.P && x.it.slot >= 0 && x.it.slot < prm.n_slots &&
-         x.it.n_kv >= 1 && x.it.kv_off >= 0;
-  x.nb = (int)((prm.L + BN - 1) / BN);
+  t = first + t % lanes;
+  x.h = t % prm.Hq;
+  x.b = t / prm.Hq;
+  x.hk = x.h / (prm.Hq / prm.Hkv);
+  x.part = -1;
+  x.blk0 = 0;
+  x.NB = prm.causal ? min(prm.nqt, x.qt + 1) : prm.nqt;
   return x;
 }
-
-// 128-key blocks of KV partition k visited for query tile qt of partition p: only the causal
-// diagonal partition is cut short.
-__device__ __forceinline__ int blocks_of(int k, int p, int causal, int nb, int qt) {
-  return (causal && k == p) ? min(nb, qt + 1) : nb;
+__device__ __forceinline__ Unit decode(int u, const Params& prm) {
+  if (u < prm.n_whole) return decode_tile(u, prm);
+  const int e = u - prm.n_whole;
+  Unit x = decode_tile(prm.n_whole + e / prm.parts, prm);
+  const int k = parts_of(x.NB, prm), i = e % prm.parts, nbk = x.NB;
+  x.part = e;
+  x.blk0 = min(i, k) * nbk / k;
+  x.NB = min(i + 1, k) * nbk / k - x.blk0;
+  return x;
 }
 
 template <int D>
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::MISC_OFF);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + Ly::MISC_OFF + 4);
   volatile int32_t* unit_ring = reinterpret_cast<volatile int32_t*>(smem + Ly::MISC_OFF + 8);
-  const int64_t L = prm.L;
+  const int64_t S = prm.S;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
@@ -223,25 +223,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ++nu;
       if (u < 0) break;
       const Unit x = decode(u, prm);
-      if (!x.ok) break;
-      const int p = x.it.p;
+      if (x.NB == 0) continue;
       const int a_t = x.qt;
-      const int32_t* kvl = prm.kv_list + x.it.kv_off;
       float m_used = -INFINITY, l_sum = 0.f;
-      for (int ki = 0; ki < x.it.n_kv && ok; ++ki) {
-        const int k = __ldg(kvl + ki);
-        const bool diag = prm.causal && k == p;
-        const int nbk = blocks_of(k, p, prm.causal, x.nb, x.qt);
-        for (int jb = 0; jb < nbk; ++jb, ++cnt) {
+      {
+        for (int jb = x.blk0; jb < x.blk0 + x.NB; ++jb, ++cnt) {
           ok = mbar_wait(bar(Ly::B_SFULL + t), (uint32_t)(cnt & 1), prm.wait_limit_ns, abort_flag, prm.status,
                          ROLE_SOFTMAX, u);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          // mask: causal diagonal block (key column > query row) and keys past the partition
-          const int kv_valid = (int)min((int64_t)BN, L - (int64_t)jb * BN);
-          int lim = BN - 1;
-          if (diag) lim = (jb < a_t) ? BN - 1 : (jb == a_t ? row : -1);
+          // mask: causal diagonal block (key column > query row) and keys past the end
+          const int kv_valid = (int)min((int64_t)BN, S - (int64_t)jb * BN);
+          int lim = prm.causal && jb == a_t ? row : BN - 1;
           lim = min(lim, kv_valid - 1);
           // The exponentials use the row's running reference m_used, which only ever grows.  A
           // block whose row maximum stays within 2^LOG2_RESCALE of it needs no maximum at all, so
@@ -335,12 +329,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) break;
       tc_fence_after();
       const int64_t row_local = (int64_t)a_t * BM + row;
-      const int64_t wrow0 = row_local - lane;  // warp's first row in the partition
+      const int64_t wrow0 = row_local - lane;  // warp's first row
       // a row without a visible key: O_m = 0, LSE = -inf (a NaN sum stays NaN)
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
       const float lse = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * 0.69314718055994531f;
-      if (prm.part_o == nullptr) {
-        // ---- direct: this warpgroup's half of the columns of both maps.  1 / l of the other map comes
+      if (x.part < 0) {
+        // ---- a whole tile: this warpgroup's half of the columns of both maps.  1 / l of the other map comes
         // through shared memory; it is written after OFINAL, which the previous unit's readers precede
         // (the products behind OFINAL waited for their OFREE).
         constexpr int CW = D / 2, NC = CW / 8;  // columns, 16-byte pieces of a row
@@ -362,7 +356,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_arrive(bar(Ly::B_OFREE));
         ++uses;
         const float lam = __bfloat162float(prm.lam[prm.lam_n == 1 ? 0 : x.h]);
-        const int64_t grow = ((int64_t)x.b * prm.Hq + x.h) * prm.S + (int64_t)p * L;  // the partition's first row
+        const int64_t grow = ((int64_t)x.b * prm.Hq + x.h) * S;  // the head's first row
         uint32_t w[CW / 2];
         uint4* stage = reinterpret_cast<uint4*>(epi);
         // 32 rows through the shared stage, so that each store writes whole 128-byte (64 at d = 64) row pieces
@@ -376,7 +370,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < NC; ++i) {
             const int r = i * (32 / NC) + lane / NC, q = lane % NC;
             const uint4 v = stage[r * NC + (q ^ (r & (NC - 1)))];
-            if (wrow0 + r < L)
+            if (wrow0 + r < S)
               *reinterpret_cast<uint4*>(out + (grow + wrow0 + r) * D + t * CW + q * 8) = v;
           }
         };
@@ -392,11 +386,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int c = 0; c < CW; c += 2) w[c / 2] = pack_bf16x2(o2[c], o2[c + 1]);
           put(prm.o2);
         }
-        if (row_local < L)
-          prm.lse[(((int64_t)x.b * prm.Hq + x.h) * 2 + t) * prm.S + (int64_t)p * L + row_local] = lse;
+        if (row_local < S) prm.lse[(((int64_t)x.b * prm.Hq + x.h) * 2 + t) * S + row_local] = lse;
         continue;
       }
-      // ---- through the merge: this map's normalised partial output
+      // ---- a part: this map's normalised output of it
       float o[D];
 #pragma unroll
       for (int c = 0; c < D; c += 32) tmem_ld32(tm_o + (uint32_t)c, o + c);
@@ -404,7 +397,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_before();
       mbar_arrive(bar(Ly::B_OFREE));
       ++uses;
-      const int64_t prow = ((((int64_t)x.b * prm.Hq + x.h) * 2 + t) * prm.n_slots + x.it.slot) * L + row_local;
+      const int64_t prow = ((int64_t)x.part * 2 + t) * BM + row;
       float* dst0 = prm.part_o + (prow - lane) * D;
       __syncwarp();
 #pragma unroll
@@ -419,11 +412,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int i = 0; i < 8; ++i) {
           const int r = i * 4 + (lane >> 3), qq = lane & 7;
           const float4 v = *reinterpret_cast<const float4*>(epi + r * 32 + ((qq ^ (r & 7)) * 4));
-          if (wrow0 + r < L) *reinterpret_cast<float4*>(dst0 + (int64_t)r * D + c + qq * 4) = v;
+          if (wrow0 + r < S) *reinterpret_cast<float4*>(dst0 + (int64_t)r * D + c + qq * 4) = v;
         }
         __syncwarp();
       }
-      if (row_local < L) prm.part_lse[prow] = lse;
+      if (row_local < S) prm.part_lse[prow] = lse;
     }
   } else {
     regs_dec<OTHER_REGS>();
@@ -462,7 +455,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int kk = 0; kk < BN / 16; ++kk)
           tc_mma_ts_warp(tm_o, tm_p + (uint32_t)(kk * 8), vd + (uint64_t)(kk * 128), idesc_pv, (!first || kk > 0) ? 1u : 0u);
       };
-      int nu = 0, nblk = 0, cnt = 0;
+      int nu = 0, nq = 0, nblk = 0, cnt = 0;
       bool ok = true;
       while (ok) {
         const int slot = nu & 1;
@@ -473,14 +466,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Ly::B_UEMPTY + slot));
         __syncwarp();
-        const int uidx = nu++;
+        ++nu;
         if (u < 0) break;
-        const Unit x = decode(u, prm);
-        if (!x.ok) break;
-        const int32_t* kvl = prm.kv_list + x.it.kv_off;
+        const int NB = decode(u, prm).NB;
+        if (NB == 0) continue;
+        const int uidx = nq++;  // units with work
         const int qb = uidx & 1;
-        int NB = 0;
-        for (int ki = 0; ki < x.it.n_kv; ++ki) NB += blocks_of(__ldg(kvl + ki), x.it.p, prm.causal, x.nb, x.qt);
         ok = mbar_wait_warp(bar(Ly::B_QFULL + qb), (uint32_t)((uidx >> 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
                             ROLE_MMA, u);
         if (ok)
@@ -556,53 +547,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int u = ok ? publish() : -1;
       while (ok && u >= 0) {
         const Unit x = decode(u, prm);
-        if (!x.ok) {
-          record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_ITEM, u);
-          *abort_flag = 1;
-          break;
-        }
         // publish the following unit now and pull its Q tile and first K/V block into L2, so
         // the unit boundary does not wait on DRAM
         const int un = publish();
         if (!ok) break;
         if (un >= 0) {
           const Unit xn = decode(un, prm);
-          if (xn.ok) {
-            const int32_t qp = (xn.b * prm.Hq + xn.h) * prm.P + xn.it.p;
-            for (int c = 0; c < D / 64; ++c) tma_prefetch_l2_3d(&tmQ, c * 64, xn.qt * BM, qp);
-            const int kn = __ldg(prm.kv_list + xn.it.kv_off);
-            if (kn >= 0 && kn < prm.P) {
-              const int32_t kp = (xn.b * prm.Hkv + xn.hk) * prm.P + kn;
-              for (int c = 0; c < D / 64; ++c) {
-                tma_prefetch_l2_3d(&tmK, c * 64, 0, kp);
-                tma_prefetch_l2_3d(&tmV, c * 64, 0, kp);
-              }
-            }
+          const int32_t qp = xn.b * prm.Hq + xn.h, kp = xn.b * prm.Hkv + xn.hk;
+          for (int c = 0; c < D / 64; ++c) {
+            tma_prefetch_l2_3d(&tmQ, c * 64, xn.qt * BM, qp);
+            tma_prefetch_l2_3d(&tmK, c * 64, xn.blk0 * BN, kp);
+            tma_prefetch_l2_3d(&tmV, c * 64, xn.blk0 * BN, kp);
           }
+        }
+        if (x.NB == 0) {
+          u = un;
+          continue;
         }
         // Q tile: the last S products of the unit before last must be done with this buffer
         const int qb = nq & 1;
         ok = mbar_wait(bar(Ly::B_QEMPTY + qb), (uint32_t)(((nq >> 1) & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
                        ROLE_LOAD, u);
         if (!ok) break;
-        const int32_t qp = (x.b * prm.Hq + x.h) * prm.P + x.it.p;
+        const int32_t qp = x.b * prm.Hq + x.h, kp = x.b * prm.Hkv + x.hk;
         mbar_expect_tx(bar(Ly::B_QFULL + qb), Ly::TILE);
         for (int c = 0; c < D / 64; ++c)
           tma_load_3d(sb + Ly::Q_OFF + (uint32_t)qb * Ly::TILE + (uint32_t)c * Ly::BOX, &tmQ, c * 64, x.qt * BM, qp,
                       bar(Ly::B_QFULL + qb));
         ++nq;
-        const int32_t* kvl = prm.kv_list + x.it.kv_off;
-        for (int ki = 0; ki < x.it.n_kv && ok; ++ki) {
-          const int k = __ldg(kvl + ki);
-          if (k < 0 || k >= prm.P) {
-            record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_LOAD, u);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          const int32_t kp = (x.b * prm.Hkv + x.hk) * prm.P + k;
-          const int nbk = blocks_of(k, x.it.p, prm.causal, x.nb, x.qt);
-          for (int jb = 0; jb < nbk; ++jb) {
+        {
+          for (int jb = x.blk0; jb < x.blk0 + x.NB; ++jb) {
             const int st = nk % NST;
             const uint32_t ph = (uint32_t)((nk / NST) & 1);
             ok = mbar_wait(bar(Ly::B_KEMPTY + st), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, u);
@@ -638,6 +612,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == WARP_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// O = sum_t w1_t O1_t - lam sum_t w2_t O2_t over a tile's parts, w = exp(lse_t - lse) of each map, O2 and the LSEs.
+// A thread takes a 16-byte piece of one map's row, all parts' loads in flight together; a CTA a few rows, so
+// that the few tiles there are still fill the GPU.
+constexpr int MERGE_THREADS = 256;
+template <int D>
+constexpr int MERGE_ROWS = MERGE_THREADS / (D / 2);
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_parts_kernel(const Params prm) {
+  constexpr int Q4 = D / 4, ROWS = MERGE_ROWS<D>, PER_TILE = BM / ROWS;
+  __shared__ float4 o2_s[ROWS * Q4];
+  wait_for_kernel_before();
+  if (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) return;
+  const int i = (int)blockIdx.x / PER_TILE, r0 = (int)blockIdx.x % PER_TILE * ROWS;
+  const int m = (int)threadIdx.x / (ROWS * Q4), at = (int)threadIdx.x % (ROWS * Q4), r = r0 + at / Q4, c = at % Q4 * 4;
+  const Unit x = decode_tile(prm.n_whole + i, prm);
+  const int k = parts_of(x.NB, prm);
+  const int64_t row = (int64_t)x.qt * BM + r, head = (int64_t)x.b * prm.Hq + x.h;
+  const bool in = row < prm.S;
+  const int64_t base = ((int64_t)i * prm.parts * 2 + m) * BM + r;  // row of part t: base + 2 t BM
+  float w[MAX_PARTS];
+  float4 v[MAX_PARTS];
+#pragma unroll
+  for (int t = 0; t < MAX_PARTS; ++t) {
+    const bool there = in && t < k;
+    w[t] = there ? prm.part_lse[base + 2 * t * BM] : -INFINITY;
+    v[t] = there ? __ldcs(reinterpret_cast<const float4*>(prm.part_o + (base + 2 * t * BM) * D + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float M = -INFINITY, W = 0.f;
+#pragma unroll
+  for (int t = 0; t < MAX_PARTS; ++t) M = fmaxf(M, w[t]);
+  const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int t = 0; t < MAX_PARTS; ++t) {
+    w[t] = __expf(w[t] - Ms);
+    W += w[t];
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;  // a NaN sum stays NaN
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int t = 0; t < MAX_PARTS; ++t) {
+    const float f = t < k ? w[t] * inv : 0.f;
+    o.x = fmaf(f, v[t].x, o.x);
+    o.y = fmaf(f, v[t].y, o.y);
+    o.z = fmaf(f, v[t].z, o.z);
+    o.w = fmaf(f, v[t].w, o.w);
+  }
+  const int64_t dst = (head * prm.S + row) * D + c;
+  if (m == 1) {
+    o2_s[at] = o;
+    if (in && prm.o2) *reinterpret_cast<uint2*>(prm.o2 + dst) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  }
+  if (in && c == 0) prm.lse[(2 * head + m) * prm.S + row] = W == 0.f ? -INFINITY : Ms + logf(W);
+  __syncthreads();
+  if (m == 0 && in) {
+    const float lam = __bfloat162float(prm.lam[prm.lam_n == 1 ? 0 : x.h]);
+    const float4 y = o2_s[at];
+    *reinterpret_cast<uint2*>(prm.o + dst) = make_uint2(pack_bf16x2(fmaf(-lam, y.x, o.x), fmaf(-lam, y.y, o.y)),
+                                                        pack_bf16x2(fmaf(-lam, y.z, o.z), fmaf(-lam, y.w, o.w)));
   }
 }
 
@@ -678,50 +713,63 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
   return true;
 }
 
+// Which tiles are cut into parts.  A part costs its tile's share of the blocks; the parts and their merge cost
+// about as much as four blocks (5 us at 1.25 us a block), so a cut has to save more.  All tiles: where at
+// most half of the SMs would have one (18 tiles of up to 18 blocks, causal: 31 -> 19 us).  The last wave's:
+// tiles without a mask all take the same time, and a wave with few of them takes as long as a full one (320 tiles
+// of 20 blocks on 152 SMs: 90 -> 79 us).
+struct Parts {
+  int64_t whole, parts;  // tiles in one piece; parts of each of the others
+};
+static Parts choose_parts(int64_t tiles, int64_t nb, bool causal, int sms) {
+  const int64_t tail = 2 * tiles <= sms ? tiles : causal || tiles < sms ? 0 : tiles % sms;
+  if (tail == 0 || 2 * tail > sms) return {tiles, 1};
+  const int64_t parts = std::min<int64_t>({sms / tail, nb / 2, MAX_PARTS});
+  if (parts < 2 || nb - nb / parts <= 4) return {tiles, 1};
+  return {tiles - tail, parts};
+}
+
 template <int D>
-static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direct, cudaStream_t st, std::string* err) {
-  const char* tb = static_cast<const char*>(a.tables);
+static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, cudaStream_t st, std::string* err) {
   Params prm{};
-  prm.header = reinterpret_cast<const TablesHeader*>(tb);
+  prm.header = static_cast<const TablesHeader*>(a.tables);
   prm.tag = a.tag;
-  prm.items = reinterpret_cast<const DevItem*>(tb + (direct ? a.tl.flat_item : a.tl.items));
-  prm.kv_list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : a.tl.kv_list));
   prm.lam = static_cast<const __nv_bfloat16*>(a.lam);
   prm.o = static_cast<__nv_bfloat16*>(a.O);
   prm.o2 = static_cast<__nv_bfloat16*>(a.O2);
   prm.lse = a.LSE;
-  prm.part_o = direct ? nullptr : reinterpret_cast<float*>(a.ws + w.part_o);
-  prm.part_lse = direct ? nullptr : reinterpret_cast<float*>(a.ws + w.part_lse);
+  prm.part_o = reinterpret_cast<float*>(a.ws + w.part_o);
+  prm.part_lse = reinterpret_cast<float*>(a.ws + w.part_lse);
   prm.status = a.status;
   prm.counter = reinterpret_cast<uint32_t*>(a.ws + w.counters);
   prm.S = a.S;
-  prm.L = direct ? a.S : a.L;
   prm.B = a.B;
   prm.Hq = a.Hq;
   prm.Hkv = a.Hkv;
-  prm.P = direct ? 1 : a.P;
-  prm.n_items = direct ? 1 : a.n_slots;
-  prm.n_slots = direct ? 1 : a.n_slots;
-  const int64_t nqt = (prm.L + BM - 1) / BM;
-  const int64_t units = nqt * prm.n_items * a.B * a.Hq;
-  if (units > 0x3fffffff) {
+  const int64_t nqt = (a.S + BM - 1) / BM, tiles = nqt * a.B * a.Hq;
+  if (tiles > 0x3fffffff) {
     *err = "too many work units for one launch";
     return (int)cudaErrorInvalidConfiguration;
   }
+  const Parts cut = choose_parts(tiles, nqt, a.causal, sms);
+  const int64_t n_cut = tiles - cut.whole, units = cut.whole + n_cut * cut.parts;
   prm.nqt = (int32_t)nqt;
+  prm.n_tiles = (int32_t)tiles;
+  prm.n_whole = (int32_t)cut.whole;
+  prm.parts = (int32_t)cut.parts;
   prm.n_units = (int32_t)units;
   prm.causal = a.causal;
   // enough lanes for about three times the grid
-  prm.batch = a.causal ? (int32_t)std::min<int64_t>(units / nqt, (3LL * sms + nqt - 1) / nqt) : 1;
+  prm.batch = a.causal ? (int32_t)std::min<int64_t>(tiles / nqt, (3LL * sms + nqt - 1) / nqt) : 1;
   prm.lam_n = a.lam_n;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
   EncodeTiledFn enc = get_encode(err);
   if (!enc) return (int)cudaErrorNotSupported;
   CUtensorMap mq, mk, mv;
-  if (!make_map(enc, &mq, a.Q, (uint64_t)prm.L, (uint64_t)a.B * a.Hq * prm.P, D, err) ||
-      !make_map(enc, &mk, a.K, (uint64_t)prm.L, (uint64_t)a.B * a.Hkv * prm.P, D, err) ||
-      !make_map(enc, &mv, a.V, (uint64_t)prm.L, (uint64_t)a.B * a.Hkv * prm.P, D, err))
+  if (!make_map(enc, &mq, a.Q, (uint64_t)a.S, (uint64_t)a.B * a.Hq, D, err) ||
+      !make_map(enc, &mk, a.K, (uint64_t)a.S, (uint64_t)a.B * a.Hkv, D, err) ||
+      !make_map(enc, &mv, a.V, (uint64_t)a.S, (uint64_t)a.B * a.Hkv, D, err))
     return (int)cudaErrorInvalidValue;
   auto kern = diff_fwd_tc_kernel<D>;
   static OncePerDevice once;
@@ -739,6 +787,10 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
   }
   const unsigned grid = (unsigned)std::min<int64_t>(units, sms);  // persistent: one CTA per SM
   e = launch_behind(kern, dim3(grid), NUM_THREADS, Layout<D>::ALLOC, st, mq, mk, mv, prm);
+  if (e == cudaSuccess && n_cut > 0) {
+    const int64_t blocks = n_cut * (BM / MERGE_ROWS<D>);
+    e = launch_behind(merge_parts_kernel<D>, dim3((unsigned)blocks), MERGE_THREADS, 0, st, prm);
+  }
   if (e != cudaSuccess) *err = std::string("diff_fwd_tc launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
@@ -746,11 +798,15 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool direc
 }  // namespace dtc
 
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err) {
-  const bool direct = rows_direct(a, a.Hq, a.single_slot, sms);
   cudaStream_t st = (cudaStream_t)stream;
-  const int ce = a.d == 128 ? dtc::launch<128>(a, w, sms, direct, st, err) : dtc::launch<64>(a, w, sms, direct, st, err);
-  if (ce != (int)cudaSuccess || direct) return ce;
-  return launch_diff_merge(a, w, MESH_ATTN_BF16, false, stream, err);
+  return a.d == 128 ? dtc::launch<128>(a, w, sms, st, err) : dtc::launch<64>(a, w, sms, st, err);
+}
+
+// Parts there may be, whatever the number of SMs.
+int64_t diff_fwd_max_parts(int64_t S, int32_t B, int32_t Hq, bool causal) {
+  const int64_t nb = (S + dtc::BM - 1) / dtc::BM, tiles = nb * B * Hq;
+  if (nb <= 4 || (causal && 2 * tiles > MAX_SMS)) return 0;
+  return std::min<int64_t>(MAX_SMS, tiles * dtc::MAX_PARTS);
 }
 
 }  // namespace mesh

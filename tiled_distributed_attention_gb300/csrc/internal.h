@@ -218,8 +218,9 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
 // (2,304 tokens, one head) 32 whole, 26 by 9 partitions, 45 by 36 of 64 tokens; 128 blocks (8,192
 // tokens, two heads) 87 whole, 119 by 16 partitions.
 bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms);
-// bf16 forward on the tensor cores, with its merge where the plan's slots split the keys.
+// bf16 forward on the tensor cores, with its merge where tiles are cut into parts; the most parts there may be.
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
+int64_t diff_fwd_max_parts(int64_t S, int32_t B, int32_t Hq, bool causal);
 // bf16 backward: dK and dV, dQ and the sums behind dlam; either written as they are (direct) or as
 // partial sums per slot.
 int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, void* stream,
@@ -233,9 +234,8 @@ struct BwdPieces {
   size_t q, k, v, g, total;  // the bf16 pieces of Q, K, V and dO ([3][rows][d] each), in bytes
 };
 BwdPieces bwd32_pieces_layout(int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d);
-// `flat`: the partials are of the whole sequence as one partition with one slot.
-int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, bool flat, void* stream,
-                      std::string* err);
+// fp32 forward's merge; `flat`: the partials are of the whole sequence as one partition with one slot.
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, bool flat, void* stream, std::string* err);
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
 // dlam from n_part partial sums of every (batch, head).
 int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,
