@@ -27,9 +27,6 @@ TablesLayout tables_layout(const Plan& p) {
   t.slot_off = take(p.slot_off.size() * 4);
   t.items = take(p.dev_items.size() * sizeof(DevItem));
   t.kv_list = take(p.kv_list.size() * 4);
-  t.kv_slot_off = take(p.kv_slot_off.size() * 4);
-  t.kv_items = take(p.dev_kv_items.size() * sizeof(DevItem));
-  t.q_list = take(p.kv_q_list.size() * 4);
   t.total = at;
   return t;
 }
@@ -53,13 +50,12 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
   const size_t qrows = (size_t)B * Hq * plan.S;
   const size_t prows = (size_t)B * Hq * plan.n_slots() * (size_t)plan.L;
   const bool f32 = dt == MESH_ATTN_F32;
-  // bf16 needs partial sums only where the plan's slots split an axis (rows_direct)
-  const int64_t tiles = (plan.S + 127) / 128 * B;
-  const bool q_slots = plan.n_slots() != plan.P && plan.L >= 128 && 4 * tiles * Hq < MAX_SMS;
-  const bool kv_slots = plan.n_kv_slots() != plan.P && plan.L >= 128 && 4 * tiles * Hkv < MAX_SMS;
+  // fp32 forward: partial outputs where the plan's slots split the keys (rows_direct)
+  const int64_t nb = (plan.S + 127) / 128;
+  const bool slots = plan.n_slots() != plan.P && plan.L >= 128 && 8 * nb * B * Hq < MAX_SMS;
   if (!backward) {
     // fp32: both maps' outputs always go through the merge; bf16: those of tiles cut into parts
-    if (const size_t rows = 2 * (f32 ? (q_slots ? std::max(prows, qrows) : qrows)
+    if (const size_t rows = 2 * (f32 ? (slots ? std::max(prows, qrows) : qrows)
                                      : (size_t)diff_fwd_max_parts(plan.S, B, Hq, plan.causal) * 128)) {
       w.part_o = take(rows * d * 4);
       w.part_lse = take(rows * 4);
@@ -67,9 +63,10 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
     if (f32) w.pieces = take(f32_pieces_layout(B, 2 * Hq, Hkv, plan.S, d).total);
   } else {
     w.dsum = take(2 * qrows * 4);
-    // per (batch, head): fp32 one sum per 64 rows; bf16 eight per 128-row block of every slot
-    const int64_t by_slot = (int64_t)plan.n_slots() * ((plan.L + 127) / 128) * 8, flat = (plan.S + 127) / 128 * 8;
-    w.dlam_part = take((size_t)B * Hq * 4 * (size_t)(f32 ? (plan.S + 63) / 64 : q_slots ? std::max(by_slot, flat) : flat));
+    const BwdParts parts = diff_bwd_parts(plan.S, B, Hq, Hkv, plan.causal);
+    // per (batch, head): fp32 one sum per 64 rows; bf16 eight per part of a 128-row block
+    w.dlam_part = take((size_t)B * Hq * 4 * (size_t)(f32 ? (plan.S + 63) / 64 : nb * 8 * parts.dq));
+    const size_t kvrows = (size_t)B * Hkv * plan.S;
     if (f32) {  // partial sums of the splits, and of a KV head's query heads
       w.pieces = take(bwd32_pieces_layout(B, Hq, Hkv, plan.S, d).total);
       const size_t splits = (size_t)diff_bwd32_splits(plan.S, B, Hq, MAX_SMS);  // grows with the SM count
@@ -78,21 +75,20 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
         w.dk_part = take(splits * qrows * d * 4);
         w.dv_part = take(splits * qrows * d * 4);
       }
-    } else if (q_slots) {
-      w.dq_part = take(prows * d * 4);
-    }
-    if (!f32 && kv_slots) {
-      const size_t kv = (size_t)B * Hkv * plan.n_kv_slots() * (size_t)plan.L * d * 4;
-      w.dk_part = take(kv);
-      w.dv_part = take(kv);
+    } else {
+      if (parts.dq > 1) w.dq_part = take(parts.dq * qrows * d * 4);
+      if (parts.kv > 1) {
+        w.dk_part = take(parts.kv * kvrows * d * 4);
+        w.dv_part = take(parts.kv * kvrows * d * 4);
+      }
     }
   }
   w.total = at;
   return w;
 }
 
-bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms) {
-  return single || a.L < 128 || 4 * ((a.S + 127) / 128) * a.B * H >= sms;
+bool rows_direct(const DiffArgs& a, int32_t H, int sms) {
+  return a.single_slot || a.L < 128 || 4 * ((a.S + 127) / 128) * a.B * H >= sms;
 }
 
 }  // namespace mesh
@@ -168,10 +164,8 @@ DiffArgs make_args(const mesh_attn_plan* plan, const void* tables, int32_t B, in
   a.d = d;
   a.P = pl.P;
   a.n_slots = pl.n_slots();
-  a.n_kv_slots = pl.n_kv_slots();
   a.causal = pl.causal ? 1 : 0;
   a.single_slot = pl.n_slots() == pl.P;
-  a.single_kv_slot = pl.n_kv_slots() == pl.P;
   a.scale = scale;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.wait_limit_ns = mesh::current_wait_limit_ns();
@@ -211,9 +205,6 @@ int mesh_attn_plan_tables_write(const mesh_attn_plan* plan, void* out, size_t ou
     put(t.slot_off, p.slot_off.data(), p.slot_off.size() * 4);
     put(t.items, p.dev_items.data(), p.dev_items.size() * sizeof(mesh::DevItem));
     put(t.kv_list, p.kv_list.data(), p.kv_list.size() * 4);
-    put(t.kv_slot_off, p.kv_slot_off.data(), p.kv_slot_off.size() * 4);
-    put(t.kv_items, p.dev_kv_items.data(), p.dev_kv_items.size() * sizeof(mesh::DevItem));
-    put(t.q_list, p.kv_q_list.data(), p.kv_q_list.size() * 4);
     return (int)MESH_ATTN_OK;
   });
 }
@@ -253,7 +244,7 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     // that the plain fp32 tile kernel over 2 Hq heads gives both maps; then the merge
     int sms = 0;
     if ((rc = sm_count(&sms))) return rc;
-    const bool direct = mesh::rows_direct(a, 2 * Hq, a.single_slot, sms);
+    const bool direct = mesh::rows_direct(a, 2 * Hq, sms);
     if ((rc = launch_status(mesh::launch_diff_split(a, w, stream, &err), err))) return rc;
     mesh::TileArgs t{};
     const char* tb = static_cast<const char*>(tables);
@@ -307,36 +298,13 @@ int mesh_attn_diff_bwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     if (!is_aligned(dlam, dtype == MESH_ATTN_BF16 ? 2 : 4))
       return set_last_error(MESH_ATTN_ERR_MISALIGNED, "dlam must be aligned to its element size");
     std::string err;
-    const char* tb = static_cast<const char*>(tables);
-    auto reduce = [&](size_t part, size_t off, void* out, int32_t H, int32_t n) -> int {
-      mesh::ReduceArgs r{};
-      r.part = reinterpret_cast<const float*>(a.ws + part);
-      r.off = reinterpret_cast<const int32_t*>(tb + off);
-      r.out = out;
-      r.status = d_status;
-      r.S = a.S;
-      r.L = a.L;
-      r.B = B;
-      r.H = H;
-      r.d = d;
-      r.P = a.P;
-      r.n_slots = n;
-      return launch_status(mesh::launch_bwd_reduce(r, dtype, stream, &err), err);
-    };
     if (dtype == MESH_ATTN_BF16) {
       int sms = 0;
       if ((rc = sm_count(&sms))) return rc;
-      const bool dq_direct = mesh::rows_direct(a, Hq, a.single_slot, sms);
-      const bool kv_direct = mesh::rows_direct(a, Hkv, a.single_kv_slot, sms);
+      const mesh::BwdParts parts = mesh::diff_bwd_parts(a.S, B, Hq, Hkv, a.causal != 0);
       if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
-      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, kv_direct, dq_direct, stream, &err), err))) return rc;
-      if (!kv_direct) {
-        if ((rc = reduce(w.dk_part, a.tl.kv_slot_off, dK, Hkv, a.n_kv_slots))) return rc;
-        if ((rc = reduce(w.dv_part, a.tl.kv_slot_off, dV, Hkv, a.n_kv_slots))) return rc;
-      }
-      if (!dq_direct && (rc = reduce(w.dq_part, a.tl.slot_off, dQ, Hq, a.n_slots))) return rc;
-      const int64_t n = dq_direct ? (a.S + 127) / 128 * 8 : a.n_slots * ((a.L + 127) / 128) * 8;
-      return launch_status(mesh::launch_diff_dlam(a, w, dtype, n, stream, &err), err);
+      if ((rc = launch_status(mesh::launch_diff_bwd_tc(a, w, sms, parts, stream, &err), err))) return rc;
+      return launch_status(mesh::launch_diff_dlam(a, w, dtype, (a.S + 127) / 128 * 8 * parts.dq, stream, &err), err);
     }
     if ((rc = launch_status(mesh::launch_diff_prep(a, w, dtype, stream, &err), err))) return rc;
     int sms = 0;

@@ -20,19 +20,19 @@
 // The streamed blocks are 64 rows deep, half of the plain pass's: two score maps, dP and the
 // accumulators then fit the 512 TMEM columns at d = 128.
 //
-// dkdv (unit = KV slot, batch, KV head, 128-key block): K and V stay in shared memory, Q and dO blocks
+// dkdv (unit = batch, KV head, 128-key block, part): K and V stay in shared memory, Q and dO blocks
 // of 64 query rows stream.  TMEM: S_1^T | S_2^T | dP^T | A^T (two buffers) | dV | dK_1 | dK_2.
 //   Issue order per block i: [S(i) read] S(i+1)   [dS(i) and A(i) ready] dK(i), dP(i+1), dV(i).
 //   dS_1 and dS_2 (bf16) replace dP in its own columns.
-// dq (unit = work item, batch, head, 128-row block): Q and dO are copied into TMEM once per unit and
+// dq (unit = batch, head, 128-row block, part): Q and dO are copied into TMEM once per unit and
 // feed the products as A operands; K and V blocks of 64 keys stream.  TMEM: S_1 | S_2 | dP (two
 // buffers) | dQ_1 | dQ_2 | Q | dO.
 //   Issue order per block j: [S(j) read] S(j+1), dP(j+1)   [dS(j) ready] dQ(j).
 // At d = 64 a map's half is 32 columns: dK_m and dQ_m are computed 64 wide and half of them is used.
 //
-// Work items: the whole sequence where its blocks alone fill the GPU; the gradients are then written
-// from the accumulators, rounded once.  With fewer blocks the plan's slots split the other axis and
-// fp32 partial sums go to the reductions.  Rows past a partition's end are loaded as zeros.
+// The gradients are written from the accumulators, rounded once, where the blocks alone fill the GPU.  With
+// fewer, a unit is cut into parts of its streamed blocks (diff_bwd_parts), which leave fp32 sums that
+// sum_parts adds in order.  Rows past the end are loaded as zeros.
 // A, dS_1 and dS_2 are rounded to bf16 for their products (2^-9 relative a term); sums are fp32.
 // Every mbarrier wait is bounded; a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT, the CTA stops,
 // drains its copies and products and frees its tensor memory.
@@ -83,21 +83,19 @@ constexpr uint32_t COL_Q = 384;   // dq: Q [D / 2], then dO [D / 2] (bf16)
 __device__ __forceinline__ uint32_t ds_col(int m, int kk) { return (uint32_t)((kk >> 1) * 32 + m * 16 + (kk & 1) * 8); }
 
 struct Params {
-  const DevItem* items;  // rows: {p, slot, kv_off, n_kv}, or columns: {k, kv slot, q_off, n_q}
-  const int32_t* list;
   const float* lse;   // [B, Hq, 2, S]
   const float* dsum;  // [B, Hq, 2, S]
   const __nv_bfloat16* lam;
-  __nv_bfloat16* out0;  // direct: dQ, or dK
+  __nv_bfloat16* out0;  // dQ, or dK
   __nv_bfloat16* out1;  //         dV
-  float* part0;         // through the reductions (NULL otherwise): dQ, or dK
-  float* part1;         //         dV
-  float* dlam_part;     // [B, Hq, n_slots, nb, N_EW]
+  float* part0;         // of units in parts, [B, H, parts, S, D]: dQ, or dK
+  float* part1;         //                                              dV
+  float* dlam_part;     // [B, Hq, parts, nb, N_EW]
   int32_t* status;
   uint32_t* counter;
-  int64_t S, L;
-  int32_t B, Hq, Hkv, P, n_items, n_slots, nb, ns, causal, n_units, lam_n;  // nb 128-row blocks, ns 64-row blocks
-  int32_t batch;  // lanes whose units are numbered together (unit_of)
+  int64_t S;
+  int32_t B, Hq, Hkv, parts, nb, ns, causal, n_tiles, n_units, lam_n;  // nb 128-row blocks, ns 64-row blocks
+  int32_t batch;  // heads whose units are numbered together (unit_of)
   float scale, scale_log2;
   int64_t wait_limit_ns;
 };
@@ -190,105 +188,62 @@ __device__ __forceinline__ float lam_of(const Params& prm, int h) {
   return __bfloat162float(prm.lam[prm.lam_n == 1 ? 0 : h]);
 }
 
-// 64-key blocks of partition k visited by query block qb (128 rows) of partition p: on the causal
-// diagonal partition up to the query block's last row.
-__device__ __forceinline__ int kblocks_of(const Params& prm, int k, int p, int qb) {
-  return (prm.causal && k == p) ? min(prm.ns, 2 * qb + 2) : prm.ns;
-}
-// first 64-row query block of partition p visited by key block kb (128 keys) of partition k
-__device__ __forceinline__ int qblock_begin(const Params& prm, int k, int p, int kb) {
-  return (prm.causal && k == p) ? 2 * kb : 0;
-}
-
-// Key blocks of a dq unit in the order the producer loads them.
-struct KCursor {
-  int ki, kp, kb, n;
-  __device__ __forceinline__ void load(const Params& prm, const DevItem& it, int qb) {
-    kp = __ldg(prm.list + it.kv_off + ki);
-    kb = 0;
-    n = kblocks_of(prm, kp, it.p, qb);
-  }
-  __device__ __forceinline__ void start(const Params& prm, const DevItem& it, int qb) {
-    ki = 0;
-    load(prm, it, qb);
-  }
-  __device__ __forceinline__ void step(const Params& prm, const DevItem& it, int qb) {
-    if (++kb < n) return;
-    ++ki;
-    if (ki < it.n_kv) load(prm, it, qb);
-    else kp = -1;
-  }
-};
-
-// Query blocks of a dkdv unit: heads of the group, then the slot's Q partitions, then the partition's blocks.
-struct QCursor {
-  int h, qi, p, qb;
-  __device__ __forceinline__ void load(const Params& prm, const DevItem& it, int kb) {
-    p = __ldg(prm.list + it.kv_off + qi);
-    qb = qblock_begin(prm, it.p, p, kb);
-  }
-  __device__ __forceinline__ void start(const Params& prm, const DevItem& it, int kb, int h0) {
-    h = h0;
-    qi = 0;
-    load(prm, it, kb);
-  }
-  __device__ __forceinline__ void step(const Params& prm, const DevItem& it, int kb) {
-    if (++qb < prm.ns) return;
-    if (++qi >= it.n_kv) {
-      qi = 0;
-      ++h;
-    }
-    load(prm, it, kb);
-  }
-};
-
-// A unit of either kernel: a 128-row block `blk` of partition it.p of a (KV) head, and the number
-// of streamed blocks.
+// A unit of either pass: 128-row block `blk` of a (KV) head, and of its streamed blocks [start, start + NB).  A dq
+// unit streams 64-key blocks, a dkdv unit the 64-row blocks of the group's query heads, head after head; causal
+// units up to, or from, the diagonal.
 struct Unit {
-  int blk, h, b, NB;
-  DevItem it;
-  bool ok;
+  int blk, h, b, part, start, NB;
 };
+template <bool KV>
+__device__ __forceinline__ int blocks_of(int blk, int ns, int causal, int group) {
+  if (KV) return (ns - (causal ? 2 * blk : 0)) * group;
+  return causal ? min(ns, 2 * blk + 2) : ns;
+}
 template <bool KV>
 __device__ __forceinline__ Unit unit_of(int u, const Params& prm) {
   Unit x;
-  const int H = KV ? prm.Hkv : prm.Hq;
-  // numbered batch of (head, sequence, item) lanes by batch, within it block by block from the longest
-  const int per = prm.batch * prm.nb, first = u / per * prm.batch;
-  const int lanes = min(prm.batch, prm.n_units / prm.nb - first);  // the last batch may be smaller
-  u %= per;
-  x.blk = u / lanes;
+  const int H = KV ? prm.Hkv : prm.Hq, g = prm.Hq / prm.Hkv;
+  x.part = u % prm.parts;
+  int t = u / prm.parts;
+  // numbered batch of (batch, head) lanes by batch, within it block by block from the longest
+  const int per = prm.batch * prm.nb, first = t / per * prm.batch;
+  const int lanes = min(prm.batch, prm.n_tiles / prm.nb - first);  // the last batch may be smaller
+  t %= per;
+  x.blk = t / lanes;
   if (!KV && prm.causal) x.blk = prm.nb - 1 - x.blk;
-  u = first + u % lanes;
-  x.h = u % H;
-  u /= H;
-  x.b = u % prm.B;
-  const int idx = u / prm.B;
-  x.NB = 0;
-  x.ok = idx >= 0 && idx < prm.n_items;
-  if (!x.ok) return x;
-  x.it = prm.items[idx];
-  x.ok = x.it.p >= 0 && x.it.p < prm.P && x.it.slot >= 0 && x.it.slot < prm.n_slots && x.it.n_kv >= 1 && x.it.kv_off >= 0;
-  if (!x.ok) return x;
-  for (int i = 0; i < x.it.n_kv; ++i) {
-    const int o = __ldg(prm.list + x.it.kv_off + i);
-    x.NB += KV ? max(0, prm.ns - qblock_begin(prm, x.it.p, o, x.blk)) : kblocks_of(prm, o, x.it.p, x.blk);
-  }
-  if (KV) x.NB *= prm.Hq / prm.Hkv;
+  t = first + t % lanes;
+  x.h = t % H;
+  x.b = t / H;
+  const int n = blocks_of<KV>(x.blk, prm.ns, prm.causal, g), k = min(prm.parts, n);
+  x.start = (int)((int64_t)min(x.part, k) * n / k);
+  x.NB = (int)((int64_t)min(x.part + 1, k) * n / k) - x.start;  // none where there are fewer blocks than parts
   return x;
 }
-// A unit travels through the shared-memory ring decoded, so that consumers never wait on the global
-// reads of the decode.
+// A unit travels through the shared-memory ring decoded.
 __device__ __forceinline__ void put_unit(volatile int32_t* e, int u, const Unit& x) {
   e[0] = u;
-  e[1] = x.blk, e[2] = x.h, e[3] = x.b, e[4] = x.NB, e[5] = x.ok ? 1 : 0;
-  e[6] = x.it.p, e[7] = x.it.slot, e[8] = x.it.kv_off, e[9] = x.it.n_kv;
+  e[1] = x.blk, e[2] = x.h, e[3] = x.b, e[4] = x.NB, e[5] = x.part, e[6] = x.start;
 }
 __device__ __forceinline__ int get_unit(const volatile int32_t* e, Unit& x) {
-  x.blk = e[1], x.h = e[2], x.b = e[3], x.NB = e[4], x.ok = e[5] != 0;
-  x.it.p = e[6], x.it.slot = e[7], x.it.kv_off = e[8], x.it.n_kv = e[9];
+  x.blk = e[1], x.h = e[2], x.b = e[3], x.NB = e[4], x.part = e[5], x.start = e[6];
   return e[0];
 }
+
+// Query blocks of a dkdv unit: heads of the group, then a head's blocks.
+struct QCursor {
+  int h, qb, begin;
+  __device__ __forceinline__ void start(const Params& prm, const Unit& x) {
+    begin = prm.causal ? 2 * x.blk : 0;
+    const int n = prm.ns - begin;
+    h = x.h * (prm.Hq / prm.Hkv) + x.start / n;
+    qb = begin + x.start % n;
+  }
+  __device__ __forceinline__ void step(const Params& prm) {
+    if (++qb < prm.ns) return;
+    qb = begin;
+    ++h;
+  }
+};
 
 // What both kernels share: barrier set-up, the unit ring and the exit.
 template <int D, bool KV>
@@ -308,7 +263,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::MISC_OFF);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + Ly::MISC_OFF + 4);
   volatile int32_t* unit_ring = reinterpret_cast<volatile int32_t*>(smem + Ly::RING_OFF);
-  const int64_t L = prm.L;
+  const int64_t S = prm.S;
   const int g = prm.Hq / prm.Hkv;
 
   if (threadIdx.x == 0) {
@@ -343,6 +298,8 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       mbar_init(bar(Ly::B_UE + s), N_EW + 1 + (KV ? 0 : N_EPI));  // the warps that read a unit
     }
     wait_for_kernel_before();
+    // without any time to wait there is nothing to start: the first load would be waited for
+    if (prm.wait_limit_ns <= 0) record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
     *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -375,13 +332,6 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
     if (lane == 0) mbar_arrive(bar(Ly::B_UE + slot));
     ++nu;
     return true;
-  };
-  auto bad_unit = [&](int u, int role) {
-    if (lane == 0) {
-      record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, role, u);
-      *abort_flag = 1;
-    }
-    __syncwarp();
   };
   auto wait_all = [&](int b, uint32_t parity, int role, int unit) -> bool {  // warp-uniform
     const bool r = mbar_wait(bar(b), parity, prm.wait_limit_ns, abort_flag, prm.status, role, unit);
@@ -423,9 +373,9 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       int lam_h = -1;
       auto fetch = [&](const Unit& y, const QCursor& c) {
         const int64_t ql = (int64_t)c.qb * BS + vq;
-        raw_in = c.p >= 0 && c.p < prm.P && ql < L;
+        raw_in = ql < S;
         if (raw_in) {
-          const int64_t at = (((int64_t)y.b * prm.Hq + c.h) * 2 + (vec & 1)) * prm.S + (int64_t)c.p * L + ql;
+          const int64_t at = (((int64_t)y.b * prm.Hq + c.h) * 2 + (vec & 1)) * S + ql;
           raw = __ldg((vec < 2 ? prm.lse : prm.dsum) + at);
         }
         if (c.h != lam_h) {
@@ -445,24 +395,19 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       // cursors: block i, and the next one to fetch (i + 2, or the next unit's first)
       QCursor cur, nxt;
       float lam_cur = 0.f, lam_pub = 0.f;  // lam of block i and of the block published last
-      if (ok && v >= 0 && x.ok && x.NB >= 1) {
-        cur.start(prm, x.it, x.blk, x.h * g);
+      if (ok && v >= 0) {
+        cur.start(prm, x);
         fetch(x, cur);
         lam_pub = raw_lam;
         publish(0);
         nxt = cur;
         if (x.NB > 1) {
-          nxt.step(prm, x.it, x.blk);
+          nxt.step(prm);
           fetch(x, nxt);
         }
       }
       while (ok && v >= 0) {
-        if (!x.ok || x.NB < 1) {
-          bad_unit(v, ROLE_EW);
-          ok = false;
-          break;
-        }
-        const int k = x.it.p, kb = x.blk, NB = x.NB;
+        const int kb = x.blk, NB = x.NB;
         QCursor c1 = nxt;  // block i + 1
         for (int i = 0; i < NB && ok; ++i) {
           const int64_t gi = g0 + i;
@@ -476,7 +421,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
             lam_pub = raw_lam;
             publish(gi + 1);
             if (i + 2 < NB) {
-              nxt.step(prm, x.it, kb);
+              nxt.step(prm);
               fetch(x, nxt);
             }
           }
@@ -484,7 +429,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           ok = wait_all(Ly::B_VEC + vb, (uint32_t)((gi / 3) & 1), ROLE_EW, i);
           if (!ok) break;
           // causal diagonal: query columns before this key row are masked
-          const int lo = (prm.causal && cur.p == k) ? kb * BM + row - cur.qb * BS - c_base : 0;
+          const int lo = prm.causal ? kb * BM + row - cur.qb * BS - c_base : 0;
           ok = wait_all(Ly::B_S, (uint32_t)(gi & 1), ROLE_EW, i);
           if (!ok) break;
           tc_fence_after();
@@ -554,8 +499,8 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         Unit xn;
         ok = take(vn, xn, ROLE_EW);
         if (!ok) break;
-        if (vn >= 0 && xn.ok && xn.NB >= 1) {
-          cur.start(prm, xn.it, xn.blk, xn.h * g);
+        if (vn >= 0) {
+          cur.start(prm, xn);
           fetch(xn, cur);
         }
         // ---- epilogue: this half's columns of the dV and dK rows of this key block
@@ -566,7 +511,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           const uint32_t tm_dv = tmem + lane_base + COL_ACC + (uint32_t)(hf * (D / 2));
           // map hf's dK: columns [hf D / 2, + D / 2), at d = 64 the half of its 64-wide product that is its own
           const uint32_t tm_dk = tmem + lane_base + COL_DK + (uint32_t)(hf * 64 + (D == 64 ? hf * 32 : 0));
-          const int64_t rl = (int64_t)kb * BM + row;  // row in the partition
+          const int64_t rl = (int64_t)kb * BM + row;
           float acc[D / 2];
 #pragma unroll
           for (int which = 0; which < 2; ++which) {  // dV, then dK
@@ -576,16 +521,16 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
             for (int c = 0; c < D / 2; c += 32) tmem_ld32(tm + (uint32_t)c, acc + c);
             tc_wait_ld();
             if (which) arrive(Ly::B_ACCE);  // both accumulators are copied out: the next unit may overwrite them
-            if (prm.part0) {
-              const int64_t row0 = (((int64_t)x.b * prm.Hkv + x.h) * prm.n_slots + x.it.slot) * L + (int64_t)kb * BM + wq * 32;
-              const int rows_valid = (int)max((int64_t)0, min((int64_t)32, L - ((int64_t)kb * BM + wq * 32)));
+            if (prm.parts > 1) {
+              const int64_t row0 = (((int64_t)x.b * prm.Hkv + x.h) * prm.parts + x.part) * S + (int64_t)kb * BM + wq * 32;
+              const int rows_valid = (int)max((int64_t)0, min((int64_t)32, S - ((int64_t)kb * BM + wq * 32)));
 #pragma unroll
               for (int c = 0; c < D / 2; c += 32)
                 store_rows<D>(*reinterpret_cast<const float(*)[32]>(acc + c), mul, which ? prm.part0 : prm.part1, row0,
                               rows_valid, hf * (D / 2) + c, lane);
-            } else if (rl < L) {
+            } else if (rl < S) {
               __nv_bfloat16* dst = (which ? prm.out0 : prm.out1) +
-                                   (((int64_t)x.b * prm.Hkv + x.h) * prm.S + (int64_t)k * L + rl) * D + hf * (D / 2);
+                                   (((int64_t)x.b * prm.Hkv + x.h) * S + rl) * D + hf * (D / 2);
 #pragma unroll
               for (int c = 0; c < D / 2; c += 32) store_bf16(acc + c, mul, dst + c);
             }
@@ -595,12 +540,12 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         g0 += NB;
         v = vn;
         x = xn;
-        if (v >= 0 && x.ok && x.NB >= 1) {
+        if (v >= 0) {
           lam_pub = raw_lam;
           publish(g0);
           nxt = cur;
           if (x.NB > 1) {
-            nxt.step(prm, x.it, x.blk);
+            nxt.step(prm);
             fetch(x, nxt);
           }
         }
@@ -612,25 +557,20 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       bool row_in = false;
       auto fetch = [&](const Unit& y) {
         const int64_t ql = (int64_t)y.blk * BM + row;
-        row_in = ql < L;
+        row_in = ql < S;
         raw_nl = -lam_of(prm, y.h);
         if (row_in) {
-          const int64_t at = (((int64_t)y.b * prm.Hq + y.h) * 2) * prm.S + (int64_t)y.it.p * L + ql;
+          const int64_t at = (((int64_t)y.b * prm.Hq + y.h) * 2) * S + ql;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            raw_l[m] = __ldg(prm.lse + at + m * prm.S);
-            raw_d[m] = __ldg(prm.dsum + at + m * prm.S);
+            raw_l[m] = __ldg(prm.lse + at + m * S);
+            raw_d[m] = __ldg(prm.dsum + at + m * S);
           }
         }
       };
-      if (ok && v >= 0 && x.ok) fetch(x);
+      if (ok && v >= 0) fetch(x);
       while (ok && v >= 0) {
-        if (!x.ok || x.NB < 1) {
-          bad_unit(v, ROLE_EW);
-          ok = false;
-          break;
-        }
-        const int p = x.it.p, qb = x.blk;
+        const int qb = x.blk;
         float nl[2], nd[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
@@ -641,17 +581,14 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         const float lam_d2 = raw_nl * nd[1];
         const uint64_t d1 = f2_pack(nd[0], nd[0]), ld2 = f2_pack(lam_d2, lam_d2), nlam2 = f2_pack(raw_nl, raw_nl);
         uint64_t t2[2] = {0ull, 0ull};  // sum of P_2 dP
-        KCursor cur;
-        cur.start(prm, x.it, qb);
-        const int n_keys = (int)L, diag_keys = qb * BM + row + 1;  // visible keys of a partition, of the diagonal one
+        const int n_keys = (int)S, diag_keys = qb * BM + row + 1;  // keys; those up to the row's own
         for (int j = 0; j < x.NB && ok; ++j) {
-          if (j > 0) cur.step(prm, x.it, qb);
+          const int kb = x.start + j;
           const int64_t gi = g0 + j;
           const uint32_t dpb = tm_dp + (uint32_t)((gi & 1) * 64);
-          // keys past the partition's end, or behind the row, are masked
-          const bool diag = prm.causal && cur.kp == p;
-          const int hi = (diag ? min(n_keys, diag_keys) : n_keys) - cur.kb * BS - c_base;
-          const bool any_mask = (cur.kb + 1) * BS > (diag ? min(n_keys, qb * BM) : n_keys);
+          // keys past the end, or behind the row, are masked
+          const int hi = (prm.causal ? min(n_keys, diag_keys) : n_keys) - kb * BS - c_base;
+          const bool any_mask = (kb + 1) * BS > (prm.causal ? min(n_keys, qb * BM) : n_keys);
           ok = wait_all(Ly::B_S, (uint32_t)(gi & 1), ROLE_EW, j);
           if (!ok) break;
           tc_fence_after();
@@ -706,14 +643,14 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
 #pragma unroll
           for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
           if (lane == 0)
-            prm.dlam_part[((((int64_t)x.b * prm.Hq + x.h) * prm.n_slots + x.it.slot) * prm.nb + qb) * N_EW + warp] = -t;
+            prm.dlam_part[((((int64_t)x.b * prm.Hq + x.h) * prm.parts + x.part) * prm.nb + qb) * N_EW + warp] = -t;
         }
         // the next unit and its row's values (the epilogue warps drain this one)
         int vn = -1;
         Unit xn;
         ok = take(vn, xn, ROLE_EW);
         if (!ok) break;
-        if (vn >= 0 && xn.ok) fetch(xn);
+        if (vn >= 0) fetch(xn);
         g0 += x.NB;
         v = vn;
         x = xn;
@@ -813,12 +750,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       Unit x;
       if (ok) ok = take(v, x, ROLE_MMA);
       if (ok && v >= 0) {
-        if (!x.ok || x.NB < 1) {
-          bad_unit(v, ROLE_MMA);
-          ok = false;
-        } else {
-          ok = start_unit(x, 0);
-        }
+        ok = start_unit(x, 0);
       }
       int64_t g0 = 0;
       int k_unit = 0;
@@ -867,11 +799,6 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         ++k_unit;
         v = vn;
         if (v < 0) break;
-        if (!x.ok || x.NB < 1) {
-          bad_unit(v, ROLE_MMA);
-          ok = false;
-          break;
-        }
         ok = start_unit(x, g0);
       }
       // exit-path drain: every MMA issued completes before TMEM is freed
@@ -881,15 +808,22 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       // ================================================================ producer
       bool ok = run;
       int np = 0;  // units published
-      auto publish = [&](Unit& y) -> int {  // a CTA's first unit is its own index, the others come from the counter
+      // a CTA's first unit is its own index, the others come from the counter; units without blocks are passed over
+      auto next = [&]() { return prm.n_units > n_ctas ? (int)(n_ctas + atomicAdd(prm.counter, 1u)) : prm.n_units; };
+      auto publish = [&](Unit& y) -> int {
         const int slot = np & 1;
         ok = mbar_wait(bar(Ly::B_UE + slot), (uint32_t)(((np >> 1) & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
                        ROLE_LOAD, -1);
         if (!ok) return -1;
-        int u = cta;
-        if (np > 0) u = prm.n_units > n_ctas ? (int)(n_ctas + atomicAdd(prm.counter, 1u)) : prm.n_units;
+        int u = np > 0 ? next() : cta;
+        for (; u < prm.n_units; u = next()) {
+          y = unit_of<KV>(u, prm);
+          if (y.NB > 0) break;
+          if (!KV)  // its share of lam's gradient
+            for (int w = 0; w < N_EW; ++w)
+              prm.dlam_part[((((int64_t)y.b * prm.Hq + y.h) * prm.parts + y.part) * prm.nb + y.blk) * N_EW + w] = 0.f;
+        }
         if (u >= prm.n_units) u = -1;
-        if (u >= 0) y = unit_of<KV>(u, prm);
         put_unit(unit_ring + 16 * slot, u, y);
         mbar_arrive(bar(Ly::B_UF + slot));
         ++np;
@@ -900,17 +834,12 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
       Unit x{}, y{};
       int u = ok ? publish(x) : -1;
       while (ok && u >= 0) {
-        if (!x.ok || x.NB < 1) {
-          record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_LOAD, u);
-          *abort_flag = 1;
-          break;
-        }
         // publish the following unit now and pull its resident rows into L2
         const int un = publish(y);
         if (!ok) break;
         const int H = KV ? prm.Hkv : prm.Hq;
-        if (un >= 0 && y.ok) {
-          const int32_t pn = (y.b * H + y.h) * prm.P + y.it.p;
+        if (un >= 0) {
+          const int32_t pn = y.b * H + y.h;
           for (int c = 0; c < D / 64; ++c) {
             tma_prefetch_l2_3d(&tmR0, c * 64, y.blk * BM, pn);
             tma_prefetch_l2_3d(&tmR1, c * 64, y.blk * BM, pn);
@@ -919,30 +848,19 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         // resident operands: the previous unit's must have been used (dkdv) or copied into TMEM (dq)
         ok = mbar_wait(bar(Ly::B_RESE), (uint32_t)((nres & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, u);
         if (!ok) break;
-        const int32_t part = (x.b * H + x.h) * prm.P + x.it.p;
+        const int32_t res = x.b * H + x.h;
         mbar_expect_tx(bar(Ly::B_RES), 2 * Ly::TILE);
         for (int c = 0; c < D / 64; ++c) {
-          tma_load_3d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmR0, c * 64, x.blk * BM, part, bar(Ly::B_RES));
-          tma_load_3d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmR1, c * 64, x.blk * BM, part, bar(Ly::B_RES));
+          tma_load_3d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmR0, c * 64, x.blk * BM, res, bar(Ly::B_RES));
+          tma_load_3d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmR1, c * 64, x.blk * BM, res, bar(Ly::B_RES));
         }
         ++nres;
         QCursor qc;
-        KCursor kc;
-        if (KV) qc.start(prm, x.it, x.blk, x.h * g);
-        else kc.start(prm, x.it, x.blk);
+        if (KV) qc.start(prm, x);
         for (int i = 0; i < x.NB && ok; ++i) {
-          if (i > 0) {
-            if (KV) qc.step(prm, x.it, x.blk);
-            else kc.step(prm, x.it, x.blk);
-          }
-          const int o = KV ? qc.p : kc.kp, blk = KV ? qc.qb : kc.kb;
-          if (o < 0 || o >= prm.P) {
-            record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_LOAD, u);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          const int32_t z = KV ? (x.b * prm.Hq + qc.h) * prm.P + o : (x.b * prm.Hkv + x.h / g) * prm.P + o;
+          if (KV && i > 0) qc.step(prm);
+          const int blk = KV ? qc.qb : x.start + i;
+          const int32_t z = KV ? x.b * prm.Hq + qc.h : x.b * prm.Hkv + x.h / g;
           const int sa = (int)(ga % Ly::NSA), st = (int)(gb % Ly::NSB);
           if (ga >= Ly::NSA) {
             ok = mbar_wait(bar(Ly::B_AE + sa), (uint32_t)((ga / Ly::NSA - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
@@ -1024,24 +942,19 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         return true;
       };
       if (ok) ok = take(v, x, ROLE_EPI);
-      if (ok && v >= 0 && x.ok && x.NB >= 1) ok = copy_in();
+      if (ok && v >= 0) ok = copy_in();
       while (ok && v >= 0) {
-        if (!x.ok || x.NB < 1) {
-          bad_unit(v, ROLE_EPI);
-          ok = false;
-          break;
-        }
         int vn = -1;
         Unit xn;
         ok = take(vn, xn, ROLE_EPI);
         if (!ok) break;
-        if (vn >= 0 && xn.ok && xn.NB >= 1) {
+        if (vn >= 0) {
           ok = copy_in();
           if (!ok) break;
         }
-        const int64_t row0 = (((int64_t)x.b * prm.Hq + x.h) * prm.n_slots + x.it.slot) * L + (int64_t)x.blk * BM + wq * 32;
-        const int rows_valid = (int)max((int64_t)0, min((int64_t)32, L - ((int64_t)x.blk * BM + wq * 32)));
-        __nv_bfloat16* dst = prm.out0 + (((int64_t)x.b * prm.Hq + x.h) * prm.S + (int64_t)x.it.p * L + (int64_t)x.blk * BM + r) * D;
+        const int64_t row0 = (((int64_t)x.b * prm.Hq + x.h) * prm.parts + x.part) * S + (int64_t)x.blk * BM + wq * 32;
+        const int rows_valid = (int)max((int64_t)0, min((int64_t)32, S - ((int64_t)x.blk * BM + wq * 32)));
+        __nv_bfloat16* dst = prm.out0 + (((int64_t)x.b * prm.Hq + x.h) * S + (int64_t)x.blk * BM + r) * D;
         ok = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(k_unit & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EPI, -1);
         if (!ok) break;
         tc_fence_after();
@@ -1052,7 +965,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           tmem_ld32(tm_dq + (uint32_t)(D == 64 ? c * 3 : c), t);
           tc_wait_ld();
           if (c + 32 == D) arrive(Ly::B_ACCE);
-          if (prm.part0) store_rows<D>(t, prm.scale, prm.part0, row0, rows_valid, c, lane);
+          if (prm.parts > 1) store_rows<D>(t, prm.scale, prm.part0, row0, rows_valid, c, lane);
           else if (lane < rows_valid) store_bf16(t, prm.scale, dst + c);
         }
         ++k_unit;
@@ -1082,6 +995,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     run_pass<D, true>(rows128.k, rows128.v, rows64.q, rows64.g, kv, (int)blockIdx.x, kv_ctas);
   else
     run_pass<D, false>(rows128.q, rows128.g, rows64.k, rows64.v, dq, (int)blockIdx.x - kv_ctas, (int)gridDim.x - kv_ctas);
+}
+
+// out[head][row] = sum over its block's parts, in order, rounded once; blockIdx.y picks one of up to three tensors
+struct SumArgs {
+  const float4* part[3];  // [head][parts][S][D]
+  uint2* out[3];
+  int64_t heads[3];
+  int32_t parts[3], kv[3];
+  int64_t S;
+  int32_t row4, ns, causal, group;  // 16-byte pieces of a row
+  const int32_t* status;
+};
+__global__ void __launch_bounds__(256) sum_parts(const SumArgs a) {
+  wait_for_kernel_before();
+  if (*reinterpret_cast<const volatile int32_t*>(a.status) != 0) return;
+  const int w = blockIdx.y;
+  const int64_t per = a.S * a.row4, total = a.heads[w] * per;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t head = i / per, at = i - head * per;
+    const int blk = (int)(at / a.row4 / BM);
+    const int n = a.kv[w] ? blocks_of<true>(blk, a.ns, a.causal, a.group) : blocks_of<false>(blk, a.ns, a.causal, a.group);
+    const int k = min(a.parts[w], n);
+    const float4* src = a.part[w] + head * a.parts[w] * per + at;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < k; ++p) {
+      const float4 x = __ldcs(src + p * per);
+      t.x += x.x, t.y += x.y, t.z += x.z, t.w += x.w;
+    }
+    a.out[w][i] = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1121,55 +1065,47 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
   return true;
 }
 
-static int64_t fill(Params& prm, const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, bool direct) {
-  const char* tb = static_cast<const char*>(a.tables);
-  prm.items = reinterpret_cast<const DevItem*>(tb + (direct ? a.tl.flat_item : kv ? a.tl.kv_items : a.tl.items));
-  prm.list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : kv ? a.tl.q_list : a.tl.kv_list));
+static int64_t fill(Params& prm, const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv, int parts) {
   prm.lse = a.LSE;
   prm.dsum = reinterpret_cast<const float*>(a.ws + w.dsum);
   prm.lam = static_cast<const __nv_bfloat16*>(a.lam);
   prm.out0 = static_cast<__nv_bfloat16*>(kv ? a.dK : a.dQ);
   prm.out1 = static_cast<__nv_bfloat16*>(a.dV);
-  prm.part0 = direct ? nullptr : reinterpret_cast<float*>(a.ws + (kv ? w.dk_part : w.dq_part));
-  prm.part1 = direct ? nullptr : reinterpret_cast<float*>(a.ws + w.dv_part);
+  prm.part0 = reinterpret_cast<float*>(a.ws + (kv ? w.dk_part : w.dq_part));
+  prm.part1 = reinterpret_cast<float*>(a.ws + w.dv_part);
   prm.dlam_part = reinterpret_cast<float*>(a.ws + w.dlam_part);
   prm.status = a.status;
   prm.counter = reinterpret_cast<uint32_t*>(a.ws + w.counters) + (kv ? 0 : 64);
   prm.S = a.S;
-  prm.L = direct ? a.S : a.L;
   prm.B = a.B;
   prm.Hq = a.Hq;
   prm.Hkv = a.Hkv;
-  prm.P = direct ? 1 : a.P;
-  prm.n_slots = direct ? 1 : kv ? a.n_kv_slots : a.n_slots;
-  prm.n_items = prm.n_slots;
-  prm.nb = (int32_t)((prm.L + BM - 1) / BM);
-  prm.ns = (int32_t)((prm.L + BS - 1) / BS);
-  const int64_t units = (int64_t)prm.nb * prm.n_items * a.B * (kv ? a.Hkv : a.Hq);
-  prm.n_units = (int32_t)units;
+  prm.parts = parts;
+  prm.nb = (int32_t)((a.S + BM - 1) / BM);
+  prm.ns = (int32_t)((a.S + BS - 1) / BS);
+  const int64_t tiles = (int64_t)prm.nb * a.B * (kv ? a.Hkv : a.Hq);
+  prm.n_tiles = (int32_t)tiles;
+  prm.n_units = (int32_t)(tiles * parts);
   prm.causal = a.causal;
   // causal units differ in length: enough lanes together for about three times the grid, so that the last ones are short
-  prm.batch = a.causal ? (int32_t)std::min<int64_t>(units / prm.nb, (3LL * sms + prm.nb - 1) / prm.nb) : 1;
+  prm.batch = a.causal ? (int32_t)std::min<int64_t>(tiles / prm.nb, (3LL * sms + prm.nb - 1) / prm.nb) : 1;
   prm.lam_n = a.lam_n;
   prm.scale = a.scale;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
-  return units;
+  return tiles * parts;
 }
 
-static bool make_maps(EncodeTiledFn enc, Maps* m, const DiffArgs& a, bool flat, int box_rows, bool q_side, bool kv_side,
-                      std::string* err) {
-  const uint64_t L = (uint64_t)(flat ? a.S : a.L), P = (uint64_t)(flat ? 1 : a.P);
-  const uint64_t qp = (uint64_t)a.B * a.Hq * P, kp = (uint64_t)a.B * a.Hkv * P;
-  return (!q_side || (make_map(enc, &m->q, a.Q, L, qp, a.d, box_rows, err) && make_map(enc, &m->g, a.dO, L, qp, a.d, box_rows, err))) &&
-         (!kv_side || (make_map(enc, &m->k, a.K, L, kp, a.d, box_rows, err) && make_map(enc, &m->v, a.V, L, kp, a.d, box_rows, err)));
+static bool make_maps(EncodeTiledFn enc, Maps* m, const DiffArgs& a, int box_rows, std::string* err) {
+  const uint64_t S = (uint64_t)a.S, nq = (uint64_t)a.B * a.Hq, nk = (uint64_t)a.B * a.Hkv;
+  return make_map(enc, &m->q, a.Q, S, nq, a.d, box_rows, err) && make_map(enc, &m->g, a.dO, S, nq, a.d, box_rows, err) &&
+         make_map(enc, &m->k, a.K, S, nk, a.d, box_rows, err) && make_map(enc, &m->v, a.V, S, nk, a.d, box_rows, err);
 }
 
 template <int D>
-static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, cudaStream_t st,
-                  std::string* err) {
+static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, BwdParts parts, cudaStream_t st, std::string* err) {
   Params kv{}, dq{};
-  const int64_t kv_units = fill(kv, a, w, sms, true, kv_direct), dq_units = fill(dq, a, w, sms, false, dq_direct);
+  const int64_t kv_units = fill(kv, a, w, sms, true, parts.kv), dq_units = fill(dq, a, w, sms, false, parts.dq);
   if (kv_units > 0x3fffffff || dq_units > 0x3fffffff) {
     *err = "too many work units for one launch";
     return (int)cudaErrorInvalidConfiguration;
@@ -1177,10 +1113,7 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_di
   EncodeTiledFn enc = get_encode(err);
   if (!enc) return (int)cudaErrorNotSupported;
   Maps rows128{}, rows64{};
-  // each pass in its own partitions: dkdv holds K, V and streams Q, dO; dq the other way round
-  if (!make_maps(enc, &rows128, a, kv_direct, BM, false, true, err) || !make_maps(enc, &rows64, a, kv_direct, BS, true, false, err) ||
-      !make_maps(enc, &rows128, a, dq_direct, BM, true, false, err) || !make_maps(enc, &rows64, a, dq_direct, BS, false, true, err))
-    return (int)cudaErrorInvalidValue;
+  if (!make_maps(enc, &rows128, a, BM, err) || !make_maps(enc, &rows64, a, BS, err)) return (int)cudaErrorInvalidValue;
   auto kern = diff_bwd_kernel<D>;
   static OncePerDevice once;
   const int dev = OncePerDevice::device();
@@ -1204,17 +1137,68 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_di
     const int kv_ctas = (int)std::min<int64_t>(kv_units, sms), dq_ctas = (int)std::min<int64_t>(dq_units, sms);
     e = launch_behind(kern, dim3((unsigned)(kv_ctas + dq_ctas)), NUM_THREADS, Layout<D>::TOTAL, st, rows128, rows64, kv, dq, kv_ctas);
   }
+  if (e == cudaSuccess && (parts.kv > 1 || parts.dq > 1)) {
+    SumArgs s{};
+    int n = 0;
+    auto add = [&](float* part, void* out, int heads, int p, bool is_kv) {
+      s.part[n] = reinterpret_cast<const float4*>(part);
+      s.out[n] = static_cast<uint2*>(out);
+      s.heads[n] = (int64_t)a.B * heads;
+      s.parts[n] = p;
+      s.kv[n++] = is_kv;
+    };
+    if (parts.kv > 1) {
+      add(kv.part0, a.dK, a.Hkv, parts.kv, true);
+      add(kv.part1, a.dV, a.Hkv, parts.kv, true);
+    }
+    if (parts.dq > 1) add(dq.part0, a.dQ, a.Hq, parts.dq, false);
+    s.S = a.S;
+    s.row4 = D / 4;
+    s.ns = kv.ns;
+    s.causal = a.causal;
+    s.group = a.Hq / a.Hkv;
+    s.status = a.status;
+    const int64_t most = (int64_t)a.B * a.Hq * a.S * s.row4;
+    e = launch_behind(sum_parts, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 152 * 8), (unsigned)n), 256, 0, st, s);
+  }
   if (e != cudaSuccess) *err = std::string("diff_bwd launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
 
 }  // namespace dbtc
 
-int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, void* stream,
-                       std::string* err) {
+// Parts of the passes' units: those with the least estimated time, in streamed blocks (about 1 us each).  A unit
+// takes UNIT blocks besides its own; the parts' sums SUM, and what their 8 bytes a value (written and read) take at
+// 5 TB/s for d = 128.  With an SM for every unit the longest decides; with
+// more units than that, their whole work shared out, and half a unit for the uneven end.  Measured, us of the
+// backward call, whole / cut: 16 heads on one, 1,192 tokens 372 / 81; one head of 8,192 161 / 114, of 2,304 54 / 37;
+// 2 x 4 heads of 1,000 tokens, where whole units just fill the GPU, 31 / 35 in halves.
+BwdParts diff_bwd_parts(int64_t S, int32_t B, int32_t Hq, int32_t Hkv, bool causal) {
+  constexpr int SMS = 152;  // the whole GPU's: so the workspace's size needs no device
+  constexpr double UNIT = 10, SUM = 3, ROW = 128 * 8 / 5e6;
+  const int64_t nb = (S + dbtc::BM - 1) / dbtc::BM, ns = (S + dbtc::BS - 1) / dbtc::BS, group = std::max(1, Hq / Hkv);
+  const double tiles_kv = (double)nb * B * Hkv, tiles_dq = (double)nb * B * Hq;
+  if (tiles_kv > SMS) return {1, 1};  // several waves of whole units
+  const double blocks = 2.0 * (double)(causal ? nb * (nb + 1) : nb * ns) * B * Hq;  // of both passes: the same pairs
+  BwdParts best{1, 1};
+  double least = 1e300;
+  constexpr int ks[] = {1, 2, 3, 4, 6, 8, 11, 16};
+  for (int kv : ks) {
+    const double len_kv = (double)((ns * group + kv - 1) / kv);
+    for (int dq : ks) {
+      const double unit = UNIT + std::max(len_kv, (double)((ns + dq - 1) / dq)), units = tiles_kv * kv + tiles_dq * dq;
+      const double shared = (units * UNIT + blocks) / SMS;
+      const double rows = (kv > 1 ? 2.0 * kv * B * Hkv * S : 0) + (dq > 1 ? (double)dq * B * Hq * S : 0);
+      const double t = (units <= SMS ? unit : std::max(unit, shared) + unit / 2) + (rows > 0 ? SUM + rows * ROW : 0);
+      if (t < least) least = t, best = {kv, dq};
+    }
+  }
+  return best;
+}
+
+int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, BwdParts parts, void* stream, std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
-  return a.d == 128 ? dbtc::launch<128>(a, w, sms, kv_direct, dq_direct, st, err)
-                    : dbtc::launch<64>(a, w, sms, kv_direct, dq_direct, st, err);
+  return a.d == 128 ? dbtc::launch<128>(a, w, sms, parts, st, err) : dbtc::launch<64>(a, w, sms, parts, st, err);
 }
 
 }  // namespace mesh

@@ -460,6 +460,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) diff_bwd32_kernel(const __grid
     mbar_init(bar(Ly::B_ACC), 1);
     mbar_init(bar(Ly::B_DRAIN), 1);
     wait_for_kernel_before();
+    // without any time to wait there is nothing to start: the first load would be waited for
+    if (prm.wait_limit_ns <= 0) record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
     *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -163,15 +163,15 @@ int launch_bwd_reduce(const ReduceArgs& a, mesh_attn_dtype out_dtype, void* stre
 constexpr int MAX_SMS = 256;
 
 // A plan's constant tables as the differential calls read them from device memory, in one block:
-// [header | flat item and lists | slot_off | items | kv_list | kv_slot_off | kv_items | kv_q_list].  The header's tag says
-// which plan they are of; the first kernel of a call compares it with the plan it was given.
+// [header | flat item and lists | slot_off | items | kv_list].  The header's tag says which plan they are
+// of; the first kernel of a call compares it with the plan it was given.
 struct TablesHeader {
   uint64_t magic, tag;
 };
 constexpr uint64_t TABLES_MAGIC = 0x6d6573685f746162ull;
 struct TablesLayout {
   size_t flat_item, flat_list;  // the whole sequence as one partition and one work item
-  size_t slot_off, items, kv_list, kv_slot_off, kv_items, q_list, total;
+  size_t slot_off, items, kv_list, total;
 };
 TablesLayout tables_layout(const Plan& plan);
 uint64_t plan_tag(const Plan& plan);
@@ -195,8 +195,8 @@ struct DiffArgs {
   void* dlam;
   char* ws;
   int64_t S, L;
-  int32_t B, Hq, Hkv, d, P, n_slots, n_kv_slots, causal, lam_n;
-  bool single_slot, single_kv_slot;  // every partition has one (KV) slot: no partial sums to merge
+  int32_t B, Hq, Hkv, d, P, n_slots, causal, lam_n;
+  bool single_slot;  // every partition has one slot: no partial outputs to merge
   float scale, scale_log2;
   int64_t wait_limit_ns;
 };
@@ -212,19 +212,20 @@ struct DiffWorkspace {
 };
 DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                              bool backward);
-// Whether a pass over the rows of H heads takes the whole sequence as one work item, which leaves no
-// partial sums to add: unless its 128-row blocks occupy less than a quarter of the SMs, the plan
-// splits the other axis (`single`: it does not) and its partitions fill a tile.  Forward, us: 18 blocks
-// (2,304 tokens, one head) 32 whole, 26 by 9 partitions, 45 by 36 of 64 tokens; 128 blocks (8,192
-// tokens, two heads) 87 whole, 119 by 16 partitions.
-bool rows_direct(const DiffArgs& a, int32_t H, bool single, int sms);
+// Whether the fp32 forward over the rows of H heads (two a query head, one a map) takes the whole sequence as
+// one work item: unless its 128-row blocks occupy less than a quarter of the SMs, the plan splits the
+// keys and its partitions fill a tile.  One head of 2,304 tokens, d = 128, causal (36 blocks), us: 84 whole, 54,
+// 43 and 61 by 4, 9 and 16 partitions.
+bool rows_direct(const DiffArgs& a, int32_t H, int sms);
 // bf16 forward on the tensor cores, with its merge where tiles are cut into parts; the most parts there may be.
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
 int64_t diff_fwd_max_parts(int64_t S, int32_t B, int32_t Hq, bool causal);
-// bf16 backward: dK and dV, dQ and the sums behind dlam; either written as they are (direct) or as
-// partial sums per slot.
-int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, bool kv_direct, bool dq_direct, void* stream,
-                       std::string* err);
+// bf16 backward: dK and dV, dQ and the sums behind dlam; parts of the units of the two passes.
+struct BwdParts {
+  int32_t kv, dq;
+};
+BwdParts diff_bwd_parts(int64_t S, int32_t B, int32_t Hq, int32_t Hkv, bool causal);
+int launch_diff_bwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, BwdParts parts, void* stream, std::string* err);
 // fp32 forward: Q (one map a head), K and V as bf16 pieces.
 int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, std::string* err);
 // fp32 backward: dQ, dK and dV, with their sums over splits and query heads.
