@@ -145,6 +145,23 @@ def test_few_tiles_and_a_last_wave_of_few(lib, shape):
     check_out(outs[0][0], outs[0][2], OD.forward(q, k, v, lam, causal), "bf16", S)
 
 
+@pytest.mark.parametrize("causal", [False, True])
+def test_long_fp32_sums_keep_their_digits(lib, causal):
+    """More keys than one accumulation on the tensor cores takes, in each pass.  Norm-wise: sums move on after 13 blocks of 64
+    rows, each block 24 truncating additions that lose at most 2^-24 of the sum on average (half an ulp at worst, the
+    mean of a truncation): 13 * 24 * 2^-24 = 1.9e-5, and a quarter of it in practice; without moving on, 2,000 rows
+    would lose 32 * 24 * 2^-24 = 4.6e-5."""
+    q, k, v, lam, g = inputs(1, 2, 1, 2000, 64, "f32", 42)
+    dev = [t.cuda() for t in (q, k, v, lam)]
+    O, O2, L = lib.mesh_diff_attention(*dev, 1, causal, return_saved=True)
+    grads = lib.mesh_diff_attention_backward(*dev, O, O2, L, g.cuda(), 1, causal)
+    ref = OD.backward(q, k, v, lam, g, causal)
+    for name, x, r in [("O", O, OD.forward(q, k, v, lam, causal)[0])] + [("d" + n, x, ref[n][0]) for n, x in zip("qkv", grads)]:
+        e = ((x.double().cpu() - r).norm() / r.norm()).item()
+        print(f"{name}: {e:.2e}")
+        assert e <= 13 * 24 * 2.0 ** -24, name
+
+
 def test_large_scores(lib):
     """Scores of some hundred: the running maximum moves, most weights vanish."""
     q, k, v, lam, g = inputs(1, 2, 2, 300, 128, "bf16", 23, k_scale=16.0)

@@ -25,6 +25,10 @@
 // Few rows leave SMs idle, so the streamed axis is split between CTAs (`splits`); the splits, and for dK and
 // dV the query heads of a KV head, leave partial sums that sum_parts adds in order.  Rows past the end are
 // loaded as zeros.  Every mbarrier wait is bounded, as in the other kernels.
+//
+// Measured (the backward call, us): 2 x 8 heads on one of 801 tokens, d = 128: 295, 45 TFLOP/s of the formulas' five
+// products (a kernel on the CUDA cores took 824); 4 heads on 2 of 777, d = 64, causal: 55 (74).  Bound by the chain of a block's steps: at d = 128 about 11,000 cycles for dQ and dK, 7,500 of products (48 each of S,
+// dP and the accumulators', 45-62 cycles) and 2,500-4,000 of the elementwise warps; 7,300 for dV.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -46,6 +50,10 @@ constexpr int N_EW = 8;
 constexpr int WARP_MMA = 8;
 constexpr int WARP_LOAD = 9;
 constexpr int NUM_THREADS = 320;
+// The tensor cores' fp32 sums truncate, so a long accumulation loses digits whatever its terms' signs (dK of 3,000
+// queries: 1.4e-5 of its norm).  After GROUP blocks at most the accumulators are added to the outputs in fp32, with
+// rounding.
+constexpr int GROUP = 13;
 constexpr int64_t DRAIN_NS = 200000000;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4;
@@ -68,7 +76,7 @@ struct Layout {
   static constexpr uint32_t VEC = C1 + NST * 3 * CP;  // [2][64][4]: LSE_1, LSE_2, D_1, D_2 of a block's query rows
   static constexpr uint32_t BAR = VEC + 2 * BS * 16;
   static constexpr int B_RF = 0, B_R1 = 1, B_C0F = 2, B_C0E = B_C0F + 2, B_C1F = B_C0E + 2, B_C1E = B_C1F + 2, B_S = B_C1E + 2,
-                       B_SR = B_S + 1, B_DS = B_SR + 1, B_ACC = B_DS + 2, B_DRAIN = B_ACC + 1, NBARS = B_DRAIN + 1;
+                       B_SR = B_S + 1, B_DS = B_SR + 1, B_ACC = B_DS + 2, B_ACCE = B_ACC + 1, B_DRAIN = B_ACCE + 1, NBARS = B_DRAIN + 1;
   static constexpr uint32_t MISC = BAR + NBARS * 8;  // tmem base, abort flag
   static constexpr uint32_t ALLOC = MISC + 16 + 1024;
 };
@@ -141,6 +149,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
   const int first = KV && prm.causal ? 2 * rb : 0, last = !KV && prm.causal ? min(n_all, 2 * rb + 2) : n_all;
   const int per = (last - first + prm.splits - 1) / prm.splits;
   const int c_begin = min(last, first + split * per), NB = min(last, c_begin + per) - c_begin;
+  const int n_groups = max(1, (NB + GROUP - 1) / GROUP), grp = max(1, (NB + n_groups - 1) / n_groups);
   const bool run = *abort_flag == 0 && NB > 0;
 
   if (warp < N_EW) {
@@ -184,9 +193,19 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         if (lane == 0) mbar_arrive(bar(Ly::B_R1));
       }
     }
+    // where this warp's half of the columns of its rows goes: [B, head, part, S, D]
+    auto out_row = [&]() {
+      const int64_t head = KV ? bk : bh;
+      const int n_part = KV ? group * prm.splits : prm.splits, part = KV ? (h % group) * prm.splits + split : split;
+      return prm.out[PASS] + ((head * n_part + part) * S + row) * D + hf * (D / 2);
+    };
+    const float f = PASS == DV ? 1.f : prm.scale;
+    // d = 64: the second map's accumulator is 64 columns behind, its half of the columns in the second 32
+    const uint32_t acc = lanes + COL_ACC + (uint32_t)(hf * (D == 64 && PASS != DV ? 96 : D / 2));
     const float nlam = -prm.lam[prm.lam_n == 1 ? 0 : h];
     const int vw = threadIdx.x >> 6, vc = threadIdx.x & 63;  // the value this thread fetches for a block
     float vnext = KV && ok ? fetch(vw, (int64_t)c_begin * BS + vc) : 0.f;
+    bool moved = true;  // a wait below that failed: told to the others by the next block's vote
     for (int j = 0; j < NB && ok; ++j) {
       const int64_t c0 = (int64_t)(c_begin + j) * BS;
       const float4* bv = reinterpret_cast<const float4*>(vec + (j & 1) * 4 * BS);
@@ -195,7 +214,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (j + 1 < NB) vnext = fetch(vw, c0 + BS + vc);
       }
-      ok = mbar_wait_warp(bar(Ly::B_S), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
+      ok = moved && mbar_wait_warp(bar(Ly::B_S), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
       // an abort ends all warps' loops: none may wait for another below
       float s1[32], s2[32], dp[32];
       if (ok) {
@@ -267,17 +286,34 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_DS + (j & 1)));
+      if ((j + 1) % grp == 0 && j + 1 < NB) {  // the group's sums to the outputs
+        moved = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)((j / grp) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
+        if (moved) {
+          tc_fence_after();
+          float* const dst = out_row();
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 32) {
+            float o[32];
+            tmem_ld32(acc + (uint32_t)c, o);
+            tc_wait_ld();
+            if (row < S)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float4* at = reinterpret_cast<float4*>(dst + c) + e;
+                const float4 y = j >= grp ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                *at = make_float4(fmaf(o[4 * e], f, y.x), fmaf(o[4 * e + 1], f, y.y), fmaf(o[4 * e + 2], f, y.z), fmaf(o[4 * e + 3], f, y.w));
+              }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Ly::B_ACCE));
+        }
+      }
     }
-    if (ok) ok = mbar_wait_warp(bar(Ly::B_ACC), 0u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, -1);
+    if (ok) ok = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(((NB - 1) / grp) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, -1);
     if (ok || (NB == 0 && *abort_flag == 0)) {
-      // this warp's half of the columns: [B, head, part, S, D]
       if (ok) tc_fence_after();
-      const int64_t head = KV ? bk : bh;
-      const int n_part = KV ? group * prm.splits : prm.splits, part = KV ? (h % group) * prm.splits + split : split;
-      float* dst = prm.out[PASS] + ((head * n_part + part) * S + row) * D + hf * (D / 2);
-      const float f = PASS == DV ? 1.f : prm.scale;
-      // d = 64: the second map's accumulator is 64 columns behind, its half of the columns in the second 32
-      const uint32_t acc = lanes + COL_ACC + (uint32_t)(hf * (D == 64 && PASS != DV ? 96 : D / 2));
+      float* const dst = out_row();
       // 32 rows x 32 columns at a time through shared memory (C0's, whose last reader is done), 16-byte pieces
       // swizzled by row, so that a store writes whole 128-byte row pieces
       float* stage = reinterpret_cast<float*>(smem + Ly::C0 + (uint32_t)warp * 4096u);
@@ -301,8 +337,12 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = i * 4 + (lane >> 3), e = lane & 7;
-          const float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + ((e ^ (r & 7)) * 4));
-          if (r < rows) *reinterpret_cast<float4*>(dst + (int64_t)(r - lane) * D + c + e * 4) = x;
+          float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + ((e ^ (r & 7)) * 4));
+          float4* at = reinterpret_cast<float4*>(dst + (int64_t)(r - lane) * D + c + e * 4);
+          if (r < rows) {
+            if (NB > grp) x.x += at->x, x.y += at->y, x.z += at->z, x.w += at->w;
+            *at = x;
+          }
         }
       }
     }
@@ -361,7 +401,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
 #pragma unroll
         for (int kk = 0; kk < BS / 16; ++kk)
           tc_mma_ts_warp(acc, a + (uint32_t)(pair_a(pr) * 32 + kk * 8), c + (c_off(pair_b(pr), 0) + (uint64_t)(kk * 128)), idesc_a,
-                         (j > 0 || pr > 0 || kk > 0) ? 1u : 0u);
+                         (j % grp > 0 || pr > 0 || kk > 0) ? 1u : 0u);
     };
     // dP before the scores: C1's stage is free before C0's, whose next load then overlaps this product
     if (ok) ok = (PASS == DV || issue_dp(0)) && issue_s(0);
@@ -373,6 +413,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         if (!(ok = wait(Ly::B_C1F + st, (uint32_t)((j / NST) & 1), j))) break;
       }
       if (!(ok = wait(Ly::B_DS + (j & 1), (uint32_t)((j >> 1) & 1), j))) break;
+      if (j > 0 && j % grp == 0 && !(ok = wait(Ly::B_ACCE, (uint32_t)((j / grp - 1) & 1), j))) break;
       tc_fence_after();
       if (PASS == DV) {
         sum(j, tmem + COL_ACC, tmem + COL_A + 96u * (uint32_t)(j & 1), c1m + stage);
@@ -385,7 +426,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         // into the place of dS(j)'s pieces, which those products have read
         if (j + 1 < NB) ok = issue_dp(j + 1) && issue_s(j + 1);
       }
-      if (j + 1 == NB) tc_commit_warp(bar(Ly::B_ACC));
+      if (j + 1 == NB || (j + 1) % grp == 0) tc_commit_warp(bar(Ly::B_ACC));
     }
     // exit-path drain: every MMA issued completes before TMEM is freed
     tc_commit_warp(bar(Ly::B_DRAIN));
@@ -458,6 +499,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) diff_bwd32_kernel(const __grid
     mbar_init(bar(Ly::B_DS), N_EW);  // two: dV's A(j + 1) may be there before the issuer has looked at A(j)
     mbar_init(bar(Ly::B_DS + 1), N_EW);
     mbar_init(bar(Ly::B_ACC), 1);
+    mbar_init(bar(Ly::B_ACCE), N_EW);
     mbar_init(bar(Ly::B_DRAIN), 1);
     wait_for_kernel_before();
     // without any time to wait there is nothing to start: the first load would be waited for

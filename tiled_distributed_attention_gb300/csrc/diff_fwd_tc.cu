@@ -9,7 +9,7 @@
 // Q's and K's columns that is their map's (K = d/2 each), the P_m V products take the same V.
 // At the end both accumulators lie in the same TMEM lanes, so each warpgroup reads both of them
 // for one half of the columns and writes O = O_1 / l_1 - lam O_2 / l_2 (and O_2 for the backward
-// pass) rounded once; no partial output leaves the SM.
+// pass) rounded once.
 //
 // A work unit is (batch, KV head, query head of the group, 128-row query tile); causal units go heaviest
 // first within batches of heads that fill the grid a few times (Params::batch).  Where tiles would
@@ -26,11 +26,11 @@
 // 2,350-2,450 cycles for its 1,536 cycles of products; an exponential costs 3.84 cycles a warp and
 // sub-partition, and the products' issue takes dispatch slots from the sub-partition of the MMA warp.
 // Slower (no mask): two warps a row 2.70 ms, 64-key steps with two score buffers a map 2.70 ms, P handed
-// over in halves 2.53 ms.
+// over in halves 2.53 ms, an MMA issuer for each map 2.78 ms, products issued in paced groups of four 2.57 ms.
 //
 // Persistent grid, one CTA per SM; warps 0-7 softmax, warp 8 MMA issuer, warp 9 producer, warps 10-11
-// idle.  TMEM (512 columns): S_1 | S_2 | O_1 | O_2; P_m overwrites S_m.  K, V and Q tiles come by
-// partition ([partitions][rows][d] tensor maps): rows past a partition's end are zeros.
+// idle.  TMEM (512 columns): S_1 | S_2 | O_1 | O_2; P_m overwrites S_m.  K, V and Q tiles come by head
+// ([heads][rows][d] tensor maps): rows past a head's end are zeros.
 // Every mbarrier wait is bounded: a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT in the status
 // block, every role of the CTA stops, in-flight copies and MMAs are drained and TMEM is freed.
 #include <cuda.h>

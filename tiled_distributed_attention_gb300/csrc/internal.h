@@ -78,6 +78,7 @@ struct TileArgs {
   int64_t wait_limit_ns;
   void* pieces;  // fp32 inputs: device buffer for the bf16 pieces of Q, K and V (f32_pieces_layout)
   bool pieces_ready;  // they are there already; Q, K and V are not read
+  int32_t chunk;      // fp32 inputs: most key blocks before O moves from tensor memory to part_o (0: at the end only)
 };
 // Kernel launchers return a cudaError_t value as int; *err gets a message on failure.
 int launch_tile_fwd_tc(const TileArgs& a, void* stream, std::string* err);

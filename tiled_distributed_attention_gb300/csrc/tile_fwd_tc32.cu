@@ -71,9 +71,17 @@ struct Params {
   int64_t q_rows, kv_parts;  // of one piece: rows of Q, B*Hq*S, and partitions of K and V, B*Hkv*P
   const uint32_t* q_pieces;  // Q's bf16 pieces [3][q_rows][D], as packed pairs
   int32_t B, Hq, Hkv, P, n_items, n_slots, nqt, nb, causal;
+  int32_t chunk;  // most blocks whose products are summed in one accumulation
   float scale_log2;
   int64_t wait_limit_ns;
 };
+
+// n blocks in the fewest chunks of at most `most`, as even as can be: the size of one.
+__device__ __forceinline__ int even_chunk(int n, int most) {
+  if (n <= most) return max(n, 1);
+  const int k = (n - 1) / most + 1;
+  return (n - 1) / k + 1;
+}
 
 // 32 lanes x 16 consecutive 32-bit columns: thread i of the warp writes lane (base + i).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -245,6 +253,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_QTMEM));
     }
+    const int64_t prow = (((int64_t)b * prm.Hq + h) * prm.n_slots + it.slot) * L + q_local;
+    float4* const o_row = reinterpret_cast<float4*>(prm.part_o + prow * D + hf * (D / 2));
+    const int chunk = even_chunk(NB, prm.chunk);
+    float moved = 0.f;  // what O's earlier chunks in part_o are to be multiplied by (0: there are none)
     for (int j = 0; j < NB && ok; ++j) {
       int kp, kbk;
       block_at(j, kp, kbk);
@@ -294,7 +306,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // PV(j-1) done: O holds every earlier product and P's buffer is free (PV(j) needs this
       // block's P, so the barrier is never a phase ahead of this wait)
       bool pv_done = (j == 0);
-      if (__any_sync(0xffffffffu, factor != 1.f)) {
+      if (j > 0 && j % chunk == 0) {  // a chunk of O is complete: to part_o, still at the old reference
+        ok = mbar_wait(bar(Ly::B_PVDONE), (uint32_t)((j - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                       ROLE_SOFTMAX, j);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        pv_done = true;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          float o[32];
+          tmem_ld32(tm_o + (uint32_t)c, o);
+          tc_wait_ld();
+          if (q_local < L) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float4 x = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              if (moved != 0.f) {
+                const float4 y = o_row[c / 4 + e];
+                x = make_float4(fmaf(y.x, moved, x.x), fmaf(y.y, moved, x.y), fmaf(y.z, moved, x.z), fmaf(y.w, moved, x.w));
+              }
+              o_row[c / 4 + e] = x;
+            }
+          }
+        }
+        moved = 1.f;
+      } else if (__any_sync(0xffffffffu, factor != 1.f)) {
         ok = mbar_wait(bar(Ly::B_PVDONE), (uint32_t)((j - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
                        ROLE_SOFTMAX, j);
         ok = __all_sync(0xffffffffu, ok);
@@ -312,6 +349,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_st32(tm_o + (uint32_t)c, w);
         }
       }
+      moved *= factor;
       uint32_t p1[16], p2[16], p3[16];
       uint64_t acc2[2] = {0ull, 0ull};
       const uint64_t nm2 = f2_pack(-mref, -mref);
@@ -369,17 +407,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (ok) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t prow = (((int64_t)b * prm.Hq + h) * prm.n_slots + it.slot) * L + q_local;
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         float o[32];
         tmem_ld32(tm_o + (uint32_t)c, o);
         tc_wait_ld();
         if (q_local < L) {
-          float4* dst = reinterpret_cast<float4*>(prm.part_o + prow * D + hf * (D / 2) + c);
+          if (moved != 0.f)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 y = o_row[c / 4 + e];
+              o[4 * e] = fmaf(y.x, moved, o[4 * e]);
+              o[4 * e + 1] = fmaf(y.y, moved, o[4 * e + 1]);
+              o[4 * e + 2] = fmaf(y.z, moved, o[4 * e + 2]);
+              o[4 * e + 3] = fmaf(y.w, moved, o[4 * e + 3]);
+            }
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+            o_row[c / 4 + e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
         }
       }
       if (q_local < L && hf == 0)
@@ -430,6 +475,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // works on block j, and S(j+2) while it works on block j+1.
     if (ok) ok = issue_s(0);
     if (ok && NB > 1) ok = issue_s(1);
+    const int chunk = even_chunk(NB, prm.chunk);
     for (int j = 0; j < NB && ok; ++j) {
       ok = mbar_wait_warp(bar(Ly::B_PFULL), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_MMA, j);
       if (ok)
@@ -445,7 +491,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
           tc_mma_ts_warp(tmem + COL_O, pa + (uint32_t)(kk * 8), vd + (uint64_t)(kk * 128), idesc_pv,
-                         (j > 0 || pr > 0 || kk > 0) ? 1u : 0u);
+                         (j % chunk > 0 || pr > 0 || kk > 0) ? 1u : 0u);
       }
       tc_commit_warp(bar(Ly::B_VEMPTY + (j & 1)));  // V(j)'s stage free once these products complete
       tc_commit_warp(bar(Ly::B_PVDONE));  // O holds PV(0..j) and P is free for block j+1
@@ -678,6 +724,7 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   prm.nqt = (int32_t)nqt;
   prm.nb = (int32_t)nb;
   prm.causal = a.causal;
+  prm.chunk = a.chunk > 0 ? a.chunk : 0x7fffffff;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
   auto kern = tile_fwd_tc32_kernel<D>;
