@@ -310,8 +310,8 @@ int mesh_attn_bwd_reduce(const mesh_attn_plan* plan, mesh_attn_dtype out_dtype, 
  *   q [B, Hq, S, d] with q_strides[3] = the batch, head and token strides in elements (the d
  *   columns are consecutive), and q_out with q_out_strides; k, Hk likewise.  Hq or Hk may be 0 (its
  *   pointers are then not used).  An output may be its input with the same strides; otherwise
- *   nothing may overlap.  Aligned to the element size; 16-byte aligned tensors whose strides,
- *   members of a pair and unrotated columns are multiples of 16 bytes take the fast path.
+ *   nothing may overlap.  Aligned to the element size; accesses are as wide as the addresses, the
+ *   strides, the columns of a pair's members and the unrotated columns allow, 16 bytes at most.
  *   freq, pair_axis   HOST arrays of n_pairs: radians a position, finite; axis, 0 .. n_axes - 1
  *                     (n_axes 1 to 8).  Read before the call returns.
  *   positions   device integers of pos_bits 32 or 64, any sign; pos_strides[3] = axis, batch and token

@@ -82,6 +82,20 @@ def test_forward_and_backward(lib, case, S):
     check(lib, rope, k, pos, dk, inverse=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("style", ["half", "adjacent"])
+@pytest.mark.parametrize("n", [32, 28, 30, 29])  # pairs of 64 columns: 16, 8, 4 and 2 bytes of bf16 an access
+@pytest.mark.parametrize("shift", [0, 2, 4])     # elements by which the tensors begin off a 16-byte boundary
+def test_every_width_of_access(lib, dtype, style, n, shift):
+    rope = lib.MeshRope(64, (n,), style=style)
+    x, pos = make((2, 3, 9, 64), dtype, 8), positions(1, 2, 9, 9)
+    x_d = torch.nn.functional.pad(x.cuda(), (shift, 8 - shift))[..., shift: shift + 64]  # rows 72 elements apart
+    out = torch.full((2, 3, 9, 72), 7.0, dtype=dtype, device="cuda")
+    lib.mesh_attn_rope(rope, x_d, None, pos.cuda(), out[..., shift: shift + 64], None)
+    check(lib, rope, x, pos, out[..., shift: shift + 64])
+    assert (out[..., :shift] == 7).all() and (out[..., shift + 64:] == 7).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_positions_of_either_width_shared_and_strided(lib, dtype):
     rope = lib.MeshRope(64, (8, 8), groups=2)

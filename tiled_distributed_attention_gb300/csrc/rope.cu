@@ -89,7 +89,7 @@ __device__ __forceinline__ void narrow(const float (&f)[V], Vec<T, V>& x) {
   }
 }
 
-// V: elements of one access (16 bytes' worth, or 1 where sizes or addresses do not allow it).
+// V: elements of one access: 16 bytes' worth, or the half, quarter or eighth that sizes and addresses allow.
 // ADJ: adjacent pairs.  A rotation item is V pairs by two accesses, one for each member, or for
 // adjacent pairs one access of V / 2 pairs (two of one element at V = 1), so that neighbouring threads
 // always touch neighbouring bytes; a copy item is V elements behind the rotated ones.
@@ -266,9 +266,12 @@ extern "C" int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32
     };
     const Arg args[2] = {{Hq, q, q_strides, q_out, q_out_strides}, {Hk, k, k_strides, k_out, k_out_strides}};
     const size_t es = dtype == MESH_ATTN_BF16 ? 2 : 4;
-    const int vec = (int)(16 / es);
-    // 16-byte accesses where every address they touch allows them
-    bool wide = (adjacent ? 2 * n_pairs : n_pairs) % vec == 0 && (dh - 2 * n_pairs) % vec == 0;
+    int vec = (int)(16 / es);  // elements of an access: the most that divide every address and size
+    auto divides = [&](int64_t elements) {
+      while (elements % vec != 0) vec /= 2;
+    };
+    divides(adjacent ? 2 * n_pairs : n_pairs);
+    divides(dh - 2 * n_pairs);
     for (int w = 0; w < 2; ++w) {
       const Arg& a = args[w];
       prm.H[w] = a.H;
@@ -283,11 +286,13 @@ extern "C" int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32
           return set_last_error(MESH_ATTN_ERR_INVALID_ARG, "an output must not be broadcast (stride 0)");
       prm.x[w] = a.x;
       prm.y[w] = a.y;
-      wide = wide && mesh::is_aligned(a.x, 16) && mesh::is_aligned(a.y, 16);
+      divides((int64_t)(reinterpret_cast<uintptr_t>(a.x) / es));
+      divides((int64_t)(reinterpret_cast<uintptr_t>(a.y) / es));
       for (int i = 0; i < 3; ++i) {
         prm.xs[w][i] = a.xs[i];
         prm.ys[w][i] = a.ys[i];
-        wide = wide && a.xs[i] % vec == 0 && a.ys[i] % vec == 0;
+        divides(a.xs[i]);
+        divides(a.ys[i]);
       }
     }
     if (!mesh::is_aligned(positions, pos_bits / 8))
@@ -307,12 +312,16 @@ extern "C" int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32
     std::string err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int ce;
+    const bool adj = adjacent != 0;
     if (dtype == MESH_ATTN_BF16)
-      ce = wide ? launch<__nv_bfloat16, 8>(prm, adjacent != 0, sms, st, &err)
-                : launch<__nv_bfloat16, 1>(prm, adjacent != 0, sms, st, &err);
+      ce = vec == 8   ? launch<__nv_bfloat16, 8>(prm, adj, sms, st, &err)
+           : vec == 4 ? launch<__nv_bfloat16, 4>(prm, adj, sms, st, &err)
+           : vec == 2 ? launch<__nv_bfloat16, 2>(prm, adj, sms, st, &err)
+                      : launch<__nv_bfloat16, 1>(prm, adj, sms, st, &err);
     else
-      ce = wide ? launch<float, 4>(prm, adjacent != 0, sms, st, &err)
-                : launch<float, 1>(prm, adjacent != 0, sms, st, &err);
+      ce = vec == 4   ? launch<float, 4>(prm, adj, sms, st, &err)
+           : vec == 2 ? launch<float, 2>(prm, adj, sms, st, &err)
+                      : launch<float, 1>(prm, adj, sms, st, &err);
     return mesh::launch_status(ce, err);
   });
 }
