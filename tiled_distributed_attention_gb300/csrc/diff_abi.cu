@@ -23,10 +23,7 @@ TablesLayout tables_layout(const Plan& p) {
     return o;
   };
   t.flat_item = take(sizeof(DevItem));
-  t.flat_list = take(2 * 4);
-  t.slot_off = take(p.slot_off.size() * 4);
-  t.items = take(p.dev_items.size() * sizeof(DevItem));
-  t.kv_list = take(p.kv_list.size() * 4);
+  t.flat_list = take(4);
   t.total = at;
   return t;
 }
@@ -48,14 +45,11 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
     return o;
   };
   const size_t qrows = (size_t)B * Hq * plan.S;
-  const size_t prows = (size_t)B * Hq * plan.n_slots() * (size_t)plan.L;
   const bool f32 = dt == MESH_ATTN_F32;
-  // fp32 forward: partial outputs where the plan's slots split the keys (rows_direct)
   const int64_t nb = (plan.S + 127) / 128;
-  const bool slots = plan.n_slots() != plan.P && plan.L >= 128 && 8 * nb * B * Hq < MAX_SMS;
   if (!backward) {
     // fp32: both maps' outputs always go through the merge; bf16: those of tiles cut into parts
-    if (const size_t rows = 2 * (f32 ? (slots ? std::max(prows, qrows) : qrows)
+    if (const size_t rows = 2 * (f32 ? qrows * diff_fwd32_parts(plan.S, B, Hq)
                                      : (size_t)diff_fwd_max_parts(plan.S, B, Hq, plan.causal) * 128)) {
       w.part_o = take(rows * d * 4);
       w.part_lse = take(rows * 4);
@@ -85,10 +79,6 @@ DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, in
   }
   w.total = at;
   return w;
-}
-
-bool rows_direct(const DiffArgs& a, int32_t H, int sms) {
-  return a.single_slot || a.L < 128 || 4 * ((a.S + 127) / 128) * a.B * H >= sms;
 }
 
 }  // namespace mesh
@@ -157,15 +147,11 @@ DiffArgs make_args(const mesh_attn_plan* plan, const void* tables, int32_t B, in
   a.LSE = LSE;
   a.ws = static_cast<char*>(workspace);
   a.S = pl.S;
-  a.L = pl.L;
   a.B = B;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.d = d;
-  a.P = pl.P;
-  a.n_slots = pl.n_slots();
   a.causal = pl.causal ? 1 : 0;
-  a.single_slot = pl.n_slots() == pl.P;
   a.scale = scale;
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.wait_limit_ns = mesh::current_wait_limit_ns();
@@ -199,12 +185,9 @@ int mesh_attn_plan_tables_write(const mesh_attn_plan* plan, void* out, size_t ou
       if (bytes) std::memcpy(o + off, src, bytes);
     };
     const mesh::DevItem flat{0, 0, 0, 1};
-    const int32_t list[2] = {0, 1};  // its KV partition, and as a slot CSR {0, 1}
+    const int32_t list = 0;  // its KV partition
     put(t.flat_item, &flat, sizeof(flat));
-    put(t.flat_list, list, sizeof(list));
-    put(t.slot_off, p.slot_off.data(), p.slot_off.size() * 4);
-    put(t.items, p.dev_items.data(), p.dev_items.size() * sizeof(mesh::DevItem));
-    put(t.kv_list, p.kv_list.data(), p.kv_list.size() * 4);
+    put(t.flat_list, &list, sizeof(list));
     return (int)MESH_ATTN_OK;
   });
 }
@@ -242,25 +225,23 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     }
     // fp32: split into bf16 pieces, one map a head with the other half of its query's columns zero, so
     // that the plain fp32 tile kernel over 2 Hq heads gives both maps; then the merge
-    int sms = 0;
-    if ((rc = sm_count(&sms))) return rc;
-    const bool direct = mesh::rows_direct(a, 2 * Hq, sms);
+    const int32_t parts = mesh::diff_fwd32_parts(a.S, B, Hq);
     if ((rc = launch_status(mesh::launch_diff_split(a, w, stream, &err), err))) return rc;
     mesh::TileArgs t{};
     const char* tb = static_cast<const char*>(tables);
     t.part_o = reinterpret_cast<float*>(a.ws + w.part_o);
     t.part_lse = reinterpret_cast<float*>(a.ws + w.part_lse);
-    t.items = reinterpret_cast<const mesh::DevItem*>(tb + (direct ? a.tl.flat_item : a.tl.items));
-    t.kv_list = reinterpret_cast<const int32_t*>(tb + (direct ? a.tl.flat_list : a.tl.kv_list));
+    t.items = reinterpret_cast<const mesh::DevItem*>(tb + a.tl.flat_item);
+    t.kv_list = reinterpret_cast<const int32_t*>(tb + a.tl.flat_list);
     t.status = d_status;
     t.S = a.S;
-    t.L = direct ? a.S : a.L;
+    t.L = a.S;
     t.B = B;
     t.Hq = 2 * Hq;
     t.Hkv = Hkv;
     t.d = d;
-    t.P = direct ? 1 : a.P;
-    t.n_items = t.n_slots = direct ? 1 : a.n_slots;
+    t.P = t.n_items = 1;
+    t.n_slots = t.parts = parts;
     t.causal = a.causal;
     t.scale = scale;
     t.scale_log2 = a.scale_log2;
@@ -272,7 +253,7 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     // added in fp32 with rounding.
     t.chunk = 13;
     if ((rc = launch_status(mesh::launch_tile_fwd_tc32(t, stream, &err), err))) return rc;
-    return launch_status(mesh::launch_diff_merge(a, w, direct, stream, &err), err);
+    return launch_status(mesh::launch_diff_merge(a, w, parts, stream, &err), err);
   });
 }
 

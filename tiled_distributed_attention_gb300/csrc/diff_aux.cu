@@ -15,7 +15,7 @@ namespace mesh {
 namespace daux {
 
 constexpr int THREADS = 256;
-constexpr int MAX_SLOTS = 64;  // R <= 64 for P <= 4096
+constexpr int MAX_PARTS = 16;  // of a tile's keys (diff_fwd32_parts)
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
@@ -70,86 +70,60 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const DiffArgs a, uint2*
   }
 }
 
-// O = sum_t w1_t O1_t - lam sum_t w2_t O2_t over a row's slots, w = exp(lse_t - lse) of each map, and
-// the second map's output, which the backward pass needs.  A CTA owns ROWS rows of one (batch,
-// head, partition); a thread a 16-byte piece of both maps.
-template <int D>
-__global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const float* part_o, const float* part_lse,
-                                                        const int32_t* slot_off, int P, int64_t L, int n_slots, int n_rblk) {
-  constexpr int Q4 = D / 4;
-  constexpr int PER = 2;
-  constexpr int ROWS = PER * THREADS / Q4;
-  __shared__ float w_s[2][MAX_SLOTS][ROWS];
+// O = sum_t w1_t O1_t - lam sum_t w2_t O2_t over a row's parts, w = exp(lse_t - lse) of each map, O2 (which the
+// backward pass needs) and the LSEs.  A thread takes a 16-byte piece of one map's row, all parts' loads in
+// flight together (MAXP of them, 1 where nothing is cut); the maps meet in shared memory.
+template <int D, int MAXP>
+__global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const float* part_o, const float* part_lse, int parts,
+                                                        int n_rblk) {
+  constexpr int Q4 = D / 4, ROWS = THREADS / (2 * Q4);
+  __shared__ float4 o2_s[ROWS * Q4];
   wait_for_kernel_before();
   if (*reinterpret_cast<volatile int32_t*>(a.status) != 0) return;
-  const int tid = threadIdx.x;
-  const int rb = (int)(blockIdx.x % (unsigned)n_rblk);
-  const int bhp = (int)(blockIdx.x / (unsigned)n_rblk);
-  const int p = bhp % P, bh = bhp / P;
-  const int64_t r0 = (int64_t)rb * ROWS;
-  const int nrows = (int)min((int64_t)ROWS, L - r0);
-  const int s0 = __ldg(slot_off + p), ns = __ldg(slot_off + p + 1) - s0;
-  if (s0 < 0 || ns < 0 || ns > MAX_SLOTS || s0 + ns > n_slots) {
-    if (tid == 0) record_error(a.status, MESH_ATTN_ERR_OUT_OF_RANGE, 5, (int32_t)blockIdx.x);
-    return;
-  }
-  const int64_t base[2] = {((2 * (int64_t)bh) * n_slots + s0) * L + r0, ((2 * (int64_t)bh + 1) * n_slots + s0) * L + r0};
-  // the first slot's pieces do not depend on the weights: their loads go out first
-  float4 head[PER][2];
+  const int m = (int)threadIdx.x / (ROWS * Q4), at = (int)threadIdx.x % (ROWS * Q4), c = at % Q4 * 4;
+  const int64_t bh = blockIdx.x / (unsigned)n_rblk, row = (int64_t)(blockIdx.x % (unsigned)n_rblk) * ROWS + at / Q4;
+  const bool in = row < a.S;
+  // the parts that the row's tile of 128 has: no more than its 64-key blocks
+  const int nb = (int)((a.S + 63) / 64), k = min(parts, a.causal ? min(nb, 2 * (int)(row / 128) + 2) : nb);
+  const int64_t base = (2 * bh + m) * parts * a.S + row;  // row of part t: base + t S
+  float w[MAXP];
+  float4 v[MAXP];
 #pragma unroll
-  for (int k = 0; k < PER; ++k)
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int idx = tid + k * THREADS, r = idx / Q4;
-      head[k][m] = r < nrows && ns > 0 ? __ldcs(reinterpret_cast<const float4*>(part_o + (base[m] + r) * D + idx % Q4 * 4))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  for (int i = tid; i < 2 * ns * ROWS; i += THREADS) {
-    const int r = i % ROWS, t = i / ROWS % ns, m = i / ROWS / ns;
-    w_s[m][t][r] = r < nrows ? __ldg(part_lse + base[m] + (int64_t)t * L + r) : -INFINITY;
+  for (int t = 0; t < MAXP; ++t) {
+    const bool there = in && t < k;
+    w[t] = there ? __ldg(part_lse + base + t * a.S) : -INFINITY;
+    v[t] = there ? __ldcs(reinterpret_cast<const float4*>(part_o + (base + t * a.S) * D + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float M = -INFINITY, W = 0.f;
+#pragma unroll
+  for (int t = 0; t < MAXP; ++t) M = fmaxf(M, w[t]);
+  const float Ms = M == -INFINITY ? 0.f : M, lse = w[0];
+#pragma unroll
+  for (int t = 0; t < MAXP; ++t) {
+    w[t] = MAXP == 1 ? (w[t] == -INFINITY ? 0.f : 1.f) : expf(w[t] - Ms);
+    W += w[t];
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int t = 0; t < MAXP; ++t) {
+    const float f = t < k ? w[t] * inv : 0.f;
+    o.x = fmaf(f, v[t].x, o.x);
+    o.y = fmaf(f, v[t].y, o.y);
+    o.z = fmaf(f, v[t].z, o.z);
+    o.w = fmaf(f, v[t].w, o.w);
+  }
+  const int64_t dst = (bh * a.S + row) * D + c;
+  if (m == 1) {
+    o2_s[at] = o;
+    if (in && a.O2) store4(static_cast<float*>(a.O2) + dst, o);
+  }
+  if (in && c == 0) a.LSE[(2 * bh + m) * a.S + row] = MAXP == 1 ? lse : W == 0.f ? -INFINITY : Ms + logf(W);
   __syncthreads();
-  if (tid < 2 * ROWS) {
-    const int r = tid % ROWS, m = tid / ROWS;
-    float M = -INFINITY;
-    for (int t = 0; t < ns; ++t) M = fmaxf(M, w_s[m][t][r]);
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float W = 0.f;
-    for (int t = 0; t < ns; ++t) {
-      const float e = expf(w_s[m][t][r] - Ms);
-      w_s[m][t][r] = e;
-      W += e;
-    }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
-    for (int t = 0; t < ns; ++t) w_s[m][t][r] *= inv;
-    if (r < nrows) a.LSE[(2 * (int64_t)bh + m) * a.S + (int64_t)p * L + r0 + r] = W > 0.f ? Ms + logf(W) : -INFINITY;
-  }
-  __syncthreads();
-  const float lam = lam_of<float>(a.lam, a.lam_n, bh % a.Hq);
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int idx = tid + k * THREADS, r = idx / Q4, c = idx % Q4 * 4;
-    if (r >= nrows) continue;
-    float4 o[2];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const float w0 = ns > 0 ? w_s[m][0][r] : 0.f;
-      o[m] = make_float4(head[k][m].x * w0, head[k][m].y * w0, head[k][m].z * w0, head[k][m].w * w0);
-      const float* src = part_o + (base[m] + r) * D + c;
-#pragma unroll 4
-      for (int t = 1; t < ns; ++t) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(src + (int64_t)t * L * D));
-        const float w = w_s[m][t][r];
-        o[m].x = fmaf(w, v.x, o[m].x);
-        o[m].y = fmaf(w, v.y, o[m].y);
-        o[m].z = fmaf(w, v.z, o[m].z);
-        o[m].w = fmaf(w, v.w, o[m].w);
-      }
-    }
-    const int64_t at = ((int64_t)bh * a.S + (int64_t)p * L + r0 + r) * D + c;
-    store4(static_cast<float*>(a.O) + at, make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
-                                                      fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
-    if (a.O2) store4(static_cast<float*>(a.O2) + at, o[1]);
+  if (m == 0 && in) {
+    const float lam = lam_of<float>(a.lam, a.lam_n, (int)(bh % a.Hq));
+    const float4 y = o2_s[at];
+    store4(static_cast<float*>(a.O) + dst, make_float4(fmaf(-lam, y.x, o.x), fmaf(-lam, y.y, o.y), fmaf(-lam, y.z, o.z), fmaf(-lam, y.w, o.w)));
   }
 }
 
@@ -267,28 +241,35 @@ int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, s
                     "diff split launch", err);
 }
 
-template <int D>
-static int merge_d(const DiffArgs& a, const DiffWorkspace& w, bool flat, cudaStream_t st, std::string* err) {
-  constexpr int ROWS = 2 * daux::THREADS / (D / 4);
-  const int64_t L = flat ? a.S : a.L;
-  const int P = flat ? 1 : a.P;
-  const int64_t n_rblk = (L + ROWS - 1) / ROWS;
-  const int64_t blocks = n_rblk * a.B * a.Hq * P;
-  if (blocks > 0x7fffffffLL || n_rblk > 0x7fffffffLL) {
+// Parts of every tile's keys in the fp32 forward: what fills the SMs, two 64-key blocks (2 us each) at least, where
+// that saves more than the merge of more than one costs (2 to 3 us).  One head of 2,304 tokens, d = 128, causal (36
+// tiles of up to 36 blocks): 84 us whole, @P@ in four parts.
+int32_t diff_fwd32_parts(int64_t S, int32_t B, int32_t Hq) {
+  constexpr int SMS = 152;  // the whole GPU's: so the workspace's size needs no device
+  const int64_t tiles = (S + 127) / 128 * B * 2 * Hq, nb = (S + 63) / 64;
+  if (tiles == 0 || 2 * tiles > SMS) return 1;
+  const int64_t parts = std::min<int64_t>({SMS / tiles, nb / 2, daux::MAX_PARTS});
+  return (int32_t)(parts < 2 || nb - nb / parts < 2 ? 1 : parts);
+}
+
+template <int D, int MAXP>
+static int merge_d(const DiffArgs& a, const DiffWorkspace& w, int32_t parts, cudaStream_t st, std::string* err) {
+  constexpr int ROWS = daux::THREADS / (D / 2);
+  const int64_t n_rblk = (a.S + ROWS - 1) / ROWS, blocks = n_rblk * a.B * a.Hq;
+  if (blocks > 0x7fffffffLL) {
     *err = "too many rows for one merge launch";
     return (int)cudaErrorInvalidConfiguration;
   }
-  const cudaError_t e = launch_behind(
-      daux::merge_kernel<D>, dim3((unsigned)blocks), daux::THREADS, 0, st, a, reinterpret_cast<const float*>(a.ws + w.part_o),
-      reinterpret_cast<const float*>(a.ws + w.part_lse),
-      reinterpret_cast<const int32_t*>(static_cast<const char*>(a.tables) + (flat ? a.tl.flat_list : a.tl.slot_off)), P, L,
-      (int)(flat ? 1 : a.n_slots), (int)n_rblk);
+  const cudaError_t e = launch_behind(daux::merge_kernel<D, MAXP>, dim3((unsigned)blocks), daux::THREADS, 0, st, a,
+                                      reinterpret_cast<const float*>(a.ws + w.part_o),
+                                      reinterpret_cast<const float*>(a.ws + w.part_lse), (int)parts, (int)n_rblk);
   return daux::done(e, "diff merge launch", err);
 }
 
-int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, bool flat, void* stream, std::string* err) {
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, int32_t parts, void* stream, std::string* err) {
   cudaStream_t st = (cudaStream_t)stream;
-  return a.d == 128 ? merge_d<128>(a, w, flat, st, err) : merge_d<64>(a, w, flat, st, err);
+  if (parts == 1) return a.d == 128 ? merge_d<128, 1>(a, w, parts, st, err) : merge_d<64, 1>(a, w, parts, st, err);
+  return a.d == 128 ? merge_d<128, daux::MAX_PARTS>(a, w, parts, st, err) : merge_d<64, daux::MAX_PARTS>(a, w, parts, st, err);
 }
 
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err) {

@@ -78,6 +78,7 @@ struct TileArgs {
   int64_t wait_limit_ns;
   void* pieces;  // fp32 inputs: device buffer for the bf16 pieces of Q, K and V (f32_pieces_layout)
   bool pieces_ready;  // they are there already; Q, K and V are not read
+  int32_t parts;      // fp32 inputs: of each work item's keys (0 or 1: none), n_slots counting them
   int32_t chunk;      // fp32 inputs: most key blocks before O moves from tensor memory to part_o (0: at the end only)
 };
 // Kernel launchers return a cudaError_t value as int; *err gets a message on failure.
@@ -164,15 +165,14 @@ int launch_bwd_reduce(const ReduceArgs& a, mesh_attn_dtype out_dtype, void* stre
 constexpr int MAX_SMS = 256;
 
 // A plan's constant tables as the differential calls read them from device memory, in one block:
-// [header | flat item and lists | slot_off | items | kv_list].  The header's tag says which plan they are
-// of; the first kernel of a call compares it with the plan it was given.
+// [header | the whole sequence as one work item, and its list of one partition].  The header's tag says which
+// plan they are of; the first kernel of a call compares it with the plan it was given.
 struct TablesHeader {
   uint64_t magic, tag;
 };
 constexpr uint64_t TABLES_MAGIC = 0x6d6573685f746162ull;
 struct TablesLayout {
-  size_t flat_item, flat_list;  // the whole sequence as one partition and one work item
-  size_t slot_off, items, kv_list, total;
+  size_t flat_item, flat_list, total;
 };
 TablesLayout tables_layout(const Plan& plan);
 uint64_t plan_tag(const Plan& plan);
@@ -195,9 +195,8 @@ struct DiffArgs {
   void* dV;
   void* dlam;
   char* ws;
-  int64_t S, L;
-  int32_t B, Hq, Hkv, d, P, n_slots, causal, lam_n;
-  bool single_slot;  // every partition has one slot: no partial outputs to merge
+  int64_t S;
+  int32_t B, Hq, Hkv, d, causal, lam_n;
   float scale, scale_log2;
   int64_t wait_limit_ns;
 };
@@ -213,11 +212,6 @@ struct DiffWorkspace {
 };
 DiffWorkspace diff_workspace(const Plan& plan, mesh_attn_dtype dt, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                              bool backward);
-// Whether the fp32 forward over the rows of H heads (two a query head, one a map) takes the whole sequence as
-// one work item: unless its 128-row blocks occupy less than a quarter of the SMs, the plan splits the
-// keys and its partitions fill a tile.  One head of 2,304 tokens, d = 128, causal (36 blocks), us: 84 whole, 54,
-// 43 and 61 by 4, 9 and 16 partitions.
-bool rows_direct(const DiffArgs& a, int32_t H, int sms);
 // bf16 forward on the tensor cores, with its merge where tiles are cut into parts; the most parts there may be.
 int launch_diff_fwd_tc(const DiffArgs& a, const DiffWorkspace& w, int sms, void* stream, std::string* err);
 int64_t diff_fwd_max_parts(int64_t S, int32_t B, int32_t Hq, bool causal);
@@ -236,8 +230,9 @@ struct BwdPieces {
   size_t q, k, v, g, total;  // the bf16 pieces of Q, K, V and dO ([3][rows][d] each), in bytes
 };
 BwdPieces bwd32_pieces_layout(int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d);
-// fp32 forward's merge; `flat`: the partials are of the whole sequence as one partition with one slot.
-int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, bool flat, void* stream, std::string* err);
+// fp32 forward: parts of every tile's keys, and the merge of their outputs.
+int32_t diff_fwd32_parts(int64_t S, int32_t B, int32_t Hq);
+int launch_diff_merge(const DiffArgs& a, const DiffWorkspace& w, int32_t parts, void* stream, std::string* err);
 int launch_diff_prep(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, void* stream, std::string* err);
 // dlam from n_part partial sums of every (batch, head).
 int launch_diff_dlam(const DiffArgs& a, const DiffWorkspace& w, mesh_attn_dtype dt, int64_t n_part, void* stream,

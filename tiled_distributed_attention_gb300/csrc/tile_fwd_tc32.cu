@@ -35,6 +35,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <string>
 
 #include "abi_util.h"
@@ -71,6 +72,7 @@ struct Params {
   int64_t q_rows, kv_parts;  // of one piece: rows of Q, B*Hq*S, and partitions of K and V, B*Hkv*P
   const uint32_t* q_pieces;  // Q's bf16 pieces [3][q_rows][D], as packed pairs
   int32_t B, Hq, Hkv, P, n_items, n_slots, nqt, nb, causal;
+  int32_t parts;  // of a work item's key blocks, each with a slot of its own
   int32_t chunk;  // most blocks whose products are summed in one accumulation
   float scale_log2;
   int64_t wait_limit_ns;
@@ -140,6 +142,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // Units are numbered KV-head-major: (batch, KV head, work item in launch order, query head of
   // the group, query tile), so the CTAs resident together share one KV head's partitions in L2.
   int64_t uu = blockIdx.x;
+  const int part = (int)(uu % prm.parts); uu /= prm.parts;
   const int g = prm.Hq / prm.Hkv;
   const int qt = (int)(uu % prm.nqt); uu /= prm.nqt;
   const int gi = (int)(uu % g); uu /= g;
@@ -154,8 +157,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   int NB = 0;
   if (unit_ok)
     for (int ki = 0; ki < it.n_kv; ++ki) NB += kblocks(__ldg(prm.kv_list + it.kv_off + ki), p, prm.causal, prm.nb, qt);
+  int j0 = 0;  // this part's first block
+  if (prm.parts > 1 && NB > 0) {
+    const int k = min(prm.parts, NB), n = NB;
+    j0 = min(part, k) * n / k;
+    NB = min(part + 1, k) * n / k - j0;
+    if (NB == 0) return;  // fewer blocks than parts: the merge does not look at this one
+  }
   auto block_at = [&](int j, int& kp, int& kbk) {
-    int r = j;
+    int r = j0 + j;
     for (int ki = 0; ki < it.n_kv; ++ki) {
       kp = __ldg(prm.kv_list + it.kv_off + ki);
       const int n = kblocks(kp, p, prm.causal, prm.nb, qt);
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_QTMEM));
     }
-    const int64_t prow = (((int64_t)b * prm.Hq + h) * prm.n_slots + it.slot) * L + q_local;
+    const int64_t prow = (((int64_t)b * prm.Hq + h) * prm.n_slots + it.slot * prm.parts + part) * L + q_local;
     float4* const o_row = reinterpret_cast<float4*>(prm.part_o + prow * D + hf * (D / 2));
     const int chunk = even_chunk(NB, prm.chunk);
     float moved = 0.f;  // what O's earlier chunks in part_o are to be multiplied by (0: there are none)
@@ -679,7 +689,7 @@ template <int D>
 static int launch(const TileArgs& a, void* stream, std::string* err) {
   const int64_t nqt = (a.L + BM - 1) / BM;
   const int64_t nb = (a.L + BN - 1) / BN;
-  const int64_t units = (int64_t)a.n_items * a.B * a.Hq * nqt;
+  const int64_t units = (int64_t)a.n_items * a.B * a.Hq * nqt * std::max(1, a.parts);
   if (units <= 0) return (int)cudaSuccess;
   const int64_t q_rows = (int64_t)a.B * a.Hq * a.S, kv_rows = (int64_t)a.B * a.Hkv * a.S;
   if (units > 0x7fffffff || 3 * q_rows >= ((int64_t)1 << 31) || 3 * kv_rows >= ((int64_t)1 << 31)) {
@@ -724,6 +734,7 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   prm.nqt = (int32_t)nqt;
   prm.nb = (int32_t)nb;
   prm.causal = a.causal;
+  prm.parts = std::max(1, a.parts);
   prm.chunk = a.chunk > 0 ? a.chunk : 0x7fffffff;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
