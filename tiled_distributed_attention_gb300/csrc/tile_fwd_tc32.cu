@@ -316,32 +316,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // PV(j-1) done: O holds every earlier product and P's buffer is free (PV(j) needs this
       // block's P, so the barrier is never a phase ahead of this wait)
       bool pv_done = (j == 0);
-      if (j > 0 && j % chunk == 0) {  // a chunk of O is complete: to part_o, still at the old reference
-        ok = mbar_wait(bar(Ly::B_PVDONE), (uint32_t)((j - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
-                       ROLE_SOFTMAX, j);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        pv_done = true;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
-          float o[32];
-          tmem_ld32(tm_o + (uint32_t)c, o);
-          tc_wait_ld();
-          if (q_local < L) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float4 x = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-              if (moved != 0.f) {
-                const float4 y = o_row[c / 4 + e];
-                x = make_float4(fmaf(y.x, moved, x.x), fmaf(y.y, moved, x.y), fmaf(y.z, moved, x.z), fmaf(y.w, moved, x.w));
-              }
-              o_row[c / 4 + e] = x;
-            }
-          }
-        }
-        moved = 1.f;
-      } else if (__any_sync(0xffffffffu, factor != 1.f)) {
+      const bool move = j > 0 && j % chunk == 0;  // O is complete up to block j - 1, and begins anew
+      if (!move && __any_sync(0xffffffffu, factor != 1.f)) {
         ok = mbar_wait(bar(Ly::B_PVDONE), (uint32_t)((j - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
                        ROLE_SOFTMAX, j);
         ok = __all_sync(0xffffffffu, ok);
@@ -359,7 +335,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tmem_st32(tm_o + (uint32_t)c, w);
         }
       }
-      moved *= factor;
       uint32_t p1[16], p2[16], p3[16];
       uint64_t acc2[2] = {0ull, 0ull};
       const uint64_t nm2 = f2_pack(-mref, -mref);
@@ -390,6 +365,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+      }
+      if (move) {  // to part_o: the chunk's O, still at the reference before this block
+        const float old = moved * factor;
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          float o[32];
+          tmem_ld32(tm_o + (uint32_t)c, o);
+          tc_wait_ld();
+          if (q_local < L) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float4 x = make_float4(o[4 * e] * factor, o[4 * e + 1] * factor, o[4 * e + 2] * factor, o[4 * e + 3] * factor);
+              if (old == 1.f) {  // the usual case: the reference has not moved
+                red_add4(reinterpret_cast<float*>(o_row + c / 4 + e), x);
+                continue;
+              }
+              if (moved != 0.f) {
+                const float4 y = __ldcg(o_row + c / 4 + e);
+                x = make_float4(fmaf(y.x, old, x.x), fmaf(y.y, old, x.y), fmaf(y.z, old, x.z), fmaf(y.w, old, x.w));
+              }
+              o_row[c / 4 + e] = x;
+            }
+          }
+        }
+        moved = 1.f;
+      } else {
+        moved *= factor;
       }
       // this warp's 32 keys are packed columns [16 hf, 16 hf + 16) of each piece
       const uint32_t tm_p = tmem + lane_base + COL_P + 16u * (uint32_t)hf;
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (moved != 0.f)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 y = o_row[c / 4 + e];
+              const float4 y = __ldcg(o_row + c / 4 + e);
               o[4 * e] = fmaf(y.x, moved, o[4 * e]);
               o[4 * e + 1] = fmaf(y.y, moved, o[4 * e + 1]);
               o[4 * e + 2] = fmaf(y.z, moved, o[4 * e + 2]);
