@@ -329,8 +329,8 @@ int mesh_attn_rope(mesh_attn_dtype dtype, int32_t B, int64_t S, int32_t d, int32
  * columns of a head's query and key are two halves, q = [q1 | q2], k = [k1 | k2], of d/2 each:
  *   P_m = softmax(scale q_m k_m^T) over the visible keys,  O_m = P_m V,
  *   O = O_1 - lam O_2,   LSE_m the natural-log row log-sum-exps.
- * The tile structure, plans, layouts and masks are those of the calls above (1/sqrt(d/2) is the
- * usual scale); LSE is [B, Hq, 2, S].  Backward, with D_m = dO . O_m and dP = dO V^T:
+ * The plan gives the sequence's length and the mask (its partitions, which share work between
+ * devices, do not matter here); 1/sqrt(d/2) is the usual scale; LSE is [B, Hq, 2, S].  Backward, with D_m = dO . O_m and dP = dO V^T:
  *   dS_1 = P_1 (dP - D_1),  dS_2 = -lam P_2 (dP - D_2),  dV = (P_1 - lam P_2)^T dO,
  *   dq_m = scale dS_m k_m,  dk_m = scale dS_m^T q_m,  dlam_h = - sum over its rows of D_2.
  * lam: lam_n device values of the inputs' type, one per query head (lam_n = Hq) or one for all

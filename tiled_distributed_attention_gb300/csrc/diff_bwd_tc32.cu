@@ -56,7 +56,7 @@ constexpr int NUM_THREADS = 320;
 constexpr int GROUP = 13;
 constexpr int64_t DRAIN_NS = 200000000;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4;
+constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3;
 constexpr uint32_t COL_R1 = 0, COL_A = 0, COL_S = 192, COL_DP = 320, COL_ACC = 384;
 enum Pass { DQ = 0, DK = 1, DV = 2 };
 
@@ -86,7 +86,6 @@ struct Maps {
 };
 
 struct Params {
-  const float* q;
   const float* v;
   const float* g;     // dO
   const float* lse;   // [B, Hq, 2, S]
@@ -664,7 +663,6 @@ int launch_diff_bwd_tc32(const DiffArgs& a, const DiffWorkspace& w, int sms, voi
     return (int)cudaErrorInvalidValue;
   const bool q_parts = splits > 1, kv_parts = splits * group > 1;
   Params p{};
-  p.q = static_cast<const float*>(a.Q);
   p.v = static_cast<const float*>(a.V);
   p.g = static_cast<const float*>(a.dO);
   p.lse = a.LSE;

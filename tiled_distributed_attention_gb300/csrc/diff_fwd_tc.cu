@@ -63,7 +63,7 @@ constexpr int MAX_PARTS = 16;          // of a tile (choose_parts)
 constexpr int64_t DRAIN_NS = 200000000;  // exit-path waits for copies in flight
 
 // roles recorded with an error
-constexpr int ROLE_SOFTMAX = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4;
+constexpr int ROLE_SOFTMAX = 1, ROLE_MMA = 2, ROLE_LOAD = 3;
 
 template <int D>
 struct Layout {
