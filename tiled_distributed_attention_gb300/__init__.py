@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the computation (tile map, greedy order, tile
 attention, LSE merge) runs in the C++ planner and the CUDA kernels behind the C ABI declared
-in include/mesh_attn.h.  The functions carry the same names as the C entry points.  PyTorch
+in include/mesh_attn.h.  The functions carry the same names as the C entry points; those of rotary
+positions and differential attention hand their tensors to _binding.so, an extension module.  PyTorch
 supplies device memory and streams; nothing here computes attention, and there is no CPU
 fallback: if the library is missing, load_library() raises.
 """
@@ -109,7 +110,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    from . import _binding
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("_binding.so is missing, or of another PyTorch: build it (python -c 'import __graft_entry__ as g; "
+                           "g.build()')") from e
     _binding.bind(*(ctypes.cast(getattr(lib, name), c_vp).value for name in (
         "mesh_attn_rope", "mesh_attn_diff_fwd", "mesh_attn_diff_bwd", "mesh_attn_diff_decode")))
     _ext = _binding
