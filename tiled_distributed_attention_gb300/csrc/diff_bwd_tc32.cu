@@ -77,7 +77,7 @@ struct Layout {
   static constexpr uint32_t BAR = VEC + 2 * BS * 16;
   static constexpr int B_RF = 0, B_R1 = 1, B_C0F = 2, B_C0E = B_C0F + 2, B_C1F = B_C0E + 2, B_C1E = B_C1F + 2, B_S = B_C1E + 2,
                        B_SR = B_S + 1, B_DS = B_SR + 1, B_ACC = B_DS + 2, B_DRAIN = B_ACC + 1, NBARS = B_DRAIN + 1;
-  static constexpr uint32_t MISC = BAR + NBARS * 8;  // tmem base, abort flag
+  static constexpr uint32_t MISC = BAR + NBARS * 8;  // tmem base, abort flag, whether to run at all
   static constexpr uint32_t ALLOC = MISC + 16 + 1024;
 };
 
@@ -149,7 +149,9 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
   const int per = (last - first + prm.splits - 1) / prm.splits;
   const int c_begin = min(last, first + split * per), NB = min(last, c_begin + per) - c_begin;
   const int n_groups = max(1, (NB + GROUP - 1) / GROUP), grp = max(1, (NB + n_groups - 1) / n_groups);
-  const bool run = *abort_flag == 0 && NB > 0;
+  // The same for all warps: the elementwise warps meet at named barriers, which wait without a limit.  (The abort
+  // flag may be set by a warp that is ahead; the vote in the block loop carries such an abort to all of them.)
+  const bool run = *reinterpret_cast<const volatile int32_t*>(smem + Ly::MISC + 8) != 0 && NB > 0;
 
   if (warp < N_EW) {
     // ================================================================ elementwise
@@ -501,7 +503,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) diff_bwd32_kernel(const __grid
     wait_for_kernel_before();
     // without any time to wait there is nothing to start: the first load would be waited for
     if (prm.wait_limit_ns <= 0) record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
-    *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
+    const bool stop = *reinterpret_cast<volatile int32_t*>(prm.status) != 0;
+    *abort_flag = stop ? 1 : 0;
+    *reinterpret_cast<volatile int32_t*>(smem + Ly::MISC + 8) = stop ? 0 : 1;  // nobody writes it again
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
