@@ -100,7 +100,7 @@ class MeshAttnError(RuntimeError):
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libmesh_attn.so (built by __graft_entry__.build()) and declare its signatures."""
-    global _lib, _ext
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -110,16 +110,25 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError("_binding.so is missing, or of another PyTorch: build it (python -c 'import __graft_entry__ as g; "
-                           "g.build()')") from e
-    _binding.bind(*(ctypes.cast(getattr(lib, name), c_vp).value for name in (
-        "mesh_attn_rope", "mesh_attn_diff_fwd", "mesh_attn_diff_bwd", "mesh_attn_diff_decode")))
-    _ext = _binding
     _lib = lib
     return lib
+
+
+def load_binding():
+    """Load _binding.so, which takes the tensors of rotary positions, differential attention and its decoding.
+    Those calls load it when they are first made; nothing else needs it."""
+    global _ext
+    if _ext is None:
+        lib = load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing, or of another PyTorch: build it (python -c 'import __graft_entry__ as "
+                               "g; g.build()')") from e
+        _binding.bind(*(ctypes.cast(getattr(lib, name), c_vp).value for name in (
+            "mesh_attn_rope", "mesh_attn_diff_fwd", "mesh_attn_diff_bwd", "mesh_attn_diff_decode")))
+        _ext = _binding
+    return _ext
 
 
 def _check(code: int, where: str):
@@ -587,9 +596,7 @@ def mesh_attn_rope(rope: MeshRope, q: torch.Tensor, k: Optional[torch.Tensor], p
 
 
 def _rope(rope, q, k, positions, q_out, k_out, inverse, stream=None):
-    if _ext is None:
-        load_library()
-    out = _ext.rope(rope._native, q, k, positions, q_out, k_out, 1 if inverse else 0, _handle_of(stream))
+    out = (_ext or load_binding()).rope(rope._native, q, k, positions, q_out, k_out, 1 if inverse else 0, _handle_of(stream))
     if out.__class__ is int:
         _check(out, "mesh_attn_rope")
     return out
@@ -660,21 +667,22 @@ def new_diff_workspace(plan: Plan, q: torch.Tensor, k: torch.Tensor, backward: b
     return torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
 
 
-def _on_plan(entry, where: str, plan: Plan, device, *args):
+def _on_plan(name: str, plan: Plan, device, *args):
     """One of _binding's calls that read a plan's tables, which are made for the device where they are not there yet."""
+    entry = getattr(_ext or load_binding(), name)
     out = entry(plan._native, *args)
     if out is None:
         plan.tables(device)
         out = entry(plan._native, *args)
     if out.__class__ is int:
-        _check(out, where)
+        _check(out, "mesh_attn_" + name)
     return out
 
 
 def mesh_attn_diff_fwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
                        scale: Optional[float], O: torch.Tensor, O2: Optional[torch.Tensor], LSE: torch.Tensor,
                        workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
-    _on_plan(_ext.diff_fwd, "mesh_attn_diff_fwd", plan, q.device, q, k, v, lam, scale, O, O2, LSE, 0, workspace, status,
+    _on_plan("diff_fwd", plan, q.device, q, k, v, lam, scale, O, O2, LSE, 0, workspace, status,
              _handle_of(stream))
 
 
@@ -682,7 +690,7 @@ def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Te
                        O2: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, scale: Optional[float], dQ: torch.Tensor,
                        dK: torch.Tensor, dV: torch.Tensor, dlam: torch.Tensor, workspace: torch.Tensor,
                        status: torch.Tensor, stream=None) -> None:
-    _on_plan(_ext.diff_bwd, "mesh_attn_diff_bwd", plan, q.device, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace,
+    _on_plan("diff_bwd", plan, q.device, q, k, v, lam, O, O2, LSE, dO, scale, dQ, dK, dV, dlam, workspace,
              status, _handle_of(stream))
 
 
@@ -705,12 +713,11 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     (new_diff_workspace) and status (new_status) and passes check_status=False, which leaves out the wait.
     """
     if plan is None or workspace is None or status is None:
-        load_library()
-        _ext.diff_check(q, k, v, lam)
+        load_binding().diff_check(q, k, v, lam)
         plan = plan or mesh_attn_plan_create(q.shape[2], P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
-    O, O2, LSE = _on_plan(_ext.diff_fwd, "mesh_attn_diff_fwd", plan, q.device, q, k, v, lam, scale, None, None, None,
+    O, O2, LSE = _on_plan("diff_fwd", plan, q.device, q, k, v, lam, scale, None, None, None,
                           1 if return_saved else 0, ws, st, None)
     if check_status:
         _raise_status(st)
@@ -724,12 +731,11 @@ def mesh_diff_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                                  status: Optional[torch.Tensor] = None, check_status: bool = True):
     """(dQ, dK, dV, dlam) from the forward's O, O2 and LSE and the gradient dO, on the current stream."""
     if plan is None or workspace is None or status is None:
-        load_library()
-        _ext.diff_check(q, k, v, lam)
+        load_binding().diff_check(q, k, v, lam)
         plan = plan or mesh_attn_plan_create(q.shape[2], P, causal, kvr, greedy)
     ws = new_diff_workspace(plan, q, k, backward=True) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
-    grads = _on_plan(_ext.diff_bwd, "mesh_attn_diff_bwd", plan, q.device, q, k, v, lam, O, O2, LSE, dO, scale, None, None, None,
+    grads = _on_plan("diff_bwd", plan, q.device, q, k, v, lam, O, O2, LSE, dO, scale, None, None, None,
                      None, ws, st, None)
     if check_status:
         _raise_status(st)
@@ -781,9 +787,7 @@ def mesh_attn_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
 
 
 def _diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, stream=None):
-    if _ext is None:
-        load_library()
-    out = _ext.diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, _handle_of(stream))
+    out = (_ext or load_binding()).diff_decode(q, k_cache, v_cache, lens, lam, scale, O, LSE, workspace, status, _handle_of(stream))
     if out.__class__ is int:
         _check(out, "mesh_attn_diff_decode")
     return out
@@ -797,8 +801,7 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     multiples).  Returns O [B, Hq, 1, d] and LSE [B, Hq, 2, 1].  A serving loop keeps workspace
     (new_diff_decode_workspace) and status and passes check_status=False."""
     if workspace is None or status is None:
-        load_library()
-        _ext.diff_check(q, k_cache, v_cache, lam)
+        load_binding().diff_check(q, k_cache, v_cache, lam)
     ws = workspace
     if ws is None:
         ws = new_diff_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[3], k_cache.shape[2], q.device)

@@ -71,7 +71,6 @@ def build(verbose: bool = False, extra=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, list(extra)), SOURCES))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -80,6 +79,7 @@ def build(verbose: bool = False, extra=()) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
+    binding.result()  # after the library, which does not need it
     return LIB
 
 
