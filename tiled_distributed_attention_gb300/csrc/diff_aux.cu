@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
 #pragma unroll
   for (int t = 0; t < MAXP; ++t) {
     const bool there = in && t < k;
-    w[t] = there ? __ldg(part_lse + base + t * a.S) : -INFINITY;
+    w[t] = there ? part_lse[base + t * a.S] : -INFINITY;
     v[t] = there ? __ldcs(reinterpret_cast<const float4*>(part_o + (base + t * a.S) * D + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   float M = -INFINITY, W = 0.f;
@@ -162,9 +162,9 @@ __global__ void __launch_bounds__(THREADS) prep_kernel(const DiffArgs a, float* 
     g[i] = o[i] = o2[i] = make_uint4(0u, 0u, 0u, 0u);
     if (s < a.S) {
       const int64_t at = (bh * a.S + s) * LANES + piece;
-      g[i] = __ldg(static_cast<const uint4*>(a.dO) + at);
-      o[i] = __ldg(static_cast<const uint4*>(a.O) + at);
-      o2[i] = __ldg(static_cast<const uint4*>(a.O2) + at);
+      g[i] = static_cast<const uint4*>(a.dO)[at];
+      o[i] = static_cast<const uint4*>(a.O)[at];
+      o2[i] = static_cast<const uint4*>(a.O2)[at];
     }
   }
   double acc = 0.0;

@@ -376,7 +376,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         raw_in = ql < S;
         if (raw_in) {
           const int64_t at = (((int64_t)y.b * prm.Hq + c.h) * 2 + (vec & 1)) * S + ql;
-          raw = __ldg((vec < 2 ? prm.lse : prm.dsum) + at);
+          raw = (vec < 2 ? prm.lse : prm.dsum)[at];
         }
         if (c.h != lam_h) {
           lam_h = c.h;
@@ -563,8 +563,8 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           const int64_t at = (((int64_t)y.b * prm.Hq + y.h) * 2) * S + ql;
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            raw_l[m] = __ldg(prm.lse + at + m * S);
-            raw_d[m] = __ldg(prm.dsum + at + m * S);
+            raw_l[m] = prm.lse[at + m * S];
+            raw_d[m] = prm.dsum[at + m * S];
           }
         }
       };

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) pieces_kernel(const PiecesArgs a) {
   const int w = blockIdx.y;
   const int64_t n = a.n4[w];
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const float4 v = __ldg(a.x[w] + i);
+    const float4 v = a.x[w][i];
     uint2 p[3];
     split3(v.x, v.y, p[0].x, p[1].x, p[2].x);
     split3(v.z, v.w, p[0].y, p[1].y, p[2].y);
@@ -163,7 +163,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
     // value w (LSE_1, LSE_2, D_1, D_2) of query row s as it enters the FMAs; a row past the end, or without a
     // visible key, gets exp2(x - inf) = 0
     auto fetch = [&](int w, int64_t s) {
-      return s < S ? __ldg((w < 2 ? prm.lse : prm.dsum) + vrow + (w & 1) * S + s) : w < 2 ? -INFINITY : 0.f;
+      return s < S ? (w < 2 ? prm.lse : prm.dsum)[vrow + (w & 1) * S + s] : w < 2 ? -INFINITY : 0.f;
     };
     auto value = [&](int w, float x) { return w >= 2 ? -x : x == -INFINITY ? -INFINITY : -x * LOG2E; };
     bool ok = run;
@@ -179,7 +179,7 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
           uint32_t p1[16], p2[16], p3[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float4 x = row < S ? __ldg(reinterpret_cast<const float4*>(src + hf * (D / 2) + c) + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 x = row < S ? reinterpret_cast<const float4*>(src + hf * (D / 2) + c)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
             split3(x.x, x.y, p1[2 * e], p2[2 * e], p3[2 * e]);
             split3(x.z, x.w, p1[2 * e + 1], p2[2 * e + 1], p3[2 * e + 1]);
           }

@@ -73,7 +73,7 @@ __host__ __device__ constexpr int part_floats(int D) { return ROWS * D + 2 * ROW
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-__device__ __forceinline__ int length_of(const Params& p, int b) { return min(max(__ldg(p.lens + b), 0), p.T); }
+__device__ __forceinline__ int length_of(const Params& p, int b) { return min(max(p.lens[b], 0), p.T); }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   const int n = in ? 16 : 0;  // 0: the 16 bytes are zero-filled and src is not read
@@ -152,8 +152,8 @@ struct EngineBf16 {
     for (int s = 0; s < D / 16; ++s) {
       qf[s][0] = qf[s][1] = 0u;
       if (head < nh) {
-        qf[s][0] = __ldg(reinterpret_cast<const uint32_t*>(q + head * D + s * 16 + c2));
-        qf[s][1] = __ldg(reinterpret_cast<const uint32_t*>(q + head * D + s * 16 + c2 + 8));
+        qf[s][0] = *reinterpret_cast<const uint32_t*>(q + head * D + s * 16 + c2);
+        qf[s][1] = *reinterpret_cast<const uint32_t*>(q + head * D + s * 16 + c2 + 8);
       }
     }
 #pragma unroll
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
       const int b = b0 + tid;
       int n = 0;
       if (b < p.B) {
-        const int raw = __ldg(p.lens + b);
+        const int raw = p.lens[b];
         if ((raw < 0 || raw > p.T) && blockIdx.x == 0) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, 6, b);
         n = (length_of(p, b) + TILE - 1) / TILE;
         if (n > 0) n += SEG_COST;

@@ -100,6 +100,8 @@ __device__ __forceinline__ bool mbar_drain(uint32_t bar, uint32_t parity, int64_
 // Launched with launch_behind, a kernel may start while the one before it in the stream still runs: this waits until
 // that one has ended and its writes are visible (at once in a kernel launched the usual way), and then lets the next
 // one start its own set-up.  Before anything that the kernel before may have written is read, or anything written.
+// What that kernel wrote was written during this one's life, so it is read by plain loads: the read-only path (__ldg) is
+// for what nobody writes while a kernel lives.
 __device__ __forceinline__ void wait_for_kernel_before() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

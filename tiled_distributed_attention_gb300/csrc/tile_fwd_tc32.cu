@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint4* src = reinterpret_cast<const uint4*>(prm.q_pieces + ((int64_t)hf * prm.q_rows + grow) * QW);
 #pragma unroll
         for (int i = 0; i < QW / 4; ++i) {
-          const uint4 v = __ldg(src + i);
+          const uint4 v = src[i];
           w[4 * i] = v.x;
           w[4 * i + 1] = v.y;
           w[4 * i + 2] = v.z;
