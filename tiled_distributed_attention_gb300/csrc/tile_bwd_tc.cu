@@ -721,10 +721,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) break;
       if (un >= 0) {
         if (y.ok) {
-          const int64_t kn = ((int64_t)y.b * prm.Hkv + y.hk) * prm.S + (int64_t)y.it.p * L + (int64_t)y.kb * BM;
+          const int32_t kn = (int32_t)(((int64_t)y.b * prm.Hkv + y.hk) * prm.P + y.it.p);
           for (int c = 0; c < D / 64; ++c) {
-            tma_prefetch_l2_2d(&tmK, c * 64, (int32_t)kn);
-            tma_prefetch_l2_2d(&tmV, c * 64, (int32_t)kn);
+            tma_prefetch_l2_3d(&tmK, c * 64, y.kb * BM, kn);
+            tma_prefetch_l2_3d(&tmV, c * 64, y.kb * BM, kn);
           }
         }
       }
@@ -732,11 +732,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ok = mbar_wait(bar(Ly::B_RESE), (uint32_t)((nres & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
                      ROLE_LOAD, u);
       if (!ok) break;
-      const int64_t kvrow = ((int64_t)x.b * prm.Hkv + x.hk) * prm.S + (int64_t)x.it.p * L + (int64_t)x.kb * BM;
+      const int32_t kvpart = (int32_t)(((int64_t)x.b * prm.Hkv + x.hk) * prm.P + x.it.p);
       mbar_expect_tx(bar(Ly::B_RES), 2 * Ly::TILE);
       for (int c = 0; c < D / 64; ++c) {
-        tma_load_2d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmK, c * 64, (int32_t)kvrow, bar(Ly::B_RES));
-        tma_load_2d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmV, c * 64, (int32_t)kvrow, bar(Ly::B_RES));
+        tma_load_3d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmK, c * 64, x.kb * BM, kvpart, bar(Ly::B_RES));
+        tma_load_3d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmV, c * 64, x.kb * BM, kvpart, bar(Ly::B_RES));
       }
       ++nres;
       QCursor cur;
@@ -749,8 +749,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = false;
           break;
         }
-        const int32_t qrow =
-            (int32_t)(((int64_t)x.b * prm.Hq + cur.h) * prm.S + (int64_t)cur.p * L + (int64_t)cur.qb * BM);
+        const int32_t qpart = (int32_t)(((int64_t)x.b * prm.Hq + cur.h) * prm.P + cur.p);
         const int sa = (int)(ga % Ly::NSA), sbb = (int)(gb % Ly::NSB);
         if (ga >= Ly::NSA) {
           ok = mbar_wait(bar(Ly::B_AE + sa), (uint32_t)((ga / Ly::NSA - 1) & 1), prm.wait_limit_ns, abort_flag,
@@ -759,7 +758,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         mbar_expect_tx(bar(Ly::B_AF + sa), Ly::TILE);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sb + Ly::A0 + (uint32_t)sa * Ly::TILE + (uint32_t)c * Ly::BOX, &tmQ, c * 64, qrow,
+          tma_load_3d(sb + Ly::A0 + (uint32_t)sa * Ly::TILE + (uint32_t)c * Ly::BOX, &tmQ, c * 64, cur.qb * BM, qpart,
                       bar(Ly::B_AF + sa));
         ++ga;
         if (gb >= Ly::NSB) {
@@ -769,7 +768,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         mbar_expect_tx(bar(Ly::B_BF + sbb), Ly::TILE);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sb + Ly::B0 + (uint32_t)sbb * Ly::TILE + (uint32_t)c * Ly::BOX, &tmG, c * 64, qrow,
+          tma_load_3d(sb + Ly::B0 + (uint32_t)sbb * Ly::TILE + (uint32_t)c * Ly::BOX, &tmG, c * 64, cur.qb * BM, qpart,
                       bar(Ly::B_BF + sbb));
         ++gb;
       }
@@ -1185,17 +1184,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) break;
       if (un >= 0) {
         if (y.ok) {
-          const int64_t qn = ((int64_t)y.b * prm.Hq + y.h) * prm.S + (int64_t)y.it.p * L + (int64_t)y.qb * BM;
+          const int32_t qn = (int32_t)(((int64_t)y.b * prm.Hq + y.h) * prm.P + y.it.p);
           for (int c = 0; c < D / 64; ++c) {
-            tma_prefetch_l2_2d(&tmQ, c * 64, (int32_t)qn);
-            tma_prefetch_l2_2d(&tmG, c * 64, (int32_t)qn);
+            tma_prefetch_l2_3d(&tmQ, c * 64, y.qb * BM, qn);
+            tma_prefetch_l2_3d(&tmG, c * 64, y.qb * BM, qn);
           }
           const int kn = __ldg(prm.kv_list + y.it.kv_off);
           if (kn >= 0 && kn < prm.P) {
-            const int64_t krn = ((int64_t)y.b * prm.Hkv + y.hk) * prm.S + (int64_t)kn * L;
+            const int32_t krn = (int32_t)(((int64_t)y.b * prm.Hkv + y.hk) * prm.P + kn);
             for (int c = 0; c < D / 64; ++c) {
-              tma_prefetch_l2_2d(&tmK, c * 64, (int32_t)krn);
-              tma_prefetch_l2_2d(&tmV, c * 64, (int32_t)krn);
+              tma_prefetch_l2_3d(&tmK, c * 64, 0, krn);
+              tma_prefetch_l2_3d(&tmV, c * 64, 0, krn);
             }
           }
         }
@@ -1204,14 +1203,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       ok = mbar_wait(bar(Ly::B_RESE), (uint32_t)((nres & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
                      ROLE_LOAD, u);
       if (!ok) break;
-      const int64_t qrow = ((int64_t)x.b * prm.Hq + x.h) * prm.S + (int64_t)x.it.p * L + (int64_t)x.qb * BM;
+      const int32_t qpart = (int32_t)(((int64_t)x.b * prm.Hq + x.h) * prm.P + x.it.p);
       mbar_expect_tx(bar(Ly::B_RES), 2 * Ly::TILE);
       for (int c = 0; c < D / 64; ++c) {
-        tma_load_2d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmQ, c * 64, (int32_t)qrow, bar(Ly::B_RES));
-        tma_load_2d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmG, c * 64, (int32_t)qrow, bar(Ly::B_RES));
+        tma_load_3d(sb + Ly::RES0 + (uint32_t)c * Ly::BOX, &tmQ, c * 64, x.qb * BM, qpart, bar(Ly::B_RES));
+        tma_load_3d(sb + Ly::RES1 + (uint32_t)c * Ly::BOX, &tmG, c * 64, x.qb * BM, qpart, bar(Ly::B_RES));
       }
       ++nres;
-      const int64_t kvbase = ((int64_t)x.b * prm.Hkv + x.hk) * prm.S;
+      const int64_t kvbase = ((int64_t)x.b * prm.Hkv + x.hk) * prm.P;  // the KV head's first partition
       KCursor cur;
       cur.start(prm, x.it, x.it.p, x.qb);
       for (int j = 0; j < x.NB && ok; ++j) {
@@ -1222,7 +1221,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = false;
           break;
         }
-        const int32_t krow = (int32_t)(kvbase + (int64_t)cur.kp * L + (int64_t)cur.kb * BM);
+        const int32_t kpart = (int32_t)(kvbase + cur.kp);
         const int sa = (int)(ga % Ly::NSA), sbb = (int)(gb % Ly::NSB);
         if (ga >= Ly::NSA) {
           ok = mbar_wait(bar(Ly::B_AE + sa), (uint32_t)((ga / Ly::NSA - 1) & 1), prm.wait_limit_ns, abort_flag,
@@ -1231,7 +1230,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         mbar_expect_tx(bar(Ly::B_AF + sa), Ly::TILE);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sb + Ly::A0 + (uint32_t)sa * Ly::TILE + (uint32_t)c * Ly::BOX, &tmK, c * 64, krow,
+          tma_load_3d(sb + Ly::A0 + (uint32_t)sa * Ly::TILE + (uint32_t)c * Ly::BOX, &tmK, c * 64, cur.kb * BM, kpart,
                       bar(Ly::B_AF + sa));
         ++ga;
         if (gb >= Ly::NSB) {
@@ -1241,7 +1240,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         mbar_expect_tx(bar(Ly::B_BF + sbb), Ly::TILE);
         for (int c = 0; c < D / 64; ++c)
-          tma_load_2d(sb + Ly::B0 + (uint32_t)sbb * Ly::TILE + (uint32_t)c * Ly::BOX, &tmV, c * 64, krow,
+          tma_load_3d(sb + Ly::B0 + (uint32_t)sbb * Ly::TILE + (uint32_t)c * Ly::BOX, &tmV, c * 64, cur.kb * BM, kpart,
                       bar(Ly::B_BF + sbb));
         ++gb;
       }
@@ -1376,13 +1375,16 @@ static EncodeTiledFn get_encode(std::string* err) {
   return fn;
 }
 
-// [rows, d] bf16 row-major tensor, boxes of 128 rows x 64 columns with 128-byte swizzle.
-static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64_t rows, int d, std::string* err) {
-  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)BM};
-  cuuint32_t es[2] = {1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+// [partitions][L rows][d] bf16, boxes of 128 rows x 64 columns with 128-byte swizzle: a box that reaches past a
+// partition's end gets zeros there and not the next partition's, head's or batch's rows, whose infinities and NaN a
+// weight of 0 would turn into NaN.
+static bool make_part_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64_t L, uint64_t parts, int d,
+                          std::string* err) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)L * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)BM, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -1405,10 +1407,10 @@ static int launch(const BwdArgs& a, void* stream, std::string* err) {
   EncodeTiledFn enc = get_encode(err);
   if (!enc) return (int)cudaErrorNotSupported;
   CUtensorMap mq, mk, mv, mg;
-  if (!make_map(enc, &mq, a.Q, (uint64_t)a.B * a.Hq * a.S, D, err) ||
-      !make_map(enc, &mk, a.K, (uint64_t)a.B * a.Hkv * a.S, D, err) ||
-      !make_map(enc, &mv, a.V, (uint64_t)a.B * a.Hkv * a.S, D, err) ||
-      !make_map(enc, &mg, a.dO, (uint64_t)a.B * a.Hq * a.S, D, err))
+  if (!make_part_map(enc, &mq, a.Q, (uint64_t)a.L, (uint64_t)a.B * a.Hq * a.P, D, err) ||
+      !make_part_map(enc, &mk, a.K, (uint64_t)a.L, (uint64_t)a.B * a.Hkv * a.P, D, err) ||
+      !make_part_map(enc, &mv, a.V, (uint64_t)a.L, (uint64_t)a.B * a.Hkv * a.P, D, err) ||
+      !make_part_map(enc, &mg, a.dO, (uint64_t)a.L, (uint64_t)a.B * a.Hq * a.P, D, err))
     return (int)cudaErrorInvalidValue;
   Params prm;
   prm.items = a.items;

@@ -498,10 +498,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               for (int c = 0; c < D / 64; ++c) tma_prefetch_l2_2d(&tmQ, c * 64, (int32_t)(qn + (int64_t)t * BM));
             const int kn = __ldg(prm.kv_list + xn.it.kv_off);
             if (kn >= 0 && kn < prm.P) {
-              const int64_t krn = ((int64_t)xn.b * prm.Hkv + xn.h / (prm.Hq / prm.Hkv)) * prm.S + (int64_t)kn * L;
+              const int32_t krn = (int32_t)(((int64_t)xn.b * prm.Hkv + xn.h / (prm.Hq / prm.Hkv)) * prm.P + kn);
               for (int c = 0; c < D / 64; ++c) {
-                tma_prefetch_l2_2d(&tmK, c * 64, (int32_t)krn);
-                tma_prefetch_l2_2d(&tmV, c * 64, (int32_t)krn);
+                tma_prefetch_l2_3d(&tmK, c * 64, 0, krn);
+                tma_prefetch_l2_3d(&tmV, c * 64, 0, krn);
               }
             }
           }
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         (int32_t)(qrow0 + (int64_t)t * BM), bar(Ly::B_QFULL));
         ++nq;
         const int hk = x.h / (prm.Hq / prm.Hkv);
-        const int64_t kvbase = ((int64_t)x.b * prm.Hkv + hk) * prm.S;
+        const int64_t kvbase = ((int64_t)x.b * prm.Hkv + hk) * prm.P;  // the KV head's first partition
         const int32_t* kvl = prm.kv_list + x.it.kv_off;
         for (int ki = 0; ki < x.it.n_kv && ok; ++ki) {
           const int k = __ldg(kvl + ki);
@@ -529,22 +529,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           const int nbk = blocks_of(k, x.it.p, prm.causal, x.nb, x.a_max);
+          const int32_t kpart = (int32_t)(kvbase + k);
           for (int jb = 0; jb < nbk; ++jb) {
             const int st = nk % NST;
             const uint32_t ph = (uint32_t)((nk / NST) & 1);
-            const int32_t krow = (int32_t)(kvbase + (int64_t)k * L + (int64_t)jb * BN);
             ok = mbar_wait(bar(Ly::B_KEMPTY + st), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, u);
             if (!ok) break;
             mbar_expect_tx(bar(Ly::B_KFULL + st), Ly::TILE);
             for (int c = 0; c < D / 64; ++c)
-              tma_load_2d(sb + Ly::K_OFF + (uint32_t)st * Ly::TILE + (uint32_t)c * Ly::BOX, &tmK, c * 64, krow,
+              tma_load_3d(sb + Ly::K_OFF + (uint32_t)st * Ly::TILE + (uint32_t)c * Ly::BOX, &tmK, c * 64, jb * BN, kpart,
                           bar(Ly::B_KFULL + st));
             ++nk;
             ok = mbar_wait(bar(Ly::B_VEMPTY + st), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, u);
             if (!ok) break;
             mbar_expect_tx(bar(Ly::B_VFULL + st), Ly::TILE);
             for (int c = 0; c < D / 64; ++c)
-              tma_load_2d(sb + Ly::V_OFF + (uint32_t)st * Ly::TILE + (uint32_t)c * Ly::BOX, &tmV, c * 64, krow,
+              tma_load_3d(sb + Ly::V_OFF + (uint32_t)st * Ly::TILE + (uint32_t)c * Ly::BOX, &tmV, c * 64, jb * BN, kpart,
                           bar(Ly::B_VFULL + st));
             ++nv;
           }
@@ -603,6 +603,25 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
   return true;
 }
 
+// [partitions][L rows][d] bf16, boxes of 128 rows x 64 columns with 128-byte swizzle: a box that reaches past a
+// partition's end gets zeros there and not the next partition's, head's or batch's rows, whose infinities and NaN a
+// weight of 0 would turn into NaN.
+static bool make_part_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64_t L, uint64_t parts, int d,
+                          std::string* err) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)L * d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)BM, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return false;
+  }
+  return true;
+}
+
 template <int D>
 static int launch(const TileArgs& a, void* stream, std::string* err) {
   const int64_t n_tiles = (a.L + BM - 1) / BM;
@@ -617,8 +636,8 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   if (!enc) return (int)cudaErrorNotSupported;
   CUtensorMap mq, mk, mv;
   if (!make_map(enc, &mq, a.Q, (uint64_t)a.B * a.Hq * a.S, D, err) ||
-      !make_map(enc, &mk, a.K, (uint64_t)a.B * a.Hkv * a.S, D, err) ||
-      !make_map(enc, &mv, a.V, (uint64_t)a.B * a.Hkv * a.S, D, err))
+      !make_part_map(enc, &mk, a.K, (uint64_t)a.L, (uint64_t)a.B * a.Hkv * a.P, D, err) ||
+      !make_part_map(enc, &mv, a.V, (uint64_t)a.L, (uint64_t)a.B * a.Hkv * a.P, D, err))
     return (int)cudaErrorInvalidValue;
   Params prm;
   prm.items = a.items;
