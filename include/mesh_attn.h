@@ -356,7 +356,7 @@ int mesh_attn_diff_workspace_size(const mesh_attn_plan* plan, mesh_attn_dtype dt
 /* Forward: O [B, Hq, S, d] and LSE [B, Hq, 2, S] (fp32); O2 [B, Hq, S, d], the second map's
  * output, is what the backward call needs beside them and may be NULL.
  *   dtype  MESH_ATTN_BF16 or MESH_ATTN_F32, of Q, K, V, lam, O and O2; arithmetic as in
- *          mesh_attn_tile_fwd.  d 64 or 128, 2 B Hq S < 2^31 (fp32: 6 B Hq S < 2^31, B < 8192).
+ *          mesh_attn_tile_fwd.  d 64 or 128, 2 B Hq S < 2^31 (fp32: 6 B Hq S < 2^31).
  *          Everything 16-byte aligned. */
 int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn_dtype dtype, int32_t B,
                        int32_t Hq, int32_t Hkv, int32_t d, const void* Q, const void* K, const void* V,

@@ -100,8 +100,8 @@ int check_sizes(const mesh_attn_plan* plan, mesh_attn_dtype dt, int32_t B, int32
   if (d != 64 && d != 128) return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "d must be 64 or 128");
   if ((int64_t)B * Hq > 0x3fffffff || 2 * (int64_t)B * Hq * plan->p.S >= (int64_t)1 << 31)
     return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "2 * B * Hq * S must be < 2^31");
-  if (dt == MESH_ATTN_F32 && (6 * (int64_t)B * Hq * plan->p.S >= (int64_t)1 << 31 || B > 8191 || Hq > 65535))
-    return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "fp32: 6 * B * Hq * S must be < 2^31, B < 8192 and Hq < 65536");
+  if (dt == MESH_ATTN_F32 && 6 * (int64_t)B * Hq * plan->p.S >= (int64_t)1 << 31)
+    return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "fp32: 6 * B * Hq * S must be < 2^31");
   return MESH_ATTN_OK;
 }
 
