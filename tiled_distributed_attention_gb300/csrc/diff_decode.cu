@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <string>
 
 #include "abi_util.h"
@@ -49,6 +50,11 @@ constexpr int STAGES = 3;
 // (4 us; a tile is 64 KB at d = 128, 1.45 us at the memory's rate).
 constexpr int SEG_COST = 3;
 constexpr int MAX_B = 4096;  // their tile counts are kept in shared memory beside the ring
+constexpr int64_t MAX_T = 1 << 30;
+// Units of a batch: a warp's sum of its sequences' units fits 32 bits, that of all of a CTA's threads does not.
+using Units = int64_t;
+static_assert(32 * (MAX_T / TILE + SEG_COST) <= std::numeric_limits<int32_t>::max());
+static_assert(THREADS * (MAX_T / TILE + SEG_COST) <= std::numeric_limits<Units>::max());
 constexpr float LN2 = 0.69314718055994531f;
 
 struct Params {
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
 
   // units before each sequence
   {
-    int64_t carry = 0;
+    Units carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += THREADS) {
       const int b = b0 + tid;
       int n = 0;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(THREADS) decode_kernel(const Params p) {
       }
       if (lane == 31) scan[warp] = x;
       __syncthreads();
-      int before = 0, all = 0;
+      Units before = 0, all = 0;
       for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += scan[w];
         all += scan[w];
@@ -747,7 +753,7 @@ static int decode_checks(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t 
   if (Hkv < 1 || Hq % Hkv != 0) return set_last_error(MESH_ATTN_ERR_INVALID_ARG, "need Hkv >= 1 and Hq % Hkv == 0");
   if (d != 64 && d != 128) return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "d must be 64 or 128");
   if (B > mesh::ddec::MAX_B) return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "B must be at most 4096");
-  if (T > 0x40000000LL) return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "T must be at most 2^30");
+  if (T > mesh::ddec::MAX_T) return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "T must be at most 2^30");
   return MESH_ATTN_OK;
 }
 
