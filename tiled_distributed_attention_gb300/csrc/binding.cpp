@@ -87,6 +87,14 @@ void like(const at::Tensor& q, std::initializer_list<const at::Tensor*> ts) {
   contiguous(ts);
 }
 
+// What the kernels write besides the outputs: nbytes() of an expanded tensor counts memory that is not there, and
+// a status block is MESH_ATTN_STATUS_WORDS long whatever the tensor's size.
+void check_scratch(const at::Tensor& ws, const at::Tensor& status) {
+  TORCH_CHECK_VALUE(ws.is_contiguous(), "workspace must be contiguous");
+  TORCH_CHECK_VALUE(status.scalar_type() == at::kInt && status.is_contiguous() && status.numel() >= MESH_ATTN_STATUS_WORDS,
+                    "status must be ", MESH_ATTN_STATUS_WORDS, " or more contiguous int32 (new_status)");
+}
+
 void* data(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // The stream of a call: the one given (its handle), or the device's current one.
@@ -291,6 +299,7 @@ PyObject* diff_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   contiguous({&k, &v});
   like(q, {&O, &O2});
   if (lse.defined()) check_lse(lse, z);
+  check_scratch(ws, status);
   const c10::Device dev = one_device({&q, &k, &v, &lam, &ws, &status, &O, &O2, &lse});
   const PlanRef plan = plan_of(a[0], z, k);
   const float scale = scale_of(a[5], z);
@@ -326,6 +335,7 @@ PyObject* diff_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   like(k, {&dK, &dV});
   like(lam, {&dlam});
   check_lse(lse, z);
+  check_scratch(ws, status);
   const c10::Device dev = one_device({&q, &k, &v, &lam, &O, &O2, &lse, &dO, &ws, &status, &dQ, &dK, &dV, &dlam});
   const PlanRef plan = plan_of(a[0], z, k);
   const float scale = scale_of(a[9], z);
@@ -379,6 +389,7 @@ PyObject* diff_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(!T || (k.stride(3) == 1 && v.stride(3) == 1), "the columns of the caches must be consecutive");
   like(q, {&O});
   if (lse.defined()) check_lse(lse, z);
+  check_scratch(ws, status);
   const c10::Device dev = one_device({&q, &k, &v, &lens, &lam, &ws, &status, &O, &lse});
   const float scale = scale_of(a[5], z);
   const cudaStream_t st = stream_of(a[10], dev);
