@@ -746,30 +746,32 @@ class MeshDiffAttentionFunction(torch.autograd.Function):
     """torch.autograd binding of mesh_diff_attention: gradients reach q, k, v and lam; LSE is a non-differentiable output."""
 
     @staticmethod
-    def forward(ctx, q, k, v, lam, P, causal, kvr, greedy, scale, plan, check_status):
+    def forward(ctx, q, k, v, lam, P, causal, kvr, greedy, scale, plan, check_status, status):
         plan = plan or mesh_attn_plan_create(q.shape[2], P, causal, kvr, greedy)
-        O, O2, LSE = mesh_diff_attention(q, k, v, lam, P, causal, kvr, greedy, scale, plan=plan, check_status=check_status,
-                                         return_saved=True)
+        O, O2, LSE = mesh_diff_attention(q, k, v, lam, P, causal, kvr, greedy, scale, plan=plan, status=status,
+                                         check_status=check_status, return_saved=True)
         ctx.save_for_backward(q, k, v, lam, O, O2, LSE)
         ctx.plan = plan
         ctx.args = (P, causal, kvr, greedy, scale)
-        ctx.check_status = check_status
+        ctx.check_status, ctx.status = check_status, status
         ctx.mark_non_differentiable(LSE)
         return O, LSE
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dLSE):
-        grads = mesh_diff_attention_backward(*ctx.saved_tensors, dO.contiguous(), *ctx.args, plan=ctx.plan,
+        grads = mesh_diff_attention_backward(*ctx.saved_tensors, dO.contiguous(), *ctx.args, plan=ctx.plan, status=ctx.status,
                                              check_status=ctx.check_status)
-        return (*grads, None, None, None, None, None, None, None)
+        return (*grads, None, None, None, None, None, None, None, None)
 
 
 def mesh_diff_attention_autograd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, P: int, causal: bool,
                                  kvr: bool = True, greedy: bool = True, scale: Optional[float] = None,
-                                 plan: Optional[Plan] = None, check_status: bool = True):
-    """mesh_diff_attention with autograd: returns (O, LSE); O.backward(...) fills the gradients of q, k, v and lam."""
-    return MeshDiffAttentionFunction.apply(q, k, v, lam, P, causal, kvr, greedy, scale, plan, check_status)
+                                 plan: Optional[Plan] = None, check_status: bool = True,
+                                 status: Optional[torch.Tensor] = None):
+    """mesh_diff_attention with autograd: returns (O, LSE); O.backward(...) fills the gradients of q, k, v and lam.  With
+    check_status=False a failure in either direction is recorded in `status` (new_status), for the program to read later."""
+    return MeshDiffAttentionFunction.apply(q, k, v, lam, P, causal, kvr, greedy, scale, plan, check_status, status)
 
 
 def new_diff_decode_workspace(B: int, Hq: int, Hkv: int, d: int, T: int, device=None) -> torch.Tensor:
