@@ -248,10 +248,6 @@ int mesh_attn_diff_fwd(const mesh_attn_plan* plan, const void* tables, mesh_attn
     t.wait_limit_ns = a.wait_limit_ns;
     t.pieces = a.ws + w.pieces;
     t.pieces_ready = true;
-    // The tensor cores' fp32 sums lose about 4e-7 of a row's value with every 64-key block (they truncate), whatever
-    // its sign: 6.9e-6 at 1,024 keys, 5.5e-5 at 8,192.  So a row's sums move on after 13 blocks at most (5.5e-6) and are
-    // added in fp32 with rounding, which costs up to 19 % (one head of 8,192 tokens: 261 -> 310 us).
-    t.chunk = 13;
     if ((rc = launch_status(mesh::launch_tile_fwd_tc32(t, stream, &err), err))) return rc;
     return launch_status(mesh::launch_diff_merge(a, w, parts, stream, &err), err);
   });

@@ -17,7 +17,7 @@
 //   TMEM: R1's pieces [0, 192) (dV: A's, two buffers) | S_1, S_2, dP [192, 384), later the pieces of dS_1 and
 //   dS_2 in their place | accumulators [384, 512).
 //   warps 0-7   elementwise: two warps per TMEM lane quadrant, each taking 32 of a block's 64 columns
-//   warp 8      MMA issuer, warp 9 producer (TMA)
+//   warp 8      MMA issuer, warp 9 producer (TMA), warps 10-11 idle
 // In dQ and dK a block's steps follow one another (dP and S, the elementwise part, dS C0), TMEM being full; in dV
 // the next block's scores run while A is made.  At d = 64 a map's half is 32 columns: its product with C0
 // is computed 64 wide and half of it is used.
@@ -26,9 +26,10 @@
 // dV the query heads of a KV head, leave partial sums that sum_parts adds in order.  Rows past the end are
 // loaded as zeros.  Every mbarrier wait is bounded, as in the other kernels.
 //
-// Measured (the backward call, us): 2 x 8 heads on one of 801 tokens, d = 128: 295, 45 TFLOP/s of the formulas' five
-// products (a kernel on the CUDA cores took 824); 4 heads on 2 of 777, d = 64, causal: 55 (74).  Bound by the chain of a block's steps: at d = 128 about 11,000 cycles for dQ and dK, 7,500 of products (48 each of S,
-// dP and the accumulators', 45-62 cycles) and 2,500-4,000 of the elementwise warps; 7,300 for dV.
+// Measured (the backward call, us): 2 x 8 heads on one of 801 tokens, d = 128: 306, 43 TFLOP/s of the formulas' five
+// products (a kernel on the CUDA cores took 824); 4 heads on 2 of 777, d = 64, causal: 56 (74).  Bound by the chain of a
+// block's steps: at d = 128 about 11,000 cycles for dQ and dK, 7,500 of products (48 each of S, dP and the
+// accumulators', 45-62 cycles) and 2,500-4,000 of the elementwise warps; 7,300 for dV.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,11 +50,10 @@ constexpr int BS = 64;   // streamed rows per block
 constexpr int N_EW = 8;
 constexpr int WARP_MMA = 8;
 constexpr int WARP_LOAD = 9;
-constexpr int NUM_THREADS = 320;
-// The tensor cores' fp32 sums truncate, so a long accumulation loses digits whatever its terms' signs (dK of 3,000
-// queries: 1.4e-5 of its norm).  After GROUP blocks at most the accumulators are added to the outputs in fp32, with
-// rounding.
-constexpr int GROUP = 13;
+constexpr int NUM_THREADS = 384;
+// Registers after setmaxnreg: the elementwise warpgroups, and the one of the MMA and load warps.  They add up to the
+// launch's 384 x 168, which the launcher checks.
+constexpr int EW_REGS = 200, OTHER_REGS = 104;
 constexpr int64_t DRAIN_NS = 200000000;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3;
@@ -148,13 +148,13 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
   const int first = KV && prm.causal ? 2 * rb : 0, last = !KV && prm.causal ? min(n_all, 2 * rb + 2) : n_all;
   const int per = (last - first + prm.splits - 1) / prm.splits;
   const int c_begin = min(last, first + split * per), NB = min(last, c_begin + per) - c_begin;
-  const int n_groups = max(1, (NB + GROUP - 1) / GROUP), grp = max(1, (NB + n_groups - 1) / n_groups);
   // The same for all warps: the elementwise warps meet at named barriers, which wait without a limit.  (The abort
   // flag may be set by a warp that is ahead; the vote in the block loop carries such an abort to all of them.)
   const bool run = *reinterpret_cast<const volatile int32_t*>(smem + Ly::MISC + 8) != 0 && NB > 0;
 
   if (warp < N_EW) {
     // ================================================================ elementwise
+    regs_inc<EW_REGS>();
     const int wq = warp & 3, hf = warp >> 2;  // lane quadrant, half of a block's columns
     const int64_t row = r0 + wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
@@ -204,9 +204,27 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
     // d = 64: the second map's accumulator is 64 columns behind, its half of the columns in the second 32
     const uint32_t acc = lanes + COL_ACC + (uint32_t)(hf * (D == 64 && PASS != DV ? 96 : D / 2));
     const float nlam = -prm.lam[prm.lam_n == 1 ? 0 : h];
+    // The tensor cores' fp32 sums truncate, so a long accumulation loses digits whatever its terms' signs (4e-6 of dK's
+    // norm at 800 queries, 8e-6 at 4,096): only a block's products are summed there, and the blocks here, with rounding
+    // (5e-7 at any length; at d = 128 up to 6 % slower).  In dQ and dK that is done while the next block's scores and dP
+    // are computed; in dV, whose next scores are there already, at the end of the next block.
+    float sums[D / 2] = {};
+    auto add_block = [&](int j) -> bool {
+      if (!mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        float o[32];
+        tmem_ld32(acc + (uint32_t)c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sums[c + e] += o[e];
+      }
+      return true;
+    };
     const int vw = threadIdx.x >> 6, vc = threadIdx.x & 63;  // the value this thread fetches for a block
     float vnext = KV && ok ? fetch(vw, (int64_t)c_begin * BS + vc) : 0.f;
-    bool moved = true;  // a wait below that failed: told to the others by the next block's vote
+    bool added = true;  // false: add_block's wait failed, which the next vote tells the others
     for (int j = 0; j < NB && ok; ++j) {
       const int64_t c0 = (int64_t)(c_begin + j) * BS;
       const float4* bv = reinterpret_cast<const float4*>(vec + (j & 1) * 4 * BS);
@@ -215,7 +233,8 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (j + 1 < NB) vnext = fetch(vw, c0 + BS + vc);
       }
-      ok = moved && mbar_wait_warp(bar(Ly::B_S), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
+      if (PASS != DV && j > 0) added = add_block(j - 1);
+      ok = added && mbar_wait_warp(bar(Ly::B_S), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
       // an abort ends all warps' loops: none may wait for another below
       float s1[32], s2[32], dp[32];
       if (ok) {
@@ -284,33 +303,13 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
         tmem_st16(at + 160u, p3);
       }
       tc_wait_st();
-      if (j > 0 && j % grp == 0) {  // the last group's sums to the outputs, before this block's begin the next
-        moved = mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)((j / grp - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, j);
-        if (moved) {
-          tc_fence_after();
-          float* const dst = out_row();
-#pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) {
-            float o[32];
-            tmem_ld32(acc + (uint32_t)c, o);
-            tc_wait_ld();
-            if (row < S)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 x = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
-                if (j > grp) red_add4(dst + c + 4 * e, x);
-                else *reinterpret_cast<float4*>(dst + c + 4 * e) = x;
-              }
-          }
-        }
-      }
+      if (PASS == DV && j > 0) added = add_block(j - 1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_DS + (j & 1)));
     }
-    if (ok) ok = moved && mbar_wait_warp(bar(Ly::B_ACC), (uint32_t)(((NB - 1) / grp) & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_EW, -1);
+    if (ok) ok = added && add_block(NB - 1);
     if (ok || (NB == 0 && *abort_flag == 0)) {
-      if (ok) tc_fence_after();
       float* const dst = out_row();
       // 32 rows x 32 columns at a time through shared memory (C0's, whose last reader is done), 16-byte pieces
       // swizzled by row, so that a store writes whole 128-byte row pieces
@@ -318,36 +317,24 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       const int rows = (int)max((int64_t)0, min((int64_t)32, S - (row - lane)));  // of this warp, inside the sequence
 #pragma unroll
       for (int c = 0; c < D / 2; c += 32) {
-        float o[32];
-        if (NB > 0) {
-          tmem_ld32(acc + (uint32_t)c, o);
-          tc_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           *reinterpret_cast<float4*>(stage + lane * 32 + ((e ^ (lane & 7)) * 4)) =
-              make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+              make_float4(sums[c + 4 * e] * f, sums[c + 4 * e + 1] * f, sums[c + 4 * e + 2] * f, sums[c + 4 * e + 3] * f);
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = i * 4 + (lane >> 3), e = lane & 7;
-          float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + ((e ^ (r & 7)) * 4));
-          float4* at = reinterpret_cast<float4*>(dst + (int64_t)(r - lane) * D + c + e * 4);
-          if (r < rows) {
-            if (NB > grp) {
-              const float4 y = __ldcg(at);
-              x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            }
-            *at = x;
-          }
+          const float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + ((e ^ (r & 7)) * 4));
+          if (r < rows) *reinterpret_cast<float4*>(dst + (int64_t)(r - lane) * D + c + e * 4) = x;
         }
       }
     }
-  } else if (warp == WARP_MMA) {
+    return;
+  }
+  regs_dec<OTHER_REGS>();
+  if (warp == WARP_MMA) {
     // ================================================================ MMA issuer
     constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BS, false);                       // S, dP: N = 64, K-major B
     constexpr uint32_t idesc_a = idesc_bf16_f32(BM, PASS == DV ? D : 64, true);       // accumulators: MN-major B
@@ -396,13 +383,13 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       tc_commit_warp(bar(Ly::B_C1E + st));
       return true;
     };
-    auto sum = [&](int j, uint32_t acc, uint32_t a, uint64_t c) {  // acc += pieces at a times a block's rows, MN-major
+    auto sum = [&](uint32_t acc, uint32_t a, uint64_t c) {  // acc = the pieces at a times a block's rows, MN-major
 #pragma unroll
       for (int pr = 0; pr < N_PAIR; ++pr)
 #pragma unroll
         for (int kk = 0; kk < BS / 16; ++kk)
           tc_mma_ts_warp(acc, a + (uint32_t)(pair_a(pr) * 32 + kk * 8), c + (c_off(pair_b(pr), 0) + (uint64_t)(kk * 128)), idesc_a,
-                         (j % grp > 0 || pr > 0 || kk > 0) ? 1u : 0u);
+                         (pr > 0 || kk > 0) ? 1u : 0u);
     };
     // dP before the scores: C1's stage is free before C0's, whose next load then overlaps this product
     if (ok) ok = (PASS == DV || issue_dp(0)) && issue_s(0);
@@ -416,17 +403,18 @@ __device__ __forceinline__ void run_pass(const Maps& maps, const Params& prm, in
       if (!(ok = wait(Ly::B_DS + (j & 1), (uint32_t)((j >> 1) & 1), j))) break;
       tc_fence_after();
       if (PASS == DV) {
-        sum(j, tmem + COL_ACC, tmem + COL_A + 96u * (uint32_t)(j & 1), c1m + stage);
+        sum(tmem + COL_ACC, tmem + COL_A + 96u * (uint32_t)(j & 1), c1m + stage);
         tc_commit_warp(bar(Ly::B_C1E + st));
+        tc_commit_warp(bar(Ly::B_ACC));
       } else {
 #pragma unroll
         for (int m = 0; m < 2; ++m)  // the map's box of 64 columns; at d = 64 both maps share one
-          sum(j, tmem + COL_ACC + 64u * m, tmem + COL_S + 96u * m, c0m + stage + (D == 128 ? (uint64_t)m * (Ly::CBOX >> 4) : 0ull));
+          sum(tmem + COL_ACC + 64u * m, tmem + COL_S + 96u * m, c0m + stage + (D == 128 ? (uint64_t)m * (Ly::CBOX >> 4) : 0ull));
         tc_commit_warp(bar(Ly::B_C0E + st));
+        tc_commit_warp(bar(Ly::B_ACC));
         // into the place of dS(j)'s pieces, which those products have read
         if (j + 1 < NB) ok = issue_dp(j + 1) && issue_s(j + 1);
       }
-      if (j + 1 == NB || (j + 1) % grp == 0) tc_commit_warp(bar(Ly::B_ACC));
     }
     // exit-path drain: every MMA issued completes before TMEM is freed
     tc_commit_warp(bar(Ly::B_DRAIN));
@@ -604,12 +592,20 @@ static bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, uint64
 }
 
 template <int D>
-static cudaError_t launch(const Maps& maps, const Params& prm, unsigned grid, cudaStream_t st) {
+static cudaError_t launch(const Maps& maps, const Params& prm, unsigned grid, cudaStream_t st, std::string* err) {
   static OncePerDevice once;
   const int dev = OncePerDevice::device();
   auto kern = diff_bwd32_kernel<D>;
   if (once.pending(dev)) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+    // a warpgroup that raises its registers beyond what the launch has would wait for ever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * EW_REGS + 128 * OTHER_REGS) {
+      *err = "fp32 differential backward built with " + std::to_string(fa.numRegs) +
+             " registers a thread, fewer than its warpgroups' register split needs";
+      return cudaErrorInvalidConfiguration;
+    }
     if (e != cudaSuccess) return e;
     once.mark(dev);
   }
@@ -686,7 +682,7 @@ int launch_diff_bwd_tc32(const DiffArgs& a, const DiffWorkspace& w, int sms, voi
   p.splits = splits;
   p.scale = a.scale;
   p.scale_log2 = a.scale_log2;
-  e = a.d == 128 ? launch<128>(m, p, (unsigned)ctas, st) : launch<64>(m, p, (unsigned)ctas, st);
+  e = a.d == 128 ? launch<128>(m, p, (unsigned)ctas, st, err) : launch<64>(m, p, (unsigned)ctas, st, err);
   if (e == cudaSuccess && (q_parts || kv_parts)) {
     SumArgs s{};
     int n = 0;
@@ -706,7 +702,7 @@ int launch_diff_bwd_tc32(const DiffArgs& a, const DiffWorkspace& w, int sms, voi
     const int64_t most = (int64_t)a.B * a.Hq * s.row4;
     e = launch_behind(sum_parts, dim3((unsigned)std::min<int64_t>((most + 255) / 256, 152 * 8), (unsigned)n), 256, 0, st, s);
   }
-  if (e != cudaSuccess) *err = std::string("diff_bwd_tc32 launch: ") + cudaGetErrorString(e);
+  if (e != cudaSuccess && err->empty()) *err = std::string("diff_bwd_tc32 launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
 

@@ -77,9 +77,8 @@ struct TileArgs {
   float scale_log2;
   int64_t wait_limit_ns;
   void* pieces;  // fp32 inputs: device buffer for the bf16 pieces of Q, K and V (f32_pieces_layout)
-  bool pieces_ready;  // they are there already; Q, K and V are not read
-  int32_t parts;      // fp32 inputs: of each work item's keys (0 or 1: none), n_slots counting them
-  int32_t chunk;      // fp32 inputs: most key blocks before O moves from tensor memory to part_o (0: at the end only)
+  bool pieces_ready;  // the differential calls: they are there already; Q, K and V are not read
+  int32_t parts;      // the differential calls: of each work item's keys (0 or 1: none), n_slots counting them
 };
 // Kernel launchers return a cudaError_t value as int; *err gets a message on failure.
 int launch_tile_fwd_tc(const TileArgs& a, void* stream, std::string* err);

@@ -73,17 +73,9 @@ struct Params {
   const uint32_t* q_pieces;  // Q's bf16 pieces [3][q_rows][D], as packed pairs
   int32_t B, Hq, Hkv, P, n_items, n_slots, nqt, nb, causal;
   int32_t parts;  // of a work item's key blocks, each with a slot of its own
-  int32_t chunk;  // most blocks whose products are summed in one accumulation
   float scale_log2;
   int64_t wait_limit_ns;
 };
-
-// n blocks in the fewest chunks of at most `most`, as even as can be: the size of one.
-__device__ __forceinline__ int even_chunk(int n, int most) {
-  if (n <= most) return max(n, 1);
-  const int k = (n - 1) / most + 1;
-  return (n - 1) / k + 1;
-}
 
 // 32 lanes x 16 consecutive 32-bit columns: thread i of the warp writes lane (base + i).
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -120,9 +112,12 @@ __device__ __forceinline__ int kblocks(int k, int p, int causal, int nb, int qt)
   return (causal && k == p) ? min(nb, 2 * qt + 2) : nb;
 }
 
-// CUT: a work item's keys may be in parts, and its sums move on after a chunk of blocks; the plain calls do neither, and
-// what decides about it a block would cost them 5 to 9 % (2 x 8 heads on 2 of 2,500 tokens, d = 128: 306 -> 321 us).
-template <int D, bool CUT>
+// DIFF: the differential calls.  A work item's keys may be in parts, and O is summed over the blocks in registers, with
+// rounding; the tensor cores sum a block's products only, since their fp32 sums truncate: 24 additions a block lose about
+// 4e-7 of a row's value whatever its sign (6.9e-6 of O at 1,024 keys, 5.5e-5 at 8,192; by registers 2e-7 to 4e-7 at any
+// length, in the same time).  The plain calls do neither, and what decides about it at run time would cost them 5 to 9 %
+// (2 x 8 heads on 2 of 2,500 tokens, d = 128: 306 -> 321 us).
+template <int D, bool DIFF>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     tile_fwd_tc32_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const Params prm) {
@@ -145,7 +140,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // the group, query tile), so the CTAs resident together share one KV head's partitions in L2.
   int64_t uu = blockIdx.x;
   int part = 0, parts = 1;
-  if constexpr (CUT) {
+  if constexpr (DIFF) {
     parts = prm.parts;
     part = (int)(uu % parts);
     uu /= parts;
@@ -165,7 +160,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (unit_ok)
     for (int ki = 0; ki < it.n_kv; ++ki) NB += kblocks(__ldg(prm.kv_list + it.kv_off + ki), p, prm.causal, prm.nb, qt);
   int j0 = 0;  // this part's first block
-  if (CUT && parts > 1 && NB > 0) {
+  if (DIFF && parts > 1 && NB > 0) {
     const int k = min(parts, NB), n = NB;
     j0 = min(part, k) * n / k;
     NB = min(part + 1, k) * n / k - j0;
@@ -272,8 +267,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     const int64_t prow = (((int64_t)b * prm.Hq + h) * prm.n_slots + it.slot * parts + part) * L + q_local;
     float4* const o_row = reinterpret_cast<float4*>(prm.part_o + prow * D + hf * (D / 2));
-    const int chunk = CUT ? even_chunk(NB, prm.chunk) : 1;
-    float moved = 0.f;  // what O's earlier chunks in part_o are to be multiplied by (0: there are none)
+    float sums[DIFF ? D / 2 : 1] = {};  // O over the earlier blocks, at reference m
     for (int j = 0; j < NB && ok; ++j) {
       int kp, kbk;
       block_at(j, kp, kbk);
@@ -323,8 +317,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // PV(j-1) done: O holds every earlier product and P's buffer is free (PV(j) needs this
       // block's P, so the barrier is never a phase ahead of this wait)
       bool pv_done = (j == 0);
-      const bool move = CUT && j > 0 && j % chunk == 0;  // O is complete up to block j - 1, and begins anew
-      if (!move && __any_sync(0xffffffffu, factor != 1.f)) {
+      if (!DIFF && __any_sync(0xffffffffu, factor != 1.f)) {
         ok = mbar_wait(bar(Ly::B_PVDONE), (uint32_t)((j - 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
                        ROLE_SOFTMAX, j);
         ok = __all_sync(0xffffffffu, ok);
@@ -373,32 +366,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      if (move) {  // to part_o: the chunk's O, still at the reference before this block
-        const float old = moved * factor;
-#pragma unroll 1
-        for (int c = 0; c < D / 2; c += 32) {
+      if (DIFF && j > 0) {  // block j - 1, still at the reference before this one, joins the sums
+#pragma unroll
+        for (int c = 0; c < (DIFF ? D / 2 : 0); c += 32) {
           float o[32];
           tmem_ld32(tm_o + (uint32_t)c, o);
           tc_wait_ld();
-          if (q_local < L) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float4 x = make_float4(o[4 * e] * factor, o[4 * e + 1] * factor, o[4 * e + 2] * factor, o[4 * e + 3] * factor);
-              if (old == 1.f) {  // the usual case: the reference has not moved
-                red_add4(reinterpret_cast<float*>(o_row + c / 4 + e), x);
-                continue;
-              }
-              if (moved != 0.f) {
-                const float4 y = __ldcg(o_row + c / 4 + e);
-                x = make_float4(fmaf(y.x, old, x.x), fmaf(y.y, old, x.y), fmaf(y.z, old, x.z), fmaf(y.w, old, x.w));
-              }
-              o_row[c / 4 + e] = x;
-            }
-          }
+          for (int e = 0; e < 32; ++e) sums[c + e] = (sums[c + e] + o[e]) * factor;
         }
-        moved = 1.f;
-      } else if (CUT) {
-        moved *= factor;
       }
       // this warp's 32 keys are packed columns [16 hf, 16 hf + 16) of each piece
       const uint32_t tm_p = tmem + lane_base + COL_P + 16u * (uint32_t)hf;
@@ -426,21 +402,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (ok) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
+#pragma unroll (DIFF ? D / 64 : 1)
       for (int c = 0; c < D / 2; c += 32) {
         float o[32];
         tmem_ld32(tm_o + (uint32_t)c, o);
         tc_wait_ld();
-        if (q_local < L) {
-          if (CUT && moved != 0.f)
+        if constexpr (DIFF) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 y = __ldcg(o_row + c / 4 + e);
-              o[4 * e] = fmaf(y.x, moved, o[4 * e]);
-              o[4 * e + 1] = fmaf(y.y, moved, o[4 * e + 1]);
-              o[4 * e + 2] = fmaf(y.z, moved, o[4 * e + 2]);
-              o[4 * e + 3] = fmaf(y.w, moved, o[4 * e + 3]);
-            }
+          for (int e = 0; e < 32; ++e) o[e] += sums[c + e];
+        }
+        if (q_local < L) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             o_row[c / 4 + e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
@@ -494,7 +465,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // works on block j, and S(j+2) while it works on block j+1.
     if (ok) ok = issue_s(0);
     if (ok && NB > 1) ok = issue_s(1);
-    const int chunk = CUT ? even_chunk(NB, prm.chunk) : 1;
     for (int j = 0; j < NB && ok; ++j) {
       ok = mbar_wait_warp(bar(Ly::B_PFULL), (uint32_t)(j & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_MMA, j);
       if (ok)
@@ -510,7 +480,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
           tc_mma_ts_warp(tmem + COL_O, pa + (uint32_t)(kk * 8), vd + (uint64_t)(kk * 128), idesc_pv,
-                         ((CUT ? j % chunk > 0 : j > 0) || pr > 0 || kk > 0) ? 1u : 0u);
+                         ((!DIFF && j > 0) || pr > 0 || kk > 0) ? 1u : 0u);
       }
       tc_commit_warp(bar(Ly::B_VEMPTY + (j & 1)));  // V(j)'s stage free once these products complete
       tc_commit_warp(bar(Ly::B_PVDONE));  // O holds PV(0..j) and P is free for block j+1
@@ -744,7 +714,6 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   prm.nb = (int32_t)nb;
   prm.causal = a.causal;
   prm.parts = std::max(1, a.parts);
-  prm.chunk = a.chunk > 0 ? a.chunk : 0x7fffffff;
   prm.scale_log2 = a.scale_log2;
   prm.wait_limit_ns = a.wait_limit_ns;
   auto go = [&](auto kern) -> cudaError_t {
@@ -755,8 +724,7 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
     kern<<<dim3((unsigned)units), dim3(NUM_THREADS), Layout<D>::TOTAL, st>>>(mq, mk, mv, prm);
     return cudaGetLastError();
   };
-  const bool cut = prm.parts > 1 || a.chunk > 0;
-  const cudaError_t e = cut ? go(tile_fwd_tc32_kernel<D, true>) : go(tile_fwd_tc32_kernel<D, false>);
+  const cudaError_t e = a.pieces_ready ? go(tile_fwd_tc32_kernel<D, true>) : go(tile_fwd_tc32_kernel<D, false>);
   if (e != cudaSuccess) *err = std::string("tile_fwd_tc32 launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
