@@ -401,7 +401,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     if (ok) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // a row without a visible key: O = 0, LSE = -inf (differential calls: a NaN sum stays NaN)
+      const bool none = DIFF ? l == 0.f : !(l > 0.f);
+      const float inv = none ? 0.f : 1.f / l;
 #pragma unroll (DIFF ? D / 64 : 1)
       for (int c = 0; c < D / 2; c += 32) {
         float o[32];
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (q_local < L && hf == 0)
-        prm.part_lse[prow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        prm.part_lse[prow] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
   } else if (warp == WARP_MMA) {
     // ================================================================ MMA issuer
