@@ -779,6 +779,14 @@ static int launch(const DiffArgs& a, const DiffWorkspace& w, int sms, cudaStream
   cudaError_t e = cudaSuccess;
   if (once.pending(dev)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+    // a warpgroup that raises its registers beyond what the launch has would wait for ever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * SOFTMAX_REGS + 128 * OTHER_REGS) {
+      *err = "differential forward built with " + std::to_string(fa.numRegs) +
+             " registers a thread, fewer than its warpgroups' register split needs";
+      return (int)cudaErrorInvalidConfiguration;
+    }
     if (e == cudaSuccess) once.mark(dev);
   }
   // with a CTA for every unit the counter is not read

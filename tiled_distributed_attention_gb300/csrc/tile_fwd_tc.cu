@@ -36,6 +36,7 @@
 
 #include <string>
 
+#include "abi_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -668,6 +669,18 @@ static int launch(const TileArgs& a, void* stream, std::string* err) {
   }
   auto kern = tile_fwd_tc_kernel<D>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+  static OncePerDevice checked;
+  if (checked.pending(dev)) {
+    // a warpgroup that raises its registers beyond what the launch has would wait for ever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * SOFTMAX_REGS + 128 * OTHER_REGS) {
+      *err = "tile forward built with " + std::to_string(fa.numRegs) +
+             " registers a thread, fewer than its warpgroups' register split needs";
+      return (int)cudaErrorInvalidConfiguration;
+    }
+    if (e == cudaSuccess) checked.mark(dev);
+  }
   if (e != cudaSuccess) {
     *err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e);
     return (int)e;
