@@ -184,7 +184,10 @@ int mesh_attn_workspace_size_for(const mesh_attn_plan* plan, mesh_attn_dtype in_
  *   partial_o, partial_lse  device fp32 outputs, sizes from mesh_attn_partials_size.
  *   workspace device buffer of at least mesh_attn_workspace_size bytes.
  *   d_status  device status block (see above).
- * Any L >= 1 works: query rows and keys past the end of a partition are masked. */
+ * Any L >= 1 works: query rows and keys past the end of a partition are masked, and what lies there
+ * (another partition, head or batch) never reaches a result.  Inside a partition masked keys get
+ * weight 0, and a weight of 0 still multiplies its value, so V (and for the backward calls every tensor)
+ * must be finite in the 128-row block of a row's last visible key. */
 int mesh_attn_tile_fwd(const mesh_attn_plan* plan, mesh_attn_dtype in_dtype, int32_t B,
                        int32_t Hq, int32_t Hkv, int32_t d, const void* Q, const void* K,
                        const void* V, float scale, float* partial_o, float* partial_lse,
@@ -303,8 +306,9 @@ int mesh_attn_bwd_reduce(const mesh_attn_plan* plan, mesh_attn_dtype out_dtype, 
  *                                                             y cos phi + x sin phi),
  * by -phi with inverse = 1, which is the backward pass (the gradient of q from the gradient of
  * the rotated q).  Pairs are columns (i, i + n_pairs) of the group, or (2 i, 2 i + 1) with
- * adjacent = 1; columns from 2 n_pairs on are copied.  Angles are exact for any integer position:
- * they are products modulo a whole turn in 64-bit fixed point.
+ * adjacent = 1; columns from 2 n_pairs on are copied.  Angles are products modulo a whole turn in
+ * 64-bit fixed point: exact in the position, and off by |position| 2^-53 turns at most from the
+ * rounding of freq / 2 pi (freq up to 2 pi; in proportion above).
  *   dtype       of q, k and both outputs; 2 <= d <= 1024, d % groups == 0,
  *               1 <= n_pairs <= 256, 2 n_pairs <= d / groups.
  *   q [B, Hq, S, d] with q_strides[3] = the batch, head and token strides in elements (the d

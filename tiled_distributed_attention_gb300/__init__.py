@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the computation (tile map, greedy order, tile
 attention, LSE merge) runs in the C++ planner and the CUDA kernels behind the C ABI declared
 in include/mesh_attn.h.  The functions carry the same names as the C entry points; those of rotary
-positions and differential attention hand their tensors to _binding.so, an extension module.  PyTorch
+positions and differential attention hand their tensors to _binding.so, an extension module loaded
+by the first of them.  PyTorch
 supplies device memory and streams; nothing here computes attention, and there is no CPU
 fallback: if the library is missing, load_library() raises.
 """
@@ -173,7 +174,8 @@ class Plan:
 
     def tables(self, device=None) -> torch.Tensor:
         """The plan's constant tables on `device`, copied there on the first call (which waits for the copy,
-        so that every stream may read them; make it before capturing a graph) and shared by all later ones."""
+        so that every stream may read them; make it before capturing a graph, and keep the plan as long as the
+        graph) and shared by all later ones."""
         got = self._tables.get(device)  # by index, the usual call
         if got is not None:
             return got
@@ -709,7 +711,8 @@ def mesh_diff_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
 
     q [B, Hq, S, d], k, v [B, Hkv, S, d], lam [Hq] or [1] (one value for all heads), all bf16 or all fp32.  Returns O (q's
     shape and dtype) and LSE (fp32 [B, Hq, 2, S]); with return_saved O, O2 and LSE, which
-    mesh_diff_attention_backward takes.  A program that calls it every step keeps plan, workspace
+    mesh_diff_attention_backward takes.  P, kvr and greedy make the plan where none is given (P has to divide S); the plan's
+    length and mask count here, its partitions do not.  A program that calls it every step keeps plan, workspace
     (new_diff_workspace) and status (new_status) and passes check_status=False, which leaves out the wait.
     """
     if plan is None or workspace is None or status is None:

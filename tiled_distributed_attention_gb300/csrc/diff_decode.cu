@@ -2,8 +2,9 @@
 //   O_h = softmax(s q1 K1^T) V - lam_h softmax(s q2 K2^T) V,   q = [q1 | q2], K = [K1 | K2] by columns,
 // over the first lens[b] tokens of sequence b's cache.
 //
-// Bound by memory: every cached byte is read once (a KV head's cache serves its whole group of
-// query heads and both maps), at 12 flops a byte and query head or fewer.
+// Bound by memory: a KV head's cache serves eight query heads of its group and both maps in one read, at 12
+// flops a byte and query head or fewer.  A group of more than eight is cut into chunks of eight heads, segments
+// of their own that read the cache once each: 16 query heads on one KV head read it twice, from L2 where it fits.
 //
 // Work split.  The batch's cached tokens, in tiles of 128 over the segments (sequence, KV head, head chunk),
 // are one long list that the CTAs share out evenly: CTA i takes the units [i W / G, (i + 1) W / G), a

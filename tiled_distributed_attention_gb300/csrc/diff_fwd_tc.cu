@@ -21,10 +21,11 @@
 // d = 128 (1,536 cycles), 32,768 exponentials.  P is rounded to bf16 for its product (2^-9 relative
 // a term), everything else is fp32.
 //
-// Measured (d = 128, 16 heads, 16,384 tokens): causal 1.10 ms, 1,500 TFLOP/s; without a mask, on 4 KV heads,
-// 2.15 ms, 1,530 TFLOP/s (0.81 of the bf16 burst rate).  Bound by the softmax warps: a block takes them
-// 2,350-2,450 cycles for its 1,536 cycles of products; an exponential costs 3.84 cycles a warp and
-// sub-partition, and the products' issue takes dispatch slots from the sub-partition of the MMA warp.
+// Measured (d = 128, 16 heads, 16,384 tokens, calls in a row): causal 1.13 to 1.18 ms, 1,400 to 1,460 TFLOP/s; without a
+// mask, on 4 KV heads, 2.18 ms, 1,510 TFLOP/s (0.80 of the bf16 burst rate).  Bound by the softmax warps: a block takes them
+// 2,350-2,450 cycles for its 1,536 cycles of products, though no pipe is full (MUFU 40 % busy, FMA 22 %): both softmax
+// warps of a sub-partition run the same phase, and in the sub-partition of the MMA warp, whose products' issue takes
+// dispatch slots, the exponentials of 64 keys take 1,000 cycles where they take 640 in the others.
 // Slower (no mask): two warps a row 2.70 ms, 64-key steps with two score buffers a map 2.70 ms, P handed
 // over in halves 2.53 ms, an MMA issuer for each map 2.78 ms, products issued in paced groups of four 2.57 ms.
 //

@@ -30,7 +30,8 @@
 //     softmax works on this one.  The softmax stores P(j) once PV(j-1) has completed.  It takes
 //     the block maximum every block but raises its reference (and rescales O and l) only when the
 //     maximum grew by more than 2^8; the exact three-piece split keeps P's full fp32 value at any
-//     magnitude up to that bound.
+//     magnitude up to that bound.  The differential calls run the same kernel over pieces and heads of
+//     their own, with O summed over the blocks in registers (see the kernel).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
