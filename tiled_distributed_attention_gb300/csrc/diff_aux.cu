@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const DiffArgs a, const 
   }
 }
 
-// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2.  A CTA takes PREP_ROWS rows of a head,
+// Row terms of dS: D1 = dO . O1 with O1 = O + lam O2, and D2 = dO . O2, from the outputs as they were rounded (an O1
+// of its own would be one more output to write and keep, for an error that stays below that of the rounded dS).  A CTA takes PREP_ROWS rows of a head,
 // a group of lanes a row, 16 bytes of each of the three tensors a lane, all passes' loads in flight together.
 constexpr int PREP_ROWS = 64;
 template <typename T>

@@ -19,7 +19,9 @@
 //
 // Per 128 x 128 block and head: 2 x 4 score products and 2 x 8 PV products of 64 cycles each at
 // d = 128 (1,536 cycles), 32,768 exponentials.  P is rounded to bf16 for its product (2^-9 relative
-// a term), everything else is fp32.
+// a term), everything else is fp32.  That rounding costs 1.9e-3 of O's norm beside the 1.7e-3 of O's own (2.6e-3
+// together, as the same rounding in 64-bit arithmetic gives); a second piece of P would take it away for 1,024 cycles of
+// products more a block, 2,560 against the softmax's 2,400.
 //
 // Measured (d = 128, 16 heads, 16,384 tokens, calls in a row): causal 1.13 to 1.18 ms, 1,400 to 1,460 TFLOP/s; without a
 // mask, on 4 KV heads, 2.18 ms, 1,510 TFLOP/s (0.80 of the bf16 burst rate).  Bound by the softmax warps: a block takes them
