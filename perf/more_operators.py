@@ -398,13 +398,12 @@ def _exact_append(s):
                 z = torch.complex(y[..., u], y[..., w]) * turn
                 y[..., u], y[..., w] = z.real, z.imag
         out.append(y)
-    kp, vp = s["k_pages"].double(), s["v_pages"].double()
     at = s["table"].long()[b, place // c["page"]] * c["page"] + place % c["page"]
-    for pages, x in ((kp, out[1]), (vp, s["v"].double())):
-        flat = pages.transpose(1, 2).reshape(-1, c["Hkv"], c["d"])
-        flat[at] = x
-        pages.copy_(flat.view(pages.shape[0], c["page"], c["Hkv"], c["d"]).transpose(1, 2))
-    return out[0], kp, vp
+    for pages, x in ((s["k_pages"], out[1]), (s["v_pages"], s["v"])):
+        flat = pages.double().transpose(1, 2).reshape(-1, c["Hkv"], c["d"]).clone()  # [tokens of all pages, Hkv, d]
+        flat[at] = x.double()
+        out.append(flat.view(-1, c["page"], c["Hkv"], c["d"]).transpose(1, 2).contiguous())
+    return out[0], out[2], out[3]
 
 
 def _exact_scores(q, k, cap, slope, far, keep):
