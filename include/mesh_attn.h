@@ -395,6 +395,92 @@ int mesh_attn_diff_decode(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t 
                           float scale, void* O, float* LSE, void* workspace, size_t workspace_bytes,
                           int32_t* d_status, void* stream);
 
+/* ---------------------------------------------------------------- a paged cache
+ *
+ * Keys and values of many sequences in pages of `page` tokens each: k_pages and v_pages [n_pages, Hkv, page, d] (strides[3] =
+ * page, head and row strides in elements; the d columns are consecutive).  Sequence b's token i is row i % page of page
+ * table[b * table_stride + i / page].  A call's new tokens stand one sequence after another: sequence b's are the rows
+ * offsets[b] .. offsets[b + 1] - 1 (offsets ascend from 0), and they are the last of the lens[b] tokens it then has, so the first of
+ * n has the place lens[b] - n.  table, offsets [B + 1] and lens [B] are int32 in device memory and are read there: a captured
+ * graph replays with other lengths, tables and offsets.  Rows of the batch from offsets[B] on are left as they are.
+ * A place, page or length that does not exist, or offsets that do not ascend, are recorded as MESH_ATTN_ERR_OUT_OF_RANGE. */
+
+/* New tokens into their pages: k rotated (or copied, with n_pairs = 0), v copied, and q rotated into q_out, in one launch.
+ *   q, k, v   [N, H, d] with strides[2] = token and head strides in elements, e.g. slices of one projection; q_out [N, Hq, d]
+ *             likewise.  Hq may be 0 (q and q_out are then not used).  q_out may be q with the same strides; otherwise nothing may
+ *             overlap.  Alignment and widths of accesses as in mesh_attn_rope.  page >= 1, 2 <= d <= 1024.
+ *   groups, n_pairs, n_axes, freq, pair_axis, adjacent   as in mesh_attn_rope.
+ *   positions  as there, pos_strides[2] = axis and token strides, [axes, N]; or NULL: each token's place in its sequence
+ *              (one axis).
+ * A token whose place or page does not exist is recorded and left out. */
+int mesh_attn_paged_append(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, const void* q,
+                           const int64_t* q_strides, void* q_out, const int64_t* q_out_strides, const void* k,
+                           const int64_t* k_strides, const void* v, const int64_t* v_strides, int32_t n_pages, int32_t page,
+                           void* k_pages, const int64_t* k_page_strides, void* v_pages, const int64_t* v_page_strides,
+                           const int32_t* table, int32_t max_pages, int64_t table_stride, const int32_t* offsets,
+                           const int32_t* lens, int32_t groups, int32_t n_pairs, int32_t n_axes, const double* freq,
+                           const int32_t* pair_axis, int32_t adjacent, const void* positions, int32_t pos_bits,
+                           const int64_t* pos_strides, int32_t* d_status, void* stream);
+
+/* Bytes of device workspace mesh_attn_paged_attn needs for at most N new tokens of B sequences, max_new of one of them, and these
+ * heads.  Caller-allocated, 16-byte aligned, zeroed before its first call; calls leave it fit for the next, whatever its
+ * sizes.  Calls that overlap on the GPU, captured graphs among them, need workspaces of their own. */
+int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
+                                   int64_t max_new, size_t* bytes);
+
+/* Attention of the new tokens over their sequences' pages, their own keys among them (append first): token i sees the keys
+ * j <= i, with window > 0 those with i - j < window, by the score
+ *   x = scale q.k, or cap tanh(scale q.k / cap) with cap > 0;   x -= slopes[h] (i - j) where slopes is not NULL.
+ * O [N, Hq, d] and LSE [N, Hq] (natural log, fp32), dense.  q [N, Hq, d] with strides[2] = token and head strides.
+ *   max_new   an upper bound of a sequence's new tokens, which picks the kernel; a sequence with more is recorded, and its tokens
+ *             from max_new on are left out.
+ *   slopes    device fp32 [Hq], finite, or NULL.
+ *   dtype     MESH_ATTN_BF16 (P in bf16 for its product; two bf16 pieces with few rows) or MESH_ATTN_F32.  d 64 or 128; page a
+ *             multiple of 16; B <= 4096; max_pages * page <= 2^30.  Tensors 16-byte aligned, strides multiples of 16 bytes.
+ * Tokens of a page from the sequence's length on never reach a result, NaN or not.  A page that does not exist is
+ * recorded and read as zeros. */
+int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, const void* q,
+                         const int64_t* q_strides, int32_t n_pages, int32_t page, const void* k_pages, const int64_t* k_strides,
+                         const void* v_pages, const int64_t* v_strides, const int32_t* table, int32_t max_pages,
+                         int64_t table_stride, const int32_t* offsets, const int32_t* lens, int64_t max_new, float scale, float cap,
+                         const float* slopes, int64_t window, void* O, float* LSE, void* workspace, size_t workspace_bytes,
+                         int32_t* d_status, void* stream);
+
+/* ---------------------------------------------------------------- range-masked attention
+ *
+ * Attention of a dense batch where query i of batch entry b sees the keys lo[b, i] <= j < hi[b, i]: causal attention
+ * (0, i + 1), documents packed into one row (the document's start, i + 1), prefixes that see one another (a larger hi), windows (a
+ * larger lo), padding (lo >= hi: no key; O = 0, LSE = -inf and no gradients).  Bounds outside 0 .. S are taken as the nearer
+ * bound.  Scores are capped and biased by distance on request:
+ *   x_ij = scale q_i.k_j, or cap tanh(scale q_i.k_j / cap) with cap > 0;   x_ij -= slopes[h] |i - j| where slopes is not NULL.
+ * Backward, with P = exp(x - LSE), dP = dO V^T, D = dO . O and t = tanh(scale q.k / cap):
+ *   dS = P (dP - D) (1 - t^2) (without a cap t = 0),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO;
+ * slopes get no gradient.  Masked keys get weight 0, and a weight of 0 still multiplies its value, so V (and for the backward call
+ * every tensor) must be finite in the 128-row blocks that a row's range touches. */
+
+/* Bytes of device workspace of the calls below: the forward's, or with backward = 1 enough for both directions.
+ * Caller-allocated, 16-byte aligned, its contents do not matter; calls that overlap on the GPU, captured graphs among them, need
+ * workspaces of their own. */
+int mesh_attn_range_workspace_size(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d,
+                                   int32_t backward, size_t* bytes);
+
+/* Forward: O [B, Hq, S, d] and LSE [B, Hq, S] (fp32) of dense Q, K, V.
+ *   lo, hi    device int32 [B, S], mask_stride elements from one batch entry to the next (0: one mask for all).
+ *   slopes    device fp32 [Hq], finite, or NULL.
+ *   dtype     MESH_ATTN_BF16 (tensor cores, P rounded to bf16 for its product) or MESH_ATTN_F32 (CUDA cores).  d 64 or 128;
+ *             S <= 2^24, B * Hq * S < 2^30.  Tensors 16-byte aligned. */
+int mesh_attn_range_fwd(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d, const void* Q,
+                        const void* K, const void* V, const int32_t* lo, const int32_t* hi, int64_t mask_stride,
+                        const float* slopes, float scale, float cap, void* O, float* LSE, void* workspace,
+                        size_t workspace_bytes, int32_t* d_status, void* stream);
+
+/* Backward: dQ [B, Hq, S, d], dK and dV [B, Hkv, S, d] of dtype, from the forward's O and LSE and the gradient dO
+ * [B, Hq, S, d].  With B, Hq or S of 0 the call writes nothing (dK and dV where Hq = 0 are the caller's to zero). */
+int mesh_attn_range_bwd(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d, const void* Q,
+                        const void* K, const void* V, const int32_t* lo, const int32_t* hi, int64_t mask_stride,
+                        const float* slopes, const void* O, const float* LSE, const void* dO, float scale, float cap, void* dQ,
+                        void* dK, void* dV, void* workspace, size_t workspace_bytes, int32_t* d_status, void* stream);
+
 /* Synchronise `stream`, copy word 0 of the device status block to *out (a mesh_attn_status).
  * Returns MESH_ATTN_ERR_CUDA if the copy or the synchronisation failed. */
 int mesh_attn_read_status(const int32_t* d_status, void* stream, int32_t* out);

@@ -3,7 +3,7 @@
 Argument marshalling only: every step of the computation (tile map, greedy order, tile
 attention, LSE merge) runs in the C++ planner and the CUDA kernels behind the C ABI declared
 in include/mesh_attn.h.  The functions carry the same names as the C entry points; those of rotary
-positions and differential attention hand their tensors to _binding.so, an extension module loaded
+positions, differential attention, the paged cache and range-masked attention hand their tensors to _binding.so, an extension module loaded
 by the first of them.  PyTorch
 supplies device memory and streams; nothing here computes attention, and there is no CPU
 fallback: if the library is missing, load_library() raises.
@@ -90,6 +90,18 @@ _SIGS = {
     "mesh_attn_diff_decode_workspace_size": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i64, P_sz]),
     "mesh_attn_diff_decode": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, P_i64, c_vp, P_i64, c_vp, c_vp,
                                       c_i32, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "mesh_attn_paged_append": (c_i32, [c_i32, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp, P_i64, c_vp, P_i64, c_vp, P_i64, c_vp, P_i64,
+                                       c_i32, c_i32, c_vp, P_i64, c_vp, P_i64, c_vp, c_i32, c_i64, c_vp, c_vp, c_i32, c_i32, c_i32,
+                                       ctypes.POINTER(ctypes.c_double), P_i32, c_i32, c_vp, c_i32, P_i64, c_vp, c_vp]),
+    "mesh_attn_paged_workspace_size": (c_i32, [c_i32, c_i64, c_i32, c_i32, c_i32, c_i32, c_i64, P_sz]),
+    "mesh_attn_paged_attn": (c_i32, [c_i32, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp, P_i64, c_i32, c_i32, c_vp, P_i64, c_vp, P_i64,
+                                     c_vp, c_i32, c_i64, c_vp, c_vp, c_i64, c_f32, c_f32, c_vp, c_i64, c_vp, c_vp, c_vp, c_sz, c_vp,
+                                     c_vp]),
+    "mesh_attn_range_workspace_size": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i64, c_i32, c_i32, P_sz]),
+    "mesh_attn_range_fwd": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_f32, c_f32,
+                                    c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
+    "mesh_attn_range_bwd": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_vp,
+                                    c_vp, c_f32, c_f32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp]),
 }
 
 
@@ -116,7 +128,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def load_binding():
-    """Load _binding.so, which takes the tensors of rotary positions, differential attention and its decoding.
+    """Load _binding.so, which takes the tensors of rotary positions, differential attention and its decoding, the paged cache
+    and range-masked attention.
     Those calls load it when they are first made; nothing else needs it."""
     global _ext
     if _ext is None:
@@ -127,7 +140,8 @@ def load_binding():
             raise RuntimeError("_binding.so is missing, or of another PyTorch: build it (python -c 'import __graft_entry__ as "
                                "g; g.build()')") from e
         _binding.bind(*(ctypes.cast(getattr(lib, name), c_vp).value for name in (
-            "mesh_attn_rope", "mesh_attn_diff_fwd", "mesh_attn_diff_bwd", "mesh_attn_diff_decode")))
+            "mesh_attn_rope", "mesh_attn_diff_fwd", "mesh_attn_diff_bwd", "mesh_attn_diff_decode", "mesh_attn_paged_append",
+            "mesh_attn_paged_attn", "mesh_attn_range_fwd", "mesh_attn_range_bwd")))
         _ext = _binding
     return _ext
 
@@ -696,8 +710,8 @@ def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Te
              status, _handle_of(stream))
 
 
-def _raise_status(status: torch.Tensor):
-    code = mesh_attn_read_status(status, torch.cuda.current_stream(status.device))
+def _raise_status(status: torch.Tensor, stream=None):
+    code = mesh_attn_read_status(status, torch.cuda.current_stream(status.device) if stream is None else stream)
     if code != 0:
         raise MeshAttnError(code, "device", f"status block {status.tolist()}")
 
@@ -815,3 +829,176 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if check_status:
         _raise_status(st)
     return O, LSE
+
+
+# ---------------------------------------------------------------- a paged cache
+
+def mesh_paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      table: torch.Tensor, offsets: torch.Tensor, lens: torch.Tensor, rope: Optional[MeshRope] = None,
+                      positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None, check_status: bool = True, stream=None) -> Optional[torch.Tensor]:
+    """New tokens' keys and values into their sequences' pages, on the current stream (or `stream`): k turned by `rope` (copied
+    without one), v copied.  Returns q turned likewise, as a dense tensor or in q_out, for mesh_paged_attention (None for no q).
+
+    q [N, Hq, d], k, v [N, Hkv, d]: the new tokens of all sequences one sequence after another, views with any token and head
+    strides, e.g. slices of one projection.  k_pages, v_pages [n_pages, Hkv, page, d], written in place; table int32 [B, pages]:
+    sequence b's token i is row i % page of page table[b, i // page].  Sequence b's new tokens are rows offsets[b] to offsets[b + 1]
+    (int32 [B + 1]) and the last of the lens[b] (int32 [B]) tokens it then has; rows from offsets[B] on are left as they
+    are (in a q_out made by the call: not set).  positions: int32 or int64 [axes, N] ([N] for one axis) where they are not the
+    tokens' places.  A token whose place or page does not exist is left out and recorded in `status`; a program that calls it every step
+    keeps status (new_status) and passes check_status=False, which leaves out the wait."""
+    st = new_status(k.device) if status is None else status
+    out = (_ext or load_binding()).paged_append(None if rope is None else rope._native, q, k, v, k_pages, v_pages, table, offsets,
+                                                lens, positions, q_out, st, _handle_of(stream))
+    if out.__class__ is int:
+        _check(out, "mesh_attn_paged_append")
+    if check_status:
+        _raise_status(st, stream)
+    return out[0]
+
+
+def new_paged_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor, max_new: int) -> torch.Tensor:
+    """Workspace of mesh_paged_attention for batches of at most as many tokens and sequences and at most max_new new tokens of
+    one, zeroed as the first call wants it."""
+    load_library()
+    n = c_sz()
+    _check(_lib.mesh_attn_paged_workspace_size(_dtype_code(q.dtype), q.shape[0], table.shape[0], q.shape[1], k_pages.shape[1],
+                                               q.shape[2], max_new, ctypes.byref(n)), "mesh_attn_paged_workspace_size")
+    return torch.zeros(max(n.value, 16), dtype=torch.uint8, device=q.device)
+
+
+def mesh_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, offsets: torch.Tensor,
+                         lens: torch.Tensor, max_new: int, scale: Optional[float] = None, cap: float = 0.0,
+                         slopes: Optional[torch.Tensor] = None, window: int = 0, O: Optional[torch.Tensor] = None,
+                         LSE: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, check_status: bool = True, stream=None):
+    """Attention of the new tokens q [N, Hq, d] over their sequences' pages, on the current stream (or `stream`); the pages hold
+    the new tokens' own keys and values already (mesh_paged_append, whose arguments these are).  Token i of a sequence sees its
+    tokens j <= i, with window > 0 those with i - j < window; scores are scale q.k (1 / sqrt(d) unless given), capped to
+    cap tanh(score / cap) with cap > 0, less slopes[h] (i - j) with slopes (fp32 [Hq]).
+
+    One call serves decoding steps (max_new = 1), guessed tokens and chunks of prompts, also mixed: max_new bounds a
+    sequence's new tokens.  Returns O [N, Hq, d] and LSE fp32 [N, Hq]; rows from offsets[B] on are not written.  q and the pages may
+    be views with strides of multiples of 16 bytes; page a multiple of 16.  A serving loop keeps workspace (new_paged_workspace) and
+    status and passes check_status=False."""
+    ws = new_paged_workspace(q, k_pages, table, max_new) if workspace is None else workspace
+    st = new_status(q.device) if status is None else status
+    out = (_ext or load_binding()).paged_attn(q, k_pages, v_pages, table, offsets, lens, max_new, scale, cap, slopes, window, O, LSE,
+                                              ws, st, _handle_of(stream))
+    if out.__class__ is int:
+        _check(out, "mesh_attn_paged_attn")
+    if check_status:
+        _raise_status(st, stream)
+    return out
+
+
+# ---------------------------------------------------------------- range-masked attention
+
+def mesh_ranges(documents: Sequence[int], causal: bool = True, prefixes: Optional[Sequence[int]] = None, window: int = 0,
+                length: Optional[int] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """lo and hi (int32 [S], on the host) of documents of these lengths packed one after another: each query sees its own document
+    (causal: up to itself), the first prefixes[i] tokens of document i also one another, with window > 0 no key further
+    back than window - 1.  `length` beyond their sum pads: rows behind see nothing and are not seen."""
+    documents = [int(n) for n in documents]
+    if any(n < 0 for n in documents):
+        raise ValueError("documents must have lengths >= 0")
+    if prefixes is not None and len(prefixes) != len(documents):
+        raise ValueError("prefixes must give a length for each document")
+    if window < 0:
+        raise ValueError("window must be >= 0")
+    S = sum(documents) if length is None else int(length)
+    if S < sum(documents):
+        raise ValueError(f"the documents have {sum(documents)} tokens, more than length = {S}")
+    lo, hi = torch.zeros(S, dtype=torch.int32), torch.zeros(S, dtype=torch.int32)
+    at = 0
+    for d, n in enumerate(documents):
+        i = torch.arange(at, at + n, dtype=torch.int32)
+        lo[at:at + n] = torch.clamp(i - (window - 1), min=at) if window else at
+        hi[at:at + n] = i + 1 if causal else at + n
+        if prefixes is not None and causal:
+            hi[at:at + n] = torch.clamp(hi[at:at + n], min=at + max(0, min(int(prefixes[d]), n)))
+        at += n
+    return lo, hi
+
+
+def new_range_workspace(q: torch.Tensor, k: torch.Tensor, backward: bool = False) -> torch.Tensor:
+    """Workspace of mesh_range_attention for tensors of q's and k's sizes; with backward, of both directions."""
+    load_library()
+    B, Hq, S, d = q.shape
+    n = c_sz()
+    _check(_lib.mesh_attn_range_workspace_size(_dtype_code(q.dtype), B, Hq, k.shape[1], S, d, int(backward), ctypes.byref(n)),
+           "mesh_attn_range_workspace_size")
+    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=q.device)
+
+
+def mesh_range_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lo: torch.Tensor, hi: torch.Tensor,
+                         scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                         O: Optional[torch.Tensor] = None, LSE: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, check_status: bool = True,
+                         stream=None):
+    """Attention where query i sees the keys lo[i] <= j < hi[i], on the current stream (or `stream`): packed documents, prefixes that
+    see one another, windows, padding (mesh_ranges makes lo and hi).  q [B, Hq, S, d], k, v [B, Hkv, S, d], all bf16 or all
+    fp32; lo, hi int32 [S] or [B, S] on the device.  Scores are scale q.k (1 / sqrt(d) unless given), capped to
+    cap tanh(score / cap) with cap > 0, less slopes[h] |i - j| with slopes (fp32 [Hq]).  Returns O (q's shape and dtype) and LSE
+    (fp32 [B, Hq, S]); a query that sees nothing gets 0 and -inf.  A program that calls it every step keeps workspace
+    (new_range_workspace) and status (new_status) and passes check_status=False, which leaves out the wait."""
+    if workspace is None or status is None:
+        load_binding().range_check(q, k, v, lo, hi, slopes)
+    ws = new_range_workspace(q, k) if workspace is None else workspace
+    st = new_status(q.device) if status is None else status
+    out = (_ext or load_binding()).range_fwd(q, k, v, lo, hi, scale, cap, slopes, O, LSE, ws, st, _handle_of(stream))
+    if out.__class__ is int:
+        _check(out, "mesh_attn_range_fwd")
+    if check_status:
+        _raise_status(st, stream)
+    return out
+
+
+def mesh_range_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lo: torch.Tensor, hi: torch.Tensor,
+                                  O: torch.Tensor, LSE: torch.Tensor, dO: torch.Tensor, scale: Optional[float] = None,
+                                  cap: float = 0.0, slopes: Optional[torch.Tensor] = None, dQ: Optional[torch.Tensor] = None,
+                                  dK: Optional[torch.Tensor] = None, dV: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                                  check_status: bool = True, stream=None):
+    """(dQ, dK, dV) from the forward's O and LSE and the gradient dO, on the current stream (or `stream`)."""
+    if workspace is None or status is None:
+        load_binding().range_check(q, k, v, lo, hi, slopes)
+    ws = new_range_workspace(q, k, backward=True) if workspace is None else workspace
+    st = new_status(q.device) if status is None else status
+    out = (_ext or load_binding()).range_bwd(q, k, v, lo, hi, O, LSE, dO, scale, cap, slopes, dQ, dK, dV, ws, st, _handle_of(stream))
+    if out.__class__ is int:
+        _check(out, "mesh_attn_range_bwd")
+    if check_status:
+        _raise_status(st, stream)
+    return out
+
+
+class MeshRangeAttentionFunction(torch.autograd.Function):
+    """torch.autograd binding of mesh_range_attention: gradients reach q, k and v; LSE is a non-differentiable output."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, lo, hi, scale, cap, slopes, check_status, status):
+        if slopes is not None and slopes.requires_grad:
+            raise ValueError("slopes get no gradient: pass them detached")
+        O, LSE = mesh_range_attention(q, k, v, lo, hi, scale, cap, slopes, status=status, check_status=check_status)
+        ctx.save_for_backward(q, k, v, lo, hi, slopes, O, LSE)
+        ctx.args = (scale, cap)
+        ctx.check_status, ctx.status = check_status, status
+        ctx.mark_non_differentiable(LSE)
+        return O, LSE
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO, dLSE):
+        q, k, v, lo, hi, slopes, O, LSE = ctx.saved_tensors
+        grads = mesh_range_attention_backward(q, k, v, lo, hi, O, LSE, dO.contiguous(), *ctx.args, slopes, status=ctx.status,
+                                              check_status=ctx.check_status)
+        return (*grads, None, None, None, None, None, None, None)
+
+
+def mesh_range_attention_autograd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lo: torch.Tensor, hi: torch.Tensor,
+                                  scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                                  check_status: bool = True, status: Optional[torch.Tensor] = None):
+    """mesh_range_attention with autograd: returns (O, LSE); O.backward(...) fills the gradients of q, k and v.  With
+    check_status=False a failure in either direction is recorded in `status` (new_status), for the program to read later."""
+    return MeshRangeAttentionFunction.apply(q, k, v, lo, hi, scale, cap, slopes, check_status, status)

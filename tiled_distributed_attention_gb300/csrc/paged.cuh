@@ -1,0 +1,49 @@
+// What the kernels over a paged cache share: which sequence a token of the packed batch is of.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace mesh {
+
+// The last b of [lo, B) with offsets[b] <= tok, or lo - 1 where there is none, by the calling thread alone.
+__device__ __forceinline__ int last_begun(const int32_t* offsets, int lo, int B, int64_t tok) {
+  int a = lo - 1, z = B;  // offsets[a] <= tok < offsets[z], as far as they are known
+  while (z - a > 1) {
+    const int c = (a + z) >> 1;
+    if (offsets[c] <= tok) a = c;
+    else z = c;
+  }
+  return a;
+}
+
+// The same for the whole of a converged warp and one token, 32 offsets at a time: -1 where tok is before offsets[0].
+__device__ __forceinline__ int last_begun_warp(const int32_t* offsets, int B, int64_t tok) {
+  const int lane = threadIdx.x & 31;
+  int a = 0, n = B;  // the answer is in [a - 1, a + n)
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int at = a + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, at < a + n && offsets[min(at, B - 1)] <= tok);
+    const int c = __popc(m);  // leading lanes, where the offsets ascend
+    if (c == 0) return a - 1;
+    const int end = a + n;
+    a += (c - 1) * step + 1;  // offsets[a - 1] <= tok
+    n = min(step - 1, end - a);
+  }
+  return a - 1;
+}
+
+// The sequence of token `tok` of a packed batch, offsets[b] <= tok < offsets[b + 1], or -1: before the first sequence or
+// behind the last.  All 32 lanes call it, `first` being the first lane's token, which none of theirs precedes.
+// Offsets that do not ascend give some sequence of 0 .. B - 1 or -1.
+__device__ __forceinline__ int sequence_of(const int32_t* offsets, int B, int64_t first, int64_t tok) {
+  const int b0 = last_begun_warp(offsets, B, first);
+  int b = b0;
+  if (tok != first) b = last_begun(offsets, max(b0, 0), B, tok);
+  if (b < 0 || b >= B || tok >= offsets[B]) return -1;
+  return b;
+}
+
+}  // namespace mesh

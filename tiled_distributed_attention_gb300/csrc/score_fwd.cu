@@ -1,0 +1,112 @@
+// Host side of the tensor-core forward with scores that are capped, biased and masked by ranges (score_fwd.cuh): how heads and
+// tokens fill its tiles, when its units are cut into parts, the workspace and the tensor maps.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "internal.h"
+#include "score_fwd.h"
+#include "tmap.h"
+
+namespace mesh {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn get_encode(std::string* err) {
+  static EncodeTiledFn fn = nullptr;
+  if (fn) return fn;
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !ptr) {
+    *err = "cuTensorMapEncodeTiled is not available from the driver";
+    return nullptr;
+  }
+  fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  return fn;
+}
+
+bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const int64_t* strides, const uint32_t* box,
+                     std::string* err) {
+  EncodeTiledFn enc = get_encode(err);
+  if (!enc) return false;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    // the stride of an axis of one is never used, and need not be one that a map takes
+    if (i > 0) s[i - 1] = dims[i] > 1 ? (cuuint64_t)strides[i - 1] * 2 : (cuuint64_t)16;
+  }
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return false;
+  }
+  return true;
+}
+
+// Tiles.  All query heads of a KV head in one tile where they and their tokens fill it (3 heads: 42 tokens, 126 rows), else the
+// heads in the fewest equal chunks that do to 7/8.
+//
+// Parts.  Units come in waves of one an SM, each about as long as its blocks (1.6 us) and a fixed part of about
+// three blocks; parts cost a merge of about four blocks.  The count that makes the waves shortest by that measure, four an SM at
+// most; S bounds a unit's blocks, half of them where a causal mask may be meant.
+ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms) {
+  ScoreFwdShape z{};
+  const int g = Hq / Hkv;
+  for (z.hc = (g + 127) / 128;; ++z.hc) {
+    z.gh = (g + z.hc - 1) / z.hc;
+    z.tt = 128 / z.gh;
+    if (z.gh * z.tt >= 112) break;
+  }
+  z.hc = (g + z.gh - 1) / z.gh;
+  const int64_t tu = 2 * z.tt;
+  const int64_t groups = paged ? N / tu + B : (S + tu - 1) / tu;
+  const int64_t lanes = (int64_t)Hkv * z.hc * (paged ? 1 : B);
+  z.groups = (int32_t)std::min<int64_t>(groups, 0x7fffffff);
+  z.lanes = (int32_t)std::min<int64_t>(lanes, 0x7fffffff);
+  const int64_t units = lanes * (paged ? std::max<int64_t>(1, groups - (N % tu == 0 ? 1 : 0)) : groups);
+  const double nb = (double)((S + 127) / 128) * (paged ? 1.0 : 0.5);
+  z.parts = 1;
+  double best = 0;
+  for (int k = 1; k <= MAX_FWD_PARTS; ++k) {
+    if (k > 1 && (nb / k < 2 || lanes * groups * k > FWD_PART_WAVES * sms)) break;
+    const double cost = (double)((units * k + sms - 1) / sms) * (nb / k + 3) + (k > 1 ? 4 : 0);
+    if (k == 1 || cost < 0.95 * best) {
+      best = cost;
+      z.parts = k;
+    }
+  }
+  size_t at = 256;  // the counter
+  if (z.parts > 1) {
+    const size_t rows = (size_t)z.lanes * z.groups * z.parts * 256;
+    z.part_o = at;
+    at += rows * d * 4;
+    z.part_lse = at;
+    at += rows * 4;
+  }
+  z.total = at;
+  return z;
+}
+
+size_t score_fwd_paged_workspace(int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d) {
+  const ScoreFwdShape z = score_fwd_shape(true, 0, N, B, Hq, Hkv, d, 1);
+  const int64_t units = std::min<int64_t>((int64_t)FWD_PART_WAVES * MAX_SMS, (int64_t)z.lanes * z.groups * MAX_FWD_PARTS);
+  return 256 + (size_t)units * 256 * (d + 1) * 4;
+}
+
+int launch_score_fwd(const ScoreFwdArgs& a, int sms, cudaStream_t st, std::string* err) {
+  const ScoreFwdShape z = score_fwd_shape(a.paged, a.S, a.N, a.B, a.Hq, a.Hkv, a.d, sms);
+  if (a.paged) return a.d == 128 ? launch_score_fwd_paged_128(a, z, sms, st, err) : launch_score_fwd_paged_64(a, z, sms, st, err);
+  return a.d == 128 ? launch_score_fwd_128(a, z, sms, st, err) : launch_score_fwd_64(a, z, sms, st, err);
+}
+
+}  // namespace mesh

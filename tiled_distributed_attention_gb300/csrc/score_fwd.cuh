@@ -1,0 +1,947 @@
+// Attention forward whose scores are capped, biased by distance and masked by a range of keys a row, bf16 inputs, on the
+// 5th-generation tensor cores (sm_103a): of a dense batch with ranges given (range-masked attention), or of the new tokens of
+// sequences in a paged cache, whose ranges follow from their places (a chunk of a prompt).
+//   x_ij = cap tanh(s q_i.k_j / cap) (or s q_i.k_j) - slope_h |i - j|,  lo_i <= j < hi_i,   O_i = sum_j softmax(x_i)_j v_j.
+//
+// A tile is 128 rows: gh query heads of one KV head times tt of their tokens, so that a tile's rows share its keys
+// and few tokens still fill it; a unit is two tiles, one softmax warpgroup each, tokens after tokens, which stream
+// the K and V blocks (128 keys) from the first to the last that any of its rows sees, in shared memory.  Roles, ring, online
+// softmax with its lazy reference, and the O accumulators in tensor memory are the plain tile kernel's (tile_fwd_tc.cu):
+//   warps 0-7  softmax, warp 8 MMA issuer, warp 9 producer (unit decode and TMA), warps 10-11 idle
+//   TMEM (512 columns): S_0 | S_1 | O_0 | O_1; P_t overwrites S_t
+// Rows see ranges: a warp masks a block only where it is not inside all of its rows' ranges, and a row that has met no key yet
+// takes no maximum pass for a block that it does not see.
+//
+// Cap (MODE 2).  tanh by a polynomial while |s q.k| <= cap in the whole warp and block (checked by the maximum of its
+// square), else by exponentials.  Slopes (MODE 1, and 2 where given): one more FMA where a block lies on one side of all of the
+// warp's rows, |i - j| only on the diagonal.
+//
+// Pages.  A block's keys are boxes of as many rows as a page (a power of two that divides it, 16 to 128), one lane of the producer
+// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Places behind the last token
+// load a page that does not exist, which arrives as zeros; what an earlier owner left behind it in its last page is
+// zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
+//
+// Few units are cut into parts of their keys (score_fwd_shape), whose normalised outputs and LSEs merge_kernel adds up in order.
+// P is rounded to bf16 for its product (2^-9 relative a term), everything else is fp32.
+//
+// Every mbarrier wait is bounded: a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT in the status
+// block, every role of the CTA stops, in-flight copies and MMAs are drained and TMEM is freed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "abi_util.h"
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+#include "score.cuh"
+#include "score_fwd.h"
+#include "tmap.h"
+
+namespace mesh {
+namespace sfw {
+
+constexpr int BM = 128;  // rows per tile = TMEM lanes
+constexpr int BN = 128;  // keys per KV block
+constexpr int NST = 2;   // K/V ring stages
+constexpr int NUM_THREADS = 384;
+constexpr int SOFTMAX_REGS = 200;  // 2 x 128 x 200 + 128 x 104 <= 384 x 168 registers at launch
+constexpr int OTHER_REGS = 104;
+constexpr int WARP_MMA = 8;
+constexpr int WARP_LOAD = 9;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.69314718055994531f;
+constexpr float LOG2_RESCALE = 8.0f;
+// Row sum of one block accepted without a max pass: every term is then at most 2^16, and a sum
+// this large implies a row maximum more than 2^LOG2_RESCALE above the reference (2^16 / BN > 2^8).
+constexpr float SUM_ACCEPT = 65536.0f;
+constexpr int MAX_PARTS = MAX_FWD_PARTS;
+constexpr int64_t DRAIN_NS = 200000000;  // exit-path waits for copies in flight
+constexpr int ROLE_SOFTMAX = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_SEQ = 4, ROLE_PAGE = 5;
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t TILE = BM * D * 2;  // bytes of one Q tile / K block / V block
+  static constexpr uint32_t BOX = BM * 64 * 2;  // its 64-column half
+  static constexpr uint32_t Q_OFF = 0;
+  static constexpr uint32_t K_OFF = Q_OFF + 2 * TILE;
+  static constexpr uint32_t V_OFF = K_OFF + NST * TILE;
+  static constexpr uint32_t EPI_OFF = V_OFF + NST * TILE;  // 8 softmax warps x 4 KB
+  static constexpr uint32_t BAR_OFF = EPI_OFF + 8 * 4096;
+  static constexpr int B_QFULL = 0, B_QEMPTY = 1, B_KFULL = 2, B_KEMPTY = B_KFULL + NST,
+                       B_VFULL = B_KEMPTY + NST, B_VEMPTY = B_VFULL + NST, B_SFULL = B_VEMPTY + NST,
+                       B_PFULL = B_SFULL + 2, B_OFINAL = B_PFULL + 2, B_OFREE = B_OFINAL + 2,
+                       B_UFULL = B_OFREE + 2, B_UEMPTY = B_UFULL + 2, B_DRAIN = B_UEMPTY + 2,
+                       NBARS = B_DRAIN + 1;
+  static constexpr uint32_t MISC_OFF = BAR_OFF + NBARS * 8 + (NBARS % 2) * 8;  // tmem base, abort flag
+  static constexpr uint32_t RING_OFF = MISC_OFF + 16;  // unit ring: 2 decoded units, 16 ints each
+  static constexpr uint32_t TOTAL = RING_OFF + 2 * 64;
+  static constexpr uint32_t ALLOC = TOTAL + 1024;
+};
+static_assert(Layout<128>::ALLOC <= 232448, "shared memory of a CTA");
+
+struct Params {
+  const float* slopes;
+  __nv_bfloat16* o;
+  int64_t os[3];  // batch, head, token strides of O
+  float* lse;
+  int64_t ls[3];
+  float* part_o;  // units in parts: [unit][part][tile][128][D] and [unit][part][tile][128]
+  float* part_lse;
+  int32_t* status;
+  uint32_t* counter;
+  const int32_t* lo;
+  const int32_t* hi;
+  int64_t mask_bs;
+  const int32_t* offsets;
+  const int32_t* lens;
+  const int32_t* table;
+  int64_t table_s;
+  int64_t S;
+  int32_t N, B, Hq, Hkv, g, gh, tt, hc, groups, lanes, batch, n_units, parts;
+  int32_t n_pages, page, max_pages, max_new, window, box_rows;
+  float scale, scale_log2, cap_log2, inv_cap;  // cap log2 e, scale / cap
+  int64_t wait_limit_ns;
+};
+
+// A unit: its rows are the tokens [tok0, tok0 + 2 tt) below n_tok of query heads h0 .. h0 + gh - 1 (below h_end), its keys the
+// blocks [blk0, blk0 + NB).  Paged: the sequence's first new token is row `row0` of the batch and has the place pos0.
+struct Unit {
+  int u, b, hk, h0, h_end, tok0, n_tok, row0, pos0, len, blk0, NB, part;
+  __device__ __forceinline__ int ntiles(int tt) const { return tok0 + tt < n_tok ? 2 : 1; }
+};
+__device__ __forceinline__ void put_unit(volatile int32_t* e, const Unit& x) {
+  e[0] = x.u, e[1] = x.b, e[2] = x.hk, e[3] = x.h0, e[4] = x.h_end, e[5] = x.tok0, e[6] = x.n_tok, e[7] = x.row0;
+  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.part;
+}
+__device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
+  Unit x;
+  x.u = e[0], x.b = e[1], x.hk = e[2], x.h0 = e[3], x.h_end = e[4], x.tok0 = e[5], x.n_tok = e[6], x.row0 = e[7];
+  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.part = e[12];
+  return x;
+}
+
+// Unit u of a launch, decoded by a whole warp: numbered batch of lanes by batch, within it from the last tokens (the
+// most keys where the mask is causal) to the first, within those lane by lane, its parts together.  A lane is a (batch, KV head,
+// chunk of heads); paged: a (KV head, chunk), whose groups are those of all sequences, sequence b's from
+// offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
+template <bool PAGED>
+__device__ __forceinline__ Unit decode(int u, const Params& prm, bool report) {
+  Unit x;
+  const int lane = threadIdx.x & 31, tu = 2 * prm.tt;
+  x.u = u;
+  x.part = prm.parts > 1 ? u % prm.parts : -1;
+  int t = prm.parts > 1 ? u / prm.parts : u;
+  const int per = prm.batch * prm.groups, first = t / per * prm.batch;
+  const int lanes = min(prm.batch, prm.lanes - first);  // the last batch may be smaller
+  t %= per;
+  const int grp = prm.groups - 1 - t / lanes;
+  int ln = first + t % lanes;
+  const int c = ln % prm.hc;
+  ln /= prm.hc;
+  x.hk = ln % prm.Hkv;
+  x.b = ln / prm.Hkv;
+  x.h0 = x.hk * prm.g + c * prm.gh;
+  x.h_end = min(x.h0 + prm.gh, (x.hk + 1) * prm.g);
+  x.blk0 = x.NB = 0;
+  int kmin = 0x7fffffff, kmax = 0;  // keys that some row sees
+  if (PAGED) {
+    // the last b with offsets[b] / tu + b <= grp
+    int a = 0, n = prm.B;
+    while (n > 0) {
+      const int step = (n + 31) / 32, at = a + lane * step;
+      const bool in = at < a + n;
+      const unsigned m = __ballot_sync(0xffffffffu, in && max(prm.offsets[in ? at : 0], 0) / tu + at <= grp);
+      const int k = __popc(m);
+      if (k == 0) break;
+      const int end = a + n;
+      a += (k - 1) * step + 1;
+      n = min(step - 1, end - a);
+    }
+    x.b = a - 1;
+    if (x.b < 0) {
+      x.b = 0, x.tok0 = x.n_tok = x.row0 = x.pos0 = x.len = 0;
+      return x;
+    }
+    const int32_t o0 = prm.offsets[x.b], o1 = prm.offsets[x.b + 1], len = prm.lens[x.b];
+    x.row0 = min(max(o0, 0), prm.N);
+    x.n_tok = min(min(max(o1, x.row0), prm.N) - x.row0, prm.max_new);
+    const int64_t most = (int64_t)prm.max_pages * prm.page;
+    x.len = (int32_t)min((int64_t)max(len, x.n_tok), most);
+    // what does not fit is recorded and taken as the nearest that does
+    if (report && lane == 0 && (x.row0 != o0 || x.n_tok != o1 - o0 || x.len != len))
+      record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, x.b);
+    x.n_tok = min(x.n_tok, x.len);
+    x.pos0 = x.len - x.n_tok;
+    x.tok0 = (grp - (x.row0 / tu + x.b)) * tu;
+    if (x.tok0 >= x.n_tok) {
+      x.n_tok = 0;
+      return x;
+    }
+    kmax = x.pos0 + min(x.tok0 + tu, x.n_tok);
+    kmin = prm.window ? max(0, x.pos0 + x.tok0 + 1 - prm.window) : 0;
+  } else {
+    x.tok0 = grp * tu;
+    x.n_tok = (int)prm.S;
+    x.row0 = x.pos0 = 0;
+    x.len = (int)prm.S;
+    const int32_t* lo = prm.lo + x.b * prm.mask_bs;
+    const int32_t* hi = prm.hi + x.b * prm.mask_bs;
+    for (int i = lane; i < tu; i += 32)
+      if (x.tok0 + i < x.n_tok) {
+        const int a = max(lo[x.tok0 + i], 0), z = min(hi[x.tok0 + i], x.len);
+        if (a < z) {
+          kmin = min(kmin, a);
+          kmax = max(kmax, z);
+        }
+      }
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
+  }
+  if (kmin < kmax) {
+    x.blk0 = kmin / BN;
+    x.NB = (kmax + BN - 1) / BN - x.blk0;
+  }
+  if (x.part >= 0) {
+    const int k = max(1, min(prm.parts, x.NB)), n = x.NB, i = min(x.part, k), j = min(x.part + 1, k);
+    x.blk0 += (int)((int64_t)i * n / k);
+    x.NB = (int)((int64_t)j * n / k) - (int)((int64_t)i * n / k);
+  }
+  return x;
+}
+
+// Keys of a row by its token.
+template <bool PAGED>
+__device__ __forceinline__ void range_of(const Params& prm, const Unit& x, int tok, int& lo, int& hi, int& pos) {
+  if (PAGED) {
+    pos = x.pos0 + tok;
+    hi = pos + 1;
+    lo = prm.window ? max(0, hi - prm.window) : 0;
+  } else {
+    pos = tok;
+    lo = max(prm.lo[x.b * prm.mask_bs + tok], 0);
+    hi = min(prm.hi[x.b * prm.mask_bs + tok], x.len);
+    if (lo >= hi) lo = hi = 0;
+  }
+}
+
+template <int D, int MODE, bool PAGED>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params prm) {
+  using Ly = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;  // 1024-aligned base (128-byte swizzle atoms)
+  uint8_t* smem = smem_raw + (sb - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sb + Ly::BAR_OFF + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::MISC_OFF);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + Ly::MISC_OFF + 4);
+  volatile int32_t* ring = reinterpret_cast<volatile int32_t*>(smem + Ly::RING_OFF);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(Ly::B_QFULL), 1);
+    mbar_init(bar(Ly::B_QEMPTY), 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(Ly::B_KFULL + s), 1);
+      mbar_init(bar(Ly::B_KEMPTY + s), 1);
+      mbar_init(bar(Ly::B_VFULL + s), 1);
+      mbar_init(bar(Ly::B_VEMPTY + s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(Ly::B_SFULL + t), 1);
+      mbar_init(bar(Ly::B_PFULL + t), BM);
+      mbar_init(bar(Ly::B_OFINAL + t), 1);
+      mbar_init(bar(Ly::B_OFREE + t), BM);
+      mbar_init(bar(Ly::B_UFULL + t), 1);
+      mbar_init(bar(Ly::B_UEMPTY + t), 1 + 8);  // one lane of the MMA warp and of each softmax warp
+    }
+    mbar_init(bar(Ly::B_DRAIN), 1);
+    wait_for_kernel_before();
+    // without any time to wait there is nothing to start: the first load would be waited for
+    if (prm.wait_limit_ns <= 0) record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
+    *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  wait_for_kernel_before();  // and before tensor memory is taken, which that kernel may still want
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (warp == WARP_LOAD && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 8) {
+    // ================================================================ softmax warpgroups
+    regs_inc<SOFTMAX_REGS>();
+    const int t = warp >> 2;
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;  // row within the tile = TMEM lane
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const uint32_t tm_s = tmem + lane_base + (uint32_t)(t * 128);
+    const uint32_t tm_o = tmem + lane_base + 256u + (uint32_t)(t * 128);
+    float* epi = reinterpret_cast<float*>(smem + Ly::EPI_OFF + (uint32_t)warp * 4096u);
+    const int row_h = row / prm.tt, row_t = row - row_h * prm.tt;  // its head and token within the tile
+    int nu = 0, cnt = 0, uses = 0;
+    bool ok = true;
+    while (ok) {
+      const int slot = nu & 1;
+      ok = mbar_wait(bar(Ly::B_UFULL + slot), (uint32_t)((nu >> 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                     ROLE_SOFTMAX, -1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const Unit x = get_unit(ring + 16 * slot);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Ly::B_UEMPTY + slot));
+      ++nu;
+      if (x.u < 0) break;
+      if (t >= x.ntiles(prm.tt) || x.n_tok == 0) continue;
+      const int tok = x.tok0 + t * prm.tt + row_t, h = x.h0 + row_h;
+      const bool valid = row_h < prm.gh && h < x.h_end && tok < x.n_tok;
+      int lo = 0, hi = 0, pos = 0;
+      float slope2 = 0.f;
+      if (valid) {
+        range_of<PAGED>(prm, x, tok, lo, hi, pos);
+        if (MODE >= 1 && prm.slopes) slope2 = prm.slopes[h] * LOG2E;
+      }
+      // keys that all of the warp's rows see, and the places between which its rows lie
+      const int all_lo = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
+      const int all_hi = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
+      int pmin = 0, pmax = 0;
+      if (MODE >= 1) {
+        pmin = __reduce_min_sync(0xffffffffu, valid ? pos : 0x7fffffff);
+        pmax = __reduce_max_sync(0xffffffffu, valid ? pos : -1);
+      }
+      float m_used = valid ? -INFINITY : 0.f, l_sum = 0.f;
+      for (int jb = x.blk0; jb < x.blk0 + x.NB; ++jb, ++cnt) {
+        ok = mbar_wait(bar(Ly::B_SFULL + t), (uint32_t)(cnt & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                       ROLE_SOFTMAX, x.u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const int j0 = jb * BN;
+        const bool edge = all_lo > j0 || all_hi < j0 + BN;
+        const bool sees = lo < j0 + BN && hi > j0;
+        // The exponentials use the row's running reference m_used, which only ever grows.  A
+        // block whose row maximum stays within 2^LOG2_RESCALE of it needs no maximum at all, so
+        // the common case skips the max pass: exponentiate against m_used and accept the block
+        // when its row sum is at most SUM_ACCEPT (every term is then bounded as well).  A row
+        // without a reference yet that sees a key of the block, or a block whose sum is too large
+        // or not finite, takes the row maximum first, raising m_used (and rescaling O and l)
+        // when it grew by more than 2^LOG2_RESCALE, and the exponentials are redone.
+        bool need_max = __any_sync(0xffffffffu, m_used == -INFINITY && sees);
+        float factor = 1.f, blk = 0.f;
+        uint32_t pk[BN / 2];
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          // S_t stays in TMEM until P_t is written, so a second pass reloads it rather than
+          // keeping 128 scores live across the pass
+          float s[BN];
+#pragma unroll
+          for (int c = 0; c < BN; c += 32) tmem_ld32(tm_s + (uint32_t)c, s + c);
+          tc_wait_ld();
+          if (MODE == 2) {
+            // base 2 scores under the cap: cap log2 e tanh(z), z = s scale / cap
+            const uint64_t k2 = f2_pack(prm.inv_cap, prm.inv_cap);
+            float um[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) um[(c >> 1) & 3] = max3f(um[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
+            const float zmax = fmaxf(max3f(um[0], um[1], um[2]), um[3]) * prm.inv_cap;
+            if (__all_sync(0xffffffffu, !valid || zmax <= 1.f)) {  // infinite: the other form; NaN: it stays NaN in both
+              const uint64_t cl2 = f2_pack(prm.cap_log2, prm.cap_log2);
+#pragma unroll
+              for (int c = 0; c < BN; c += 2) {
+                const uint64_t z = f2_mul(f2_pack(s[c], s[c + 1]), k2);
+                f2_unpack(f2_mul(f2_mul(z, cl2), tanh_ratio2(f2_mul(z, z))), s[c], s[c + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < BN; ++c) s[c] = prm.cap_log2 * tanh_any(s[c] * prm.inv_cap);
+            }
+          }
+          if (MODE >= 1) {
+            if (MODE == 1 || prm.slopes) {
+              const float sc = MODE == 2 ? 1.f : prm.scale_log2;
+              const bool before = j0 + BN - 1 <= pmin, behind = j0 >= pmax;
+              if (before || behind) {  // |i - j| = +-(i - j): linear in the column
+                const float sl = before ? slope2 : -slope2, base = sl * (float)(j0 - pos);
+#pragma unroll
+                for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], sc, fmaf(sl, (float)c, base));
+              } else {
+                const float off = (float)(j0 - pos);
+#pragma unroll
+                for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], sc, -slope2 * fabsf(off + (float)c));
+              }
+            }
+          }
+          if (edge) {
+            const int a = lo - j0, n = hi - lo;
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if ((uint32_t)(c - a) >= (uint32_t)n) s[c] = -INFINITY;
+          }
+          constexpr bool RAW = MODE == 0;  // s is not scaled yet
+          if (need_max) {
+            // row max: four independent chains of 3-input max
+            float mc[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v = max3f(s[32 * q], s[32 * q + 1], s[32 * q + 2]);
+#pragma unroll
+              for (int i = 3; i + 1 < 32; i += 2) v = max3f(v, s[32 * q + i], s[32 * q + i + 1]);
+              mc[q] = fmaxf(v, s[32 * q + 31]);
+            }
+            const float mx = fmaxf(max3f(mc[0], mc[1], mc[2]), mc[3]);
+            const float m_new = RAW ? mx * prm.scale_log2 : mx;
+            if (valid && m_new > -INFINITY) {
+              if (m_used == -INFINITY) {
+                m_used = m_new;
+              } else if (m_new > m_used + LOG2_RESCALE) {
+                factor *= fast_exp2(m_used - m_new);
+                m_used = m_new;
+              }
+            }
+          }
+          const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+          // p = 2^(x - m): two elements per FMA or ADD, four independent sum chains
+          const uint64_t sc2 = f2_pack(prm.scale_log2, prm.scale_log2);
+          const uint64_t nm2 = f2_pack(-mref, -mref);
+          uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < BN / 2; ++c) {
+            float x0, x1;
+            const uint64_t s2 = f2_pack(s[2 * c], s[2 * c + 1]);
+            f2_unpack(RAW ? f2_fma(s2, sc2, nm2) : f2_add(s2, nm2), x0, x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            acc2[c & 3] = f2_add(acc2[c & 3], f2_pack(p0, p1));
+            pk[c] = pack_bf16x2(p0, p1);
+          }
+          float sa, sb2;
+          f2_unpack(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), sa, sb2);
+          blk = sa + sb2;
+          // NaN fails the comparison: a NaN row takes the max pass once and is then accepted
+          if (pass == 1 || __all_sync(0xffffffffu, !valid || blk <= SUM_ACCEPT)) break;
+          need_max = true;
+        }
+        if (__any_sync(0xffffffffu, factor != 1.f)) {
+          // O_t holds every earlier PV product of this unit: S_t(j) was issued after
+          // PV_t(j-1) and its completion covers all earlier tensor-core work.
+          l_sum *= factor;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tm_o + (uint32_t)c, o);
+            tc_wait_ld();
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * factor);
+            tmem_st32(tm_o + (uint32_t)c, w);
+          }
+        }
+        l_sum += blk;
+        tmem_st32(tm_s, pk);
+        tmem_st32(tm_s + 32u, pk + 32);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(Ly::B_PFULL + t));
+      }
+      if (!ok) break;
+      // ---- epilogue: O_t out of TMEM
+      // a row without a visible key: O = 0, LSE = -inf (a NaN sum stays NaN).  What its accumulator holds is a sum of
+      // zeros, or nothing where the unit has no blocks
+      const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
+      const float lse = l_sum == 0.f ? -INFINITY : (m_used + log2f(l_sum)) * LN2;
+      if (x.NB > 0) {
+        ok = mbar_wait(bar(Ly::B_OFINAL + t), (uint32_t)(uses & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                       ROLE_SOFTMAX, x.u);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (x.part < 0) {
+        uint32_t w[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 2; ++c) w[c] = 0u;
+        if (x.NB > 0) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tm_o + (uint32_t)c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              w[(c + e) / 2] = l_sum == 0.f ? 0u : pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+          }
+          tc_fence_before();
+          mbar_arrive(bar(Ly::B_OFREE + t));
+          ++uses;
+        }
+        const int64_t bo = PAGED ? 0 : x.b, to = (int64_t)x.row0 + tok;
+        const int64_t at = valid ? bo * prm.os[0] + h * prm.os[1] + to * prm.os[2] : -1;
+        uint4* stage = reinterpret_cast<uint4*>(epi);
+        // 32 rows x 64 columns through the stage, 16-byte pieces swizzled by row: a store writes four whole 128-byte lines
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            stage[lane * 8 + (q ^ (lane & 7))] =
+                make_uint4(w[c / 2 + 4 * q], w[c / 2 + 4 * q + 1], w[c / 2 + 4 * q + 2], w[c / 2 + 4 * q + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), q = lane & 7;
+            const int64_t ra = __shfl_sync(0xffffffffu, at, r);
+            const uint4 v = stage[r * 8 + (q ^ (r & 7))];
+            if (ra >= 0) *reinterpret_cast<uint4*>(prm.o + ra + c + q * 8) = v;
+          }
+        }
+        if (valid) prm.lse[bo * prm.ls[0] + h * prm.ls[1] + to * prm.ls[2]] = lse;
+        continue;
+      }
+      // ---- a part: its normalised output, in fp32
+      const int64_t prow = ((int64_t)x.u * 2 + t) * BM + row;
+      if (x.NB > 0) {
+        float* dst0 = prm.part_o + (prow - lane) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tm_o + (uint32_t)c, o);
+          tc_wait_ld();
+          __syncwarp();
+          // 32 rows x 32 columns: 16-byte chunks swizzled by row, read back 4 rows per store
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<float4*>(epi + lane * 32 + ((q ^ (lane & 7)) * 4)) =
+                make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), qq = lane & 7;
+            const float4 v = *reinterpret_cast<const float4*>(epi + r * 32 + ((qq ^ (r & 7)) * 4));
+            *reinterpret_cast<float4*>(dst0 + (int64_t)r * D + c + qq * 4) = v;
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar(Ly::B_OFREE + t));
+        ++uses;
+      }
+      prm.part_lse[prow] = valid ? lse : -INFINITY;
+    }
+  } else {
+    regs_dec<OTHER_REGS>();
+    if (warp == WARP_MMA) {
+      // ================================================================ MMA issuer
+      // The whole warp runs this loop converged; tcgen05.mma and tcgen05.commit are issued by
+      // one elected lane (tc_*_warp), every wait is warp-uniform (mbar_wait_warp).
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(BM, BN, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, true);
+      // Base descriptors are built once; per instruction only the start-address field (the
+      // low 14 bits, address / 16) advances by a compile-time offset.
+      const uint64_t q_desc0 = smem_desc_sw128(sb + Ly::Q_OFF, 16u, 1024u);
+      const uint64_t k_desc0 = smem_desc_sw128(sb + Ly::K_OFF, 16u, 1024u);
+      const uint64_t v_desc0 = smem_desc_sw128(sb + Ly::V_OFF, Ly::BOX, 1024u);
+      constexpr uint64_t TILE16 = Ly::TILE >> 4, BOX16 = Ly::BOX >> 4;
+      // K-major operand (Q or K): K-step kk of 16 elements sits in box kk/4 at byte 32*(kk%4)
+      auto kmaj_off = [](int kk) { return (uint64_t)((kk >> 2) * BOX16 + (kk & 3) * 2); };
+      // MN-major V: K-step kk covers key rows 16kk..16kk+15 (two 8-row swizzle atoms, 2048
+      // bytes); the second 64-column half of d is the next box (leading byte offset)
+      auto issue_s = [&](int t, int stage) {
+        const uint64_t qd = q_desc0 + (uint64_t)t * TILE16;
+        const uint64_t kd = k_desc0 + (uint64_t)stage * TILE16;
+        const uint32_t d_tm = tmem + (uint32_t)(t * 128);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) tc_mma_ss_warp(d_tm, qd + kmaj_off(kk), kd + kmaj_off(kk), idesc_qk, kk > 0);
+        tc_commit_warp(bar(Ly::B_SFULL + t));
+      };
+      auto issue_pv = [&](int t, int stage, bool first) {
+        const uint64_t vd = v_desc0 + (uint64_t)stage * TILE16;
+        const uint32_t tm_p = tmem + (uint32_t)(t * 128);
+        const uint32_t tm_o = tmem + 256u + (uint32_t)(t * 128);
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          tc_mma_ts_warp(tm_o, tm_p + (uint32_t)(kk * 8), vd + (uint64_t)(kk * 128), idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      };
+      int nu = 0, nq = 0, nblk = 0;
+      int cnt[2] = {0, 0}, uses[2] = {0, 0};
+      bool ok = true;
+      while (ok) {
+        const int slot = nu & 1;
+        ok = mbar_wait_warp(bar(Ly::B_UFULL + slot), (uint32_t)((nu >> 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                            ROLE_MMA, -1);
+        if (!ok) break;
+        const Unit x = get_unit(ring + 16 * slot);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Ly::B_UEMPTY + slot));
+        __syncwarp();
+        ++nu;
+        const int u = x.u;
+        if (u < 0) break;
+        const int NB = x.NB;
+        if (NB == 0 || x.n_tok == 0) continue;
+        const int ntiles = x.ntiles(prm.tt);
+        const int uidx = nq++;
+        ok = mbar_wait_warp(bar(Ly::B_QFULL), (uint32_t)(uidx & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_MMA, u);
+        if (ok)
+          ok = mbar_wait_warp(bar(Ly::B_KFULL + nblk % NST), (uint32_t)((nblk / NST) & 1), prm.wait_limit_ns, abort_flag,
+                              prm.status, ROLE_MMA, u);
+        if (!ok) break;
+        tc_fence_after();
+        for (int t = 0; t < ntiles; ++t) issue_s(t, nblk % NST);
+        if (NB == 1) tc_commit_warp(bar(Ly::B_QEMPTY));
+        tc_commit_warp(bar(Ly::B_KEMPTY + nblk % NST));
+        for (int j = 0; j < NB && ok; ++j) {
+          const int g = nblk + j;
+          const int st = g % NST;
+          ok = mbar_wait_warp(bar(Ly::B_VFULL + st), (uint32_t)((g / NST) & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                              ROLE_MMA, u);
+          if (PAGED && ok) {
+            // the last token's page may go on behind it, with whatever an earlier owner left: zeros there
+            const int r0 = x.len - (x.blk0 + j) * BN;
+            if (r0 < BN) {
+              const int r1 = min(BN, (r0 + prm.box_rows - 1) / prm.box_rows * prm.box_rows);
+              uint8_t* vs = smem + Ly::V_OFF + (uint32_t)st * Ly::TILE;
+              for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  *reinterpret_cast<uint4*>(vs + (uint32_t)c * Ly::BOX + (uint32_t)i * 16u) = make_uint4(0u, 0u, 0u, 0u);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+            }
+          }
+          for (int t = 0; t < ntiles && ok; ++t) {
+            ok = mbar_wait_warp(bar(Ly::B_PFULL + t), (uint32_t)(cnt[t] & 1), prm.wait_limit_ns, abort_flag, prm.status,
+                                ROLE_MMA, u);
+            if (ok && j == 0 && uses[t] > 0)  // the previous unit's epilogue has copied O_t out
+              ok = mbar_wait_warp(bar(Ly::B_OFREE + t), (uint32_t)((uses[t] - 1) & 1), prm.wait_limit_ns, abort_flag,
+                                  prm.status, ROLE_MMA, u);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(t, st, j == 0);
+            ++cnt[t];
+            if (j + 1 == NB) {  // tile t's last product of the unit: its epilogue may start
+              tc_commit_warp(bar(Ly::B_OFINAL + t));
+              ++uses[t];
+            }
+            if (j + 1 < NB) {
+              const int sn = (g + 1) % NST;
+              if (t == 0) {
+                ok = mbar_wait_warp(bar(Ly::B_KFULL + sn), (uint32_t)(((g + 1) / NST) & 1), prm.wait_limit_ns, abort_flag,
+                                    prm.status, ROLE_MMA, u);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              issue_s(t, sn);
+            }
+          }
+          if (!ok) break;
+          if (j + 1 < NB) tc_commit_warp(bar(Ly::B_KEMPTY + (g + 1) % NST));
+          if (j + 2 == NB) tc_commit_warp(bar(Ly::B_QEMPTY));  // the unit's last S products are issued
+          tc_commit_warp(bar(Ly::B_VEMPTY + st));
+        }
+        if (!ok) break;
+        nblk += NB;
+      }
+      // exit-path drain: every MMA issued completes before TMEM is freed
+      tc_commit_warp(bar(Ly::B_DRAIN));
+      mbar_drain(bar(Ly::B_DRAIN), 0u, DRAIN_NS);
+    } else if (warp == WARP_LOAD) {
+      // ================================================================ producer: the whole warp, converged
+      int nu = 0, nq = 0, nk = 0;
+      bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
+      Unit next;
+      // a CTA's first unit is its own index, the others come from the counter; decoded and published to the consumers' ring
+      auto publish = [&]() {
+        const int slot = nu & 1;
+        ok = mbar_wait_warp(bar(Ly::B_UEMPTY + slot), (uint32_t)(((nu >> 1) & 1) ^ 1), prm.wait_limit_ns, abort_flag,
+                            prm.status, ROLE_LOAD, -1);
+        if (!ok) return;
+        int v = (int)blockIdx.x;
+        if (nu > 0) {
+          v = prm.n_units;
+          if (prm.n_units > (int)gridDim.x) {
+            if (lane == 0) v = (int)(gridDim.x + atomicAdd(prm.counter, 1u));
+            v = __shfl_sync(0xffffffffu, v, 0);
+          }
+        }
+        if (v < prm.n_units) {
+          next = decode<PAGED>(v, prm, true);
+        } else {
+          next.u = -1;
+        }
+        if (lane == 0) {
+          put_unit(ring + 16 * slot, next);
+          mbar_arrive(bar(Ly::B_UFULL + slot));
+        }
+        __syncwarp();
+        ++nu;
+      };
+      // this lane's box of a block: 64-column half `bc`, rows [br, br + box_rows)
+      const int n_box = (D / 64) * (BN / prm.box_rows);
+      const int bc = lane % (D / 64), br = lane / (D / 64) * prm.box_rows;
+      // where that box of block jb lies: {row, page or batch}
+      auto where = [&](const Unit& x, int jb, int& r, int& p) {
+        const int key = jb * BN + br;
+        if (!PAGED) {
+          r = key;
+          p = x.b;
+          return;
+        }
+        r = 0;
+        p = prm.n_pages;  // no such page: zeros
+        if (lane < n_box && key < x.len) {
+          const int at = key / prm.page;
+          r = key - at * prm.page;
+          p = prm.table[x.b * prm.table_s + at];
+          if (p < 0 || p >= prm.n_pages) {
+            record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_PAGE, x.b);
+            p = prm.n_pages;
+          }
+        }
+      };
+      if (ok) publish();
+      while (ok && next.u >= 0) {
+        const Unit x = next;
+        publish();  // the following unit
+        if (!ok) break;
+        if (x.NB == 0 || x.n_tok == 0) continue;
+        // Q tiles: the previous unit's last S products must be done with the Q buffer
+        ok = mbar_wait_warp(bar(Ly::B_QEMPTY), (uint32_t)((nq & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
+                            ROLE_LOAD, x.u);
+        if (!ok) break;
+        const int ntiles = x.ntiles(prm.tt);
+        if (lane == 0) mbar_expect_tx(bar(Ly::B_QFULL), (uint32_t)(ntiles * prm.gh * prm.tt) * D * 2u);
+        __syncwarp();
+        if (lane < ntiles * (D / 64)) {
+          const int t = lane / (D / 64), c = lane % (D / 64);
+          tma_load_3d(sb + Ly::Q_OFF + (uint32_t)t * Ly::TILE + (uint32_t)c * Ly::BOX, &tmQ, c * 64,
+                      x.row0 + x.tok0 + t * prm.tt, (PAGED ? 0 : x.b * prm.Hq) + x.h0, bar(Ly::B_QFULL));
+        }
+        ++nq;
+        int r, p;
+        where(x, x.blk0, r, p);
+        for (int jb = x.blk0; jb < x.blk0 + x.NB; ++jb) {
+          const int st = nk % NST;
+          const uint32_t ph = (uint32_t)((nk / NST) & 1);
+          const int r0 = r, p0 = p;
+          if (jb + 1 < x.blk0 + x.NB) where(x, jb + 1, r, p);
+          ok = mbar_wait_warp(bar(Ly::B_KEMPTY + st), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, x.u);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(bar(Ly::B_KFULL + st), Ly::TILE);
+          __syncwarp();
+          const uint32_t at = (uint32_t)st * Ly::TILE + (uint32_t)bc * Ly::BOX + (uint32_t)br * 128u;
+          if (lane < n_box) tma_load_4d(sb + Ly::K_OFF + at, &tmK, bc * 64, r0, x.hk, p0, bar(Ly::B_KFULL + st));
+          ok = mbar_wait_warp(bar(Ly::B_VEMPTY + st), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, x.u);
+          if (!ok) {  // K's block is on its way, V's is not
+            mbar_drain(bar(Ly::B_KFULL + st), ph, DRAIN_NS);
+            break;
+          }
+          if (lane == 0) mbar_expect_tx(bar(Ly::B_VFULL + st), Ly::TILE);
+          __syncwarp();
+          if (lane < n_box) tma_load_4d(sb + Ly::V_OFF + at, &tmV, bc * 64, r0, x.hk, p0, bar(Ly::B_VFULL + st));
+          ++nk;
+        }
+      }
+      // exit-path drain: every load issued lands before the CTA exits
+      __syncwarp();
+      if (nq > 0) mbar_drain(bar(Ly::B_QFULL), (uint32_t)((nq - 1) & 1), DRAIN_NS);
+      for (int jj = (nk > NST ? nk - NST : 0); jj < nk; ++jj) {
+        mbar_drain(bar(Ly::B_KFULL + jj % NST), (uint32_t)((jj / NST) & 1), DRAIN_NS);
+        mbar_drain(bar(Ly::B_VFULL + jj % NST), (uint32_t)((jj / NST) & 1), DRAIN_NS);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// O = sum_t w_t O_t over a unit's parts, w_t = exp(lse_t - lse), and the LSE.  A thread takes a 16-byte piece of a row,
+// all parts' loads in flight together; a CTA a few rows, so that the few units there are still fill the GPU.
+constexpr int MERGE_THREADS = 256;
+template <int D>
+constexpr int MERGE_ROWS = MERGE_THREADS / (D / 4);
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_constant__ Params prm) {
+  constexpr int Q4 = D / 4, ROWS = MERGE_ROWS<D>, PER_UNIT = 2 * BM / ROWS;
+  wait_for_kernel_before();
+  if (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) return;
+  const int i = (int)blockIdx.x / PER_UNIT;  // unit before the cut
+  const int r = (int)blockIdx.x % PER_UNIT * ROWS + (int)threadIdx.x / Q4, c = (int)threadIdx.x % Q4 * 4;
+  const Unit x = decode<PAGED>(i * prm.parts, prm, false);
+  const int t = r / BM, row = r % BM, row_h = row / prm.tt, row_t = row - row_h * prm.tt;
+  const int tok = x.tok0 + t * prm.tt + row_t, h = x.h0 + row_h;
+  if (!(row_h < prm.gh && h < x.h_end && tok < x.n_tok)) return;
+  const int64_t base = ((int64_t)i * prm.parts * 2 + t) * BM + row;  // row of part k: base + 2 k BM
+  float w[MAX_PARTS];
+  float4 v[MAX_PARTS];
+  float M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k) {
+    w[k] = k < prm.parts ? prm.part_lse[base + (int64_t)2 * k * BM] : -INFINITY;
+    M = fmaxf(M, w[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k)
+    v[k] = w[k] != -INFINITY ? __ldcs(reinterpret_cast<const float4*>(prm.part_o + (base + (int64_t)2 * k * BM) * D + c))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float Ms = M == -INFINITY ? 0.f : M;
+  float W = 0.f;
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k) {
+    w[k] = __expf(w[k] - Ms);
+    W += w[k];
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;  // a NaN sum stays NaN
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k) {
+    const float f = w[k] * inv;
+    o.x = fmaf(f, v[k].x, o.x);
+    o.y = fmaf(f, v[k].y, o.y);
+    o.z = fmaf(f, v[k].z, o.z);
+    o.w = fmaf(f, v[k].w, o.w);
+  }
+  const int64_t bo = PAGED ? 0 : x.b, to = (int64_t)x.row0 + tok;
+  *reinterpret_cast<uint2*>(prm.o + bo * prm.os[0] + h * prm.os[1] + to * prm.os[2] + c) =
+      make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (c == 0) prm.lse[bo * prm.ls[0] + h * prm.ls[1] + to * prm.ls[2]] = W == 0.f ? -INFINITY : Ms + logf(W);
+}
+
+// ------------------------------------------------------------------ host side
+template <int D, int MODE, bool PAGED>
+static int launch_mode(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& prm, int sms,
+                       cudaStream_t st, std::string* err) {
+  auto kern = fwd_kernel<D, MODE, PAGED>;
+  static OncePerDevice once;
+  const int dev = OncePerDevice::device();
+  cudaError_t e = cudaSuccess;
+  if (once.pending(dev)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Layout<D>::ALLOC);
+    // a warpgroup that raises its registers beyond what the launch has would wait for ever
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && fa.numRegs * NUM_THREADS < 2 * 128 * SOFTMAX_REGS + 128 * OTHER_REGS) {
+      *err = "score forward built with " + std::to_string(fa.numRegs) +
+             " registers a thread, fewer than its warpgroups' register split needs";
+      return (int)cudaErrorInvalidConfiguration;
+    }
+    if (e == cudaSuccess) once.mark(dev);
+  }
+  // with a CTA for every unit the counter is not read
+  if (e == cudaSuccess && prm.n_units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
+  if (e != cudaSuccess) {
+    *err = std::string("score_fwd: ") + cudaGetErrorString(e);
+    return (int)e;
+  }
+  const unsigned grid = (unsigned)std::min<int64_t>(prm.n_units, sms);  // persistent: one CTA per SM
+  e = launch_behind(kern, dim3(grid), NUM_THREADS, Layout<D>::ALLOC, st, mq, mk, mv, prm);
+  if (e == cudaSuccess && prm.parts > 1)
+    e = launch_behind(merge_kernel<D, PAGED>, dim3((unsigned)(prm.n_units / prm.parts * (2 * BM / MERGE_ROWS<D>))),
+                      MERGE_THREADS, 0, st, prm);
+  if (e != cudaSuccess) *err = std::string("score_fwd launch: ") + cudaGetErrorString(e);
+  return (int)e;
+}
+
+template <int D, bool PAGED>
+static int launch(const ScoreFwdArgs& a, const ScoreFwdShape& z, int sms, cudaStream_t st, std::string* err) {
+  Params prm{};
+  prm.slopes = a.slopes;
+  prm.o = static_cast<__nv_bfloat16*>(a.o);
+  prm.lse = a.lse;
+  if (PAGED) {
+    prm.os[1] = D, prm.os[2] = (int64_t)a.Hq * D;
+    prm.ls[1] = 1, prm.ls[2] = a.Hq;
+  } else {
+    prm.os[0] = (int64_t)a.Hq * a.S * D, prm.os[1] = a.S * D, prm.os[2] = D;
+    prm.ls[0] = (int64_t)a.Hq * a.S, prm.ls[1] = a.S, prm.ls[2] = 1;
+  }
+  prm.part_o = reinterpret_cast<float*>(a.ws + z.part_o);
+  prm.part_lse = reinterpret_cast<float*>(a.ws + z.part_lse);
+  prm.status = a.status;
+  prm.counter = reinterpret_cast<uint32_t*>(a.ws + z.counter);
+  prm.lo = a.lo;
+  prm.hi = a.hi;
+  prm.mask_bs = a.mask_bs;
+  prm.offsets = a.offsets;
+  prm.lens = a.lens;
+  prm.table = a.table;
+  prm.table_s = a.table_s;
+  prm.S = a.S;
+  prm.N = a.N;
+  prm.B = a.B;
+  prm.Hq = a.Hq;
+  prm.Hkv = a.Hkv;
+  prm.g = a.Hq / a.Hkv;
+  prm.gh = z.gh;
+  prm.tt = z.tt;
+  prm.hc = z.hc;
+  prm.groups = z.groups;
+  prm.lanes = z.lanes;
+  prm.parts = z.parts;
+  const int64_t units = (int64_t)z.lanes * z.groups * z.parts;
+  if (units > 0x3fffffff) {
+    *err = "too many work units for one launch";
+    return (int)cudaErrorInvalidConfiguration;
+  }
+  prm.n_units = (int32_t)units;
+  // lanes numbered together: enough for about three times the grid, so that the last units are short where lengths differ
+  prm.batch = (int32_t)std::min<int64_t>(z.lanes, (3LL * sms + z.groups - 1) / z.groups);
+  prm.n_pages = a.n_pages;
+  prm.page = a.page;
+  prm.max_pages = a.max_pages;
+  prm.max_new = a.max_new;
+  prm.window = a.window;
+  prm.box_rows = BN;
+  if (PAGED)
+    while (a.page % prm.box_rows != 0) prm.box_rows /= 2;
+  prm.scale = a.scale;
+  prm.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  prm.cap_log2 = (float)((double)a.cap * 1.4426950408889634);
+  prm.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  prm.wait_limit_ns = a.wait_limit_ns;
+  CUtensorMap mq, mk, mv;
+  bool ok;
+  if (PAGED) {
+    const uint64_t qd[3] = {D, (uint64_t)a.N, (uint64_t)a.Hq};
+    const int64_t qst[2] = {a.qs[0], a.qs[1]};
+    const uint64_t kd[4] = {D, (uint64_t)a.page, (uint64_t)a.Hkv, (uint64_t)a.n_pages};
+    const int64_t kst[3] = {a.ks[2], a.ks[1], a.ks[0]}, vst[3] = {a.vs[2], a.vs[1], a.vs[0]};
+    const uint32_t qb[3] = {64, (uint32_t)z.tt, (uint32_t)z.gh}, kb[4] = {64, (uint32_t)prm.box_rows, 1, 1};
+    ok = encode_bf16_map(&mq, a.q, 3, qd, qst, qb, err) && encode_bf16_map(&mk, a.k, 4, kd, kst, kb, err) &&
+         encode_bf16_map(&mv, a.v, 4, kd, vst, kb, err);
+  } else {
+    const uint64_t qd[3] = {D, (uint64_t)a.S, (uint64_t)a.B * a.Hq};
+    const int64_t qst[2] = {D, a.S * D};
+    const uint64_t kd[4] = {D, (uint64_t)a.S, (uint64_t)a.Hkv, (uint64_t)a.B};
+    const int64_t kst[3] = {D, a.S * D, (int64_t)a.Hkv * a.S * D};
+    const uint32_t qb[3] = {64, (uint32_t)z.tt, (uint32_t)z.gh}, kb[4] = {64, BN, 1, 1};
+    ok = encode_bf16_map(&mq, a.q, 3, qd, qst, qb, err) && encode_bf16_map(&mk, a.k, 4, kd, kst, kb, err) &&
+         encode_bf16_map(&mv, a.v, 4, kd, kst, kb, err);
+  }
+  if (!ok) return (int)cudaErrorInvalidValue;
+  if (a.cap > 0.f) return launch_mode<D, 2, PAGED>(mq, mk, mv, prm, sms, st, err);
+  if (a.slopes) return launch_mode<D, 1, PAGED>(mq, mk, mv, prm, sms, st, err);
+  return launch_mode<D, 0, PAGED>(mq, mk, mv, prm, sms, st, err);
+}
+
+}  // namespace sfw
+}  // namespace mesh

@@ -1,0 +1,10 @@
+// The forward of score_fwd.cuh for heads of 64 columns, of dense batches.
+#include "score_fwd.cuh"
+
+namespace mesh {
+
+int launch_score_fwd_64(const ScoreFwdArgs& a, const ScoreFwdShape& z, int sms, cudaStream_t st, std::string* err) {
+  return sfw::launch<64, false>(a, z, sms, st, err);
+}
+
+}  // namespace mesh
