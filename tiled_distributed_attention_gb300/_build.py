@@ -26,7 +26,7 @@ SOURCES = ["planner.cpp", "abi.cu", "tile_fwd_tc.cu", "tile_fwd_tc32.cu", "merge
            "tile_bwd_simt.cu", "tile_bwd_tc.cu", "bwd_aux.cu", "rope.cu", "diff_abi.cu", "diff_aux.cu", "diff_fwd_tc.cu",
            "diff_bwd_tc.cu", "diff_bwd_tc32.cu", "diff_decode.cu", "paged_append.cu", "paged_rows.cu", "score_abi.cu",
            "score_fwd.cu", "score_fwd_64.cu", "score_fwd_128.cu", "score_fwd_paged_64.cu", "score_fwd_paged_128.cu",
-           "score_simt.cu"]
+           "score_bwd.cu", "score_bwd_64.cu", "score_bwd_128.cu", "score_simt.cu"]
 
 
 def nvcc() -> str:

@@ -41,7 +41,8 @@ size_t paged_rows_slots();
 int launch_paged_rows(const PagedArgs& a, int sms, cudaStream_t st, std::string* err);
 
 // fp32, any rows: on the CUDA cores.
-int launch_paged_simt(const PagedArgs& a, cudaStream_t st, std::string* err);
+int launch_paged_simt(const PagedArgs& a, int sms, cudaStream_t st, std::string* err);
+size_t score_simt_workspace(int32_t d);  // of it, and of the fp32 forward of range-masked attention
 
 struct RangeArgs {
   bool bf16;
@@ -66,6 +67,6 @@ struct RangeArgs {
   int64_t wait_limit_ns;
 };
 // fp32, on the CUDA cores.
-int launch_range_fwd_simt(const RangeArgs& a, cudaStream_t st, std::string* err);
+int launch_range_fwd_simt(const RangeArgs& a, int sms, cudaStream_t st, std::string* err);
 
 }  // namespace mesh

@@ -9,6 +9,7 @@
 #include "abi_util.h"
 #include "internal.h"
 #include "paged.h"
+#include "score_bwd.h"
 #include "score_fwd.h"
 
 namespace mesh {
@@ -18,14 +19,15 @@ static bool few_rows(bool bf16, int64_t rows) { return rows <= (bf16 ? 16 : 8); 
 
 static size_t paged_workspace(bool bf16, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t max_new) {
   size_t need = paged_rows_slots();
-  if (bf16 && !few_rows(bf16, max_new * (Hq / Hkv))) need = std::max(need, score_fwd_paged_workspace(N, B, Hq, Hkv, d));
+  if (!few_rows(bf16, max_new * (Hq / Hkv)))
+    need = std::max(need, bf16 ? score_fwd_paged_workspace(N, B, Hq, Hkv, d) : score_simt_workspace(d));
   return PAGED_WS_HEAD + need;
 }
 
-// Workspace of the range-masked calls (bytes from its start): the forward's counter and parts.
+// Workspace of the range-masked calls, of one direction after the other.
 static size_t range_workspace(bool bf16, int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d, bool backward, int sms) {
-  (void)backward;
-  return bf16 ? score_fwd_shape(false, S, 0, B, Hq, Hkv, d, sms).total : 256;
+  if (backward) return range_bwd_shape(bf16, S, B, Hq, Hkv, d, sms).total;
+  return bf16 ? score_fwd_shape(false, S, 0, B, Hq, Hkv, d, sms).total : score_simt_workspace(d);
 }
 
 }  // namespace mesh
@@ -161,7 +163,7 @@ extern "C" int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     std::string err;
     if (mesh::few_rows(bf16, max_new * (Hq / Hkv))) return launch_status(mesh::launch_paged_rows(a, sms, st, &err), err);
-    if (!bf16) return launch_status(mesh::launch_paged_simt(a, st, &err), err);
+    if (!bf16) return launch_status(mesh::launch_paged_simt(a, sms, st, &err), err);
     mesh::ScoreFwdArgs f{};
     f.paged = true;
     f.q = q;
@@ -205,7 +207,8 @@ extern "C" int mesh_attn_range_workspace_size(mesh_attn_dtype dtype, int32_t B, 
     size_t most = 256;
     if (B > 0 && Hq > 0 && S > 0)
       for (int sms = 1; sms <= mesh::MAX_SMS; ++sms)
-        most = std::max(most, mesh::range_workspace(dtype == MESH_ATTN_BF16, B, Hq, Hkv, S, d, backward, sms));
+        for (int dir = 0; dir <= backward; ++dir)
+          most = std::max(most, mesh::range_workspace(dtype == MESH_ATTN_BF16, B, Hq, Hkv, S, d, dir != 0, sms));
     *bytes = most;
     return (int)MESH_ATTN_OK;
   });
@@ -246,7 +249,7 @@ extern "C" int mesh_attn_range_fwd(mesh_attn_dtype dtype, int32_t B, int32_t Hq,
     if (const int rc = check_range_args(a, workspace, workspace_bytes, false, &sms)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     std::string err;
-    if (!a.bf16) return launch_status(mesh::launch_range_fwd_simt(a, st, &err), err);
+    if (!a.bf16) return launch_status(mesh::launch_range_fwd_simt(a, sms, st, &err), err);
     mesh::ScoreFwdArgs f{};
     f.q = Q, f.k = K, f.v = V, f.slopes = slopes, f.o = O, f.lse = LSE, f.status = d_status, f.ws = a.ws;
     f.S = S, f.B = B, f.Hq = Hq, f.Hkv = Hkv, f.d = d, f.lo = lo, f.hi = hi, f.mask_bs = mask_stride;
@@ -255,13 +258,28 @@ extern "C" int mesh_attn_range_fwd(mesh_attn_dtype dtype, int32_t B, int32_t Hq,
   });
 }
 
-extern "C" int mesh_attn_range_bwd(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d, const void*,
-                                   const void*, const void*, const int32_t*, const int32_t*, int64_t, const float*, const void*,
-                                   const float*, const void*, float scale, float cap, void*, void*, void*, void*, size_t, int32_t*,
-                                   void*) {
+extern "C" int mesh_attn_range_bwd(mesh_attn_dtype dtype, int32_t B, int32_t Hq, int32_t Hkv, int64_t S, int32_t d, const void* Q,
+                                   const void* K, const void* V, const int32_t* lo, const int32_t* hi, int64_t mask_stride,
+                                   const float* slopes, const void* O, const float* LSE, const void* dO, float scale, float cap,
+                                   void* dQ, void* dK, void* dV, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                                   void* stream) {
   return mesh::guarded_call([&]() -> int {
     if (const int rc = check_range_sizes(dtype, B, Hq, Hkv, S, d)) return rc;
-    if (const int rc = check_score(scale, cap)) return rc;
-    return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "the backward pass is not built yet");
+    if (B == 0 || Hq == 0 || S == 0) return check_score(scale, cap);
+    mesh::RangeArgs a{};
+    a.bf16 = dtype == MESH_ATTN_BF16;
+    a.q = Q, a.k = K, a.v = V, a.lo = lo, a.hi = hi, a.mask_bs = mask_stride, a.slopes = slopes;
+    a.o = const_cast<void*>(O), a.lse = const_cast<float*>(LSE), a.go = dO, a.dq = dQ, a.dk = dK, a.dv = dV;
+    a.ws = static_cast<char*>(workspace), a.status = d_status;
+    a.S = S, a.B = B, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.scale = scale, a.cap = cap;
+    a.wait_limit_ns = mesh::current_wait_limit_ns();
+    int sms = 0;
+    if (const int rc = check_range_args(a, workspace, workspace_bytes, true, &sms)) return rc;
+    const mesh::RangeBwdShape z = mesh::range_bwd_shape(a.bf16, S, B, Hq, Hkv, d, sms);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    std::string err;
+    if (!a.bf16) return launch_status(mesh::launch_range_bwd_simt(a, z, st, &err), err);
+    return launch_status(d == 128 ? mesh::launch_range_bwd_128(a, z, sms, st, &err) : mesh::launch_range_bwd_64(a, z, sms, st, &err),
+                         err);
   });
 }
