@@ -27,6 +27,7 @@ RangeBwdShape range_bwd_shape(bool bf16, int64_t S, int32_t B, int32_t Hq, int32
     z.kv_parts = parts_for(nb * B * Hkv, nb * g, sms / 2);
     z.dq_parts = parts_for(nb * B * Hq, nb, sms / 2);
     z.bounds = take((size_t)B * nb * 16);
+    z.order = take((size_t)B * nb * 16);
   } else {
     const int64_t nb = (S + 63) / 64, tiles = (S * g + 63) / 64;
     z.kv_parts = parts_for(nb * B * Hkv, nb * g, sms);

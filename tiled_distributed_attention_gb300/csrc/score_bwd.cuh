@@ -72,10 +72,18 @@ struct alignas(16) Bounds {
   int32_t kb0, kb1, all_lo, all_hi;
 };
 
+// Up to so many blocks a row of the batch, prep_kernel also sorts them by length: [masks][nb] query blocks, the longest first, then
+// key blocks, and the query blocks [x, y) that see each key block.  Beyond, units are taken as a causal mask wants them: there are
+// many more than SMs.
+constexpr int ORDER_MAX = 512;
+
 struct Params {
   const float* lse;   // [B, Hq, S]
   const float* dsum;  // [B, Hq, S]
   const Bounds* bounds;  // [B or 1, nb]
+  const int32_t* order_q;  // [B or 1, nb], or NULL
+  const int32_t* order_kv;
+  const int2* seen_by;
   const int32_t* lo;
   const int32_t* hi;
   int64_t mask_bs;
@@ -92,7 +100,8 @@ struct Params {
   int64_t S;
   int32_t B, Hq, Hkv, g, nb;
   int32_t kv_units, dq_units, kv_ctas, dq_ctas, kv_parts, dq_parts, kv_batch, dq_batch;
-  float scale, scale_log2, cap_log2, inv_cap;
+  float scale, scale_log2;
+  Cap cap;
   int64_t wait_limit_ns;
 };
 
@@ -206,8 +215,8 @@ __device__ __forceinline__ void get_unit(const volatile int32_t* e, Unit& x) {
   x.u = e[0], x.blk = e[1], x.h = e[2], x.first = e[4], x.per = e[5], x.start = e[6], x.NB = e[7];
   x.b = e[3] & 0xffff, x.part = e[3] >> 16;
 }
-// Decoded by a whole warp.  Units are numbered batch of (batch, head) lanes by batch, within it block by block, causal masks'
-// longest first, within those lane by lane, its parts together.
+// Decoded by a whole warp.  Units are numbered batch of (batch, head) lanes by batch, within it block by block, the longest
+// first, within those lane by lane, its parts together.
 template <bool KV>
 __device__ __forceinline__ Unit unit_of(int u, const Params& prm) {
   const int lane = threadIdx.x & 31;
@@ -219,13 +228,25 @@ __device__ __forceinline__ Unit unit_of(int u, const Params& prm) {
   const int per = batch * prm.nb, first = t / per * batch;
   const int lanes = min(batch, prm.B * H - first);  // the last batch may be smaller
   t %= per;
-  x.blk = KV ? t / lanes : prm.nb - 1 - t / lanes;
+  const int idx = t / lanes;
   t = first + t % lanes;
   x.h = t % H;
   x.b = t / H;
-  const Bounds* bd = prm.bounds + (int64_t)x.b * prm.bounds_bs;
+  const int64_t mask = (int64_t)x.b * prm.bounds_bs;
   int lo = 0x7fffffff, hi = 0;
-  if (KV) {  // the query blocks from the first to the last that see key block blk
+  if (prm.order_q) {
+    x.blk = (KV ? prm.order_kv : prm.order_q)[mask + idx];
+  } else {
+    x.blk = KV ? idx : prm.nb - 1 - idx;
+  }
+  if (!KV) {
+    lo = prm.bounds[mask + x.blk].kb0;
+    hi = prm.bounds[mask + x.blk].kb1;
+  } else if (prm.order_q) {
+    lo = prm.seen_by[mask + x.blk].x;
+    hi = prm.seen_by[mask + x.blk].y;
+  } else {  // the query blocks from the first to the last that see key block blk
+    const Bounds* bd = prm.bounds + mask;
     for (int q = lane; q < prm.nb; q += 32)
       if (bd[q].kb0 <= x.blk && x.blk < bd[q].kb1) {
         lo = min(lo, q);
@@ -233,9 +254,6 @@ __device__ __forceinline__ Unit unit_of(int u, const Params& prm) {
       }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
-  } else {
-    lo = bd[x.blk].kb0;
-    hi = bd[x.blk].kb1;
   }
   x.first = lo < hi ? lo : 0;
   x.per = lo < hi ? hi - lo : 0;
@@ -261,11 +279,13 @@ struct Cursor {
   }
 };
 
-// 64 scores of consecutive columns to weights, MODE as in the forward (0 plain, 1 slopes, 2 cap, and slopes where given):
+// 64 scores of consecutive columns to weights, MODE 0 plain, 1 slopes, 2 cap (and slopes where given); `reload` fetches the scores
+// again for a higher tier of the cap:
 //   P = 2^(x + nl(c)), nl(c) being -LSE in base 2 of columns c and c + 1, and |i - j| = |c + off|.
 // Leaves P (1 - t^2) in s and, with PACK, P in bf16 pairs in pk.
-template <int MODE, bool PACK, typename F>
-__device__ __forceinline__ void weights(const Params& prm, float (&s)[64], uint32_t* pk, float slope2, int off, F&& nl) {
+template <int MODE, bool PACK, typename F, typename L>
+__device__ __forceinline__ void weights(const Params& prm, float (&s)[64], uint32_t* pk, float slope2, int off, int& tier, F&& nl,
+                                        L&& reload) {
   const uint64_t sc2 = f2_pack(prm.scale_log2, prm.scale_log2);
   const bool slopes = MODE == 1 || (MODE == 2 && prm.slopes);
   const float o = (float)off;
@@ -290,32 +310,16 @@ __device__ __forceinline__ void weights(const Params& prm, float (&s)[64], uint3
     }
     return;
   }
-  float um[4] = {0.f, 0.f, 0.f, 0.f};
+  cap_scores(prm.cap, s, tier, true, reload);
+  const uint64_t i2 = f2_pack(-prm.cap.inv2, -prm.cap.inv2), one = f2_pack(1.f, 1.f);
 #pragma unroll
-  for (int c = 0; c < 64; c += 2) um[(c >> 1) & 3] = max3f(um[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
-  const float zmax = fmaxf(max3f(um[0], um[1], um[2]), um[3]) * prm.inv_cap;
-  const uint64_t k2 = f2_pack(prm.inv_cap, prm.inv_cap), cl2 = f2_pack(prm.cap_log2, prm.cap_log2);
-  const uint64_t one = f2_pack(1.f, 1.f), minus = f2_pack(-1.f, -1.f);
-  if (__all_sync(0xffffffffu, zmax <= 1.f)) {
-#pragma unroll
-    for (int c = 0; c < 64; c += 2) {
-      const uint64_t z = f2_mul(f2_pack(s[c], s[c + 1]), k2), t = f2_mul(z, tanh_ratio2(f2_mul(z, z)));
-      float x0, x1;
-      f2_unpack(f2_fma(t, cl2, base(c)), x0, x1);
-      const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-      if (PACK) pk[c / 2] = pack_bf16x2(p0, p1);
-      f2_unpack(f2_mul(f2_pack(p0, p1), f2_fma(f2_mul(t, minus), t, one)), s[c], s[c + 1]);
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 64; c += 2) {
-      const uint64_t t = f2_pack(tanh_any(s[c] * prm.inv_cap), tanh_any(s[c + 1] * prm.inv_cap));
-      float x0, x1;
-      f2_unpack(f2_fma(t, cl2, base(c)), x0, x1);
-      const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-      if (PACK) pk[c / 2] = pack_bf16x2(p0, p1);
-      f2_unpack(f2_mul(f2_pack(p0, p1), f2_fma(f2_mul(t, minus), t, one)), s[c], s[c + 1]);
-    }
+  for (int c = 0; c < 64; c += 2) {
+    const uint64_t y = f2_pack(s[c], s[c + 1]);
+    float x0, x1;
+    f2_unpack(f2_add(y, base(c)), x0, x1);
+    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+    if (PACK) pk[c / 2] = pack_bf16x2(p0, p1);
+    f2_unpack(f2_mul(f2_pack(p0, p1), f2_fma(f2_mul(y, y), i2, one)), s[c], s[c + 1]);  // t = y / (cap log2 e)
   }
 }
 
@@ -429,6 +433,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
     if (ok) ok = take(x, ROLE_EW);
     int64_t g0 = 0;  // global index of the unit's first block
     int k_unit = 0;
+    int tier = 0;  // of the cap
     if constexpr (KV) {
       // ---------------------------------------------------------------- dK and dV
       float* nlse_s = reinterpret_cast<float*>(smem + Ly::VEC_OFF);  // [2][BM] -LSE log2 e of the query columns
@@ -490,15 +495,21 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           if (!ok) break;
           tc_fence_after();
           float pv[64];
-          tmem_ld32(tm_s, pv);
-          tmem_ld32(tm_s + 32u, pv + 32);
-          tc_wait_ld();
+          auto load_s = [&]() {
+            tmem_ld32(tm_s, pv);
+            tmem_ld32(tm_s + 32u, pv + 32);
+            tc_wait_ld();
+          };
+          load_s();
           const float* lv = nlse_s + vb * BM + c_base;
           uint32_t pk[32];
-          weights<MODE, true>(prm, pv, pk, slope2, qb * BM + c_base - (k0 + row), [&](int c) {
-            const float2 l2 = *reinterpret_cast<const float2*>(lv + c);
-            return f2_pack(l2.x, l2.y);
-          });
+          weights<MODE, true>(
+              prm, pv, pk, slope2, qb * BM + c_base - (k0 + row), tier,
+              [&](int c) {
+                const float2 l2 = *reinterpret_cast<const float2*>(lv + c);
+                return f2_pack(l2.x, l2.y);
+              },
+              load_s);
           if (edge) {
             const uint4* rv = reinterpret_cast<const uint4*>(rng_s + vb * BM + c_base);
 #pragma unroll
@@ -589,6 +600,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           }
         }
         ++k_unit;
+        tier = 0;
         g0 += NB;
         x = xn;
       }
@@ -628,11 +640,16 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           if (!ok) break;
           tc_fence_after();
           float pv[64];
-          tmem_ld32(tm_s, pv);
-          tmem_ld32(tm_s + 32u, pv + 32);
-          tc_wait_ld();
-          arrive(Ly::B_SREAD);  // S(g) is in registers: the next block's S may overwrite it
-          weights<MODE, false>(prm, pv, nullptr, slope2, k0 + c_base - q, [&](int) { return nl2; });
+          auto load_s = [&]() {
+            tmem_ld32(tm_s, pv);
+            tmem_ld32(tm_s + 32u, pv + 32);
+            tc_wait_ld();
+          };
+          load_s();
+          if (MODE < 2) arrive(Ly::B_SREAD);  // S(g) is in registers: the next block's S may overwrite it
+          weights<MODE, false>(prm, pv, nullptr, slope2, k0 + c_base - q, tier, [&](int) { return nl2; }, load_s);
+          // with a cap it may be read again until here (picking the tier by the scores' maximum first instead: 10 % slower)
+          if (MODE == 2) arrive(Ly::B_SREAD);
           if (all_lo > k0 || all_hi < k0 + BM) {
             const int a = lo - k0 - c_base, n = max(hi - lo, 0);
 #pragma unroll
@@ -665,6 +682,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         ok = take(xn, ROLE_EW);
         if (!ok) break;
         if (xn.u >= 0) fetch(xn);
+        tier = 0;
         g0 += x.NB;
         x = xn;
       }
@@ -1017,14 +1035,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     run_pass<D, MODE, false>(tmQ, tmG, tmK, tmV, prm, (int)blockIdx.x - prm.kv_ctas, prm.dq_ctas);
 }
 
-// D = dO . O by rows, the query blocks' bounds, and the unit counters at zero, in one launch: the first blocks of the grid take
-// a query block each (a warp's worth of work), the others 16-byte pieces of rows, D / 8 lanes a row.
+// D = dO . O by rows, the query blocks' bounds, the order of the blocks, and the unit counters at zero, in one launch: the first CTAs
+// of the grid take a mask each (beyond ORDER_MAX blocks: eight query blocks each), the others 16-byte pieces of rows, D / 8
+// lanes a row.
 constexpr int PREP_THREADS = 256;
 struct PrepParams {
   const uint4* o;
   const uint4* go;
   float* dsum;
   Bounds* bounds;
+  int32_t* order_q;  // or NULL
+  int32_t* order_kv;
+  int2* seen_by;
   const int32_t* lo;
   const int32_t* hi;
   uint32_t* counters;
@@ -1046,30 +1068,58 @@ template <int D>
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const __grid_constant__ PrepParams p) {
   wait_for_kernel_before();
   if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int WARPS = PREP_THREADS / 32;
   if ((int)blockIdx.x < p.bounds_blocks) {
+    __shared__ int2 see[ORDER_MAX], seen[ORDER_MAX];  // key blocks of a query block, and the other way round
     if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x * 64] = 0u;
-    const int i = (int)blockIdx.x * (PREP_THREADS / 32) + (int)(threadIdx.x >> 5);
-    if (i >= p.n_bounds) return;
-    const int m = i / p.nb, qb = i - m * p.nb;
-    int kmin = 0x7fffffff, kmax = 0, all_lo = 0, all_hi = 0x7fffffff;
+    const int first = p.order_q ? (int)blockIdx.x * p.nb : (int)blockIdx.x * WARPS;
+    const int end = p.order_q ? first + p.nb : min(first + WARPS, p.n_bounds);
+    for (int i = first + warp; i < end; i += WARPS) {
+      const int m = i / p.nb, qb = i - m * p.nb;
+      int kmin = 0x7fffffff, kmax = 0, all_lo = 0, all_hi = 0x7fffffff;
 #pragma unroll
-    for (int e = 0; e < BM / 32; ++e) {
-      const int64_t q = (int64_t)qb * BM + e * 32 + lane;
-      if (q >= p.S) continue;
-      const int a = max(p.lo[m * p.mask_bs + q], 0), z = (int)min((int64_t)p.hi[m * p.mask_bs + q], p.S);
-      if (a >= z) continue;
-      kmin = min(kmin, a), kmax = max(kmax, z);
-      all_lo = max(all_lo, a), all_hi = min(all_hi, z);
-    }
-    kmin = __reduce_min_sync(0xffffffffu, kmin);
-    kmax = __reduce_max_sync(0xffffffffu, kmax);
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-    if (lane == 0) {
+      for (int e = 0; e < BM / 32; ++e) {
+        const int64_t q = (int64_t)qb * BM + e * 32 + lane;
+        if (q >= p.S) continue;
+        const int a = max(p.lo[m * p.mask_bs + q], 0), z = (int)min((int64_t)p.hi[m * p.mask_bs + q], p.S);
+        if (a >= z) continue;
+        kmin = min(kmin, a), kmax = max(kmax, z);
+        all_lo = max(all_lo, a), all_hi = min(all_hi, z);
+      }
+      kmin = __reduce_min_sync(0xffffffffu, kmin);
+      kmax = __reduce_max_sync(0xffffffffu, kmax);
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
       Bounds b{0, 0, all_lo, all_hi};
       if (kmin < kmax) b.kb0 = kmin / BM, b.kb1 = (kmax + BM - 1) / BM;
-      p.bounds[i] = b;
+      if (lane == 0) {
+        p.bounds[i] = b;
+        if (p.order_q) see[qb] = make_int2(b.kb0, b.kb1);
+      }
+    }
+    if (!p.order_q) return;
+    __syncthreads();
+    for (int k = threadIdx.x; k < p.nb; k += PREP_THREADS) {
+      int a = 0, z = 0;
+      for (int q = 0; q < p.nb; ++q)
+        if (see[q].x <= k && k < see[q].y) {
+          if (z == 0) a = q;
+          z = q + 1;
+        }
+      seen[k] = make_int2(a, z);
+      p.seen_by[first + k] = seen[k];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.nb; i += PREP_THREADS) {
+      const int2* r = i < p.nb ? see : seen;
+      const int e = i < p.nb ? i : i - p.nb, n = r[e].y - r[e].x;
+      int rank = 0;
+      for (int j = 0; j < p.nb; ++j) {
+        const int m = r[j].y - r[j].x;
+        rank += m > n || (m == n && j < e);
+      }
+      (i < p.nb ? p.order_q : p.order_kv)[first + rank] = e;
     }
     return;
   }
@@ -1161,11 +1211,20 @@ static int launch(const RangeArgs& a, const RangeBwdShape& z, int sms, cudaStrea
   pp.nb = (int32_t)nb;
   pp.n_bounds = (int32_t)(nb * masks);
   pp.bounds_blocks = (pp.n_bounds + PREP_THREADS / 32 - 1) / (PREP_THREADS / 32);
+  if (nb <= ORDER_MAX) {
+    pp.order_q = reinterpret_cast<int32_t*>(a.ws + z.order);
+    pp.order_kv = pp.order_q + pp.n_bounds;
+    pp.seen_by = reinterpret_cast<int2*>(pp.order_kv + pp.n_bounds);
+    pp.bounds_blocks = (int32_t)masks;
+  }
   const int64_t prep_blocks = pp.bounds_blocks + (rows * (D / 8) + PREP_THREADS - 1) / PREP_THREADS;
   Params prm{};
   prm.lse = a.lse;
   prm.dsum = pp.dsum;
   prm.bounds = pp.bounds;
+  prm.order_q = pp.order_q;
+  prm.order_kv = pp.order_kv;
+  prm.seen_by = pp.seen_by;
   prm.lo = a.lo;
   prm.hi = a.hi;
   prm.mask_bs = a.mask_bs;
@@ -1196,8 +1255,7 @@ static int launch(const RangeArgs& a, const RangeBwdShape& z, int sms, cudaStrea
   prm.dq_batch = (int32_t)std::min<int64_t>((int64_t)a.B * a.Hq, (3LL * sms + nb - 1) / nb);
   prm.scale = a.scale;
   prm.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-  prm.cap_log2 = (float)((double)a.cap * 1.4426950408889634);
-  prm.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  prm.cap = make_cap(a.scale, a.cap);
   prm.wait_limit_ns = a.wait_limit_ns;
   CUtensorMap mq, mk, mv, mg;
   const uint64_t qd[3] = {D, (uint64_t)a.S, (uint64_t)a.B * a.Hq}, kd[3] = {D, (uint64_t)a.S, (uint64_t)a.B * a.Hkv};

@@ -14,7 +14,7 @@ namespace mesh {
 // Workspace of the backward pass (bytes from its start) and the parts that units are cut into.
 struct RangeBwdShape {
   int32_t kv_parts, dq_parts;
-  size_t counters, dsum, bounds, dq_part, dk_part, dv_part, total;
+  size_t counters, dsum, bounds, order, dq_part, dk_part, dv_part, total;
 };
 RangeBwdShape range_bwd_shape(bool bf16, int64_t S, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms);
 // bf16, by head size, one translation unit each

@@ -56,9 +56,11 @@ bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
 // Tiles.  All query heads of a KV head in one tile where they and their tokens fill it (3 heads: 42 tokens, 126 rows), else the
 // heads in the fewest equal chunks that do to 7/8.
 //
-// Parts.  Units come in waves of one an SM, each about as long as its blocks (1.6 us) and a fixed part of about
-// three blocks; parts cost a merge of about four blocks.  The count that makes the waves shortest by that measure, four an SM at
-// most; S bounds a unit's blocks, half of them where a causal mask may be meant.
+// Parts.  The longest unit has to be done, and the SMs share all blocks: a chunk's units see about as many each and go in whole waves,
+// those of a dense batch half of the longest on average, as under a causal mask.  A unit costs about three blocks besides
+// its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of their fp32 rows.  The best count is taken where it
+// saves a fifth or more: 8 units of 512 blocks go in 16 parts; 160 units of up to 20 blocks stay whole (40 us; 68 in 2 parts), and 128
+// of 512 (687 us; 726 in 8 parts).
 ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms) {
   ScoreFwdShape z{};
   const int g = Hq / Hkv;
@@ -74,13 +76,16 @@ ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32
   z.groups = (int32_t)std::min<int64_t>(groups, 0x7fffffff);
   z.lanes = (int32_t)std::min<int64_t>(lanes, 0x7fffffff);
   const int64_t units = lanes * (paged ? std::max<int64_t>(1, groups - (N % tu == 0 ? 1 : 0)) : groups);
-  const double nb = (double)((S + 127) / 128) * (paged ? 1.0 : 0.5);
+  const double nb = (double)((S + 127) / 128);
   z.parts = 1;
-  double best = 0;
+  double whole = 0, best = 0;
   for (int k = 1; k <= MAX_FWD_PARTS; ++k) {
     if (k > 1 && (nb / k < 2 || lanes * groups * k > FWD_PART_WAVES * sms)) break;
-    const double cost = (double)((units * k + sms - 1) / sms) * (nb / k + 3) + (k > 1 ? 4 : 0);
-    if (k == 1 || cost < 0.95 * best) {
+    const double own = nb / k + 3;
+    const double waves = paged ? (double)((units * k + sms - 1) / sms) * own : std::max(own, (double)units * (nb * 0.5 + 3 * k) / sms);
+    const double cost = waves + (k > 1 ? 4 + 0.02 * (double)units * k : 0);
+    if (k == 1) whole = best = cost;
+    if (cost < best && cost <= 0.8 * whole) {
       best = cost;
       z.parts = k;
     }

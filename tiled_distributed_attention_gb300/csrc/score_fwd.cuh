@@ -12,8 +12,8 @@
 // Rows see ranges: a warp masks a block only where it is not inside all of its rows' ranges, and a row that has met no key yet
 // takes no maximum pass for a block that it does not see.
 //
-// Cap (MODE 2).  tanh by a polynomial while |s q.k| <= cap in the whole warp and block (checked by the maximum of its
-// square), else by exponentials.  Slopes (MODE 1, and 2 where given): one more FMA where a block lies on one side of all of the
+// Cap (MODE 2, with slopes 3).  tanh by a polynomial while the whole warp's scores of a block stay below the cap, of fewer steps below
+// half of it, else by exponentials (score.cuh).  Slopes (MODE 1 and 3): one more FMA where a block lies on one side of all of the
 // warp's rows, |i - j| only on the diagonal.
 //
 // Pages.  A block's keys are boxes of as many rows as a page (a power of two that divides it, 16 to 128), one lane of the producer
@@ -80,7 +80,8 @@ struct Layout {
                        NBARS = B_DRAIN + 1;
   static constexpr uint32_t MISC_OFF = BAR_OFF + NBARS * 8 + (NBARS % 2) * 8;  // tmem base, abort flag
   static constexpr uint32_t RING_OFF = MISC_OFF + 16;  // unit ring: 2 decoded units, 16 ints each
-  static constexpr uint32_t TOTAL = RING_OFF + 2 * 64;
+  static constexpr uint32_t MINE_OFF = RING_OFF + 2 * 64;    // each softmax warp's unit, 16 ints
+  static constexpr uint32_t TOTAL = MINE_OFF + 8 * 64;
   static constexpr uint32_t ALLOC = TOTAL + 1024;
 };
 static_assert(Layout<128>::ALLOC <= 232448, "shared memory of a CTA");
@@ -105,7 +106,8 @@ struct Params {
   int64_t S;
   int32_t N, B, Hq, Hkv, g, gh, tt, hc, groups, lanes, batch, n_units, parts;
   int32_t n_pages, page, max_pages, max_new, window, box_rows;
-  float scale, scale_log2, cap_log2, inv_cap;  // cap log2 e, scale / cap
+  float scale_log2;
+  Cap cap;
   int64_t wait_limit_ns;
 };
 
@@ -114,6 +116,16 @@ struct Params {
 struct Unit {
   int u, b, hk, h0, h_end, tok0, n_tok, row0, pos0, len, blk0, NB, part;
   __device__ __forceinline__ int ntiles(int tt) const { return tok0 + tt < n_tok ? 2 : 1; }
+  // Its i-th block: from the one of its last token's own key down to the first, then up from behind it.  So rows meet their own key
+  // early, where a causal document or a slope has its largest weights, and the running maximum seldom grows (blocks from the first
+  // on: 352 us where this takes 219, 16 heads of 8,192 tokens with slopes).
+  __device__ __forceinline__ int mid(int tt) const {
+    return min(max((pos0 + min(tok0 + 2 * tt, n_tok) - 1) / BN, blk0), blk0 + NB - 1);
+  }
+  __device__ __forceinline__ int block(int i, int tt) const {
+    const int m = mid(tt);
+    return i <= m - blk0 ? m - i : blk0 + i;
+  }
 };
 __device__ __forceinline__ void put_unit(volatile int32_t* e, const Unit& x) {
   e[0] = x.u, e[1] = x.b, e[2] = x.hk, e[3] = x.h0, e[4] = x.h_end, e[5] = x.tok0, e[6] = x.n_tok, e[7] = x.row0;
@@ -126,12 +138,12 @@ __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   return x;
 }
 
-// Unit u of a launch, decoded by a whole warp: numbered batch of lanes by batch, within it from the last tokens (the
+// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone): numbered batch of lanes by batch, within it from the last tokens (the
 // most keys where the mask is causal) to the first, within those lane by lane, its parts together.  A lane is a (batch, KV head,
 // chunk of heads); paged: a (KV head, chunk), whose groups are those of all sequences, sequence b's from
 // offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
 template <bool PAGED>
-__device__ __forceinline__ Unit decode(int u, const Params& prm, bool report) {
+__device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
   Unit x;
   const int lane = threadIdx.x & 31, tu = 2 * prm.tt;
   x.u = u;
@@ -174,7 +186,7 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool report) {
     const int64_t most = (int64_t)prm.max_pages * prm.page;
     x.len = (int32_t)min((int64_t)max(len, x.n_tok), most);
     // what does not fit is recorded and taken as the nearest that does
-    if (report && lane == 0 && (x.row0 != o0 || x.n_tok != o1 - o0 || x.len != len))
+    if (bounds && lane == 0 && (x.row0 != o0 || x.n_tok != o1 - o0 || x.len != len))
       record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, x.b);
     x.n_tok = min(x.n_tok, x.len);
     x.pos0 = x.len - x.n_tok;
@@ -183,6 +195,7 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool report) {
       x.n_tok = 0;
       return x;
     }
+    if (!bounds) return x;
     kmax = x.pos0 + min(x.tok0 + tu, x.n_tok);
     kmin = prm.window ? max(0, x.pos0 + x.tok0 + 1 - prm.window) : 0;
   } else {
@@ -190,16 +203,26 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool report) {
     x.n_tok = (int)prm.S;
     x.row0 = x.pos0 = 0;
     x.len = (int)prm.S;
+    if (!bounds) return x;
     const int32_t* lo = prm.lo + x.b * prm.mask_bs;
     const int32_t* hi = prm.hi + x.b * prm.mask_bs;
-    for (int i = lane; i < tu; i += 32)
-      if (x.tok0 + i < x.n_tok) {
-        const int a = max(lo[x.tok0 + i], 0), z = min(hi[x.tok0 + i], x.len);
-        if (a < z) {
-          kmin = min(kmin, a);
-          kmax = max(kmax, z);
-        }
+    int a[2 * BM / 32], z[2 * BM / 32];  // all loads in flight together
+#pragma unroll
+    for (int e = 0; e < 2 * BM / 32; ++e) {
+      const int i = e * 32 + lane;
+      const bool in = i < tu && x.tok0 + i < x.n_tok;
+      a[e] = in ? lo[x.tok0 + i] : 0;
+      z[e] = in ? hi[x.tok0 + i] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 2 * BM / 32; ++e) {
+      a[e] = max(a[e], 0);
+      z[e] = min(z[e], x.len);
+      if (a[e] < z[e]) {
+        kmin = min(kmin, a[e]);
+        kmax = max(kmax, z[e]);
       }
+    }
     kmin = __reduce_min_sync(0xffffffffu, kmin);
     kmax = __reduce_max_sync(0xffffffffu, kmax);
   }
@@ -230,6 +253,10 @@ __device__ __forceinline__ void range_of(const Params& prm, const Unit& x, int t
   }
 }
 
+// What is computed from x stays behind this: the columns' 128 biases, alike in both passes over a block, would else be kept in
+// registers that are not there.
+__device__ __forceinline__ void keep_here(float& x) { asm volatile("" : "+f"(x)); }
+
 template <int D, int MODE, bool PAGED>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -239,6 +266,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sb = (raw + 1023u) & ~1023u;  // 1024-aligned base (128-byte swizzle atoms)
   uint8_t* smem = smem_raw + (sb - raw);
+  constexpr bool SLOPES = MODE == 1 || MODE == 3;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sb + Ly::BAR_OFF + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::MISC_OFF);
@@ -296,6 +324,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t tm_o = tmem + lane_base + 256u + (uint32_t)(t * 128);
     float* epi = reinterpret_cast<float*>(smem + Ly::EPI_OFF + (uint32_t)warp * 4096u);
     const int row_h = row / prm.tt, row_t = row - row_h * prm.tt;  // its head and token within the tile
+    volatile int32_t* mine = reinterpret_cast<volatile int32_t*>(smem + Ly::MINE_OFF + (uint32_t)warp * 64u);
     int nu = 0, cnt = 0, uses = 0;
     bool ok = true;
     while (ok) {
@@ -304,36 +333,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                      ROLE_SOFTMAX, -1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const Unit x = get_unit(ring + 16 * slot);
+      // the unit stays in shared memory, the warp's own copy: the block loop has no registers to spare
+      if (lane < 13) mine[lane] = ring[16 * slot + lane];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(Ly::B_UEMPTY + slot));
       ++nu;
-      if (x.u < 0) break;
-      if (t >= x.ntiles(prm.tt) || x.n_tok == 0) continue;
-      const int tok = x.tok0 + t * prm.tt + row_t, h = x.h0 + row_h;
-      const bool valid = row_h < prm.gh && h < x.h_end && tok < x.n_tok;
+      int NB, blk0, mid;  // its blocks: mid down to blk0, then up from mid + 1
+      bool valid;
       int lo = 0, hi = 0, pos = 0;
       float slope2 = 0.f;
-      if (valid) {
-        range_of<PAGED>(prm, x, tok, lo, hi, pos);
-        if (MODE >= 1 && prm.slopes) slope2 = prm.slopes[h] * LOG2E;
+      {
+        const Unit x = get_unit(mine);
+        if (x.u < 0) break;
+        if (t >= x.ntiles(prm.tt) || x.n_tok == 0) continue;
+        NB = __reduce_max_sync(0xffffffffu, x.NB);  // in uniform registers
+        blk0 = __reduce_max_sync(0xffffffffu, x.blk0);
+        mid = __reduce_max_sync(0xffffffffu, x.mid(prm.tt));
+        const int tok = x.tok0 + t * prm.tt + row_t, h = x.h0 + row_h;
+        valid = row_h < prm.gh && h < x.h_end && tok < x.n_tok;
+        if (valid) {
+          range_of<PAGED>(prm, x, tok, lo, hi, pos);
+          if (SLOPES) slope2 = prm.slopes[h] * LOG2E;
+        }
       }
       // keys that all of the warp's rows see, and the places between which its rows lie
       const int all_lo = __reduce_max_sync(0xffffffffu, valid ? lo : 0);
       const int all_hi = __reduce_min_sync(0xffffffffu, valid ? hi : 0x7fffffff);
       int pmin = 0, pmax = 0;
-      if (MODE >= 1) {
+      if (SLOPES) {
         pmin = __reduce_min_sync(0xffffffffu, valid ? pos : 0x7fffffff);
         pmax = __reduce_max_sync(0xffffffffu, valid ? pos : -1);
       }
       float m_used = valid ? -INFINITY : 0.f, l_sum = 0.f;
-      for (int jb = x.blk0; jb < x.blk0 + x.NB; ++jb, ++cnt) {
+      int tier = 0;  // of the cap
+      for (int j = 0; j < NB; ++j, ++cnt) {
         ok = mbar_wait(bar(Ly::B_SFULL + t), (uint32_t)(cnt & 1), prm.wait_limit_ns, abort_flag, prm.status,
-                       ROLE_SOFTMAX, x.u);
+                       ROLE_SOFTMAX, j);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const int j0 = jb * BN;
+        const int j0 = (j <= mid - blk0 ? mid - j : blk0 + j) * BN;
         const bool edge = all_lo > j0 || all_hi < j0 + BN;
         const bool sees = lo < j0 + BN && hi > j0;
         // The exponentials use the row's running reference m_used, which only ever grows.  A
@@ -354,38 +393,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < BN; c += 32) tmem_ld32(tm_s + (uint32_t)c, s + c);
           tc_wait_ld();
-          if (MODE == 2) {
-            // base 2 scores under the cap: cap log2 e tanh(z), z = s scale / cap
-            const uint64_t k2 = f2_pack(prm.inv_cap, prm.inv_cap);
-            float um[4] = {0.f, 0.f, 0.f, 0.f};
+          if (MODE >= 2) {
+            cap_scores(prm.cap, s, tier, valid, [&]() {
 #pragma unroll
-            for (int c = 0; c < BN; c += 2) um[(c >> 1) & 3] = max3f(um[(c >> 1) & 3], fabsf(s[c]), fabsf(s[c + 1]));
-            const float zmax = fmaxf(max3f(um[0], um[1], um[2]), um[3]) * prm.inv_cap;
-            if (__all_sync(0xffffffffu, !valid || zmax <= 1.f)) {  // infinite: the other form; NaN: it stays NaN in both
-              const uint64_t cl2 = f2_pack(prm.cap_log2, prm.cap_log2);
-#pragma unroll
-              for (int c = 0; c < BN; c += 2) {
-                const uint64_t z = f2_mul(f2_pack(s[c], s[c + 1]), k2);
-                f2_unpack(f2_mul(f2_mul(z, cl2), tanh_ratio2(f2_mul(z, z))), s[c], s[c + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < BN; ++c) s[c] = prm.cap_log2 * tanh_any(s[c] * prm.inv_cap);
-            }
+              for (int c = 0; c < BN; c += 32) tmem_ld32(tm_s + (uint32_t)c, s + c);
+              tc_wait_ld();
+            });
           }
-          if (MODE >= 1) {
-            if (MODE == 1 || prm.slopes) {
-              const float sc = MODE == 2 ? 1.f : prm.scale_log2;
-              const bool before = j0 + BN - 1 <= pmin, behind = j0 >= pmax;
-              if (before || behind) {  // |i - j| = +-(i - j): linear in the column
-                const float sl = before ? slope2 : -slope2, base = sl * (float)(j0 - pos);
+          if (SLOPES) {
+            const float sc = MODE == 3 ? 1.f : prm.scale_log2;
+            const bool before = j0 + BN - 1 <= pmin, behind = j0 >= pmax;
+            if (before || behind) {  // |i - j| = +-(i - j): linear in the column
+              const float sl = before ? slope2 : -slope2;
+              float base = sl * (float)(j0 - pos);
+              keep_here(base);
 #pragma unroll
-                for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], sc, fmaf(sl, (float)c, base));
-              } else {
-                const float off = (float)(j0 - pos);
+              for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], sc, fmaf(sl, (float)c, base));
+            } else {
+              float off = (float)(j0 - pos);
+              keep_here(off);
 #pragma unroll
-                for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], sc, -slope2 * fabsf(off + (float)c));
-              }
+              for (int c = 0; c < BN; ++c) s[c] = fmaf(s[c], sc, -slope2 * fabsf(off + (float)c));
             }
           }
           if (edge) {
@@ -461,6 +489,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
       // ---- epilogue: O_t out of TMEM
+      const Unit x = get_unit(mine);
+      const int tok = x.tok0 + t * prm.tt + row_t, h = x.h0 + row_h;
       // a row without a visible key: O = 0, LSE = -inf (a NaN sum stays NaN).  What its accumulator holds is a sum of
       // zeros, or nothing where the unit has no blocks
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
@@ -611,7 +641,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                               ROLE_MMA, u);
           if (PAGED && ok) {
             // the last token's page may go on behind it, with whatever an earlier owner left: zeros there
-            const int r0 = x.len - (x.blk0 + j) * BN;
+            const int r0 = x.len - x.block(j, prm.tt) * BN;
             if (r0 < BN) {
               const int r1 = min(BN, (r0 + prm.box_rows - 1) / prm.box_rows * prm.box_rows);
               uint8_t* vs = smem + Ly::V_OFF + (uint32_t)st * Ly::TILE;
@@ -716,9 +746,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (ok) publish();
       while (ok && next.u >= 0) {
         const Unit x = next;
-        publish();  // the following unit
-        if (!ok) break;
-        if (x.NB == 0 || x.n_tok == 0) continue;
+        // the following unit, once this one's first loads are on their way
+        auto follow = [&]() {
+          publish();
+          if (ok && next.u >= 0 && next.NB > 0 && next.n_tok > 0) {
+            // its Q tiles and first K and V block into L2, so that the unit boundary does not wait on DRAM
+            if (lane < next.ntiles(prm.tt) * (D / 64))
+              tma_prefetch_l2_3d(&tmQ, lane % (D / 64) * 64, next.row0 + next.tok0 + lane / (D / 64) * prm.tt,
+                                 (PAGED ? 0 : next.b * prm.Hq) + next.h0);
+            int rn, pn;
+            where(next, next.block(0, prm.tt), rn, pn);
+            if (lane < n_box) {
+              tma_prefetch_l2_4d(&tmK, bc * 64, rn, next.hk, pn);
+              tma_prefetch_l2_4d(&tmV, bc * 64, rn, next.hk, pn);
+            }
+          }
+        };
+        if (x.NB == 0 || x.n_tok == 0) {
+          follow();
+          continue;
+        }
+        int r, p;
+        where(x, x.block(0, prm.tt), r, p);
         // Q tiles: the previous unit's last S products must be done with the Q buffer
         ok = mbar_wait_warp(bar(Ly::B_QEMPTY), (uint32_t)((nq & 1) ^ 1), prm.wait_limit_ns, abort_flag, prm.status,
                             ROLE_LOAD, x.u);
@@ -732,13 +781,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                       x.row0 + x.tok0 + t * prm.tt, (PAGED ? 0 : x.b * prm.Hq) + x.h0, bar(Ly::B_QFULL));
         }
         ++nq;
-        int r, p;
-        where(x, x.blk0, r, p);
-        for (int jb = x.blk0; jb < x.blk0 + x.NB; ++jb) {
+        for (int j = 0; j < x.NB; ++j) {
           const int st = nk % NST;
           const uint32_t ph = (uint32_t)((nk / NST) & 1);
           const int r0 = r, p0 = p;
-          if (jb + 1 < x.blk0 + x.NB) where(x, jb + 1, r, p);
+          if (j + 1 < x.NB) where(x, x.block(j + 1, prm.tt), r, p);
           ok = mbar_wait_warp(bar(Ly::B_KEMPTY + st), ph ^ 1u, prm.wait_limit_ns, abort_flag, prm.status, ROLE_LOAD, x.u);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(bar(Ly::B_KFULL + st), Ly::TILE);
@@ -754,6 +801,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           __syncwarp();
           if (lane < n_box) tma_load_4d(sb + Ly::V_OFF + at, &tmV, bc * 64, r0, x.hk, p0, bar(Ly::B_VFULL + st));
           ++nk;
+          if (j == 0) {
+            follow();
+            if (!ok) break;
+          }
         }
       }
       // exit-path drain: every load issued lands before the CTA exits
@@ -913,10 +964,8 @@ static int launch(const ScoreFwdArgs& a, const ScoreFwdShape& z, int sms, cudaSt
   prm.box_rows = BN;
   if (PAGED)
     while (a.page % prm.box_rows != 0) prm.box_rows /= 2;
-  prm.scale = a.scale;
   prm.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-  prm.cap_log2 = (float)((double)a.cap * 1.4426950408889634);
-  prm.inv_cap = a.cap > 0.f ? a.scale / a.cap : 0.f;
+  prm.cap = make_cap(a.scale, a.cap);
   prm.wait_limit_ns = a.wait_limit_ns;
   CUtensorMap mq, mk, mv;
   bool ok;
@@ -938,6 +987,7 @@ static int launch(const ScoreFwdArgs& a, const ScoreFwdShape& z, int sms, cudaSt
          encode_bf16_map(&mv, a.v, 4, kd, kst, kb, err);
   }
   if (!ok) return (int)cudaErrorInvalidValue;
+  if (a.cap > 0.f && a.slopes) return launch_mode<D, 3, PAGED>(mq, mk, mv, prm, sms, st, err);
   if (a.cap > 0.f) return launch_mode<D, 2, PAGED>(mq, mk, mv, prm, sms, st, err);
   if (a.slopes) return launch_mode<D, 1, PAGED>(mq, mk, mv, prm, sms, st, err);
   return launch_mode<D, 0, PAGED>(mq, mk, mv, prm, sms, st, err);
