@@ -66,8 +66,8 @@ constexpr int64_t DRAIN_NS = 200000000;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4, ROLE_EPI = 5;
 
-// What prep_kernel leaves of a 128-row query block: the key blocks [kb0, kb1) that its rows see, and the keys
-// [all_lo, all_hi) that all of those that see any do.
+// What prep_kernel leaves of a 128-row query block, over the rows that see any key: the key blocks [kb0, kb1) that they see, and the
+// keys [all_lo, all_hi) that all of them do.
 struct alignas(16) Bounds {
   int32_t kb0, kb1, all_lo, all_hi;
 };
@@ -511,18 +511,36 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
               },
               load_s);
           if (edge) {
+            asm volatile("" ::: "memory");  // a branch, not selects that every block would run
             const uint4* rv = reinterpret_cast<const uint4*>(rng_s + vb * BM + c_base);
+            // all columns may have one range, as behind a document's start: this thread's key then counts or is dropped as a whole
+            const uint32_t one = (rv[0].x & 0xffffu) * 0x10001u;
+            uint32_t differ = 0u;
 #pragma unroll
-            for (int c = 0; c < 64; c += 8) {
-              const uint4 r4 = rv[c / 8];
+            for (int c = 0; c < 8; ++c) {
+              const uint4 r4 = rv[c];
+              differ |= (r4.x ^ one) | (r4.y ^ one) | (r4.z ^ one) | (r4.w ^ one);
+            }
+            if (differ == 0u) {
+              asm volatile("" ::: "memory");
+              const bool in = (uint32_t)(row - (int)(one & 255u)) < (one >> 24);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t r2 = e == 0 ? r4.x : e == 1 ? r4.y : e == 2 ? r4.z : r4.w;
-                const bool in0 = (uint32_t)(row - (int)(r2 & 255u)) < ((r2 >> 8) & 255u);
-                const bool in1 = (uint32_t)(row - (int)((r2 >> 16) & 255u)) < (r2 >> 24);
-                pk[c / 2 + e] &= (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
-                if (!in0) pv[c + 2 * e] = 0.f;
-                if (!in1) pv[c + 2 * e + 1] = 0.f;
+              for (int c = 0; c < 32; ++c) pk[c] = in ? pk[c] : 0u;
+#pragma unroll
+              for (int c = 0; c < 64; ++c) pv[c] = in ? pv[c] : 0.f;
+            } else {
+#pragma unroll
+              for (int c = 0; c < 64; c += 8) {
+                const uint4 r4 = rv[c / 8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t r2 = e == 0 ? r4.x : e == 1 ? r4.y : e == 2 ? r4.z : r4.w;
+                  const bool in0 = (uint32_t)(row - (int)(r2 & 255u)) < ((r2 >> 8) & 255u);
+                  const bool in1 = (uint32_t)(row - (int)((r2 >> 16) & 255u)) < (r2 >> 24);
+                  pk[c / 2 + e] &= (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
+                  if (!in0) pv[c + 2 * e] = 0.f;
+                  if (!in1) pv[c + 2 * e + 1] = 0.f;
+                }
               }
             }
           }
@@ -651,6 +669,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           // with a cap it may be read again until here (picking the tier by the scores' maximum first instead: 10 % slower)
           if (MODE == 2) arrive(Ly::B_SREAD);
           if (all_lo > k0 || all_hi < k0 + BM) {
+            asm volatile("" ::: "memory");
             const int a = lo - k0 - c_base, n = max(hi - lo, 0);
 #pragma unroll
             for (int c = 0; c < 64; ++c)
@@ -1037,7 +1056,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // D = dO . O by rows, the query blocks' bounds, the order of the blocks, and the unit counters at zero, in one launch: the first CTAs
 // of the grid take a mask each (beyond ORDER_MAX blocks: eight query blocks each), the others 16-byte pieces of rows, D / 8
-// lanes a row.
+// lanes a row (four pieces a thread: 1 to 2 % slower for the pass as a whole).
 constexpr int PREP_THREADS = 256;
 struct PrepParams {
   const uint4* o;
@@ -1075,27 +1094,43 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const __grid_constan
     if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x * 64] = 0u;
     const int first = p.order_q ? (int)blockIdx.x * p.nb : (int)blockIdx.x * WARPS;
     const int end = p.order_q ? first + p.nb : min(first + WARPS, p.n_bounds);
-    for (int i = first + warp; i < end; i += WARPS) {
-      const int m = i / p.nb, qb = i - m * p.nb;
-      int kmin = 0x7fffffff, kmax = 0, all_lo = 0, all_hi = 0x7fffffff;
+    constexpr int U = 4;  // query blocks of a warp whose loads are in flight together
+    for (int i0 = first + warp; i0 < end; i0 += WARPS * U) {
+      int a[U][BM / 32], z[U][BM / 32];
 #pragma unroll
-      for (int e = 0; e < BM / 32; ++e) {
-        const int64_t q = (int64_t)qb * BM + e * 32 + lane;
-        if (q >= p.S) continue;
-        const int a = max(p.lo[m * p.mask_bs + q], 0), z = (int)min((int64_t)p.hi[m * p.mask_bs + q], p.S);
-        if (a >= z) continue;
-        kmin = min(kmin, a), kmax = max(kmax, z);
-        all_lo = max(all_lo, a), all_hi = min(all_hi, z);
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * WARPS, m = i / p.nb, qb = i - m * p.nb;
+#pragma unroll
+        for (int e = 0; e < BM / 32; ++e) {
+          const int64_t q = (int64_t)qb * BM + e * 32 + lane;
+          const bool in = i < end && q < p.S;
+          a[u][e] = in ? p.lo[m * p.mask_bs + q] : 0;
+          z[u][e] = in ? p.hi[m * p.mask_bs + q] : 0;
+        }
       }
-      kmin = __reduce_min_sync(0xffffffffu, kmin);
-      kmax = __reduce_max_sync(0xffffffffu, kmax);
-      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-      Bounds b{0, 0, all_lo, all_hi};
-      if (kmin < kmax) b.kb0 = kmin / BM, b.kb1 = (kmax + BM - 1) / BM;
-      if (lane == 0) {
-        p.bounds[i] = b;
-        if (p.order_q) see[qb] = make_int2(b.kb0, b.kb1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * WARPS, qb = i % p.nb;
+        if (i >= end) continue;
+        int kmin = 0x7fffffff, kmax = 0, all_lo = 0, all_hi = 0x7fffffff;
+#pragma unroll
+        for (int e = 0; e < BM / 32; ++e) {
+          const int x = max(a[u][e], 0), y = (int)min((int64_t)z[u][e], p.S);
+          if (x < y) {
+            kmin = min(kmin, x), kmax = max(kmax, y);
+            all_lo = max(all_lo, x), all_hi = min(all_hi, y);
+          }
+        }
+        kmin = __reduce_min_sync(0xffffffffu, kmin);
+        kmax = __reduce_max_sync(0xffffffffu, kmax);
+        all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+        all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+        Bounds b{0, 0, all_lo, all_hi};
+        if (kmin < kmax) b.kb0 = kmin / BM, b.kb1 = (kmax + BM - 1) / BM;
+        if (lane == 0) {
+          p.bounds[i] = b;
+          if (p.order_q) see[qb] = make_int2(b.kb0, b.kb1);
+        }
       }
     }
     if (!p.order_q) return;

@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           if (edge) {
+            asm volatile("" ::: "memory");  // a branch, not selects that every block would run
             const int a = lo - j0, n = hi - lo;
 #pragma unroll
             for (int c = 0; c < BN; ++c)
