@@ -978,7 +978,7 @@ class MeshRangeAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, lo, hi, scale, cap, slopes, check_status, status):
-        if slopes is not None and slopes.requires_grad:
+        if ctx.needs_input_grad[7]:
             raise ValueError("slopes get no gradient: pass them detached")
         O, LSE = mesh_range_attention(q, k, v, lo, hi, scale, cap, slopes, status=status, check_status=check_status)
         ctx.save_for_backward(q, k, v, lo, hi, slopes, O, LSE)

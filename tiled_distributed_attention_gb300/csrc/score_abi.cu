@@ -126,11 +126,11 @@ extern "C" int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B,
     for (int i = 0; i < 3; ++i)
       if (!stride_ok(kd[i], k_strides[i]) || !stride_ok(kd[i], v_strides[i]))
         return set_last_error(MESH_ATTN_ERR_MISALIGNED, "strides of the pages must be positive multiples of 16 bytes");
-    int sms = 0;
-    if (const int rc = sm_count(&sms)) return rc;
     const size_t need = mesh::paged_workspace(bf16, N, B, Hq, Hkv, d, max_new);
     if (workspace_bytes < need)
       return set_last_error(MESH_ATTN_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+    int sms = 0;
+    if (const int rc = sm_count(&sms)) return rc;
     mesh::PagedArgs a{};
     a.bf16 = bf16;
     a.q = q;
@@ -225,6 +225,7 @@ static int check_range_args(const mesh::RangeArgs& a, const void* workspace, siz
     if (!is_aligned(x, 4)) return set_last_error(MESH_ATTN_ERR_MISALIGNED, "lo, hi, slopes, LSE and status must be 4-byte aligned");
   if (a.mask_bs != 0 && a.mask_bs < a.S && a.B > 1)
     return set_last_error(MESH_ATTN_ERR_INVALID_ARG, "mask_stride must be 0 (one mask for all) or at least S");
+  if (workspace_bytes < 256) return set_last_error(MESH_ATTN_ERR_WORKSPACE, "workspace needs 256 bytes or more");
   if (const int rc = sm_count(sms)) return rc;
   const size_t need = mesh::range_workspace(a.bf16, a.B, a.Hq, a.Hkv, a.S, a.d, backward, *sms);
   if (workspace_bytes < need)
