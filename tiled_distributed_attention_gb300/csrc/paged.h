@@ -35,7 +35,7 @@ struct PagedArgs {
 // Workspace of the calls over a paged cache: [arrival counters of the few-rows kernel, zero between calls | the slots of its
 // pieces, or the tensor-core kernel's counter and parts].  The counters have the same place whatever the sizes, so that a workspace
 // serves calls of different sizes in turn.
-constexpr size_t PAGED_WS_HEAD = 1024;  // MAX_SMS counters
+constexpr size_t PAGED_WS_HEAD = 2048;  // a counter for each of its CTAs
 size_t paged_rows_slots();
 // Few rows a sequence and KV head, both types.
 int launch_paged_rows(const PagedArgs& a, int sms, cudaStream_t st, std::string* err);

@@ -42,7 +42,11 @@ constexpr int WT = 16;            // tokens of a warp in a tile, all in one page
 constexpr int TILE = WARPS * WT;  // tokens of a tile
 constexpr int ROWS = 16;          // rows of a chunk in the buffers (fp32 uses 8 of them)
 constexpr int HALF_ROWS = 8;
-constexpr int STAGES = 3;
+// CTAs an SM: one with 192 KB of ring at d = 128; two at d = 64, whose tiles are half as long and keep one CTA's warps from the
+// memory's rate (64 sequences up to 8,192 tokens, 32 heads on 8: 134 us with one CTA of either depth of ring, 99 with two).
+template <int D>
+constexpr int CTAS = D == 128 ? 1 : 2;
+constexpr int MAX_CTAS = 2 * MAX_SMS;
 // Filling the ring and adding up the warps' sums at a segment's end take about as long as three tiles
 // (4 us; a tile is 64 KB at d = 128, 1.45 us at the memory's rate).
 constexpr int SEG_COST = 3;
@@ -71,6 +75,8 @@ struct Params {
 };
 
 __host__ __device__ constexpr int part_floats(int D) { return ROWS * D + 2 * ROWS; }
+// Floats from row to row of the warps' sums in shared memory: the eight rows that a warp's lanes write at once lie in other banks.
+__host__ __device__ constexpr int sum_ld(int D) { return D + 8; }
 
 // What a sequence asks for, with what does not fit taken as the nearest that does.
 struct Seq {
@@ -177,7 +183,7 @@ __device__ __forceinline__ float score2(const Params& p, float dot, int far, flo
 // running maximum (base 2) and sum of each row, written for the merge by put().
 
 // bf16: products on the tensor cores (mma.sync: 16 rows are far below what a tcgen05 tile wants, and the kernel is
-// bound by memory).  Each warp streams its own 16 tokens of every tile through its own three-stage cp.async ring, so
+// bound by memory).  Each warp streams its own 16 tokens of every tile through its own cp.async ring, so
 // no barrier stands in the loop.
 template <int D>
 struct EngineBf16 {
@@ -186,6 +192,7 @@ struct EngineBf16 {
   static constexpr int CH = D / 8;                    // 16-byte chunks of a row
   static constexpr uint32_t HALF = WT * D * 2;        // K or V of a warp's stage
   static constexpr uint32_t STAGE = 2 * HALF;
+  static constexpr int STAGES = 3;
   static constexpr uint32_t SMEM = WARPS * STAGES * STAGE;
   uint32_t qf[D / 16][4];
   float acc[D / 8][4];
@@ -369,16 +376,17 @@ struct EngineBf16 {
       }
     }
   }
-  // buf[row][D] = sums * 2^(m - M[row])
-  __device__ __forceinline__ void put(float* buf, const float* M, int lane) const {
+  // buf[row][sum_ld(D)] = sums * 2^(m - M[row]), of the first nr rows
+  __device__ __forceinline__ void put(float* buf, const float* M, int nr, int lane) const {
     const int c2 = (lane & 3) * 2;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int row = w * HALF_ROWS + (lane >> 2);
+      if (row >= nr) continue;
       const float f = m[w] == -INFINITY ? 0.f : exp2f(m[w] - M[row]);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(buf + row * D + i * 8 + c2) = make_float2(acc[i][2 * w] * f, acc[i][2 * w + 1] * f);
+        *reinterpret_cast<float2*>(buf + row * sum_ld(D) + i * 8 + c2) = make_float2(acc[i][2 * w] * f, acc[i][2 * w + 1] * f);
     }
   }
 };
@@ -537,29 +545,101 @@ struct EngineF32 {
       }
     }
   }
-  __device__ __forceinline__ void put(float* buf, const float* M, int lane) const {
+  __device__ __forceinline__ void put(float* buf, const float* M, int, int lane) const {
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - M[i]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) buf[i * D + lane * E + e] = acc[i][e] * f;
+      for (int e = 0; e < E; ++e) buf[i * sum_ld(D) + lane * E + e] = acc[i][e] * f;
     }
   }
 };
 
+// The last CTA of a segment adds its pieces up, in order: row r's weights 2^(m - M) into wts [n_p][ROWS] and its maximum and sum, sixteen
+// threads a row; then every thread takes one or two 16-byte columns of the rows over all pieces, or over every GR-th of them where
+// there are fewer columns than threads, into part [GR][nr][D].  Returns GR.  The first loads of both are in flight together.  A function of its own:
+// its registers would else cost the loop over the tokens some of its loads in flight (185 us where it takes 174, 64 sequences).
+template <int D>
+__device__ __noinline__ int merge_pieces(const float* slots, int64_t i0, int n_p, int nr, float* wts, float* part, float* Ms, float* Ls) {
+  const int tid = threadIdx.x;
+  auto slot_of = [&](int k) { return slots + ((i0 + k) * 2 + (k == 0 ? 1 : 0)) * part_floats(D); };
+  const int cols = nr * (D / 4), GR = cols >= THREADS ? 1 : THREADS / cols;
+  constexpr int PRE = 20;
+  float4 pre[PRE];
+  {
+    const int grp = tid / cols, q = tid - grp * cols, r = q / (D / 4), at = q % (D / 4) * 4;
+#pragma unroll
+    for (int u = 0; u < PRE; ++u) {
+      const int k = grp + u * GR;
+      pre[u] = tid < cols * GR && k < n_p ? __ldcg(reinterpret_cast<const float4*>(slot_of(k) + r * D + at)) : make_float4(0, 0, 0, 0);
+    }
+  }
+  {
+    const int r = tid >> 4, k0 = tid & 15;
+    constexpr int PER = MAX_SMS * CTAS<D> / 16;
+    float m[PER], l[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int k = k0 + 16 * u;
+      const float* st = slot_of(k) + ROWS * D + r;
+      m[u] = k < n_p ? __ldcg(st) : -INFINITY;
+      l[u] = k < n_p ? __ldcg(st + ROWS) : 0.f;
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) M = fmaxf(M, m[u]);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const float f = m[u] == -INFINITY ? 0.f : exp2f(m[u] - M);
+      if (k0 + 16 * u < n_p) wts[(k0 + 16 * u) * ROWS + r] = f;
+      L += m[u] == -INFINITY ? l[u] : l[u] * f;  // l is 0 there, or NaN
+    }
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (k0 == 0) {
+      Ms[r] = M;
+      Ls[r] = L;
+    }
+  }
+  __syncthreads();
+  for (int o = tid; o < cols * GR; o += THREADS) {
+    const int grp = o / cols, q = o - grp * cols, r = q / (D / 4), at = q % (D / 4) * 4;
+    float4 t = make_float4(0, 0, 0, 0);
+    int k = grp;
+    if (o == tid) {
+#pragma unroll
+      for (int u = 0; u < PRE; ++u, k += GR) {
+        const float f = k < n_p ? wts[k * ROWS + r] : 0.f;
+        t.x = fmaf(pre[u].x, f, t.x), t.y = fmaf(pre[u].y, f, t.y), t.z = fmaf(pre[u].z, f, t.z), t.w = fmaf(pre[u].w, f, t.w);
+      }
+    }
+#pragma unroll 16
+    for (; k < n_p; k += GR) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k) + r * D + at));
+      const float f = wts[k * ROWS + r];
+      t.x = fmaf(y.x, f, t.x), t.y = fmaf(y.y, f, t.y), t.z = fmaf(y.z, f, t.z), t.w = fmaf(y.w, f, t.w);
+    }
+    *reinterpret_cast<float4*>(part + (grp * nr + r) * D + at) = t;
+  }
+  return GR;
+}
+
 // Bytes of the engine's ring, or of the warps' sums that take its place at a piece's end.
 template <typename Engine, int D>
 struct Big {
-  static constexpr uint32_t SUMS = (uint32_t)(WARPS * ROWS * D * 4);
+  static constexpr uint32_t SUMS = (uint32_t)(WARPS * ROWS * sum_ld(D) * 4);
   static constexpr uint32_t BYTES = Engine::SMEM > SUMS ? Engine::SMEM : SUMS;
   // the last CTA's weights, and its columns' sums by group of pieces
-  static_assert(MAX_SMS * ROWS * 4 + 2 * THREADS * 16 <= SUMS, "room for the merge");
+  static_assert(MAX_SMS * CTAS<D> * ROWS * 4 + 2 * THREADS * 16 <= BYTES, "room for the merge");
 };
 // behind the ring: warps' maxima and sums, M, L, the scan
 constexpr uint32_t STATS = 4 * (2 * WARPS * ROWS + 2 * ROWS) + 8 * (WARPS + 2);
 
 template <typename Engine, int D>
-__global__ void __launch_bounds__(THREADS) rows_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) {
   using T = typename Engine::T;
   constexpr int R = Engine::R;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -660,6 +740,8 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params p) {
     c.t1 = tile0 + (int)(end - s0);
     c.len = s.len;
     c.pos0 = s.len - s.n;
+    const bool whole = s0 >= lo && s1 <= hi;
+    const int64_t i0 = whole ? 0 : owner_of(s0), i1 = whole ? 0 : owner_of(s1 - 1);  // the CTAs that have pieces of the segment
     eng.piece(p, c, warp, lane);
 
     // a row's output: sums / l, and its LSE
@@ -693,18 +775,17 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params p) {
       Ls[tid] = L;
     }
     __syncthreads();
-    eng.put(sums + warp * ROWS * D, Ms, lane);
+    eng.put(sums + warp * ROWS * sum_ld(D), Ms, c.nr, lane);
     __syncthreads();
     constexpr int RP = THREADS / (D / 4);  // rows that the threads take at once: 8, or 16 at d = 64
     const int r_at = tid / (D / 4), c4 = tid % (D / 4) * 4;
-    const bool whole = s0 >= lo && s1 <= hi;
     // a piece: slot 1 where the segment begins here and goes on, slot 0 where it began before
     float* slot = p.part + ((int64_t)blockIdx.x * 2 + (s0 >= lo ? 1 : 0)) * part_floats(D);
     for (int r = r_at; r < c.nr; r += RP) {
       float4 a = make_float4(0, 0, 0, 0);
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(sums + (w * ROWS + r) * D + c4);
+        const float4 y = *reinterpret_cast<const float4*>(sums + (w * ROWS + r) * sum_ld(D) + c4);
         a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
       }
       if (whole) finish(r, c4, a, Ms[r], Ls[r]);
@@ -717,7 +798,6 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params p) {
       }
       __threadfence();
       __syncthreads();
-      const int64_t i0 = owner_of(s0), i1 = owner_of(s1 - 1);
       if (tid == 0) {
         uint32_t* ctr = p.counters + i0;
         const bool last = atomicAdd(ctr, 1u) == (uint32_t)(i1 - i0);
@@ -726,50 +806,9 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Params p) {
       }
       __syncthreads();
       if (scan[WARPS]) {
-        // the last CTA adds the segment's pieces up, in order.  Row r's weights 2^(m - M) first, sixteen
-        // threads a row; then every thread takes one or two 16-byte columns of the rows over all pieces, or
-        // over every G-th of them where there are fewer columns than threads.
         __threadfence();
-        const int n_p = (int)(i1 - i0 + 1);
-        float* wts = sums;                    // [n_p][ROWS]
-        float* part = sums + MAX_SMS * ROWS;  // [G][nr][D]
-        auto slot_of = [&](int k) { return p.part + ((i0 + k) * 2 + (k == 0 ? 1 : 0)) * part_floats(D); };
-        {
-          const int r = tid >> 4, k0 = tid & 15;
-          float M = -INFINITY;
-#pragma unroll 4
-          for (int k = k0; k < n_p; k += 16) M = fmaxf(M, __ldcg(slot_of(k) + ROWS * D + r));
-#pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          float L = 0.f;
-#pragma unroll 4
-          for (int k = k0; k < n_p; k += 16) {
-            const float* st = slot_of(k) + ROWS * D + r;
-            const float m = __ldcg(st), l = __ldcg(st + ROWS);
-            const float f = m == -INFINITY ? 0.f : exp2f(m - M);
-            wts[k * ROWS + r] = f;
-            L += m == -INFINITY ? l : l * f;  // l is 0 there, or NaN
-          }
-#pragma unroll
-          for (int o = 8; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-          if (k0 == 0) {
-            Ms[r] = M;
-            Ls[r] = L;
-          }
-        }
-        __syncthreads();
-        const int cols = c.nr * (D / 4), GR = cols >= THREADS ? 1 : THREADS / cols;
-        for (int o = tid; o < cols * GR; o += THREADS) {
-          const int grp = o / cols, q = o - grp * cols, r = q / (D / 4), at = q % (D / 4) * 4;
-          float4 t = make_float4(0, 0, 0, 0);
-#pragma unroll 16
-          for (int k = grp; k < n_p; k += GR) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(slot_of(k) + r * D + at));
-            const float f = wts[k * ROWS + r];
-            t.x = fmaf(y.x, f, t.x), t.y = fmaf(y.y, f, t.y), t.z = fmaf(y.z, f, t.z), t.w = fmaf(y.w, f, t.w);
-          }
-          *reinterpret_cast<float4*>(part + (grp * c.nr + r) * D + at) = t;
-        }
+        float* part = sums + MAX_SMS * CTAS<D> * ROWS;  // [GR][nr][D]
+        const int GR = merge_pieces<D>(p.part, i0, (int)(i1 - i0 + 1), c.nr, sums, part, Ms, Ls);
         __syncthreads();
         for (int r = r_at; r < c.nr; r += RP) {
           float4 a = make_float4(0, 0, 0, 0);
@@ -812,7 +851,9 @@ static int launch_f32(const Params& p, int64_t rows, int grid, cudaStream_t st, 
 
 }  // namespace prow
 
-size_t paged_rows_slots() { return (size_t)2 * MAX_SMS * prow::part_floats(128) * 4; }
+static_assert(PAGED_WS_HEAD >= prow::MAX_CTAS * 4, "room for the counters");
+// two slots a CTA
+size_t paged_rows_slots() { return (size_t)2 * 4 * std::max(MAX_SMS * prow::CTAS<128> * prow::part_floats(128), MAX_SMS * prow::CTAS<64> * prow::part_floats(64)); }
 
 int launch_paged_rows(const PagedArgs& a, int sms, cudaStream_t st, std::string* err) {
   using namespace prow;
@@ -845,10 +886,10 @@ int launch_paged_rows(const PagedArgs& a, int sms, cudaStream_t st, std::string*
   p.scale = a.scale;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   p.cap = a.cap;
-  // a CTA for every tile there may be, no more than SMs
+  // a CTA for every tile there may be, no more than are resident
   const int64_t rows = (int64_t)a.max_new * p.g;  // of a sequence and KV head, at most
   const int64_t tiles = ((int64_t)a.max_pages * a.page + TILE - 1) / TILE * a.B * a.Hkv * ((rows + 7) / 8);
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, std::min(sms, MAX_SMS)));
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, std::min(sms, MAX_SMS) * (a.d == 128 ? CTAS<128> : CTAS<64>)));
   if (a.bf16)
     return a.d == 128 ? launch<EngineBf16<128>, 128>(p, grid, st, err) : launch<EngineBf16<64>, 64>(p, grid, st, err);
   return a.d == 128 ? launch_f32<128>(p, rows, grid, st, err) : launch_f32<64>(p, rows, grid, st, err);
