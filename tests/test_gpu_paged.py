@@ -213,6 +213,59 @@ def test_attention(lib, case, dtype):
     check(O2, L2, ref, dtype, False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new, lens, window", [([1, 1], [900, 131], 100), ([2, 40], [300, 500], 7), ([150], [1000], 260)], ids=str)
+def test_pages_before_a_window_need_not_exist(lib, dtype, new, lens, window):
+    """A sliding window's old pages have been given away: no entries in the table, other sequences' tokens and NaN in them."""
+    q, _, _, kp, vp, table, off, ln = cache(new, lens, 16, 4, 1, 64, dtype, 54)
+    ref = OR.paged(q, kp, vp, table, off, ln, window=window)
+    for b, x in enumerate(lens):
+        gone = max(0, x - new[b] + 1 - window) // 16
+        for i in range(gone):
+            kp[int(table[b, i])] = math.nan
+            vp[int(table[b, i])] = math.nan
+            table[b, i] = -1
+    for bound in (max(new), max(new) + 60):
+        O, L = lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), bound, window=window)
+        check(O, L, ref, dtype, False)
+
+
+def test_offsets_beyond_32_bits(lib):
+    """Pages that begin beyond 2^31 elements of the pool, by append and by every attention kernel."""
+    n, page, Hkv, d = 1_100_000, 16, 2, 64  # 2.25e9 elements a pool
+    for dtype in (torch.bfloat16, torch.float32):
+        kp, vp = (torch.empty(n, Hkv, page, d, dtype=dtype, device="cuda") for _ in range(2))
+        assert kp.numel() > 1 << 31
+        new, lens = [33, 1], [50, 70]
+        q, k, v, ks, vs, table, off, ln = cache(new, lens, page, 8, Hkv, d, "bf16" if dtype == torch.bfloat16 else "f32", 55)
+        far = torch.arange(n - ks.shape[0], n)
+        kp[far.cuda()], vp[far.cuda()] = ks.cuda(), vs.cuda()
+        low = table.clone()
+        table = torch.where(table < ks.shape[0], table + (n - ks.shape[0]), table)
+        dev = [t.cuda() for t in (q, k, v)]
+        lib.mesh_paged_append(*dev, kp, vp, table.cuda(), off.cuda(), ln.cuda())
+        for i, (b, p) in enumerate(place_of(new, lens)):
+            ks[int(low[b, p // page]), :, p % page], vs[int(low[b, p // page]), :, p % page] = k[i], v[i]
+        assert torch.equal(kp[far.cuda()].cpu(), ks) and torch.equal(vp[far.cuda()].cpu(), vs)
+        name = "bf16" if dtype == torch.bfloat16 else "f32"
+        for rows, o, l, t in ((slice(0, 34), off, ln, table), (slice(33, 34), torch.tensor([0, 1], dtype=torch.int32), ln[1:], table[1:])):
+            ref = OR.paged(q[rows], ks, vs, low[1:] if rows.start else low, o, l)
+            O, L = lib.mesh_paged_attention(dev[0][rows], kp, vp, t.cuda(), o.cuda(), l.cuda(), rows.stop - rows.start)
+            check(O, L, ref, name, False)
+        del kp, vp
+
+
+def test_sequences_that_share_pages(lib):
+    """A common prefix in pages of several sequences, as its owner wrote it."""
+    new, lens = [1, 20, 1], [70, 70, 40]
+    q, _, _, kp, vp, table, off, ln = cache(new, lens, 16, 4, 2, 64, "bf16", 56)
+    table[1, :2] = table[0, :2]
+    table[2, :2] = table[0, :2]
+    ref = OR.paged(q, kp, vp, table, off, ln)
+    O, L = lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), 20)
+    check(O, L, ref, "bf16", False)
+
+
 def test_a_batch_padded_behind(lib):
     """Rows behind the last sequence are left as they are, by both kernels and in both types."""
     for dtype in ("bf16", "f32"):
@@ -262,7 +315,8 @@ def test_what_does_not_fit_is_recorded(lib, dtype, new):
             rows = slice(new[0], None)
         check(O[rows], L[rows], tuple(x[rows] for x in ref), dtype, False)
     # offsets beyond the batch, or out of order: recorded, and nothing outside is touched
-    for bad in ([0, new[0], q.shape[0] + 9, q.shape[0] + 9], [0, 2, 1, q.shape[0]], [-4, 1, 2, 3]):
+    for bad in ([0, new[0], q.shape[0] + 9, q.shape[0] + 9], [0, 2, 1, q.shape[0]], [-4, 1, 2, 3], [q.shape[0], 1, 0, 2], [3, 2, 1, 0],
+                [1 << 30, 0, -(1 << 30), 5]):
         assert call(table, torch.tensor(bad, dtype=torch.int32), ln, max(new))[1] == 6
     # and the next good call in the same context is right
     (O, L), code = call(table, off, ln, max(new))

@@ -710,8 +710,8 @@ def mesh_attn_diff_bwd(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Te
              status, _handle_of(stream))
 
 
-def _raise_status(status: torch.Tensor, stream=None):
-    code = mesh_attn_read_status(status, torch.cuda.current_stream(status.device) if stream is None else stream)
+def _raise_status(status: torch.Tensor):
+    code = mesh_attn_read_status(status, torch.cuda.current_stream(status.device))
     if code != 0:
         raise MeshAttnError(code, "device", f"status block {status.tolist()}")
 
@@ -836,8 +836,8 @@ def mesh_diff_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
 def mesh_paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                       table: torch.Tensor, offsets: torch.Tensor, lens: torch.Tensor, rope: Optional[MeshRope] = None,
                       positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
-                      status: Optional[torch.Tensor] = None, check_status: bool = True, stream=None) -> Optional[torch.Tensor]:
-    """New tokens' keys and values into their sequences' pages, on the current stream (or `stream`): k turned by `rope` (copied
+                      status: Optional[torch.Tensor] = None, check_status: bool = True) -> Optional[torch.Tensor]:
+    """New tokens' keys and values into their sequences' pages, on the current stream: k turned by `rope` (copied
     without one), v copied.  Returns q turned likewise, as a dense tensor or in q_out, for mesh_paged_attention (None for no q).
 
     q [N, Hq, d], k, v [N, Hkv, d]: the new tokens of all sequences one sequence after another, views with any token and head
@@ -849,11 +849,11 @@ def mesh_paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
     keeps status (new_status) and passes check_status=False, which leaves out the wait."""
     st = new_status(k.device) if status is None else status
     out = (_ext or load_binding()).paged_append(None if rope is None else rope._native, q, k, v, k_pages, v_pages, table, offsets,
-                                                lens, positions, q_out, st, _handle_of(stream))
+                                                lens, positions, q_out, st, None)
     if out.__class__ is int:
         _check(out, "mesh_attn_paged_append")
     if check_status:
-        _raise_status(st, stream)
+        _raise_status(st)
     return out[0]
 
 
@@ -871,8 +871,8 @@ def mesh_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
                          lens: torch.Tensor, max_new: int, scale: Optional[float] = None, cap: float = 0.0,
                          slopes: Optional[torch.Tensor] = None, window: int = 0, O: Optional[torch.Tensor] = None,
                          LSE: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                         status: Optional[torch.Tensor] = None, check_status: bool = True, stream=None):
-    """Attention of the new tokens q [N, Hq, d] over their sequences' pages, on the current stream (or `stream`); the pages hold
+                         status: Optional[torch.Tensor] = None, check_status: bool = True):
+    """Attention of the new tokens q [N, Hq, d] over their sequences' pages, on the current stream; the pages hold
     the new tokens' own keys and values already (mesh_paged_append, whose arguments these are).  Token i of a sequence sees its
     tokens j <= i, with window > 0 those with i - j < window; scores are scale q.k (1 / sqrt(d) unless given), capped to
     cap tanh(score / cap) with cap > 0, less slopes[h] (i - j) with slopes (fp32 [Hq]).
@@ -884,11 +884,11 @@ def mesh_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     ws = new_paged_workspace(q, k_pages, table, max_new) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
     out = (_ext or load_binding()).paged_attn(q, k_pages, v_pages, table, offsets, lens, max_new, scale, cap, slopes, window, O, LSE,
-                                              ws, st, _handle_of(stream))
+                                              ws, st, None)
     if out.__class__ is int:
         _check(out, "mesh_attn_paged_attn")
     if check_status:
-        _raise_status(st, stream)
+        _raise_status(st)
     return out
 
 
@@ -934,9 +934,9 @@ def new_range_workspace(q: torch.Tensor, k: torch.Tensor, backward: bool = False
 def mesh_range_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lo: torch.Tensor, hi: torch.Tensor,
                          scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                          O: Optional[torch.Tensor] = None, LSE: Optional[torch.Tensor] = None,
-                         workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, check_status: bool = True,
-                         stream=None):
-    """Attention where query i sees the keys lo[i] <= j < hi[i], on the current stream (or `stream`): packed documents, prefixes that
+                         workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                         check_status: bool = True):
+    """Attention where query i sees the keys lo[i] <= j < hi[i], on the current stream: packed documents, prefixes that
     see one another, windows, padding (mesh_ranges makes lo and hi).  q [B, Hq, S, d], k, v [B, Hkv, S, d], all bf16 or all
     fp32; lo, hi int32 [S] or [B, S] on the device.  Scores are scale q.k (1 / sqrt(d) unless given), capped to
     cap tanh(score / cap) with cap > 0, less slopes[h] |i - j| with slopes (fp32 [Hq]).  Returns O (q's shape and dtype) and LSE
@@ -946,11 +946,11 @@ def mesh_range_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lo: 
         load_binding().range_check(q, k, v, lo, hi, slopes)
     ws = new_range_workspace(q, k) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
-    out = (_ext or load_binding()).range_fwd(q, k, v, lo, hi, scale, cap, slopes, O, LSE, ws, st, _handle_of(stream))
+    out = (_ext or load_binding()).range_fwd(q, k, v, lo, hi, scale, cap, slopes, O, LSE, ws, st, None)
     if out.__class__ is int:
         _check(out, "mesh_attn_range_fwd")
     if check_status:
-        _raise_status(st, stream)
+        _raise_status(st)
     return out
 
 
@@ -959,17 +959,17 @@ def mesh_range_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
                                   cap: float = 0.0, slopes: Optional[torch.Tensor] = None, dQ: Optional[torch.Tensor] = None,
                                   dK: Optional[torch.Tensor] = None, dV: Optional[torch.Tensor] = None,
                                   workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
-                                  check_status: bool = True, stream=None):
-    """(dQ, dK, dV) from the forward's O and LSE and the gradient dO, on the current stream (or `stream`)."""
+                                  check_status: bool = True):
+    """(dQ, dK, dV) from the forward's O and LSE and the gradient dO, on the current stream."""
     if workspace is None or status is None:
         load_binding().range_check(q, k, v, lo, hi, slopes)
     ws = new_range_workspace(q, k, backward=True) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
-    out = (_ext or load_binding()).range_bwd(q, k, v, lo, hi, O, LSE, dO, scale, cap, slopes, dQ, dK, dV, ws, st, _handle_of(stream))
+    out = (_ext or load_binding()).range_bwd(q, k, v, lo, hi, O, LSE, dO, scale, cap, slopes, dQ, dK, dV, ws, st, None)
     if out.__class__ is int:
         _check(out, "mesh_attn_range_bwd")
     if check_status:
-        _raise_status(st, stream)
+        _raise_status(st)
     return out
 
 

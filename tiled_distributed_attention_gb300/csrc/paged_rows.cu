@@ -17,7 +17,7 @@
 //
 // A row's statistics are fp32; sums of P V are fp32.  A warp's 16 tokens of a tile lie in one page (pages are multiples of
 // 16), so a tile costs a warp one look at the table, one tile ahead.  What lies behind a sequence's last token, in its
-// last page or in pages of the table behind it, is never read: its places in shared memory are zero-filled, so NaN there
+// last page or in pages of the table behind it, and what lies before all windows, is never read: its places in shared memory are zero-filled, so NaN there
 // does not reach a sum.  Lengths, offsets and pages that do not fit are recorded in the status block and taken as the
 // nearest that do (a page that does not exist: zeros); the kernel never skips on the status block, since a CTA that
 // skipped would leave its counters and slots half done.
@@ -140,6 +140,7 @@ struct Piece {
   int b, r0, nr;             // the chunk's first row and its rows
   int t0, t1;                // tiles
   int len, pos0;             // cached tokens; the place of the first new token
+  int lo;                    // the first token that any of the sequence's rows sees
 };
 
 // A row's keys [lo, hi), its own place, its slope in base 2.
@@ -164,12 +165,14 @@ __device__ __forceinline__ const T* q_row(const Params& p, const Piece<T>& c, in
   const int row = c.r0 + r, t = row / p.g;
   return c.q + t * p.qs[0] + (row - t * p.g) * p.qs[1];
 }
-// A page that the table names, or none: recorded, and read as zeros.
-__device__ __forceinline__ int page_at(const Params& p, const int32_t* pages, int tok0, int len, int b, int lane) {
-  if (tok0 >= len) return -1;
-  const int pg = pages[tok0 / p.page];
+// The page of the WT tokens from tok0 on, or -1 where none of them is seen (behind the last token, or before a window, whose
+// pages need not be there any more) or where the table names none that exists: recorded, and read as zeros.
+template <typename T>
+__device__ __forceinline__ int page_at(const Params& p, const Piece<T>& c, int tok0, int lane) {
+  if (tok0 >= c.len || tok0 / WT * WT + WT <= c.lo) return -1;
+  const int pg = c.pages[tok0 / p.page];
   if (pg >= 0 && pg < p.n_pages) return pg;
-  if (lane == 0) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_PAGE, b);
+  if (lane == 0) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_PAGE, c.b);
   return -1;
 }
 // A score q.k in base 2: scaled, capped, biased.
@@ -210,7 +213,7 @@ struct EngineBf16 {
     for (int i = 0; i < WT * CH / 32; ++i) {
       const int idx = i * 32 + lane, row = idx / CH, ch = idx % CH;
       const uint32_t at = dst + (uint32_t)(row * D * 2) + (uint32_t)((ch ^ (row & 7)) << 4);
-      const bool in = pg >= 0 && tok0 + row < c.len;
+      const bool in = pg >= 0 && tok0 + row < c.len && tok0 + row >= c.lo;
       const int64_t t = in ? row : 0;  // a safe address where nothing is read
       cp_async16(at, in ? kp + t * p.ks[2] + ch * 8 : static_cast<const T*>(p.k), in);
       cp_async16(at + HALF, in ? vp + t * p.vs[2] + ch * 8 : static_cast<const T*>(p.v), in);
@@ -220,12 +223,12 @@ struct EngineBf16 {
   __device__ __forceinline__ void piece(const Params& p, const Piece<T>& c, int warp, int lane) {
     const int c2 = (lane & 3) * 2;
     auto tok_of = [&](int t) { return t * TILE + warp * WT; };
-    int pg_next = page_at(p, c.pages, tok_of(c.t0), c.len, c.b, lane);
+    int pg_next = page_at(p, c, tok_of(c.t0), lane);
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
       if (c.t0 + s < c.t1) {
         const int pg = pg_next;
-        if (c.t0 + s + 1 < c.t1) pg_next = page_at(p, c.pages, tok_of(c.t0 + s + 1), c.len, c.b, lane);
+        if (c.t0 + s + 1 < c.t1) pg_next = page_at(p, c, tok_of(c.t0 + s + 1), lane);
         load(p, c, s, tok_of(c.t0 + s), pg, lane);
       }
       cp_commit();
@@ -262,7 +265,7 @@ struct EngineBf16 {
         if (s >= STAGES) s -= STAGES;
         if (ahead < c.t1) {
           const int pg = pg_next;
-          if (ahead + 1 < c.t1) pg_next = page_at(p, c.pages, tok_of(ahead + 1), c.len, c.b, lane);
+          if (ahead + 1 < c.t1) pg_next = page_at(p, c, tok_of(ahead + 1), lane);
           load(p, c, s, tok_of(ahead), pg, lane);
         }
         cp_commit();
@@ -424,7 +427,7 @@ struct EngineF32 {
 #pragma unroll
     for (int i = 0; i < U * CH / 32; ++i) {
       const int idx = i * 32 + lane, row = idx / CH, ch = idx % CH;
-      const bool in = pg >= 0 && tok0 + row < c.len;
+      const bool in = pg >= 0 && tok0 + row < c.len && tok0 + row >= c.lo;
       const int64_t t = in ? row : 0;  // a safe address where nothing is read
       cp_async16(dst + (uint32_t)idx * 16u, in ? kp + t * p.ks[2] + ch * 4 : static_cast<const T*>(p.k), in);
       cp_async16(dst + ROWB + (uint32_t)idx * 16u, in ? vp + t * p.vs[2] + ch * 4 : static_cast<const T*>(p.v), in);
@@ -437,7 +440,7 @@ struct EngineF32 {
     int pg = -1;  // the page of the groups of a tile being loaded
     auto load_group = [&](int g, int s) {
       if (g < n) {
-        if (g % (WT / U) == 0) pg = page_at(p, c.pages, tok_of(g), c.len, c.b, lane);
+        if (g % (WT / U) == 0) pg = page_at(p, c, tok_of(g), lane);
         load(p, c, s, tok_of(g), pg, lane);
       }
       cp_commit();
@@ -740,6 +743,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
     c.t1 = tile0 + (int)(end - s0);
     c.len = s.len;
     c.pos0 = s.len - s.n;
+    c.lo = p.window ? max(0, c.pos0 + 1 - p.window) : 0;
     const bool whole = s0 >= lo && s1 <= hi;
     const int64_t i0 = whole ? 0 : owner_of(s0), i1 = whole ? 0 : owner_of(s1 - 1);  // the CTAs that have pieces of the segment
     eng.piece(p, c, warp, lane);

@@ -17,8 +17,8 @@
 // warp's rows, |i - j| only on the diagonal.
 //
 // Pages.  A block's keys are boxes of as many rows as a page (a power of two that divides it, 16 to 128), one lane of the producer
-// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Places behind the last token
-// load a page that does not exist, which arrives as zeros; what an earlier owner left behind it in its last page is
+// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Places behind the last token, or before the
+// first that any row's window holds, load a page that does not exist, which arrives as zeros; what an earlier owner left behind it in its last page is
 // zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
 //
 // Few units are cut into parts of their keys (score_fwd_shape), whose normalised outputs and LSEs merge_kernel adds up in order.
@@ -114,7 +114,7 @@ struct Params {
 // A unit: its rows are the tokens [tok0, tok0 + 2 tt) below n_tok of query heads h0 .. h0 + gh - 1 (below h_end), its keys the
 // blocks [blk0, blk0 + NB).  Paged: the sequence's first new token is row `row0` of the batch and has the place pos0.
 struct Unit {
-  int u, b, hk, h0, h_end, tok0, n_tok, row0, pos0, len, blk0, NB, part;
+  int u, b, hk, h0, h_end, tok0, n_tok, row0, pos0, len, blk0, NB, part, kmin;  // kmin: the first key that any row sees
   __device__ __forceinline__ int ntiles(int tt) const { return tok0 + tt < n_tok ? 2 : 1; }
   // Its i-th block: from the one of its last token's own key down to the first, then up from behind it.  So rows meet their own key
   // early, where a causal document or a slope has its largest weights, and the running maximum seldom grows (blocks from the first
@@ -129,12 +129,12 @@ struct Unit {
 };
 __device__ __forceinline__ void put_unit(volatile int32_t* e, const Unit& x) {
   e[0] = x.u, e[1] = x.b, e[2] = x.hk, e[3] = x.h0, e[4] = x.h_end, e[5] = x.tok0, e[6] = x.n_tok, e[7] = x.row0;
-  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.part;
+  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.part;  // kmin is the producer's own
 }
 __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   Unit x;
   x.u = e[0], x.b = e[1], x.hk = e[2], x.h0 = e[3], x.h_end = e[4], x.tok0 = e[5], x.n_tok = e[6], x.row0 = e[7];
-  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.part = e[12];
+  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.part = e[12], x.kmin = 0;
   return x;
 }
 
@@ -160,7 +160,7 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
   x.b = ln / prm.Hkv;
   x.h0 = x.hk * prm.g + c * prm.gh;
   x.h_end = min(x.h0 + prm.gh, (x.hk + 1) * prm.g);
-  x.blk0 = x.NB = 0;
+  x.blk0 = x.NB = x.kmin = 0;
   int kmin = 0x7fffffff, kmax = 0;  // keys that some row sees
   if (PAGED) {
     // the last b with offsets[b] / tu + b <= grp
@@ -191,8 +191,8 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
     x.n_tok = min(x.n_tok, x.len);
     x.pos0 = x.len - x.n_tok;
     x.tok0 = (grp - (x.row0 / tu + x.b)) * tu;
-    if (x.tok0 >= x.n_tok) {
-      x.n_tok = 0;
+    if (x.tok0 < 0 || x.tok0 >= x.n_tok) {  // below 0 where offsets do not ascend
+      x.tok0 = x.n_tok = 0;
       return x;
     }
     if (!bounds) return x;
@@ -227,6 +227,7 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
     kmax = __reduce_max_sync(0xffffffffu, kmax);
   }
   if (kmin < kmax) {
+    x.kmin = kmin;
     x.blk0 = kmin / BN;
     x.NB = (kmax + BN - 1) / BN - x.blk0;
   }
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         r = 0;
         p = prm.n_pages;  // no such page: zeros
-        if (lane < n_box && key < x.len) {
+        if (lane < n_box && key < x.len && key + prm.box_rows > x.kmin) {  // pages before a window need not be there any more
           const int at = key / prm.page;
           r = key - at * prm.page;
           p = prm.table[x.b * prm.table_s + at];

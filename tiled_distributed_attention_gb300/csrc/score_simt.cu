@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Pa
     // K and V: keys behind the last are zeros
     for (int i = tid; i < TK * (D / 4); i += THREADS) {
       const int r = i / (D / 4), c = i % (D / 4) * 4, key = j0 + r;
-      bool in = key < t.len;
+      bool in = key < t.len && key >= t.kmin;  // pages before a window need not be there any more
       int64_t pg = 0, row = key;
       if (PAGED && in) {
         const int at = key / p.page;
