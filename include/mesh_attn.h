@@ -437,10 +437,11 @@ int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, 
  *   slopes    device fp32 [Hq], finite, or NULL.
  *   dtype     MESH_ATTN_BF16 (P in bf16 for its product; two bf16 pieces with few rows) or MESH_ATTN_F32.  d 64 or 128; page a
  *             multiple of 16; B <= 4096; max_pages * page <= 2^30.  Tensors 16-byte aligned, strides multiples of 16 bytes.
- * Tokens of a page from the sequence's length on never reach a result, NaN or not; with a window, pages wholly before all new tokens'
- * windows (16 tokens of one, or a power of two that divides the page, at a time) are not read and need not exist.  Another page
- * that does not exist is recorded and read as zeros.  With few rows (16 of max_new * Hq / Hkv in bf16, 8 in fp32) the kernel does
- * its work whatever the status block holds, which keeps the workspace fit for the next call. */
+ * Tokens of a page from the sequence's length on never reach a result, NaN or not; with a window, pages wholly before all
+ * new tokens' windows (16 tokens of one, or a power of two that divides the page, at a time) are not read and need not exist.
+ * Another page that does not exist is recorded and read as zeros; where the status block holds an error the outputs are
+ * not to be used.  With few rows (16 of max_new * Hq / Hkv in bf16, 8 in fp32) the kernel does its work whatever the status
+ * block holds, which keeps the workspace fit for the next call. */
 int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, const void* q,
                          const int64_t* q_strides, int32_t n_pages, int32_t page, const void* k_pages, const int64_t* k_strides,
                          const void* v_pages, const int64_t* v_strides, const int32_t* table, int32_t max_pages,
@@ -457,8 +458,8 @@ int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq
  *   x_ij = scale q_i.k_j, or cap tanh(scale q_i.k_j / cap) with cap > 0;   x_ij -= slopes[h] |i - j| where slopes is not NULL.
  * Backward, with P = exp(x - LSE), dP = dO V^T, D = dO . O and t = tanh(scale q.k / cap):
  *   dS = P (dP - D) (1 - t^2) (without a cap t = 0),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO;
- * slopes get no gradient.  Masked keys get weight 0, and a weight of 0 still multiplies its value, so V (and for the backward call
- * every tensor) must be finite in the 128-row blocks that a row's range touches. */
+ * slopes get no gradient.  Masked scores may be infinite or NaN, but a weight of 0 still multiplies its value: V (and for
+ * the backward call every tensor) must be finite in all rows, those of padding too. */
 
 /* Bytes of device workspace of the calls below: the forward's, or with backward = 1 enough for both directions.
  * Caller-allocated, 16-byte aligned, its contents do not matter; calls that overlap on the GPU, captured graphs among them, need

@@ -12,15 +12,15 @@
 // segment whose tiles fall into one CTA is finished there; of the others every CTA leaves unnormalised sums with their
 // running maxima in a slot of its own (two a CTA: the piece that began before it and the piece that goes on behind it),
 // and the last CTA to arrive adds them up in order, so results do not depend on the arrival order.  At most one segment
-// begins in a CTA and goes on behind it, so a segment's arrival counter is that CTA's: as many as there are SMs, zero between
-// calls (the last CTA puts them back).
+// begins in a CTA and goes on behind it, so a segment's arrival counter is that CTA's: one a CTA, zero between calls (the last
+// CTA puts them back).
 //
 // A row's statistics are fp32; sums of P V are fp32.  A warp's 16 tokens of a tile lie in one page (pages are multiples of
 // 16), so a tile costs a warp one look at the table, one tile ahead.  What lies behind a sequence's last token, in its
-// last page or in pages of the table behind it, and what lies before all windows, is never read: its places in shared memory are zero-filled, so NaN there
-// does not reach a sum.  Lengths, offsets and pages that do not fit are recorded in the status block and taken as the
-// nearest that do (a page that does not exist: zeros); the kernel never skips on the status block, since a CTA that
-// skipped would leave its counters and slots half done.
+// last page or in pages of the table behind it, and what lies before all windows, is never read: its places in shared memory
+// are zero-filled, so NaN there does not reach a sum.  Lengths, offsets and pages that do not fit are recorded in the status
+// block and taken as the nearest that do (a page that does not exist: zeros); the kernel never skips on the status block, since
+// a CTA that skipped would leave its counters and slots half done.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -558,10 +558,11 @@ struct EngineF32 {
   }
 };
 
-// The last CTA of a segment adds its pieces up, in order: row r's weights 2^(m - M) into wts [n_p][ROWS] and its maximum and sum, sixteen
-// threads a row; then every thread takes one or two 16-byte columns of the rows over all pieces, or over every GR-th of them where
-// there are fewer columns than threads, into part [GR][nr][D].  Returns GR.  The first loads of both are in flight together.  A function of its own:
-// its registers would else cost the loop over the tokens some of its loads in flight (185 us where it takes 174, 64 sequences).
+// The last CTA of a segment adds its pieces up, in order: row r's weights 2^(m - M) into wts [n_p][ROWS] and its maximum and
+// sum, sixteen threads a row; then every thread takes one or two 16-byte columns of the rows over all pieces, or over every
+// GR-th of them where there are fewer columns than threads, into part [GR][nr][D].  Returns GR.  The first loads of both are in
+// flight together.  A function of its own: its registers would else cost the loop over the tokens some of its loads in flight
+// (185 us where it takes 174, 64 sequences).
 template <int D>
 __device__ __noinline__ int merge_pieces(const float* slots, int64_t i0, int n_p, int nr, float* wts, float* part, float* Ms, float* Ls) {
   const int tid = threadIdx.x;

@@ -10,9 +10,9 @@
 
 namespace mesh {
 
-// Caps are taken by tiers, the lowest that holds for all of a warp's scores of a block (the highest z^2 says so afterwards, and what
-// was too low is done again from the next): |z| <= 1/2, |z| <= 1, any.  A score is seldom near its cap, and every step of the
-// polynomial costs the FMA pipe a cycle a score and sub-partition, 256 a block, beside the softmax's two.
+// Caps are taken by tiers, the lowest that holds for all of a warp's scores of a block (the highest z^2 says so afterwards, and
+// what was too low is done again from the next): |z| <= 1/2, |z| <= 1, any.  A score is seldom near its cap, and every step of
+// the polynomial costs the FMA pipe a cycle a score and sub-partition, 256 a block, beside the softmax's two.
 //
 // tanh(z) / z as a polynomial of z^2: least maximum of the relative error (iterated weighted least squares on 4,000
 // points), 5.4e-7 at degree 3 up to 1/2 and 5.9e-7 at degree 5 up to 1.
@@ -64,7 +64,8 @@ inline Cap make_cap(float scale, float cap) {
   return c;
 }
 
-// A pair of scores by tier 0 or 1: r with y = s' r, s' being s (tier 0) or s k (tier 1, left in s), and the highest s'^2 so far in um.
+// A pair of scores by tier 0 or 1: r with y = s' r, s' being s (tier 0) or s k (tier 1, left in s), and the highest s'^2 so far
+// in um.
 template <int TIER>
 __device__ __forceinline__ uint64_t cap_pair(const Cap& cap, uint64_t& s, float& um) {
   uint64_t v, r;
@@ -85,10 +86,6 @@ __device__ __forceinline__ uint64_t cap_pair(const Cap& cap, uint64_t& s, float&
 }
 // Up to which um a tier holds.
 __device__ __forceinline__ float cap_limit(const Cap& cap, int tier) { return tier == 0 ? cap.low : tier == 1 ? TANH_HIGH : INFINITY; }
-// The tier that scores of at most `most` in magnitude want.
-__device__ __forceinline__ int cap_tier(const Cap& cap, float most) {
-  return most * most <= cap.low ? 0 : most * cap.k <= 1.f ? 1 : 2;
-}
 // y of any score.
 __device__ __forceinline__ float cap_any(const Cap& cap, float s) { return cap.log2 * tanh_any(s * cap.k); }
 

@@ -11,7 +11,8 @@
 //   warps 0-7   elementwise: two warps per TMEM lane quadrant, each taking 64 of a block's 128 columns
 //   warp 8      MMA issuer, warp 9 producer, warps 10-11 idle
 //   warps 12-15 (dq) copy each unit's Q and dO into TMEM, and drain and store dQ
-// dkdv (unit = batch, KV head, 128-key block, part): K and V stay in shared memory, the Q and dO blocks of the query blocks that see the
+// dkdv (unit = batch, KV head, 128-key block, part): K and V stay in shared memory, the Q and dO blocks of the query blocks
+// that see the
 //   key block stream, head of the group after head.  TMEM: S^T | dP^T | dV | dK.
 // dq (unit = batch, head, 128-row block, part): Q and dO are copied into TMEM, the K and V blocks that the rows see stream.
 //   TMEM: S | dP | dQ | Q | dO.
@@ -66,8 +67,8 @@ constexpr int64_t DRAIN_NS = 200000000;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4, ROLE_EPI = 5;
 
-// What prep_kernel leaves of a 128-row query block, over the rows that see any key: the key blocks [kb0, kb1) that they see, and the
-// keys [all_lo, all_hi) that all of them do.
+// What prep_kernel leaves of a 128-row query block, over the rows that see any key: the key blocks [kb0, kb1) that they see,
+// and the keys [all_lo, all_hi) that all of them do.
 struct alignas(16) Bounds {
   int32_t kb0, kb1, all_lo, all_hi;
 };
@@ -1054,9 +1055,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     run_pass<D, MODE, false>(tmQ, tmG, tmK, tmV, prm, (int)blockIdx.x - prm.kv_ctas, prm.dq_ctas);
 }
 
-// D = dO . O by rows, the query blocks' bounds, the order of the blocks, and the unit counters at zero, in one launch: the first CTAs
-// of the grid take a mask each (beyond ORDER_MAX blocks: eight query blocks each), the others 16-byte pieces of rows, D / 8
-// lanes a row (four pieces a thread: 1 to 2 % slower for the pass as a whole).
+// D = dO . O by rows, the query blocks' bounds, the order of the blocks, and the unit counters at zero, in one launch: the
+// first CTAs of the grid take a mask each (beyond ORDER_MAX blocks: eight query blocks each), the others 16-byte pieces of
+// rows, D / 8 lanes a row (four pieces a thread: 1 to 2 % slower for the pass as a whole).
 constexpr int PREP_THREADS = 256;
 struct PrepParams {
   const uint4* o;

@@ -56,11 +56,11 @@ bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
 // Tiles.  All query heads of a KV head in one tile where they and their tokens fill it (3 heads: 42 tokens, 126 rows), else the
 // heads in the fewest equal chunks that do to 7/8.
 //
-// Parts.  The longest unit has to be done, and the SMs share all blocks: a chunk's units see about as many each and go in whole waves,
-// those of a dense batch half of the longest on average, as under a causal mask.  A unit costs about three blocks besides
-// its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of their fp32 rows.  The best count is taken where it
-// saves a fifth or more: 8 units of 512 blocks go in 16 parts; 160 units of up to 20 blocks stay whole (40 us; 68 in 2 parts), and 128
-// of 512 (687 us; 726 in 8 parts).
+// Parts.  The longest unit has to be done, and the SMs share all blocks: a chunk's units see about as many each and go in whole
+// waves, those of a dense batch half of the longest on average, as under a causal mask.  A unit costs about three blocks
+// besides its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of their fp32 rows.  The best count
+// is taken where it saves a fifth or more: 8 units of 512 blocks go in 16 parts; 160 units of up to 20 blocks stay whole (40
+// us; 68 in 2 parts), and 128 of 512 (687 us; 726 in 8 parts).
 ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms) {
   ScoreFwdShape z{};
   const int g = Hq / Hkv;

@@ -12,14 +12,14 @@
 // Rows see ranges: a warp masks a block only where it is not inside all of its rows' ranges, and a row that has met no key yet
 // takes no maximum pass for a block that it does not see.
 //
-// Cap (MODE 2, with slopes 3).  tanh by a polynomial while the whole warp's scores of a block stay below the cap, of fewer steps below
-// half of it, else by exponentials (score.cuh).  Slopes (MODE 1 and 3): one more FMA where a block lies on one side of all of the
-// warp's rows, |i - j| only on the diagonal.
+// Cap (MODE 2, with slopes 3).  tanh by a polynomial while the whole warp's scores of a block stay below the cap, of fewer
+// steps below half of it, else by exponentials (score.cuh).  Slopes (MODE 1 and 3): one more FMA where a block lies on one side
+// of all of the warp's rows, |i - j| only on the diagonal.
 //
 // Pages.  A block's keys are boxes of as many rows as a page (a power of two that divides it, 16 to 128), one lane of the producer
-// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Places behind the last token, or before the
-// first that any row's window holds, load a page that does not exist, which arrives as zeros; what an earlier owner left behind it in its last page is
-// zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
+// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Places behind the last token, or
+// before the first that any row's window holds, load a page that does not exist, which arrives as zeros; what an earlier owner
+// left behind it in its last page is zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
 //
 // Few units are cut into parts of their keys (score_fwd_shape), whose normalised outputs and LSEs merge_kernel adds up in order.
 // P is rounded to bf16 for its product (2^-9 relative a term), everything else is fp32.
@@ -138,10 +138,10 @@ __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   return x;
 }
 
-// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone): numbered batch of lanes by batch, within it from the last tokens (the
-// most keys where the mask is causal) to the first, within those lane by lane, its parts together.  A lane is a (batch, KV head,
-// chunk of heads); paged: a (KV head, chunk), whose groups are those of all sequences, sequence b's from
-// offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
+// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone): numbered batch of lanes by batch, within it
+// from the last tokens (the most keys where the mask is causal) to the first, within those lane by lane, its parts together.  A
+// lane is a (batch, KV head, chunk of heads); paged: a (KV head, chunk), whose groups are those of all sequences, sequence b's
+// from offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
 template <bool PAGED>
 __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
   Unit x;

@@ -538,8 +538,8 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Bwd
   }
 }
 
-// dK and dV of 64 keys of a batch entry and KV head, over part blockIdx.z of the blocks of 64 queries of its query heads that may see
-// them: those from the first to the last query that does.
+// dK and dV of 64 keys of a batch entry and KV head, over part blockIdx.z of the blocks of 64 queries of its query heads that
+// may see them: those from the first to the last query that does.
 template <int D>
 __global__ void __launch_bounds__(THREADS) dkdv_kernel(const __grid_constant__ BwdParams p) {
   using Sm = BwdSmem<D>;
