@@ -439,9 +439,8 @@ int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, 
  *             multiple of 16; B <= 4096; max_pages * page <= 2^30.  Tensors 16-byte aligned, strides multiples of 16 bytes.
  * Tokens of a page from the sequence's length on never reach a result, NaN or not; with a window, pages wholly before all
  * new tokens' windows (16 tokens of one, or a power of two that divides the page, at a time) are not read and need not exist.
- * Another page that does not exist is recorded and read as zeros; where the status block holds an error the outputs are
- * not to be used.  With few rows (16 of max_new * Hq / Hkv in bf16, 8 in fp32) the kernel does its work whatever the status
- * block holds, which keeps the workspace fit for the next call. */
+ * Another page that does not exist is recorded and read as zeros.  MESH_ATTN_ERR_OUT_OF_RANGE in the status block keeps
+ * neither the other sequences nor later calls from their work; after another error outputs are not to be used. */
 int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, const void* q,
                          const int64_t* q_strides, int32_t n_pages, int32_t page, const void* k_pages, const int64_t* k_strides,
                          const void* v_pages, const int64_t* v_strides, const int32_t* table, int32_t max_pages,

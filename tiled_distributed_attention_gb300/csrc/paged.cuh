@@ -5,7 +5,17 @@
 
 #include <cstdint>
 
+#include "mesh_attn.h"
+
 namespace mesh {
+
+// Whether a kernel has nothing to do for what the status block holds.  Over a paged cache, lengths and pages that do not fit are taken
+// as the nearest that do, and do not keep the other sequences, later kernels and later calls from their work.
+template <bool PAGED>
+__device__ __forceinline__ bool stopped(const int32_t* status) {
+  const int32_t s = *reinterpret_cast<const volatile int32_t*>(status);
+  return s != 0 && !(PAGED && s == MESH_ATTN_ERR_OUT_OF_RANGE);
+}
 
 // The last b of [lo, B) with offsets[b] <= tok, or lo - 1 where there is none, by the calling thread alone.
 __device__ __forceinline__ int last_begun(const int32_t* offsets, int lo, int B, int64_t tok) {

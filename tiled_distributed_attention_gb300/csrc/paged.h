@@ -9,6 +9,9 @@
 
 namespace mesh {
 
+// Rows of a sequence and KV head (new tokens times query heads) up to which the few-rows kernel takes a batch: one product's, and
+// in fp32 what a lane's registers hold.
+constexpr int PAGED_FEW_BF16 = 16, PAGED_FEW_F32 = 8;
 constexpr int PAGED_MAX_B = 4096;  // the few-rows kernel keeps their unit counts in shared memory beside its ring
 
 struct PagedArgs {

@@ -1,19 +1,18 @@
 // Attention over a paged cache for few new tokens a sequence: one of a decoding step, or a few guessed ones.
 //   x = cap tanh(s q.k / cap) (or s q.k) - slope_h (i - j) over the keys j of i - window < j <= i,  O = softmax(x) V.
 //
-// A sequence's rows are its new tokens times the query heads of a KV head, row t g + h; chunks of ROWS of them (16 in
-// bf16: one M = 16 product; 8 in fp32) read the cache once each.  Bound by memory: 16 rows are 32 flops a byte at most.
+// A sequence's rows are its new tokens times the query heads of a KV head, row t g + h, 16 at most in bf16 (one M = 16 product)
+// and 8 in fp32.  Bound by memory: 16 rows are 32 flops a byte.
 //
-// Work split.  The batch's cached tokens, in tiles of 128 over the segments (sequence, KV head, row chunk), are one long
-// list that the CTAs share out evenly: CTA i takes the units [i W / G, (i + 1) W / G), a unit being a tile, or one of
-// the SEG_COST units that stand before each segment for what a segment costs besides its tiles.  So the split does not
-// depend on how ragged the batch is, one long sequence fills the GPU as well as many short ones, and short ones do not
-// pile up in one CTA.  Lengths are read on the device: a captured graph replays with other lengths, tables and pages.  A
-// segment whose tiles fall into one CTA is finished there; of the others every CTA leaves unnormalised sums with their
-// running maxima in a slot of its own (two a CTA: the piece that began before it and the piece that goes on behind it),
-// and the last CTA to arrive adds them up in order, so results do not depend on the arrival order.  At most one segment
-// begins in a CTA and goes on behind it, so a segment's arrival counter is that CTA's: one a CTA, zero between calls (the last
-// CTA puts them back).
+// Work split.  The batch's cached tokens, in tiles of 128 over the segments (sequence, KV head), are one long list that the
+// CTAs share out evenly: CTA i takes the units [i W / G, (i + 1) W / G), a unit being a tile, or one of the SEG_COST units that
+// stand before each segment for what a segment costs besides its tiles.  So the split does not depend on how ragged the batch
+// is, one long sequence fills the GPU as well as many short ones, and short ones do not pile up in one CTA.  Lengths are read
+// on the device: a captured graph replays with other lengths, tables and pages.  A segment whose tiles fall into one CTA is
+// finished there; of the others every CTA leaves unnormalised sums with their running maxima in a slot of its own (two a CTA:
+// the piece that began before it and the piece that goes on behind it), and the last CTA to arrive adds them up in order, so
+// results do not depend on the arrival order.  At most one segment begins in a CTA and goes on behind it, so a segment's
+// arrival counter is that CTA's: one a CTA, zero between calls (the last CTA puts them back).
 //
 // A row's statistics are fp32; sums of P V are fp32.  A warp's 16 tokens of a tile lie in one page (pages are multiples of
 // 16), so a tile costs a warp one look at the table, one tile ahead.  What lies behind a sequence's last token, in its
@@ -40,7 +39,7 @@ constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
 constexpr int WT = 16;            // tokens of a warp in a tile, all in one page
 constexpr int TILE = WARPS * WT;  // tokens of a tile
-constexpr int ROWS = 16;          // rows of a chunk in the buffers (fp32 uses 8 of them)
+constexpr int ROWS = PAGED_FEW_BF16;  // rows of a segment in the buffers (fp32 uses 8 of them)
 constexpr int HALF_ROWS = 8;
 // CTAs an SM: one with 192 KB of ring at d = 128; two at d = 64, whose tiles are half as long and keep one CTA's warps from the
 // memory's rate (64 sequences up to 8,192 tokens, 32 heads on 8: 134 us with one CTA of either depth of ring, 99 with two).
@@ -98,10 +97,6 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
 __device__ __forceinline__ int first_tile(const Params& p, const Seq& s) {
   return p.window ? max(s.len - s.n - p.window + 1, 0) / TILE : 0;
 }
-template <int R>
-__device__ __forceinline__ int chunks_of(const Params& p, const Seq& s) {
-  return (int)(((int64_t)s.n * p.g + R - 1) / R);
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
   const int n = in ? 16 : 0;  // 0: the 16 bytes are zero-filled and src is not read
@@ -137,7 +132,7 @@ struct Piece {
   const int32_t* pages;      // the sequence's row of the table
   const T* q;                // the sequence's first new token, the KV head's first query head
   const float* slopes;       // of the KV head's query heads, or NULL
-  int b, r0, nr;             // the chunk's first row and its rows
+  int b, nr;                 // its rows
   int t0, t1;                // tiles
   int len, pos0;             // cached tokens; the place of the first new token
   int lo;                    // the first token that any of the sequence's rows sees
@@ -152,18 +147,18 @@ template <typename T>
 __device__ __forceinline__ RowMask mask_of(const Params& p, const Piece<T>& c, int r) {
   RowMask m{0, 0, 0, 0.f};
   if (r < c.nr) {
-    const int row = c.r0 + r, t = row / p.g;
+    const int t = r / p.g;
     m.pos = c.pos0 + t;
     m.hi = m.pos + 1;
     m.lo = p.window ? max(0, m.hi - p.window) : 0;
-    if (c.slopes) m.slope2 = c.slopes[row - t * p.g] * LOG2E;
+    if (c.slopes) m.slope2 = c.slopes[r - t * p.g] * LOG2E;
   }
   return m;
 }
 template <typename T>
 __device__ __forceinline__ const T* q_row(const Params& p, const Piece<T>& c, int r) {
-  const int row = c.r0 + r, t = row / p.g;
-  return c.q + t * p.qs[0] + (row - t * p.g) * p.qs[1];
+  const int t = r / p.g;
+  return c.q + t * p.qs[0] + (r - t * p.g) * p.qs[1];
 }
 // The page of the WT tokens from tok0 on, or -1 where none of them is seen (behind the last token, or before a window, whose
 // pages need not be there any more) or where the table names none that exists: recorded, and read as zeros.
@@ -191,7 +186,7 @@ __device__ __forceinline__ float score2(const Params& p, float dot, int far, flo
 template <int D>
 struct EngineBf16 {
   using T = __nv_bfloat16;
-  static constexpr int R = 16;                        // rows of a chunk
+  static constexpr int R = PAGED_FEW_BF16;            // rows of a segment, at most
   static constexpr int CH = D / 8;                    // 16-byte chunks of a row
   static constexpr uint32_t HALF = WT * D * 2;        // K or V of a warp's stage
   static constexpr uint32_t STAGE = 2 * HALF;
@@ -246,8 +241,8 @@ struct EngineBf16 {
       }
     }
     const RowMask mk[2] = {mask_of(p, c, ra), mask_of(p, c, rb)};
-    // tokens that every row of the chunk sees: no mask there
-    const int all_lo = p.window ? max(0, c.pos0 + (c.r0 + c.nr - 1) / p.g + 1 - p.window) : 0, all_hi = c.pos0 + c.r0 / p.g + 1;
+    // tokens that every row sees: no mask there
+    const int all_lo = p.window ? max(0, c.pos0 + (c.nr - 1) / p.g + 1 - p.window) : 0, all_hi = c.pos0 + 1;
     const bool plain = p.cap <= 0.f && !c.slopes;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -667,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
       if (b < p.B) {
         const Seq s = seq_of(p, b);
         if (s.bad && blockIdx.x == 0) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, b);
-        if (s.n > 0) n = (int64_t)chunks_of<R>(p, s) * ((s.len + TILE - 1) / TILE - first_tile(p, s) + SEG_COST);
+        if (s.n > 0) n = (s.len + TILE - 1) / TILE - first_tile(p, s) + SEG_COST;
       }
       int64_t x = n;
 #pragma unroll
@@ -719,17 +714,15 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
       b = a;
     }
     const Seq s = seq_of(p, b);
-    const int chunks = chunks_of<R>(p, s);
-    const int64_t n = (prefix[b + 1] - prefix[b]) / chunks;  // of a segment, > SEG_COST
-    const int64_t seg = (x - prefix[b] * per) / n;
-    const int64_t s1 = prefix[b] * per + (seg + 1) * n, s0 = s1 - n + SEG_COST;  // the segment's tiles are [s0, s1)
+    const int64_t n = prefix[b + 1] - prefix[b];  // of a segment, > SEG_COST
+    const int hk = (int)((x - prefix[b] * per) / n);
+    const int64_t s1 = prefix[b] * per + (hk + 1) * n, s0 = s1 - n + SEG_COST;  // the segment's tiles are [s0, s1)
     const int64_t end = min(hi, s1);
     if (end <= s0) {  // nothing of it but the units before its tiles
       x = end;
       continue;
     }
     x = max(x, s0);
-    const int hk = (int)(seg / chunks), chunk = (int)(seg % chunks);
     Piece<T> c;
     c.b = b;
     c.kb = static_cast<const T*>(p.k) + hk * p.ks[1];
@@ -737,8 +730,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
     c.pages = p.table + b * p.table_s;
     c.q = static_cast<const T*>(p.q) + s.begin * p.qs[0] + (int64_t)hk * p.g * p.qs[1];
     c.slopes = p.slopes ? p.slopes + hk * p.g : nullptr;
-    c.r0 = chunk * R;
-    c.nr = min(R, s.n * p.g - c.r0);
+    c.nr = s.n * p.g;
     const int tile0 = first_tile(p, s);
     c.t0 = tile0 + (int)(x - s0);
     c.t1 = tile0 + (int)(end - s0);
@@ -751,7 +743,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
 
     // a row's output: sums / l, and its LSE
     auto finish = [&](int r, int c4, float4 a, float m, float l) {
-      const int row = c.r0 + r, t = row / p.g, h = hk * p.g + row - t * p.g;
+      const int t = r / p.g, h = hk * p.g + r - t * p.g;
       const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible token: O = 0 (a NaN sum stays NaN)
       const int64_t at = ((int64_t)(s.begin + t) * p.Hq + h) * D + c4;
       if constexpr (sizeof(T) == 2) {
@@ -893,7 +885,7 @@ int launch_paged_rows(const PagedArgs& a, int sms, cudaStream_t st, std::string*
   p.cap = a.cap;
   // a CTA for every tile there may be, no more than are resident
   const int64_t rows = (int64_t)a.max_new * p.g;  // of a sequence and KV head, at most
-  const int64_t tiles = ((int64_t)a.max_pages * a.page + TILE - 1) / TILE * a.B * a.Hkv * ((rows + 7) / 8);
+  const int64_t tiles = ((int64_t)a.max_pages * a.page + TILE - 1) / TILE * a.B * a.Hkv;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, std::min(sms, MAX_SMS) * (a.d == 128 ? CTAS<128> : CTAS<64>)));
   if (a.bf16)
     return a.d == 128 ? launch<EngineBf16<128>, 128>(p, grid, st, err) : launch<EngineBf16<64>, 64>(p, grid, st, err);

@@ -15,7 +15,7 @@
 namespace mesh {
 
 // Whether a sequence's rows (new tokens times query heads of a KV head) go to the few-rows kernel.
-static bool few_rows(bool bf16, int64_t rows) { return rows <= (bf16 ? 16 : 8); }
+static bool few_rows(bool bf16, int64_t rows) { return rows <= (bf16 ? PAGED_FEW_BF16 : PAGED_FEW_F32); }
 
 static size_t paged_workspace(bool bf16, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int64_t max_new) {
   size_t need = paged_rows_slots();

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     wait_for_kernel_before();
     // without any time to wait there is nothing to start: the first load would be waited for
     if (prm.wait_limit_ns <= 0) record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
-    *abort_flag = (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) ? 1 : 0;
+    *abort_flag = stopped<PAGED>(prm.status) ? 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -836,7 +836,7 @@ template <int D, bool PAGED>
 __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_constant__ Params prm) {
   constexpr int Q4 = D / 4, ROWS = MERGE_ROWS<D>, PER_UNIT = 2 * BM / ROWS;
   wait_for_kernel_before();
-  if (*reinterpret_cast<volatile int32_t*>(prm.status) != 0) return;
+  if (stopped<PAGED>(prm.status)) return;
   const int i = (int)blockIdx.x / PER_UNIT;  // unit before the cut
   const int r = (int)blockIdx.x % PER_UNIT * ROWS + (int)threadIdx.x / Q4, c = (int)threadIdx.x % Q4 * 4;
   const Unit x = decode<PAGED>(i * prm.parts, prm, false);

@@ -4,8 +4,9 @@
 //
 // A tile is 64 rows, the query heads of a KV head and their tokens (row = token * g + head), which stream blocks of
 // 64 keys through shared memory; 256 threads hold 4 x 4 scores and 4 x D / 16 outputs each, read operands by
-// 16-byte accesses (12 shared-memory wavefronts for 64 FMAs of the scores, 20 for 128 of the outputs: the FMA pipe is the
-// bound), and keep the row statistics in registers, 16 lanes a row.
+// 16-byte accesses (12 shared-memory wavefronts for 64 FMAs of the scores, 20 for 128 of the outputs: with what else there is
+// the SMs that have most to do keep the FMA pipe busy 40 % of the time and shared memory 58 %), and keep the row statistics in
+// registers, 16 lanes a row.  FMAs in pairs (half the instructions, the weights twice in shared memory) made no difference.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,6 +27,7 @@ constexpr int TR = 64;  // rows of a tile
 constexpr int TK = 64;  // keys of a block
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.69314718055994531f;
+constexpr int MAX_PARTS = 16;
 constexpr int ROLE_SEQ = 1, ROLE_PAGE = 2;
 
 struct Params {
@@ -68,9 +70,10 @@ struct Tile {
 };
 
 // Tile `slot` of KV head hk (and batch entry b; paged: of all sequences) by all threads of a CTA of TR or more; false where
-// there is none.  The last tokens, the longest where the mask is causal, have the first slots.
+// there is none.  The last tokens, the longest where the mask is causal, have the first slots.  With `bounds` (shared memory)
+// its keys too, and what does not fit is reported.
 template <bool PAGED>
-__device__ __forceinline__ bool tile_of(const Params& p, int slot, int hk, int b, bool report, Tile& t, int (&bounds)[2]) {
+__device__ __forceinline__ bool tile_of(const Params& p, int slot, int hk, int b, Tile& t, int* bounds = nullptr) {
   const int tid = threadIdx.x;
   slot = p.tiles - 1 - slot;
   t.hk = hk;
@@ -88,7 +91,7 @@ __device__ __forceinline__ bool tile_of(const Params& p, int slot, int hk, int b
     t.row0 = min(max(o0, 0), p.N);
     n_tok = min(min(max(o1, t.row0), p.N) - t.row0, p.max_new);
     t.len = (int32_t)min((int64_t)max(len, n_tok), (int64_t)p.max_pages * p.page);
-    if (report && tid == 0 && (t.row0 != o0 || n_tok != o1 - o0 || t.len != len))
+    if (bounds && tid == 0 && (t.row0 != o0 || n_tok != o1 - o0 || t.len != len))
       record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, a);
     n_tok = min(n_tok, t.len);
     t.pos0 = t.len - n_tok;
@@ -104,6 +107,7 @@ __device__ __forceinline__ bool tile_of(const Params& p, int slot, int hk, int b
     t.len = (int)p.S;
     t.r0 = slot * TR;
     t.nr = (int)min((int64_t)TR, p.S * p.g - t.r0);
+    if (!bounds) return true;
     if (tid == 0) {
       bounds[0] = 0x7fffffff;
       bounds[1] = 0;
@@ -146,17 +150,17 @@ __device__ __forceinline__ float score2(const Params& p, float dot, int far, flo
 }
 
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1) fwd_kernel(const __grid_constant__ Params p) {
   using Sm = Smem<D>;
   constexpr int CW = D / 16;  // columns of a thread's outputs
   extern __shared__ __align__(16) float sm[];
   __shared__ int bounds[2];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   wait_for_kernel_before();
-  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
+  if (stopped<PAGED>(p.status)) return;
   Tile t;
   const int part = PAGED ? (int)blockIdx.z : (int)blockIdx.z % p.parts;
-  if (!tile_of<PAGED>(p, (int)blockIdx.x, (int)blockIdx.y, PAGED ? 0 : (int)blockIdx.z / p.parts, true, t, bounds)) return;
+  if (!tile_of<PAGED>(p, (int)blockIdx.x, (int)blockIdx.y, PAGED ? 0 : (int)blockIdx.z / p.parts, t, bounds)) return;
   int j_begin, j_end;
   part_of(t, p.parts, part, j_begin, j_end);
   const float* kb = p.k + (PAGED ? 0 : t.b * p.ks[0]) + t.hk * p.ks[1];
@@ -314,36 +318,45 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const __grid_constant__ Pa
   }
 }
 
-// O = sum_t w_t O_t over a tile's parts, w_t = exp(lse_t - lse), and the LSE, parts in order.
+// O = sum_t w_t O_t over a tile's parts, w_t = exp(lse_t - lse), and the LSE, parts in order.  A thread takes a 16-byte piece of a
+// row, all parts' loads in flight together; a CTA a few rows.
+template <int D>
+constexpr int MERGE_ROWS = THREADS / (D / 4);
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(THREADS) merge_kernel(const __grid_constant__ Params p) {
-  __shared__ int bounds[2];
+  constexpr int PER_TILE = TR / MERGE_ROWS<D>;
   wait_for_kernel_before();
-  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
+  if (stopped<PAGED>(p.status)) return;
+  const int slot = (int)blockIdx.x / PER_TILE;
+  const int r = (int)blockIdx.x % PER_TILE * MERGE_ROWS<D> + (int)threadIdx.x / (D / 4), c = (int)threadIdx.x % (D / 4) * 4;
   Tile t;
-  if (!tile_of<PAGED>(p, (int)blockIdx.x, (int)blockIdx.y, (int)blockIdx.z, false, t, bounds)) return;
-  const int64_t tile = ((int64_t)(PAGED ? 0 : t.b) * p.Hkv + t.hk) * p.tiles + blockIdx.x;
-  for (int i = threadIdx.x; i < t.nr * (D / 4); i += THREADS) {
-    const int r = i / (D / 4), c = i % (D / 4) * 4, row = t.r0 + r, tok = row / p.g, h = t.hk * p.g + row - tok * p.g;
-    const int64_t at = tile * p.parts * TR + r;
-    float M = -INFINITY, W = 0.f;
-    for (int k = 0; k < p.parts; ++k) M = fmaxf(M, p.part_lse[at + (int64_t)k * TR]);
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < p.parts; ++k) {
-      const float l = p.part_lse[at + (int64_t)k * TR];
-      if (l == -INFINITY) continue;
-      const float w = expf(l - Ms);
-      const float4 y = *reinterpret_cast<const float4*>(p.part_o + (at + (int64_t)k * TR) * D + c);
-      W += w;
-      o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y), o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
-    }
-    const float inv = W == 0.f ? 0.f : 1.f / W;
-    const int64_t bo = PAGED ? 0 : t.b, to = t.row0 + tok;
-    *reinterpret_cast<float4*>(p.o + bo * p.os[0] + h * p.os[1] + to * p.os[2] + c) =
-        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (c == 0) p.lse[bo * p.ls[0] + h * p.ls[1] + to * p.ls[2]] = W == 0.f ? -INFINITY : Ms + logf(W);
+  if (!tile_of<PAGED>(p, slot, (int)blockIdx.y, (int)blockIdx.z, t) || r >= t.nr) return;
+  const int row = t.r0 + r, tok = row / p.g, h = t.hk * p.g + row - tok * p.g;
+  const int64_t at = (((int64_t)(PAGED ? 0 : t.b) * p.Hkv + t.hk) * p.tiles + slot) * p.parts * TR + r;
+  float w[MAX_PARTS];
+  float4 y[MAX_PARTS];
+  float M = -INFINITY, W = 0.f;
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k) {
+    w[k] = k < p.parts ? p.part_lse[at + (int64_t)k * TR] : -INFINITY;
+    M = fmaxf(M, w[k]);
   }
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k)
+    y[k] = w[k] != -INFINITY ? *reinterpret_cast<const float4*>(p.part_o + (at + (int64_t)k * TR) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float Ms = M == -INFINITY ? 0.f : M;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < MAX_PARTS; ++k) {
+    const float f = expf(w[k] - Ms);
+    W += f;
+    o.x = fmaf(f, y[k].x, o.x), o.y = fmaf(f, y[k].y, o.y), o.z = fmaf(f, y[k].z, o.z), o.w = fmaf(f, y[k].w, o.w);
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;  // a NaN sum stays NaN
+  const int64_t bo = PAGED ? 0 : t.b, to = t.row0 + tok;
+  *reinterpret_cast<float4*>(p.o + bo * p.os[0] + h * p.os[1] + to * p.os[2] + c) =
+      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (c == 0) p.lse[bo * p.ls[0] + h * p.ls[1] + to * p.ls[2]] = W == 0.f ? -INFINITY : Ms + logf(W);
 }
 
 // ---------------------------------------------------------------- backward
@@ -445,18 +458,13 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const float* src, int64_
   }
 }
 
-// dQ of 64 rows (token * g + head) of a batch entry and KV head, over part blockIdx.z of the key blocks that they see.
+// dQ of 64 rows (token * g + head) of a batch entry and KV head, over a part of the key blocks that they see.
 template <int D>
-__global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void dq_tile(const BwdParams& p, float* sm, int (&bounds)[2], int tile, int hk, int b, int part) {
   using Sm = BwdSmem<D>;
   constexpr int CW = D / 16;
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int bounds[2];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  wait_for_kernel_before();
-  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
-  const int b = (int)blockIdx.z / p.dq_parts, part = (int)blockIdx.z % p.dq_parts, hk = (int)blockIdx.y;
-  const int r0 = (p.dq_tiles - 1 - (int)blockIdx.x) * TR, nr = (int)min((int64_t)TR, p.S * p.g - r0);
+  const int r0 = (p.dq_tiles - 1 - tile) * TR, nr = (int)min((int64_t)TR, p.S * p.g - r0);
   if (tid < 2) bounds[tid] = tid ? 0 : 0x7fffffff;
   __syncthreads();
   if (tid < nr) {
@@ -485,19 +493,18 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Bwd
   }
   int lo[4], hi[4], pos[4];
   float slope2[4], nlse[4], dsum[4];
-  int64_t rows[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = r0 + ty * 4 + i, tok = row / p.g, h = row - tok * p.g;
     const bool in = ty * 4 + i < nr;
-    rows[i] = in ? (head0 + h) * p.S + tok : -1;
+    const int64_t at = (head0 + h) * p.S + tok;
     pos[i] = tok;
     lo[i] = in ? max(p.lo[b * p.mask_bs + tok], 0) : 0;
     hi[i] = in ? min(p.hi[b * p.mask_bs + tok], (int)p.S) : 0;
     slope2[i] = in && p.slopes ? p.slopes[hk * p.g + h] * LOG2E : 0.f;
-    const float l = in ? p.lse[rows[i]] : -INFINITY;
+    const float l = in ? p.lse[at] : -INFINITY;
     nlse[i] = l == -INFINITY ? -INFINITY : -l * LOG2E;
-    dsum[i] = in ? p.dsum[rows[i]] : 0.f;
+    dsum[i] = in ? p.dsum[at] : 0.f;
   }
   float o[4][CW];
 #pragma unroll
@@ -529,8 +536,9 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Bwd
   cp_wait_all();  // Q's copies, where no block was read
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (rows[i] < 0) continue;
-    const int64_t at = p.dq_parts > 1 ? (rows[i] / p.S * p.dq_parts + part) * p.S + rows[i] % p.S : rows[i];
+    if (ty * 4 + i >= nr) continue;
+    const int row = r0 + ty * 4 + i, h = row - pos[i] * p.g;
+    const int64_t at = ((head0 + h) * p.dq_parts + part) * p.S + pos[i];
 #pragma unroll
     for (int c = 0; c < CW; c += 4)
       *reinterpret_cast<float4*>(p.dq + at * D + c * 16 + tx * 4) =
@@ -538,19 +546,14 @@ __global__ void __launch_bounds__(THREADS) dq_kernel(const __grid_constant__ Bwd
   }
 }
 
-// dK and dV of 64 keys of a batch entry and KV head, over part blockIdx.z of the blocks of 64 queries of its query heads that
-// may see them: those from the first to the last query that does.
+// dK and dV of 64 keys of a batch entry and KV head, over a part of the blocks of 64 queries of its query heads that may see them:
+// those from the first to the last query that does.
 template <int D>
-__global__ void __launch_bounds__(THREADS) dkdv_kernel(const __grid_constant__ BwdParams p) {
+__device__ __forceinline__ void dkdv_tile(const BwdParams& p, float* sm, int (&bounds)[2], int tile, int hk, int b, int part) {
   using Sm = BwdSmem<D>;
   constexpr int CW = D / 16;
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int bounds[2];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  wait_for_kernel_before();
-  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
-  const int b = (int)blockIdx.z / p.kv_parts, part = (int)blockIdx.z % p.kv_parts, hk = (int)blockIdx.y;
-  const int k0 = (int)blockIdx.x * TK;
+  const int k0 = tile * TK;
   if (tid < 2) bounds[tid] = tid ? 0 : 0x7fffffff;
   __syncthreads();
   {
@@ -640,6 +643,24 @@ __global__ void __launch_bounds__(THREADS) dkdv_kernel(const __grid_constant__ B
   }
 }
 
+// Both in one launch, a CTA a tile and part: those of dK and dV, which take longer, first (one after the other they leave half of
+// the SMs idle at each one's end: 84 us of forward and backward where this takes 69, 777 tokens of 4 heads on 2).
+template <int D>
+__global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1) bwd_kernel(const __grid_constant__ BwdParams p) {
+  extern __shared__ __align__(16) float sm[];
+  __shared__ int bounds[2];
+  wait_for_kernel_before();
+  if (*reinterpret_cast<volatile int32_t*>(p.status) != 0) return;
+  const int n_kv = p.kv_tiles * p.Hkv * p.B * p.kv_parts;
+  int i = (int)blockIdx.x;
+  const bool kv = i < n_kv;
+  if (!kv) i -= n_kv;
+  const int tiles = kv ? p.kv_tiles : p.dq_tiles, parts = kv ? p.kv_parts : p.dq_parts;
+  const int tile = i % tiles, hk = i / tiles % p.Hkv, z = i / tiles / p.Hkv;
+  if (kv) dkdv_tile<D>(p, sm, bounds, tile, hk, z / parts, z % parts);
+  else dq_tile<D>(p, sm, bounds, tile, hk, z / parts, z % parts);
+}
+
 // D = dO . O by rows, D / 4 lanes a row.
 template <int D>
 __global__ void __launch_bounds__(THREADS) dsum_kernel(const float4* o, const float4* go, float* dsum, int64_t rows, int32_t* status) {
@@ -703,7 +724,8 @@ static int launch_fwd(const Params& p, dim3 grid, cudaStream_t st, std::string* 
   static OncePerDevice once;
   cudaError_t e = allow_smem(kern, smem, once);
   if (e == cudaSuccess) e = launch_behind(kern, dim3(grid.x, grid.y, grid.z * p.parts), THREADS, smem, st, p);
-  if (e == cudaSuccess && p.parts > 1) e = launch_behind(merge_kernel<D, PAGED>, grid, THREADS, 0, st, p);
+  if (e == cudaSuccess && p.parts > 1)
+    e = launch_behind(merge_kernel<D, PAGED>, dim3(grid.x * (TR / MERGE_ROWS<D>), grid.y, grid.z), THREADS, 0, st, p);
   if (e != cudaSuccess) *err = std::string("score fp32 forward launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
@@ -712,16 +734,14 @@ template <int D>
 static int launch_bwd(const RangeArgs& a, const RangeBwdShape& z, BwdParams p, cudaStream_t st, std::string* err) {
   const int64_t rows = (int64_t)a.B * a.Hq * a.S;
   const size_t smem = (size_t)BwdSmem<D>::TOTAL * 4;
-  static OncePerDevice once_q, once_kv;
-  cudaError_t e = allow_smem(dq_kernel<D>, smem, once_q);
-  if (e == cudaSuccess) e = allow_smem(dkdv_kernel<D>, smem, once_kv);
+  static OncePerDevice once;
+  cudaError_t e = allow_smem(bwd_kernel<D>, smem, once);
   if (e == cudaSuccess)
     e = launch_behind(dsum_kernel<D>, dim3((unsigned)((rows * (D / 4) + THREADS - 1) / THREADS)), THREADS, 0, st,
                       static_cast<const float4*>(a.o), static_cast<const float4*>(a.go), const_cast<float*>(p.dsum), rows, a.status);
   if (e == cudaSuccess)
-    e = launch_behind(dkdv_kernel<D>, dim3((unsigned)p.kv_tiles, (unsigned)a.Hkv, (unsigned)(a.B * z.kv_parts)), THREADS, smem, st, p);
-  if (e == cudaSuccess)
-    e = launch_behind(dq_kernel<D>, dim3((unsigned)p.dq_tiles, (unsigned)a.Hkv, (unsigned)(a.B * z.dq_parts)), THREADS, smem, st, p);
+    e = launch_behind(bwd_kernel<D>, dim3((unsigned)a.Hkv * (unsigned)a.B * (unsigned)(p.kv_tiles * z.kv_parts + p.dq_tiles * z.dq_parts)),
+                      THREADS, smem, st, p);
   if (e == cudaSuccess && (z.kv_parts > 1 || z.dq_parts > 1)) {
     SumParams sp{};
     const float* parts[3] = {p.dq, p.dk, p.dv};
@@ -750,15 +770,17 @@ static bool grid_fits(int64_t x, int64_t y, int64_t z, std::string* err) {
   return false;
 }
 
-// Tiles are cut into parts of their keys where whole ones would leave SMs idle (two CTAs an SM), of two blocks at least.
+// Tiles are cut into parts of their keys where whole ones would leave SMs idle: down to a block, and to twice the CTAs that are
+// resident (two an SM), since tiles of ragged batches are of very different lengths (777 tokens of 4 heads on 2 in three
+// documents: 22 us; 36 with parts of two blocks and half as many).
 static int32_t fwd_parts(int64_t tiles, int64_t blocks, int sms) {
-  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({2 * sms / std::max<int64_t>(tiles, 1), blocks / 2, 16}));
+  return (int32_t)std::max<int64_t>(1, std::min<int64_t>({4 * sms / std::max<int64_t>(tiles, 1), blocks, simt::MAX_PARTS}));
 }
-size_t score_simt_workspace(int32_t d) { return (size_t)2 * MAX_SMS * simt::TR * (d + 1) * 4; }
+size_t score_simt_workspace(int32_t d) { return (size_t)4 * MAX_SMS * simt::TR * (d + 1) * 4; }
 static void set_parts(simt::Params& p, int64_t tiles, int64_t blocks, int sms, int32_t d, char* ws) {
   p.parts = fwd_parts(tiles, blocks, sms);
   p.part_o = reinterpret_cast<float*>(ws);
-  p.part_lse = p.part_o + (size_t)2 * MAX_SMS * simt::TR * d;
+  p.part_lse = p.part_o + (size_t)4 * MAX_SMS * simt::TR * d;
 }
 
 int launch_paged_simt(const PagedArgs& a, int sms, cudaStream_t st, std::string* err) {
@@ -858,8 +880,7 @@ int launch_range_bwd_simt(const RangeArgs& a, const RangeBwdShape& z, cudaStream
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   p.cap = a.cap;
   const int64_t dq_tiles = (a.S * p.g + simt::TR - 1) / simt::TR, kv_tiles = (a.S + simt::TK - 1) / simt::TK;
-  if (!grid_fits(std::max(dq_tiles, kv_tiles), a.Hkv, (int64_t)a.B * std::max(z.dq_parts, z.kv_parts), err))
-    return (int)cudaErrorInvalidConfiguration;
+  if (!grid_fits((int64_t)a.Hkv * a.B * (kv_tiles * z.kv_parts + dq_tiles * z.dq_parts), 1, 1, err)) return (int)cudaErrorInvalidConfiguration;
   p.dq_tiles = (int32_t)dq_tiles;
   p.kv_tiles = (int32_t)kv_tiles;
   return a.d == 128 ? simt::launch_bwd<128>(a, z, p, st, err) : simt::launch_bwd<64>(a, z, p, st, err);
