@@ -56,11 +56,10 @@ bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
 // Tiles.  All query heads of a KV head in one tile where they and their tokens fill it (3 heads: 42 tokens, 126 rows), else the
 // heads in the fewest equal chunks that do to 7/8.
 //
-// Parts.  The longest unit has to be done, and the SMs share all blocks: a chunk's units see about as many each and go in whole
-// waves, those of a dense batch half of the longest on average, as under a causal mask.  A unit costs about three blocks
-// besides its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of their fp32 rows.  The best count
-// is taken where it saves a fifth or more: 8 units of 512 blocks go in 16 parts; 160 units of up to 20 blocks stay whole (40
-// us; 68 in 2 parts), and 128 of 512 (687 us; 726 in 8 parts).
+// Parts, of range-masked attention (over pages plan_kernel decides by the lengths, which are on the device).  The longest unit has to be
+// done, and the SMs share all blocks, those of a dense batch half of the longest on average, as under a causal mask.  A unit costs about
+// three blocks besides its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of their fp32 rows.  The best
+// count is taken where it saves a fifth or more: 160 units of up to 20 blocks stay whole (40 us; 68 in 2 parts).
 ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms) {
   ScoreFwdShape z{};
   const int g = Hq / Hkv;
@@ -75,22 +74,40 @@ ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32
   const int64_t lanes = (int64_t)Hkv * z.hc * (paged ? 1 : B);
   z.groups = (int32_t)std::min<int64_t>(groups, 0x7fffffff);
   z.lanes = (int32_t)std::min<int64_t>(lanes, 0x7fffffff);
-  const int64_t units = lanes * (paged ? std::max<int64_t>(1, groups - (N % tu == 0 ? 1 : 0)) : groups);
-  const double nb = (double)((S + 127) / 128);
   z.parts = 1;
+  size_t at = 256;  // the counter
+  if (paged) {
+    // room as for the most SMs and whether there is a plan or not, so that a workspace serves smaller batches too
+    const size_t plan = at;
+    at += (PLAN_BYTES + 255) / 256 * 256;
+    const int64_t most = std::min<int64_t>((int64_t)FWD_PART_WAVES * MAX_SMS, lanes * std::min<int64_t>(groups, PLAN_GROUPS) * MAX_FWD_PARTS);
+    z.part_o = at;
+    z.part_lse = at + (size_t)most * 256 * d * 4;
+    at += (size_t)most * 256 * (d + 1) * 4;
+    // Parts may come of it where the longest unit there can be takes 2.5 times the SMs' share of all, half as long on average; with
+    // less the merge's launch (4 us where there is nothing to merge) goes for nothing.  An order is wanted where units wait for an SM, but
+    // those of a single sequence are in order as they come.
+    const int64_t nb = (S + 127) / 128, units = lanes * (N / tu + 1);
+    const bool cut = nb >= 8 && 2 * nb * sms > 5 * units * (nb / 2 + 3);
+    if (groups <= PLAN_GROUPS && (cut || (B > 1 && lanes * groups > sms))) {
+      z.plan = plan;
+      if (cut) z.slots = (int32_t)most;
+    }
+    z.total = at;
+    return z;
+  }
+  const int64_t units = lanes * groups;
+  const double nb = (double)((S + 127) / 128);
   double whole = 0, best = 0;
   for (int k = 1; k <= MAX_FWD_PARTS; ++k) {
-    if (k > 1 && (nb / k < 2 || lanes * groups * k > FWD_PART_WAVES * sms)) break;
-    const double own = nb / k + 3;
-    const double waves = paged ? (double)((units * k + sms - 1) / sms) * own : std::max(own, (double)units * (nb * 0.5 + 3 * k) / sms);
-    const double cost = waves + (k > 1 ? 4 + 0.02 * (double)units * k : 0);
+    if (k > 1 && (nb / k < 2 || units * k > FWD_PART_WAVES * sms)) break;
+    const double cost = std::max(nb / k + 3, (double)units * (nb * 0.5 + 3 * k) / sms) + (k > 1 ? 4 + 0.02 * (double)units * k : 0);
     if (k == 1) whole = best = cost;
     if (cost < best && cost <= 0.8 * whole) {
       best = cost;
       z.parts = k;
     }
   }
-  size_t at = 256;  // the counter
   if (z.parts > 1) {
     const size_t rows = (size_t)z.lanes * z.groups * z.parts * 256;
     z.part_o = at;
@@ -103,9 +120,7 @@ ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32
 }
 
 size_t score_fwd_paged_workspace(int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d) {
-  const ScoreFwdShape z = score_fwd_shape(true, 0, N, B, Hq, Hkv, d, 1);
-  const int64_t units = std::min<int64_t>((int64_t)FWD_PART_WAVES * MAX_SMS, (int64_t)z.lanes * z.groups * MAX_FWD_PARTS);
-  return 256 + (size_t)units * 256 * (d + 1) * 4;
+  return score_fwd_shape(true, 0, N, B, Hq, Hkv, d, 1).total;
 }
 
 int launch_score_fwd(const ScoreFwdArgs& a, int sms, cudaStream_t st, std::string* err) {

@@ -86,6 +86,7 @@ struct Layout {
 };
 static_assert(Layout<128>::ALLOC <= 232448, "shared memory of a CTA");
 
+struct Plan;
 struct Params {
   const float* slopes;
   __nv_bfloat16* o;
@@ -106,15 +107,31 @@ struct Params {
   int64_t S;
   int32_t N, B, Hq, Hkv, g, gh, tt, hc, groups, lanes, batch, n_units, parts;
   int32_t n_pages, page, max_pages, max_new, window, box_rows;
+  Plan* plan;  // paged, or NULL
+  int32_t slots;  // parts that part_o has room for
   float scale_log2;
   Cap cap;
   int64_t wait_limit_ns;
 };
 
+// Paged, up to PLAN_GROUPS groups of tokens: what plan_kernel leaves.  The groups in the order of work, the longest first; each in k
+// parts, of which the first of a lane is part first of all.
+struct Group {
+  int32_t b, tok0, k, slot;  // slot: parts of a lane's split groups before it
+};
+struct Plan {
+  int32_t pieces, groups, split, pad;  // parts of a lane, groups with work, those of them in more than one part (the first ones)
+  int32_t first[PLAN_GROUPS];
+  Group group[PLAN_GROUPS];
+};
+static_assert(sizeof(Plan) == PLAN_BYTES, "the plan in the workspace");
+
 // A unit: its rows are the tokens [tok0, tok0 + 2 tt) below n_tok of query heads h0 .. h0 + gh - 1 (below h_end), its keys the
 // blocks [blk0, blk0 + NB).  Paged: the sequence's first new token is row `row0` of the batch and has the place pos0.
 struct Unit {
-  int u, b, hk, h0, h_end, tok0, n_tok, row0, pos0, len, blk0, NB, part, kmin;  // kmin: the first key that any row sees
+  int u, b, hk, h0, h_end, tok0, n_tok, row0, pos0, len, blk0, NB;
+  int slot;  // of a part of its keys' output in part_o, -1 for all of them
+  int kmin;  // the first key that any row sees
   __device__ __forceinline__ int ntiles(int tt) const { return tok0 + tt < n_tok ? 2 : 1; }
   // Its i-th block: from the one of its last token's own key down to the first, then up from behind it.  So rows meet their own key
   // early, where a causal document or a slope has its largest weights, and the running maximum seldom grows (blocks from the first
@@ -129,39 +146,86 @@ struct Unit {
 };
 __device__ __forceinline__ void put_unit(volatile int32_t* e, const Unit& x) {
   e[0] = x.u, e[1] = x.b, e[2] = x.hk, e[3] = x.h0, e[4] = x.h_end, e[5] = x.tok0, e[6] = x.n_tok, e[7] = x.row0;
-  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.part;  // kmin is the producer's own
+  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.slot;  // kmin is the producer's own
 }
 __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   Unit x;
   x.u = e[0], x.b = e[1], x.hk = e[2], x.h0 = e[3], x.h_end = e[4], x.tok0 = e[5], x.n_tok = e[6], x.row0 = e[7];
-  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.part = e[12], x.kmin = 0;
+  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.slot = e[12], x.kmin = 0;
   return x;
 }
 
-// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone): numbered batch of lanes by batch, within it
-// from the last tokens (the most keys where the mask is causal) to the first, within those lane by lane, its parts together.  A
-// lane is a (batch, KV head, chunk of heads); paged: a (KV head, chunk), whose groups are those of all sequences, sequence b's
-// from offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
-template <bool PAGED>
-__device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
-  Unit x;
-  const int lane = threadIdx.x & 31, tu = 2 * prm.tt;
-  x.u = u;
-  x.part = prm.parts > 1 ? u % prm.parts : -1;
-  int t = prm.parts > 1 ? u / prm.parts : u;
-  const int per = prm.batch * prm.groups, first = t / per * prm.batch;
-  const int lanes = min(prm.batch, prm.lanes - first);  // the last batch may be smaller
-  t %= per;
-  const int grp = prm.groups - 1 - t / lanes;
-  int ln = first + t % lanes;
+// Sequence b of a batch over pages, and the group of tokens from tok0 on: its rows and keys, with what does not fit recorded (where
+// `report`) and taken as the nearest that does.
+__device__ __forceinline__ void sequence(const Params& prm, int b, bool report, Unit& x) {
+  x.b = b;
+  const int32_t o0 = prm.offsets[b], o1 = prm.offsets[b + 1], len = prm.lens[b];
+  x.row0 = min(max(o0, 0), prm.N);
+  x.n_tok = min(min(max(o1, x.row0), prm.N) - x.row0, prm.max_new);
+  const int64_t most = (int64_t)prm.max_pages * prm.page;
+  x.len = (int32_t)min((int64_t)max(len, x.n_tok), most);
+  if (report && (x.row0 != o0 || x.n_tok != o1 - o0 || x.len != len))
+    record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, b);
+  x.n_tok = min(x.n_tok, x.len);
+  x.pos0 = x.len - x.n_tok;
+}
+__device__ __forceinline__ void keys_of(const Params& prm, Unit& x) {  // paged: of its group of tokens
+  const int kmax = x.pos0 + min(x.tok0 + 2 * prm.tt, x.n_tok);
+  x.kmin = prm.window ? max(0, x.pos0 + x.tok0 + 1 - prm.window) : 0;
+  x.blk0 = x.kmin / BN;
+  x.NB = (kmax + BN - 1) / BN - x.blk0;
+}
+// Part `part` of k of its blocks.
+__device__ __forceinline__ void cut(Unit& x, int part, int k) {
+  k = max(1, min(k, x.NB));
+  const int n = x.NB, i = min(part, k), j = min(part + 1, k);
+  x.blk0 += (int)((int64_t)i * n / k);
+  x.NB = (int)((int64_t)j * n / k) - (int)((int64_t)i * n / k);
+}
+__device__ __forceinline__ void heads_of(const Params& prm, int ln, Unit& x) {  // of a lane
   const int c = ln % prm.hc;
   ln /= prm.hc;
   x.hk = ln % prm.Hkv;
   x.b = ln / prm.Hkv;
   x.h0 = x.hk * prm.g + c * prm.gh;
   x.h_end = min(x.h0 + prm.gh, (x.hk + 1) * prm.g);
+}
+
+// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone).  Units are numbered batch of lanes by batch, within it
+// from the last tokens (the most keys where the mask is causal) to the first, or in the plan's order, within those lane by lane,
+// its parts together.  A lane is a (batch, KV head, chunk of heads); paged: a (KV head, chunk), whose groups are those of all
+// sequences, sequence b's from offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
+template <bool PAGED>
+__device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds, const Plan* plan) {
+  Unit x;
+  const int lane = threadIdx.x & 31, tu = 2 * prm.tt;
+  x.u = u;
+  int groups = prm.groups, batch = prm.batch;
+  if (PAGED && plan) {
+    groups = plan->pieces;
+    batch = min(prm.lanes, (3 * (int)gridDim.x + groups - 1) / groups);
+  }
+  int t = prm.parts > 1 ? u / prm.parts : u;
+  const int per = batch * groups, first = t / per * batch;
+  const int lanes = min(batch, prm.lanes - first);  // the last batch may be smaller
+  t %= per;
+  const int idx = t / lanes, grp = prm.groups - 1 - idx, ln = first + t % lanes;
+  heads_of(prm, ln, x);
+  x.slot = prm.parts > 1 ? u : -1;
   x.blk0 = x.NB = x.kmin = 0;
-  int kmin = 0x7fffffff, kmax = 0;  // keys that some row sees
+  if (PAGED && plan) {
+    const int e = last_begun_warp(plan->first, plan->groups, idx);
+    const Group g = plan->group[e];
+    sequence(prm, g.b, false, x);
+    x.tok0 = g.tok0;
+    keys_of(prm, x);
+    if (g.k > 1) {
+      const int part = idx - plan->first[e];
+      x.slot = g.slot * prm.lanes + ln * g.k + part;
+      cut(x, part, g.k);
+    }
+    return x;
+  }
   if (PAGED) {
     // the last b with offsets[b] / tu + b <= grp
     int a = 0, n = prm.B;
@@ -175,68 +239,135 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds) {
       a += (k - 1) * step + 1;
       n = min(step - 1, end - a);
     }
-    x.b = a - 1;
-    if (x.b < 0) {
+    if (a == 0) {
       x.b = 0, x.tok0 = x.n_tok = x.row0 = x.pos0 = x.len = 0;
       return x;
     }
-    const int32_t o0 = prm.offsets[x.b], o1 = prm.offsets[x.b + 1], len = prm.lens[x.b];
-    x.row0 = min(max(o0, 0), prm.N);
-    x.n_tok = min(min(max(o1, x.row0), prm.N) - x.row0, prm.max_new);
-    const int64_t most = (int64_t)prm.max_pages * prm.page;
-    x.len = (int32_t)min((int64_t)max(len, x.n_tok), most);
-    // what does not fit is recorded and taken as the nearest that does
-    if (bounds && lane == 0 && (x.row0 != o0 || x.n_tok != o1 - o0 || x.len != len))
-      record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, x.b);
-    x.n_tok = min(x.n_tok, x.len);
-    x.pos0 = x.len - x.n_tok;
+    sequence(prm, a - 1, bounds && lane == 0, x);
     x.tok0 = (grp - (x.row0 / tu + x.b)) * tu;
     if (x.tok0 < 0 || x.tok0 >= x.n_tok) {  // below 0 where offsets do not ascend
       x.tok0 = x.n_tok = 0;
       return x;
     }
-    if (!bounds) return x;
-    kmax = x.pos0 + min(x.tok0 + tu, x.n_tok);
-    kmin = prm.window ? max(0, x.pos0 + x.tok0 + 1 - prm.window) : 0;
-  } else {
-    x.tok0 = grp * tu;
-    x.n_tok = (int)prm.S;
-    x.row0 = x.pos0 = 0;
-    x.len = (int)prm.S;
-    if (!bounds) return x;
-    const int32_t* lo = prm.lo + x.b * prm.mask_bs;
-    const int32_t* hi = prm.hi + x.b * prm.mask_bs;
-    int a[2 * BM / 32], z[2 * BM / 32];  // all loads in flight together
-#pragma unroll
-    for (int e = 0; e < 2 * BM / 32; ++e) {
-      const int i = e * 32 + lane;
-      const bool in = i < tu && x.tok0 + i < x.n_tok;
-      a[e] = in ? lo[x.tok0 + i] : 0;
-      z[e] = in ? hi[x.tok0 + i] : 0;
-    }
-#pragma unroll
-    for (int e = 0; e < 2 * BM / 32; ++e) {
-      a[e] = max(a[e], 0);
-      z[e] = min(z[e], x.len);
-      if (a[e] < z[e]) {
-        kmin = min(kmin, a[e]);
-        kmax = max(kmax, z[e]);
-      }
-    }
-    kmin = __reduce_min_sync(0xffffffffu, kmin);
-    kmax = __reduce_max_sync(0xffffffffu, kmax);
+    if (bounds) keys_of(prm, x);
+    return x;
   }
+  x.tok0 = grp * tu;
+  x.n_tok = (int)prm.S;
+  x.row0 = x.pos0 = 0;
+  x.len = (int)prm.S;
+  if (!bounds) return x;
+  const int32_t* lo = prm.lo + x.b * prm.mask_bs;
+  const int32_t* hi = prm.hi + x.b * prm.mask_bs;
+  int kmin = 0x7fffffff, kmax = 0;              // keys that some row sees
+  int a[2 * BM / 32], z[2 * BM / 32];  // all loads in flight together
+#pragma unroll
+  for (int e = 0; e < 2 * BM / 32; ++e) {
+    const int i = e * 32 + lane;
+    const bool in = i < tu && x.tok0 + i < x.n_tok;
+    a[e] = in ? lo[x.tok0 + i] : 0;
+    z[e] = in ? hi[x.tok0 + i] : 0;
+  }
+#pragma unroll
+  for (int e = 0; e < 2 * BM / 32; ++e) {
+    a[e] = max(a[e], 0);
+    z[e] = min(z[e], x.len);
+    if (a[e] < z[e]) {
+      kmin = min(kmin, a[e]);
+      kmax = max(kmax, z[e]);
+    }
+  }
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
   if (kmin < kmax) {
     x.kmin = kmin;
     x.blk0 = kmin / BN;
     x.NB = (kmax + BN - 1) / BN - x.blk0;
   }
-  if (x.part >= 0) {
-    const int k = max(1, min(prm.parts, x.NB)), n = x.NB, i = min(x.part, k), j = min(x.part + 1, k);
-    x.blk0 += (int)((int64_t)i * n / k);
-    x.NB = (int)((int64_t)j * n / k) - (int)((int64_t)i * n / k);
-  }
+  if (x.slot >= 0) cut(x, u % prm.parts, prm.parts);
   return x;
+}
+
+// The plan of a batch over pages, by one CTA, a thread a group; it also puts the unit counter to zero.  A batch of chunks and single
+// tokens ends when its longest units do, so those start first: 16 sequences of up to 4,096 tokens, 2,048 new ones in four of them,
+// 16 heads on 4, capped, 86 us, where units as they come take 108-130.  The kernel itself costs a call 3 us.
+//
+// Parts.  The SMs' share of all blocks, three more a group for its start (5 us at 1.6 us a block), is what a group should take.  Those
+// of twice that and more, and of eight blocks or more, are cut into parts of a share, whose outputs merge_kernel adds up (200 new
+// tokens of three sequences of up to 16,000: 63 us; 288 whole).  Parts that save less than half of the longest unit do not pay for
+// their fp32 rows' way through memory.
+template <bool PAGED>
+__global__ void __launch_bounds__(PLAN_GROUPS) plan_kernel(const __grid_constant__ Params prm, int sms) {
+  __shared__ __align__(16) int32_t nb[PLAN_GROUPS];  // blocks of a group, 0 for one without work
+  __shared__ int32_t parts[PLAN_GROUPS], sums[PLAN_GROUPS / 32];  // parts in the order of work; sums of the warps
+  __shared__ unsigned long long total;
+  __shared__ int32_t split, split_parts;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = prm.groups, tu = 2 * prm.tt;
+  if (tid == 0) total = 0ull, split = split_parts = 0;
+  nb[tid] = 0;
+  __syncthreads();
+  wait_for_kernel_before();
+  if (tid == 0) *prm.counter = 0u;
+  Unit x;
+  x.NB = 0;
+  {
+    int a = 0, z = tid < n ? prm.B : 0;  // the last b with offsets[b] / tu + b <= tid, or 0
+    while (z - a > 1) {
+      const int c = (a + z) >> 1;
+      if (max(prm.offsets[c], 0) / tu + c <= tid) a = c;
+      else z = c;
+    }
+    if (tid < n) {
+      sequence(prm, a, true, x);
+      const int64_t t0 = ((int64_t)tid - (x.row0 / tu + a)) * tu;
+      if (t0 >= 0 && t0 < x.n_tok) {
+        x.tok0 = (int)t0;
+        keys_of(prm, x);
+        nb[tid] = x.NB;
+      }
+    }
+    const unsigned c = __reduce_add_sync(0xffffffffu, x.NB ? (unsigned)x.NB + 3u : 0u);
+    if (lane == 0 && c) atomicAdd(&total, (unsigned long long)c);
+  }
+  const int have = __syncthreads_count(x.NB > 0), mine = x.NB;
+  const int64_t share = ((int64_t)total * prm.lanes + sms - 1) / sms;
+  int rank = 0;  // groups with more blocks, or as many and a higher number
+  if (mine) {
+    for (int i = 0; i < n; i += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(nb + i);
+      rank += (o.x > mine || (o.x == mine && i > tid)) + (o.y > mine || (o.y == mine && i + 1 > tid)) +
+              (o.z > mine || (o.z == mine && i + 2 > tid)) + (o.w > mine || (o.w == mine && i + 3 > tid));
+    }
+    parts[rank] = mine >= 8 ? (int)max((int64_t)1, min((int64_t)MAX_PARTS, mine / share)) : 1;
+  }
+  __syncthreads();
+  // those to be split come first, as many as part_o has room for
+  int k = tid < have ? parts[tid] : 1;
+  const int want = k > 1 ? k : 0;
+  int before = want;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  if (lane == 31) sums[warp] = before;
+  __syncthreads();
+  before -= want;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+  if (k > 1 && (int64_t)(before + k) * prm.lanes > prm.slots) k = 1;
+  if (k > 1) {
+    atomicAdd(&split, 1);
+    atomicAdd(&split_parts, k);
+  }
+  __syncthreads();
+  Plan* plan = prm.plan;
+  if (tid < have) {
+    plan->first[tid] = k > 1 ? before : split_parts + tid - split;
+    plan->group[tid].k = k;
+    plan->group[tid].slot = before;
+  }
+  if (mine) plan->group[rank].b = x.b, plan->group[rank].tok0 = x.tok0;
+  if (tid == 0) plan->pieces = split_parts + have - split, plan->groups = have, plan->split = split;
 }
 
 // Keys of a row by its token.
@@ -504,7 +635,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
       }
-      if (x.part < 0) {
+      if (x.slot < 0) {
         uint32_t w[D / 2];
 #pragma unroll
         for (int c = 0; c < D / 2; ++c) w[c] = 0u;
@@ -546,7 +677,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         continue;
       }
       // ---- a part: its normalised output, in fp32
-      const int64_t prow = ((int64_t)x.u * 2 + t) * BM + row;
+      const int64_t prow = ((int64_t)x.slot * 2 + t) * BM + row;
       if (x.NB > 0) {
         float* dst0 = prm.part_o + (prow - lane) * D;
 #pragma unroll 1
@@ -696,6 +827,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int nu = 0, nq = 0, nk = 0;
       bool ok = __all_sync(0xffffffffu, *abort_flag == 0);
       Unit next;
+      const Plan* plan = PAGED ? prm.plan : nullptr;
+      const int n_units = PAGED && plan ? plan->pieces * prm.lanes : prm.n_units;
       // a CTA's first unit is its own index, the others come from the counter; decoded and published to the consumers' ring
       auto publish = [&]() {
         const int slot = nu & 1;
@@ -704,14 +837,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) return;
         int v = (int)blockIdx.x;
         if (nu > 0) {
-          v = prm.n_units;
-          if (prm.n_units > (int)gridDim.x) {
+          v = n_units;
+          if (n_units > (int)gridDim.x) {
             if (lane == 0) v = (int)(gridDim.x + atomicAdd(prm.counter, 1u));
             v = __shfl_sync(0xffffffffu, v, 0);
           }
         }
-        if (v < prm.n_units) {
-          next = decode<PAGED>(v, prm, true);
+        if (v < n_units) {
+          next = decode<PAGED>(v, prm, true, plan);
         } else {
           next.u = -1;
         }
@@ -832,24 +965,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 constexpr int MERGE_THREADS = 256;
 template <int D>
 constexpr int MERGE_ROWS = MERGE_THREADS / (D / 4);
+// A row's 16 bytes: `base` its row of the first of k parts, h and tok its head and token.
 template <int D, bool PAGED>
-__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_constant__ Params prm) {
-  constexpr int Q4 = D / 4, ROWS = MERGE_ROWS<D>, PER_UNIT = 2 * BM / ROWS;
-  wait_for_kernel_before();
-  if (stopped<PAGED>(prm.status)) return;
-  const int i = (int)blockIdx.x / PER_UNIT;  // unit before the cut
-  const int r = (int)blockIdx.x % PER_UNIT * ROWS + (int)threadIdx.x / Q4, c = (int)threadIdx.x % Q4 * 4;
-  const Unit x = decode<PAGED>(i * prm.parts, prm, false);
-  const int t = r / BM, row = r % BM, row_h = row / prm.tt, row_t = row - row_h * prm.tt;
-  const int tok = x.tok0 + t * prm.tt + row_t, h = x.h0 + row_h;
-  if (!(row_h < prm.gh && h < x.h_end && tok < x.n_tok)) return;
-  const int64_t base = ((int64_t)i * prm.parts * 2 + t) * BM + row;  // row of part k: base + 2 k BM
+__device__ __forceinline__ void merge_row(const Params& prm, const Unit& x, int64_t base, int parts, int h, int tok, int c) {
   float w[MAX_PARTS];
   float4 v[MAX_PARTS];
   float M = -INFINITY;
 #pragma unroll
   for (int k = 0; k < MAX_PARTS; ++k) {
-    w[k] = k < prm.parts ? prm.part_lse[base + (int64_t)2 * k * BM] : -INFINITY;
+    w[k] = k < parts ? prm.part_lse[base + (int64_t)2 * k * BM] : -INFINITY;
     M = fmaxf(M, w[k]);
   }
 #pragma unroll
@@ -878,6 +1002,38 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_const
       make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   if (c == 0) prm.lse[bo * prm.ls[0] + h * prm.ls[1] + to * prm.ls[2]] = W == 0.f ? -INFINITY : Ms + logf(W);
 }
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const __grid_constant__ Params prm) {
+  constexpr int Q4 = D / 4, ROWS = MERGE_ROWS<D>, PER_UNIT = 2 * BM / ROWS;
+  wait_for_kernel_before();
+  if (stopped<PAGED>(prm.status)) return;
+  const Plan* plan = prm.plan;
+  const int n = PAGED ? plan->split * prm.lanes * PER_UNIT : (int)gridDim.x;
+  for (int i = (int)blockIdx.x; i < n; i += (int)gridDim.x) {
+    const int unit = i / PER_UNIT;  // before the cut
+    const int r = i % PER_UNIT * ROWS + (int)threadIdx.x / Q4, c = (int)threadIdx.x % Q4 * 4;
+    Unit x;
+    int64_t slot;
+    int parts;
+    if (PAGED) {
+      const Group g = plan->group[unit / prm.lanes];
+      const int ln = unit % prm.lanes;
+      heads_of(prm, ln, x);
+      sequence(prm, g.b, false, x);
+      x.tok0 = g.tok0;
+      slot = (int64_t)g.slot * prm.lanes + ln * g.k;
+      parts = g.k;
+    } else {
+      x = decode<PAGED>(unit * prm.parts, prm, false, nullptr);
+      slot = (int64_t)unit * prm.parts;
+      parts = prm.parts;
+    }
+    const int t = r / BM, row = r % BM, row_h = row / prm.tt;
+    const int tok = x.tok0 + t * prm.tt + row - row_h * prm.tt, h = x.h0 + row_h;
+    if (row_h < prm.gh && h < x.h_end && tok < x.n_tok)
+      merge_row<D, PAGED>(prm, x, (slot * 2 + t) * BM + row, parts, h, tok, c);
+  }
+}
 
 // ------------------------------------------------------------------ host side
 template <int D, int MODE, bool PAGED>
@@ -900,16 +1056,18 @@ static int launch_mode(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
     if (e == cudaSuccess) once.mark(dev);
   }
   // with a CTA for every unit the counter is not read
-  if (e == cudaSuccess && prm.n_units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
+  if (e == cudaSuccess && prm.plan) e = launch_behind(plan_kernel<PAGED>, dim3(1), PLAN_GROUPS, 0, st, prm, sms);
+  else if (e == cudaSuccess && prm.n_units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
   if (e != cudaSuccess) {
     *err = std::string("score_fwd: ") + cudaGetErrorString(e);
     return (int)e;
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(prm.n_units, sms);  // persistent: one CTA per SM
+  // persistent: one CTA per SM
+  const unsigned grid = (unsigned)std::min<int64_t>((int64_t)prm.n_units * (prm.plan ? MAX_PARTS : 1), sms);
   e = launch_behind(kern, dim3(grid), NUM_THREADS, Layout<D>::ALLOC, st, mq, mk, mv, prm);
-  if (e == cudaSuccess && prm.parts > 1)
-    e = launch_behind(merge_kernel<D, PAGED>, dim3((unsigned)(prm.n_units / prm.parts * (2 * BM / MERGE_ROWS<D>))),
-                      MERGE_THREADS, 0, st, prm);
+  if (e == cudaSuccess && (prm.parts > 1 || prm.slots > 0))
+    e = launch_behind(merge_kernel<D, PAGED>,
+                      dim3((unsigned)(PAGED ? 8 * sms : prm.n_units / prm.parts * (2 * BM / MERGE_ROWS<D>))), MERGE_THREADS, 0, st, prm);
   if (e != cudaSuccess) *err = std::string("score_fwd launch: ") + cudaGetErrorString(e);
   return (int)e;
 }
@@ -950,6 +1108,8 @@ static int launch(const ScoreFwdArgs& a, const ScoreFwdShape& z, int sms, cudaSt
   prm.groups = z.groups;
   prm.lanes = z.lanes;
   prm.parts = z.parts;
+  prm.plan = z.plan ? reinterpret_cast<Plan*>(a.ws + z.plan) : nullptr;
+  prm.slots = z.slots;
   const int64_t units = (int64_t)z.lanes * z.groups * z.parts;
   if (units > 0x3fffffff) {
     *err = "too many work units for one launch";

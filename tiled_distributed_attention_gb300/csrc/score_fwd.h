@@ -42,9 +42,14 @@ struct ScoreFwdShape {
   int32_t gh, tt, hc;  // heads and tokens of a tile, chunks of heads
   int32_t groups;      // units of a (batch, KV head, chunk), or of a (KV head, chunk) in paged, that there may be
   int32_t lanes, parts;
-  size_t counter, part_o, part_lse, total;  // workspace
+  int32_t slots;  // paged: parts that there is room for, 0 where none are made
+  size_t counter, plan, part_o, part_lse, total;  // workspace; plan 0 where there is none
 };
 constexpr int MAX_FWD_PARTS = 16, FWD_PART_WAVES = 4;
+// Paged: up to so many groups of tokens of a lane are sorted and long ones cut (score_fwd.cuh); beyond there are several for each SM, and
+// they are taken as they come.
+constexpr int PLAN_GROUPS = 768;
+constexpr size_t PLAN_BYTES = 16 + PLAN_GROUPS * (4 + 16);
 ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms);
 // Enough for any batch of these heads with at most N tokens and B sequences, on any number of SMs.
 size_t score_fwd_paged_workspace(int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d);
