@@ -24,6 +24,12 @@
 // Few units are cut into parts of their keys (score_fwd_shape), whose normalised outputs and LSEs merge_kernel adds up in order.
 // P is rounded to bf16 for its product (2^-9 relative a term), everything else is fp32.
 //
+// Bound by the softmax warps: a block of 256 rows takes them 1.45 us plain (tensor pipe 74 % busy) and 2.3 to 2.5 with a cap
+// (24 %).  Measured, bf16, d 128: 1,024 new tokens over 65,536 cached, 32 heads on 8, 690-740 us (1,480-1,580 TFLOP/s, 128 units
+// on 152 SMs); 16,384 tokens of 16 heads, causal, one document 650 us (1,670), six documents 208 (1,030: units of 17 blocks, of
+// which the change from one to the next costs five, and masked blocks at documents' edges); 2 x 2,500 with prefixes,
+// capped, 53.
+//
 // Every mbarrier wait is bounded: a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT in the status
 // block, every role of the CTA stops, in-flight copies and MMAs are drained and TMEM is freed.
 #pragma once
@@ -114,8 +120,8 @@ struct Params {
   int64_t wait_limit_ns;
 };
 
-// Paged, up to PLAN_GROUPS groups of tokens: what plan_kernel leaves.  The groups in the order of work, the longest first; each in k
-// parts, of which the first of a lane is part first of all.
+// Paged, up to PLAN_GROUPS groups of tokens: what plan_kernel leaves.  The groups in the order of work, the longest first; each
+// in k parts, of which the first of a lane is part first of all.
 struct Group {
   int32_t b, tok0, k, slot;  // slot: parts of a lane's split groups before it
 };
@@ -191,10 +197,11 @@ __device__ __forceinline__ void heads_of(const Params& prm, int ln, Unit& x) {  
   x.h_end = min(x.h0 + prm.gh, (x.hk + 1) * prm.g);
 }
 
-// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone).  Units are numbered batch of lanes by batch, within it
-// from the last tokens (the most keys where the mask is causal) to the first, or in the plan's order, within those lane by lane,
-// its parts together.  A lane is a (batch, KV head, chunk of heads); paged: a (KV head, chunk), whose groups are those of all
-// sequences, sequence b's from offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty (n_tok = 0).
+// Unit u of a launch, decoded by a whole warp (without bounds: its rows alone).  Units are numbered batch of lanes by batch,
+// within it from the last tokens (the most keys where the mask is causal) to the first, or in the plan's order, within those
+// lane by lane, its parts together.  A lane is a (batch, KV head, chunk of heads); paged: a (KV head, chunk), whose groups are
+// those of all sequences, sequence b's from offsets[b] / (2 tt) + b on: each has room for its own there, and a few are empty
+// (n_tok = 0).
 template <bool PAGED>
 __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds, const Plan* plan) {
   Unit x;
@@ -288,14 +295,14 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds, co
   return x;
 }
 
-// The plan of a batch over pages, by one CTA, a thread a group; it also puts the unit counter to zero.  A batch of chunks and single
-// tokens ends when its longest units do, so those start first: 16 sequences of up to 4,096 tokens, 2,048 new ones in four of them,
-// 16 heads on 4, capped, 86 us, where units as they come take 108-130.  The kernel itself costs a call 3 us.
+// The plan of a batch over pages, by one CTA, a thread a group; it also puts the unit counter to zero.  A batch of chunks and
+// single tokens ends when its longest units do, so those start first: 16 sequences of up to 4,096 tokens, 2,048 new ones in
+// four of them, 16 heads on 4, capped, 86 us, where units as they come take 108-130.  The kernel itself costs a call 3 us.
 //
-// Parts.  The SMs' share of all blocks, three more a group for its start (5 us at 1.6 us a block), is what a group should take.  Those
-// of twice that and more, and of eight blocks or more, are cut into parts of a share, whose outputs merge_kernel adds up (200 new
-// tokens of three sequences of up to 16,000: 63 us; 288 whole).  Parts that save less than half of the longest unit do not pay for
-// their fp32 rows' way through memory.
+// Parts.  The SMs' share of all blocks, three more a group for its start (5 us at 1.6 us a block), is what a group should take.
+// Those of twice that and more, and of eight blocks or more, are cut into parts of a share, whose outputs merge_kernel adds up
+// (200 new tokens of three sequences of up to 16,000: 63 us; 288 whole).  Parts that save less than half of the longest unit do
+// not pay for their fp32 rows' way through memory.
 template <bool PAGED>
 __global__ void __launch_bounds__(PLAN_GROUPS) plan_kernel(const __grid_constant__ Params prm, int sms) {
   __shared__ __align__(16) int32_t nb[PLAN_GROUPS];  // blocks of a group, 0 for one without work
