@@ -266,6 +266,50 @@ def test_sequences_that_share_pages(lib):
     check(O, L, ref, "bf16", False)
 
 
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("new, lens, Hq, Hkv", [
+    ([70, 1, 33], [5000, 3000, 40], 4, 1),       # few units over a long cache: all but the short one in parts
+    ([300], [9000], 2, 1),                       # one sequence, groups of nearly one length
+    ([40, 1, 1, 25, 200], [6000, 1, 2500, 25, 1500], 12, 4),  # 3 heads a KV head: 42 tokens a tile
+    ([20] * 12, [130 * i + 20 for i in range(12)], 16, 8),    # more units than parts would pay for
+], ids=str)
+def test_units_of_very_different_lengths(lib, new, lens, Hq, Hkv, window):
+    q, _, _, kp, vp, table, off, ln = cache(new, lens, 32, Hq, Hkv, 128, "bf16", 57)
+    ref = OR.paged(q, kp, vp, table, off, ln, window=window, cap=30.0)
+    args = tuple(t.cuda() for t in (q, kp, vp, table, off, ln))
+    O, L = lib.mesh_paged_attention(*args, max(new), window=window, cap=30.0)
+    check(O, L, ref, "bf16", False)
+    again = lib.mesh_paged_attention(*args, max(new), window=window, cap=30.0)
+    assert torch.equal(O, again[0]) and torch.equal(L, again[1])
+
+
+def test_more_sequences_than_are_sorted(lib):
+    """900 sequences in one call, one of them with a chunk: more groups of tokens than the plan takes."""
+    new, lens = [1] * 450 + [40] + [1] * 449, [1 + 7 * i % 50 for i in range(900)]
+    lens[450] = 75
+    q, _, _, kp, vp, table, off, ln = cache(new, lens, 16, 4, 1, 64, "bf16", 58)
+    ref = OR.paged(q, kp, vp, table, off, ln)
+    O, L = lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), 40)
+    check(O, L, ref, "bf16", False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new, lens", [([1, 1], [900, 131]), ([40, 25], [2000, 500])], ids=str)
+def test_a_recorded_page_keeps_no_later_call_from_its_work(lib, dtype, new, lens):
+    q, _, _, kp, vp, table, off, ln = (t.cuda() for t in cache(new, lens, 16, 8, 2, 64, dtype, 59))
+    ws, st = lib.new_paged_workspace(q, kp, table, max(new)), lib.new_status()
+    keep = dict(workspace=ws, status=st, check_status=False)
+    want = [t.clone() for t in lib.mesh_paged_attention(q, kp, vp, table, off, ln, max(new), **keep)]
+    assert lib.mesh_attn_read_status(st) == 0
+    bad = table.clone()
+    bad[1, 2] = -7
+    got = lib.mesh_paged_attention(q, kp, vp, bad, off, ln, max(new), **keep)
+    assert lib.mesh_attn_read_status(st) == 6  # MESH_ATTN_ERR_OUT_OF_RANGE
+    assert torch.equal(got[0][:new[0]], want[0][:new[0]])  # the other sequence's rows
+    got = lib.mesh_paged_attention(q, kp, vp, table, off, ln, max(new), **keep)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_a_batch_padded_behind(lib):
     """Rows behind the last sequence are left as they are, by both kernels and in both types."""
     for dtype in ("bf16", "f32"):

@@ -309,6 +309,40 @@ def test_streams_graphs_and_two_at_once(lib, dtype):
     assert all(lib.mesh_attn_read_status(s) == 0 for s in stats)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_captured_autograd_step(lib, dtype):
+    """torch.autograd.grad inside a graph, no other autograd graph of the same tensors being alive."""
+    lo, hi = (t.cuda() for t in mask_of("docs", 2, 300))
+    slopes = torch.tensor([0.5, 0.25, 0.125, 0.0625], device="cuda")
+    st = lib.new_status()
+
+    def step(q, k, v, g):
+        O, L = lib.mesh_range_attention_autograd(q, k, v, lo, hi, cap=20.0, slopes=slopes, check_status=False, status=st)
+        return (O.detach(), L, *torch.autograd.grad(O, (q, k, v), g))
+
+    def fresh(seed):
+        return [t.cuda().requires_grad_(i < 3) for i, t in enumerate(inputs(2, 4, 2, 300, 64, dtype, seed))]
+
+    bufs, new = fresh(41), fresh(42)
+    want = step(*new)
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(*bufs)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(*bufs)
+    with torch.no_grad():
+        for b, x in zip(bufs, new):
+            b.copy_(x)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert lib.mesh_attn_read_status(st) == 0
+
+
 def test_waits_that_run_out(lib):
     """Every role stops, copies and products are drained, and the next call in the same context gives the same bits.  Without any time
     nothing starts.  One look at a barrier waits a microsecond or so by itself, which the forward's waits may get by with; in the backward

@@ -1000,5 +1000,6 @@ def mesh_range_attention_autograd(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
                                   scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
                                   check_status: bool = True, status: Optional[torch.Tensor] = None):
     """mesh_range_attention with autograd: returns (O, LSE); O.backward(...) fills the gradients of q, k and v.  With
-    check_status=False a failure in either direction is recorded in `status` (new_status), for the program to read later."""
+    check_status=False a failure in either direction is recorded in `status` (new_status), for the program to read later.  Inside a
+    captured graph take gradients with torch.autograd.grad, while no autograd graph made outside of it holds the same tensors."""
     return MeshRangeAttentionFunction.apply(q, k, v, lo, hi, scale, cap, slopes, check_status, status)
