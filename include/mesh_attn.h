@@ -423,8 +423,8 @@ int mesh_attn_paged_append(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t 
                            const int64_t* pos_strides, int32_t* d_status, void* stream);
 
 /* Bytes of device workspace mesh_attn_paged_attn needs for at most N new tokens of B sequences, max_new of one of them, and these
- * heads.  Caller-allocated, 16-byte aligned, zeroed before its first call; calls leave it fit for the next, whatever its
- * sizes.  Calls that overlap on the GPU, captured graphs among them, need workspaces of their own. */
+ * heads.  Caller-allocated, 16-byte aligned, its first 2,048 bytes zeroed before its first call; calls leave it fit for the next,
+ * whatever its sizes.  Calls that overlap on the GPU, captured graphs among them, need workspaces of their own. */
 int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
                                    int64_t max_new, size_t* bytes);
 

@@ -283,6 +283,17 @@ def test_units_of_very_different_lengths(lib, new, lens, Hq, Hkv, window):
     assert torch.equal(O, again[0]) and torch.equal(L, again[1])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new, lens", [([1, 1], [900, 131]), ([70, 1, 33], [5000, 3000, 40])], ids=str)
+def test_what_a_workspace_holds_behind_its_head_does_not_matter(lib, dtype, new, lens):
+    q, _, _, kp, vp, table, off, ln = (t.cuda() for t in cache(new, lens, 16, 8, 2, 64, dtype, 60))
+    want = lib.mesh_paged_attention(q, kp, vp, table, off, ln, max(new))
+    ws = lib.new_paged_workspace(q, kp, table, max(new))
+    ws[2048:].fill_(255)  # NaN
+    got = lib.mesh_paged_attention(q, kp, vp, table, off, ln, max(new), workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_more_sequences_than_are_sorted(lib):
     """900 sequences in one call, one of them with a chunk: more groups of tokens than the plan takes."""
     new, lens = [1] * 450 + [40] + [1] * 449, [1 + 7 * i % 50 for i in range(900)]

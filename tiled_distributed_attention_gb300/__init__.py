@@ -859,12 +859,14 @@ def mesh_paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tenso
 
 def new_paged_workspace(q: torch.Tensor, k_pages: torch.Tensor, table: torch.Tensor, max_new: int) -> torch.Tensor:
     """Workspace of mesh_paged_attention for batches of at most as many tokens and sequences and at most max_new new tokens of
-    one, zeroed as the first call wants it."""
+    one, its head zeroed as the first call wants it."""
     load_library()
     n = c_sz()
     _check(_lib.mesh_attn_paged_workspace_size(_dtype_code(q.dtype), q.shape[0], table.shape[0], q.shape[1], k_pages.shape[1],
                                                q.shape[2], max_new, ctypes.byref(n)), "mesh_attn_paged_workspace_size")
-    return torch.zeros(max(n.value, 16), dtype=torch.uint8, device=q.device)
+    ws = torch.empty(max(n.value, 2048), dtype=torch.uint8, device=q.device)
+    ws[:2048].zero_()
+    return ws
 
 
 def mesh_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, table: torch.Tensor, offsets: torch.Tensor,

@@ -11,9 +11,11 @@
 // With few tokens the heads are spread over blockIdx.y.  A warp looks its first token's sequence up 32 offsets at a time
 // (one step up to 32 sequences, two up to 1,024), and a lane whose token is of a later one searches on from there.
 //
-// Measured: 16,384 tokens of 8 sequences, 32 + 8 heads, d 128, bf16, 403 MB in 72 us, 5.6 TB/s (a plain copy: 6.8); one token
-// of 64 sequences 6.2 us, most of it the host's call.  Smaller and larger blocks, two and eight heads in flight and fewer
-// registers made no difference to the former.
+// Four or five loads follow one another for that; the first heads' own are issued before them.
+//
+// Measured: 16,384 tokens of 8 sequences, 32 + 8 heads, d 128, bf16, 403 MB in 67.5 us, 6.0 TB/s (a plain copy: 6.8; 71 with
+// the look-up first, and 500 tokens 11 us for 8); one token of 64 sequences 6.2 us, most of it the host's call.  A second set of
+// heads' loads beside the first's stores: 67 us, and 10 for 500 tokens; other block sizes and fewer registers no gain.
 //
 // A token whose place or page does not exist is recorded in the status block and left out; rows from offsets[B] on
 // are left as they are.
@@ -66,18 +68,6 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
   const int64_t lin = (int64_t)blockIdx.x * THREADS + threadIdx.x;
   const int item = (int)(lin % prm.items);
   const int64_t tok = lin / prm.items;
-  const int b = sequence_of(prm.offsets, prm.B, __shfl_sync(0xffffffffu, tok, 0), tok);
-  if (b < 0 || tok >= prm.N) return;
-  const int32_t begin = prm.offsets[b], len = prm.lens[b];
-  const int64_t place = (int64_t)len - prm.offsets[b + 1] + tok;  // len - n + (tok - begin)
-  int32_t at = -1;
-  if (tok >= begin && place >= 0 && place < (int64_t)prm.max_pages * prm.page)
-    at = prm.table[b * prm.table_s + place / prm.page];
-  if (at < 0 || at >= prm.n_pages) {
-    if (item == 0) record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_TOKEN, (int32_t)b);
-    return;
-  }
-  const int64_t row = place % prm.page;
   constexpr int NP = Item<V, ADJ>::PAIRS;
   constexpr bool TWO = Item<V, ADJ>::TWO;
   const int rot = prm.n / NP;                      // rotation items of a group
@@ -96,6 +86,42 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
     c0 += r * V;
     c1 = c0 + prm.n;
   }
+  // this block's heads of q, then those of k, then those of v, a few at a time: heads h .. h + n - 1 of tensor w, their loads
+  // in flight together.  The first ones' are on their way before the token's page is looked up
+  using Vc = Vec<T, V>;
+  constexpr int U = 4;
+  Vc a[U], c[U];
+  int left = min(prm.heads_per_block, prm.H[0] + prm.H[1] + prm.H[2] - (int)blockIdx.y * prm.heads_per_block);
+  int w = 0, h = (int)blockIdx.y * prm.heads_per_block, n = 0;
+  auto next = [&]() {
+    while (w < 2 && h >= prm.H[w]) h -= prm.H[w++];
+    n = min(min(U, left), prm.H[w] - h);
+  };
+  auto load = [&]() {
+    const T* src = static_cast<const T*>(prm.x[w]) + tok * prm.xs[w][0] + h * prm.xs[w][1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u < n) {
+        a[u] = *reinterpret_cast<const Vc*>(src + c0);
+        if (TWO && !copy) c[u] = *reinterpret_cast<const Vc*>(src + c1);
+      }
+      src += prm.xs[w][1];
+    }
+  };
+  next();
+  if (tok < prm.N) load();
+  const int b = sequence_of(prm.offsets, prm.B, __shfl_sync(0xffffffffu, tok, 0), tok);
+  if (b < 0 || tok >= prm.N) return;
+  const int32_t begin = prm.offsets[b], len = prm.lens[b];
+  const int64_t place = (int64_t)len - prm.offsets[b + 1] + tok;  // len - n + (tok - begin)
+  int32_t at = -1;
+  if (tok >= begin && place >= 0 && place < (int64_t)prm.max_pages * prm.page)
+    at = prm.table[b * prm.table_s + place / prm.page];
+  if (at < 0 || at >= prm.n_pages) {
+    if (item == 0) record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_TOKEN, (int32_t)b);
+    return;
+  }
+  const int64_t row = place % prm.page;
   float cs[NP], sn[NP];
   if (!copy) {
     int have = -1;
@@ -114,54 +140,38 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
       sincospif((float)half_turns * 0x1p-31f, &sn[i], &cs[i]);
     }
   }
-  using Vc = Vec<T, V>;
-  constexpr int U = 4;  // heads whose loads are in flight together
-  // this block's heads of q, then those of k, then those of v
-  const int h_begin = (int)blockIdx.y * prm.heads_per_block, h_stop = h_begin + prm.heads_per_block;
-  int before = 0;
 #pragma unroll 1
-  for (int w = 0; w < 3; ++w) {
-    int h = max(h_begin - before, 0);
-    const int h_end = min(h_stop - before, prm.H[w]);
-    before += prm.H[w];
-    if (h >= h_end) continue;
-    const int64_t xh = prm.xs[w][1], yh = w == 0 ? prm.qs[1] : prm.ps[w - 1][1];
-    const T* src = static_cast<const T*>(prm.x[w]) + tok * prm.xs[w][0] + h * xh;
+  for (;;) {
+    const int64_t yh = w == 0 ? prm.qs[1] : prm.ps[w - 1][1];
     T* dst = static_cast<T*>(prm.y[w]) + (w == 0 ? tok * prm.qs[0] : at * prm.ps[w - 1][0] + row * prm.ps[w - 1][2]) + h * yh;
     const bool turn = !copy && w < 2;
-    for (; h < h_end; h += U) {
-      Vc a[U], c[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h + u < h_end) {
-          a[u] = *reinterpret_cast<const Vc*>(src + c0);
-          if (TWO && !copy) c[u] = *reinterpret_cast<const Vc*>(src + c1);
-        }
-        src += xh;
-      }
+    for (int u = 0; u < U; ++u) {
+      if (u < n) {
+        if (turn) {
+          float xa[V], xc[V];
+          rope::widen(a[u], xa);
+          if (TWO) rope::widen(c[u], xc);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h + u < h_end) {
-          if (turn) {
-            float xa[V], xc[V];
-            rope::widen(a[u], xa);
-            if (TWO) rope::widen(c[u], xc);
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              const int i0 = TWO ? i : (2 * i) % V, i1 = TWO ? i : (2 * i + 1) % V;
-              const float x0 = xa[i0], x1 = TWO ? xc[i1] : xa[i1];
-              xa[i0] = fmaf(x0, cs[i], -x1 * sn[i]);
-              (TWO ? xc[i1] : xa[i1]) = fmaf(x1, cs[i], x0 * sn[i]);
-            }
-            rope::narrow(xa, a[u]);
-            if (TWO) rope::narrow(xc, c[u]);
+          for (int i = 0; i < NP; ++i) {
+            const int i0 = TWO ? i : (2 * i) % V, i1 = TWO ? i : (2 * i + 1) % V;
+            const float x0 = xa[i0], x1 = TWO ? xc[i1] : xa[i1];
+            xa[i0] = fmaf(x0, cs[i], -x1 * sn[i]);
+            (TWO ? xc[i1] : xa[i1]) = fmaf(x1, cs[i], x0 * sn[i]);
           }
-          *reinterpret_cast<Vc*>(dst + c0) = a[u];
-          if (TWO && !copy) *reinterpret_cast<Vc*>(dst + c1) = c[u];
+          rope::narrow(xa, a[u]);
+          if (TWO) rope::narrow(xc, c[u]);
         }
-        dst += yh;
+        *reinterpret_cast<Vc*>(dst + c0) = a[u];
+        if (TWO && !copy) *reinterpret_cast<Vc*>(dst + c1) = c[u];
       }
+      dst += yh;
     }
+    left -= n;
+    if (left == 0) return;
+    h += n;
+    next();
+    load();
   }
 }
 
