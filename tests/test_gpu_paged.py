@@ -304,6 +304,20 @@ def test_more_sequences_than_are_sorted(lib):
     check(O, L, ref, "bf16", False)
 
 
+def test_offsets_that_do_not_fit_in_a_sorted_batch(lib):
+    """Offsets beyond the batch, not ascending and negative where groups are sorted and cut: recorded, and the next call is right."""
+    q, _, _, kp, vp, table, off, ln = (t.cuda() for t in cache([30, 1, 40], [300, 200, 2000], 16, 64, 64, 64, "bf16", 61))
+    ws, st = lib.new_paged_workspace(q, kp, table, 40), lib.new_status()
+    keep = dict(workspace=ws, status=st, check_status=False)
+    want = [t.clone() for t in lib.mesh_paged_attention(q, kp, vp, table, off, ln, 40, **keep)]
+    assert lib.mesh_attn_read_status(st) == 0
+    for bad in ([0, 30, 90, 90], [71, 1, 0, 2], [-4, 1, 2, 3], [1 << 30, 0, -(1 << 30), 5]):
+        lib.mesh_paged_attention(q, kp, vp, table, torch.tensor(bad, dtype=torch.int32, device="cuda"), ln, 40, **keep)
+        assert lib.mesh_attn_read_status(st) == 6  # MESH_ATTN_ERR_OUT_OF_RANGE
+        got = lib.mesh_paged_attention(q, kp, vp, table, off, ln, 40, **keep)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("new, lens", [([1, 1], [900, 131]), ([40, 25], [2000, 500])], ids=str)
 def test_a_recorded_page_keeps_no_later_call_from_its_work(lib, dtype, new, lens):
