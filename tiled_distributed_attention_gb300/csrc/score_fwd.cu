@@ -53,13 +53,17 @@ bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
   return true;
 }
 
+// Units are two tiles, whose products and softmax go on beside one another; one where that leaves an SM idle for each (2 x 1,000
+// tokens of 4 heads, d 64, slopes: forward 18 us, 21 with two).
+//
 // Tiles.  All query heads of a KV head in one tile where they and their tokens fill it (3 heads: 42 tokens, 126 rows), else the
 // heads in the fewest equal chunks that do to 7/8.
 //
-// Parts, of range-masked attention (over pages plan_kernel decides by the lengths, which are on the device).  The longest unit has to be
-// done, and the SMs share all blocks, those of a dense batch half of the longest on average, as under a causal mask.  A unit costs about
-// three blocks besides its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of their fp32 rows.  The best
-// count is taken where it saves a fifth or more: 160 units of up to 20 blocks stay whole (40 us; 68 in 2 parts).
+// Parts, of range-masked attention (over pages plan_kernel decides by the lengths, which are on the device).  The longest unit
+// has to be done, and the SMs share all blocks, those of a dense batch half of the longest on average, as under a causal mask.
+// A unit costs about three blocks besides its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of
+// their fp32 rows.  The best count is taken where it saves a fifth or more: 160 units of up to 20 blocks stay whole (40 us; 68
+// in 2 parts).
 ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms) {
   ScoreFwdShape z{};
   const int g = Hq / Hkv;
@@ -69,12 +73,18 @@ ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32
     if (z.gh * z.tt >= 112) break;
   }
   z.hc = (g + z.gh - 1) / z.gh;
-  const int64_t tu = 2 * z.tt;
+  z.tu = 2 * z.tt;
+  const int64_t tu = z.tu;
   const int64_t groups = paged ? N / tu + B : (S + tu - 1) / tu;
   const int64_t lanes = (int64_t)Hkv * z.hc * (paged ? 1 : B);
   z.groups = (int32_t)std::min<int64_t>(groups, 0x7fffffff);
   z.lanes = (int32_t)std::min<int64_t>(lanes, 0x7fffffff);
   z.parts = 1;
+  // units of one tile where there is an SM for each: a block of one takes less time than a block of two
+  auto one_tile = [&](int64_t n) {
+    z.tu = z.tt;
+    z.groups = (int32_t)n;
+  };
   size_t at = 256;  // the counter
   if (paged) {
     // room as for the most SMs and whether there is a plan or not, so that a workspace serves smaller batches too
@@ -85,13 +95,15 @@ ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32
     z.part_lse = at + (size_t)most * 256 * d * 4;
     at += (size_t)most * 256 * (d + 1) * 4;
     // Parts may come of it where the longest unit there can be takes 2.5 times the SMs' share of all, half as long on average; with
-    // less the merge's launch (4 us where there is nothing to merge) goes for nothing.  An order is wanted where units wait for an SM, but
-    // those of a single sequence are in order as they come.
+    // less the merge's launch (4 us where there is nothing to merge) goes for nothing.  An order is wanted where units wait for
+    // an SM, but those of a single sequence are in order as they come.
     const int64_t nb = (S + 127) / 128, units = lanes * (N / tu + 1);
     const bool cut = nb >= 8 && 2 * nb * sms > 5 * units * (nb / 2 + 3);
     if (groups <= PLAN_GROUPS && (cut || (B > 1 && lanes * groups > sms))) {
       z.plan = plan;
       if (cut) z.slots = (int32_t)most;
+    } else if (lanes * (N / z.tt + B) <= sms) {
+      one_tile(N / z.tt + B);
     }
     z.total = at;
     return z;
@@ -108,6 +120,7 @@ ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32
       z.parts = k;
     }
   }
+  if (z.parts == 1 && 2 * units <= sms) one_tile((S + z.tt - 1) / z.tt);
   if (z.parts > 1) {
     const size_t rows = (size_t)z.lanes * z.groups * z.parts * 256;
     z.part_o = at;

@@ -111,7 +111,7 @@ struct Params {
   const int32_t* table;
   int64_t table_s;
   int64_t S;
-  int32_t N, B, Hq, Hkv, g, gh, tt, hc, groups, lanes, batch, n_units, parts;
+  int32_t N, B, Hq, Hkv, g, gh, tt, tu, hc, groups, lanes, batch, n_units, parts;
   int32_t n_pages, page, max_pages, max_new, window, box_rows;
   Plan* plan;  // paged, or NULL
   int32_t slots;  // parts that part_o has room for
@@ -176,7 +176,7 @@ __device__ __forceinline__ void sequence(const Params& prm, int b, bool report, 
   x.pos0 = x.len - x.n_tok;
 }
 __device__ __forceinline__ void keys_of(const Params& prm, Unit& x) {  // paged: of its group of tokens
-  const int kmax = x.pos0 + min(x.tok0 + 2 * prm.tt, x.n_tok);
+  const int kmax = x.pos0 + min(x.tok0 + prm.tu, x.n_tok);
   x.kmin = prm.window ? max(0, x.pos0 + x.tok0 + 1 - prm.window) : 0;
   x.blk0 = x.kmin / BN;
   x.NB = (kmax + BN - 1) / BN - x.blk0;
@@ -205,7 +205,7 @@ __device__ __forceinline__ void heads_of(const Params& prm, int ln, Unit& x) {  
 template <bool PAGED>
 __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds, const Plan* plan) {
   Unit x;
-  const int lane = threadIdx.x & 31, tu = 2 * prm.tt;
+  const int lane = threadIdx.x & 31, tu = prm.tu;
   x.u = u;
   int groups = prm.groups, batch = prm.batch;
   if (PAGED && plan) {
@@ -257,10 +257,11 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds, co
       return x;
     }
     if (bounds) keys_of(prm, x);
+    x.n_tok = min(x.n_tok, x.tok0 + tu);
     return x;
   }
   x.tok0 = grp * tu;
-  x.n_tok = (int)prm.S;
+  x.n_tok = min((int)prm.S, x.tok0 + tu);
   x.row0 = x.pos0 = 0;
   x.len = (int)prm.S;
   if (!bounds) return x;
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(PLAN_GROUPS) plan_kernel(const __grid_constant
   __shared__ int32_t parts[PLAN_GROUPS], sums[PLAN_GROUPS / 32];  // parts in the order of work; sums of the warps
   __shared__ unsigned long long total;
   __shared__ int32_t split, split_parts;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = prm.groups, tu = 2 * prm.tt;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = prm.groups, tu = prm.tu;
   if (tid == 0) total = 0ull, split = split_parts = 0;
   nb[tid] = 0;
   __syncthreads();
@@ -1111,6 +1112,7 @@ static int launch(const ScoreFwdArgs& a, const ScoreFwdShape& z, int sms, cudaSt
   prm.g = a.Hq / a.Hkv;
   prm.gh = z.gh;
   prm.tt = z.tt;
+  prm.tu = z.tu;
   prm.hc = z.hc;
   prm.groups = z.groups;
   prm.lanes = z.lanes;

@@ -40,6 +40,7 @@ struct ScoreFwdArgs {
 // (two tiles) are cut.
 struct ScoreFwdShape {
   int32_t gh, tt, hc;  // heads and tokens of a tile, chunks of heads
+  int32_t tu;          // tokens of a unit
   int32_t groups;      // units of a (batch, KV head, chunk), or of a (KV head, chunk) in paged, that there may be
   int32_t lanes, parts;
   int32_t slots;  // paged: parts that there is room for, 0 where none are made
