@@ -3,12 +3,14 @@
 // score_fwd.cuh and score_bwd.cuh; everything is fp32, sums in the order of the keys.
 //
 // A tile is 64 rows, the query heads of a KV head and their tokens (row = token * g + head), which stream blocks of
-// 64 keys through shared memory; 256 threads hold 4 x 4 scores and 4 x D / 16 outputs each, read operands by
-// 16-byte accesses (12 shared-memory wavefronts for 64 FMAs of the scores, 20 for 128 of the outputs: with what else there is
-// the SMs that have most to do keep the FMA pipe busy 40 % of the time and shared memory 58 %), and keep the row statistics in
-// registers, 16 lanes a row.  FMAs in pairs (half the instructions, the weights twice in shared memory) made no difference, 8 x 4
-// scores a thread were 5 to 15 % slower.  Measured: 777 tokens in three documents, 4 heads on 2, d 64, capped, slopes, both
-// directions 66 us; 2 x 1,024, 8 heads on 2, causal, 366 (20 TFLOP/s), at d = 128 659 (23).
+// 64 keys through shared memory; 256 threads hold 4 x 4 scores and 4 x D / 16 outputs each, read operands by 16-byte accesses
+// and keep the row statistics in registers, 16 lanes a row.
+//
+// Bound by those accesses: a warp's 16 bytes a lane take four cycles of the SM's 128 bytes a cycle, whichever rows they are of, and
+// eight of them stand before 64 FMAs, so that the FMA pipe is busy half of the time (measured 52 %).  In keeping with that, FMAs in
+// pairs (half the instructions) and warps of 4 x 8 threads (fewer distinct rows an access) made no difference; 8 x 4 scores a
+// thread have fewer accesses but half the warps, and were 5 to 15 % slower.  Measured: 777 tokens in three documents, 4 heads
+// on 2, d 64, capped, slopes, both directions 66 us; 2 x 1,024, 8 heads on 2, causal, 358 (21 TFLOP/s), at d = 128 650 (23).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1) fwd_kernel(const __g
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < D; c += 4) {
       float4 a[4], b[4];
 #pragma unroll
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, D == 64 ? 2 : 1) fwd_kernel(const __g
       for (int c = 0; c < CW; ++c) o[i][c] *= f;
     }
     __syncwarp();  // a row's weights are its own half-warp's
-#pragma unroll 2
+#pragma unroll 4
     for (int k0 = 0; k0 < TK; k0 += 4) {
       float4 w[4];
 #pragma unroll
@@ -411,7 +413,7 @@ __device__ __forceinline__ void rows_by_rows(const float* a_s, const float* b_s,
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = 0; c < D; c += 4) {
     float4 a[4], b[4];
 #pragma unroll
@@ -429,7 +431,7 @@ __device__ __forceinline__ void rows_by_rows(const float* a_s, const float* b_s,
 template <int D>
 __device__ __forceinline__ void weights_by_rows(const float* w_s, const float* x_s, int tx, int ty, float (&o)[4][D / 16]) {
   constexpr int LD = D + 4, LP = TK + 4;
-#pragma unroll 2
+#pragma unroll 4
   for (int k0 = 0; k0 < TK; k0 += 4) {
     float4 w[4];
 #pragma unroll
