@@ -1,0 +1,47 @@
+"""Range-masked attention at bounds, scores and caps of any size, both directions, against the fp64 oracle.  Bounds as in
+test_gpu_range.py."""
+import pytest
+import torch
+
+from oracle import range_attention as OR
+from tests.test_gpu_range import check_grads, check_out, dev, inputs, mask_of, slopes_of, within
+
+pytestmark = pytest.mark.gpu
+
+LOW, HIGH = torch.iinfo(torch.int32).min, torch.iinfo(torch.int32).max
+
+
+def both(lib, q, k, v, g, lo, hi, dtype, n, **kw):
+    """Both directions by the kernels, checked against the oracle."""
+    qd, kd, vd, gd, lod, hid = dev(q, k, v, g, lo, hi)
+    kd_ = {a: x.cuda() if torch.is_tensor(x) else x for a, x in kw.items()}
+    O, L = lib.mesh_range_attention(qd, kd, vd, lod, hid, **kd_)
+    check_out(O, L, OR.forward(q, k, v, lo, hi, **kw), dtype, n)
+    grads = lib.mesh_range_attention_backward(qd, kd, vd, lod, hid, O, L, gd, **kd_)
+    check_grads(grads, OR.backward(q, k, v, g, lo, hi, **kw), dtype, n, q.shape[1] // k.shape[1])
+
+
+def far_mask(kind, S):
+    i = torch.arange(S, dtype=torch.int32)
+    if kind == "causal":  # no lower bound
+        return torch.full_like(i, LOW), i + 1
+    if kind == "all":  # none at all
+        return torch.full_like(i, LOW), torch.full_like(i, HIGH)
+    if kind == "padding":  # rows behind that see nothing, as far out as it goes
+        lo, hi = torch.full_like(i, LOW + 1), i + 1
+        lo[S - 70:], hi[S - 70:] = HIGH, LOW
+        return lo, hi
+    lo, hi = torch.clamp(i - 36, min=0), i + 1  # every bound there is, row beside row
+    lo[1::7], lo[2::7], lo[3::7], lo[4::7] = LOW, LOW + 130, -1, HIGH
+    hi[1::5], hi[2::5], hi[3::5] = HIGH, HIGH - 130, LOW
+    return lo, hi
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["causal", "all", "padding", "mixed"])
+@pytest.mark.parametrize("S, d", [(100, 64), (300, 128), (700, 64)], ids=str)
+def test_bounds_of_any_size(lib, S, d, kind, dtype):
+    """Bounds outside 0 .. S are the nearer bound, down to the type's lowest value and up to its highest."""
+    q, k, v, g = inputs(1, 4, 2, S, d, dtype, 70)
+    lo, hi = far_mask(kind, S)
+    both(lib, q, k, v, g, lo, hi, dtype, S)

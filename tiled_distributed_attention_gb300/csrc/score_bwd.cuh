@@ -284,6 +284,10 @@ struct Cursor {
   }
 };
 
+// A row's bound as the nearest that there is: it may be any 32-bit number, from which a block's first key or another bound could not
+// be taken.
+__device__ __forceinline__ int clip(int bound, int64_t S) { return min(max(bound, 0), (int)S); }
+
 // 64 scores of consecutive columns to weights, MODE 0 plain, 1 slopes, 2 cap (and slopes where given); `reload` fetches the scores
 // again for a higher tier of the cap:
 //   P = 2^(x + nl(c)), nl(c) being -LSE in base 2 of columns c and c + 1, and |i - j| = |c + off|.
@@ -488,7 +492,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
             // no such query row, or one that sees nothing: exp2(s - inf) = 0, so it needs no mask
             nlse_s[vb * BM + row] = raw_in && raw_lse != -INFINITY ? -raw_lse * LOG2E : -INFINITY;
             ndsum_s[vb * BM + row] = raw_in ? -raw_d : 0.f;
-            const int a = min(max(raw_lo - k0, 0), BM), z = min(max(raw_hi - k0, a), BM);
+            const int a = min(max(clip(raw_lo, S) - k0, 0), BM), z = min(max(clip(raw_hi, S) - k0, a), BM);
             rng_s[vb * BM + row] = (uint16_t)(a | (z - a) << 8);
             mbar_arrive(bar(Ly::B_VEC + vb));
           }
@@ -653,7 +657,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
         // a row that is not there, or sees nothing: weights of 0
         const float nlse = row_in && raw_lse != -INFINITY ? -raw_lse * LOG2E : -INFINITY;
         const float dsum = row_in ? raw_d : 0.f, slope2 = raw_slope;
-        const int lo = raw_lo, hi = min(raw_hi, (int)S), all_lo = raw_all_lo, all_hi = raw_all_hi;
+        const int lo = clip(raw_lo, S), hi = clip(raw_hi, S), all_lo = raw_all_lo, all_hi = raw_all_hi;
         const int q = x.blk * BM + row;
         const uint64_t nl2 = f2_pack(nlse, nlse), nd2 = f2_pack(-dsum, -dsum);
         for (int j = 0; j < x.NB && ok; ++j) {
