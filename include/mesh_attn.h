@@ -440,7 +440,8 @@ int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, 
  * Tokens of a page from the sequence's length on never reach a result, NaN or not; with a window, pages wholly before all
  * new tokens' windows (16 tokens of one, or a power of two that divides the page, at a time) are not read and need not exist.
  * Another page that does not exist is recorded and read as zeros.  MESH_ATTN_ERR_OUT_OF_RANGE in the status block keeps
- * neither the other sequences nor later calls from their work; after another error outputs are not to be used. */
+ * neither the other sequences nor later calls over pages from their work (range-masked and plain attention do nothing where their
+ * block holds any error: they want another one).  Another error takes its place; outputs are then not to be used. */
 int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, const void* q,
                          const int64_t* q_strides, int32_t n_pages, int32_t page, const void* k_pages, const int64_t* k_strides,
                          const void* v_pages, const int64_t* v_strides, const int32_t* table, int32_t max_pages,

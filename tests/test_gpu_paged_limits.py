@@ -1,0 +1,37 @@
+"""Attention over a paged cache at the limits of its lengths, bounds, windows and status block, against the fp64 oracle.  Bounds as in
+test_gpu_paged.py."""
+import pytest
+import torch
+
+from tests.test_gpu_paged import cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("new, lens, Hq", [([700, 1], [1500, 60], 8), ([70, 1, 33], [5000, 3000, 40], 4)], ids=str)
+def test_a_timeout_behind_a_recorded_page(lib, new, lens, Hq):
+    """A status block that holds what an earlier call recorded takes a wait that runs out all the same, parts that were never written are not
+    added up, and what comes behind does nothing."""
+    args = tuple(t.cuda() for t in (cache(new, lens, 16, Hq, 1, 128, "bf16", 83)[i] for i in (0, 3, 4, 5, 6, 7)))
+    want = lib.mesh_paged_attention(*args, max(new))
+    ws = lib.new_paged_workspace(args[0], args[1], args[3], max(new))
+    for limit in (0, 1, 2_000, 20_000):
+        st = torch.tensor([6, 1, 0, 0], dtype=torch.int32, device="cuda")
+        O, L = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+        lib.mesh_attn_set_wait_limit_ns(limit)
+        try:
+            lib.mesh_paged_attention(*args, max(new), O=O, LSE=L, workspace=ws, status=st, check_status=False)
+            code = lib.mesh_attn_read_status(st)
+        finally:
+            lib.mesh_attn_set_wait_limit_ns(2_000_000_000)
+        assert code in ((5,) if limit == 0 else (5, 6)), limit
+        if limit == 0:
+            assert (O == 7).all() and (L == 7).all()
+        if code == 6:
+            assert torch.equal(O, want[0]) and torch.equal(L, want[1])
+            continue
+        O.fill_(7.0)
+        lib.mesh_paged_attention(*args, max(new), O=O, LSE=L, workspace=ws, status=st, check_status=False)
+        assert lib.mesh_attn_read_status(st) == 5 and (O == 7).all()
+    O, L = lib.mesh_paged_attention(*args, max(new), workspace=ws)
+    assert torch.equal(O, want[0]) and torch.equal(L, want[1])

@@ -882,7 +882,8 @@ def mesh_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     One call serves decoding steps (max_new = 1), guessed tokens and chunks of prompts, also mixed: max_new bounds a
     sequence's new tokens.  Returns O [N, Hq, d] and LSE fp32 [N, Hq]; rows from offsets[B] on are not written.  q and the pages may
     be views with strides of multiples of 16 bytes; page a multiple of 16.  A serving loop keeps workspace (new_paged_workspace) and
-    status and passes check_status=False."""
+    status and passes check_status=False; its status block is for its calls over pages alone, which go on behind an index out of range
+    (code 6) where range-masked and plain attention do not.  A wait that ran out (code 5) takes its place."""
     ws = new_paged_workspace(q, k_pages, table, max_new) if workspace is None else workspace
     st = new_status(q.device) if status is None else status
     out = (_ext or load_binding()).paged_attn(q, k_pages, v_pages, table, offsets, lens, max_new, scale, cap, slopes, window, O, LSE,
