@@ -459,7 +459,7 @@ int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq
  * Backward, with P = exp(x - LSE), dP = dO V^T, D = dO . O and t = tanh(scale q.k / cap):
  *   dS = P (dP - D) (1 - t^2) (without a cap t = 0),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO;
  * slopes get no gradient.  Masked scores may be infinite or NaN, but a weight of 0 still multiplies its value: V (and for
- * the backward call every tensor) must be finite in all rows, those of padding too. */
+ * the backward call every tensor, and the sums dO V^T in fp32) must be finite in all rows, those of padding too. */
 
 /* Bytes of device workspace of the calls below: the forward's, or with backward = 1 enough for both directions.
  * Caller-allocated, 16-byte aligned, its contents do not matter; calls that overlap on the GPU, captured graphs among them, need

@@ -45,3 +45,16 @@ def test_bounds_of_any_size(lib, S, d, kind, dtype):
     q, k, v, g = inputs(1, 4, 2, S, d, dtype, 70)
     lo, hi = far_mask(kind, S)
     both(lib, q, k, v, g, lo, hi, dtype, S)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cap, steep", [(0.0, False), (0.0, True), (5.0, False)], ids=str)
+def test_masked_scores_beyond_every_number(lib, cap, steep, dtype):
+    """Padding whose scores overflow fp32, as queries and as keys, beside rows that see whole blocks: it reaches no gradient."""
+    S, n = 384, 300
+    q, k, v, g = inputs(1, 2, 1, S, 64, dtype, 71)
+    q[:, :, n:] = torch.sign(q[:, :, n:].float()).to(q.dtype) * 2e38
+    k[:, :, n:] = torch.sign(k[:, :, n:].float()).to(k.dtype) * 2e38
+    lo, hi = torch.zeros(S, dtype=torch.int32), torch.full((S,), n, dtype=torch.int32)
+    hi[n:] = 0
+    both(lib, q, k, v, g, lo, hi, dtype, S, cap=cap, slopes=slopes_of(2, steep))

@@ -18,8 +18,8 @@
 //
 // Masks.  prep_kernel leaves for each 128-row query block the key blocks that it sees and the keys that all of its rows see
 // (an elementwise warp masks a block only where it is not inside those), beside D.  A dkdv unit's query blocks are the first to the
-// last that see its key block.  Rows that see nothing have an LSE of -inf, and weights of 0 by it.  In dkdv the
-// columns' ranges travel beside LSE and D through shared memory, clipped to the key block, two bytes a column.
+// last that see its key block.  In dkdv the columns' ranges travel beside LSE and D through shared memory, clipped to the key
+// block, two bytes a column.
 // A unit that meets no block is not published: the producer warp writes its zeros.
 //
 // Bound by the elementwise warps: a block takes dkdv 1.4 us and dq 1.1 (tensor pipe 57 % busy), with a cap 2.3 and 2.1 (39 %).
@@ -71,8 +71,8 @@ constexpr int64_t DRAIN_NS = 200000000;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int ROLE_EW = 1, ROLE_MMA = 2, ROLE_LOAD = 3, ROLE_ITEM = 4, ROLE_EPI = 5;
 
-// What prep_kernel leaves of a 128-row query block, over the rows that see any key: the key blocks [kb0, kb1) that they see,
-// and the keys [all_lo, all_hi) that all of them do.
+// What prep_kernel leaves of a 128-row query block: the key blocks [kb0, kb1) that its rows see, and the keys [all_lo, all_hi) that
+// all of them do.  Where one sees nothing, none are: its weight of 2^(x - inf) is no number when the score x is infinite.
 struct alignas(16) Bounds {
   int32_t kb0, kb1, all_lo, all_hi;
 };
@@ -489,7 +489,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& tmR0, const CUtensor
           const bool edge = raw_all_lo > k0 || raw_all_hi < k0 + BM;
           const float slope2 = raw_slope;
           if (hf == 0) {
-            // no such query row, or one that sees nothing: exp2(s - inf) = 0, so it needs no mask
+            // no such query row: exp2(0 - inf) = 0, so it needs no mask
             nlse_s[vb * BM + row] = raw_in && raw_lse != -INFINITY ? -raw_lse * LOG2E : -INFINITY;
             ndsum_s[vb * BM + row] = raw_in ? -raw_d : 0.f;
             const int a = min(max(clip(raw_lo, S) - k0, 0), BM), z = min(max(clip(raw_hi, S) - k0, a), BM);
@@ -1128,6 +1128,8 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const __grid_constan
           if (x < y) {
             kmin = min(kmin, x), kmax = max(kmax, y);
             all_lo = max(all_lo, x), all_hi = min(all_hi, y);
+          } else if ((int64_t)qb * BM + e * 32 + lane < p.S) {
+            all_hi = 0;
           }
         }
         kmin = __reduce_min_sync(0xffffffffu, kmin);
