@@ -435,6 +435,7 @@ int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, 
  *   max_new   an upper bound of a sequence's new tokens, which picks the kernel; a sequence with more is recorded, and its tokens
  *             from max_new on are left out.
  *   slopes    device fp32 [Hq], finite, or NULL.
+ *   cap       0, or within 1e-18 and 1e18, as scale / cap is.
  *   dtype     MESH_ATTN_BF16 (P in bf16 for its product; two bf16 pieces with few rows) or MESH_ATTN_F32.  d 64 or 128; page a
  *             multiple of 16; B <= 4096; max_pages * page <= 2^30.  Tensors 16-byte aligned, strides multiples of 16 bytes.
  * Tokens of a page from the sequence's length on never reach a result, NaN or not; with a window, pages wholly before all
@@ -456,6 +457,7 @@ int mesh_attn_paged_attn(mesh_attn_dtype dtype, int64_t N, int32_t B, int32_t Hq
  * larger lo), padding (lo >= hi: no key; O = 0, LSE = -inf and no gradients).  Bounds outside 0 .. S are taken as the nearer
  * bound.  Scores are capped and biased by distance on request:
  *   x_ij = scale q_i.k_j, or cap tanh(scale q_i.k_j / cap) with cap > 0;   x_ij -= slopes[h] |i - j| where slopes is not NULL.
+ * A cap, and scale / cap, is within 1e-18 and 1e18.
  * Backward, with P = exp(x - LSE), dP = dO V^T, D = dO . O and t = tanh(scale q.k / cap):
  *   dS = P (dP - D) (1 - t^2) (without a cap t = 0),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO;
  * slopes get no gradient.  Masked scores may be infinite or NaN, but a weight of 0 still multiplies its value: V (and for

@@ -58,3 +58,17 @@ def test_masked_scores_beyond_every_number(lib, cap, steep, dtype):
     lo, hi = torch.zeros(S, dtype=torch.int32), torch.full((S,), n, dtype=torch.int32)
     hi[n:] = 0
     both(lib, q, k, v, g, lo, hi, dtype, S, cap=cap, slopes=slopes_of(2, steep))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale, cap", [(1.0, 2e-7), (0.125, 1e-5), (1e-4, 1e-18), (0.05, 1e15), (2e4, 1e18)], ids=str)
+def test_caps_far_from_the_scores(lib, scale, cap, dtype):
+    """Caps far below and far above the scores, and queries of zeros, whose scores are 0 whatever the cap."""
+    S = 200
+    q, k, v, g = inputs(1, 4, 2, S, 64, dtype, 72)
+    if scale > 1:
+        q = q * (1.0 / 65536)
+    q[:, :, ::3] = 0
+    q[:, :, 40:160] = 0  # whole warps of them
+    lo, hi = mask_of("docs", 1, S)
+    both(lib, q, k, v, g, lo, hi, dtype, S, scale=scale, cap=cap)

@@ -59,7 +59,9 @@ inline Cap make_cap(float scale, float cap) {
   c.k = (float)k;
   double f = l * k;
   for (int i = 0; i < 4; ++i, f *= k * k) c.b[i] = (float)(p[i] * f);
-  c.low = std::fabs(c.b[3]) > 1e-30f && c.b[0] < 1e30f ? (float)(TANH_LOW / (k * k)) : -1.f;
+  // the coefficients are a power of k apart each, so those between the first and the last are in range where these are
+  const auto fits = [](float x) { return std::fabs(x) > 1e-30f && std::fabs(x) < 1e30f; };
+  c.low = fits(c.b[0]) && fits(c.b[3]) ? (float)(TANH_LOW / (k * k)) : -1.f;
   c.inv2 = (float)(1.0 / (l * l));
   return c;
 }

@@ -54,8 +54,9 @@ int check_score(float scale, float cap) {
   if (!(scale > 0.f) || !std::isfinite(scale)) return set_last_error(MESH_ATTN_ERR_INVALID_ARG, "scale must be finite and > 0");
   if (!(cap >= 0.f) || !std::isfinite(cap))
     return set_last_error(MESH_ATTN_ERR_INVALID_ARG, "cap must be finite and >= 0 (0: scores are not capped)");
-  if (cap > 0.f && !(scale / cap >= 1e-18f && scale / cap <= 1e18f))
-    return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "scale / cap must be within 1e-18 and 1e18");
+  // squares of both are taken in fp32
+  if (cap > 0.f && !(cap >= 1e-18f && cap <= 1e18f && scale / cap >= 1e-18f && scale / cap <= 1e18f))
+    return set_last_error(MESH_ATTN_ERR_UNSUPPORTED, "a cap, and scale / cap, must be within 1e-18 and 1e18");
   return MESH_ATTN_OK;
 }
 int sm_count(int* sms) {
