@@ -19,12 +19,9 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   return t;
 }
 
-// Record the first device-side error of a launch: word 0 code, word 1 role, word 2 unit.  An index out of range, which leaves the
-// rest of a paged call's results good, gives way to any other error, which does not.
+// Record the first device-side error of a launch: word 0 code, word 1 role, word 2 unit.
 __device__ __forceinline__ void record_error(int32_t* status, int32_t code, int32_t role, int32_t unit) {
-  int32_t held = atomicCAS(status, MESH_ATTN_OK, code);
-  if (held == MESH_ATTN_ERR_OUT_OF_RANGE && code != held && atomicCAS(status, held, code) == held) held = MESH_ATTN_OK;
-  if (held == MESH_ATTN_OK) {
+  if (atomicCAS(status, 0, code) == 0) {
     status[1] = role;
     status[2] = unit;
   }

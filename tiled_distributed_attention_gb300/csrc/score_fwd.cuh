@@ -433,7 +433,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(bar(Ly::B_DRAIN), 1);
     wait_for_kernel_before();
     // without any time to wait there is nothing to start: the first load would be waited for
-    if (prm.wait_limit_ns <= 0) record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
+    if (prm.wait_limit_ns <= 0) {
+      record_error(prm.status, MESH_ATTN_ERR_DEVICE_TIMEOUT, ROLE_LOAD, -1);
+      if (PAGED) timeout_takes_over(prm.status);
+    }
     *abort_flag = stopped<PAGED>(prm.status) ? 1 : 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -966,6 +969,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (PAGED && threadIdx.x == 0 && *abort_flag) timeout_takes_over(prm.status);
 }
 
 // O = sum_t w_t O_t over a unit's parts, w_t = exp(lse_t - lse), and the LSE.  A thread takes a 16-byte piece of a row,
