@@ -438,8 +438,10 @@ int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, 
  *   cap       0, or within 1e-18 and 1e18, as scale / cap is.
  *   dtype     MESH_ATTN_BF16 (P in bf16 for its product; two bf16 pieces with few rows) or MESH_ATTN_F32.  d 64 or 128; page a
  *             multiple of 16; B <= 4096; max_pages * page <= 2^30.  Tensors 16-byte aligned, strides multiples of 16 bytes.
- * Tokens of a page from the sequence's length on never reach a result, NaN or not; with a window, pages wholly before all
- * new tokens' windows (16 tokens of one, or a power of two that divides the page, at a time) are not read and need not exist.
+ * Tokens of a page from the sequence's length on, and with a window those before all of its new tokens' windows, never reach a
+ * result, NaN or not; values that some new token sees must be finite for all of its sequence's (a weight of 0 still multiplies them).
+ * Pages wholly before all new tokens' windows (16 tokens of one, or a power of two that divides the page, at a time) are not read
+ * and need not exist.
  * Another page that does not exist is recorded and read as zeros.  MESH_ATTN_ERR_OUT_OF_RANGE in the status block keeps
  * neither the other sequences nor later calls over pages from their work (range-masked and plain attention do nothing where their
  * block holds any error: they want another one).  Another error takes its place; outputs are then not to be used. */

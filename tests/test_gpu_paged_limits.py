@@ -1,9 +1,12 @@
 """Attention over a paged cache at the limits of its lengths, bounds, windows and status block, against the fp64 oracle.  Bounds as in
 test_gpu_paged.py."""
+import math
+
 import pytest
 import torch
 
-from tests.test_gpu_paged import cache
+from oracle import range_attention as OR
+from tests.test_gpu_paged import cache, check
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +38,23 @@ def test_a_timeout_behind_a_recorded_page(lib, new, lens, Hq):
         assert lib.mesh_attn_read_status(st) == 5 and (O == 7).all()
     O, L = lib.mesh_paged_attention(*args, max(new), workspace=ws)
     assert torch.equal(O, want[0]) and torch.equal(L, want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new, lens, page, window", [
+    ([1, 1], [900, 131], 64, 100),         # few rows
+    ([2, 1], [900, 131], 16, 7),
+    ([40, 25], [1000, 500], 128, 301),     # chunks
+    ([150, 30], [1000, 333], 48, 130),
+    ([200, 1], [9000, 70], 256, 5001),     # in parts
+], ids=str)
+def test_what_lies_before_every_window_is_never_met(lib, new, lens, page, window, dtype):
+    """NaN in the tokens before the first that any new token sees, up to the one beside it in its page."""
+    q, _, _, kp, vp, table, off, ln = cache(new, lens, page, 4, 1, 64, dtype, 82)
+    ref = OR.paged(q, kp, vp, table, off, ln, window=window)
+    for b, (n, m) in enumerate(zip(new, lens)):
+        for i in range(max(0, m - n + 1 - window)):
+            for p in (kp, vp):
+                p[int(table[b, i // page]), :, i % page] = math.nan
+    O, L = lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), max(new), window=window)
+    check(O, L, ref, dtype, max(new) <= 2)

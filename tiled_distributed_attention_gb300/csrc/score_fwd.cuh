@@ -17,9 +17,9 @@
 // of all of the warp's rows, |i - j| only on the diagonal.
 //
 // Pages.  A block's keys are boxes of as many rows as a page (a power of two that divides it, 16 to 128), one lane of the producer
-// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Places behind the last token, or
-// before the first that any row's window holds, load a page that does not exist, which arrives as zeros; what an earlier owner
-// left behind it in its last page is zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
+// warp a box and 64-column half; each lane looks the next block's page up a block ahead.  Boxes behind the last token, or
+// before the first that any row's window holds, load a page that does not exist, which arrives as zeros; the other rows of the
+// last token's box and of the first one's are zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
 //
 // Few units are cut into parts of their keys (score_fwd_shape), whose normalised outputs and LSEs merge_kernel adds up in order.
 // P is rounded to bf16 for its product (2^-9 relative a term), everything else is fp32.
@@ -150,14 +150,16 @@ struct Unit {
     return i <= m - blk0 ? m - i : blk0 + i;
   }
 };
+template <bool PAGED>
 __device__ __forceinline__ void put_unit(volatile int32_t* e, const Unit& x) {
   e[0] = x.u, e[1] = x.b, e[2] = x.hk, e[3] = x.h0, e[4] = x.h_end, e[5] = x.tok0, e[6] = x.n_tok, e[7] = x.row0;
-  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.slot;  // kmin is the producer's own
+  e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.slot;
+  if (PAGED) e[13] = x.kmin;  // else the producer's own
 }
 __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   Unit x;
   x.u = e[0], x.b = e[1], x.hk = e[2], x.h0 = e[3], x.h_end = e[4], x.tok0 = e[5], x.n_tok = e[6], x.row0 = e[7];
-  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.slot = e[12], x.kmin = 0;
+  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.slot = e[12], x.kmin = e[13];
   return x;
 }
 
@@ -768,6 +770,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int NB = x.NB;
         if (NB == 0 || x.n_tok == 0) continue;
         const int ntiles = x.ntiles(prm.tt);
+        // paged: the blocks whose boxes hold rows behind the last token or before all windows, or -1
+        const int ragged_end = (x.len & (prm.box_rows - 1)) ? x.len / BN : -1, ragged_first = (x.kmin & (prm.box_rows - 1)) ? x.kmin / BN : -1;
         const int uidx = nq++;
         ok = mbar_wait_warp(bar(Ly::B_QFULL), (uint32_t)(uidx & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_MMA, u);
         if (ok)
@@ -784,15 +788,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = mbar_wait_warp(bar(Ly::B_VFULL + st), (uint32_t)((g / NST) & 1), prm.wait_limit_ns, abort_flag, prm.status,
                               ROLE_MMA, u);
           if (PAGED && ok) {
-            // the last token's page may go on behind it, with whatever an earlier owner left: zeros there
-            const int r0 = x.len - x.block(j, prm.tt) * BN;
-            if (r0 < BN) {
-              const int r1 = min(BN, (r0 + prm.box_rows - 1) / prm.box_rows * prm.box_rows);
+            // the last token's box may go on behind it, with whatever an earlier owner left, and the first one's begin before any
+            // row's window: zeros there
+            const int jb = x.block(j, prm.tt);
+            if (jb == ragged_end || jb == ragged_first) {
               uint8_t* vs = smem + Ly::V_OFF + (uint32_t)st * Ly::TILE;
-              for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll 1
+              for (int i = lane; i < BN * 8; i += 32) {
+                const int key = jb * BN + (i >> 3);
+                if (key >= x.kmin && key < x.len) continue;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                   *reinterpret_cast<uint4*>(vs + (uint32_t)c * Ly::BOX + (uint32_t)i * 16u) = make_uint4(0u, 0u, 0u, 0u);
+              }
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
               __syncwarp();
             }
@@ -860,7 +868,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           next.u = -1;
         }
         if (lane == 0) {
-          put_unit(ring + 16 * slot, next);
+          put_unit<PAGED>(ring + 16 * slot, next);
           mbar_arrive(bar(Ly::B_UFULL + slot));
         }
         __syncwarp();
