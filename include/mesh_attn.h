@@ -433,7 +433,7 @@ int mesh_attn_paged_workspace_size(mesh_attn_dtype dtype, int64_t N, int32_t B, 
  *   x = scale q.k, or cap tanh(scale q.k / cap) with cap > 0;   x -= slopes[h] (i - j) where slopes is not NULL.
  * O [N, Hq, d] and LSE [N, Hq] (natural log, fp32), dense.  q [N, Hq, d] with strides[2] = token and head strides.
  *   max_new   an upper bound of a sequence's new tokens, which picks the kernel; a sequence with more is recorded, and its tokens
- *             from max_new on are left out.
+ *             from max_new on are left out (those before have their places and results all the same).
  *   slopes    device fp32 [Hq], finite, or NULL.
  *   cap       0, or within 1e-18 and 1e18, as scale / cap is.
  *   dtype     MESH_ATTN_BF16 (P in bf16 for its product; two bf16 pieces with few rows) or MESH_ATTN_F32.  d 64 or 128; page a

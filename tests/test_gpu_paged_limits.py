@@ -58,3 +58,26 @@ def test_what_lies_before_every_window_is_never_met(lib, new, lens, page, window
                 p[int(table[b, i // page]), :, i % page] = math.nan
     O, L = lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), max(new), window=window)
     check(O, L, ref, dtype, max(new) <= 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new, lens, bound, window", [
+    ([3, 1, 2], [90, 33, 2], 2, 0),          # few rows
+    ([3, 1, 2], [700, 33, 2], 1, 300),
+    ([70, 1, 33], [300, 20, 40], 50, 0),     # chunks
+    ([170, 1, 33], [5000, 20, 40], 130, 0),  # in parts
+    ([170, 1, 33], [900, 20, 40], 40, 100),
+], ids=str)
+def test_more_new_tokens_than_the_bound(lib, new, lens, bound, window, dtype):
+    """Recorded; the sequence's tokens up to the bound come out right, at the places that the append gives them, the others
+    are left out."""
+    q, _, _, kp, vp, table, off, ln = cache(new, lens, 16, 4, 2, 64, dtype, 80)
+    ref = OR.paged(q, kp, vp, table, off, ln, window=window)
+    O, L = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda"), torch.full(q.shape[:2], 7.0, device="cuda")
+    st = lib.new_status()
+    lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), bound, window=window, O=O, LSE=L, status=st,
+                             check_status=False)
+    assert lib.mesh_attn_read_status(st) == 6
+    kept = torch.cat([torch.arange(n) < bound for n in new])
+    check(O[kept.cuda()], L[kept.cuda()], tuple(x[kept] for x in ref), dtype, False)
+    assert (O[~kept.cuda()] == 7).all() and (L[~kept.cuda()] == 7).all()

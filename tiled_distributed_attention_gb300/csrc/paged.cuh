@@ -63,4 +63,26 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int B, int64_
   return b;
 }
 
+// What a sequence asks for: n tokens, the rows of the batch from `begin` on, that are the last of `len` cached ones.  What does not fit
+// is taken as the nearest that does: offsets within the batch, a length that the new tokens need and the table holds.  Of more new
+// tokens than the bound the first ones are taken, at their places, and the cache as far as the last of them.
+struct Asked {
+  int32_t begin, n, len;
+  bool bad;
+};
+__device__ __forceinline__ Asked asked(const int32_t* offsets, const int32_t* lens, int b, int32_t N, int32_t max_new, int32_t max_pages,
+                                       int32_t page) {
+  const int32_t o0 = offsets[b], o1 = offsets[b + 1], len = lens[b];
+  Asked x;
+  x.begin = min(max(o0, 0), N);
+  const int32_t end = min(max(o1, x.begin), N);
+  int32_t all = end - x.begin;
+  x.len = (int32_t)min((int64_t)max(len, all), (int64_t)max_pages * page);
+  x.bad = x.begin != o0 || end != o1 || x.len != len || all > max_new;
+  all = min(all, x.len);
+  x.n = min(all, max_new);
+  x.len -= all - x.n;
+  return x;
+}
+
 }  // namespace mesh

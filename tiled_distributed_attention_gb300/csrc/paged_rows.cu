@@ -32,6 +32,7 @@
 
 #include "abi_util.h"
 #include "internal.h"
+#include "paged.cuh"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -80,24 +81,11 @@ __host__ __device__ constexpr int part_floats(int D) { return ROWS * D + 2 * ROW
 // Floats from row to row of the warps' sums in shared memory: the eight rows that a warp's lanes write at once lie in other banks.
 __host__ __device__ constexpr int sum_ld(int D) { return D + 8; }
 
-// What a sequence asks for, with what does not fit taken as the nearest that does.
-struct Seq {
-  int32_t begin, n, len;  // first new token's row, new tokens, cached tokens
-  bool bad;
-};
-__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
-  Seq s;
-  const int32_t o0 = p.offsets[b], o1 = p.offsets[b + 1], len = p.lens[b];
-  s.begin = min(max(o0, 0), p.N);
-  s.n = min(min(max(o1, s.begin), p.N) - s.begin, p.max_new);
-  const int64_t most = (int64_t)p.max_pages * p.page;
-  s.len = (int32_t)min((int64_t)max(len, s.n), most);
-  s.bad = s.begin != o0 || s.n != o1 - o0 || s.len != len;
-  if (s.len < s.n) s.n = s.len;  // a table of fewer tokens than there are new ones
-  return s;
+__device__ __forceinline__ Asked seq_of(const Params& p, int b) {
+  return asked(p.offsets, p.lens, b, p.N, p.max_new, p.max_pages, p.page);
 }
 // The first tile that a segment of it reads.
-__device__ __forceinline__ int first_tile(const Params& p, const Seq& s) {
+__device__ __forceinline__ int first_tile(const Params& p, const Asked& s) {
   return p.window ? max(s.len - s.n - p.window + 1, 0) / TILE : 0;
 }
 
@@ -663,7 +651,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
       const int b = b0 + tid;
       int64_t n = 0;
       if (b < p.B) {
-        const Seq s = seq_of(p, b);
+        const Asked s = seq_of(p, b);
         if (s.bad && blockIdx.x == 0) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, b);
         if (s.n > 0) n = (s.len + TILE - 1) / TILE - first_tile(p, s) + SEG_COST;
       }
@@ -716,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, CTAS<D>) rows_kernel(const Params p) 
       }
       b = a;
     }
-    const Seq s = seq_of(p, b);
+    const Asked s = seq_of(p, b);
     const int64_t n = prefix[b + 1] - prefix[b];  // of a segment, > SEG_COST
     const int hk = (int)((x - prefix[b] * per) / n);
     const int64_t s1 = prefix[b] * per + (hk + 1) * n, s0 = s1 - n + SEG_COST;  // the segment's tiles are [s0, s1)

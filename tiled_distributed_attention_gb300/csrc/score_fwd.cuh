@@ -163,19 +163,15 @@ __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   return x;
 }
 
-// Sequence b of a batch over pages, and the group of tokens from tok0 on: its rows and keys, with what does not fit recorded (where
-// `report`) and taken as the nearest that does.
+// Sequence b of a batch over pages: its rows and keys, with what does not fit recorded (where `report`).
 __device__ __forceinline__ void sequence(const Params& prm, int b, bool report, Unit& x) {
+  const Asked s = asked(prm.offsets, prm.lens, b, prm.N, prm.max_new, prm.max_pages, prm.page);
+  if (report && s.bad) record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, b);
   x.b = b;
-  const int32_t o0 = prm.offsets[b], o1 = prm.offsets[b + 1], len = prm.lens[b];
-  x.row0 = min(max(o0, 0), prm.N);
-  x.n_tok = min(min(max(o1, x.row0), prm.N) - x.row0, prm.max_new);
-  const int64_t most = (int64_t)prm.max_pages * prm.page;
-  x.len = (int32_t)min((int64_t)max(len, x.n_tok), most);
-  if (report && (x.row0 != o0 || x.n_tok != o1 - o0 || x.len != len))
-    record_error(prm.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, b);
-  x.n_tok = min(x.n_tok, x.len);
-  x.pos0 = x.len - x.n_tok;
+  x.row0 = s.begin;
+  x.n_tok = s.n;
+  x.len = s.len;
+  x.pos0 = s.len - s.n;
 }
 __device__ __forceinline__ void keys_of(const Params& prm, Unit& x) {  // paged: of its group of tokens
   const int kmax = x.pos0 + min(x.tok0 + prm.tu, x.n_tok);

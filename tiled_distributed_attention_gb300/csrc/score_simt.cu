@@ -91,14 +91,12 @@ __device__ __forceinline__ bool tile_of(const Params& p, int slot, int hk, int b
       else z = c;
     }
     t.b = a;
-    const int32_t o0 = p.offsets[a], o1 = p.offsets[a + 1], len = p.lens[a];
-    t.row0 = min(max(o0, 0), p.N);
-    n_tok = min(min(max(o1, t.row0), p.N) - t.row0, p.max_new);
-    t.len = (int32_t)min((int64_t)max(len, n_tok), (int64_t)p.max_pages * p.page);
-    if (bounds && tid == 0 && (t.row0 != o0 || n_tok != o1 - o0 || t.len != len))
-      record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, a);
-    n_tok = min(n_tok, t.len);
-    t.pos0 = t.len - n_tok;
+    const Asked s = asked(p.offsets, p.lens, a, p.N, p.max_new, p.max_pages, p.page);
+    if (bounds && tid == 0 && s.bad) record_error(p.status, MESH_ATTN_ERR_OUT_OF_RANGE, ROLE_SEQ, a);
+    t.row0 = s.begin;
+    t.len = s.len;
+    t.pos0 = s.len - s.n;
+    n_tok = s.n;
     const int64_t r = ((int64_t)slot - ((int64_t)t.row0 * p.g / TR + a)) * TR;
     if (r < 0 || r >= (int64_t)n_tok * p.g) return false;
     t.r0 = (int)r;
