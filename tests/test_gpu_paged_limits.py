@@ -81,3 +81,19 @@ def test_more_new_tokens_than_the_bound(lib, new, lens, bound, window, dtype):
     kept = torch.cat([torch.arange(n) < bound for n in new])
     check(O[kept.cuda()], L[kept.cuda()], tuple(x[kept] for x in ref), dtype, False)
     assert (O[~kept.cuda()] == 7).all() and (L[~kept.cuda()] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_more_new_tokens_than_the_table_holds(lib, dtype):
+    """A length that the table just holds, of a sequence with more new tokens than that: recorded, as the append does, and the
+    other sequence comes out right."""
+    new = [40, 5]
+    q, k, v, kp, vp, table, off, ln = cache(new, [32, 20], 16, 4, 2, 64, dtype, 81)
+    st = lib.new_status()
+    lib.mesh_paged_append(*(t.cuda() for t in (q, k, v, kp, vp, table, off, ln)), status=st, check_status=False)
+    assert lib.mesh_attn_read_status(st) == 6
+    st = lib.new_status()
+    O, L = lib.mesh_paged_attention(*(t.cuda() for t in (q, kp, vp, table, off, ln)), 40, status=st, check_status=False)
+    assert lib.mesh_attn_read_status(st) == 6
+    one = torch.tensor([0, 5], dtype=torch.int32)
+    check(O[40:], L[40:], OR.paged(q[40:], kp, vp, table[1:], one, ln[1:]), dtype, False)

@@ -78,7 +78,7 @@ __device__ __forceinline__ Asked asked(const int32_t* offsets, const int32_t* le
   const int32_t end = min(max(o1, x.begin), N);
   int32_t all = end - x.begin;
   x.len = (int32_t)min((int64_t)max(len, all), (int64_t)max_pages * page);
-  x.bad = x.begin != o0 || end != o1 || x.len != len || all > max_new;
+  x.bad = x.begin != o0 || end != o1 || x.len != len || all > x.len || all > max_new;
   all = min(all, x.len);
   x.n = min(all, max_new);
   x.len -= all - x.n;
