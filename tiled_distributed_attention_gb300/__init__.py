@@ -510,6 +510,13 @@ def mesh_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, P: int, ca
     return O, LSE
 
 
+def _dense_gradient(g: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels take it: contiguous, on a 16-byte boundary.  PyTorch hands on views of larger gradients (of a cat, say)
+    that begin anywhere."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class MeshAttentionFunction(torch.autograd.Function):
     """torch.autograd binding of the two public calls: the forward runs mesh_attention and keeps
     q, k, v, O and LSE; the backward runs mesh_attention_backward with the incoming dO.  Gradients
@@ -530,7 +537,7 @@ class MeshAttentionFunction(torch.autograd.Function):
     def backward(ctx, dO, dLSE):
         q, k, v, O, LSE = ctx.saved_tensors
         P, causal, kvr, greedy, scale = ctx.args
-        dQ, dK, dV = mesh_attention_backward(q, k, v, O, LSE, dO.contiguous(), P, causal, kvr, greedy, scale,
+        dQ, dK, dV = mesh_attention_backward(q, k, v, O, LSE, _dense_gradient(dO), P, causal, kvr, greedy, scale,
                                              plan=ctx.plan)
         return dQ, dK, dV, None, None, None, None, None
 
@@ -777,7 +784,7 @@ class MeshDiffAttentionFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dLSE):
-        grads = mesh_diff_attention_backward(*ctx.saved_tensors, dO.contiguous(), *ctx.args, plan=ctx.plan, status=ctx.status,
+        grads = mesh_diff_attention_backward(*ctx.saved_tensors, _dense_gradient(dO), *ctx.args, plan=ctx.plan, status=ctx.status,
                                              check_status=ctx.check_status)
         return (*grads, None, None, None, None, None, None, None, None)
 
@@ -994,7 +1001,7 @@ class MeshRangeAttentionFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO, dLSE):
         q, k, v, lo, hi, slopes, O, LSE = ctx.saved_tensors
-        grads = mesh_range_attention_backward(q, k, v, lo, hi, O, LSE, dO.contiguous(), *ctx.args, slopes, status=ctx.status,
+        grads = mesh_range_attention_backward(q, k, v, lo, hi, O, LSE, _dense_gradient(dO), *ctx.args, slopes, status=ctx.status,
                                               check_status=ctx.check_status)
         return (*grads, None, None, None, None, None, None, None)
 
