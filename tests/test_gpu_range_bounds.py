@@ -72,3 +72,13 @@ def test_caps_far_from_the_scores(lib, scale, cap, dtype):
     q[:, :, 40:160] = 0  # whole warps of them
     lo, hi = mask_of("docs", 1, S)
     both(lib, q, k, v, g, lo, hi, dtype, S, scale=scale, cap=cap)
+
+
+@pytest.mark.parametrize("shape, kind", [((1, 1, 1, 2304, 128), "causal"), ((2, 4, 1, 700, 64), "causal"), ((1, 2, 1, 8200, 64), "causal"),
+                                         ((1, 2, 2, 2304, 64), "prefix"), ((1, 2, 1, 3001, 128), "docs")], ids=str)
+def test_every_row_of_units_in_parts(lib, shape, kind):
+    """Few long units, which go in parts of their keys: every row and key, those at the borders of parts and tiles among them."""
+    B, Hq, Hkv, S, d = shape
+    q, k, v, g = inputs(B, Hq, Hkv, S, d, "bf16", 73)
+    lo, hi = mask_of(kind, B, S)
+    both(lib, q, k, v, g, lo, hi, "bf16", S)
