@@ -1071,9 +1071,10 @@ static int launch_mode(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
     }
     if (e == cudaSuccess) once.mark(dev);
   }
+  if constexpr (PAGED)
+    if (e == cudaSuccess && prm.plan) e = launch_behind(plan_kernel<PAGED>, dim3(1), PLAN_GROUPS, 0, st, prm, sms);
   // with a CTA for every unit the counter is not read
-  if (e == cudaSuccess && prm.plan) e = launch_behind(plan_kernel<PAGED>, dim3(1), PLAN_GROUPS, 0, st, prm, sms);
-  else if (e == cudaSuccess && prm.n_units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
+  if (e == cudaSuccess && !prm.plan && prm.n_units > sms) e = cudaMemsetAsync(prm.counter, 0, 4, st);
   if (e != cudaSuccess) {
     *err = std::string("score_fwd: ") + cudaGetErrorString(e);
     return (int)e;
