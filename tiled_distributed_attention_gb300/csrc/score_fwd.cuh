@@ -154,12 +154,13 @@ template <bool PAGED>
 __device__ __forceinline__ void put_unit(volatile int32_t* e, const Unit& x) {
   e[0] = x.u, e[1] = x.b, e[2] = x.hk, e[3] = x.h0, e[4] = x.h_end, e[5] = x.tok0, e[6] = x.n_tok, e[7] = x.row0;
   e[8] = x.pos0, e[9] = x.len, e[10] = x.blk0, e[11] = x.NB, e[12] = x.slot;
-  if (PAGED) e[13] = x.kmin;  // else the producer's own
+  if (PAGED) e[13] = x.kmin;  // for the MMA warp, else the producer's own
 }
+template <bool KMIN = false>
 __device__ __forceinline__ Unit get_unit(const volatile int32_t* e) {
   Unit x;
   x.u = e[0], x.b = e[1], x.hk = e[2], x.h0 = e[3], x.h_end = e[4], x.tok0 = e[5], x.n_tok = e[6], x.row0 = e[7];
-  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.slot = e[12], x.kmin = e[13];
+  x.pos0 = e[8], x.len = e[9], x.blk0 = e[10], x.NB = e[11], x.slot = e[12], x.kmin = KMIN ? e[13] : 0;
   return x;
 }
 
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = mbar_wait_warp(bar(Ly::B_UFULL + slot), (uint32_t)((nu >> 1) & 1), prm.wait_limit_ns, abort_flag, prm.status,
                             ROLE_MMA, -1);
         if (!ok) break;
-        const Unit x = get_unit(ring + 16 * slot);
+        const Unit x = get_unit<PAGED>(ring + 16 * slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Ly::B_UEMPTY + slot));
         __syncwarp();
