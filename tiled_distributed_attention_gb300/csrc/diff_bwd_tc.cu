@@ -33,7 +33,7 @@
 // The gradients are written from the accumulators, rounded once, where the blocks alone fill the GPU.  With
 // fewer, a unit is cut into parts of its streamed blocks (diff_bwd_parts), which leave fp32 sums that
 // sum_parts adds in order.  Rows past the end are loaded as zeros.
-// A, dS_1 and dS_2 are rounded to bf16 for their products (2^-9 relative a term); sums are fp32.
+// A, dS_1 and dS_2 are rounded to bf16 for their products (2^-8 relative a term at most); sums are fp32.
 // Every mbarrier wait is bounded; a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT, the CTA stops,
 // drains its copies and products and frees its tensor memory.
 //

@@ -18,7 +18,7 @@
 // merge_parts_kernel adds up (choose_parts).
 //
 // Per 128 x 128 block and head: 2 x 4 score products and 2 x 8 PV products of 64 cycles each at
-// d = 128 (1,536 cycles), 32,768 exponentials.  P is rounded to bf16 for its product (2^-9 relative
+// d = 128 (1,536 cycles), 32,768 exponentials.  P is rounded to bf16 for its product (2^-8 relative
 // a term), everything else is fp32.  That rounding costs 1.9e-3 of O's norm beside the 1.7e-3 of O's own (2.6e-3
 // together, as the same rounding in 64-bit arithmetic gives); a second piece of P would take it away for 1,024 cycles of
 // products more a block, 2,560 against the softmax's 2,400.

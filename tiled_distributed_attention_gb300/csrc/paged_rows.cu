@@ -14,8 +14,9 @@
 // results do not depend on the arrival order.  At most one segment begins in a CTA and goes on behind it, so a segment's
 // arrival counter is that CTA's: one a CTA, zero between calls (the last CTA puts them back).
 //
-// Measured (bf16, d 128): 64 sequences of up to 8,192 tokens, 32 heads on 8, 169 us = 6.5 TB/s, 96 % of a plain copy; one of
-// 131,072, 16 heads on 4, 49.5 us = 5.4 TB/s, 9 us of it the start, the SMs' spread and the merge.
+// Measured: 64 sequences of up to 8,192 tokens, 32 heads on 8, bf16, d 128, 171 us = 6.4 TB/s, 95 % of a plain copy (d 64: 98 us,
+// 5.6); one of 131,072, 16 heads on 4, 50 us = 5.4 TB/s, 9 us of it the start, the SMs' spread and the merge.  fp32, the same 64:
+// 624 us at d 128 and 321 at d 64, 3.5 and 3.4 TB/s: not memory but the warps bound it (EngineF32).
 //
 // A row's statistics are fp32; sums of P V are fp32.  A warp's 16 tokens of a tile lie in one page (pages are multiples of
 // 16), so a tile costs a warp one look at the table, one tile ahead.  What lies behind a sequence's last token, in its
@@ -382,7 +383,9 @@ struct EngineBf16 {
 
 // fp32: CUDA cores.  A lane owns D / 32 columns.  A warp takes four tokens at a time from its own ring; the
 // reduction over the lanes transposes as it goes (two values, then one, travel), so that afterwards a lane holds one
-// token's score and takes one exponential, and four shuffles hand the weights to all lanes.
+// token's score and takes one exponential, and four shuffles hand the weights to all lanes.  Bound by the latency
+// of that chain, twelve shuffles and a vote a row and four tokens, with two warps a scheduler: it issues in 40 % of the cycles, and
+// waits for results of fixed latency in 31 % of a warp's time and for shuffles and shared memory in 26 % (d 128).
 template <int D, int G>
 struct EngineF32 {
   using T = float;

@@ -23,11 +23,11 @@
 // A unit that meets no block is not published: the producer warp writes its zeros.
 //
 // Bound by the elementwise warps: a block takes dkdv 1.4 us and dq 1.1 (tensor pipe 57 % busy), with a cap 2.3 and 2.1 (39 %).
-// Measured, bf16: 8,192 tokens in five documents, 16 heads on 4, d 128, 322 us capped, 230 without a cap; one document 610
-// (1,130 TFLOP/s); 2 x 1,000 tokens, 4 heads, d 64, slopes, 23.
+// Measured, bf16: 8,192 tokens in five documents, 16 heads on 4, d 128, 322 us capped, 233 without a cap; one document 631
+// (1,090 TFLOP/s); 2 x 1,000 tokens, 4 heads, d 64, slopes, 23.
 //
 // D is of O as the forward returned it, in bf16: its rounding reaches every dS of the row, 1e-3 to 2e-3 of the norm of dQ and
-// dK, as much as dS's own.  P and dS are rounded to bf16 for their products (2^-9 relative a term); sums are fp32; the
+// dK, as much as dS's own.  P and dS are rounded to bf16 for their products (2^-8 relative a term at most); sums are fp32; the
 // gradients are rounded once. Every mbarrier wait is bounded; a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT, the CTA stops,
 // drains its copies and products and frees its tensor memory.
 #pragma once
@@ -1232,7 +1232,7 @@ static cudaError_t launch_main(const CUtensorMap& mq, const CUtensorMap& mk, con
   }
   if (e != cudaSuccess) return e;
   // not launch_behind: begun beside the end of prep_kernel, the whole took 404 us where this takes 322 (8,192 tokens in five
-  // documents, 16 heads on 4, capped; without a cap 252 and 230), for 2 us less where there is little to do
+  // documents, 16 heads on 4, capped; without a cap 252 and 233), for 2 us less where there is little to do
   kern<<<dim3((unsigned)(prm.kv_ctas + prm.dq_ctas)), NUM_THREADS, Layout<D>::TOTAL, st>>>(mq, mk, mv, mg, prm);
   return cudaGetLastError();
 }

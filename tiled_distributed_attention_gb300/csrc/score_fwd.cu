@@ -62,8 +62,8 @@ bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
 // Parts, of range-masked attention (over pages plan_kernel decides by the lengths, which are on the device).  The longest unit
 // has to be done, and the SMs share all blocks, those of a dense batch half of the longest on average, as under a causal mask.
 // A unit costs about three blocks besides its own (5 us at 1.6 us a block), and parts a merge: four blocks and the traffic of
-// their fp32 rows.  The best count is taken where it saves a fifth or more: 160 units of up to 20 blocks stay whole (40 us; 68
-// in 2 parts).
+// their fp32 rows.  The best count is taken where it saves a fifth or more: 160 units of up to 20 blocks stay whole (38 us; 67
+// in 2 parts; capped, 52 and 80).
 ScoreFwdShape score_fwd_shape(bool paged, int64_t S, int64_t N, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int sms) {
   ScoreFwdShape z{};
   const int g = Hq / Hkv;

@@ -22,13 +22,13 @@
 // last token's box and of the first one's are zeroed in V before the product (a weight of 0 times NaN is NaN), and masked in S.
 //
 // Few units are cut into parts of their keys (score_fwd_shape), whose normalised outputs and LSEs merge_kernel adds up in order.
-// P is rounded to bf16 for its product (2^-9 relative a term), everything else is fp32.
+// P is rounded to bf16 for its product (2^-8 relative a term at most), everything else is fp32.
 //
 // Bound by the softmax warps: a block of 256 rows takes them 1.45 us plain (tensor pipe 74 % busy) and 2.3 to 2.5 with a cap
-// (24 %).  Measured, bf16, d 128: 1,024 new tokens over 65,536 cached, 32 heads on 8, 690-740 us (1,480-1,580 TFLOP/s, 128 units
-// on 152 SMs); 16,384 tokens of 16 heads, causal, one document 650 us (1,670), six documents 208 (1,030: units of 17 blocks, of
+// (24 %).  Measured, bf16, d 128: 1,024 new tokens over 65,536 cached, 32 heads on 8, 740-760 us (1,440-1,470 TFLOP/s, 128 units
+// on 152 SMs); 16,384 tokens of 16 heads, causal, one document 700 us (1,560), six documents 208 (1,030: units of 17 blocks, of
 // which the change from one to the next costs five, and masked blocks at documents' edges); 2 x 2,500 with prefixes,
-// capped, 53.
+// capped, 52.
 //
 // Every mbarrier wait is bounded: a timeout records MESH_ATTN_ERR_DEVICE_TIMEOUT in the status
 // block, every role of the CTA stops, in-flight copies and MMAs are drained and TMEM is freed.
@@ -141,7 +141,7 @@ struct Unit {
   __device__ __forceinline__ int ntiles(int tt) const { return tok0 + tt < n_tok ? 2 : 1; }
   // Its i-th block: from the one of its last token's own key down to the first, then up from behind it.  So rows meet their own key
   // early, where a causal document or a slope has its largest weights, and the running maximum seldom grows (blocks from the first
-  // on: 352 us where this takes 219, 16 heads of 8,192 tokens with slopes).
+  // on: 352 us where this takes 219, 16 heads on 4 of 8,192 tokens with slopes).
   __device__ __forceinline__ int mid(int tt) const {
     return min(max((pos0 + min(tok0 + 2 * tt, n_tok) - 1) / BN, blk0), blk0 + NB - 1);
   }
@@ -297,7 +297,7 @@ __device__ __forceinline__ Unit decode(int u, const Params& prm, bool bounds, co
 
 // The plan of a batch over pages, by one CTA, a thread a group; it also puts the unit counter to zero.  A batch of chunks and
 // single tokens ends when its longest units do, so those start first: 16 sequences of up to 4,096 tokens, 2,048 new ones in
-// four of them, 16 heads on 4, capped, 86 us, where units as they come take 108-130.  The kernel itself costs a call 3 us.
+// four of them, 16 heads on 4, capped, 91-95 us, where units as they come take 108-130.  The kernel itself costs a call 3 us.
 //
 // Parts.  The SMs' share of all blocks, three more a group for its start (5 us at 1.6 us a block), is what a group should take.
 // Those of twice that and more, and of eight blocks or more, are cut into parts of a share, whose outputs merge_kernel adds up
