@@ -884,7 +884,7 @@ def mesh_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     """Attention of the new tokens q [N, Hq, d] over their sequences' pages, on the current stream; the pages hold
     the new tokens' own keys and values already (mesh_paged_append, whose arguments these are).  Token i of a sequence sees its
     tokens j <= i, with window > 0 those with i - j < window; scores are scale q.k (1 / sqrt(d) unless given), capped to
-    cap tanh(score / cap) with cap > 0, less slopes[h] (i - j) with slopes (fp32 [Hq]).
+    cap tanh(score / cap) with cap > 0 (1e-18 to 1e18), less slopes[h] (i - j) with slopes (fp32 [Hq]).
 
     One call serves decoding steps (max_new = 1), guessed tokens and chunks of prompts, also mixed: max_new bounds a
     sequence's new tokens.  Returns O [N, Hq, d] and LSE fp32 [N, Hq]; rows from offsets[B] on are not written.  q and the pages may
@@ -948,8 +948,8 @@ def mesh_range_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lo: 
                          check_status: bool = True):
     """Attention where query i sees the keys lo[i] <= j < hi[i], on the current stream: packed documents, prefixes that
     see one another, windows, padding (mesh_ranges makes lo and hi).  q [B, Hq, S, d], k, v [B, Hkv, S, d], all bf16 or all
-    fp32; lo, hi int32 [S] or [B, S] on the device.  Scores are scale q.k (1 / sqrt(d) unless given), capped to
-    cap tanh(score / cap) with cap > 0, less slopes[h] |i - j| with slopes (fp32 [Hq]).  Returns O (q's shape and dtype) and LSE
+    fp32; lo, hi int32 [S] or [B, S] on the device, any values.  Scores are scale q.k (1 / sqrt(d) unless given), capped to
+    cap tanh(score / cap) with cap > 0 (1e-18 to 1e18), less slopes[h] |i - j| with slopes (fp32 [Hq]).  Returns O (q's shape and dtype) and LSE
     (fp32 [B, Hq, S]); a query that sees nothing gets 0 and -inf.  A program that calls it every step keeps workspace
     (new_range_workspace) and status (new_status) and passes check_status=False, which leaves out the wait."""
     if workspace is None or status is None:
