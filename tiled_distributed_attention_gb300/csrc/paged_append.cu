@@ -14,8 +14,9 @@
 // Four or five loads follow one another for that; the first heads' own are issued before them.
 //
 // Measured: 16,384 tokens of 8 sequences, 32 + 8 heads, d 128, bf16, 403 MB in 67.5 us, 6.0 TB/s (a plain copy: 6.8; 71 with
-// the look-up first, and 500 tokens 11 us for 8); one token of 64 sequences 6.2 us, most of it the host's call; the prompts in fp32 130 us, 6.2 TB/s.  A second set of
-// heads' loads beside the first's stores: 67 us, and 10 for 500 tokens; other block sizes and fewer registers no gain.
+// the look-up first, and 500 tokens 11 us for 8); in fp32 130 us, 6.2 TB/s; one token of 64 sequences 6.2 us, most of it the host's
+// call.  A second set of heads' loads beside the first's stores: 67 us, and 10 for 500 tokens; other block sizes and fewer registers
+// no gain.
 //
 // A token whose place or page does not exist is recorded in the status block and left out; rows from offsets[B] on
 // are left as they are.

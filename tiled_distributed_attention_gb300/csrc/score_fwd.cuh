@@ -768,7 +768,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (NB == 0 || x.n_tok == 0) continue;
         const int ntiles = x.ntiles(prm.tt);
         // paged: the blocks whose boxes hold rows behind the last token or before all windows, or -1
-        const int ragged_end = (x.len & (prm.box_rows - 1)) ? x.len / BN : -1, ragged_first = (x.kmin & (prm.box_rows - 1)) ? x.kmin / BN : -1;
+        const int ragged_end = (x.len & (prm.box_rows - 1)) ? x.len / BN : -1;
+        const int ragged_first = (x.kmin & (prm.box_rows - 1)) ? x.kmin / BN : -1;
         const int uidx = nq++;
         ok = mbar_wait_warp(bar(Ly::B_QFULL), (uint32_t)(uidx & 1), prm.wait_limit_ns, abort_flag, prm.status, ROLE_MMA, u);
         if (ok)
